@@ -328,6 +328,121 @@ SDV_API sdv_status sdv_moe_route(const float* router_logits, int32_t S, int32_t 
                          int32_t* ids, float* weights, int32_t* offsets, int32_t* pair_rows,
                          int32_t* n_hit, int32_t* hit, sdv_stream_t stream);
 
+/* ---- token mixing: a paged key/value cache, its attention, linear attention --------
+ *
+ * What the attention and linear-attention layers of a verify forward need besides
+ * the products above ("Spec-decode on GDN hybrids (Qwen3.5/3.6 family) -- static-S
+ * verify design", sections "Verify graph = STATIC S=K+1 + chunked GDN scan" and
+ * "Hybrid state discipline": rejected drafts must leave no trace in a layer's
+ * state).  Both 16-bit types are served; q, k, v and the outputs of one call share
+ * one type.  Sums, softmax statistics and states are fp32.
+ *
+ * Rows of q, k and v are given with a token stride in elements (a multiple of 8,
+ * at least heads * dim): token t of sequence b starts at element
+ * (b * T + t) * stride, its heads and their dim elements are contiguous, so the
+ * slices of a fused projection's output can be passed as they are.  Base pointers
+ * are 16-byte aligned.  Outputs are contiguous.
+ */
+typedef enum { SDV_F16 = 16, SDV_BF16 = 17 } sdv_dtype;
+
+/*
+ * A paged cache: position p of sequence b lives in slot p % page_size of page
+ * table[b][p / page_size].  Pages are head-major: k, v [n_pages][heads][page_size][dim].
+ * dim: a multiple of 8, 8 to 256.  page_size: any from 1 (the tensor-core attention
+ * needs a power of two from 8 up, see sdv_paged_attn).  Entries of a sequence's table
+ * row past its last used page are not read.  An entry outside [0, n_pages) is never
+ * followed: the positions behind it are taken as absent, and the workspace's status
+ * reports SDV_ERR_INVALID_ARG.
+ */
+typedef struct {
+  int32_t dtype;        /* SDV_F16 or SDV_BF16 */
+  int32_t n_pages;      /* >= 1 */
+  int32_t heads;        /* key/value heads */
+  int32_t page_size;    /* positions per page */
+  int32_t dim;          /* elements per head */
+  int32_t max_pages;    /* entries of a table row */
+  void* k;              /* device, 16-byte aligned */
+  void* v;              /* device, 16-byte aligned */
+  const int32_t* table; /* device int32 [B][max_pages] */
+} sdv_kvcache;
+
+/*
+ * Append rows to the cache: row t < n_rows[b] of sequence b goes to position
+ * ctx[b] + t.  k, v: [B][T] rows of [heads][dim].  ctx: device int32 [B], the
+ * sequence's tokens in the cache.  n_rows_or_null: device int32 [B] (NULL: T rows
+ * of every sequence; values are clamped to [0, T]).  T is any number from 1: a
+ * verify window or a whole prompt.  The caller advances ctx by what it keeps: a
+ * rejected draft's rows are overwritten by the next append.  Rows outside the
+ * table (ctx < 0, or past max_pages * page_size) and rows whose table entry is
+ * outside [0, n_pages) are not written; ws_or_null (256 bytes or more) then
+ * records it for sdv_last_device_status (SDV_ERR_INVALID_ARG).  Sequences must
+ * not share a page that one of them appends to.
+ */
+SDV_API sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const void* v, int64_t k_stride,
+                         int64_t v_stride, int32_t B, int32_t T, const int32_t* ctx,
+                         const int32_t* n_rows_or_null, void* ws_or_null, sdv_stream_t stream);
+
+/*
+ * Attention of a window's rows over the cache.  Sequence b has ctx[b] context
+ * positions and n_rows[b] <= S window rows, appended at positions ctx[b] .. before
+ * the call.  Row i < n_rows[b] sees every context position, and of the window
+ * position ctx[b] + j (j < n_rows[b]) where bit j of mask[b][i] is set; without a
+ * mask, j <= i.  S == 1 is the single-token form.
+ *   s_p = scale * q . k_p over the visible p;  lse = log sum_p exp(s_p);
+ *   out = sum_p exp(s_p - lse) v_p.
+ * A row that sees nothing, and every row i >= n_rows[b], gives out = 0 and
+ * lse = -inf.  A position that a row does not see has no effect on it, whatever
+ * its keys and values hold (infinities and NaN among them), nor has anything
+ * behind a sequence's last row.
+ *   q: [B][S] rows of [Hq][dim]; query head h reads cache head h / (Hq / heads).
+ *   mask_or_null: device uint32 [B][S].  A draft tree (sdv_tree_accept) is the
+ *   mask of each node's ancestors and itself, a pad node's word is 0.
+ *   out: [B][S][Hq][dim];  lse_or_null: fp32 [B][S][Hq] (natural logarithm).
+ * 1 <= S <= 32; Hq a multiple of heads.  ctx is clamped to [0, max_pages *
+ * page_size] and n_rows to what the table holds behind it; a clamp of either is
+ * reported as for a bad table entry.
+ * The workspace is sdv_paged_attn_workspace_bytes(...) bytes.  Deterministic: the
+ * split of a call over the GPU depends on ctx, n_rows and the shapes alone.
+ */
+SDV_API sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S,
+                          int32_t Hq, const int32_t* ctx, const int32_t* n_rows_or_null,
+                          const uint32_t* mask_or_null, float scale, void* out, float* lse_or_null,
+                          void* ws, size_t ws_bytes, sdv_stream_t stream);
+
+/* Workspace bytes of sdv_paged_attn on the current device; 0 for invalid arguments. */
+SDV_API size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim);
+
+/*
+ * Linear attention with a decay for each head, over T tokens of B sequences.  Per
+ * value head h (of H), with the state M in fp32 [Dk][Dv]:
+ *   M_t = exp(g_t) M_{t-1} + k_t v_t^T;   o_t = scale * q_t^T M_t
+ * q, k: [B][T] rows of [Hqk][Dk]; value head h uses q/k head h / (H / Hqk).
+ * v: [B][T] rows of [H][Dv].  log_decay g: fp32 [B][T][H] where decay_per_token is
+ * 1, fp32 [H] (the same for every token) where it is 0; 0 or below, -inf drops the
+ * state before the token; values above 0 are taken as 0.
+ * n_tokens_or_null: device int32 [B] (NULL: T each; clamped to [0, T]): tokens
+ * t >= n_tokens[b] neither enter the state nor are they read, and their o is 0.
+ * state_in_or_null: fp32 [B][H][Dk][Dv] before the first token (NULL: zeros);
+ * state_out_or_null: the state after the last one (NULL: not written).  The two may
+ * be the same array.  o_or_null: [B][T][H][Dv] (NULL: not computed; q is then not
+ * read and may be NULL).
+ * One entry point serves a prompt (state_in NULL or zeros), a single token
+ * (T == 1), the verify of a window (state_out NULL: the state stays as it is) and
+ * its commit (o NULL, n_tokens = the accepted rows, on the device).
+ * Dk, Dv: multiples of 8, 8 to 256.  H a multiple of Hqk.  Outputs and states do
+ * not overlap the inputs otherwise.  The workspace is
+ * sdv_linear_attn_workspace_bytes(...) bytes.
+ */
+SDV_API sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, const void* v,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* log_decay,
+                           int32_t decay_per_token, float scale, int32_t B, int32_t T, int32_t H, int32_t Hqk,
+                           int32_t Dk, int32_t Dv, const int32_t* n_tokens_or_null,
+                           const float* state_in_or_null, float* state_out_or_null, void* o_or_null,
+                           void* ws, size_t ws_bytes, sdv_stream_t stream);
+
+/* Workspace bytes of sdv_linear_attn on the current device; 0 for invalid arguments. */
+SDV_API size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv);
+
 /*
  * Workspace bytes an operation needs on the current device.
  * `op` is an sdv_op; n, k are the weight's (for SDV_OP_MOE: n = I, k = H);
@@ -345,7 +460,8 @@ SDV_API sdv_status sdv_workspace_init(void* ws, size_t ws_bytes, sdv_stream_t st
  * Synchronise `stream`, then read and clear the device status word a kernel
  * leaves in `ws`: SDV_OK, or SDV_ERR_TIMEOUT if a bounded device-side wait gave
  * up (the outputs of that call are then undefined; later calls on the same
- * workspace are unaffected).  Any other flag (the tensor-memory allocation was
+ * workspace are unaffected), or SDV_ERR_INVALID_ARG if a device-side table entry
+ * or length was out of range (sdv_kv_append, sdv_paged_attn).  Any other flag (the tensor-memory allocation was
  * not where the kernel expects it) reads as SDV_ERR_CUDA.  The status word
  * collects the flags of every call since the last read.
  * (The boundary's "bounded-wait / debug-assert flags" read: "Stream C --

@@ -576,7 +576,8 @@ sdv_status sdv_last_device_status(void* ws, sdv_stream_t stream) {
   if (word == 0) return SDV_OK;
   const int zero = 0;
   if (cudaMemcpy(ws, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return SDV_ERR_CUDA;
-  return (word & sdv::kDevErrTimeout) ? SDV_ERR_TIMEOUT : SDV_ERR_CUDA;
+  if (word & sdv::kDevErrTimeout) return SDV_ERR_TIMEOUT;
+  return word == sdv::kDevErrIndex ? SDV_ERR_INVALID_ARG : SDV_ERR_CUDA;
 }
 
 sdv_status sdv_device_status(void* ws, sdv_stream_t stream) { return sdv_last_device_status(ws, stream); }

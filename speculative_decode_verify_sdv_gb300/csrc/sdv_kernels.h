@@ -38,6 +38,7 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 // Device status word bits (first word of every workspace).
 constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrTmemBase = 2;  // tensor-memory allocation not at column 0
+constexpr int kDevErrIndex = 4;     // a table entry or a length on the device out of range
 
 constexpr int kModeY = 0;     // write fp32 Y [S][N]
 constexpr int kModeHead = 1;  // verify head: argmax partials + last-CTA reduce + accept

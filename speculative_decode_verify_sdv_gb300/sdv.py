@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libsdv.so")
 
 SDV_OK, SDV_ERR_INVALID_ARG, SDV_ERR_UNSUPPORTED, SDV_ERR_CUDA, SDV_ERR_TIMEOUT, SDV_ERR_WORKSPACE = range(6)
 SDV_Q8, SDV_Q4, SDV_F4 = 8, 4, 2
+SDV_F16, SDV_BF16 = 16, 17
 SDV_OP_QLINEAR, SDV_OP_QLINEAR_SWIGLU, SDV_OP_VERIFY_HEAD, SDV_OP_MOE, SDV_OP_VERIFY_SAMPLE = 1, 2, 3, 4, 5
 
 EXPORTED = (
@@ -25,6 +26,8 @@ EXPORTED = (
     "sdv_last_device_status", "sdv_device_status", "sdv_noalloc_device_status", "sdv_status_string", "sdv_version", "sdv_launch_count", "sdv_verify_head_noalloc", "sdv_set_gemm_path",
     "sdv_moe_route", "sdv_verify_sample", "sdv_tree_accept", "sdv_debug_fault",
     "sdv_ngram_create", "sdv_ngram_destroy", "sdv_ngram_append", "sdv_ngram_propose",
+    "sdv_kv_append", "sdv_paged_attn", "sdv_paged_attn_workspace_bytes", "sdv_linear_attn",
+    "sdv_linear_attn_workspace_bytes",
 )
 
 
@@ -39,6 +42,12 @@ class sdv_qweight(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class sdv_kvcache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("dim", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -51,6 +60,8 @@ def load() -> ctypes.CDLL:
         raise RuntimeError(f"libsdv.so not found at {LIB_PATH}; run __graft_entry__.build() first")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    kvc = ctypes.POINTER(sdv_kvcache)
     qw = ctypes.POINTER(sdv_qweight)
     sig = {
         "sdv_quantize_block32": ([vp, i32, i32, i32, vp, vp, vp], i32),
@@ -78,6 +89,12 @@ def load() -> ctypes.CDLL:
         "sdv_ngram_destroy": ([vp], i32),
         "sdv_ngram_append": ([vp, vp, i32], i32),
         "sdv_ngram_propose": ([vp, i32, vp, ctypes.POINTER(i32)], i32),
+        "sdv_kv_append": ([kvc, vp, vp, i64, i64, i32, i32, vp, vp, vp, vp], i32),
+        "sdv_paged_attn": ([kvc, vp, i64, i32, i32, i32, vp, vp, vp, f32, vp, vp, vp, sz, vp], i32),
+        "sdv_paged_attn_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "sdv_linear_attn": ([i32, vp, vp, vp, i64, i64, i64, vp, i32, f32, i32, i32, i32, i32, i32, i32, vp, vp, vp,
+                             vp, vp, sz, vp], i32),
+        "sdv_linear_attn_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -290,6 +307,133 @@ def sdv_moe_route(router_logits: torch.Tensor, S: int, E: int, top_k: int, ids: 
         _ptr(n_hit), _ptr(hit), _stream(stream)))
 
 
+# ---- token mixing: paged cache, its attention, linear attention ------------------
+
+_DTYPES = {torch.float16: SDV_F16, torch.bfloat16: SDV_BF16}
+
+
+def _addr(t, dtype, name, shape=None):
+    """Device address of a contiguous CUDA tensor (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, B, T, heads, dim):
+    """(address, token stride) of [B, T, heads, dim] rows: heads and dim contiguous,
+    the tokens of all sequences at one stride (the slices of a fused projection)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape != (B, T, heads, dim):
+        raise ValueError(f"{name} must be {(B, T, heads, dim)}, got {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    if T == 1:
+        st = sb if B > 1 else heads * dim
+    if sd != 1 or (heads > 1 and sh != dim) or (B > 1 and sb != T * st):
+        raise ValueError(f"{name}: heads and dim must be contiguous and its tokens evenly strided")
+    return t.data_ptr(), st
+
+
+def _kvcache(k_pages, v_pages, table):
+    dt = k_pages.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"a cache is float16 or bfloat16, got {dt}")
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_pages and v_pages are [n_pages, heads, page_size, dim], table is [B, max_pages]")
+    n, heads, page, dim = k_pages.shape
+    return sdv_kvcache(_DTYPES[dt], n, heads, page, dim, table.shape[1], _addr(k_pages, dt, "k_pages"),
+                       _addr(v_pages, dt, "v_pages", k_pages.shape), _addr(table, torch.int32, "table"))
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def sdv_paged_attn_workspace_bytes(B: int, S: int, Hq: int, heads: int, dim: int) -> int:
+    return int(load().sdv_paged_attn_workspace_bytes(B, S, Hq, heads, dim))
+
+
+def sdv_linear_attn_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int) -> int:
+    return int(load().sdv_linear_attn_workspace_bytes(B, T, H, Dk, Dv))
+
+
+def sdv_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  table: torch.Tensor, ctx: torch.Tensor, n_rows, ws, stream=None) -> None:
+    """Rows k, v [B, T, heads, dim] into the cache behind ctx [B]; n_rows [B] or
+    None (all T); ws: a workspace for the device status, or None."""
+    c = _kvcache(k_pages, v_pages, table)
+    B, T = k.shape[:2]
+    i32 = torch.int32
+    dt = k_pages.dtype
+    ka, ks = _rows(k, dt, "k", B, T, c.heads, c.dim)
+    va, vs = _rows(v, dt, "v", B, T, c.heads, c.dim)
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
+    if ws is not None and ws.numel() * ws.element_size() < 256:
+        raise ValueError("ws must hold at least 256 bytes")
+    st = load().sdv_kv_append(ctypes.byref(c), ka, va, ks, vs, B, T, _addr(ctx, i32, "ctx", (B,)),
+                              _addr(n_rows, i32, "n_rows", (B,)), None if ws is None else _addr(ws, ws.dtype, "ws"),
+                              _raw_stream(stream))
+    if st:
+        _check("sdv_kv_append", st)
+
+
+def sdv_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                   ctx: torch.Tensor, n_rows, mask, scale: float, out: torch.Tensor, lse, ws: torch.Tensor,
+                   stream=None) -> None:
+    """Attention of the window rows q [B, S, Hq, dim] over the cache; mask: int32
+    [B, S] visibility words or None (causal); lse: fp32 [B, S, Hq] or None."""
+    c = _kvcache(k_pages, v_pages, table)
+    B, S, hq = q.shape[:3]
+    i32 = torch.int32
+    dt = k_pages.dtype
+    qa, qs = _rows(q, dt, "q", B, S, hq, c.dim)
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
+    st = load().sdv_paged_attn(
+        ctypes.byref(c), qa, qs, B, S, hq, _addr(ctx, i32, "ctx", (B,)), _addr(n_rows, i32, "n_rows", (B,)),
+        _addr(mask, i32, "mask", (B, S)), scale, _addr(out, dt, "out", q.shape),
+        _addr(lse, torch.float32, "lse", (B, S, hq)), _addr(ws, ws.dtype, "ws"), ws.numel() * ws.element_size(),
+        _raw_stream(stream))
+    if st:
+        _check("sdv_paged_attn", st)
+
+
+def sdv_linear_attn(q, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, scale: float, n_tokens,
+                    state_in, state_out, o, ws: torch.Tensor, stream=None) -> None:
+    """Linear attention with a decay per head: q, k [B, T, Hqk, Dk], v [B, T, H, Dv],
+    log_decay fp32 [B, T, H] or [H], states fp32 [B, H, Dk, Dv], o [B, T, H, Dv];
+    n_tokens int32 [B], state_in, state_out, o (and then q) may be None."""
+    if k.dtype not in _DTYPES:
+        raise TypeError(f"q, k and v are float16 or bfloat16, got {k.dtype}")
+    B, T, hqk, dk = k.shape
+    H, dv = v.shape[2:]
+    dt, f32 = k.dtype, torch.float32
+    ka, ks = _rows(k, dt, "k", B, T, hqk, dk)
+    va, vs = _rows(v, dt, "v", B, T, H, dv)
+    qa, qs = (None, 0) if q is None else _rows(q, dt, "q", B, T, hqk, dk)
+    per_token = log_decay.dim() == 3
+    state = (B, H, dk, dv)
+    st = load().sdv_linear_attn(
+        _DTYPES[dt], qa, ka, va, qs, ks, vs, _addr(log_decay, f32, "log_decay", (B, T, H) if per_token else (H,)),
+        1 if per_token else 0, scale, B, T, H, hqk, dk, dv, _addr(n_tokens, torch.int32, "n_tokens", (B,)),
+        _addr(state_in, f32, "state_in", state), _addr(state_out, f32, "state_out", state),
+        _addr(o, dt, "o", (B, T, H, dv)), _addr(ws, ws.dtype, "ws"), ws.numel() * ws.element_size(),
+        _raw_stream(stream))
+    if st:
+        _check("sdv_linear_attn", st)
+
+
 # ---- host n-gram drafter (host pointers; no GPU involved) -------------------------
 
 def sdv_ngram_create(m: int) -> int:
@@ -332,3 +476,17 @@ def quantize(w: torch.Tensor, bits: int) -> QWeight:
     scales = torch.empty((n, k // 32), dtype=torch.float16, device=w.device)
     sdv_quantize_block32(w.contiguous(), bits, codes, scales)
     return QWeight(codes, scales, bits, n, k)
+
+
+def paged_attn_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for sdv_paged_attn calls of this shape (q [B, S, Hq, dim])."""
+    B, S, hq, dim = q.shape
+    nbytes = max(sdv_paged_attn_workspace_bytes(B, S, hq, k_pages.shape[1], dim), 256)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+
+
+def linear_attn_workspace(k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for sdv_linear_attn calls of this shape (k [B, T, Hqk, Dk], v [B, T, H, Dv])."""
+    B, T = k.shape[:2]
+    nbytes = max(sdv_linear_attn_workspace_bytes(B, T, v.shape[2], k.shape[3], v.shape[3]), 256)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=k.device)
