@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "attn_sched.cuh"
+#include "attn_tc.h"
 #include "host_util.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int d = tid + 128 * c;
-          if (d < D) a.part_o[(slot * a.row_tile + r) * D + d] = o[c][r];
+          if (d < D) a.part_o[((slot * (D / 4) + d / 4) * a.row_tile + r) * 4 + d % 4] = o[c][r];
         }
         if (tid == 0) {
           a.part_ml[(slot * a.row_tile + r) * 2] = ps[r];
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
 
 // ---- join -----------------------------------------------------------------------------
 
-// Adds the partials of the units that several CTAs shared, a warp per row:
+// Adds the partials of the units that several CTAs shared, a thread per row and
+// four columns (a unit's rows side by side, as the partials lie):
 // M = max m_j, out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, in CTA order.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
@@ -228,9 +230,6 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   griddep_wait();
   const int units = a.Hkv * a.row_tiles;
   const int b = blockIdx.x / units, unit = blockIdx.x % units;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
-  if (r >= min(a.row_tile, a.rows - r0)) return;
   long long before = 0, all = 0;
   for (int s = lane; s < a.B; s += 32) {
     const int t = attn_seq(a, s).tiles;
@@ -247,33 +246,42 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int live = attn_live_ctas(a, total);
   const int c0 = attn_owner(total, live, first), c1 = attn_owner(total, live, first + seq.tiles - 1);
   if (c0 == c1) return;
-  auto slot_of = [&](int c) { return (size_t)2 * c + (c == c0 ? 1 : 0); };
+  const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
+  const int e = blockIdx.y * 128 + threadIdx.x, r = e % a.row_tile, d4 = e / a.row_tile;
+  if (d4 >= a.D / 4 || r >= a.rows - r0) return;
+  const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + r;
+  const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)d4 * a.row_tile + r;
+  const size_t step = (size_t)(a.D / 4) * a.row_tile;
   float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[(slot_of(c) * a.row_tile + r) * 2]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, ml[(size_t)(2 * c + (c == c0)) * a.row_tile].x);
   const float ref = m == -INFINITY ? 0.f : m;
-  float o[8], l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  const int D = a.D;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
-    const size_t row = slot_of(c) * a.row_tile + r;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
-    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
-    l = fmaf(f, ml.y, l);
-    if (f == 0.f) continue;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < D) o[i] = fmaf(f, a.part_o[row * D + lane + 32 * i], o[i]);
+    const size_t slot = 2 * c + (c == c0);
+    const float2 s = ml[slot * a.row_tile];
+    const float4 x = po[slot * step];
+    const float f = exp2f(s.x - ref);  // 0 where the CTA saw nothing (max -inf)
+    l = fmaf(f, s.y, l);
+    if (f != 0.f) {
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
   }
   const int row = r0 + r;
   const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (lane + 32 * i < D) from_float(l == 0.f ? 0.f : o[i] / l, static_cast<T*>(a.out)[orow * D + lane + 32 * i]);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  alignas(8) T y[4];
+  from_float(l == 0.f ? 0.f : o.x * inv, y[0]);
+  from_float(l == 0.f ? 0.f : o.y * inv, y[1]);
+  from_float(l == 0.f ? 0.f : o.z * inv, y[2]);
+  from_float(l == 0.f ? 0.f : o.w * inv, y[3]);
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * a.D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
+  if (d4 == 0 && a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 int simple_smem(int D) {
@@ -294,7 +302,8 @@ cudaError_t launch_attn_simple(int dtype, const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_join(int dtype, const AttnArgs& a, cudaStream_t st) {
   auto kernel = dtype == SDV_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
-  return launch_pdl(kernel, dim3(a.B * a.Hkv * a.row_tiles, (a.row_tile + 3) / 4), dim3(128), 0, st, a);
+  return launch_pdl(kernel, dim3(a.B * a.Hkv * a.row_tiles, (a.row_tile * (a.D / 4) + 127) / 128),
+                    dim3(128), 0, st, a);
 }
 
 }  // namespace sdv
@@ -378,8 +387,12 @@ size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t 
   const int sms = sdv::sm_count();
   AttnArgs a{};
   a.rows = S * (Hq / heads);
+  // the larger of the two kernels' needs: which one runs depends on the page size too
   set_rows(a, sdv::kAttnSimpleRows);
-  return sdv::kHeaderBytes + part_bytes(kSimplePerSm * (sms > 0 ? sms : 256), a.row_tile, dim);
+  const size_t simple = part_bytes(kSimplePerSm * (sms > 0 ? sms : 256), a.row_tile, dim);
+  set_rows(a, sdv::kAttnTcRows);
+  const size_t tc = part_bytes(sms > 0 ? sms : 256, a.row_tile, dim);
+  return sdv::kHeaderBytes + (simple > tc ? simple : tc);
 }
 
 sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
@@ -421,14 +434,15 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   a.status = static_cast<int*>(ws);
   const int sms = sdv::sm_count();
   if (sms <= 0) return SDV_ERR_CUDA;
-  set_rows(a, sdv::kAttnSimpleRows);
-  a.tile = sdv::kAttnSimpleTile;
-  a.ctas = kSimplePerSm * sms;
+  const bool tc = sdv::attn_tc_takes(a.D, a.page, (long long)a.n_pages * a.Hkv * a.page);
+  set_rows(a, tc ? sdv::kAttnTcRows : sdv::kAttnSimpleRows);
+  a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
+  a.ctas = tc ? sms : kSimplePerSm * sms;
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
   a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
                                       sdv::round_256((size_t)2 * a.ctas * a.row_tile * 8));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = sdv::launch_attn_simple(cache->dtype, a, st);
+  cudaError_t e = tc ? sdv::launch_attn_tc(cache->dtype, a, st) : sdv::launch_attn_simple(cache->dtype, a, st);
   // the join, unless no unit can have more than one tile
   if (e == cudaSuccess && (long long)a.max_pages * a.page > a.tile) e = sdv::launch_attn_join(cache->dtype, a, st);
   return sdv::status_of(e);

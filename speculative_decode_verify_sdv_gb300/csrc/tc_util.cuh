@@ -1,0 +1,126 @@
+// tcgen05 building blocks of the token-mixing kernels: 128-byte-swizzled operand
+// descriptors, single MMAs issued by one thread, 32-column tensor-memory accesses.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sdv_device.cuh"
+
+namespace sdv {
+
+// Operand tiles in shared memory are blocks of 64 16-bit elements (128 bytes) per
+// row under the 128-byte swizzle: 16-byte chunk c of row r sits at chunk
+// c ^ (r % 8), 8 rows (1024 bytes) to a swizzle atom.
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk) {
+  return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
+// Shared-memory matrix descriptor under the 128-byte swizzle.  K-major operand
+// (64 reduction elements per row): sbo = 1024 between 8-row groups, lbo unused;
+// 16 reduction elements further = 32 bytes further.  MN-major operand (64 rows
+// or columns of the matrix per 128 bytes, one reduction index per row): sbo = 1024
+// between groups of 8 reduction indices, lbo = bytes between 64-element blocks.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;  // descriptor version of this tensor-core generation
+  d |= (uint64_t)2 << 61;  // 128-byte swizzle
+  return d;
+}
+
+// Instruction descriptor of kind::f16: 16-bit A and B of one type, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_16_f32(bool bf16, int m, int n, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn_major ? 1u << 15 : 0u) |
+         (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// One MMA (K = 16), A from shared memory / from tensor memory; issued by one thread.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+#define SDV_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), \
+                     "=r"(v[o + 6]), "=r"(v[o + 7])
+#define SDV_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), \
+                     "r"(v[o + 6]), "r"(v[o + 7])
+// 32 columns of a warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : SDV_R8(v, 0), SDV_R8(v, 8), SDV_R8(v, 16), SDV_R8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      SDV_W8(v, 0), SDV_W8(v, 8), SDV_W8(v, 16), SDV_W8(v, 24)
+      : "memory");
+}
+#undef SDV_R8
+#undef SDV_W8
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// L2 policy of data that other CTAs read too.
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats to a packed pair of the 16-bit type (a in the low half).
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Whether either half of a packed pair is an infinity or NaN: bits of the halves that are.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite16(uint32_t x);
+template <>
+__device__ __forceinline__ uint32_t nonfinite16<__half>(uint32_t x) {
+  return ((x & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
+}
+template <>
+__device__ __forceinline__ uint32_t nonfinite16<__nv_bfloat16>(uint32_t x) {
+  return ((x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 2u : 0u);
+}
+
+}  // namespace sdv

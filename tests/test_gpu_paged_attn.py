@@ -138,6 +138,25 @@ def test_attention_matches_the_oracle(sdv, case):
         assert torch.equal(out3, out)
 
 
+@pytest.mark.parametrize("dt,B,S,hq,hkv,d,most", [
+    (F16, 64, 1, 16, 8, 64, 400), (BF16, 48, 1, 16, 8, 128, 300), (F16, 30, 5, 12, 6, 256, 200),
+    (BF16, 20, 32, 20, 4, 128, 150)])
+def test_many_sequences_per_cta(sdv, dt, B, S, hq, hkv, d, most):
+    # several units in a CTA's share, of one tile and of more
+    rng = np.random.default_rng(B)
+    ctx, n = [int(x) for x in rng.integers(0, most, B)], [int(x) for x in rng.integers(0, S + 1, B)]
+    q, kp, vp, table = make(dt, B, S, hq, hkv, d, 16, ctx, n, B)
+    mask = words(rng, B, S) if S > 1 else None
+    ref = mixing.attention(f64(q), f64(kp), f64(vp), table.tolist(), ctx, n, mask, d ** -0.5)
+    first = None
+    for _ in range(5):
+        out, lse, ws = call(sdv, q, kp, vp, table, ctx, n, None if mask is None else as_i32(mask), d ** -0.5)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    check(dt, ref, out, lse, d)
+
+
 @pytest.mark.parametrize("dt", [F16, BF16])
 @pytest.mark.parametrize("std", [0.0, 1e-3, 60.0])
 def test_flat_and_sharp_softmax(sdv, dt, std):
