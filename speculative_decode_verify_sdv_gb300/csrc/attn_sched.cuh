@@ -2,9 +2,11 @@
 //
 // The cache positions of every (sequence, kv head, row tile) -- a unit -- are cut
 // into tiles of `tile` positions; the tiles of all units, laid end to end, are
-// dealt in equal contiguous ranges to the CTAs of one wave.  Ragged contexts are
-// then balanced to one tile whatever their lengths, and one long context spreads
-// over the whole GPU.  A unit inside one CTA's range is finished there; the others
+// dealt in equal contiguous ranges to the CTAs of one wave.  A unit weighs its
+// tiles and `lead` more, the time that its queries, its last tile's cleaning and its
+// outputs take in tiles' time, laid before its first tile: short contexts in a batch
+// would otherwise all fall to a few CTAs.  Ragged contexts are then balanced to one
+// tile whatever their lengths, and one long context spreads over the whole GPU.  A unit inside one CTA's range is finished there; the others
 // leave (unnormalised output, max, sum) partials that the join launch adds in CTA
 // order.  The lengths live on the device, so every warp that needs the split
 // computes it from them (a warp-wide scan over the sequences), and the split is a
@@ -33,12 +35,14 @@ struct AttnArgs {
   int rows;                 // S * G query rows of a kv head, row r = (window row r / G, head r % G)
   int row_tiles, row_tile;  // row tiles of a kv head, rows of one (the last may hold fewer)
   int tile;                 // cache positions per tile
+  int lead;                 // weight of a unit beyond its tiles
   void* out;
   float* lse;               // or null
   float* part_o;            // [2 * CTAs][row_tile][D]
   float* part_ml;           // [2 * CTAs][row_tile][2]: max (log2 domain), sum
   int* status;
   int ctas;                 // CTAs of the attention launch
+  int slots, q_bufs;        // tensor-core kernel: ring slots, Q buffers
 };
 
 struct AttnSeq {
@@ -60,11 +64,10 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// Tiles of all units, and the units before sequence b times their tiles.
-// Warp-collective; every lane gets the results.
+// Weight of all units.  Warp-collective; every lane gets the result.
 __device__ __forceinline__ long long attn_total(const AttnArgs& a, int lane) {
   long long sum = 0;
-  for (int b = lane; b < a.B; b += 32) sum += attn_seq(a, b).tiles;
+  for (int b = lane; b < a.B; b += 32) sum += attn_seq(a, b).tiles + a.lead;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   return sum * a.Hkv * a.row_tiles;
@@ -73,7 +76,7 @@ __device__ __forceinline__ long long attn_total(const AttnArgs& a, int lane) {
 __device__ __forceinline__ int attn_live_ctas(const AttnArgs& a, long long total) {
   return total < a.ctas ? (int)total : a.ctas;
 }
-// First tile of CTA c's range, and the CTA whose range holds tile w.
+// Start of CTA c's range, and the CTA whose range holds place w.
 __device__ __forceinline__ long long attn_first(long long total, int live, int c) { return c * total / live; }
 __device__ __forceinline__ int attn_owner(long long total, int live, long long w) {
   return (int)(((w + 1) * live - 1) / total);
@@ -81,22 +84,21 @@ __device__ __forceinline__ int attn_owner(long long total, int live, long long w
 
 // A CTA's way through its range, one segment (part of a unit) after another.
 struct AttnWalk {
-  long long total, at, end;  // all tiles; this CTA's next tile and its end
-  int live;
-  int b, unit, tile;         // of the next tile: sequence, unit within it, tile within the unit
+  long long at, end;  // place of the next tile, end of the CTA's range
+  int b, unit, tile;  // of the next tile: sequence, unit within it, tile within the unit
   AttnSeq seq;
 
   // Warp-collective.  False where the CTA has nothing to do.
   __device__ __forceinline__ bool start(const AttnArgs& a, int cta, int lane) {
-    total = attn_total(a, lane);
-    live = attn_live_ctas(a, total);
+    const long long total = attn_total(a, lane);
+    const int live = attn_live_ctas(a, total);
     if (cta >= live) return false;
     at = attn_first(total, live, cta);
     end = attn_first(total, live, cta + 1);
     const int units = a.Hkv * a.row_tiles;
-    long long before = 0;  // tiles of the sequences before this group of 32
+    long long before = 0;  // weight of the sequences before this group of 32
     for (int b0 = 0;; b0 += 32) {
-      const long long mine = b0 + lane < a.B ? (long long)attn_seq(a, b0 + lane).tiles * units : 0;
+      const long long mine = b0 + lane < a.B ? ((long long)attn_seq(a, b0 + lane).tiles + a.lead) * units : 0;
       long long incl = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -114,9 +116,12 @@ struct AttnWalk {
     }
     seq = attn_seq(a, b);
     const long long rest = at - before;
-    unit = (int)(rest / seq.tiles);
-    tile = (int)(rest % seq.tiles);
-    return true;
+    const int weight = seq.tiles + a.lead;
+    unit = (int)(rest / weight);
+    const int place = (int)(rest % weight);
+    tile = place > a.lead ? place - a.lead : 0;
+    at += tile + a.lead - place;
+    return at < end;
   }
   __device__ __forceinline__ bool more() const { return at < end; }
   // Tiles of the segment that starts at the next tile.
@@ -129,6 +134,7 @@ struct AttnWalk {
     tile += count;
     if (tile < seq.tiles) return;
     tile = 0;
+    at += a.lead;
     if (++unit < a.Hkv * a.row_tiles) return;
     unit = 0;
     if (++b < a.B) seq = attn_seq(a, b);

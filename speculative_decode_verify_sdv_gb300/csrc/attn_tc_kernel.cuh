@@ -1,0 +1,707 @@
+// Attention of a verify window over a paged cache on the 5th-generation tensor
+// cores (sm_103a): sdv_paged_attn for head sizes 64, 128 and 256.
+//
+// Per row r of a kv head's S * G query rows and cache position p:
+//   s = q_r . k_p;  m = running max of scale s;  P = 2^((scale s - m) log2 e)
+//   l += sum P;  O = O 2^(m_old - m) + P V;  out = O / l
+// One pass over keys and values.  A unit's rows (at most 128) are one MMA tile, so
+// a window reads the cache once for all its rows and heads of a group: 4 D flops
+// per row and position against 4 D bytes per position, far inside the tensor
+// cores' rate for any window -- reading the cache bounds it.
+//
+// One persistent CTA per SM walks an equal share of all tiles (attn_sched.cuh).
+// Warp roles:
+//   warps 0, 6  TMA producers of keys and of values: a lane per (page, 64-element
+//               block) box; the tiles alternate through a ring of equal slots;
+//   warp 1      allocates tensor memory, one lane issues the MMAs:
+//               S = Q K^T (both K-major in shared memory), one tile ahead of
+//               O += P V (P in tensor memory, V as it lies in the cache, MN-major);
+//   warps 2-5   softmax, a thread per row: S from tensor memory, P back into its
+//               columns; they also write the outputs;
+//   warp 7      walks the units ahead of the others: stages a segment's Q (two
+//               buffers of the row tile's rows) and what it is, so that short
+//               contexts follow each other without a load in between.
+// With at most 32 rows (single tokens, short windows) the rows stand four times in
+// the MMA's 128, and each softmax warp takes a quarter of a tile's positions for all
+// of them, the other positions' weights being zero in its copy: the softmax of a tile
+// then takes a quarter of the time, and the four (m, l, O) are merged at the end.
+//
+// The reference maximum moves only when it grows by more than 2^8 (the sum and
+// output stay exact relative to it), so O in tensor memory is rescaled rarely.
+// P carries a factor 2^6: with it the weights down to 2^-20 of the row's largest
+// stay in fp16's normal range, and 2^14 is the most it can reach.  Rounding P to
+// the 16-bit type is the one rounding inside the sum (the sum l takes P before
+// it); it is what a matrix instruction on 16-bit values needs.
+//
+// Pages past the end and absent ones are boxes past the tensor map's end: the copy
+// fills zeros.  In tiles that reach past the context V is cleaned in shared memory
+// before P V: what the last page holds behind the end becomes zeros, and a window
+// row's infinities and NaN are zeroed and noted, then added at the end to the rows
+// that do see them -- 0 * inf would otherwise reach the others.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_sched.cuh"
+#include "attn_tc.h"
+#include "sdv_kernels.h"
+#include "tc_util.cuh"
+
+namespace sdv {
+
+namespace {
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnSmem = 232448;                // all of an SM's: one CTA, one tensor-memory allocation
+constexpr uint64_t kAttnDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
+constexpr int kMaxSlots = 8;
+constexpr int kSpreadRows = 32;                  // rows that stand four times in the MMA tile
+// The merge buffer: 4 copies of up to 32 rows, at least 32 columns and 4 of padding.
+constexpr int kMergeBytes = 4 * kSpreadRows * (32 + 4) * 4;
+
+// What a segment is, from warp 7 to the MMA and softmax warps.
+struct AttnSegment {
+  int count;  // tiles; 0: no more segments
+  int b, unit, tile, ctx, n, tiles;
+  int absent;          // a table entry of the segment cannot be followed
+  uint32_t words[32];  // visibility of the window rows
+};
+
+// Shared memory: the Q buffers, the ring, small things.  The MMA reads 128 rows of a
+// Q buffer; what lies behind the staged ones feeds rows that nobody looks at.
+template <int D, bool SPREAD>
+struct AttnPlan {
+  static constexpr int TK = attn_tc_tile(D);
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kSlot = TK * D * 2;
+  static constexpr int kNumBars = 2 * kMaxSlots + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;  // the last for alignment
+  static constexpr int kMerge = SPREAD ? kMergeBytes + 4 * kSpreadRows * 8 + kSpreadRows * 4 : 0;
+  static constexpr int kSmall = 2 * D * 4 + kNumBars * 8 + 2 * (int)sizeof(AttnSegment) + 16 + kMerge;
+  static constexpr int kS = 0;       // tensor-memory columns: two score tiles (P inside),
+  static constexpr int kO = 2 * TK;  // then the output
+  static_assert(kO + D <= 512, "tensor memory");
+  static_assert((2 * D * 4 + kNumBars * 8) % 16 == 0 && sizeof(AttnSegment) % 16 == 0, "16-byte merge rows");
+  // rows between a Q buffer's 64-element blocks, bytes between the buffers, all buffers
+  __host__ __device__ static int q_rows(int row_tile) { return SPREAD ? 128 : (row_tile + 7) / 8 * 8; }
+  __host__ __device__ static int q_step(int row_tile) {
+    return SPREAD ? (row_tile + 7) / 8 * 1024 : q_rows(row_tile) * D * 2;
+  }
+  __host__ __device__ static int q_bytes(int row_tile, int q_bufs) {
+    return SPREAD ? 128 * D * 2 : q_bufs * q_step(row_tile);
+  }
+  static int slots(int row_tile, int q_bufs) {
+    const int n = (kAttnSmem - 1024 - kSmall - q_bytes(row_tile, q_bufs)) / kSlot;
+    return n < kMaxSlots ? n : kMaxSlots;
+  }
+};
+
+// Sum of the values that are not finite in column d of the window positions `bits`.
+template <typename T>
+__device__ __noinline__ float poison_of(const AttnArgs& a, const int32_t* trow, int h, int ctx, uint32_t bits, int d) {
+  float sum = 0.f;
+  for (; bits; bits &= bits - 1) {
+    const int p = ctx + __ffs(bits) - 1;
+    const int id = __ldg(trow + p / a.page);  // in range: the position's page was followed
+    sum += (float)static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d];
+  }
+  return sum;
+}
+
+// Visibility of 32 positions from p on: context positions, the window's by `word`.
+__device__ __forceinline__ uint32_t attn_visible(int p, int ctx, uint32_t word) {
+  const int nc = min(max(ctx - p, 0), 32);
+  uint32_t bits = nc >= 32 ? 0xffffffffu : (1u << nc) - 1u;
+  if (p < ctx) bits |= nc >= 32 ? 0u : word << nc;
+  else bits |= p - ctx < 32 ? word >> (p - ctx) : 0u;
+  return bits;
+}
+
+template <typename T, int D, bool SPREAD>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const AttnArgs a) {
+  using PL = AttnPlan<D, SPREAD>;
+  constexpr int TK = PL::TK;
+  constexpr int CW = SPREAD ? TK / 4 : TK;  // score columns of a softmax warp
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const sb = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NS = a.slots, q_bufs = a.q_bufs;
+  const int q_block = PL::q_rows(a.row_tile) * 128, q_step = PL::q_step(a.row_tile);
+  const uint32_t ring = base + PL::q_bytes(a.row_tile, q_bufs);
+  const uint32_t small = ring + NS * PL::kSlot, bars = small + 2 * D * 4;
+  uint8_t* const sp = sb + (small - base);
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kMaxSlots + s); };
+  constexpr int kB = 2 * kMaxSlots;
+  auto s_full = [&](int i) { return bars + 8u * (kB + i); };
+  auto p_ready = [&](int i) { return bars + 8u * (kB + 2 + i); };
+  auto q_full = [&](int i) { return bars + 8u * (kB + 4 + i); };
+  auto q_free = [&](int i) { return bars + 8u * (kB + 6 + i); };
+  const uint32_t pv_done = bars + 8u * (kB + 8), drain = pv_done + 8, rows_met = pv_done + 16;
+  uint32_t* const poison = reinterpret_cast<uint32_t*>(sp);  // [2][D]
+  AttnSegment* const segs = reinterpret_cast<AttnSegment*>(sp + 2 * D * 4 + PL::kNumBars * 8);
+  volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);  // tmem base, poison seen [2]
+  float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 4));
+  float2* const mstat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + kMergeBytes);  // [4][32]
+  uint32_t* const mword = reinterpret_cast<uint32_t*>(mstat + 4 * kSpreadRows);
+  const int nq = SPREAD ? 4 : (a.row_tile + 31) / 32;  // softmax warps with rows
+
+  if (warp == 1) {
+    tmem_alloc(smem_addr(const_cast<uint32_t*>(misc)), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_ready(i), nq);
+      mbar_init(q_full(i), 1);
+      mbar_init(q_free(i), 1 + nq);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(rows_met, nq);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  for (int e = threadIdx.x; e < 2 * D; e += kAttnThreads) poison[e] = 0;
+  if (threadIdx.x < 2) misc[1 + threadIdx.x] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = misc[0];
+  griddep_wait();
+  griddep_launch_dependents();
+  bool ok = true;
+  auto await = [&](uint32_t bar, uint32_t parity) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
+      ok = false;
+      if (lane == 0) atomicOr(a.status, kDevErrTimeout);
+    }
+    return ok;
+  };
+  // P V products complete in tile order.  Each role that needs them waits for every
+  // one, in order, and before the next can be issued: a parity wait on an older one
+  // would otherwise meet the newer phase of the same parity.
+  int pv_seen = 0;
+  auto pv_wait = [&](int tiles) {
+    for (; pv_seen < tiles; ++pv_seen)
+      if (!await(pv_done, pv_seen & 1)) return false;
+    return true;
+  };
+  // segment s is in Q buffer and note s % q_bufs
+  auto seg_buf = [&](int s) { return q_bufs == 2 ? s & 1 : 0; };
+  auto seg_parity = [&](int s) { return (q_bufs == 2 ? s >> 1 : s) & 1; };
+
+  if (warp == 0 || warp == 6) {
+    // ---- producers: the warp's tile i takes ring place 2i (keys) or 2i + 1 (values) ----
+    AttnWalk w;
+    const bool values = warp == 6;
+    const int box = min(a.page, TK), chunks = TK / box;  // rows per box, pages (or page parts) per tile
+    const int beyond = a.n_pages * a.Hkv * a.page;       // a row past the tensor map's end: zeros
+    const uint64_t policy = a.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_normal();
+    const int cb = lane % PL::kBlocks, chunk = lane / PL::kBlocks;
+    const bool mine = chunk < chunks;
+    const uint32_t dst = ring + cb * (TK * 128) + chunk * box * 128;
+    int slot = values ? 1 : 0, use = 0;  // ring place: slot, and how often the ring has been passed
+    bool more = w.start(a, blockIdx.x, lane);
+    while (more) {
+      const int count = w.segment();
+      const int h = w.unit / a.row_tiles;
+      const int total = w.seq.ctx + w.seq.n;
+      const int32_t* const row = a.table + (size_t)w.b * a.max_pages;
+      auto page_of = [&](int t) {
+        const int p = t * TK + chunk * box;
+        return mine && p < total ? __ldg(row + p / a.page) : -1;
+      };
+      int next = page_of(w.tile);
+      for (int t = w.tile; t < w.tile + count; ++t) {
+        const int id = next, p = t * TK + chunk * box;
+        if (t + 1 < w.tile + count) next = page_of(t + 1);
+        const int y = id >= 0 && id < a.n_pages ? (id * a.Hkv + h) * a.page + p % a.page : beyond;
+        if (use > 0 && !await(empty(slot), (use - 1) & 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full(slot), PL::kSlot);
+        __syncwarp();
+        if (mine) tma_load_2d(dst + slot * PL::kSlot, values ? &tm_v : &tm_k, cb * 64, y, full(slot), policy);
+        slot += 2;
+        if (slot >= NS) {
+          slot -= NS;
+          ++use;
+        }
+      }
+      if (!ok) break;
+      w.advance(a, count);
+      more = w.more();
+    }
+    // After a timeout the copies whose consumers gave up have to land before the CTA
+    // ends (otherwise their consumers have seen them): the places of the last pass
+    // before the next one.
+    if (!ok)
+      for (int back = 2; back <= 2 * NS; back += 2) {
+        int s = slot - back, u = use;
+        while (s < 0) {
+          s += NS;
+          --u;
+        }
+        if (u < 0) break;
+        mbar_wait_bounded(full(s), u & 1, kAttnDrainNs);
+      }
+  } else if (warp == 7) {
+    // ---- segments: Q by 16-byte asynchronous copies, and what the others need to know ----
+    AttnWalk w;
+    bool more = w.start(a, blockIdx.x, lane);
+    for (int sg = 0;; ++sg) {
+      const int buf = seg_buf(sg);
+      if (sg >= q_bufs && !await(q_free(buf), seg_parity(sg - q_bufs))) break;
+      AttnSegment& g = segs[buf];
+      if (!more) {
+        if (lane == 0) {
+          g.count = 0;
+          mbar_arrive(q_full(buf));
+        }
+        break;
+      }
+      const int count = w.segment();
+      const int h = w.unit / a.row_tiles, r0 = (w.unit % a.row_tiles) * a.row_tile;
+      const int nr = min(a.row_tile, a.rows - r0);
+      const T* const q = static_cast<const T*>(a.q) + (long long)w.b * a.S * a.q_stride + h * a.G * D;
+      const uint32_t qb = base + buf * q_step;
+      for (int e = lane; e < nr * (D / 8); e += 32) {
+        const int rr = e / (D / 8), ch = e % (D / 8), s = (r0 + rr) / a.G, hd = r0 + rr - s * a.G;
+        const T* const src = q + s * a.q_stride + hd * D + ch * 8;
+        const uint32_t dst = qb + (ch >> 3) * q_block + swz128(rr, ch & 7);
+        // rows past n_rows: zeros, not read
+#pragma unroll
+        for (int c = 0; c < (SPREAD ? 4 : 1); ++c) cp_async16(dst + c * 4096, src, s < w.seq.n);
+      }
+      if (lane < a.S) g.words[lane] = attn_word(a, w.b, lane, w.seq.n);
+      // the segment's table entries
+      const int last = min((w.tile + count) * TK, w.seq.ctx + w.seq.n) - 1;  // its last position
+      const int32_t* const row = a.table + (size_t)w.b * a.max_pages;
+      bool absent = false;
+#pragma unroll 4
+      for (int e = w.tile * TK / a.page + lane; e <= last / a.page && last >= 0; e += 32) {
+        const int id = __ldg(row + e);
+        absent |= id < 0 || id >= a.n_pages;
+      }
+      absent = __any_sync(0xffffffffu, absent);
+      if (lane == 0) {
+        g.count = count;
+        g.b = w.b;
+        g.unit = w.unit;
+        g.tile = w.tile;
+        g.ctx = w.seq.ctx;
+        g.n = w.seq.n;
+        g.tiles = w.seq.tiles;
+        g.absent = absent;
+        if (w.seq.bad || absent) atomicOr(a.status, kDevErrIndex);
+      }
+      w.advance(a, count);
+      more = w.more();
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(buf));
+    }
+  } else if (warp == 1) {
+    // ---- MMA: every lane keeps the same state, one elected lane issues ----
+    constexpr uint32_t id_pv = idesc_16_f32(kBf16, 128, D, false, true);
+    // a negative scale negates Q in the product: the maximum is then over scale * s
+    const uint32_t id_qk = idesc_16_f32(kBf16, 128, TK, false, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
+    int ks = 0, ku = 0, vs = 1, vu = 0;  // ring places of the next keys and values
+    auto step2 = [&](int& s, int& u) {
+      s += 2;
+      if (s >= NS) {
+        s -= NS;
+        ++u;
+      }
+    };
+    auto qk = [&](int i, int buf, bool last) {  // S of tile i; last: of its segment
+      if (!pv_wait(i - 1)) return;              // the P that held these columns has been read
+      if (!await(full(ks), ku & 1)) return;
+      tc_fence_after();
+      const uint64_t qd = smem_desc_sw128(base + buf * q_step, 16, 1024);
+      const uint64_t kd = smem_desc_sw128(ring + ks * PL::kSlot, 16, 1024);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        tc_mma4_ss(tm + PL::kS + (i & 1) * TK, qd + (uint32_t)(j * (q_block >> 4)), kd + j * (TK * 128 >> 4), id_qk,
+                   j > 0);
+      tc_commit_elect(s_full(i & 1));
+      tc_commit_elect(empty(ks));
+      if (last) tc_commit_elect(q_free(buf));
+      step2(ks, ku);
+    };
+    int i = 0;
+    for (int sg = 0; ok; ++sg) {
+      const int buf = seg_buf(sg);
+      if (!await(q_full(buf), seg_parity(sg))) break;
+      const int count = __reduce_max_sync(0xffffffffu, *const_cast<volatile int*>(&segs[buf].count));
+      if (count == 0) break;
+      tc_fence_after();
+      qk(i, buf, count == 1);
+      for (int t = 0; ok && t < count; ++t, ++i) {
+        if (t + 1 < count) qk(i + 1, buf, t + 2 == count);
+        if (!await(full(vs), vu & 1) || !await(p_ready(i & 1), (i >> 1) & 1) || !pv_wait(i)) break;
+        tc_fence_after();
+        const uint64_t vd = smem_desc_sw128(ring + vs * PL::kSlot, TK * 128, 1024);
+#pragma unroll
+        for (int j = 0; j < TK / 64; ++j)
+          tc_mma4_ts(tm + PL::kO, tm + PL::kS + (i & 1) * TK + j * 32, vd + j * (4 * 2048 >> 4), id_pv, t > 0 || j > 0);
+        tc_commit_elect(pv_done);
+        tc_commit_elect(empty(vs));
+        step2(vs, vu);
+      }
+    }
+    // every MMA has ended before tensor memory is freed
+    tc_commit_elect(drain);
+    mbar_wait_bounded(drain, 0, kAttnDrainNs);
+  } else if ((warp & 3) < nq) {
+    // ---- softmax and outputs: a thread per row ----
+    const int quarter = warp & 3, r = SPREAD ? lane : quarter * 32 + lane;
+    const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
+    const int box = min(a.page, TK);
+    // a scale of 0 becomes one that leaves every finite score at 0 (times 0 a masked
+    // score would be NaN)
+    const float c = fmaxf(fabsf(a.scale_log2), 1e-36f);
+    // the softmax warps meet (a bounded wait, as every one here)
+    uint32_t meetings = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_met);
+      return await(rows_met, meetings++ & 1);
+    };
+    int i = 0, vs = 1, vu = 0;
+    for (int sg = 0; ok; ++sg) {
+      const int buf = seg_buf(sg);
+      if (!await(q_full(buf), seg_parity(sg))) break;
+      const AttnSegment& g = segs[buf];
+      const int count = g.count;
+      if (count == 0) break;
+      const int b = g.b, tile0 = g.tile, ctx = g.ctx, n = g.n, tiles = g.tiles, unit = g.unit, total = ctx + n;
+      const bool some_absent = g.absent != 0;
+      const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
+      const int nr = min(a.row_tile, a.rows - r0);
+      const int row = r0 + r, wr = row / a.G;
+      const bool live = r < nr && wr < n;
+      const uint32_t word = live ? g.words[wr] : 0u;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_free(buf));
+      const int32_t* const trow = a.table + (size_t)b * a.max_pages;
+      uint32_t* const pois = poison + (sg & 1) * D;
+      float m = -INFINITY, l = 0.f;  // reference maximum (log2 domain), sum of P relative to it
+      for (int t = tile0; t < tile0 + count; ++t, ++i) {
+        const int p0 = t * TK;
+        const bool edge = some_absent || p0 + TK > ctx;
+        if (!await(s_full(i & 1), (i >> 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t ts = tq + PL::kS + (i & 1) * TK;
+        const int j0 = SPREAD ? quarter * CW : 0;  // the warp's first column
+        uint32_t sr[CW];
+        if constexpr (CW == 16) {
+          tmem_ld16(ts + j0, sr);
+        } else {
+#pragma unroll
+          for (int j = 0; j < CW; j += 32) tmem_ld32(ts + j0 + j, sr + j);
+        }
+        tmem_wait_ld();
+        if (edge) {
+          uint32_t absent = 0;  // pages of the tile that cannot be followed, a bit each
+          if (some_absent) {
+            const int p = p0 + lane * box;
+            bool gone = false;
+            if (lane * box < TK && p < total) {
+              const int id = __ldg(trow + p / a.page);
+              gone = id < 0 || id >= a.n_pages;
+            }
+            absent = __ballot_sync(0xffffffffu, gone);
+          }
+#pragma unroll
+          for (int j = 0; j < CW; j += 32) {
+            uint32_t bits = live ? attn_visible(p0 + j0 + j, ctx, word) : 0u;
+            if (absent != 0) {
+              for (int e = 0; e < 32; e += 8)
+                if (absent >> ((j0 + j + e) / box) & 1) bits &= ~(0xffu << e);
+            }
+#pragma unroll
+            for (int e = 0; e < (CW < 32 ? CW : 32); ++e)
+              if (!(bits >> e & 1)) sr[j + e] = 0xff800000u;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(sr[j]);
+#pragma unroll
+        for (int j = 4; j < CW; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool grow = live && mt > m + 8.f;  // also from -inf to any number
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow && m != -INFINITY ? exp2_approx(m - mt) : 1.f;
+          if (grow) m = mt;
+          l *= f;
+          if (t > tile0 && __any_sync(0xffffffffu, f != 1.f)) {
+            if (!pv_wait(i)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+              uint32_t o[32];
+              tmem_ld32(tq + PL::kO + j, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tq + PL::kO + j, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? -6.f : m - 6.f;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < CW; j += 2) {
+          const float e0 = exp2_approx(fmaf(__uint_as_float(sr[j]), c, -ref));
+          const float e1 = exp2_approx(fmaf(__uint_as_float(sr[j + 1]), c, -ref));
+          l4[j & 2] += e0;
+          l4[(j & 2) + 1] += e1;
+          sr[j >> 1] = pack16<T>(e0, e1);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if constexpr (SPREAD) {  // the other positions' weights are zero in this copy of the rows
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (CW == 32) {
+              if (j == quarter) tmem_st16(ts + j * 16, reinterpret_cast<const uint32_t(&)[16]>(sr));
+              else tmem_st16(ts + j * 16, zero);
+            } else {
+              tmem_st8(ts + j * 8, j == quarter ? sr : zero);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < CW / 2; j += 32) tmem_st32(ts + j, sr + j);
+        }
+        if (edge) {
+          // clean V from the first window row to the end of the last page
+          const int from = max(ctx - p0, 0), to = min(TK, (int)(((uint32_t)total + a.page - 1) / a.page * a.page - p0));
+          if (from < to) {
+            if (!await(full(vs), vu & 1)) break;
+            const uint32_t vb = ring + vs * PL::kSlot;
+            bool wrote = false;
+            for (int e = from * (D / 8) + quarter * 32 + lane; e < to * (D / 8); e += 32 * nq) {
+              const int j = e / (D / 8), ch = e % (D / 8), p = p0 + j;
+              const uint32_t at = vb + (ch >> 3) * (TK * 128) + swz128(j, ch & 7);
+              if (p >= total) {
+                sts128(at, make_uint4(0, 0, 0, 0));
+                wrote = true;
+              } else {
+                const uint4 x = lds128(at);
+                uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                uint32_t bad = 0;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) bad |= nonfinite16<T>(xs[z]) << (2 * z);
+                if (bad) {
+#pragma unroll
+                  for (int z = 0; z < 8; ++z)
+                    if (bad >> z & 1) {
+                      atomicOr(pois + ch * 8 + z, 1u << (p - ctx));
+                      xs[z >> 1] &= z & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                  sts128(at, make_uint4(xs[0], xs[1], xs[2], xs[3]));
+                  misc[1 + (sg & 1)] = 1;
+                  wrote = true;
+                }
+              }
+            }
+            if (wrote) fence_proxy_async_smem();
+          }
+        }
+        vs += 2;
+        if (vs >= NS) {
+          vs -= NS;
+          ++vu;
+        }
+        if (!pv_wait(i)) break;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready(i & 1));
+      }
+      if (!ok) break;
+      const bool starts = tile0 == 0, final = starts && tile0 + count == tiles;
+      const size_t slot = 2 * (size_t)blockIdx.x + (starts ? 1 : 0);
+      const float mm = m == -INFINITY ? -INFINITY : m - 6.f;
+      if (!pv_wait(i)) break;  // every warp has delivered its last P: it is past the last segment's merge
+      tc_fence_after();
+      const bool poisoned = misc[1 + (sg & 1)] != 0;  // noted before the P that this P V waited for
+      if constexpr (SPREAD) {
+        // Merge the four copies: M = max m_q, out = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q,
+        // in rounds of the columns that the merge buffer holds.
+        const int cols = min(D, (kMergeBytes / 16 / a.row_tile - 4) / 32 * 32), pad = cols + 4;  // 32 at least
+        if (lane < nr) mstat[quarter * kSpreadRows + lane] = live ? make_float2(mm, l) : make_float2(-INFINITY, 0.f);
+        if (quarter == 0) mword[lane] = word;
+        for (int j0 = 0; j0 < D; j0 += cols) {
+          if (j0 > 0 && !meet()) break;  // the last round has been read
+          const int now = min(cols, D - j0);
+#pragma unroll 1
+          for (int j = 0; j < now; j += 32) {
+            uint32_t o[32];
+            tmem_ld32(tq + PL::kO + j0 + j, o);
+            tmem_wait_ld();
+            if (lane < nr) {
+              float4* const dst = reinterpret_cast<float4*>(merge + (quarter * a.row_tile + lane) * pad + j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            }
+          }
+          if (!meet()) break;
+          for (int e = quarter * 32 + lane; e < nr * (now / 4); e += 128) {
+            const int rr = e / (now / 4), j = e % (now / 4) * 4;
+            float mq[4], lq = 0.f, mo = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mq[q] = mstat[q * kSpreadRows + rr].x;
+              mo = fmaxf(mo, mq[q]);
+            }
+            const float ref = mo == -INFINITY ? 0.f : mo;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float f = exp2_approx(mq[q] - ref), lx = mstat[q * kSpreadRows + rr].y;
+              lq = fmaf(f, lx, lq);
+              const float4 y = *reinterpret_cast<const float4*>(merge + (q * a.row_tile + rr) * pad + j);
+              // a copy that saw nothing has weights 0 only: its O is 0 (or NaN by 0 * inf)
+              if (lx == 0.f) continue;
+              x.x = fmaf(f, y.x, x.x);
+              x.y = fmaf(f, y.y, x.y);
+              x.z = fmaf(f, y.z, x.z);
+              x.w = fmaf(f, y.w, x.w);
+            }
+            if (poisoned) {
+              float* const xs = &x.x;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t bits = pois[j0 + j + z] & mword[rr];
+                if (bits) xs[z] += poison_of<T>(a, trow, h, ctx, bits, j0 + j + z);
+              }
+            }
+            const int rw = r0 + rr, rs = rw / a.G;
+            const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
+            if (final) {
+              const float inv = lq == 0.f ? 0.f : 1.f / lq;
+              const uint2 y = lq == 0.f ? make_uint2(0u, 0u)
+                                        : make_uint2(pack16<T>(x.x * inv, x.y * inv), pack16<T>(x.z * inv, x.w * inv));
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + j0 + j) = y;
+              if (j0 + j == 0 && a.lse != nullptr)
+                a.lse[orow] = lq == 0.f ? -INFINITY : (mo + log2f(lq)) * 0.6931471805599453f;
+            } else {
+              reinterpret_cast<float4*>(a.part_o)[(slot * (D / 4) + (j0 + j) / 4) * a.row_tile + rr] = x;
+              if (j0 + j == 0)
+                *reinterpret_cast<float2*>(a.part_ml + (slot * a.row_tile + rr) * 2) = make_float2(mo, lq);
+            }
+          }
+        }
+        if (!ok) break;
+      } else {
+        const long long orow = ((long long)b * a.S + wr) * a.Hq + h * a.G + (row - wr * a.G);
+        const bool none = !live || l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        constexpr int OC = D < 128 ? D : 128;  // columns at once
+#pragma unroll 1
+        for (int j = 0; j < D; j += OC) {
+          uint32_t o[OC];
+#pragma unroll
+          for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
+          tmem_wait_ld();
+          if (poisoned) {
+#pragma unroll
+            for (int e = 0; e < OC; ++e) {
+              const uint32_t bits = pois[j + e] & word;
+              if (bits) o[e] = __float_as_uint(__uint_as_float(o[e]) + poison_of<T>(a, trow, h, ctx, bits, j + e));
+            }
+          }
+          if (r >= nr) continue;
+          if (final) {
+            uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);
+#pragma unroll
+            for (int e = 0; e < OC; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                y[z] = none ? 0u : pack16<T>(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+              dst[e / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+            float4* const dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + j / 4) * a.row_tile + r;
+#pragma unroll
+            for (int e = 0; e < OC; e += 4)
+              dst[(e / 4) * a.row_tile] = live ? make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                             __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]))
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        if (r < nr) {
+          if (final) {
+            if (a.lse != nullptr) a.lse[orow] = none ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+          } else {
+            *reinterpret_cast<float2*>(a.part_ml + (slot * a.row_tile + r) * 2) =
+                live ? make_float2(mm, l) : make_float2(-INFINITY, 0.f);
+          }
+        }
+      }
+      if (poisoned) {  // every warp has read the notes: clear them for the segment after the next
+        if (!meet()) break;
+        for (int e = quarter * 32 + lane; e < D; e += 32 * nq) pois[e] = 0;
+        if (quarter == 0 && lane == 0) misc[1 + (sg & 1)] = 0;
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+template <typename T, int D, bool SPREAD>
+cudaError_t attn_tc_launch(const CUtensorMap& k, const CUtensorMap& v, AttnArgs a, cudaStream_t st) {
+  using PL = AttnPlan<D, SPREAD>;
+  auto kernel = attn_tc_kernel<T, D, SPREAD>;
+  // two Q buffers where they cost the ring nothing (spread rows: two sets of up to 16
+  // in the buffer of 128), or leave it five slots (two and a half tiles)
+  a.q_bufs = SPREAD ? (a.row_tile <= 16 ? 2 : 1) : PL::slots(a.row_tile, 2) >= 5 ? 2 : 1;
+  a.slots = PL::slots(a.row_tile, a.q_bufs);
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(a.ctas), dim3(kAttnThreads), kAttnSmem, st, k, v, a);
+}
+
+}  // namespace
+
+// The instance for one 16-bit type.
+template <typename T>
+cudaError_t attn_tc_dispatch(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t st) {
+  const bool spread = a.row_tile <= kSpreadRows;
+  switch (a.D) {
+    case 64: return spread ? attn_tc_launch<T, 64, true>(k, v, a, st) : attn_tc_launch<T, 64, false>(k, v, a, st);
+    case 128: return spread ? attn_tc_launch<T, 128, true>(k, v, a, st) : attn_tc_launch<T, 128, false>(k, v, a, st);
+    default: return spread ? attn_tc_launch<T, 256, true>(k, v, a, st) : attn_tc_launch<T, 256, false>(k, v, a, st);
+  }
+}
+
+}  // namespace sdv

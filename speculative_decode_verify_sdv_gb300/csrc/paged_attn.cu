@@ -25,12 +25,6 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void from_float(float x, __half& y) { y = __float2half_rn(x); }
 __device__ __forceinline__ void from_float(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ---- append ---------------------------------------------------------------------------
 
 struct AppendArgs {
@@ -221,18 +215,25 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
 
 // ---- join -----------------------------------------------------------------------------
 
-// Adds the partials of the units that several CTAs shared, a thread per row and
-// four columns (a unit's rows side by side, as the partials lie):
-// M = max m_j, out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, in CTA order.
+// Adds the partials of the units that several CTAs shared:
+//   M = max m_j, out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
+// A thread per row and four columns (a unit's rows side by side, as the partials
+// lie) and quarter of the partials, eight loads in flight each: the partials sit in
+// L2, so latency is what there is to hide.  The order of the sums is fixed by the
+// split.
+constexpr int kJoinItems = 64, kJoinParts = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const AttnArgs a) {
+  __shared__ float4 so[kJoinParts][kJoinItems];
+  __shared__ float2 sml[kJoinParts][kJoinItems];
   const int lane = threadIdx.x & 31;
   griddep_wait();
   const int units = a.Hkv * a.row_tiles;
   const int b = blockIdx.x / units, unit = blockIdx.x % units;
   long long before = 0, all = 0;
   for (int s = lane; s < a.B; s += 32) {
-    const int t = attn_seq(a, s).tiles;
+    const int t = attn_seq(a, s).tiles + a.lead;
     all += t;
     if (s < b) before += t;
   }
@@ -242,36 +243,53 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
     before += __shfl_xor_sync(0xffffffffu, before, off);
   }
   const AttnSeq seq = attn_seq(a, b);
-  const long long total = all * units, first = before * units + (long long)unit * seq.tiles;
+  const long long total = all * units, first = before * units + (long long)unit * (seq.tiles + a.lead) + a.lead;
   const int live = attn_live_ctas(a, total);
   const int c0 = attn_owner(total, live, first), c1 = attn_owner(total, live, first + seq.tiles - 1);
   if (c0 == c1) return;
   const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
-  const int e = blockIdx.y * 128 + threadIdx.x, r = e % a.row_tile, d4 = e / a.row_tile;
-  if (d4 >= a.D / 4 || r >= a.rows - r0) return;
-  const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + r;
-  const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)d4 * a.row_tile + r;
-  const size_t step = (size_t)(a.D / 4) * a.row_tile;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, ml[(size_t)(2 * c + (c == c0)) * a.row_tile].x);
-  const float ref = m == -INFINITY ? 0.f : m;
+  const int item = threadIdx.x % kJoinItems, part = threadIdx.x / kJoinItems;
+  const int e = blockIdx.y * kJoinItems + item, r = e % a.row_tile, d4 = e / a.row_tile;
+  const bool mine = d4 < a.D / 4 && r < a.rows - r0;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const size_t slot = 2 * c + (c == c0);
-    const float2 s = ml[slot * a.row_tile];
-    const float4 x = po[slot * step];
-    const float f = exp2f(s.x - ref);  // 0 where the CTA saw nothing (max -inf)
-    l = fmaf(f, s.y, l);
-    if (f != 0.f) {
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+  float l = 0.f, m = -INFINITY;
+  auto add = [&](float m2, float l2, const float4& x) {  // one more partial (or sum of some)
+    if (m2 == -INFINITY && l2 == 0.f) return;            // it saw nothing
+    const float mn = fmaxf(m, m2), f = exp2f(m - mn), f2 = exp2f(m2 - mn);
+    m = mn;
+    l = l * f + l2 * f2;
+    o.x = o.x * f + x.x * f2;
+    o.y = o.y * f + x.y * f2;
+    o.z = o.z * f + x.z * f2;
+    o.w = o.w * f + x.w * f2;
+  };
+  if (mine) {
+    const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + r;
+    const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)d4 * a.row_tile + r;
+    const size_t step = (size_t)(a.D / 4) * a.row_tile;
+    const int per = (c1 - c0 + kJoinParts) / kJoinParts, from = c0 + part * per, to = min(from + per - 1, c1);
+    for (int c = from; c <= to; c += 8) {
+      float2 s[8];
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[k] = make_float2(-INFINITY, 0.f);
+        if (c + k <= to) {
+          const size_t slot = 2 * (size_t)(c + k) + (c + k == c0);
+          s[k] = __ldcg(ml + slot * a.row_tile);
+          x[k] = __ldcg(po + slot * step);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(s[k].x, s[k].y, x[k]);
     }
   }
+  so[part][item] = o;
+  sml[part][item] = make_float2(m, l);
+  __syncthreads();
+  if (part != 0 || !mine) return;
+#pragma unroll
+  for (int j = 1; j < kJoinParts; ++j) add(sml[j][item].x, sml[j][item].y, so[j][item]);
   const int row = r0 + r;
   const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -302,8 +320,8 @@ cudaError_t launch_attn_simple(int dtype, const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_join(int dtype, const AttnArgs& a, cudaStream_t st) {
   auto kernel = dtype == SDV_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
-  return launch_pdl(kernel, dim3(a.B * a.Hkv * a.row_tiles, (a.row_tile * (a.D / 4) + 127) / 128),
-                    dim3(128), 0, st, a);
+  return launch_pdl(kernel, dim3(a.B * a.Hkv * a.row_tiles, (a.row_tile * (a.D / 4) + kJoinItems - 1) / kJoinItems),
+                    dim3(kJoinItems * kJoinParts), 0, st, a);
 }
 
 }  // namespace sdv
@@ -437,6 +455,7 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   const bool tc = sdv::attn_tc_takes(a.D, a.page, (long long)a.n_pages * a.Hkv * a.page);
   set_rows(a, tc ? sdv::kAttnTcRows : sdv::kAttnSimpleRows);
   a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
+  a.lead = tc ? 2 : 1;
   a.ctas = tc ? sms : kSimplePerSm * sms;
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
   a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +

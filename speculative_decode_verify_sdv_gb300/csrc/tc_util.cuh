@@ -38,21 +38,42 @@ __host__ __device__ constexpr uint32_t idesc_16_f32(bool bf16, int m, int n, boo
          (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// One MMA (K = 16), A from shared memory / from tensor memory; issued by one thread.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Four MMAs (K = 16 each, 64 along the reduction) issued by one elected lane of a
+// converged warp; operands are the same in every lane.  _ss: A and B K-major in shared
+// memory, 32 bytes further each; _ts: A in tensor memory, 8 columns further each, B
+// MN-major in shared memory, 16 reduction indices (2048 bytes) further each.  The
+// first overwrites D unless `accumulate`.
+__device__ __forceinline__ void tc_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 ta, tb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 ta, %1, 2;\n\tadd.u64 tb, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t"
+      "add.u64 ta, %1, 4;\n\tadd.u64 tb, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t"
+      "add.u64 ta, %1, 6;\n\tadd.u64 tb, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 ta;\n\t.reg .b64 tb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 ta, %1, 8;\n\tadd.u64 tb, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, t;\n\t"
+      "add.u32 ta, %1, 16;\n\tadd.u64 tb, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, t;\n\t"
+      "add.u32 ta, %1, 24;\n\tadd.u64 tb, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+// Negates A in the product.
+constexpr uint32_t kIdescNegateA = 1u << 13;
 
 #define SDV_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), \
                      "=r"(v[o + 6]), "=r"(v[o + 7])
@@ -74,6 +95,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       SDV_W8(v, 0), SDV_W8(v, 8), SDV_W8(v, 16), SDV_W8(v, 24)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               SDV_W8(v, 0)
+               : "memory");
+}
 #undef SDV_R8
 #undef SDV_W8
 
@@ -81,6 +107,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
+
+// Asynchronous 16-byte copy to shared memory; zeros, and no read, where !read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // L2 policy of data that other CTAs read too.
 __device__ __forceinline__ uint64_t l2_policy_normal() {

@@ -167,6 +167,17 @@ def test_flat_and_sharp_softmax(sdv, dt, std):
     check(dt, ref, out, lse, d)
 
 
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128, 256, 48])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 1e-30, -3.0])
+def test_scales_of_any_sign(sdv, dt, d, scale):
+    ctx, n = [300], [4]
+    q, kp, vp, table = make(dt, 1, 4, 4, 2, d, 16, ctx, n, 15)
+    out, lse, _ = call(sdv, q, kp, vp, table, ctx, n, None, scale)
+    ref = mixing.attention(f64(q), f64(kp), f64(vp), table.tolist(), ctx, n, None, scale)
+    check(dt, ref, out, lse, d)
+
+
 @pytest.mark.parametrize("d,page", [(128, 16), (64, 64), (256, 32), (40, 16), (128, 12)])
 @pytest.mark.parametrize("order", ["rising", "falling"])
 def test_scores_that_rise_or_fall_along_the_cache(sdv, d, page, order):
