@@ -34,12 +34,14 @@ struct AttnArgs {
   int n_pages, page, max_pages;
   int rows;                 // S * G query rows of a kv head, row r = (window row r / G, head r % G)
   int row_tiles, row_tile;  // row tiles of a kv head, rows of one (the last may hold fewer)
+  int tile_wrows;           // tensor-core kernel: window rows of a row tile (row_tile / G)
   int tile;                 // cache positions per tile
   int lead;                 // weight of a unit beyond its tiles
   void* out;
   float* lse;               // or null
-  float* part_o;            // [2 * CTAs][row_tile][D]
+  float* part_o;            // [2 * CTAs][D / 4][row_tile][4]
   float* part_ml;           // [2 * CTAs][row_tile][2]: max (log2 domain), sum
+  unsigned* shared;         // [CTAs] arrivals at the unit whose first sharer a CTA is, or null: a join follows
   int* status;
   int ctas;                 // CTAs of the attention launch
   int slots, q_bufs;        // tensor-core kernel: ring slots, Q buffers
@@ -51,54 +53,61 @@ struct AttnSeq {
   bool bad;     // a length was out of range
 };
 
-__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int c, int n) {
   AttnSeq s;
   const long long cap = (long long)a.max_pages * a.page;
   const int most = cap > 0x7fffff00ll ? 0x7fffff00 : (int)cap;
-  const int c = __ldg(a.ctx + b);
-  const int n = a.n_rows != nullptr ? __ldg(a.n_rows + b) : a.S;
   s.ctx = min(max(c, 0), most);
   s.n = min(min(max(n, 0), a.S), most - s.ctx);
   s.bad = s.ctx != c || s.n != n;
-  s.tiles = max(1, (int)(((long long)s.ctx + s.n + a.tile - 1) / a.tile));
+  s.tiles = max(1, (int)(((unsigned)s.ctx + s.n + a.tile - 1) / (unsigned)a.tile));
   return s;
 }
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
+  return attn_seq(a, __ldg(a.ctx + b), a.n_rows != nullptr ? __ldg(a.n_rows + b) : a.S);
+}
 
-// Weight of all units.  Warp-collective; every lane gets the result.
-__device__ __forceinline__ long long attn_total(const AttnArgs& a, int lane) {
-  long long sum = 0;
-  for (int b = lane; b < a.B; b += 32) sum += attn_seq(a, b).tiles + a.lead;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  return sum * a.Hkv * a.row_tiles;
+// x * y / z and x / z with small numbers (the common case) in 32 bits: a 64-bit
+// division takes most of a microsecond of a lone warp's time.
+__device__ __forceinline__ long long muldiv(long long x, int y, long long z) {
+  const unsigned long long p = (unsigned long long)x * (unsigned)y;
+  return (p | (unsigned long long)z) >> 32 == 0 ? (long long)((unsigned)p / (unsigned)z) : (long long)(p / z);
 }
 
 __device__ __forceinline__ int attn_live_ctas(const AttnArgs& a, long long total) {
   return total < a.ctas ? (int)total : a.ctas;
 }
 // Start of CTA c's range, and the CTA whose range holds place w.
-__device__ __forceinline__ long long attn_first(long long total, int live, int c) { return c * total / live; }
+__device__ __forceinline__ long long attn_first(long long total, int live, int c) { return muldiv(total, c, live); }
 __device__ __forceinline__ int attn_owner(long long total, int live, long long w) {
-  return (int)(((w + 1) * live - 1) / total);
+  const unsigned long long p = (unsigned long long)(w + 1) * (unsigned)live - 1;
+  return (int)((p | (unsigned long long)total) >> 32 == 0 ? (unsigned)p / (unsigned)total : p / total);
 }
 
 // A CTA's way through its range, one segment (part of a unit) after another.
 struct AttnWalk {
-  long long at, end;  // place of the next tile, end of the CTA's range
+  long long total, at, end;  // all weight; place of the next tile, end of the CTA's range
+  int live;                  // CTAs with a range
   int b, unit, tile;  // of the next tile: sequence, unit within it, tile within the unit
   AttnSeq seq;
+  int next_ctx, next_n;  // lengths of sequence b + 1, loaded ahead of their use
 
   // Warp-collective.  False where the CTA has nothing to do.
   __device__ __forceinline__ bool start(const AttnArgs& a, int cta, int lane) {
-    const long long total = attn_total(a, lane);
-    const int live = attn_live_ctas(a, total);
+    const int units = a.Hkv * a.row_tiles;
+    // the first 32 sequences' weights serve for the total and for the search
+    const long long w0 = lane < a.B ? ((long long)attn_seq(a, lane).tiles + a.lead) * units : 0;
+    total = w0;
+    for (int s = lane + 32; s < a.B; s += 32) total += ((long long)attn_seq(a, s).tiles + a.lead) * units;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    live = attn_live_ctas(a, total);
     if (cta >= live) return false;
     at = attn_first(total, live, cta);
     end = attn_first(total, live, cta + 1);
-    const int units = a.Hkv * a.row_tiles;
     long long before = 0;  // weight of the sequences before this group of 32
     for (int b0 = 0;; b0 += 32) {
-      const long long mine = b0 + lane < a.B ? ((long long)attn_seq(a, b0 + lane).tiles + a.lead) * units : 0;
+      const long long mine = b0 == 0 ? w0 : b0 + lane < a.B ? ((long long)attn_seq(a, b0 + lane).tiles + a.lead) * units : 0;
       long long incl = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -115,15 +124,21 @@ struct AttnWalk {
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     seq = attn_seq(a, b);
+    load_next(a);
     const long long rest = at - before;
     const int weight = seq.tiles + a.lead;
-    unit = (int)(rest / weight);
-    const int place = (int)(rest % weight);
+    unit = (int)muldiv(rest, 1, weight);
+    const int place = (int)(rest - (long long)unit * weight);
     tile = place > a.lead ? place - a.lead : 0;
     at += tile + a.lead - place;
     return at < end;
   }
   __device__ __forceinline__ bool more() const { return at < end; }
+  // The first and the last CTA with tiles of the unit that the next tile is in.
+  __device__ __forceinline__ void sharers(int& first, int& last) const {
+    first = attn_owner(total, live, at - tile);
+    last = attn_owner(total, live, at - tile + seq.tiles - 1);
+  }
   // Tiles of the segment that starts at the next tile.
   __device__ __forceinline__ int segment() const {
     const long long left = end - at;
@@ -137,7 +152,35 @@ struct AttnWalk {
     at += a.lead;
     if (++unit < a.Hkv * a.row_tiles) return;
     unit = 0;
-    if (++b < a.B) seq = attn_seq(a, b);
+    if (++b < a.B) {
+      seq = attn_seq(a, next_ctx, next_n);
+      load_next(a);
+    }
+  }
+  __device__ __forceinline__ void load_next(const AttnArgs& a) {
+    const bool is = b + 1 < a.B;
+    next_ctx = is ? __ldg(a.ctx + b + 1) : 0;
+    next_n = is && a.n_rows != nullptr ? __ldg(a.n_rows + b + 1) : a.S;
+  }
+};
+
+// Softmax sums of four columns, partial by partial (m: reference maximum in the log2
+// domain, l and o relative to it; a partial that saw nothing is (-inf, 0)).
+struct AttnSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float m2, float l2, const float4& x) {
+    if (m2 == -INFINITY && l2 == 0.f) return;
+    const float mn = fmaxf(m, m2), f = exp2f(m - mn), f2 = exp2f(m2 - mn);
+    m = mn;
+    l = l * f + l2 * f2;
+    o.x = o.x * f + x.x * f2;
+    o.y = o.y * f + x.y * f2;
+    o.z = o.z * f + x.z * f2;
+    o.w = o.w * f + x.w * f2;
+  }
+  __device__ __forceinline__ float lse() const {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 };
 

@@ -4,8 +4,8 @@
 
 namespace sdv {
 
-cudaError_t attn_tc_bf16(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t st) {
-  return attn_tc_dispatch<__nv_bfloat16>(k, v, a, st);
+cudaError_t attn_tc_bf16(const AttnMaps& m, const AttnArgs& a, cudaStream_t st) {
+  return attn_tc_dispatch<__nv_bfloat16>(m, a, st);
 }
 
 }  // namespace sdv

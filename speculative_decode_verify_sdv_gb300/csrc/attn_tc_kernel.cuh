@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -68,9 +69,11 @@ constexpr int kMergeBytes = 4 * kSpreadRows * (32 + 4) * 4;
 // What a segment is, from warp 7 to the MMA and softmax warps.
 struct AttnSegment {
   int count;  // tiles; 0: no more segments
-  int b, unit, tile, ctx, n, tiles;
-  int absent;          // a table entry of the segment cannot be followed
+  int b, h, r0, tile, ctx, n;
+  int flags;           // 1: the unit ends here; 2: a table entry of the segment cannot be followed
+  int first, last;     // the CTAs that share the unit
   uint32_t words[32];  // visibility of the window rows
+  int pad[2];
 };
 
 // Shared memory: the Q buffers, the ring, small things.  The MMA reads 128 rows of a
@@ -122,10 +125,13 @@ __device__ __forceinline__ uint32_t attn_visible(int p, int ctx, uint32_t word) 
   return bits;
 }
 
+// x / g for 0 <= x < 2^16 and 1 <= g <= 128, from 1 / g: x + 1/2 is at least 1/(2 g)
+// of a quotient away from the next, more than the error of two roundings.
+__device__ __forceinline__ int small_div(int x, float inv_g) { return (int)(((float)x + 0.5f) * inv_g); }
+
 template <typename T, int D, bool SPREAD>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const AttnArgs a) {
+    attn_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   using PL = AttnPlan<D, SPREAD>;
   constexpr int TK = PL::TK;
   constexpr int CW = SPREAD ? TK / 4 : TK;  // score columns of a softmax warp
@@ -149,7 +155,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t pv_done = bars + 8u * (kB + 8), drain = pv_done + 8, rows_met = pv_done + 16;
   uint32_t* const poison = reinterpret_cast<uint32_t*>(sp);  // [2][D]
   AttnSegment* const segs = reinterpret_cast<AttnSegment*>(sp + 2 * D * 4 + PL::kNumBars * 8);
-  volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);  // tmem base, poison seen [2]
+  // tmem base, poison seen [2], shared units: arrivals made and whether this was the last
+  volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);
   float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 4));
   float2* const mstat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + kMergeBytes);  // [4][32]
   uint32_t* const mword = reinterpret_cast<uint32_t*>(mstat + 4 * kSpreadRows);
@@ -174,11 +181,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(drain, 1);
     mbar_init(rows_met, nq);
     fence_barrier_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
   for (int e = threadIdx.x; e < 2 * D; e += kAttnThreads) poison[e] = 0;
-  if (threadIdx.x < 2) misc[1 + threadIdx.x] = 0;
+  if (threadIdx.x < 3) misc[1 + threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -211,6 +219,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     AttnWalk w;
     const bool values = warp == 6;
     const int box = min(a.page, TK), chunks = TK / box;  // rows per box, pages (or page parts) per tile
+    const int page_log = 31 - __clz(a.page);
     const int beyond = a.n_pages * a.Hkv * a.page;       // a row past the tensor map's end: zeros
     const uint64_t policy = a.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_normal();
     const int cb = lane % PL::kBlocks, chunk = lane / PL::kBlocks;
@@ -225,21 +234,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int32_t* const row = a.table + (size_t)w.b * a.max_pages;
       auto page_of = [&](int t) {
         const int p = t * TK + chunk * box;
-        return mine && p < total ? __ldg(row + p / a.page) : -1;
+        return mine && p < total ? __ldg(row + (p >> page_log)) : -1;
       };
-      int next = page_of(w.tile);
-      for (int t = w.tile; t < w.tile + count; ++t) {
-        const int id = next, p = t * TK + chunk * box;
-        if (t + 1 < w.tile + count) next = page_of(t + 1);
-        const int y = id >= 0 && id < a.n_pages ? (id * a.Hkv + h) * a.page + p % a.page : beyond;
-        if (use > 0 && !await(empty(slot), (use - 1) & 1)) break;
-        if (lane == 0) mbar_arrive_expect_tx(full(slot), PL::kSlot);
-        __syncwarp();
-        if (mine) tma_load_2d(dst + slot * PL::kSlot, values ? &tm_v : &tm_k, cb * 64, y, full(slot), policy);
-        slot += 2;
-        if (slot >= NS) {
-          slot -= NS;
-          ++use;
+      // table entries are loaded four tiles ahead
+      const int end = w.tile + count;
+      int ids[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ids[k] = w.tile + k < end ? page_of(w.tile + k) : -1;
+      for (int t0 = w.tile; ok && t0 < end; t0 += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = t0 + k;
+          if (t >= end) break;
+          const int id = ids[k], p = t * TK + chunk * box;
+          ids[k] = t + 4 < end ? page_of(t + 4) : -1;
+          const int y = id >= 0 && id < a.n_pages ? (id * a.Hkv + h) * a.page + (p & (a.page - 1)) : beyond;
+          if (use > 0 && !await(empty(slot), (use - 1) & 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(full(slot), PL::kSlot);
+          __syncwarp();
+          if (mine)
+            tma_load_2d(dst + slot * PL::kSlot, values ? &maps.v : &maps.k, cb * 64, y, full(slot), policy);
+          slot += 2;
+          if (slot >= NS) {
+            slot -= NS;
+            ++use;
+          }
         }
       }
       if (!ok) break;
@@ -260,8 +279,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_wait_bounded(full(s), u & 1, kAttnDrainNs);
       }
   } else if (warp == 7) {
-    // ---- segments: Q by 16-byte asynchronous copies, and what the others need to know ----
+    // ---- segments: Q by TMA, and what the others need to know ----
     AttnWalk w;
+    const int page_log = 31 - __clz(a.page);
+    const uint64_t policy = l2_policy_normal();
+    constexpr int kCopies = SPREAD ? 4 : 1;
+    uint32_t staged = 0;  // segments whose Q was asked for
     bool more = w.start(a, blockIdx.x, lane);
     for (int sg = 0;; ++sg) {
       const int buf = seg_buf(sg);
@@ -275,47 +298,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         break;
       }
       const int count = w.segment();
-      const int h = w.unit / a.row_tiles, r0 = (w.unit % a.row_tiles) * a.row_tile;
-      const int nr = min(a.row_tile, a.rows - r0);
-      const T* const q = static_cast<const T*>(a.q) + (long long)w.b * a.S * a.q_stride + h * a.G * D;
-      const uint32_t qb = base + buf * q_step;
-      for (int e = lane; e < nr * (D / 8); e += 32) {
-        const int rr = e / (D / 8), ch = e % (D / 8), s = (r0 + rr) / a.G, hd = r0 + rr - s * a.G;
-        const T* const src = q + s * a.q_stride + hd * D + ch * 8;
-        const uint32_t dst = qb + (ch >> 3) * q_block + swz128(rr, ch & 7);
-        // rows past n_rows: zeros, not read
-#pragma unroll
-        for (int c = 0; c < (SPREAD ? 4 : 1); ++c) cp_async16(dst + c * 4096, src, s < w.seq.n);
-      }
-      if (lane < a.S) g.words[lane] = attn_word(a, w.b, lane, w.seq.n);
+      const int h = w.unit / a.row_tiles, rt = w.unit - h * a.row_tiles;
       // the segment's table entries
       const int last = min((w.tile + count) * TK, w.seq.ctx + w.seq.n) - 1;  // its last position
       const int32_t* const row = a.table + (size_t)w.b * a.max_pages;
       bool absent = false;
+      if (last >= 0) {
 #pragma unroll 4
-      for (int e = w.tile * TK / a.page + lane; e <= last / a.page && last >= 0; e += 32) {
-        const int id = __ldg(row + e);
-        absent |= id < 0 || id >= a.n_pages;
+        for (int e = (w.tile * TK >> page_log) + lane; e <= last >> page_log; e += 32) {
+          const int id = __ldg(row + e);
+          absent |= id < 0 || id >= a.n_pages;
+        }
       }
+      if (lane < a.S) g.words[lane] = attn_word(a, w.b, lane, w.seq.n);
       absent = __any_sync(0xffffffffu, absent);
+      __syncwarp();
       if (lane == 0) {
         g.count = count;
         g.b = w.b;
-        g.unit = w.unit;
+        g.h = h;
+        g.r0 = rt * a.row_tile;
         g.tile = w.tile;
         g.ctx = w.seq.ctx;
         g.n = w.seq.n;
-        g.tiles = w.seq.tiles;
-        g.absent = absent;
+        g.flags = (w.tile + count == w.seq.tiles ? 1 : 0) | (absent ? 2 : 0);
+        w.sharers(g.first, g.last);
         if (w.seq.bad || absent) atomicOr(a.status, kDevErrIndex);
+        mbar_arrive_expect_tx(q_full(buf), kCopies * PL::kBlocks * a.row_tile * 128);
       }
+      __syncwarp();
+      if (lane < kCopies * PL::kBlocks)  // rows past n_rows or S: whatever lies there, for rows that give 0
+        tma_load_3d(base + buf * q_step + (lane / kCopies) * q_block + lane % kCopies * 4096, &maps.q,
+                    lane / kCopies * 64, h * a.G, w.b * a.S + rt * a.tile_wrows, q_full(buf), policy);
+      ++staged;
       w.advance(a, count);
       more = w.more();
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(buf));
     }
+    if (!ok && staged > 0) mbar_wait_bounded(q_full(seg_buf(staged - 1)), seg_parity(staged - 1), kAttnDrainNs);
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
     constexpr uint32_t id_pv = idesc_16_f32(kBf16, 128, D, false, true);
@@ -383,6 +402,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(rows_met);
       return await(rows_met, meetings++ & 1);
     };
+    const float inv_g = 1.f / (float)a.G;
     int i = 0, vs = 1, vu = 0;
     for (int sg = 0; ok; ++sg) {
       const int buf = seg_buf(sg);
@@ -390,11 +410,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const AttnSegment& g = segs[buf];
       const int count = g.count;
       if (count == 0) break;
-      const int b = g.b, tile0 = g.tile, ctx = g.ctx, n = g.n, tiles = g.tiles, unit = g.unit, total = ctx + n;
-      const bool some_absent = g.absent != 0;
-      const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
+      const int b = g.b, tile0 = g.tile, ctx = g.ctx, n = g.n, h = g.h, r0 = g.r0, total = ctx + n;
+      const bool some_absent = g.flags & 2, ends = g.flags & 1;
+      const int g_first = g.first, g_last = g.last;
       const int nr = min(a.row_tile, a.rows - r0);
-      const int row = r0 + r, wr = row / a.G;
+      const int row = r0 + r, wr = small_div(row, inv_g);
       const bool live = r < nr && wr < n;
       const uint32_t word = live ? g.words[wr] : 0u;
       __syncwarp();
@@ -538,7 +558,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(p_ready(i & 1));
       }
       if (!ok) break;
-      const bool starts = tile0 == 0, final = starts && tile0 + count == tiles;
+      const bool starts = tile0 == 0, final = starts && ends;
       const size_t slot = 2 * (size_t)blockIdx.x + (starts ? 1 : 0);
       const float mm = m == -INFINITY ? -INFINITY : m - 6.f;
       if (!pv_wait(i)) break;  // every warp has delivered its last P: it is past the last segment's merge
@@ -554,15 +574,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (j0 > 0 && !meet()) break;  // the last round has been read
           const int now = min(cols, D - j0);
 #pragma unroll 1
-          for (int j = 0; j < now; j += 32) {
-            uint32_t o[32];
+          for (int j = 0; j < now; j += 64) {
+            uint32_t o[64];
             tmem_ld32(tq + PL::kO + j0 + j, o);
+            if (j + 32 < now) tmem_ld32(tq + PL::kO + j0 + j + 32, o + 32);
             tmem_wait_ld();
             if (lane < nr) {
               float4* const dst = reinterpret_cast<float4*>(merge + (quarter * a.row_tile + lane) * pad + j);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+              for (int e = 0; e < 16; ++e)
+                if (e < 8 || j + 32 < now) dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                      __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
             }
           }
@@ -597,7 +618,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (bits) xs[z] += poison_of<T>(a, trow, h, ctx, bits, j0 + j + z);
               }
             }
-            const int rw = r0 + rr, rs = rw / a.G;
+            const int rw = r0 + rr, rs = small_div(rw, inv_g);
             const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
             if (final) {
               const float inv = lq == 0.f ? 0.f : 1.f / lq;
@@ -614,6 +635,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
         if (!ok) break;
+        if (a.shared != nullptr && !final) {
+          // The last CTA of a shared unit to arrive adds all its partials, in CTA order
+          // (the sharers' count wraps to 0 with it); a launch of its own for what one
+          // SM reads in a microsecond would take longer.
+          __threadfence();
+          if (!meet()) break;
+          const int first = g_first, last = g_last;
+          if (quarter == 0 && lane == 0) {
+            const unsigned before = atomicInc(a.shared + first, (unsigned)(last - first));
+            misc[3] = (misc[3] & ~1u) + 2u + (before == (unsigned)(last - first) ? 1u : 0u);
+          }
+          if (!meet()) break;
+          if (misc[3] & 1u) {
+            __threadfence();
+            for (int e = quarter * 32 + lane; e < nr * (D / 4); e += 128) {
+              const int rr = e / (D / 4), j = e % (D / 4);
+              const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + rr;
+              const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)j * a.row_tile + rr;
+              const size_t step = (size_t)(D / 4) * a.row_tile;
+              AttnSum sum;
+              for (int k0 = first; k0 <= last; k0 += 8) {
+                float2 sx[8];
+                float4 ox[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  sx[k] = make_float2(-INFINITY, 0.f);
+                  if (k0 + k <= last) {
+                    const size_t from = 2 * (size_t)(k0 + k) + (k0 + k == first);
+                    sx[k] = __ldcg(ml + from * a.row_tile);
+                    ox[k] = __ldcg(po + from * step);
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum.add(sx[k].x, sx[k].y, ox[k]);
+              }
+              const int rw = r0 + rr, rs = small_div(rw, inv_g);
+              const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
+              const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + j * 4) =
+                  sum.l == 0.f ? make_uint2(0u, 0u)
+                               : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv),
+                                            pack16<T>(sum.o.z * inv, sum.o.w * inv));
+              if (j == 0 && a.lse != nullptr) a.lse[orow] = sum.lse();
+            }
+          }
+        }
       } else {
         const long long orow = ((long long)b * a.S + wr) * a.Hq + h * a.G + (row - wr * a.G);
         const bool none = !live || l == 0.f;
@@ -670,7 +737,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok) && a.shared != nullptr && warp == 0) {
+    // After a timeout: the arrivals that were not made, so that the counts are back at 0
+    // when every CTA has ended.
+    AttnWalk w;
+    int made = misc[3] >> 1;
+    for (bool more = w.start(a, blockIdx.x, lane); more; more = w.more()) {
+      const int count = w.segment();
+      int first, last;
+      w.sharers(first, last);
+      if (first != last && --made < 0 && lane == 0) atomicInc(a.shared + first, (unsigned)(last - first));
+      w.advance(a, count);
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
@@ -678,29 +757,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 template <typename T, int D, bool SPREAD>
-cudaError_t attn_tc_launch(const CUtensorMap& k, const CUtensorMap& v, AttnArgs a, cudaStream_t st) {
+cudaError_t attn_tc_launch(const AttnMaps& m, AttnArgs a, cudaStream_t st) {
   using PL = AttnPlan<D, SPREAD>;
   auto kernel = attn_tc_kernel<T, D, SPREAD>;
   // two Q buffers where they cost the ring nothing (spread rows: two sets of up to 16
   // in the buffer of 128), or leave it five slots (two and a half tiles)
   a.q_bufs = SPREAD ? (a.row_tile <= 16 ? 2 : 1) : PL::slots(a.row_tile, 2) >= 5 ? 2 : 1;
   a.slots = PL::slots(a.row_tile, a.q_bufs);
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+  // more than half an SM's: one CTA and one tensor-memory allocation per SM
+  const int smem = 1024 + PL::kSmall + PL::q_bytes(a.row_tile, a.q_bufs) + a.slots * PL::kSlot;
+  static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(a.ctas), dim3(kAttnThreads), kAttnSmem, st, k, v, a);
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kAttnSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3(a.ctas), dim3(kAttnThreads), smem, st, m, a);
 }
 
 }  // namespace
 
 // The instance for one 16-bit type.
 template <typename T>
-cudaError_t attn_tc_dispatch(const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t st) {
+cudaError_t attn_tc_dispatch(const AttnMaps& m, const AttnArgs& a, cudaStream_t st) {
   const bool spread = a.row_tile <= kSpreadRows;
   switch (a.D) {
-    case 64: return spread ? attn_tc_launch<T, 64, true>(k, v, a, st) : attn_tc_launch<T, 64, false>(k, v, a, st);
-    case 128: return spread ? attn_tc_launch<T, 128, true>(k, v, a, st) : attn_tc_launch<T, 128, false>(k, v, a, st);
-    default: return spread ? attn_tc_launch<T, 256, true>(k, v, a, st) : attn_tc_launch<T, 256, false>(k, v, a, st);
+    case 64: return spread ? attn_tc_launch<T, 64, true>(m, a, st) : attn_tc_launch<T, 64, false>(m, a, st);
+    case 128: return spread ? attn_tc_launch<T, 128, true>(m, a, st) : attn_tc_launch<T, 128, false>(m, a, st);
+    default: return spread ? attn_tc_launch<T, 256, true>(m, a, st) : attn_tc_launch<T, 256, false>(m, a, st);
   }
 }
 

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
   __shared__ float4 so[kJoinParts][kJoinItems];
   __shared__ float2 sml[kJoinParts][kJoinItems];
   const int lane = threadIdx.x & 31;
-  griddep_wait();
+  // The split first, before the attention launch has ended: lengths are inputs, and
+  // whatever wrote them had ended before that launch let this one start.
   const int units = a.Hkv * a.row_tiles;
   const int b = blockIdx.x / units, unit = blockIdx.x % units;
   long long before = 0, all = 0;
@@ -246,23 +247,13 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
   const long long total = all * units, first = before * units + (long long)unit * (seq.tiles + a.lead) + a.lead;
   const int live = attn_live_ctas(a, total);
   const int c0 = attn_owner(total, live, first), c1 = attn_owner(total, live, first + seq.tiles - 1);
+  griddep_wait();
   if (c0 == c1) return;
   const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
   const int item = threadIdx.x % kJoinItems, part = threadIdx.x / kJoinItems;
   const int e = blockIdx.y * kJoinItems + item, r = e % a.row_tile, d4 = e / a.row_tile;
   const bool mine = d4 < a.D / 4 && r < a.rows - r0;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f, m = -INFINITY;
-  auto add = [&](float m2, float l2, const float4& x) {  // one more partial (or sum of some)
-    if (m2 == -INFINITY && l2 == 0.f) return;            // it saw nothing
-    const float mn = fmaxf(m, m2), f = exp2f(m - mn), f2 = exp2f(m2 - mn);
-    m = mn;
-    l = l * f + l2 * f2;
-    o.x = o.x * f + x.x * f2;
-    o.y = o.y * f + x.y * f2;
-    o.z = o.z * f + x.z * f2;
-    o.w = o.w * f + x.w * f2;
-  };
+  AttnSum sum;
   if (mine) {
     const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + r;
     const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)d4 * a.row_tile + r;
@@ -281,25 +272,26 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) add(s[k].x, s[k].y, x[k]);
+      for (int k = 0; k < 8; ++k) sum.add(s[k].x, s[k].y, x[k]);
     }
   }
-  so[part][item] = o;
-  sml[part][item] = make_float2(m, l);
+  so[part][item] = sum.o;
+  sml[part][item] = make_float2(sum.m, sum.l);
   __syncthreads();
   if (part != 0 || !mine) return;
 #pragma unroll
-  for (int j = 1; j < kJoinParts; ++j) add(sml[j][item].x, sml[j][item].y, so[j][item]);
+  for (int j = 1; j < kJoinParts; ++j) sum.add(sml[j][item].x, sml[j][item].y, so[j][item]);
   const int row = r0 + r;
   const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const bool none = sum.l == 0.f;
+  const float inv = none ? 0.f : 1.f / sum.l;
   alignas(8) T y[4];
-  from_float(l == 0.f ? 0.f : o.x * inv, y[0]);
-  from_float(l == 0.f ? 0.f : o.y * inv, y[1]);
-  from_float(l == 0.f ? 0.f : o.z * inv, y[2]);
-  from_float(l == 0.f ? 0.f : o.w * inv, y[3]);
+  from_float(none ? 0.f : sum.o.x * inv, y[0]);
+  from_float(none ? 0.f : sum.o.y * inv, y[1]);
+  from_float(none ? 0.f : sum.o.z * inv, y[2]);
+  from_float(none ? 0.f : sum.o.w * inv, y[3]);
   *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * a.D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
-  if (d4 == 0 && a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (d4 == 0 && a.lse != nullptr) a.lse[orow] = sum.lse();
 }
 
 int simple_smem(int D) {
@@ -357,8 +349,18 @@ void set_rows(AttnArgs& a, int most) {
   a.row_tile = (a.rows + a.row_tiles - 1) / a.row_tiles;
 }
 
+// The tensor-core kernel's: whole window rows, at most 128 query rows.
+void set_window_rows(AttnArgs& a) {
+  const int most = a.G < sdv::kAttnTcRows ? sdv::kAttnTcRows / a.G : 1;
+  a.row_tiles = (a.S + most - 1) / most;
+  a.tile_wrows = (a.S + a.row_tiles - 1) / a.row_tiles;
+  a.row_tile = a.tile_wrows * a.G;
+}
+
+// Behind the header: arrival counts, (max, sum) partials, output partials.
+size_t count_bytes(int ctas) { return sdv::round_256((size_t)ctas * 4); }
 size_t part_bytes(int ctas, int row_tile, int D) {
-  return sdv::round_256((size_t)2 * ctas * row_tile * 8) + sdv::round_256((size_t)2 * ctas * row_tile * D * 4);
+  return count_bytes(ctas) + sdv::round_256((size_t)2 * ctas * row_tile * 8) + sdv::round_256((size_t)2 * ctas * row_tile * D * 4);
 }
 
 constexpr int kSimplePerSm = 2;
@@ -404,11 +406,13 @@ size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t 
     return 0;
   const int sms = sdv::sm_count();
   AttnArgs a{};
-  a.rows = S * (Hq / heads);
+  a.S = S;
+  a.G = Hq / heads;
+  a.rows = S * a.G;
   // the larger of the two kernels' needs: which one runs depends on the page size too
   set_rows(a, sdv::kAttnSimpleRows);
   const size_t simple = part_bytes(kSimplePerSm * (sms > 0 ? sms : 256), a.row_tile, dim);
-  set_rows(a, sdv::kAttnTcRows);
+  set_window_rows(a);
   const size_t tc = part_bytes(sms > 0 ? sms : 256, a.row_tile, dim);
   return sdv::kHeaderBytes + (simple > tc ? simple : tc);
 }
@@ -452,18 +456,25 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   a.status = static_cast<int*>(ws);
   const int sms = sdv::sm_count();
   if (sms <= 0) return SDV_ERR_CUDA;
-  const bool tc = sdv::attn_tc_takes(a.D, a.page, (long long)a.n_pages * a.Hkv * a.page);
-  set_rows(a, tc ? sdv::kAttnTcRows : sdv::kAttnSimpleRows);
+  const bool tc = sdv::attn_tc_takes(a.D, a.G, a.page, (long long)a.n_pages * a.Hkv * a.page);
+  if (tc) set_window_rows(a);
+  else set_rows(a, sdv::kAttnSimpleRows);
   a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
   a.lead = tc ? 2 : 1;
   a.ctas = tc ? sms : kSimplePerSm * sms;
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
+  char* const counts = static_cast<char*>(ws) + sdv::kHeaderBytes;
+  // Shared units are joined by their last CTA where a partial is at most 4 KB (single
+  // tokens): the GPU's time a call hardly changes (613 positions, 8 heads: 9.8 and
+  // 10.0 us) and the host issues one launch less (8.1 against 6.6 us).  Larger ones go
+  // to the join's many CTAs.
+  if (tc && a.row_tile * a.D <= 1024) a.shared = reinterpret_cast<unsigned*>(counts);
+  a.part_ml = reinterpret_cast<float*>(counts + count_bytes(a.ctas));
   a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
                                       sdv::round_256((size_t)2 * a.ctas * a.row_tile * 8));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = tc ? sdv::launch_attn_tc(cache->dtype, a, st) : sdv::launch_attn_simple(cache->dtype, a, st);
-  // the join, unless no unit can have more than one tile
-  if (e == cudaSuccess && (long long)a.max_pages * a.page > a.tile) e = sdv::launch_attn_join(cache->dtype, a, st);
+  // the join, unless the kernel joins or no unit can have more than one tile
+  if (e == cudaSuccess && a.shared == nullptr && (long long)a.max_pages * a.page > a.tile) e = sdv::launch_attn_join(cache->dtype, a, st);
   return sdv::status_of(e);
 }
 
