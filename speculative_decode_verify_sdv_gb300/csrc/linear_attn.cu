@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "host_util.h"
+#include "linear_args.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
 #include "sdv_kernels.h"
@@ -16,33 +17,10 @@ namespace sdv {
 
 namespace {
 
-struct LinArgs {
-  const void *q, *k, *v;
-  long long q_stride, k_stride, v_stride;
-  const float* g;
-  int g_token;             // 1: [B][T][H], 0: [H]
-  float scale;
-  int B, T, H, Hqk, Dk, Dv;
-  const int32_t* n_tokens;
-  const float* s_in;
-  float* s_out;
-  void* o;
-};
-
 __device__ __forceinline__ float lin_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float lin_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void lin_round(float x, __half& y) { y = __float2half_rn(x); }
 __device__ __forceinline__ void lin_round(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
-  return a.n_tokens != nullptr ? min(max(__ldg(a.n_tokens + b), 0), a.T) : a.T;
-}
-
-// The log decay of token t, head h: at most 0 (NaN stays NaN).
-__device__ __forceinline__ float lin_decay(const LinArgs& a, int b, int t, int h) {
-  const float g = __ldg(a.g + (a.g_token ? ((long long)b * a.T + t) * a.H + h : h));
-  return g > 0.f ? 0.f : g;
-}
 
 // Recurrent form: the state's definition, token by token.  A CTA holds 128 value
 // columns of one head's state in registers: lane l the columns 4l .. 4l+3, warp w
@@ -53,6 +31,7 @@ __device__ __forceinline__ float lin_decay(const LinArgs& a, int b, int t, int h
 constexpr int kRecWarps = 8;
 constexpr int kRecTokens = 8;  // tokens staged at once
 
+// With `repair` it recomputes the heads noted there and clears the notes.
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kRecWarps) linear_recurrent_kernel(const LinArgs a) {
   __shared__ float qs[kRecTokens][kRecWarps * R], ks[kRecTokens][kRecWarps * R];
@@ -60,6 +39,13 @@ __global__ void __launch_bounds__(32 * kRecWarps) linear_recurrent_kernel(const 
   __shared__ float ds[kRecTokens];
   __shared__ float4 red[kRecWarps][32];
   griddep_wait();
+  if (a.repair != nullptr) {  // (one block a head: Dv is at most 128 here)
+    int* const note = a.repair + (long long)blockIdx.z * a.H + blockIdx.y;
+    const bool noted = *note != 0;
+    __syncthreads();
+    if (!noted) return;
+    if (threadIdx.x == 0) *note = 0;
+  }
   const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.H / a.Hqk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 128 + lane * 4;  // value columns
@@ -155,6 +141,16 @@ bool lin_shape(int B, int T, int H, int Dk, int Dv) {
   return B >= 1 && T >= 1 && H >= 1 && Dk >= 8 && Dk % 8 == 0 && Dv >= 8 && Dv % 8 == 0;
 }
 
+// The chunked form's workspace: notes of heads to repair, the CTAs' local states.
+size_t lin_notes(int B, int H) { return round_256((size_t)B * H * 4); }
+size_t lin_parts(int ctas, int Dk, int Dv) { return round_256((size_t)ctas * 8) + (size_t)ctas * Dk * Dv * 4; }
+
+// The chunked form for the head sizes that it has and for kLinChunkFrom tokens or more.
+constexpr int kLinChunkFrom = 5;
+bool lin_chunked(int B, int T, int Dk, int Dv) {
+  return linear_tc_takes(Dk, Dv) && T >= kLinChunkFrom && (long long)B * T <= INT32_MAX - 2 * kLinChunk;
+}
+
 bool lin_limits(int B, int H, int Dk, int Dv) { return B <= 65535 && H <= 4096 && Dk <= 256 && Dv <= 256; }
 
 bool lin_rows(const void* p, long long stride, int heads, int dim) {
@@ -169,7 +165,9 @@ extern "C" {
 
 size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv) {
   if (!sdv::lin_shape(B, T, H, Dk, Dv) || !sdv::lin_limits(B, H, Dk, Dv)) return 0;
-  return sdv::kHeaderBytes;
+  if (!sdv::lin_chunked(B, T, Dk, Dv)) return sdv::kHeaderBytes;
+  const int sms = sdv::sm_count();
+  return sdv::kHeaderBytes + sdv::lin_notes(B, H) + sdv::lin_parts(sms > 0 ? sms : 256, Dk, Dv);
 }
 
 sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, const void* v, int64_t q_stride,
@@ -213,6 +211,17 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
   a.s_out = state_out_or_null;
   a.o = o_or_null;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (lin_chunked(B, T, Dk, Dv)) {
+    a.ctas = sm_count();
+    if (a.ctas <= 0) return SDV_ERR_CUDA;
+    char* const w8 = static_cast<char*>(ws);
+    a.status = reinterpret_cast<int*>(w8);
+    a.repair = reinterpret_cast<int*>(w8 + kHeaderBytes);
+    a.part_decay = reinterpret_cast<double*>(w8 + kHeaderBytes + lin_notes(B, H));
+    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_decay) + round_256((size_t)a.ctas * 8));
+    const cudaError_t e = launch_linear_tc(dtype, a, st);
+    if (e != cudaSuccess) return status_of(e);
+  }
   return status_of(dtype == SDV_F16 ? launch_recurrent<__half>(a, st) : launch_recurrent<__nv_bfloat16>(a, st));
 }
 

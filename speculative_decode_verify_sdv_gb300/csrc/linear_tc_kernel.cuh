@@ -1,0 +1,790 @@
+// Linear attention in chunks of 128 tokens on the 5th-generation tensor cores
+// (sm_103a): sdv_linear_attn for prompts and windows, key and value sizes 64 and 128.
+//
+// With G the cumulative log decay inside a chunk and M the state before it, per head:
+//   O_t  = scale (e^{G_t} q_t M + sum_{s <= t} (q_t . k_s) e^{G_t - G_s} v_s)
+//   M'   = e^{G_C} M + sum_s e^{G_C - G_s} k_s v_s^T
+// as four products of 128 x 128 tiles: Q K^T, Q M, P V (P the decayed scores) and
+// K~^T V (K~ the decayed keys).  Scores, both parts of the output and the state are
+// fp32 in tensor memory (128 + 3 Dv columns); the state never leaves it inside a run.
+//
+// Precision.  M is a sum over all tokens, so its terms are kept to 22 (fp16) or 16
+// (bf16) bits: K~ goes into the product as high and low part.  P and the copy of M
+// that Q multiplies are rounded to the 16-bit type once, as the values of a matrix
+// instruction have to be.  fp16 has neither the range of scores nor of states nor of
+// decayed keys, so each carries a power of two: P one per row, M's copy one per chunk,
+// K~ one per chunk (the state in tensor memory is kept in its units).  G is summed in
+// fp64 and used as differences (high and low float), so a token far behind a reset
+// loses nothing.
+//
+// The chunks of all heads are dealt to the CTAs in equal contiguous ranges.  A head
+// that several CTAs share needs its state at the start of each part: a first launch
+// computes each part's own contribution (keys and values alone), and in the second
+// one each CTA sums those before it, decayed, on its way in.
+//
+// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 zeros behind a sequence's end; 4-7 the
+// state (one thread per key row of M: 16-bit copy for Q M, decay); 8-11 the keys (K~ in
+// place and beside) and the cleaning of V; 12-15 scores to P, outputs.
+//
+// A zero weight must not meet an infinite value (0 * inf): a head with keys or values
+// that are not finite is noted, its state left unwritten, and the recurrent kernel,
+// launched behind, recomputes noted heads by the definition.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <type_traits>
+
+#include "linear_args.h"
+#include "sdv_kernels.h"
+#include "tc_util.cuh"
+
+namespace sdv {
+
+namespace {
+
+constexpr int kLC = kLinChunk;
+constexpr uint64_t kLinDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
+
+// Bits of |x|, 0 for an infinity or NaN.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t x) {
+  const uint32_t m = x & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
+}
+
+// Decay tables of a chunk.
+struct LinTables {
+  float hi[kLC], lo[kLC];  // G_t (log2 units)
+  float eg[kLC];           // e^{G_t}
+  float w[kLC];            // e^{G_C - G_s}
+  float rf[kLC];           // e^{G_t - G_r}, r the last token before t's block of 32
+  float cf[3][kLC];        // e^{G_r - G_s} for the blocks 1, 2, 3 (s <= r)
+  float dec;               // e^{G_C}
+  float pad[3];
+};
+
+template <int DK, int DV>
+struct LinPlan {
+  static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2, kSt = 128 * DV * 2;
+  static constexpr int oK = 0, oLo = oK + 2 * kK, oQ = oLo + kK, oV = oQ + kK, oSt = oV + kV;
+  static constexpr int oTab = oSt + kSt;
+  static constexpr int oBars = oTab + 2 * (int)sizeof(LinTables);
+  static constexpr int kNumBars = 24;
+  static constexpr int oMisc = oBars + kNumBars * 8;
+  static constexpr int kTotal = oMisc + 128 + 1024;  // the base is aligned to 1024
+  static constexpr int cS = 0, cO1 = 128, cO2 = 256, cM = 384;  // tensor-memory columns
+  static_assert(kTotal <= 232448, "shared memory");
+};
+
+// A CTA's way through its range of chunks; all lanes of a warp keep the same.
+struct LinWalk {
+  long long total, at, end;
+  int live, b, h, chunk, n, chunks;
+
+  static __device__ __forceinline__ int chunks_of(int n) { return n <= kLC ? 1 : (n + kLC - 1) / kLC; }
+  __device__ __forceinline__ void sequence(const LinArgs& a) {
+    n = lin_tokens(a, b);
+    chunks = chunks_of(n);
+  }
+  __device__ __forceinline__ bool start(const LinArgs& a, int cta, int lane) {
+    long long sum = 0;
+    for (int s = lane; s < a.B; s += 32) sum += chunks_of(lin_tokens(a, s));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    total = sum * a.H;
+    const long long most = (long long)kLinRuns * a.B * a.H;
+    live = (int)min((long long)a.ctas, min(total, most));
+    if (cta >= live) return false;
+    at = total * cta / live;
+    end = total * (cta + 1) / live;
+    long long before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const long long mine = b0 + lane < a.B ? (long long)chunks_of(lin_tokens(a, b0 + lane)) * a.H : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > at);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        before += __shfl_sync(0xffffffffu, incl - mine, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    sequence(a);
+    const long long rest = at - before;
+    h = (int)(rest / chunks);
+    chunk = (int)(rest - (long long)h * chunks);
+    // the first launch takes the range's last part alone, and that only if the head goes on
+    if (a.pass == 0) {
+      while (more() && chunk + count() == chunks) advance(a, count());
+    }
+    return more();
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ int count() const {  // chunks of the part that starts here
+    const long long left = end - at;
+    return left < chunks - chunk ? (int)left : chunks - chunk;
+  }
+  __device__ __forceinline__ void advance(const LinArgs& a, int c) {
+    at += c;
+    chunk += c;
+    if (chunk < chunks) return;
+    chunk = 0;
+    if (++h < a.H) return;
+    h = 0;
+    if (++b < a.B) sequence(a);
+  }
+  // The first CTA with chunks of the head.
+  __device__ __forceinline__ int first_cta() const { return (int)(((at - chunk + 1) * live - 1) / total); }
+};
+
+template <typename T, int DK, int DV, bool OUT>
+__global__ void __launch_bounds__(OUT ? 512 : 384, 1)
+    linear_tc_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
+  using PL = LinPlan<DK, DV>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kScaled = !kBf16;  // powers of two beside fp16 operands
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const sb = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  LinTables* const tabs = reinterpret_cast<LinTables*>(sb + PL::oTab);
+  const uint32_t bars = base + PL::oBars;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  const uint32_t q_full = bar(4), v_full = bar(5), s_full = bar(6), qm_done = bar(7), upd_done = bar(8),
+                 pv_done = bar(9), m_ready = bar(10), kv_ready = bar(11), p_ready = bar(12), o_free = bar(13),
+                 met = bar(14), met_m = bar(15), drain = bar(16);
+  auto k_full = [&](int i) { return bar(i & 1); };
+  auto tab_full = [&](int i) { return bar(2 + (i & 1)); };
+  auto tab_free = [&](int i) { return bar(18 + (i & 1)); };
+  auto ek_ready = [&](int i) { return bar(20 + (i & 1)); };
+  volatile int* const misc = reinterpret_cast<int*>(sb + PL::oMisc);
+  // misc: 0 tmem base; 2, 3 a part whose values are not all finite; 4, 5 exponent of K~;
+  // 6, 7 exponent of M's copy; 8-11 and 12-15 the warps' maxima of keys and of the state
+  volatile float* const fmisc = reinterpret_cast<volatile float*>(misc);
+
+  if (warp == 1) {
+    tmem_alloc(base + PL::oMisc, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
+    for (int i = 10; i < 16; ++i) mbar_init(bar(i), 4);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(18 + i), OUT ? 12 : 8);
+      mbar_init(bar(20 + i), 1);
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+    if (OUT) tma_prefetch_desc(&maps.q);
+  }
+  if (threadIdx.x >= 32 && threadIdx.x < 34) misc[2 + threadIdx.x - 32] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = misc[0];
+  griddep_wait();
+  griddep_launch_dependents();
+  bool ok = true;
+  auto await = [&](uint32_t b, uint32_t parity) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(b, parity))) {
+      ok = false;
+      if (lane == 0) atomicOr(a.status, kDevErrTimeout);
+    }
+    return ok;
+  };
+  auto arrive = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+  // Barriers that complete once a chunk: a role waits for every phase, in order, before
+  // the next can complete.
+  int upd_seen = 0, pv_seen = 0;
+  auto upd_wait = [&](int chunks) {
+    for (; upd_seen < chunks; ++upd_seen)
+      if (!await(upd_done, upd_seen & 1)) return false;
+    return true;
+  };
+  auto pv_wait = [&](int chunks) {
+    for (; pv_seen < chunks; ++pv_seen)
+      if (!await(pv_done, pv_seen & 1)) return false;
+    return true;
+  };
+  LinWalk w;
+  int i = 0;  // the CTA's chunk number
+
+  if (warp == 0) {
+    // ---- TMA ----
+    const uint64_t normal = l2_policy_normal();
+    const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
+    const int shared = a.H / a.Hqk;
+    int asked_q = 0, asked_v = 0;
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count(), hk = w.h / shared;
+      for (int c = 0; c < count; ++c, ++i) {
+        const int z = w.b * a.T + (w.chunk + c) * kLC;
+        // (phase i - 2 of upd_done has been seen by the values of chunk i - 1)
+        if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
+        __syncwarp();
+        if (lane < DK / 64)
+          tma_load_3d(base + PL::oK + (i & 1) * PL::kK + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
+        if (OUT) {
+          if (i > 0 && !await(qm_done, (i - 1) & 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, PL::kK);
+          __syncwarp();
+          if (lane < DK / 64) tma_load_3d(base + PL::oQ + lane * 16384, &maps.q, lane * 64, hk, z, q_full, normal);
+          ++asked_q;
+        }
+        if (!upd_wait(i) || (OUT && !pv_wait(i))) break;
+        if (lane == 0) mbar_arrive_expect_tx(v_full, PL::kV);
+        __syncwarp();
+        if (lane < DV / 64) tma_load_3d(base + PL::oV + lane * 16384, &maps.v, lane * 64, w.h, z, v_full, v_policy);
+        ++asked_v;
+      }
+      if (!ok) break;
+      w.advance(a, count);
+    }
+    if (!ok) {  // copies whose consumers gave up have to land before the CTA ends
+      for (int e = i > 0 ? i - 1 : 0; e <= i; ++e) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
+      if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
+      if (asked_v > 0) mbar_wait_bounded(v_full, (asked_v - 1) & 1, kLinDrainNs);
+    }
+  } else if (warp == 1) {
+    // ---- MMA: every lane keeps the same state, one elected lane issues ----
+    constexpr uint32_t id_qk = idesc_16_f32(kBf16, 128, kLC, false, false);
+    constexpr uint32_t id_kb = idesc_16_f32(kBf16, 128, DV, false, true);  // Q M and P V
+    constexpr uint32_t id_up = idesc_16_f32(kBf16, 128, DV, true, true);
+    const uint64_t qd = smem_desc_sw128(base + PL::oQ, 16, 1024);
+    const uint64_t vd = smem_desc_sw128(base + PL::oV, 16384, 1024);
+    const uint64_t md = smem_desc_sw128(base + PL::oSt, 16384, 1024);
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count();
+      for (int c = 0; c < count; ++c, ++i) {
+        const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
+        if (OUT) {
+          // scores; P of the chunk before has been read
+          if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), (i >> 1) & 1)) break;
+          tc_fence_after();
+          const uint64_t kd = smem_desc_sw128(kb, 16, 1024);
+#pragma unroll
+          for (int j = 0; j < DK / 64; ++j)
+            tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
+          tc_commit_elect(s_full);
+        }
+        if (!await(m_ready, i & 1)) break;
+        if (OUT) {
+          // Q M over M's copy: 128 rows (at Dk = 64 the state's high and low part, both by Q)
+          if (i > 0 && !await(o_free, (i - 1) & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            tc_mma4_ss<2, 128>(tm + PL::cO1, qd + (DK == 128 ? j * 1024 : 0), md + j * 512, id_kb, j > 0);
+          tc_commit_elect(qm_done);
+        }
+        if (!await(kv_ready, i & 1)) break;
+        tc_fence_after();
+        if constexpr (DK == 128) {
+          const uint64_t hd = smem_desc_sw128(kb, 16384, 1024);
+          const uint64_t ld = smem_desc_sw128(base + PL::oLo, 16384, 1024);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, ld + j * 512, vd + j * 512, id_up, 1);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, hd + j * 512, vd + j * 512, id_up, 1);
+        } else {
+          // both parts at once: rows 0-63 from the high, 64-127 from the low part
+          const uint64_t kd = smem_desc_sw128(kb, base + PL::oLo - kb, 1024);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, kd + j * 512, vd + j * 512, id_up, 1);
+        }
+        tc_commit_elect(upd_done);
+        if (OUT) {
+          if (!await(p_ready, i & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tc_mma4_ts(tm + PL::cO2, tm + PL::cS + j * 32, vd + j * 512, id_kb, j > 0);
+          tc_commit_elect(pv_done);
+        }
+      }
+      if (!ok) break;
+      w.advance(a, count);
+    }
+    tc_commit_elect(drain);  // every MMA has ended before tensor memory is freed
+    mbar_wait_bounded(drain, 0, kLinDrainNs);
+  } else if (warp == 2) {
+    // ---- decay tables: four tokens a lane, sums in fp64 ----
+    double run = 0.0;  // log2 decay of the part so far
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count();
+      for (int c = 0; c < count; ++c, ++i) {
+        const int t0 = (w.chunk + c) * kLC, t = t0 + 4 * lane;
+        double g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = t + e < w.n ? lin_decay(a, w.b, t + e, w.h) : 0.f;
+          // -1e4 (a decay of 0 in fp32) for anything below; NaN stays
+          g[e] = (double)(x < -1e4f ? -1e4f : x) * 1.4426950408889634;
+        }
+#pragma unroll
+        for (int e = 1; e < 4; ++e) g[e] += g[e - 1];
+        double incl = g[3];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const double o = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += o;
+        }
+        double before = __shfl_up_sync(0xffffffffu, incl, 1);
+        if (lane == 0) before = 0.0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] += before;
+        const double all = __shfl_sync(0xffffffffu, incl, 31);
+        double ref[3];
+#pragma unroll
+        for (int e = 0; e < 3; ++e) ref[e] = __shfl_sync(0xffffffffu, incl, 8 * e + 7);
+        if (i >= 2 && !await(tab_free(i), ((i - 2) >> 1) & 1)) break;
+        LinTables& tb = tabs[i & 1];
+        const int blk = lane >> 3;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = 4 * lane + e;
+          const float hi = (float)g[e];
+          tb.hi[s] = hi;
+          tb.lo[s] = (float)(g[e] - (double)hi);
+          tb.eg[s] = exp2f(hi);
+          tb.w[s] = exp2f((float)(all - g[e]));
+          if (OUT) {
+            const double r = blk == 0 ? g[e] : blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2];
+            tb.rf[s] = exp2f((float)(g[e] - r));
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+              if (blk <= q) tb.cf[q][s] = exp2f((float)(ref[q] - g[e]));
+          }
+        }
+        if (lane == 0) tb.dec = exp2f((float)all);
+        run += all;
+        arrive(tab_full(i));
+      }
+      if (!ok) break;
+      if (a.pass == 0 && lane == 0) a.part_decay[blockIdx.x] = run;
+      run = 0.0;
+      w.advance(a, count);
+    }
+  } else if (warp == 3) {
+    // ---- zeros behind the sequences' ends, whole chunks (heads dealt to the CTAs) ----
+    if (OUT) {
+      for (long long u = blockIdx.x; u < (long long)a.B * a.H; u += gridDim.x) {
+        const int b = (int)(u / a.H), h = (int)(u % a.H);
+        const int from = LinWalk::chunks_of(lin_tokens(a, b)) * kLC;
+        constexpr int per = DV / 8;  // 16-byte units of a row
+        for (long long e = (long long)from * per + lane; e < (long long)a.T * per; e += 32)
+          reinterpret_cast<uint4*>(a.o)[(((long long)b * a.T + e / per) * a.H + h) * per + e % per] =
+              make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else if (warp < 8) {
+    // ---- the state: thread = key row of M (at Dk = 64: rows 64-127 hold the low part) ----
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t tq = tm + PL::cM + ((uint32_t)(quarter * 32) << 16);
+    const bool owner = r < DK;  // rows with a place in the state's array
+    uint32_t meetings = 0;
+    int part = 0;
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count();
+      const long long unit = (long long)w.b * a.H + w.h;
+      // the state before the part
+      {
+        const int first = w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
+#pragma unroll 1
+        for (int j = 0; j < DV; j += 32) {
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          if (owner && a.pass == 1) {
+            double lg = 0.0;
+            float f = 1.f;
+            for (int c = (int)blockIdx.x - 1; c >= first && f != 0.f; --c) {
+              const float4* const p = reinterpret_cast<const float4*>(a.part + ((long long)c * DK + r) * DV + j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 y = __ldg(p + e);
+                x[4 * e] = fmaf(f, y.x, x[4 * e]);
+                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
+                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
+                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
+              }
+              lg += a.part_decay[c];
+              f = exp2f((float)lg);
+            }
+            if (a.s_in != nullptr && f != 0.f) {
+              const float4* const p = reinterpret_cast<const float4*>(a.s_in + (unit * DK + r) * DV + j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 y = p[e];
+                x[4 * e] = fmaf(f, y.x, x[4 * e]);
+                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
+                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
+                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
+              }
+            }
+          }
+          tmem_st32(tq + j, reinterpret_cast<const uint32_t*>(x));
+        }
+        tmem_wait_st();
+      }
+      int ek = 0;  // tensor memory holds 2^ek M
+      for (int c = 0; c < count; ++c, ++i) {
+        if (!await(tab_full(i), (i >> 1) & 1)) break;
+        float dec = tabs[i & 1].dec;
+        int ek_now = 0;
+        if (kScaled) {
+          if (!await(ek_ready(i), (i >> 1) & 1)) break;
+          ek_now = misc[4 + (i & 1)];
+        }
+        arrive(tab_free(i));
+        if (!upd_wait(i)) break;
+        tc_fence_after();
+        const bool drop = dec == 0.f;  // whatever the state holds
+        const int ek_old = ek;
+        const float up = kScaled ? exp2f((float)(ek_now - ek_old)) : 1.f;  // a power of two: exact
+        ek = ek_now;
+        float cs = 1.f;  // what M's copy carries
+        if (OUT && kScaled) {
+          uint32_t mx = 0;  // bits of the largest finite magnitude
+#pragma unroll 1
+          for (int j = 0; j < DV; j += 32) {
+            uint32_t x[32];
+            tmem_ld32(tq + j, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = max(mx, finite_bits(x[e]));
+          }
+          mx = __reduce_max_sync(0xffffffffu, mx);
+          if (lane == 0) misc[12 + quarter] = (int)mx;
+          arrive(met_m);
+          if (!await(met_m, meetings++ & 1)) break;
+          mx = max(max(misc[12], misc[13]), max(misc[14], misc[15]));
+          // the largest to [2^14, 2^15)
+          const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
+          cs = exp2f((float)(14 - ex));
+          if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14 - ek_old));
+        }
+#pragma unroll 1
+        for (int j = 0; j < DV; j += 32) {
+          uint32_t x[32];
+          tmem_ld32(tq + j, x);
+          tmem_wait_ld();
+          if (OUT) {
+            const uint32_t blk = base + PL::oSt + (j >> 6) * 16384;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                y[z] = pack16<T>(__uint_as_float(x[8 * e + 2 * z]) * cs, __uint_as_float(x[8 * e + 2 * z + 1]) * cs);
+              sts128(blk + swz128(r, ((j & 32) >> 3) + e), make_uint4(y[0], y[1], y[2], y[3]));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = drop ? 0u : __float_as_uint(__uint_as_float(x[e]) * dec * up);
+          tmem_st32(tq + j, x);
+        }
+        if (OUT) fence_proxy_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(m_ready);
+      }
+      if (!ok || !upd_wait(i)) break;
+      tc_fence_after();
+      // the state behind the part: into the array if the head ends here, else this CTA's contribution
+      const bool ends = w.chunk + count == w.chunks;
+      float* dst = nullptr;
+      if (a.pass == 0) dst = a.part + (long long)blockIdx.x * DK * DV;
+      else if (ends && a.s_out != nullptr && misc[2 + (part & 1)] != part + 1 && a.repair[unit] == 0)
+        dst = a.s_out + unit * DK * DV;
+      const float down = kScaled ? exp2f((float)-ek) : 1.f;
+      if (dst != nullptr || DK == 64) {
+#pragma unroll 1
+        for (int j = 0; j < DV; j += 32) {
+          uint32_t x[32];
+          tmem_ld32(tq + j, x);
+          tmem_wait_ld();
+          if constexpr (DK == 64) {
+            // rows 64-127 add theirs to rows 0-63 through the (idle) place of M's copy
+            float* const ex = reinterpret_cast<float*>(sb + PL::oSt);
+            if (!owner) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ex[(r - 64) * 33 + e] = __uint_as_float(x[e]);
+            }
+            arrive(met_m);
+            if (!await(met_m, meetings++ & 1)) break;
+            if (owner) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + ex[r * 33 + e]);
+            }
+            arrive(met_m);
+            if (!await(met_m, meetings++ & 1)) break;
+          }
+          if (owner && dst != nullptr) {
+            float4* const p = reinterpret_cast<float4*>(dst + (long long)r * DV + j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              p[e] = make_float4(__uint_as_float(x[4 * e]) * down, __uint_as_float(x[4 * e + 1]) * down,
+                                 __uint_as_float(x[4 * e + 2]) * down, __uint_as_float(x[4 * e + 3]) * down);
+          }
+        }
+      }
+      if (!ok) break;
+      ++part;
+      w.advance(a, count);
+    }
+  } else if (warp < 12) {
+    // ---- keys and values: thread = token ----
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    uint32_t meetings = 0;
+    int part = 0;
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count();
+      const long long unit = (long long)w.b * a.H + w.h;
+      for (int c = 0; c < count; ++c, ++i) {
+        const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
+        const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
+        if (!await(k_full(i), (i >> 1) & 1)) break;
+        float up = 1.f;
+        if (kScaled) {
+          // the largest finite key of the chunk sets the chunk's power of two
+          uint32_t mx = 0;
+          if (r < nv) {
+#pragma unroll
+            for (int ch = 0; ch < DK / 8; ++ch) {
+              const uint4 x = lds128(kb + (ch >> 3) * 16384 + swz128(r, ch & 7));
+              mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+            }
+          }
+          mx = max(mx & 0xffffu, mx >> 16);
+          mx = __reduce_max_sync(0xffffffffu, mx);
+          if (lane == 0) misc[8 + quarter] = (int)mx;
+          arrive(met);
+          if (!await(met, meetings++ & 1)) break;
+          const int bits = max(max(misc[8], misc[9]), max(misc[10], misc[11]));
+          // fp16 bits to an exponent: 2^(e) <= largest < 2^(e + 1)
+          const float top = __half2float(__ushort_as_half((unsigned short)min(bits, 0x7bff)));
+          const int ex = top == 0.f ? 0 : (int)(__float_as_uint(top) >> 23) - 127;
+          const int ek = 14 - ex;  // -1 .. 38
+          up = exp2f((float)ek);
+          if (quarter == 0 && lane == 0) {
+            misc[4 + (i & 1)] = ek;
+            __threadfence_block();
+            mbar_arrive(ek_ready(i));
+          }
+        }
+        if (!await(tab_full(i), (i >> 1) & 1)) break;
+        const float wt = r < nv ? tabs[i & 1].w[r] : 0.f;
+        arrive(tab_free(i));
+        if (OUT && !await(s_full, i & 1)) break;  // Q K^T has read the keys
+        if (!upd_wait(i)) break;                  // and the last product the low parts
+        const float f = wt * up;
+        const bool zero = wt == 0.f;
+        uint32_t odd = 0;  // something here is not finite
+#pragma unroll 4
+        for (int ch = 0; ch < DK / 8; ++ch) {
+          const uint32_t off = (ch >> 3) * 16384 + swz128(r, ch & 7);
+          const uint4 x = lds128(kb + off);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float2 y = unpack16<T>(xs[z]);
+            odd |= nonfinite16<T>(xs[z]);
+            const float y0 = zero ? 0.f : y.x * f, y1 = zero ? 0.f : y.y * f;
+            hi[z] = pack16<T>(y0, y1);
+            const float2 hv = unpack16<T>(hi[z]);
+            lo[z] = pack16<T>(y0 - hv.x, y1 - hv.y);
+          }
+          sts128(kb + off, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(base + PL::oLo + off, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+        if (!await(v_full, i & 1)) break;
+#pragma unroll 4
+        for (int ch = 0; ch < DV / 8; ++ch) {
+          const uint32_t at = base + PL::oV + (ch >> 3) * 16384 + swz128(r, ch & 7);
+          if (r < nv) {
+            const uint4 x = lds128(at);
+            odd |= nonfinite16<T>(x.x) | nonfinite16<T>(x.y) | nonfinite16<T>(x.z) | nonfinite16<T>(x.w);
+          } else {
+            sts128(at, make_uint4(0, 0, 0, 0));
+          }
+        }
+        if (odd != 0 && r < nv) {
+          misc[2 + (part & 1)] = part + 1;
+          a.repair[unit] = 1;
+        }
+        fence_proxy_async_smem();
+        arrive(kv_ready);
+      }
+      if (!ok) break;
+      ++part;
+      w.advance(a, count);
+    }
+  } else if (OUT) {
+    // ---- scores and outputs: thread = token ----
+    const int quarter = warp & 3, t = quarter * 32 + lane;
+    const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
+    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+      const int count = w.count();
+      for (int c = 0; c < count; ++c, ++i) {
+        const int t0 = (w.chunk + c) * kLC, nv = w.n - t0;
+        if (!await(tab_full(i), (i >> 1) & 1)) break;
+        const LinTables& tb = tabs[i & 1];
+        if (!await(s_full, i & 1)) break;
+        tc_fence_after();
+        const uint32_t ts = tq + PL::cS;
+        // fp16: the row's largest score sets the row's power of two
+        float up = 1.f, down = 1.f;
+        if (kScaled) {
+          uint32_t mx = 0;
+#pragma unroll 1
+          for (int j = 0; j <= quarter; ++j) {
+            uint32_t x[32];
+            tmem_ld32(ts + 32 * j, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (j < quarter || e <= lane) mx = max(mx, finite_bits(x[e]));
+          }
+          const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
+          up = exp2f((float)(14 - ex));
+          down = exp2f((float)(ex - 14));
+        }
+        const float rf = tb.rf[t] * up, hi = tb.hi[t], lo = tb.lo[t];
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t y[16];
+          if (j <= quarter) {
+            uint32_t x[32];
+            tmem_ld32(ts + 32 * j, x);
+            tmem_wait_ld();
+            if (j < quarter) {
+              const float4* const cf = reinterpret_cast<const float4*>(tb.cf[quarter - 1] + 32 * j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 f = cf[e];
+                y[2 * e] = pack16<T>(__uint_as_float(x[4 * e]) * (rf * f.x), __uint_as_float(x[4 * e + 1]) * (rf * f.y));
+                y[2 * e + 1] =
+                    pack16<T>(__uint_as_float(x[4 * e + 2]) * (rf * f.z), __uint_as_float(x[4 * e + 3]) * (rf * f.w));
+              }
+            } else {
+              const float4* const h4 = reinterpret_cast<const float4*>(tb.hi + 32 * j);
+              const float4* const l4 = reinterpret_cast<const float4*>(tb.lo + 32 * j);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 hs = h4[e], ls = l4[e];
+                const float d0 = (hi - hs.x) + (lo - ls.x), d1 = (hi - hs.y) + (lo - ls.y);
+                const float d2 = (hi - hs.z) + (lo - ls.z), d3 = (hi - hs.w) + (lo - ls.w);
+                const float p0 = 4 * e <= lane ? __uint_as_float(x[4 * e]) * (up * exp2_approx(d0)) : 0.f;
+                const float p1 = 4 * e + 1 <= lane ? __uint_as_float(x[4 * e + 1]) * (up * exp2_approx(d1)) : 0.f;
+                const float p2 = 4 * e + 2 <= lane ? __uint_as_float(x[4 * e + 2]) * (up * exp2_approx(d2)) : 0.f;
+                const float p3 = 4 * e + 3 <= lane ? __uint_as_float(x[4 * e + 3]) * (up * exp2_approx(d3)) : 0.f;
+                y[2 * e] = pack16<T>(p0, p1);
+                y[2 * e + 1] = pack16<T>(p2, p3);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 0u;
+          }
+          tmem_st16(ts + 16 * j, y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(p_ready);
+        const float eg = tb.eg[t];
+        if (!pv_wait(i + 1)) break;
+        tc_fence_after();
+        // (the state's part of the output was done before P V)
+        const float f1 = eg * a.scale * (kScaled ? fmisc[6 + (i & 1)] : 1.f), f2 = a.scale * down;
+        const bool drop = eg == 0.f;
+        T* const dst = static_cast<T*>(a.o) + (((long long)w.b * a.T + t0 + t) * a.H + w.h) * DV;
+#pragma unroll 1
+        for (int j = 0; j < DV; j += 32) {
+          uint32_t x[32], z[32];
+          tmem_ld32(tq + PL::cO1 + j, x);
+          tmem_ld32(tq + PL::cO2 + j, z);
+          tmem_wait_ld();
+          if (t0 + t < a.T) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float u0 = drop ? 0.f : __uint_as_float(x[e + 2 * k]) * f1;
+                const float u1 = drop ? 0.f : __uint_as_float(x[e + 2 * k + 1]) * f1;
+                y[k] = t < nv ? pack16<T>(fmaf(__uint_as_float(z[e + 2 * k]), f2, u0),
+                                          fmaf(__uint_as_float(z[e + 2 * k + 1]), f2, u1))
+                              : 0u;
+              }
+              *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        arrive(o_free);
+        arrive(tab_free(i));
+      }
+      if (!ok) break;
+      w.advance(a, count);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+template <typename T, int DK, int DV, bool OUT>
+cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st) {
+  auto kernel = linear_tc_kernel<T, DK, DV, OUT>;
+  // more than half an SM's: one CTA and one tensor-memory allocation per SM
+  constexpr int half = 232448 / 2 + 1024;
+  constexpr int smem = LinPlan<DK, DV>::kTotal > half ? LinPlan<DK, DV>::kTotal : half;
+  static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 512 : 384), smem, st, m, a);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t linear_tc_dispatch(const LinMaps& m, const LinArgs& a, cudaStream_t st) {
+  const bool out = a.pass == 1 && a.o != nullptr;
+  if (a.Dk == 128 && a.Dv == 128)
+    return out ? linear_tc_launch<T, 128, 128, true>(m, a, st) : linear_tc_launch<T, 128, 128, false>(m, a, st);
+  if (a.Dk == 128)
+    return out ? linear_tc_launch<T, 128, 64, true>(m, a, st) : linear_tc_launch<T, 128, 64, false>(m, a, st);
+  if (a.Dv == 128)
+    return out ? linear_tc_launch<T, 64, 128, true>(m, a, st) : linear_tc_launch<T, 64, 128, false>(m, a, st);
+  return out ? linear_tc_launch<T, 64, 64, true>(m, a, st) : linear_tc_launch<T, 64, 64, false>(m, a, st);
+}
+
+}  // namespace sdv

@@ -39,22 +39,23 @@ __host__ __device__ constexpr uint32_t idesc_16_f32(bool bf16, int m, int n, boo
 }
 
 // Four MMAs (K = 16 each, 64 along the reduction) issued by one elected lane of a
-// converged warp; operands are the same in every lane.  _ss: A and B K-major in shared
-// memory, 32 bytes further each; _ts: A in tensor memory, 8 columns further each, B
-// MN-major in shared memory, 16 reduction indices (2048 bytes) further each.  The
-// first overwrites D unless `accumulate`.
+// converged warp; operands are the same in every lane.  _ss: A and B in shared memory,
+// DA and DB 16-byte units further each (a K-major operand under the 128-byte swizzle: 2,
+// an MN-major one: 128); _ts: A in tensor memory, 8 columns further each, B MN-major.
+// The first overwrites D unless `accumulate`.
+template <int DA = 2, int DB = 2>
 __device__ __forceinline__ void tc_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred e, p, t;\n\t.reg .b64 ta, tb;\n\t"
       "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.u64 ta, %1, 2;\n\tadd.u64 tb, %2, 2;\n\t"
+      "add.u64 ta, %1, %5;\n\tadd.u64 tb, %2, %8;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t"
-      "add.u64 ta, %1, 4;\n\tadd.u64 tb, %2, 4;\n\t"
+      "add.u64 ta, %1, %6;\n\tadd.u64 tb, %2, %9;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t"
-      "add.u64 ta, %1, 6;\n\tadd.u64 tb, %2, 6;\n\t"
+      "add.u64 ta, %1, %7;\n\tadd.u64 tb, %2, %10;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ta, tb, %3, t;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(DA), "n"(2 * DA), "n"(3 * DA), "n"(DB), "n"(2 * DB), "n"(3 * DB)
       : "memory");
 }
 __device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -145,6 +146,18 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+
+// A packed pair to two floats.
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t x);
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
 // Whether either half of a packed pair is an infinity or NaN: bits of the halves that are.
