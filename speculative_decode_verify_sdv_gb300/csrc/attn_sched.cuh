@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "sdv_kernels.h"
+#include "split_math.cuh"
 
 namespace sdv {
 
@@ -67,21 +68,13 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return attn_seq(a, __ldg(a.ctx + b), a.n_rows != nullptr ? __ldg(a.n_rows + b) : a.S);
 }
 
-// x * y / z and x / z with small numbers (the common case) in 32 bits: a 64-bit
-// division takes most of a microsecond of a lone warp's time.
-__device__ __forceinline__ long long muldiv(long long x, int y, long long z) {
-  const unsigned long long p = (unsigned long long)x * (unsigned)y;
-  return (p | (unsigned long long)z) >> 32 == 0 ? (long long)((unsigned)p / (unsigned)z) : (long long)(p / z);
-}
-
 __device__ __forceinline__ int attn_live_ctas(const AttnArgs& a, long long total) {
   return total < a.ctas ? (int)total : a.ctas;
 }
 // Start of CTA c's range, and the CTA whose range holds place w.
 __device__ __forceinline__ long long attn_first(long long total, int live, int c) { return muldiv(total, c, live); }
 __device__ __forceinline__ int attn_owner(long long total, int live, long long w) {
-  const unsigned long long p = (unsigned long long)(w + 1) * (unsigned)live - 1;
-  return (int)((p | (unsigned long long)total) >> 32 == 0 ? (unsigned)p / (unsigned)total : p / total);
+  return (int)div_fast((unsigned long long)(w + 1) * (unsigned)live - 1, total);
 }
 
 // A CTA's way through its range, one segment (part of a unit) after another.
@@ -93,7 +86,7 @@ struct AttnWalk {
   int next_ctx, next_n;  // lengths of sequence b + 1, loaded ahead of their use
 
   // Warp-collective.  False where the CTA has nothing to do.
-  __device__ __forceinline__ bool start(const AttnArgs& a, int cta, int lane) {
+  __device__ __noinline__ bool start(const AttnArgs& a, int cta, int lane) {
     const int units = a.Hkv * a.row_tiles;
     // the first 32 sequences' weights serve for the total and for the search
     const long long w0 = lane < a.B ? ((long long)attn_seq(a, lane).tiles + a.lead) * units : 0;

@@ -131,7 +131,7 @@ __device__ __forceinline__ int small_div(int x, float inv_g) { return (int)(((fl
 
 template <typename T, int D, bool SPREAD>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
+    attn_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs a) {
   using PL = AttnPlan<D, SPREAD>;
   constexpr int TK = PL::TK;
   constexpr int CW = SPREAD ? TK / 4 : TK;  // score columns of a softmax warp
@@ -195,10 +195,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
-      ok = false;
-      if (lane == 0) atomicOr(a.status, kDevErrTimeout);
-    }
+    if (ok) ok = mbar_wait_warp(bar, parity, a.status);
     return ok;
   };
   // P V products complete in tile order.  Each role that needs them waits for every
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (warp == 0 || warp == 6) {
     // ---- producers: the warp's tile i takes ring place 2i (keys) or 2i + 1 (values) ----
-    AttnWalk w;
+    AttnWalk first;
     const bool values = warp == 6;
     const int box = min(a.page, TK), chunks = TK / box;  // rows per box, pages (or page parts) per tile
     const int page_log = 31 - __clz(a.page);
@@ -226,7 +223,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const bool mine = chunk < chunks;
     const uint32_t dst = ring + cb * (TK * 128) + chunk * box * 128;
     int slot = values ? 1 : 0, use = 0;  // ring place: slot, and how often the ring has been passed
-    bool more = w.start(a, blockIdx.x, lane);
+    bool more = first.start(a, blockIdx.x, lane);
+    AttnWalk w = first;
     while (more) {
       const int count = w.segment();
       const int h = w.unit / a.row_tiles;
@@ -280,12 +278,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
   } else if (warp == 7) {
     // ---- segments: Q by TMA, and what the others need to know ----
-    AttnWalk w;
+    AttnWalk start;
     const int page_log = 31 - __clz(a.page);
     const uint64_t policy = l2_policy_normal();
     constexpr int kCopies = SPREAD ? 4 : 1;
     uint32_t staged = 0;  // segments whose Q was asked for
-    bool more = w.start(a, blockIdx.x, lane);
+    bool more = start.start(a, blockIdx.x, lane);
+    AttnWalk w = start;
     for (int sg = 0;; ++sg) {
       const int buf = seg_buf(sg);
       if (sg >= q_bufs && !await(q_free(buf), seg_parity(sg - q_bufs))) break;
@@ -611,12 +610,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               x.w = fmaf(f, y.w, x.w);
             }
             if (poisoned) {
-              float* const xs = &x.x;
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint32_t bits = pois[j0 + j + z] & mword[rr];
-                if (bits) xs[z] += poison_of<T>(a, trow, h, ctx, bits, j0 + j + z);
-              }
+              const int d = j0 + j;
+              const uint32_t see = mword[rr];
+              x.x += poison_of<T>(a, trow, h, ctx, pois[d] & see, d);
+              x.y += poison_of<T>(a, trow, h, ctx, pois[d + 1] & see, d + 1);
+              x.z += poison_of<T>(a, trow, h, ctx, pois[d + 2] & see, d + 2);
+              x.w += poison_of<T>(a, trow, h, ctx, pois[d + 3] & see, d + 3);
             }
             const int rw = r0 + rr, rs = small_div(rw, inv_g);
             const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
@@ -685,6 +684,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const long long orow = ((long long)b * a.S + wr) * a.Hq + h * a.G + (row - wr * a.G);
         const bool none = !live || l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
+        if (poisoned) {  // into the output where it lies
+#pragma unroll 1
+          for (int j = 0; j < D; ++j) {
+            const uint32_t bits = pois[j] & word;
+            if (!__any_sync(0xffffffffu, bits != 0)) continue;
+            const uint32_t x = tmem_ld1(tq + PL::kO + j);
+            tmem_wait_ld();
+            const float add = bits ? poison_of<T>(a, trow, h, ctx, bits, j) : 0.f;
+            __syncwarp();
+            tmem_st1(tq + PL::kO + j, bits ? __float_as_uint(__uint_as_float(x) + add) : x);
+          }
+          tmem_wait_st();
+        }
         constexpr int OC = D < 128 ? D : 128;  // columns at once
 #pragma unroll 1
         for (int j = 0; j < D; j += OC) {
@@ -692,13 +704,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
           tmem_wait_ld();
-          if (poisoned) {
-#pragma unroll
-            for (int e = 0; e < OC; ++e) {
-              const uint32_t bits = pois[j + e] & word;
-              if (bits) o[e] = __float_as_uint(__uint_as_float(o[e]) + poison_of<T>(a, trow, h, ctx, bits, j + e));
-            }
-          }
           if (r >= nr) continue;
           if (final) {
             uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);

@@ -7,6 +7,29 @@
 
 namespace sdv {
 
+// A sum of log2 decays as a pair of floats (48 bits).
+struct DecaySum {
+  float hi = 0.f, lo = 0.f;
+#ifdef __CUDACC__
+  // log2 of e^x, x at most 0; -1e4 (a decay of 0 in fp32) for anything below; NaN stays.
+  static __device__ __forceinline__ DecaySum log2_of(float x) {
+    constexpr float c = 1.4426950216293335f, cl = 1.925963033500583e-08f;  // log2 e = c + cl
+    x = x < -1e4f ? -1e4f : x;
+    const float h = __fmul_rn(x, c);
+    return DecaySum{h, fmaf(x, cl, fmaf(x, c, -h))};
+  }
+  // The exact sum of the high parts (two-sum), the low parts beside it.
+  __device__ __forceinline__ void add(const DecaySum& o) {
+    const float s = __fadd_rn(hi, o.hi), b = __fadd_rn(s, -hi);
+    const float e = __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(o.hi, -b));
+    const float l = __fadd_rn(__fadd_rn(lo, o.lo), e);
+    hi = __fadd_rn(s, l);
+    lo = __fadd_rn(l, -__fadd_rn(hi, -s));
+  }
+  __device__ __forceinline__ float minus(const DecaySum& o) const { return (hi - o.hi) + (lo - o.lo); }
+#endif
+};
+
 struct LinArgs {
   const void *q, *k, *v;
   long long q_stride, k_stride, v_stride;
@@ -21,7 +44,7 @@ struct LinArgs {
   // chunked form: a CTA's local state and its log2 decay, heads whose values are not
   // finite (recomputed by the recurrent kernel), status
   float* part;             // [CTAs][Dk][Dv]
-  double* part_decay;      // [CTAs]
+  DecaySum* part_decay;    // [CTAs]
   int* repair;             // [B][H]
   int* status;
   int ctas;

@@ -217,7 +217,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
     char* const w8 = static_cast<char*>(ws);
     a.status = reinterpret_cast<int*>(w8);
     a.repair = reinterpret_cast<int*>(w8 + kHeaderBytes);
-    a.part_decay = reinterpret_cast<double*>(w8 + kHeaderBytes + lin_notes(B, H));
+    a.part_decay = reinterpret_cast<DecaySum*>(w8 + kHeaderBytes + lin_notes(B, H));
     a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_decay) + round_256((size_t)a.ctas * 8));
     const cudaError_t e = launch_linear_tc(dtype, a, st);
     if (e != cudaSuccess) return status_of(e);

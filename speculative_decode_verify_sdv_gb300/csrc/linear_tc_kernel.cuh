@@ -5,17 +5,18 @@
 //   O_t  = scale (e^{G_t} q_t M + sum_{s <= t} (q_t . k_s) e^{G_t - G_s} v_s)
 //   M'   = e^{G_C} M + sum_s e^{G_C - G_s} k_s v_s^T
 // as four products of 128 x 128 tiles: Q K^T, Q M, P V (P the decayed scores) and
-// K~^T V (K~ the decayed keys).  Scores, both parts of the output and the state are
-// fp32 in tensor memory (128 + 3 Dv columns); the state never leaves it inside a run.
+// U = K~^T V (K~ the decayed keys).  Scores, outputs (Q M, scaled row by row, then P V on
+// top), U and the state are fp32 in tensor memory (128 + 3 Dv columns).  The state takes
+// U with rounded fp32 operations: added up inside the tensor cores over a long prompt it
+// was 5 times less exact.
 //
 // Precision.  M is a sum over all tokens, so its terms are kept to 22 (fp16) or 16
 // (bf16) bits: K~ goes into the product as high and low part.  P and the copy of M
 // that Q multiplies are rounded to the 16-bit type once, as the values of a matrix
 // instruction have to be.  fp16 has neither the range of scores nor of states nor of
 // decayed keys, so each carries a power of two: P one per row, M's copy one per chunk,
-// K~ one per chunk (the state in tensor memory is kept in its units).  G is summed in
-// fp64 and used as differences (high and low float), so a token far behind a reset
-// loses nothing.
+// K~ one per chunk.  G is summed in pairs of floats and used as differences, so a token
+// far behind a reset loses nothing.
 //
 // The chunks of all heads are dealt to the CTAs in equal contiguous ranges.  A head
 // that several CTAs share needs its state at the start of each part: a first launch
@@ -23,8 +24,10 @@
 // one each CTA sums those before it, decayed, on its way in.
 //
 // Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 zeros behind a sequence's end; 4-7 the
-// state (one thread per key row of M: 16-bit copy for Q M, decay); 8-11 the keys (K~ in
-// place and beside) and the cleaning of V; 12-15 scores to P, outputs.
+// state (one thread per key row of M: decay, 16-bit copy for Q M) and the values' check;
+// 8-11 the keys (K~ in place and beside); 12-15 scores to P, outputs.  All of it runs in
+// rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
+// times as slow).
 //
 // A zero weight must not meet an infinite value (0 * inf): a head with keys or values
 // that are not finite is noted, its state left unwritten, and the recurrent kernel,
@@ -42,6 +45,7 @@
 
 #include "linear_args.h"
 #include "sdv_kernels.h"
+#include "split_math.cuh"
 #include "tc_util.cuh"
 
 namespace sdv {
@@ -51,10 +55,59 @@ namespace {
 constexpr int kLC = kLinChunk;
 constexpr uint64_t kLinDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
 
-// Bits of |x|, 0 for an infinity or NaN.
-__device__ __forceinline__ uint32_t finite_bits(uint32_t x) {
-  const uint32_t m = x & 0x7fffffffu;
-  return m < 0x7f800000u ? m : 0u;
+__device__ __forceinline__ float abs_max32(const uint32_t (&x)[32]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], fabsf(__uint_as_float(x[e])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// The largest finite magnitude among columns 0 .. last of 32, by a warp.
+__device__ __noinline__ float finite_max32(uint32_t taddr, int last) {
+  uint32_t x[32];
+  tmem_ld32(taddr, x);
+  tmem_wait_ld();
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const float y = fabsf(__uint_as_float(x[e]));
+    if (e <= last && y < INFINITY) m = fmaxf(m, y);
+  }
+  return m;
+}
+
+// x under a decay; one of 0 drops x whatever it holds.
+__device__ __forceinline__ float keep(float x, float dec) { return dec == 0.f ? 0.f : x * dec; }
+
+__device__ __forceinline__ uint32_t abs_max2(const uint4& x) {  // of 16-bit magnitudes, per half
+  return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+
+// A pair times f = fh + fl (each in both halves) as the 16-bit type's nearest (in place)
+// and the rest: k fh rounds to h, the rest k fh - h is a value of the type and exact
+// (twice the type's bits less those of h), and k fl goes on top.
+template <typename T>
+__device__ __forceinline__ void split16(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo);
+template <>
+__device__ __forceinline__ void split16<__half>(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo) {
+  asm("{\n\t.reg .b32 h, n, r;\n\t"
+      "mul.rn.f16x2 h, %0, %2;\n\tneg.f16x2 n, h;\n\t"
+      "fma.rn.f16x2 r, %0, %2, n;\n\tfma.rn.f16x2 %1, %0, %3, r;\n\tmov.b32 %0, h;\n\t}"
+      : "+r"(x), "=&r"(lo)
+      : "r"(fh), "r"(fl));
+}
+template <>
+__device__ __forceinline__ void split16<__nv_bfloat16>(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo) {
+  asm("{\n\t.reg .b32 h, n, r;\n\t"
+      "mul.rn.bf16x2 h, %0, %2;\n\tneg.bf16x2 n, h;\n\t"
+      "fma.rn.bf16x2 r, %0, %2, n;\n\tfma.rn.bf16x2 %1, %0, %3, r;\n\tmov.b32 %0, h;\n\t}"
+      : "+r"(x), "=&r"(lo)
+      : "r"(fh), "r"(fl));
+}
+
+__device__ __forceinline__ uint32_t mul16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 
 // Decay tables of a chunk.
@@ -72,12 +125,13 @@ template <int DK, int DV>
 struct LinPlan {
   static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2, kSt = 128 * DV * 2;
   static constexpr int oK = 0, oLo = oK + 2 * kK, oQ = oLo + kK, oV = oQ + kK, oSt = oV + kV;
-  static constexpr int oTab = oSt + kSt;
+  static constexpr int oOut = oSt + kSt;        // the output warps' 32 rows of 64 columns each
+  static constexpr int oTab = oOut + 4 * 4096;
   static constexpr int oBars = oTab + 2 * (int)sizeof(LinTables);
   static constexpr int kNumBars = 24;
   static constexpr int oMisc = oBars + kNumBars * 8;
   static constexpr int kTotal = oMisc + 128 + 1024;  // the base is aligned to 1024
-  static constexpr int cS = 0, cO1 = 128, cO2 = 256, cM = 384;  // tensor-memory columns
+  static constexpr int cS = 0, cO = 128, cU = 256, cM = 384;  // tensor-memory columns
   static_assert(kTotal <= 232448, "shared memory");
 };
 
@@ -91,20 +145,23 @@ struct LinWalk {
     n = lin_tokens(a, b);
     chunks = chunks_of(n);
   }
-  __device__ __forceinline__ bool start(const LinArgs& a, int cta, int lane) {
-    long long sum = 0;
-    for (int s = lane; s < a.B; s += 32) sum += chunks_of(lin_tokens(a, s));
+  __device__ __noinline__ bool start(const LinArgs& a, int cta, int lane) {
+    // the first 32 sequences' chunks serve for the total and for the search
+    const int c0 = lane < a.B ? chunks_of(lin_tokens(a, lane)) : 0;
+    long long sum = c0;
+    for (int s = lane + 32; s < a.B; s += 32) sum += chunks_of(lin_tokens(a, s));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     total = sum * a.H;
     const long long most = (long long)kLinRuns * a.B * a.H;
     live = (int)min((long long)a.ctas, min(total, most));
     if (cta >= live) return false;
-    at = total * cta / live;
-    end = total * (cta + 1) / live;
+    at = muldiv(total, cta, live);
+    end = muldiv(total, cta + 1, live);
     long long before = 0;
     for (int b0 = 0;; b0 += 32) {
-      const long long mine = b0 + lane < a.B ? (long long)chunks_of(lin_tokens(a, b0 + lane)) * a.H : 0;
+      const long long mine =
+          (long long)(b0 == 0 ? c0 : b0 + lane < a.B ? chunks_of(lin_tokens(a, b0 + lane)) : 0) * a.H;
       long long incl = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -122,7 +179,7 @@ struct LinWalk {
     }
     sequence(a);
     const long long rest = at - before;
-    h = (int)(rest / chunks);
+    h = (int)muldiv(rest, 1, chunks);
     chunk = (int)(rest - (long long)h * chunks);
     // the first launch takes the range's last part alone, and that only if the head goes on
     if (a.pass == 0) {
@@ -145,12 +202,12 @@ struct LinWalk {
     if (++b < a.B) sequence(a);
   }
   // The first CTA with chunks of the head.
-  __device__ __forceinline__ int first_cta() const { return (int)(((at - chunk + 1) * live - 1) / total); }
+  __device__ __forceinline__ int first_cta() const { return (int)div_fast((unsigned long long)(at - chunk + 1) * (unsigned)live - 1, total); }
 };
 
 template <typename T, int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
-    linear_tc_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
+    linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using PL = LinPlan<DK, DV>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kScaled = !kBf16;  // powers of two beside fp16 operands
@@ -179,8 +236,10 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
-    for (int i = 10; i < 16; ++i) mbar_init(bar(i), 4);
+    for (int i = 10; i < 16; ++i)
+      if (i != 11) mbar_init(bar(i), 4);
     mbar_init(drain, 1);
+    mbar_init(kv_ready, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(18 + i), OUT ? 12 : 8);
       mbar_init(bar(20 + i), 1);
@@ -199,10 +258,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(b, parity))) {
-      ok = false;
-      if (lane == 0) atomicOr(a.status, kDevErrTimeout);
-    }
+    if (ok) ok = mbar_wait_warp(b, parity, a.status);
     return ok;
   };
   auto arrive = [&](uint32_t b) {
@@ -222,7 +278,10 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       if (!await(pv_done, pv_seen & 1)) return false;
     return true;
   };
-  LinWalk w;
+  // Every role but the zeros' walks the CTA's range.
+  LinWalk from;
+  const bool any = warp == 3 ? false : from.start(a, blockIdx.x, lane);
+  LinWalk w = from;
   int i = 0;  // the CTA's chunk number
 
   if (warp == 0) {
@@ -231,7 +290,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
     const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
     const int shared = a.H / a.Hqk;
     int asked_q = 0, asked_v = 0;
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+    for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count(), hk = w.h / shared;
       for (int c = 0; c < count; ++c, ++i) {
         const int z = w.b * a.T + (w.chunk + c) * kLC;
@@ -269,115 +328,129 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
     const uint64_t qd = smem_desc_sw128(base + PL::oQ, 16, 1024);
     const uint64_t vd = smem_desc_sw128(base + PL::oV, 16384, 1024);
     const uint64_t md = smem_desc_sw128(base + PL::oSt, 16384, 1024);
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
-      const int count = w.count();
-      for (int c = 0; c < count; ++c, ++i) {
-        const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
-        if (OUT) {
-          // scores; P of the chunk before has been read
-          if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), (i >> 1) & 1)) break;
-          tc_fence_after();
-          const uint64_t kd = smem_desc_sw128(kb, 16, 1024);
-#pragma unroll
-          for (int j = 0; j < DK / 64; ++j)
-            tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
-          tc_commit_elect(s_full);
-        }
-        if (!await(m_ready, i & 1)) break;
-        if (OUT) {
-          // Q M over M's copy: 128 rows (at Dk = 64 the state's high and low part, both by Q)
-          if (i > 0 && !await(o_free, (i - 1) & 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            tc_mma4_ss<2, 128>(tm + PL::cO1, qd + (DK == 128 ? j * 1024 : 0), md + j * 512, id_kb, j > 0);
-          tc_commit_elect(qm_done);
-        }
-        if (!await(kv_ready, i & 1)) break;
+    // the chunks of all parts follow each other alike; a uniform count keeps the operands
+    // in uniform registers
+    const int total = __reduce_max_sync(0xffffffffu, any ? (int)(w.end - w.at) : 0);
+    for (; ok && i < total; ++i) {
+      const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
+      if (OUT) {
+        // scores; P of the chunk before has been read
+        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), (i >> 1) & 1)) break;
         tc_fence_after();
-        if constexpr (DK == 128) {
-          const uint64_t hd = smem_desc_sw128(kb, 16384, 1024);
-          const uint64_t ld = smem_desc_sw128(base + PL::oLo, 16384, 1024);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, ld + j * 512, vd + j * 512, id_up, 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, hd + j * 512, vd + j * 512, id_up, 1);
-        } else {
-          // both parts at once: rows 0-63 from the high, 64-127 from the low part
-          const uint64_t kd = smem_desc_sw128(kb, base + PL::oLo - kb, 1024);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) tc_mma4_ss<128, 128>(tm + PL::cM, kd + j * 512, vd + j * 512, id_up, 1);
-        }
-        tc_commit_elect(upd_done);
-        if (OUT) {
-          if (!await(p_ready, i & 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < 2; ++j) tc_mma4_ts(tm + PL::cO2, tm + PL::cS + j * 32, vd + j * 512, id_kb, j > 0);
-          tc_commit_elect(pv_done);
-        }
+        const uint64_t kd = smem_desc_sw128(kb, 16, 1024);
+#pragma unroll 1
+        for (int j = 0; j < DK / 64; ++j)
+          tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
+        tc_commit_elect(s_full);
       }
-      if (!ok) break;
-      w.advance(a, count);
+      if (!await(m_ready, i & 1)) break;
+      if (OUT) {
+        // Q M over M's copy: 128 rows (at Dk = 64 the state's high and low part, both by Q)
+        if (i > 0 && !await(o_free, (i - 1) & 1)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j)
+          tc_mma4_ss<2, 128>(tm + PL::cO, qd + (DK == 128 ? j * 1024 : 0), md + j * 512, id_kb, j > 0);
+        tc_commit_elect(qm_done);
+      }
+      if (!await(kv_ready, i & 1)) break;
+      tc_fence_after();
+      // K~^T V: the low parts first; at Dk = 64 both at once (rows 0-63 from the high,
+      // 64-127 from the low part)
+      if constexpr (DK == 128) {
+        const uint64_t hd = smem_desc_sw128(kb, 16384, 1024);
+        const uint64_t ld = smem_desc_sw128(base + PL::oLo, 16384, 1024);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)
+          tc_mma4_ss<128, 128>(tm + PL::cU, (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
+      } else {
+        const uint64_t kd = smem_desc_sw128(kb, base + PL::oLo - kb, 1024);
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j)
+          tc_mma4_ss<128, 128>(tm + PL::cU, kd + j * 512, vd + j * 512, id_up, j > 0);
+      }
+      tc_commit_elect(upd_done);
+      if (OUT) {
+        if (!await(p_ready, i & 1)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) tc_mma4_ts(tm + PL::cO, tm + PL::cS + j * 32, vd + j * 512, id_kb, 1);
+        tc_commit_elect(pv_done);
+      }
     }
     tc_commit_elect(drain);  // every MMA has ended before tensor memory is freed
     mbar_wait_bounded(drain, 0, kLinDrainNs);
   } else if (warp == 2) {
-    // ---- decay tables: four tokens a lane, sums in fp64 ----
-    double run = 0.0;  // log2 decay of the part so far
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+    // ---- decay tables: four tokens a lane, sums in pairs of floats ----
+    DecaySum run;  // log2 decay of the part so far
+    float next[4];
+    auto load = [&](int t0) {  // natural log decays of the chunk at t0, ahead of their use
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + 4 * lane + e;
+        next[e] = t < w.n ? lin_decay(a, w.b, t, w.h) : 0.f;
+      }
+    };
+    for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
+      load(w.chunk * kLC);
       for (int c = 0; c < count; ++c, ++i) {
-        const int t0 = (w.chunk + c) * kLC, t = t0 + 4 * lane;
-        double g[4];
+        DecaySum g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = t + e < w.n ? lin_decay(a, w.b, t + e, w.h) : 0.f;
-          // -1e4 (a decay of 0 in fp32) for anything below; NaN stays
-          g[e] = (double)(x < -1e4f ? -1e4f : x) * 1.4426950408889634;
-        }
+        for (int e = 0; e < 4; ++e) g[e] = DecaySum::log2_of(next[e]);
+        if (c + 1 < count) load((w.chunk + c + 1) * kLC);
 #pragma unroll
-        for (int e = 1; e < 4; ++e) g[e] += g[e - 1];
-        double incl = g[3];
+        for (int e = 1; e < 4; ++e) g[e].add(g[e - 1]);
+        DecaySum incl = g[3];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-          const double o = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += o;
+          const DecaySum o{__shfl_up_sync(0xffffffffu, incl.hi, off), __shfl_up_sync(0xffffffffu, incl.lo, off)};
+          if (lane >= off) incl.add(o);
         }
-        double before = __shfl_up_sync(0xffffffffu, incl, 1);
-        if (lane == 0) before = 0.0;
+        DecaySum before{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+        if (lane == 0) before = DecaySum();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] += before;
-        const double all = __shfl_sync(0xffffffffu, incl, 31);
-        double ref[3];
+        for (int e = 0; e < 4; ++e) g[e].add(before);
+        const DecaySum all{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+        DecaySum ref[3];
 #pragma unroll
-        for (int e = 0; e < 3; ++e) ref[e] = __shfl_sync(0xffffffffu, incl, 8 * e + 7);
+        for (int e = 0; e < 3; ++e)
+          ref[e] = DecaySum{__shfl_sync(0xffffffffu, incl.hi, 8 * e + 7), __shfl_sync(0xffffffffu, incl.lo, 8 * e + 7)};
         if (i >= 2 && !await(tab_free(i), ((i - 2) >> 1) & 1)) break;
         LinTables& tb = tabs[i & 1];
         const int blk = lane >> 3;
+        float hi[4], lo[4], eg[4], wt[4], rf[4], cf[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int s = 4 * lane + e;
-          const float hi = (float)g[e];
-          tb.hi[s] = hi;
-          tb.lo[s] = (float)(g[e] - (double)hi);
-          tb.eg[s] = exp2f(hi);
-          tb.w[s] = exp2f((float)(all - g[e]));
+          hi[e] = g[e].hi;
+          lo[e] = g[e].lo;
+          eg[e] = exp2_approx(g[e].hi + g[e].lo);
+          wt[e] = exp2_approx(all.minus(g[e]));
           if (OUT) {
-            const double r = blk == 0 ? g[e] : blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2];
-            tb.rf[s] = exp2f((float)(g[e] - r));
+            rf[e] = blk == 0 ? 1.f : exp2_approx(g[e].minus(blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2]));
 #pragma unroll
-            for (int q = 0; q < 3; ++q)
-              if (blk <= q) tb.cf[q][s] = exp2f((float)(ref[q] - g[e]));
+            for (int q = 0; q < 3; ++q) cf[q][e] = blk <= q ? exp2_approx(ref[q].minus(g[e])) : 0.f;
           }
         }
-        if (lane == 0) tb.dec = exp2f((float)all);
-        run += all;
+        auto put = [&](float* at, const float (&x)[4]) {
+          *reinterpret_cast<float4*>(at + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+        };
+        put(tb.hi, hi);
+        put(tb.lo, lo);
+        put(tb.eg, eg);
+        put(tb.w, wt);
+        if (OUT) {
+          put(tb.rf, rf);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) put(tb.cf[q], cf[q]);
+        }
+        if (lane == 0) tb.dec = exp2_approx(all.hi + all.lo);
+        run.add(all);
         arrive(tab_full(i));
       }
       if (!ok) break;
       if (a.pass == 0 && lane == 0) a.part_decay[blockIdx.x] = run;
-      run = 0.0;
+      run = DecaySum();
       w.advance(a, count);
     }
   } else if (warp == 3) {
@@ -395,241 +468,274 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
   } else if (warp < 8) {
     // ---- the state: thread = key row of M (at Dk = 64: rows 64-127 hold the low part) ----
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t tq = tm + PL::cM + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
     const bool owner = r < DK;  // rows with a place in the state's array
     uint32_t meetings = 0;
     int part = 0;
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+    for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;
-      // the state before the part
-      {
-        const int first = w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
+      // the state before the part: what was given, then the parts before this one, in order
+      const int first = a.pass == 1 && w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
 #pragma unroll 1
-        for (int j = 0; j < DV; j += 32) {
-          float x[32];
+      for (int j = 0; j < DV; j += 32) {
+        float x[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.f;
-          if (owner && a.pass == 1) {
-            double lg = 0.0;
-            float f = 1.f;
-            for (int c = (int)blockIdx.x - 1; c >= first && f != 0.f; --c) {
-              const float4* const p = reinterpret_cast<const float4*>(a.part + ((long long)c * DK + r) * DV + j);
+        for (int e = 0; e < 32; ++e) x[e] = 0.f;
+        if (owner && a.pass == 1) {
+#pragma unroll 1
+          for (int c = first - 1; c < (int)blockIdx.x; ++c) {
+            if (c < first && a.s_in == nullptr) continue;
+            const float* const src =
+                (c < first ? a.s_in + unit * DK * DV : a.part + (long long)c * DK * DV) + (long long)r * DV + j;
+            float dec = 0.f;
+            if (c >= first) dec = exp2f(a.part_decay[c].hi + a.part_decay[c].lo);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 y = __ldg(p + e);
-                x[4 * e] = fmaf(f, y.x, x[4 * e]);
-                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
-                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
-                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
-              }
-              lg += a.part_decay[c];
-              f = exp2f((float)lg);
-            }
-            if (a.s_in != nullptr && f != 0.f) {
-              const float4* const p = reinterpret_cast<const float4*>(a.s_in + (unit * DK + r) * DV + j);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 y = p[e];
-                x[4 * e] = fmaf(f, y.x, x[4 * e]);
-                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
-                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
-                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
-              }
+            for (int e = 0; e < 32; e += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(src + e);
+              x[e] = keep(x[e], dec) + y.x;
+              x[e + 1] = keep(x[e + 1], dec) + y.y;
+              x[e + 2] = keep(x[e + 2], dec) + y.z;
+              x[e + 3] = keep(x[e + 3], dec) + y.w;
             }
           }
-          tmem_st32(tq + j, reinterpret_cast<const uint32_t*>(x));
         }
-        tmem_wait_st();
+        tmem_st32(tq + PL::cM + j, reinterpret_cast<const uint32_t*>(x));
       }
-      int ek = 0;  // tensor memory holds 2^ek M
-      for (int c = 0; c < count; ++c, ++i) {
-        if (!await(tab_full(i), (i >> 1) & 1)) break;
-        float dec = tabs[i & 1].dec;
-        int ek_now = 0;
-        if (kScaled) {
-          if (!await(ek_ready(i), (i >> 1) & 1)) break;
-          ek_now = misc[4 + (i & 1)];
+      tmem_wait_st();
+      float dec = 0.f, dn = 1.f;  // of the last chunk: M = dec M + dn U
+      auto state_of = [&](int j, uint32_t (&x)[32], bool take) {  // 32 columns of M behind the last chunk
+        tmem_ld32(tq + PL::cM + j, x);
+        if (!take) {
+          tmem_wait_ld();
+          return;
         }
-        arrive(tab_free(i));
+        uint32_t u[32];
+        tmem_ld32(tq + PL::cU + j, u);
+        tmem_wait_ld();
+        if (dec == 0.f) {  // drops M whatever it holds
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0u;
+        }
+        const f32x2 dec2 = pair2(dec, dec), dn2 = pair2(dn, dn);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = unpair2(fma2(pair2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), dn2,
+                                        mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), dec2)));
+          x[e] = __float_as_uint(y.x);
+          x[e + 1] = __float_as_uint(y.y);
+        }
+      };
+      auto copy_out = [&](int j, const uint32_t (&x)[32], float cs) {  // M's copy for Q M
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            y[z] = pack16<T>(mul2(pair2(__uint_as_float(x[e + 2 * z]), __uint_as_float(x[e + 2 * z + 1])), pair2(cs, cs)));
+          sts128(base + PL::oSt + (j >> 6) * 16384 + swz128(r, ((j & 32) + e) >> 3), make_uint4(y[0], y[1], y[2], y[3]));
+        }
+      };
+      for (int c = 0; c < count; ++c, ++i) {
+        const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
         if (!upd_wait(i)) break;
         tc_fence_after();
-        const bool drop = dec == 0.f;  // whatever the state holds
-        const int ek_old = ek;
-        const float up = kScaled ? exp2f((float)(ek_now - ek_old)) : 1.f;  // a power of two: exact
-        ek = ek_now;
-        float cs = 1.f;  // what M's copy carries
-        if (OUT && kScaled) {
-          uint32_t mx = 0;  // bits of the largest finite magnitude
+        if (OUT || c > 0) {
+          float big = 0.f;
 #pragma unroll 1
           for (int j = 0; j < DV; j += 32) {
             uint32_t x[32];
-            tmem_ld32(tq + j, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = max(mx, finite_bits(x[e]));
+            state_of(j, x, c > 0);
+            if (c > 0) tmem_st32(tq + PL::cM + j, x);
+            if (OUT && kScaled) big = fmaxf(big, abs_max32(x));
+            if (OUT && !kScaled) copy_out(j, x, 1.f);
           }
-          mx = __reduce_max_sync(0xffffffffu, mx);
-          if (lane == 0) misc[12 + quarter] = (int)mx;
-          arrive(met_m);
-          if (!await(met_m, meetings++ & 1)) break;
-          mx = max(max(misc[12], misc[13]), max(misc[14], misc[15]));
-          // the largest to [2^14, 2^15)
-          const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
-          cs = exp2f((float)(14 - ex));
-          if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14 - ek_old));
-        }
+          if (OUT && kScaled) {
+            tmem_wait_st();
+            if (__any_sync(0xffffffffu, big == INFINITY)) {  // by its finite entries
+              big = 0.f;
 #pragma unroll 1
-        for (int j = 0; j < DV; j += 32) {
-          uint32_t x[32];
-          tmem_ld32(tq + j, x);
-          tmem_wait_ld();
-          if (OUT) {
-            const uint32_t blk = base + PL::oSt + (j >> 6) * 16384;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t y[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                y[z] = pack16<T>(__uint_as_float(x[8 * e + 2 * z]) * cs, __uint_as_float(x[8 * e + 2 * z + 1]) * cs);
-              sts128(blk + swz128(r, ((j & 32) >> 3) + e), make_uint4(y[0], y[1], y[2], y[3]));
+              for (int j = 0; j < DV; j += 32) big = fmaxf(big, finite_max32(tq + PL::cM + j, 31));
+            }
+            uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+            if (lane == 0) misc[12 + quarter] = (int)mx;
+            arrive(met_m);
+            if (!await(met_m, meetings++ & 1)) break;
+            mx = max(max(misc[12], misc[13]), max(misc[14], misc[15]));
+            // the largest to [2^14, 2^15)
+            const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
+            const float cs = exp2f((float)(14 - ex));
+            if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14));
+#pragma unroll 1
+            for (int j = 0; j < DV; j += 32) {
+              uint32_t x[32];
+              tmem_ld32(tq + PL::cM + j, x);
+              tmem_wait_ld();
+              copy_out(j, x, cs);
             }
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = drop ? 0u : __float_as_uint(__uint_as_float(x[e]) * dec * up);
-          tmem_st32(tq + j, x);
+          if (OUT) fence_proxy_async_smem();
+          tmem_wait_st();
         }
-        if (OUT) fence_proxy_async_smem();
-        tmem_wait_st();
         tc_fence_before();
         arrive(m_ready);
+        if (!await(tab_full(i), (i >> 1) & 1)) break;
+        dec = tabs[i & 1].dec;
+        arrive(tab_free(i));
+        if (kScaled) {
+          if (!await(ek_ready(i), (i >> 1) & 1)) break;
+          dn = exp2f((float)-misc[4 + (i & 1)]);
+        }
+        // the values: zeros behind the end, a note where one is not finite (thread = token)
+        if (!await(v_full, i & 1)) break;
+        if (r < nv) {
+          uint32_t mx = 0;
+#pragma unroll 1
+          for (int h = 0; h < DV / 8; h += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = lds128(base + PL::oV + ((h + k) >> 3) * 16384 + swz128(r, k));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+          }
+          if (max(mx & 0xffffu, mx >> 16) >= (kBf16 ? 0x7f80u : 0x7c00u)) {
+            misc[2 + (part & 1)] = part + 1;
+            a.repair[unit] = 1;
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < DV / 8; ++h)
+            sts128(base + PL::oV + (h >> 3) * 16384 + swz128(r, h & 7), make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();
+        }
+        arrive(kv_ready);
       }
       if (!ok || !upd_wait(i)) break;
       tc_fence_after();
-      // the state behind the part: into the array if the head ends here, else this CTA's contribution
+      // into the array if the head ends here, else this CTA's contribution
       const bool ends = w.chunk + count == w.chunks;
       float* dst = nullptr;
       if (a.pass == 0) dst = a.part + (long long)blockIdx.x * DK * DV;
       else if (ends && a.s_out != nullptr && misc[2 + (part & 1)] != part + 1 && a.repair[unit] == 0)
         dst = a.s_out + unit * DK * DV;
-      const float down = kScaled ? exp2f((float)-ek) : 1.f;
-      if (dst != nullptr || DK == 64) {
 #pragma unroll 1
-        for (int j = 0; j < DV; j += 32) {
-          uint32_t x[32];
-          tmem_ld32(tq + j, x);
-          tmem_wait_ld();
-          if constexpr (DK == 64) {
-            // rows 64-127 add theirs to rows 0-63 through the (idle) place of M's copy
-            float* const ex = reinterpret_cast<float*>(sb + PL::oSt);
-            if (!owner) {
+      for (int j = 0; j < DV; j += 32) {
+        uint32_t x[32];
+        state_of(j, x, true);
+        if constexpr (DK == 64) {
+          // rows 64-127 add theirs to rows 0-63 through the (idle) place of M's copy
+          float* const ex = reinterpret_cast<float*>(sb + PL::oSt);
+          if (!owner) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ex[(r - 64) * 33 + e] = __uint_as_float(x[e]);
-            }
-            arrive(met_m);
-            if (!await(met_m, meetings++ & 1)) break;
-            if (owner) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + ex[r * 33 + e]);
-            }
-            arrive(met_m);
-            if (!await(met_m, meetings++ & 1)) break;
+            for (int e = 0; e < 32; ++e) ex[(r - 64) * 33 + e] = __uint_as_float(x[e]);
           }
-          if (owner && dst != nullptr) {
-            float4* const p = reinterpret_cast<float4*>(dst + (long long)r * DV + j);
+          arrive(met_m);
+          if (!await(met_m, meetings++ & 1)) break;
+          if (owner) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              p[e] = make_float4(__uint_as_float(x[4 * e]) * down, __uint_as_float(x[4 * e + 1]) * down,
-                                 __uint_as_float(x[4 * e + 2]) * down, __uint_as_float(x[4 * e + 3]) * down);
+            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + ex[r * 33 + e]);
           }
+          arrive(met_m);
+          if (!await(met_m, meetings++ & 1)) break;
+        }
+        if (owner && dst != nullptr) {
+          float4* const p = reinterpret_cast<float4*>(dst + (long long)r * DV + j);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            p[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
+                               __uint_as_float(x[4 * e + 3]));
         }
       }
       if (!ok) break;
+      tc_fence_before();
       ++part;
       w.advance(a, count);
     }
   } else if (warp < 12) {
-    // ---- keys and values: thread = token ----
+    // ---- keys: thread = token ----
     const int quarter = warp & 3, r = quarter * 32 + lane;
     uint32_t meetings = 0;
     int part = 0;
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+    for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
         const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
         if (!await(k_full(i), (i >> 1) & 1)) break;
-        float up = 1.f;
-        if (kScaled) {
-          // the largest finite key of the chunk sets the chunk's power of two
-          uint32_t mx = 0;
-          if (r < nv) {
+        // the largest key of the chunk sets its power of two; one that is not finite is noted
+        uint32_t mx = 0;
+        if (r < nv) {
+#pragma unroll 1
+          for (int h = 0; h < DK / 8; h += 8) {
+            uint4 x[8];
 #pragma unroll
-            for (int ch = 0; ch < DK / 8; ++ch) {
-              const uint4 x = lds128(kb + (ch >> 3) * 16384 + swz128(r, ch & 7));
-              mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-            }
+            for (int k = 0; k < 8; ++k) x[k] = lds128(kb + (h >> 3) * 16384 + swz128(r, k));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
           }
           mx = max(mx & 0xffffu, mx >> 16);
+          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
+            misc[2 + (part & 1)] = part + 1;
+            a.repair[unit] = 1;
+          }
+        }
+        float up = 1.f;
+        int pre = 0;
+        if (kScaled) {
           mx = __reduce_max_sync(0xffffffffu, mx);
           if (lane == 0) misc[8 + quarter] = (int)mx;
           arrive(met);
           if (!await(met, meetings++ & 1)) break;
           const int bits = max(max(misc[8], misc[9]), max(misc[10], misc[11]));
-          // fp16 bits to an exponent: 2^(e) <= largest < 2^(e + 1)
           const float top = __half2float(__ushort_as_half((unsigned short)min(bits, 0x7bff)));
           const int ex = top == 0.f ? 0 : (int)(__float_as_uint(top) >> 23) - 127;
-          const int ek = 14 - ex;  // -1 .. 38
-          up = exp2f((float)ek);
+          // the largest to [2^14, 2^15): low parts then end at 2^-39 of it.  2^15 of it goes
+          // into the factor (times a decay it has to be a fp16 value), the rest of small
+          // keys' into the keys, exactly.
+          const int ek = min(14 - ex, 30);  // -1 .. 30
+          pre = max(ek - 15, 0);
+          up = exp2f((float)(ek - pre));
           if (quarter == 0 && lane == 0) {
             misc[4 + (i & 1)] = ek;
-            __threadfence_block();
             mbar_arrive(ek_ready(i));
           }
         }
         if (!await(tab_full(i), (i >> 1) & 1)) break;
-        const float wt = r < nv ? tabs[i & 1].w[r] : 0.f;
+        const float f = r < nv ? tabs[i & 1].w[r] * up : 0.f;
+        const uint32_t fh = pack16<T>(f, f);
+        const float fr = f - unpack16<T>(fh).x;
+        const uint32_t fl = pack16<T>(fr, fr);
+        const float pw = exp2f((float)pre);
+        const uint32_t up2 = pack16<T>(pw, pw);
         arrive(tab_free(i));
         if (OUT && !await(s_full, i & 1)) break;  // Q K^T has read the keys
         if (!upd_wait(i)) break;                  // and the last product the low parts
-        const float f = wt * up;
-        const bool zero = wt == 0.f;
-        uint32_t odd = 0;  // something here is not finite
-#pragma unroll 4
-        for (int ch = 0; ch < DK / 8; ++ch) {
-          const uint32_t off = (ch >> 3) * 16384 + swz128(r, ch & 7);
-          const uint4 x = lds128(kb + off);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], lo[4];
+#pragma unroll 1
+        for (int h = 0; h < DK / 8; h += 4) {  // four 16-byte units in flight
+          const uint32_t blk = (h >> 3) * 16384;
+          uint4 x[4], lo[4];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float2 y = unpack16<T>(xs[z]);
-            odd |= nonfinite16<T>(xs[z]);
-            const float y0 = zero ? 0.f : y.x * f, y1 = zero ? 0.f : y.y * f;
-            hi[z] = pack16<T>(y0, y1);
-            const float2 hv = unpack16<T>(hi[z]);
-            lo[z] = pack16<T>(y0 - hv.x, y1 - hv.y);
+          for (int k = 0; k < 4; ++k) x[k] = lds128(kb + blk + swz128(r, (h & 7) + k));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (r >= nv) x[k] = make_uint4(0, 0, 0, 0);
+            if (pre > 0) {
+              x[k].x = mul16x2(x[k].x, up2);
+              x[k].y = mul16x2(x[k].y, up2);
+              x[k].z = mul16x2(x[k].z, up2);
+              x[k].w = mul16x2(x[k].w, up2);
+            }
+            split16<T>(x[k].x, fh, fl, lo[k].x);
+            split16<T>(x[k].y, fh, fl, lo[k].y);
+            split16<T>(x[k].z, fh, fl, lo[k].z);
+            split16<T>(x[k].w, fh, fl, lo[k].w);
           }
-          sts128(kb + off, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(base + PL::oLo + off, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
-        if (!await(v_full, i & 1)) break;
-#pragma unroll 4
-        for (int ch = 0; ch < DV / 8; ++ch) {
-          const uint32_t at = base + PL::oV + (ch >> 3) * 16384 + swz128(r, ch & 7);
-          if (r < nv) {
-            const uint4 x = lds128(at);
-            odd |= nonfinite16<T>(x.x) | nonfinite16<T>(x.y) | nonfinite16<T>(x.z) | nonfinite16<T>(x.w);
-          } else {
-            sts128(at, make_uint4(0, 0, 0, 0));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sts128(kb + blk + swz128(r, (h & 7) + k), x[k]);
+            sts128(base + PL::oLo + blk + swz128(r, (h & 7) + k), lo[k]);
           }
-        }
-        if (odd != 0 && r < nv) {
-          misc[2 + (part & 1)] = part + 1;
-          a.repair[unit] = 1;
         }
         fence_proxy_async_smem();
         arrive(kv_ready);
@@ -642,10 +748,10 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
     // ---- scores and outputs: thread = token ----
     const int quarter = warp & 3, t = quarter * 32 + lane;
     const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
-    for (bool more = w.start(a, blockIdx.x, lane); ok && more; more = w.more()) {
+    for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
-        const int t0 = (w.chunk + c) * kLC, nv = w.n - t0;
+        const int t0 = (w.chunk + c) * kLC;
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         const LinTables& tb = tabs[i & 1];
         if (!await(s_full, i & 1)) break;
@@ -654,19 +760,29 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         // fp16: the row's largest score sets the row's power of two
         float up = 1.f, down = 1.f;
         if (kScaled) {
-          uint32_t mx = 0;
+          float big = 0.f;
 #pragma unroll 1
           for (int j = 0; j <= quarter; ++j) {
             uint32_t x[32];
             tmem_ld32(ts + 32 * j, x);
             tmem_wait_ld();
+            if (j == quarter) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (j < quarter || e <= lane) mx = max(mx, finite_bits(x[e]));
+              for (int e = 0; e < 32; ++e)
+                if (e > lane) x[e] = 0u;
+            }
+            big = fmaxf(big, abs_max32(x));
           }
+          if (__any_sync(0xffffffffu, big == INFINITY)) {  // by its finite scores
+            big = 0.f;
+#pragma unroll 1
+            for (int j = 0; j <= quarter; ++j) big = fmaxf(big, finite_max32(ts + 32 * j, j == quarter ? lane : 31));
+          }
+          const uint32_t mx = __float_as_uint(big);
           const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
-          up = exp2f((float)(14 - ex));
-          down = exp2f((float)(ex - 14));
+          const int eu = min(14 - ex, 40);  // (a bound for the state's part in the same units)
+          up = exp2f((float)eu);
+          down = exp2f((float)-eu);
         }
         const float rf = tb.rf[t] * up, hi = tb.hi[t], lo = tb.lo[t];
 #pragma unroll 1
@@ -681,9 +797,11 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float4 f = cf[e];
-                y[2 * e] = pack16<T>(__uint_as_float(x[4 * e]) * (rf * f.x), __uint_as_float(x[4 * e + 1]) * (rf * f.y));
-                y[2 * e + 1] =
-                    pack16<T>(__uint_as_float(x[4 * e + 2]) * (rf * f.z), __uint_as_float(x[4 * e + 3]) * (rf * f.w));
+                const f32x2 r2 = pair2(rf, rf);
+                y[2 * e] = pack16<T>(mul2(pair2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])),
+                                          mul2(pair2(f.x, f.y), r2)));
+                y[2 * e + 1] = pack16<T>(mul2(pair2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])),
+                                              mul2(pair2(f.z, f.w), r2)));
               }
             } else {
               const float4* const h4 = reinterpret_cast<const float4*>(tb.hi + 32 * j);
@@ -707,40 +825,74 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           }
           tmem_st16(ts + 16 * j, y);
         }
+        // the state's part of the output, in the units of P V: by e^{G_t}, M's copy's power
+        // of two and the row's
+        const float eg = tb.eg[t];
+        if (!await(qm_done, i & 1)) break;
+        tc_fence_after();
+        {
+          const float f = eg * (kScaled ? fmisc[6 + (i & 1)] : 1.f) * up;
+          const f32x2 f2 = pair2(f, f);
+          const bool drop = eg == 0.f;  // whatever the state holds
+#pragma unroll 1
+          for (int j = 0; j < DV; j += 32) {
+            uint32_t x[32];
+            tmem_ld32(tq + PL::cO + j, x);
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, drop)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (drop) x[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = unpair2(mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2));
+              x[e] = __float_as_uint(y.x);
+              x[e + 1] = __float_as_uint(y.y);
+            }
+            tmem_st32(tq + PL::cO + j, x);
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         arrive(p_ready);
-        const float eg = tb.eg[t];
         if (!pv_wait(i + 1)) break;
         tc_fence_after();
-        // (the state's part of the output was done before P V)
-        const float f1 = eg * a.scale * (kScaled ? fmisc[6 + (i & 1)] : 1.f), f2 = a.scale * down;
-        const bool drop = eg == 0.f;
-        T* const dst = static_cast<T*>(a.o) + (((long long)w.b * a.T + t0 + t) * a.H + w.h) * DV;
+        const float f1 = a.scale * down;
+        const f32x2 f12 = pair2(f1, f1);
+        // 64 columns at a time through shared memory: rows leave as 128-byte lines
+        const uint32_t stage = base + PL::oOut + quarter * 4096;
+        const int row = t0 + quarter * 32 + (lane >> 3);
+        T* const dst = static_cast<T*>(a.o) + (((long long)w.b * a.T + row) * a.H + w.h) * DV + (lane & 7) * 8;
 #pragma unroll 1
-        for (int j = 0; j < DV; j += 32) {
-          uint32_t x[32], z[32];
-          tmem_ld32(tq + PL::cO1 + j, x);
-          tmem_ld32(tq + PL::cO2 + j, z);
-          tmem_wait_ld();
-          if (t0 + t < a.T) {
+        for (int j = 0; j < DV; j += 64) {
+#pragma unroll 1
+          for (int hf = 0; hf < 64; hf += 32) {
+            uint32_t x[32];
+            tmem_ld32(tq + PL::cO + j + hf, x);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint32_t y[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float u0 = drop ? 0.f : __uint_as_float(x[e + 2 * k]) * f1;
-                const float u1 = drop ? 0.f : __uint_as_float(x[e + 2 * k + 1]) * f1;
-                y[k] = t < nv ? pack16<T>(fmaf(__uint_as_float(z[e + 2 * k]), f2, u0),
-                                          fmaf(__uint_as_float(z[e + 2 * k + 1]), f2, u1))
-                              : 0u;
-              }
-              *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int k = 0; k < 8; k += 2)
+                y[k / 2] = pack16<T>(mul2(pair2(__uint_as_float(x[e + k]), __uint_as_float(x[e + k + 1])), f12));
+              sts128(stage + swz128(lane, (hf + e) >> 3), make_uint4(y[0], y[1], y[2], y[3]));
             }
           }
+          if (j + 64 == DV) {  // the last read of this chunk's outputs
+            tc_fence_before();
+            arrive(o_free);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint4 y = lds128(stage + swz128(4 * k + (lane >> 3), lane & 7));
+            if (row + 4 * k >= w.n) y = make_uint4(0, 0, 0, 0);  // behind the sequence's end
+            if (row + 4 * k < a.T) *reinterpret_cast<uint4*>(dst + (long long)4 * k * a.H * DV + j) = y;
+          }
+          __syncwarp();
         }
-        tc_fence_before();
-        arrive(o_free);
         arrive(tab_free(i));
       }
       if (!ok) break;

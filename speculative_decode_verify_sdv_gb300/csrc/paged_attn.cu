@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
 // kernel's; a position a row does not see has weight zero and is skipped, so
 // nothing its values hold reaches the row.
 template <typename T>
-__global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = kAttnSimpleRows, P = kAttnSimpleTile;
   extern __shared__ float sm[];
   const int D = a.D, ld = D + 1;

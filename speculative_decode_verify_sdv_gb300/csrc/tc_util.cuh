@@ -96,6 +96,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       SDV_W8(v, 0), SDV_W8(v, 8), SDV_W8(v, 16), SDV_W8(v, 24)
       : "memory");
 }
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                SDV_W8(v, 0)
@@ -119,6 +127,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// A bounded wait by a whole warp, in few instructions: the roles of one kernel share
+// the SM's instruction cache.  On expiry the status word is set.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  bool done = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  if (!done) {
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    do done = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+    while (!done && global_timer_ns() - t0 < kWaitLimitNs);
+    if (!done && (threadIdx.x & 31) == 0) atomicOr(status, 1 /* kDevErrTimeout */);
+  }
+  return done;
+}
+
 // L2 policy of data that other CTAs read too.
 __device__ __forceinline__ uint64_t l2_policy_normal() {
   uint64_t p;
@@ -130,6 +152,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction, on register pairs.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // Two floats to a packed pair of the 16-bit type (a in the low half).
@@ -146,6 +191,12 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(f32x2 x) {
+  const float2 y = unpair2(x);
+  return pack16<T>(y.x, y.y);
 }
 
 // A packed pair to two floats.
