@@ -23,10 +23,10 @@
 // computes each part's own contribution (keys and values alone), and in the second
 // one each CTA sums those before it, decayed, on its way in.
 //
-// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 zeros behind a sequence's end; 4-7 the
-// state (one thread per key row of M: decay, 16-bit copy for Q M) and the values' check;
-// 8-11 the keys (K~ in place and beside); 12-15 scores to P, outputs.  All of it runs in
-// rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
+// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 the values' check; 4-7 the state (one
+// thread per key row of M: U, decay, 16-bit copy for Q M); 8-11 the keys (K~'s two
+// parts; 8-15 in the first launch); 12-15 scores to P; 16-19 outputs.  All of it
+// runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
 // times as slow).
 //
 // A zero weight must not meet an infinite value (0 * inf): a head with keys or values
@@ -115,22 +115,25 @@ struct LinTables {
   float hi[kLC], lo[kLC];  // G_t (log2 units)
   float eg[kLC];           // e^{G_t}
   float w[kLC];            // e^{G_C - G_s}
-  float rf[kLC];           // e^{G_t - G_r}, r the last token before t's block of 32
+  float rf[kLC];           // e^{G_t - G_r}, r the last token before t's block of 32 (G_r = 0 in the first)
   float cf[3][kLC];        // e^{G_r - G_s} for the blocks 1, 2, 3 (s <= r)
+  float cd[kLC];           // e^{G_r - G_s} inside s's own block, where `mild`
   float dec;               // e^{G_C}
+  int mild[4];             // blocks that decay by less than 2^-60: e^{G_t - G_s} = rf_t cd_s there too
   float pad[3];
 };
 
 template <int DK, int DV>
 struct LinPlan {
   static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2, kSt = 128 * DV * 2;
-  static constexpr int oK = 0, oLo = oK + 2 * kK, oQ = oLo + kK, oV = oQ + kK, oSt = oV + kV;
+  static constexpr int oK = 0, oHi = oK + kK, oLo = oHi + kK, oQ = oLo + kK, oV = oQ + kK, oSt = oV + kV;
   static constexpr int oOut = oSt + kSt;        // the output warps' 32 rows of 64 columns each
   static constexpr int oTab = oOut + 4 * 4096;
   static constexpr int oBars = oTab + 2 * (int)sizeof(LinTables);
   static constexpr int kNumBars = 24;
   static constexpr int oMisc = oBars + kNumBars * 8;
-  static constexpr int kTotal = oMisc + 128 + 1024;  // the base is aligned to 1024
+  static constexpr int oUp = oMisc + 128;     // the rows' powers of two [2][128]
+  static constexpr int kTotal = oUp + 2 * kLC * 4 + 1024;  // the base is aligned to 1024
   static constexpr int cS = 0, cO = 128, cU = 256, cM = 384;  // tensor-memory columns
   static_assert(kTotal <= 232448, "shared memory");
 };
@@ -206,11 +209,12 @@ struct LinWalk {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(OUT ? 512 : 384, 1)
+__global__ void __launch_bounds__(OUT ? 640 : 512, 1)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using PL = LinPlan<DK, DV>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kScaled = !kBf16;  // powers of two beside fp16 operands
+  constexpr int kKeyWarps = OUT ? 4 : 8;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const sb = smem_raw + (base - raw);
@@ -220,15 +224,17 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   const uint32_t q_full = bar(4), v_full = bar(5), s_full = bar(6), qm_done = bar(7), upd_done = bar(8),
                  pv_done = bar(9), m_ready = bar(10), kv_ready = bar(11), p_ready = bar(12), o_free = bar(13),
-                 met = bar(14), met_m = bar(15), drain = bar(16);
-  auto k_full = [&](int i) { return bar(i & 1); };
+                 met = bar(14), met_m = bar(15), drain = bar(16), up_ready = bar(22);
+  const uint32_t k_full = bar(0), k_read = bar(17);
   auto tab_full = [&](int i) { return bar(2 + (i & 1)); };
   auto tab_free = [&](int i) { return bar(18 + (i & 1)); };
   auto ek_ready = [&](int i) { return bar(20 + (i & 1)); };
   volatile int* const misc = reinterpret_cast<int*>(sb + PL::oMisc);
   // misc: 0 tmem base; 2, 3 a part whose values are not all finite; 4, 5 exponent of K~;
-  // 6, 7 exponent of M's copy; 8-11 and 12-15 the warps' maxima of keys and of the state
+  // 6, 7 M's copy's power of two undone; 8-15 the warps' maxima of keys; 16-19 of the
+  // state; 20, 21 the chunk's largest value
   volatile float* const fmisc = reinterpret_cast<volatile float*>(misc);
+  volatile float* const ups = reinterpret_cast<volatile float*>(sb + PL::oUp);
 
   if (warp == 1) {
     tmem_alloc(base + PL::oMisc, 512);
@@ -236,12 +242,17 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
-    for (int i = 10; i < 16; ++i)
-      if (i != 11) mbar_init(bar(i), 4);
+    mbar_init(m_ready, 4);
+    mbar_init(o_free, 4);
+    mbar_init(met_m, 4);
     mbar_init(drain, 1);
-    mbar_init(kv_ready, 8);
+    mbar_init(k_read, kKeyWarps);
+    mbar_init(kv_ready, kKeyWarps + 1);
+    mbar_init(met, kKeyWarps);
+    mbar_init(p_ready, 8);
+    mbar_init(up_ready, 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(18 + i), OUT ? 12 : 8);
+      mbar_init(bar(18 + i), 4 + kKeyWarps + (OUT ? 8 : 0));
       mbar_init(bar(20 + i), 1);
     }
     fence_barrier_init();
@@ -278,9 +289,8 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       if (!await(pv_done, pv_seen & 1)) return false;
     return true;
   };
-  // Every role but the zeros' walks the CTA's range.
   LinWalk from;
-  const bool any = warp == 3 ? false : from.start(a, blockIdx.x, lane);
+  const bool any = from.start(a, blockIdx.x, lane);
   LinWalk w = from;
   int i = 0;  // the CTA's chunk number
 
@@ -289,16 +299,17 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
     const uint64_t normal = l2_policy_normal();
     const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
     const int shared = a.H / a.Hqk;
-    int asked_q = 0, asked_v = 0;
+    int asked_k = 0, asked_q = 0, asked_v = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count(), hk = w.h / shared;
       for (int c = 0; c < count; ++c, ++i) {
         const int z = w.b * a.T + (w.chunk + c) * kLC;
-        // (phase i - 2 of upd_done has been seen by the values of chunk i - 1)
-        if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
+        // the keys before: read by Q K^T and by the keys' warps
+        if (i > 0 && (!await(k_read, (i - 1) & 1) || (OUT && !await(s_full, (i - 1) & 1)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(k_full, PL::kK);
         __syncwarp();
-        if (lane < DK / 64)
-          tma_load_3d(base + PL::oK + (i & 1) * PL::kK + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
+        if (lane < DK / 64) tma_load_3d(base + PL::oK + lane * 16384, &maps.k, lane * 64, hk, z, k_full, normal);
+        ++asked_k;
         if (OUT) {
           if (i > 0 && !await(qm_done, (i - 1) & 1)) break;
           if (lane == 0) mbar_arrive_expect_tx(q_full, PL::kK);
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       w.advance(a, count);
     }
     if (!ok) {  // copies whose consumers gave up have to land before the CTA ends
-      for (int e = i > 0 ? i - 1 : 0; e <= i; ++e) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
+      if (asked_k > 0) mbar_wait_bounded(k_full, (asked_k - 1) & 1, kLinDrainNs);
       if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
       if (asked_v > 0) mbar_wait_bounded(v_full, (asked_v - 1) & 1, kLinDrainNs);
     }
@@ -326,18 +337,17 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
     constexpr uint32_t id_kb = idesc_16_f32(kBf16, 128, DV, false, true);  // Q M and P V
     constexpr uint32_t id_up = idesc_16_f32(kBf16, 128, DV, true, true);
     const uint64_t qd = smem_desc_sw128(base + PL::oQ, 16, 1024);
+    const uint64_t kd = smem_desc_sw128(base + PL::oK, 16, 1024);
     const uint64_t vd = smem_desc_sw128(base + PL::oV, 16384, 1024);
     const uint64_t md = smem_desc_sw128(base + PL::oSt, 16384, 1024);
     // the chunks of all parts follow each other alike; a uniform count keeps the operands
     // in uniform registers
     const int total = __reduce_max_sync(0xffffffffu, any ? (int)(w.end - w.at) : 0);
     for (; ok && i < total; ++i) {
-      const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
       if (OUT) {
         // scores; P of the chunk before has been read
-        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), (i >> 1) & 1)) break;
+        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full, i & 1)) break;
         tc_fence_after();
-        const uint64_t kd = smem_desc_sw128(kb, 16, 1024);
 #pragma unroll 1
         for (int j = 0; j < DK / 64; ++j)
           tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
@@ -358,16 +368,16 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       // K~^T V: the low parts first; at Dk = 64 both at once (rows 0-63 from the high,
       // 64-127 from the low part)
       if constexpr (DK == 128) {
-        const uint64_t hd = smem_desc_sw128(kb, 16384, 1024);
+        const uint64_t hd = smem_desc_sw128(base + PL::oHi, 16384, 1024);
         const uint64_t ld = smem_desc_sw128(base + PL::oLo, 16384, 1024);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j)
           tc_mma4_ss<128, 128>(tm + PL::cU, (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
       } else {
-        const uint64_t kd = smem_desc_sw128(kb, base + PL::oLo - kb, 1024);
+        const uint64_t bd = smem_desc_sw128(base + PL::oHi, PL::oLo - PL::oHi, 1024);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j)
-          tc_mma4_ss<128, 128>(tm + PL::cU, kd + j * 512, vd + j * 512, id_up, j > 0);
+          tc_mma4_ss<128, 128>(tm + PL::cU, bd + j * 512, vd + j * 512, id_up, j > 0);
       }
       tc_commit_elect(upd_done);
       if (OUT) {
@@ -427,7 +437,6 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           eg[e] = exp2_approx(g[e].hi + g[e].lo);
           wt[e] = exp2_approx(all.minus(g[e]));
           if (OUT) {
-            rf[e] = blk == 0 ? 1.f : exp2_approx(g[e].minus(blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2]));
 #pragma unroll
             for (int q = 0; q < 3; ++q) cf[q][e] = blk <= q ? exp2_approx(ref[q].minus(g[e])) : 0.f;
           }
@@ -440,9 +449,23 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         put(tb.eg, eg);
         put(tb.w, wt);
         if (OUT) {
-          put(tb.rf, rf);
 #pragma unroll
           for (int q = 0; q < 3; ++q) put(tb.cf[q], cf[q]);
+        }
+        if (OUT) {
+          // within the block: its last token's sum against r's
+          const DecaySum r = blk == 0 ? DecaySum() : blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2];
+          const DecaySum end{__shfl_sync(0xffffffffu, incl.hi, lane | 7), __shfl_sync(0xffffffffu, incl.lo, lane | 7)};
+          const bool mild = end.minus(r) > -60.f;
+          float cd[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            cd[e] = mild ? exp2_approx(r.minus(g[e])) : 0.f;
+            rf[e] = exp2_approx(g[e].minus(r));
+          }
+          put(tb.cd, cd);
+          put(tb.rf, rf);
+          if ((lane & 7) == 0) tb.mild[blk] = mild;
         }
         if (lane == 0) tb.dec = exp2_approx(all.hi + all.lo);
         run.add(all);
@@ -454,16 +477,48 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       w.advance(a, count);
     }
   } else if (warp == 3) {
-    // ---- zeros behind the sequences' ends, whole chunks (heads dealt to the CTAs) ----
-    if (OUT) {
-      for (long long u = blockIdx.x; u < (long long)a.B * a.H; u += gridDim.x) {
-        const int b = (int)(u / a.H), h = (int)(u % a.H);
-        const int from = LinWalk::chunks_of(lin_tokens(a, b)) * kLC;
-        constexpr int per = DV / 8;  // 16-byte units of a row
-        for (long long e = (long long)from * per + lane; e < (long long)a.T * per; e += 32)
-          reinterpret_cast<uint4*>(a.o)[(((long long)b * a.T + e / per) * a.H + h) * per + e % per] =
-              make_uint4(0, 0, 0, 0);
+    // ---- the values: zeros behind the end, a note where one is not finite, the largest ----
+    int part = 0;
+    for (bool more = any; ok && more; more = w.more()) {
+      const int count = w.count();
+      for (int c = 0; c < count; ++c, ++i) {
+        const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
+        if (!await(v_full, i & 1)) break;
+        uint32_t mx = 0;
+        bool wrote = false;
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const int r = 32 * e + lane;
+#pragma unroll 1
+          for (int h = 0; h < DV / 64; ++h) {
+            const uint32_t row = base + PL::oV + h * 16384;
+            if (r < nv) {
+              uint4 x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = lds128(row + swz128(r, k));
+#pragma unroll
+              for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) sts128(row + swz128(r, k), make_uint4(0, 0, 0, 0));
+              wrote = true;
+            }
+          }
+        }
+        if (wrote) fence_proxy_async_smem();
+        mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+        if (lane == 0) {
+          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
+            misc[2 + (part & 1)] = part + 1;
+            a.repair[(long long)w.b * a.H + w.h] = 1;
+          }
+          if (kScaled) fmisc[20 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
+        }
+        arrive(kv_ready);
       }
+      if (!ok) break;
+      ++part;
+      w.advance(a, count);
     }
   } else if (warp < 8) {
     // ---- the state: thread = key row of M (at Dk = 64: rows 64-127 hold the low part) ----
@@ -476,6 +531,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;
       // the state before the part: what was given, then the parts before this one, in order
+      float bound = 0.f;  // of M's finite entries: what they start at, then what a chunk can add
       const int first = a.pass == 1 && w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
 #pragma unroll 1
       for (int j = 0; j < DV; j += 32) {
@@ -501,8 +557,19 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           }
         }
         tmem_st32(tq + PL::cM + j, reinterpret_cast<const uint32_t*>(x));
+        if (OUT && kScaled) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) bound = fmaxf(bound, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
+        }
       }
       tmem_wait_st();
+      if (OUT && kScaled) {
+        const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(bound));
+        if (lane == 0) misc[16 + quarter] = (int)mx;
+        arrive(met_m);
+        if (!await(met_m, meetings++ & 1)) break;
+        bound = __uint_as_float(max(max(misc[16], misc[17]), max(misc[18], misc[19])));
+      }
       float dec = 0.f, dn = 1.f;  // of the last chunk: M = dec M + dn U
       auto state_of = [&](int j, uint32_t (&x)[32], bool take) {  // 32 columns of M behind the last chunk
         tmem_ld32(tq + PL::cM + j, x);
@@ -537,48 +604,30 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         }
       };
       for (int c = 0; c < count; ++c, ++i) {
-        const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
         if (!upd_wait(i)) break;
         tc_fence_after();
         if (OUT || c > 0) {
-          float big = 0.f;
+          float cs = 1.f;  // what M's copy carries
+          if (OUT && kScaled) {
+            // |U| is at most 128 times the largest |k~| (below 2^15 in U's units) times the
+            // largest value: the bound is loose by the square root of what it counts, far
+            // within what fp16's 30 octaves leave
+            if (c > 0) bound = bound * dec + 4194304.f * dn * fmisc[20 + ((i - 1) & 1)];
+            const int ex = min(max((int)(__float_as_uint(bound) >> 23) - 127, -100), 120);
+            cs = exp2f((float)(14 - ex));  // the bound to [2^14, 2^15)
+            if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14));
+          }
 #pragma unroll 1
           for (int j = 0; j < DV; j += 32) {
             uint32_t x[32];
             state_of(j, x, c > 0);
             if (c > 0) tmem_st32(tq + PL::cM + j, x);
-            if (OUT && kScaled) big = fmaxf(big, abs_max32(x));
-            if (OUT && !kScaled) copy_out(j, x, 1.f);
-          }
-          if (OUT && kScaled) {
-            tmem_wait_st();
-            if (__any_sync(0xffffffffu, big == INFINITY)) {  // by its finite entries
-              big = 0.f;
-#pragma unroll 1
-              for (int j = 0; j < DV; j += 32) big = fmaxf(big, finite_max32(tq + PL::cM + j, 31));
-            }
-            uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-            if (lane == 0) misc[12 + quarter] = (int)mx;
-            arrive(met_m);
-            if (!await(met_m, meetings++ & 1)) break;
-            mx = max(max(misc[12], misc[13]), max(misc[14], misc[15]));
-            // the largest to [2^14, 2^15)
-            const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
-            const float cs = exp2f((float)(14 - ex));
-            if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14));
-#pragma unroll 1
-            for (int j = 0; j < DV; j += 32) {
-              uint32_t x[32];
-              tmem_ld32(tq + PL::cM + j, x);
-              tmem_wait_ld();
-              copy_out(j, x, cs);
-            }
+            if (OUT) copy_out(j, x, cs);
           }
           if (OUT) fence_proxy_async_smem();
           tmem_wait_st();
         }
-        tc_fence_before();
-        arrive(m_ready);
+        // this chunk's factors, before the product may go on (the next but one's come after it)
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         dec = tabs[i & 1].dec;
         arrive(tab_free(i));
@@ -586,29 +635,8 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           if (!await(ek_ready(i), (i >> 1) & 1)) break;
           dn = exp2f((float)-misc[4 + (i & 1)]);
         }
-        // the values: zeros behind the end, a note where one is not finite (thread = token)
-        if (!await(v_full, i & 1)) break;
-        if (r < nv) {
-          uint32_t mx = 0;
-#pragma unroll 1
-          for (int h = 0; h < DV / 8; h += 8) {
-            uint4 x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = lds128(base + PL::oV + ((h + k) >> 3) * 16384 + swz128(r, k));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
-          }
-          if (max(mx & 0xffffu, mx >> 16) >= (kBf16 ? 0x7f80u : 0x7c00u)) {
-            misc[2 + (part & 1)] = part + 1;
-            a.repair[unit] = 1;
-          }
-        } else {
-#pragma unroll 1
-          for (int h = 0; h < DV / 8; ++h)
-            sts128(base + PL::oV + (h >> 3) * 16384 + swz128(r, h & 7), make_uint4(0, 0, 0, 0));
-          fence_proxy_async_smem();
-        }
-        arrive(kv_ready);
+        tc_fence_before();
+        arrive(m_ready);
       }
       if (!ok || !upd_wait(i)) break;
       tc_fence_after();
@@ -651,9 +679,11 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       ++part;
       w.advance(a, count);
     }
-  } else if (warp < 12) {
-    // ---- keys: thread = token ----
+  } else if (warp < 8 + kKeyWarps) {
+    // ---- keys: thread = token (at eight warps: half of its elements) ----
     const int quarter = warp & 3, r = quarter * 32 + lane;
+    constexpr int kUnits = DK / 8 / (kKeyWarps / 4);  // a thread's 16-byte units
+    const int u0 = (warp - 8) / 4 * kUnits;
     uint32_t meetings = 0;
     int part = 0;
     for (bool more = any; ok && more; more = w.more()) {
@@ -661,18 +691,18 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
       const long long unit = (long long)w.b * a.H + w.h;
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
-        const uint32_t kb = base + PL::oK + (i & 1) * PL::kK;
-        if (!await(k_full(i), (i >> 1) & 1)) break;
+        const uint32_t kb = base + PL::oK;
+        if (!await(k_full, i & 1)) break;
         // the largest key of the chunk sets its power of two; one that is not finite is noted
         uint32_t mx = 0;
         if (r < nv) {
 #pragma unroll 1
-          for (int h = 0; h < DK / 8; h += 8) {
-            uint4 x[8];
+          for (int h = u0; h < u0 + kUnits; h += 4) {
+            uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = lds128(kb + (h >> 3) * 16384 + swz128(r, k));
+            for (int k = 0; k < 4; ++k) x[k] = lds128(kb + (h >> 3) * 16384 + swz128(r, (h & 7) + k));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+            for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
           }
           mx = max(mx & 0xffffu, mx >> 16);
           if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
@@ -684,10 +714,11 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         int pre = 0;
         if (kScaled) {
           mx = __reduce_max_sync(0xffffffffu, mx);
-          if (lane == 0) misc[8 + quarter] = (int)mx;
+          if (lane == 0) misc[warp] = (int)mx;
           arrive(met);
           if (!await(met, meetings++ & 1)) break;
-          const int bits = max(max(misc[8], misc[9]), max(misc[10], misc[11]));
+          int bits = max(max(misc[8], misc[9]), max(misc[10], misc[11]));
+          if (kKeyWarps == 8) bits = max(bits, max(max(misc[12], misc[13]), max(misc[14], misc[15])));
           const float top = __half2float(__ushort_as_half((unsigned short)min(bits, 0x7bff)));
           const int ex = top == 0.f ? 0 : (int)(__float_as_uint(top) >> 23) - 127;
           // the largest to [2^14, 2^15): low parts then end at 2^-39 of it.  2^15 of it goes
@@ -696,7 +727,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           const int ek = min(14 - ex, 30);  // -1 .. 30
           pre = max(ek - 15, 0);
           up = exp2f((float)(ek - pre));
-          if (quarter == 0 && lane == 0) {
+          if (warp == 8 && lane == 0) {
             misc[4 + (i & 1)] = ek;
             mbar_arrive(ek_ready(i));
           }
@@ -709,10 +740,9 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         const float pw = exp2f((float)pre);
         const uint32_t up2 = pack16<T>(pw, pw);
         arrive(tab_free(i));
-        if (OUT && !await(s_full, i & 1)) break;  // Q K^T has read the keys
-        if (!upd_wait(i)) break;                  // and the last product the low parts
+        if (!upd_wait(i)) break;  // the last product has read K~
 #pragma unroll 1
-        for (int h = 0; h < DK / 8; h += 4) {  // four 16-byte units in flight
+        for (int h = u0; h < u0 + kUnits; h += 4) {  // four 16-byte units in flight
           const uint32_t blk = (h >> 3) * 16384;
           uint4 x[4], lo[4];
 #pragma unroll
@@ -733,32 +763,32 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            sts128(kb + blk + swz128(r, (h & 7) + k), x[k]);
+            sts128(base + PL::oHi + blk + swz128(r, (h & 7) + k), x[k]);
             sts128(base + PL::oLo + blk + swz128(r, (h & 7) + k), lo[k]);
           }
         }
         fence_proxy_async_smem();
+        arrive(k_read);
         arrive(kv_ready);
       }
       if (!ok) break;
       ++part;
       w.advance(a, count);
     }
-  } else if (OUT) {
-    // ---- scores and outputs: thread = token ----
+  } else if (OUT && warp < 16) {
+    // ---- scores: thread = token ----
     const int quarter = warp & 3, t = quarter * 32 + lane;
     const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
-        const int t0 = (w.chunk + c) * kLC;
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         const LinTables& tb = tabs[i & 1];
         if (!await(s_full, i & 1)) break;
         tc_fence_after();
         const uint32_t ts = tq + PL::cS;
         // fp16: the row's largest score sets the row's power of two
-        float up = 1.f, down = 1.f;
+        float up = 1.f;
         if (kScaled) {
           float big = 0.f;
 #pragma unroll 1
@@ -782,9 +812,13 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
           const int eu = min(14 - ex, 40);  // (a bound for the state's part in the same units)
           up = exp2f((float)eu);
-          down = exp2f((float)-eu);
+        }
+        if (kScaled) {
+          ups[(i & 1) * kLC + t] = up;
+          arrive(up_ready);
         }
         const float rf = tb.rf[t] * up, hi = tb.hi[t], lo = tb.lo[t];
+        const bool mild = tb.mild[quarter] != 0;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
           uint32_t y[16];
@@ -792,16 +826,20 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
             uint32_t x[32];
             tmem_ld32(ts + 32 * j, x);
             tmem_wait_ld();
-            if (j < quarter) {
-              const float4* const cf = reinterpret_cast<const float4*>(tb.cf[quarter - 1] + 32 * j);
+            if (j < quarter || mild) {
+              const float4* const cf = reinterpret_cast<const float4*>((j < quarter ? tb.cf[quarter - 1] : tb.cd) + 32 * j);
+              const f32x2 r2 = pair2(rf, rf);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float4 f = cf[e];
-                const f32x2 r2 = pair2(rf, rf);
                 y[2 * e] = pack16<T>(mul2(pair2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])),
                                           mul2(pair2(f.x, f.y), r2)));
                 y[2 * e + 1] = pack16<T>(mul2(pair2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])),
                                               mul2(pair2(f.z, f.w), r2)));
+              }
+              if (j == quarter) {  // tokens behind t
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] &= 2 * e + 1 <= lane ? 0xffffffffu : 2 * e <= lane ? 0x0000ffffu : 0u;
               }
             } else {
               const float4* const h4 = reinterpret_cast<const float4*>(tb.hi + 32 * j);
@@ -825,9 +863,41 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
           }
           tmem_st16(ts + 16 * j, y);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(p_ready);
+        arrive(tab_free(i));
+      }
+      if (!ok) break;
+      w.advance(a, count);
+    }
+  } else if (OUT) {
+    // ---- outputs: thread = token, then rows as 128-byte lines ----
+    // first the zeros behind the sequences' ends, whole chunks (heads dealt to the CTAs)
+    for (long long u = blockIdx.x; u < (long long)a.B * a.H; u += gridDim.x) {
+      const int b = (int)(u / a.H), h = (int)(u % a.H);
+      const int first = LinWalk::chunks_of(lin_tokens(a, b)) * kLC;
+      constexpr int per = DV / 8;  // 16-byte units of a row
+      for (long long e = (long long)first * per + (warp - 16) * 32 + lane; e < (long long)a.T * per; e += 128)
+        reinterpret_cast<uint4*>(a.o)[(((long long)b * a.T + e / per) * a.H + h) * per + e % per] =
+            make_uint4(0, 0, 0, 0);
+    }
+    const int quarter = warp & 3, t = quarter * 32 + lane;
+    const uint32_t tq = tm + PL::cO + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t stage = base + PL::oOut + quarter * 4096;
+    for (bool more = any; ok && more; more = w.more()) {
+      const int count = w.count();
+      for (int c = 0; c < count; ++c, ++i) {
         // the state's part of the output, in the units of P V: by e^{G_t}, M's copy's power
         // of two and the row's
-        const float eg = tb.eg[t];
+        if (!await(tab_full(i), (i >> 1) & 1)) break;
+        const float eg = tabs[i & 1].eg[t];
+        arrive(tab_free(i));
+        float up = 1.f;
+        if (kScaled) {
+          if (!await(up_ready, i & 1)) break;
+          up = ups[(i & 1) * kLC + t];
+        }
         if (!await(qm_done, i & 1)) break;
         tc_fence_after();
         {
@@ -837,7 +907,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
 #pragma unroll 1
           for (int j = 0; j < DV; j += 32) {
             uint32_t x[32];
-            tmem_ld32(tq + PL::cO + j, x);
+            tmem_ld32(tq + j, x);
             tmem_wait_ld();
             if (__any_sync(0xffffffffu, drop)) {
 #pragma unroll
@@ -850,7 +920,7 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
               x[e] = __float_as_uint(y.x);
               x[e + 1] = __float_as_uint(y.y);
             }
-            tmem_st32(tq + PL::cO + j, x);
+            tmem_st32(tq + j, x);
           }
         }
         tmem_wait_st();
@@ -858,42 +928,37 @@ __global__ void __launch_bounds__(OUT ? 512 : 384, 1)
         arrive(p_ready);
         if (!pv_wait(i + 1)) break;
         tc_fence_after();
-        const float f1 = a.scale * down;
-        const f32x2 f12 = pair2(f1, f1);
-        // 64 columns at a time through shared memory: rows leave as 128-byte lines
-        const uint32_t stage = base + PL::oOut + quarter * 4096;
-        const int row = t0 + quarter * 32 + (lane >> 3);
+        const float f = a.scale / up;  // (a power of two)
+        const int row = (w.chunk + c) * kLC + quarter * 32 + (lane >> 3);
         T* const dst = static_cast<T*>(a.o) + (((long long)w.b * a.T + row) * a.H + w.h) * DV + (lane & 7) * 8;
 #pragma unroll 1
-        for (int j = 0; j < DV; j += 64) {
-#pragma unroll 1
+        for (int j = 0; j < DV; j += 64) {  // 64 columns at a time through shared memory
+          uint32_t y[32];
+#pragma unroll
           for (int hf = 0; hf < 64; hf += 32) {
             uint32_t x[32];
-            tmem_ld32(tq + PL::cO + j + hf, x);
+            tmem_ld32(tq + j + hf, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 8; k += 2)
-                y[k / 2] = pack16<T>(mul2(pair2(__uint_as_float(x[e + k]), __uint_as_float(x[e + k + 1])), f12));
-              sts128(stage + swz128(lane, (hf + e) >> 3), make_uint4(y[0], y[1], y[2], y[3]));
-            }
+            for (int e = 0; e < 32; e += 2)
+              y[(hf + e) / 2] = pack16<T>(mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair2(f, f)));
           }
           if (j + 64 == DV) {  // the last read of this chunk's outputs
             tc_fence_before();
             arrive(o_free);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sts128(stage + swz128(lane, e), make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            uint4 y = lds128(stage + swz128(4 * k + (lane >> 3), lane & 7));
-            if (row + 4 * k >= w.n) y = make_uint4(0, 0, 0, 0);  // behind the sequence's end
-            if (row + 4 * k < a.T) *reinterpret_cast<uint4*>(dst + (long long)4 * k * a.H * DV + j) = y;
+            uint4 v = lds128(stage + swz128(4 * k + (lane >> 3), lane & 7));
+            if (row + 4 * k >= w.n) v = make_uint4(0, 0, 0, 0);  // behind the sequence's end
+            if (row + 4 * k < a.T) *reinterpret_cast<uint4*>(dst + (long long)4 * k * a.H * DV + j) = v;
           }
           __syncwarp();
         }
-        arrive(tab_free(i));
       }
       if (!ok) break;
       w.advance(a, count);
@@ -922,7 +987,7 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 512 : 384), smem, st, m, a);
+  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 640 : 512), smem, st, m, a);
 }
 
 }  // namespace
