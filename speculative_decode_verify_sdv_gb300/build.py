@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libsdv.so")
 
 SOURCES = ["api.cu", "dq_gemm.cu", "tc_gemm.cu", "gemv.cu", "small_kernels.cu", "moe_kernels.cu", "noalloc.cu",
            "ngram_drafter.cu", "paged_attn.cu", "attn_tc.cu", "attn_tc_bf16.cu",
-           "linear_attn.cu", "linear_tc.cu", "linear_tc_bf16.cu"]
+           "linear_attn.cu", "linear_tc.cu", "linear_tc_bf16.cu",
+           "linear_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -58,8 +58,11 @@ struct LinMaps {
 constexpr int kLinChunk = 128;   // tokens of a chunk
 constexpr int kLinRuns = 16;     // CTAs that share one head at most
 
-// Whether the chunked form has an instance for the head sizes.
+constexpr int kLinWindow = 32;   // tokens of the window form at most
+
+// Whether the chunked and the window form have an instance for the head sizes.
 inline bool linear_tc_takes(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
+cudaError_t launch_linear_window(int dtype, const LinArgs& a, cudaStream_t st);
 cudaError_t launch_linear_tc(int dtype, const LinArgs& a, cudaStream_t st);
 cudaError_t linear_tc_f16(const LinMaps& m, const LinArgs& a, cudaStream_t st);
 cudaError_t linear_tc_bf16(const LinMaps& m, const LinArgs& a, cudaStream_t st);

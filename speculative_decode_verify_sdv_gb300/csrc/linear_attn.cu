@@ -145,10 +145,12 @@ bool lin_shape(int B, int T, int H, int Dk, int Dv) {
 size_t lin_notes(int B, int H) { return round_256((size_t)B * H * 4); }
 size_t lin_parts(int ctas, int Dk, int Dv) { return round_256((size_t)ctas * 8) + (size_t)ctas * Dk * Dv * 4; }
 
-// The chunked form for the head sizes that it has and for kLinChunkFrom tokens or more.
-constexpr int kLinChunkFrom = 5;
+// The window form for kLinWindowFrom to 32 tokens, the chunked form for more, both for
+// the head sizes that they have; one token, and other head sizes, are the recurrent form's.
+constexpr int kLinWindowFrom = 2;
+bool lin_window(int T, int Dk, int Dv) { return linear_tc_takes(Dk, Dv) && T >= kLinWindowFrom && T <= kLinWindow; }
 bool lin_chunked(int B, int T, int Dk, int Dv) {
-  return linear_tc_takes(Dk, Dv) && T >= kLinChunkFrom && (long long)B * T <= INT32_MAX - 2 * kLinChunk;
+  return linear_tc_takes(Dk, Dv) && T > kLinWindow && (long long)B * T <= INT32_MAX - 2 * kLinChunk;
 }
 
 bool lin_limits(int B, int H, int Dk, int Dv) { return B <= 65535 && H <= 4096 && Dk <= 256 && Dv <= 256; }
@@ -211,6 +213,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
   a.s_out = state_out_or_null;
   a.o = o_or_null;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (lin_window(T, Dk, Dv)) return status_of(launch_linear_window(dtype, a, st));
   if (lin_chunked(B, T, Dk, Dv)) {
     a.ctas = sm_count();
     if (a.ctas <= 0) return SDV_ERR_CUDA;
