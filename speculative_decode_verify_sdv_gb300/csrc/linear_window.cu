@@ -44,6 +44,19 @@ __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&d)[4], const uint32
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// D += A B, m16n8k8, tf32 operands (10-bit mantissas, fp32's range), fp32 sums.
+__device__ __forceinline__ void mma8_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -110,11 +123,16 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
     *reinterpret_cast<uint4*>(&sq[t][c]) = x;
     *reinterpret_cast<uint4*>(&sk[t][c]) = y;
   }
+  uint32_t vmax = 0;
   for (int e = threadIdx.x; e < kWin * (DV / 8); e += kThreads) {
     const int t = e / (DV / 8), c = e % (DV / 8) * 8;
-    *reinterpret_cast<uint4*>(&sv[t][c]) =
-        t < n ? __ldg(reinterpret_cast<const uint4*>(v + t * a.v_stride + c)) : make_uint4(0, 0, 0, 0);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (t < n) x = __ldg(reinterpret_cast<const uint4*>(v + t * a.v_stride + c));
+    *reinterpret_cast<uint4*>(&sv[t][c]) = x;
+    vmax = __vmaxu2(vmax, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
   }
+  const bool odd = max(vmax & 0xffffu, vmax >> 16) >= (kBf16 ? 0x7f80u : 0x7c00u);
   if (warp == 0) sg[lane] = window_decay(a, b, h, n, lane);
   // the largest finite entry of the state sets the copy's power of two (fp16)
   if (!kBf16) {
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
     const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
     if (lane == 0) smax[warp] = __uint_as_float(mx);
   }
-  __syncthreads();
+  const bool infinite = __syncthreads_or(odd);  // a value that is not finite
   float up = 1.f, down = 1.f;
   if (!kBf16) {
     float big = smax[0];
@@ -194,7 +212,28 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[mt][j][e] = eg == 0.f ? 0.f : o[mt][j][e] * f;  // drops whatever the state holds
     }
-  // the parts' sums to part 0 (sp is complete behind the same barrier)
+  // the window's own tokens: P V in steps of 8 tokens dealt to the parts.  P as tf32 keeps
+  // fp32's range (scores need no scale) and 11 bits; a value of the type is one of tf32's.
+  __syncthreads();
+  if (!infinite) {
+#pragma unroll 1
+    for (int s0 = 8 * part; s0 < n; s0 += 8 * kParts) {
+      const int s = s0 + (lane & 3);
+      const uint2 x0 = *reinterpret_cast<const uint2*>(&sv[s][32 * grp + 4 * nc]);
+      const uint2 x1 = *reinterpret_cast<const uint2*>(&sv[s + 4][32 * grp + 4 * nc]);
+      const float2 u0 = unpack16<T>(x0.x), u1 = unpack16<T>(x0.y), w0 = unpack16<T>(x1.x), w1 = unpack16<T>(x1.y);
+      const float b0[4] = {u0.x, u0.y, u1.x, u1.y}, b1[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        if (mt == 1 && !two) break;
+        const uint32_t fa[4] = {to_tf32(sp[16 * mt + nc][s]), to_tf32(sp[16 * mt + nc + 8][s]),
+                                to_tf32(sp[16 * mt + nc][s + 4]), to_tf32(sp[16 * mt + nc + 8][s + 4])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma8_tf32(o[mt][j], fa, __float_as_uint(b0[j]), __float_as_uint(b1[j]));
+      }
+    }
+  }
+  // the parts' sums to part 0
   if (part > 0) {
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
@@ -219,55 +258,55 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
         o[mt][2][e] += y.z;
         o[mt][3][e] += y.w;
       }
-  // the window's own tokens in fp32: a lane's eight rows and columns (the scores are few)
   T* const out = static_cast<T*>(a.o) + ((long long)b * a.T * a.H + h) * DV;
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int t = 16 * mt + nc + 8 * hf;
-      if (16 * mt >= a.T) continue;
-      for (int s = 0; s <= t && s < n; ++s) {
-        const float p = sp[t][s];
-        if (p == 0.f) continue;  // dropped since, whatever its values are
+      if (t >= a.T) continue;
+      if (infinite) {  // one by one: a weight of zero must not meet them
+        for (int s = 0; s <= t && s < n; ++s) {
+          const float p = sp[t][s];
+          if (p == 0.f) continue;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint2 x = *reinterpret_cast<const uint2*>(&sv[s][32 * grp + 4 * (kr + e)]);
-          const float2 y0 = unpack16<T>(x.x), y1 = unpack16<T>(x.y);
-          float* const w = &o[mt][0][2 * hf + e];
-          w[0] = fmaf(p, y0.x, w[0]);
-          w[4] = fmaf(p, y0.y, w[4]);
-          w[8] = fmaf(p, y1.x, w[8]);
-          w[12] = fmaf(p, y1.y, w[12]);
+          for (int e = 0; e < 2; ++e) {
+            const uint2 x = *reinterpret_cast<const uint2*>(&sv[s][32 * grp + 4 * (kr + e)]);
+            const float2 y0 = unpack16<T>(x.x), y1 = unpack16<T>(x.y);
+            o[mt][0][2 * hf + e] = fmaf(p, y0.x, o[mt][0][2 * hf + e]);
+            o[mt][1][2 * hf + e] = fmaf(p, y0.y, o[mt][1][2 * hf + e]);
+            o[mt][2][2 * hf + e] = fmaf(p, y1.x, o[mt][2][2 * hf + e]);
+            o[mt][3][2 * hf + e] = fmaf(p, y1.y, o[mt][3][2 * hf + e]);
+          }
         }
       }
-      if (t < a.T) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float* const w = &o[mt][0][2 * hf + e];
-          const uint2 y = t < n ? make_uint2(pack16<T>(w[0] * a.scale, w[4] * a.scale),
-                                             pack16<T>(w[8] * a.scale, w[12] * a.scale))
-                                : make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(out + (long long)t * a.H * DV + 32 * grp + 4 * (kr + e)) = y;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const float f = a.scale;
+        const uint2 y = t < n ? make_uint2(pack16<T>(o[mt][0][2 * hf + e] * f, o[mt][1][2 * hf + e] * f),
+                                           pack16<T>(o[mt][2][2 * hf + e] * f, o[mt][3][2 * hf + e] * f))
+                              : make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(out + (long long)t * a.H * DV + 32 * grp + 4 * (kr + e)) = y;
       }
     }
 }
 
 // ---- the state behind the window --------------------------------------------------------
 
-// A CTA per head; thread = 4 columns x DK / 8 rows of the state.  Decayed keys and values
-// come from shared memory in fp32.
+// A CTA per head and 64 value columns; thread = 4 columns x DK / 16 rows of the state:
+// few enough registers for four CTAs and more per SM (one CTA of twice the rows per head
+// was 1.7 waves of two: 21.8 us for 512 heads).  Keys and values come from shared memory
+// in fp32.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kWinThreads) linear_commit_kernel(const LinArgs a) {
-  constexpr int kCols = DV / 4, kRowSets = kWinThreads / kCols, kRows = DK / kRowSets;
-  __shared__ float4 sk[kWin][DK / 4], sv[kWin][DV / 4];
+  constexpr int kCols = 16, kRowSets = kWinThreads / kCols, kRows = DK / kRowSets;
+  __shared__ float4 sk[kWin][DK / 4], sv[kWin][kCols];
   __shared__ float sw[kWin], sdec;
   griddep_wait();
-  const int h = blockIdx.x, b = blockIdx.y, hk = h / (a.H / a.Hqk);
+  const int h = blockIdx.x / (DV / 64), c0 = blockIdx.x % (DV / 64) * 64, b = blockIdx.y, hk = h / (a.H / a.Hqk);
   const int n = lin_tokens(a, b);
   const int c = threadIdx.x % kCols, r0 = threadIdx.x / kCols * kRows;
-  const long long at = ((long long)b * a.H + h) * DK * DV + (long long)r0 * DV + 4 * c;
+  const long long at = ((long long)b * a.H + h) * DK * DV + (long long)r0 * DV + c0 + 4 * c;
   float4 m[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
@@ -281,15 +320,15 @@ __global__ void __launch_bounds__(kWinThreads) linear_commit_kernel(const LinArg
     if (lane == 0) sdec = exp2f(all.hi + all.lo);
   }
   const T* const k = static_cast<const T*>(a.k) + (long long)b * a.T * a.k_stride + hk * DK;
-  const T* const v = static_cast<const T*>(a.v) + (long long)b * a.T * a.v_stride + h * DV;
+  const T* const v = static_cast<const T*>(a.v) + (long long)b * a.T * a.v_stride + h * DV + c0;
   for (int e = threadIdx.x; e < n * (DK / 4); e += kWinThreads) {
     const int t = e / (DK / 4), d = e % (DK / 4);
     const uint2 x = __ldg(reinterpret_cast<const uint2*>(k + t * a.k_stride + 4 * d));
     const float2 y = unpack16<T>(x.x), z = unpack16<T>(x.y);
     sk[t][d] = make_float4(y.x, y.y, z.x, z.y);
   }
-  for (int e = threadIdx.x; e < n * (DV / 4); e += kWinThreads) {
-    const int t = e / (DV / 4), d = e % (DV / 4);
+  for (int e = threadIdx.x; e < n * kCols; e += kWinThreads) {
+    const int t = e / kCols, d = e % kCols;
     const uint2 x = __ldg(reinterpret_cast<const uint2*>(v + t * a.v_stride + 4 * d));
     const float2 y = unpack16<T>(x.x), z = unpack16<T>(x.y);
     sv[t][d] = make_float4(y.x, y.y, z.x, z.y);
@@ -333,7 +372,7 @@ cudaError_t window_launch(const LinArgs& a, cudaStream_t st) {
     e = launch_pdl(linear_window_kernel<T, DK, DV>, dim3(a.H, a.B), dim3(DV * 2), 0, st, a);
   // behind the outputs: the two states may be one array
   if (e == cudaSuccess && a.s_out != nullptr)
-    e = launch_pdl(linear_commit_kernel<T, DK, DV>, dim3(a.H, a.B), dim3(kWinThreads), 0, st, a);
+    e = launch_pdl(linear_commit_kernel<T, DK, DV>, dim3(a.H * (DV / 64), a.B), dim3(kWinThreads), 0, st, a);
   return e;
 }
 
