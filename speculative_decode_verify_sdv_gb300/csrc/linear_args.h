@@ -43,7 +43,7 @@ struct LinArgs {
   void* o;
   // chunked form: a CTA's local state and its log2 decay, heads whose values are not
   // finite (recomputed by the recurrent kernel), status
-  float* part;             // [CTAs][Dk][Dv]
+  float* part;             // [CTAs][Dv / 4][Dk][4]
   DecaySum* part_decay;    // [CTAs]
   int* repair;             // [B][H]
   int* status;

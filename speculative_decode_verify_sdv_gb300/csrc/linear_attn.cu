@@ -149,8 +149,11 @@ size_t lin_parts(int ctas, int Dk, int Dv) { return round_256((size_t)ctas * 8) 
 // the head sizes that they have; one token, and other head sizes, are the recurrent form's.
 constexpr int kLinWindowFrom = 2;
 bool lin_window(int T, int Dk, int Dv) { return linear_tc_takes(Dk, Dv) && T >= kLinWindowFrom && T <= kLinWindow; }
-bool lin_chunked(int B, int T, int Dk, int Dv) {
-  return linear_tc_takes(Dk, Dv) && T > kLinWindow && (long long)B * T <= INT32_MAX - 2 * kLinChunk;
+bool lin_chunked(int B, int T, int H, int Dk, int Dv) {
+  // the tensor maps' coordinates and the split's arithmetic are 32-bit
+  const long long chunks = (long long)B * H * ((T + kLinChunk - 1) / kLinChunk);
+  return linear_tc_takes(Dk, Dv) && T > kLinWindow && (long long)B * T <= INT32_MAX - 2 * kLinChunk &&
+         chunks <= INT32_MAX / 512;
 }
 
 bool lin_limits(int B, int H, int Dk, int Dv) { return B <= 65535 && H <= 4096 && Dk <= 256 && Dv <= 256; }
@@ -167,7 +170,7 @@ extern "C" {
 
 size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv) {
   if (!sdv::lin_shape(B, T, H, Dk, Dv) || !sdv::lin_limits(B, H, Dk, Dv)) return 0;
-  if (!sdv::lin_chunked(B, T, Dk, Dv)) return sdv::kHeaderBytes;
+  if (!sdv::lin_chunked(B, T, H, Dk, Dv)) return sdv::kHeaderBytes;
   const int sms = sdv::sm_count();
   return sdv::kHeaderBytes + sdv::lin_notes(B, H) + sdv::lin_parts(sms > 0 ? sms : 256, Dk, Dv);
 }
@@ -214,7 +217,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
   a.o = o_or_null;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (lin_window(T, Dk, Dv)) return status_of(launch_linear_window(dtype, a, st));
-  if (lin_chunked(B, T, Dk, Dv)) {
+  if (lin_chunked(B, T, H, Dk, Dv)) {
     a.ctas = sm_count();
     if (a.ctas <= 0) return SDV_ERR_CUDA;
     char* const w8 = static_cast<char*>(ws);

@@ -23,10 +23,10 @@
 // computes each part's own contribution (keys and values alone), and in the second
 // one each CTA sums those before it, decayed, on its way in.
 //
-// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 the values' check; 4-7 the state (one
-// thread per key row of M: U, decay, 16-bit copy for Q M); 8-11 the keys (K~'s two
-// parts; 8-15 in the first launch); 12-15 scores to P; 16-19 outputs.  All of it
-// runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
+// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 the values' check; then the
+// state's (key rows of M: U, decay, 16-bit copy for Q M; four, or eight with outputs,
+// where the copy is waited for), the keys' (K~'s two parts; eight, or four with outputs),
+// four for scores to P and four for outputs.  All of it runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
 // times as slow).
 //
 // A zero weight must not meet an infinite value (0 * inf): a head with keys or values
@@ -45,7 +45,6 @@
 
 #include "linear_args.h"
 #include "sdv_kernels.h"
-#include "split_math.cuh"
 #include "tc_util.cuh"
 
 namespace sdv {
@@ -54,26 +53,6 @@ namespace {
 
 constexpr int kLC = kLinChunk;
 constexpr uint64_t kLinDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
-
-__device__ __forceinline__ float abs_max32(const uint32_t (&x)[32]) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], fabsf(__uint_as_float(x[e])));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-// The largest finite magnitude among columns 0 .. last of 32, by a warp.
-__device__ __noinline__ float finite_max32(uint32_t taddr, int last) {
-  uint32_t x[32];
-  tmem_ld32(taddr, x);
-  tmem_wait_ld();
-  float m = 0.f;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const float y = fabsf(__uint_as_float(x[e]));
-    if (e <= last && y < INFINITY) m = fmaxf(m, y);
-  }
-  return m;
-}
 
 // x under a decay; one of 0 drops x whatever it holds.
 __device__ __forceinline__ float keep(float x, float dec) { return dec == 0.f ? 0.f : x * dec; }
@@ -123,24 +102,29 @@ struct LinTables {
   float pad[3];
 };
 
-template <int DK, int DV>
+template <int DK, int DV, bool OUT>
 struct LinPlan {
-  static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2, kSt = 128 * DV * 2;
-  static constexpr int oK = 0, oHi = oK + kK, oLo = oHi + kK, oQ = oLo + kK, oV = oQ + kK, oSt = oV + kV;
-  static constexpr int oOut = oSt + kSt;        // the output warps' 32 rows of 64 columns each
-  static constexpr int oTab = oOut + 4 * 4096;
+  // The first launch, without queries, state copy and outputs, has room for two buffers
+  // of keys, whose place K~'s high part then takes, of its low part and of values.
+  static constexpr int kBufs = OUT ? 1 : 2;
+  static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2;
+  static constexpr int oK = 0, oHi = OUT ? oK + kK : oK, oLo = oK + 2 * kK, oV = oLo + kBufs * kK, oQ = oV + kBufs * kV;
+  static constexpr int oSt = oQ + (OUT ? kK : 0), oOut = oSt + (OUT ? 128 * DV * 2 : 0);
+  static constexpr int oEx = oOut + (OUT ? 4 * 4096 : 0);  // Dk = 64: the state's low rows on their way to the high ones
+  static constexpr int oTab = oEx + (DK == 64 ? (OUT ? 2 : 1) * 64 * 33 * 4 : 0);
   static constexpr int oBars = oTab + 2 * (int)sizeof(LinTables);
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 36;
   static constexpr int oMisc = oBars + kNumBars * 8;
-  static constexpr int oUp = oMisc + 128;     // the rows' powers of two [2][128]
+  static constexpr int oUp = oMisc + 256;         // the rows' powers of two [2][128]
   static constexpr int kTotal = oUp + 2 * kLC * 4 + 1024;  // the base is aligned to 1024
   static constexpr int cS = 0, cO = 128, cU = 256, cM = 384;  // tensor-memory columns
   static_assert(kTotal <= 232448, "shared memory");
 };
 
-// A CTA's way through its range of chunks; all lanes of a warp keep the same.
+// A CTA's way through its range of chunks; all lanes of a warp keep the same.  The host
+// takes this form only where chunks times CTAs stay below 2^31.
 struct LinWalk {
-  long long total, at, end;
+  int total, at, end;
   int live, b, h, chunk, n, chunks;
 
   static __device__ __forceinline__ int chunks_of(int n) { return n <= kLC ? 1 : (n + kLC - 1) / kLC; }
@@ -151,24 +135,22 @@ struct LinWalk {
   __device__ __noinline__ bool start(const LinArgs& a, int cta, int lane) {
     // the first 32 sequences' chunks serve for the total and for the search
     const int c0 = lane < a.B ? chunks_of(lin_tokens(a, lane)) : 0;
-    long long sum = c0;
+    int sum = c0;
     for (int s = lane + 32; s < a.B; s += 32) sum += chunks_of(lin_tokens(a, s));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    total = sum * a.H;
+    total = __reduce_add_sync(0xffffffffu, sum) * a.H;
     const long long most = (long long)kLinRuns * a.B * a.H;
-    live = (int)min((long long)a.ctas, min(total, most));
+    live = min(a.ctas, total);
+    if (live > most) live = (int)most;
     if (cta >= live) return false;
-    at = muldiv(total, cta, live);
-    end = muldiv(total, cta + 1, live);
-    long long before = 0;
+    at = (int)((unsigned)(total * cta) / (unsigned)live);
+    end = (int)((unsigned)(total * (cta + 1)) / (unsigned)live);
+    int before = 0;
     for (int b0 = 0;; b0 += 32) {
-      const long long mine =
-          (long long)(b0 == 0 ? c0 : b0 + lane < a.B ? chunks_of(lin_tokens(a, b0 + lane)) : 0) * a.H;
-      long long incl = mine;
+      const int mine = (b0 == 0 ? c0 : b0 + lane < a.B ? chunks_of(lin_tokens(a, b0 + lane)) : 0) * a.H;
+      int incl = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += o;
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + incl > at);
@@ -181,9 +163,9 @@ struct LinWalk {
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     sequence(a);
-    const long long rest = at - before;
-    h = (int)muldiv(rest, 1, chunks);
-    chunk = (int)(rest - (long long)h * chunks);
+    const unsigned rest = (unsigned)(at - before);
+    h = (int)(rest / (unsigned)chunks);
+    chunk = (int)(rest - (unsigned)h * (unsigned)chunks);
     // the first launch takes the range's last part alone, and that only if the head goes on
     if (a.pass == 0) {
       while (more() && chunk + count() == chunks) advance(a, count());
@@ -191,10 +173,8 @@ struct LinWalk {
     return more();
   }
   __device__ __forceinline__ bool more() const { return at < end; }
-  __device__ __forceinline__ int count() const {  // chunks of the part that starts here
-    const long long left = end - at;
-    return left < chunks - chunk ? (int)left : chunks - chunk;
-  }
+  // chunks of the part that starts here
+  __device__ __forceinline__ int count() const { return min(end - at, chunks - chunk); }
   __device__ __forceinline__ void advance(const LinArgs& a, int c) {
     at += c;
     chunk += c;
@@ -205,16 +185,19 @@ struct LinWalk {
     if (++b < a.B) sequence(a);
   }
   // The first CTA with chunks of the head.
-  __device__ __forceinline__ int first_cta() const { return (int)div_fast((unsigned long long)(at - chunk + 1) * (unsigned)live - 1, total); }
+  __device__ __forceinline__ int first_cta() const {
+    return (int)((unsigned)((at - chunk + 1) * live - 1) / (unsigned)total);
+  }
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(OUT ? 640 : 512, 1)
+__global__ void __launch_bounds__(OUT ? 768 : 512, 1)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
-  using PL = LinPlan<DK, DV>;
+  using PL = LinPlan<DK, DV, OUT>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kScaled = !kBf16;  // powers of two beside fp16 operands
-  constexpr int kKeyWarps = OUT ? 4 : 8;
+  constexpr int kStateWarps = OUT ? 8 : 4, kKeyWarps = OUT ? 4 : 8;
+  constexpr int kKeys0 = 4 + kStateWarps, kScores0 = kKeys0 + 4, kOut0 = kScores0 + 4;  // the roles' first warps
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const sb = smem_raw + (base - raw);
@@ -222,17 +205,28 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
   LinTables* const tabs = reinterpret_cast<LinTables*>(sb + PL::oTab);
   const uint32_t bars = base + PL::oBars;
   auto bar = [&](int i) { return bars + 8u * i; };
-  const uint32_t q_full = bar(4), v_full = bar(5), s_full = bar(6), qm_done = bar(7), upd_done = bar(8),
-                 pv_done = bar(9), m_ready = bar(10), kv_ready = bar(11), p_ready = bar(12), o_free = bar(13),
-                 met = bar(14), met_m = bar(15), drain = bar(16), up_ready = bar(22);
-  const uint32_t k_full = bar(0), k_read = bar(17);
+  const uint32_t q_full = bar(4), s_full = bar(6), qm_done = bar(7),
+                 pv_done = bar(9), p_ready = bar(12), o_free = bar(13),
+                 met = bar(14), met_m = bar(15), drain = bar(16), q_read = bar(23), k_read = bar(28);
+  // keys and values per buffer, otherwise a barrier's phase is the chunk
+  auto buf = [&](int i) { return PL::kBufs == 2 ? i & 1 : 0; };
+  auto u_col = [&](int i) { return PL::kBufs == 2 && (i & 1) ? PL::cO : PL::cU; };
+  auto phase = [&](int i) { return (uint32_t)(PL::kBufs == 2 ? i >> 1 : i) & 1u; };
+  auto k_full = [&](int i) { return bar(24 + buf(i)); };
+  auto v_full = [&](int i) { return bar(26 + buf(i)); };
+  auto v_free = [&](int i) { return bar(30 + buf(i)); };
+  auto upd_done = [&](int i) { return i & 1 ? bar(8) : bar(32); };
+  auto m_ready = [&](int i) { return i & 1 ? bar(10) : bar(33); };
+  auto kv_ready = [&](int i) { return i & 1 ? bar(11) : bar(34); };
+  auto v_seen = [&](int i) { return i & 1 ? bar(5) : bar(17); };
   auto tab_full = [&](int i) { return bar(2 + (i & 1)); };
   auto tab_free = [&](int i) { return bar(18 + (i & 1)); };
+  auto up_ready = [&](int i) { return i & 1 ? bar(1) : bar(22); };
   auto ek_ready = [&](int i) { return bar(20 + (i & 1)); };
   volatile int* const misc = reinterpret_cast<int*>(sb + PL::oMisc);
   // misc: 0 tmem base; 2, 3 a part whose values are not all finite; 4, 5 exponent of K~;
-  // 6, 7 M's copy's power of two undone; 8-15 the warps' maxima of keys; 16-19 of the
-  // state; 20, 21 the chunk's largest value
+  // 6, 7 M's copy's power of two undone; 16-23 the warps' maxima of the state; 24, 25 the
+  // chunk's largest value; 32-47 the warps' maxima of keys
   volatile float* const fmisc = reinterpret_cast<volatile float*>(misc);
   volatile float* const ups = reinterpret_cast<volatile float*>(sb + PL::oUp);
 
@@ -241,18 +235,28 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
-    mbar_init(m_ready, 4);
+    for (int i = 0; i < 10; ++i)
+      if (i != 1) mbar_init(bar(i), 1);
+    mbar_init(upd_done(0), 1);
     mbar_init(o_free, 4);
-    mbar_init(met_m, 4);
+    mbar_init(met_m, kStateWarps);
+    mbar_init(q_read, 4);
     mbar_init(drain, 1);
     mbar_init(k_read, kKeyWarps);
-    mbar_init(kv_ready, kKeyWarps + 1);
+    mbar_init(v_seen(0), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(24 + i), 1);
+      mbar_init(bar(26 + i), 1);
+      mbar_init(bar(30 + i), 2 + kStateWarps);
+      mbar_init(m_ready(i), kStateWarps);
+      mbar_init(kv_ready(i), kKeyWarps + 1);
+    }
     mbar_init(met, kKeyWarps);
     mbar_init(p_ready, 8);
-    mbar_init(up_ready, 4);
+    mbar_init(up_ready(0), 4);
+    mbar_init(up_ready(1), 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(18 + i), 4 + kKeyWarps + (OUT ? 8 : 0));
+      mbar_init(bar(18 + i), kStateWarps + kKeyWarps + (OUT ? 8 : 0));
       mbar_init(bar(20 + i), 1);
     }
     fence_barrier_init();
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
   int upd_seen = 0, pv_seen = 0;
   auto upd_wait = [&](int chunks) {
     for (; upd_seen < chunks; ++upd_seen)
-      if (!await(upd_done, upd_seen & 1)) return false;
+      if (!await(upd_done(upd_seen), (upd_seen >> 1) & 1)) return false;
     return true;
   };
   auto pv_wait = [&](int chunks) {
@@ -302,34 +306,40 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
     int asked_k = 0, asked_q = 0, asked_v = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count(), hk = w.h / shared;
+      const int z0 = w.b * a.T + w.chunk * kLC;
       for (int c = 0; c < count; ++c, ++i) {
-        const int z = w.b * a.T + (w.chunk + c) * kLC;
-        // the keys before: read by Q K^T and by the keys' warps
-        if (i > 0 && (!await(k_read, (i - 1) & 1) || (OUT && !await(s_full, (i - 1) & 1)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(k_full, PL::kK);
+        const int z = z0 + c * kLC;
+        // the keys before in this buffer: read by their warps and by Q K^T, or, where K~
+        // took their place, by the product, which also ends the use of the values
+        if (OUT && i > 0 && (!await(k_read, (i - 1) & 1) || !await(s_full, (i - 1) & 1))) break;
+        if (!OUT && i >= 2 && !await(v_free(i), phase(i - 2))) break;
+        if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
         __syncwarp();
-        if (lane < DK / 64) tma_load_3d(base + PL::oK + lane * 16384, &maps.k, lane * 64, hk, z, k_full, normal);
+        if (lane < DK / 64)
+          tma_load_3d(base + PL::oK + buf(i) * PL::kK + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
         ++asked_k;
         if (OUT) {
-          if (i > 0 && !await(qm_done, (i - 1) & 1)) break;
+          if (i > 0 && (!await(qm_done, (i - 1) & 1) || (kScaled && !await(q_read, (i - 1) & 1)))) break;
           if (lane == 0) mbar_arrive_expect_tx(q_full, PL::kK);
           __syncwarp();
           if (lane < DK / 64) tma_load_3d(base + PL::oQ + lane * 16384, &maps.q, lane * 64, hk, z, q_full, normal);
           ++asked_q;
         }
-        if (!upd_wait(i) || (OUT && !pv_wait(i))) break;
-        if (lane == 0) mbar_arrive_expect_tx(v_full, PL::kV);
+        // the values before in this buffer: read by the products and by their check
+        if (OUT && i > 0 && !await(v_free(i), (i - 1) & 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(v_full(i), PL::kV);
         __syncwarp();
-        if (lane < DV / 64) tma_load_3d(base + PL::oV + lane * 16384, &maps.v, lane * 64, w.h, z, v_full, v_policy);
+        if (lane < DV / 64)
+          tma_load_3d(base + PL::oV + buf(i) * PL::kV + lane * 16384, &maps.v, lane * 64, w.h, z, v_full(i), v_policy);
         ++asked_v;
       }
       if (!ok) break;
       w.advance(a, count);
     }
     if (!ok) {  // copies whose consumers gave up have to land before the CTA ends
-      if (asked_k > 0) mbar_wait_bounded(k_full, (asked_k - 1) & 1, kLinDrainNs);
+      for (int e = max(asked_k - PL::kBufs, 0); e < asked_k; ++e) mbar_wait_bounded(k_full(e), phase(e), kLinDrainNs);
+      for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
       if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
-      if (asked_v > 0) mbar_wait_bounded(v_full, (asked_v - 1) & 1, kLinDrainNs);
     }
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
@@ -338,22 +348,23 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
     constexpr uint32_t id_up = idesc_16_f32(kBf16, 128, DV, true, true);
     const uint64_t qd = smem_desc_sw128(base + PL::oQ, 16, 1024);
     const uint64_t kd = smem_desc_sw128(base + PL::oK, 16, 1024);
-    const uint64_t vd = smem_desc_sw128(base + PL::oV, 16384, 1024);
     const uint64_t md = smem_desc_sw128(base + PL::oSt, 16384, 1024);
     // the chunks of all parts follow each other alike; a uniform count keeps the operands
     // in uniform registers
     const int total = __reduce_max_sync(0xffffffffu, any ? (int)(w.end - w.at) : 0);
     for (; ok && i < total; ++i) {
+      const uint64_t vd = smem_desc_sw128(base + PL::oV + buf(i) * PL::kV, 16384, 1024);
       if (OUT) {
         // scores; P of the chunk before has been read
-        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full, i & 1)) break;
+        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), phase(i))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < DK / 64; ++j)
           tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
         tc_commit_elect(s_full);
       }
-      if (!await(m_ready, i & 1)) break;
+      // M's copy; the first launch, with two buffers of U, wants U's before taken
+      if (OUT ? !await(m_ready(i), (i >> 1) & 1) : i > 0 && !await(m_ready(i - 1), ((i - 1) >> 1) & 1)) break;
       if (OUT) {
         // Q M over M's copy: 128 rows (at Dk = 64 the state's high and low part, both by Q)
         if (i > 0 && !await(o_free, (i - 1) & 1)) break;
@@ -363,29 +374,31 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           tc_mma4_ss<2, 128>(tm + PL::cO, qd + (DK == 128 ? j * 1024 : 0), md + j * 512, id_kb, j > 0);
         tc_commit_elect(qm_done);
       }
-      if (!await(kv_ready, i & 1)) break;
+      if (!await(kv_ready(i), (i >> 1) & 1)) break;
       tc_fence_after();
       // K~^T V: the low parts first; at Dk = 64 both at once (rows 0-63 from the high,
       // 64-127 from the low part)
       if constexpr (DK == 128) {
-        const uint64_t hd = smem_desc_sw128(base + PL::oHi, 16384, 1024);
-        const uint64_t ld = smem_desc_sw128(base + PL::oLo, 16384, 1024);
+        const uint64_t hd = smem_desc_sw128(base + PL::oHi + buf(i) * PL::kK, 16384, 1024);
+        const uint64_t ld = smem_desc_sw128(base + PL::oLo + buf(i) * PL::kK, 16384, 1024);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j)
-          tc_mma4_ss<128, 128>(tm + PL::cU, (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
+          tc_mma4_ss<128, 128>(tm + u_col(i), (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
       } else {
-        const uint64_t bd = smem_desc_sw128(base + PL::oHi, PL::oLo - PL::oHi, 1024);
+        const uint64_t bd = smem_desc_sw128(base + PL::oHi + buf(i) * PL::kK, PL::oLo - PL::oHi, 1024);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j)
-          tc_mma4_ss<128, 128>(tm + PL::cU, bd + j * 512, vd + j * 512, id_up, j > 0);
+          tc_mma4_ss<128, 128>(tm + u_col(i), bd + j * 512, vd + j * 512, id_up, j > 0);
       }
-      tc_commit_elect(upd_done);
+      tc_commit_elect(upd_done(i));
+      if (!OUT) tc_commit_elect(v_free(i));
       if (OUT) {
         if (!await(p_ready, i & 1)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) tc_mma4_ts(tm + PL::cO, tm + PL::cS + j * 32, vd + j * 512, id_kb, 1);
         tc_commit_elect(pv_done);
+        tc_commit_elect(v_free(i));
       }
     }
     tc_commit_elect(drain);  // every MMA has ended before tensor memory is freed
@@ -483,47 +496,47 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
-        if (!await(v_full, i & 1)) break;
-        uint32_t mx = 0;
-        bool wrote = false;
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          const int r = 32 * e + lane;
-#pragma unroll 1
-          for (int h = 0; h < DV / 64; ++h) {
-            const uint32_t row = base + PL::oV + h * 16384;
-            if (r < nv) {
-              uint4 x[8];
+        if (!await(v_full(i), phase(i))) break;
+        const uint32_t vb = base + PL::oV + buf(i) * PL::kV;
+        if (nv < kLC) {
+          for (int e = max(nv, 0) * 8 + lane; e < kLC * 8; e += 32)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] = lds128(row + swz128(r, k));
-#pragma unroll
-              for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) sts128(row + swz128(r, k), make_uint4(0, 0, 0, 0));
-              wrote = true;
-            }
-          }
+            for (int h = 0; h < DV / 64; ++h) sts128(vb + h * 16384 + swz128(e >> 3, e & 7), make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();
         }
-        if (wrote) fence_proxy_async_smem();
+        arrive(kv_ready(i));  // the check reads beside the products
+        uint32_t mx = 0;
+#pragma unroll 1
+        for (int e = 0; e < DV / 16; ++e) {  // rows 32 (e % 4) + lane, 64 columns
+          const uint32_t row = vb + (e >> 2) * 16384;
+          const int r = 32 * (e & 3) + lane;
+          uint4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = lds128(row + swz128(r, k));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+        }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
         if (lane == 0) {
           if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
             misc[2 + (part & 1)] = part + 1;
             a.repair[(long long)w.b * a.H + w.h] = 1;
           }
-          if (kScaled) fmisc[20 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
+          if (kScaled) fmisc[24 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
         }
-        arrive(kv_ready);
+        arrive(v_seen(i));
+        if (lane == 0) mbar_arrive(v_free(i));
       }
       if (!ok) break;
       ++part;
       w.advance(a, count);
     }
-  } else if (warp < 8) {
-    // ---- the state: thread = key row of M (at Dk = 64: rows 64-127 hold the low part) ----
+  } else if (warp < kKeys0) {
+    // ---- the state: thread = key row of M, or half of one (at Dk = 64: rows 64-127 hold the low part) ----
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
+    const int half = (warp - 4) >> 2;  // at eight warps a thread has half of the columns
+    const int col0 = half * (DV / 2), col1 = kStateWarps == 8 ? col0 + DV / 2 : DV;
     const bool owner = r < DK;  // rows with a place in the state's array
     uint32_t meetings = 0;
     int part = 0;
@@ -534,7 +547,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       float bound = 0.f;  // of M's finite entries: what they start at, then what a chunk can add
       const int first = a.pass == 1 && w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
 #pragma unroll 1
-      for (int j = 0; j < DV; j += 32) {
+      for (int j = col0; j < col1; j += 32) {
         float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = 0.f;
@@ -542,13 +555,15 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
 #pragma unroll 1
           for (int c = first - 1; c < (int)blockIdx.x; ++c) {
             if (c < first && a.s_in == nullptr) continue;
-            const float* const src =
-                (c < first ? a.s_in + unit * DK * DV : a.part + (long long)c * DK * DV) + (long long)r * DV + j;
+            // a row of the given state; the parts' lie column by column, as this reads them
+            const float* const src = c < first ? a.s_in + (unit * DK + r) * DV + j
+                                               : a.part + (long long)c * DK * DV + (j * DK + r * 4);
+            const int step = c < first ? 4 : DK * 4;
             float dec = 0.f;
             if (c >= first) dec = exp2f(a.part_decay[c].hi + a.part_decay[c].lo);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(src + e);
+              const float4 y = *reinterpret_cast<const float4*>(src + e / 4 * step);
               x[e] = keep(x[e], dec) + y.x;
               x[e + 1] = keep(x[e + 1], dec) + y.y;
               x[e + 2] = keep(x[e + 2], dec) + y.z;
@@ -565,11 +580,20 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       tmem_wait_st();
       if (OUT && kScaled) {
         const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(bound));
-        if (lane == 0) misc[16 + quarter] = (int)mx;
+        if (lane == 0) misc[warp + 12] = (int)mx;
         arrive(met_m);
         if (!await(met_m, meetings++ & 1)) break;
-        bound = __uint_as_float(max(max(misc[16], misc[17]), max(misc[18], misc[19])));
+        int top = 0;
+#pragma unroll
+        for (int e = 0; e < kStateWarps; ++e) top = max(top, misc[16 + e]);
+        bound = __int_as_float(top);
       }
+      auto take_u = [&](int chunks) {  // the last chunk's U is there, and its values checked
+        if (!upd_wait(chunks) || !await(v_seen(chunks - 1), ((chunks - 1) >> 1) & 1)) return false;
+        if (lane == 0) mbar_arrive(v_free(chunks - 1));
+        tc_fence_after();
+        return true;
+      };
       float dec = 0.f, dn = 1.f;  // of the last chunk: M = dec M + dn U
       auto state_of = [&](int j, uint32_t (&x)[32], bool take) {  // 32 columns of M behind the last chunk
         tmem_ld32(tq + PL::cM + j, x);
@@ -578,7 +602,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           return;
         }
         uint32_t u[32];
-        tmem_ld32(tq + PL::cU + j, u);
+        tmem_ld32(tq + u_col(i - 1) + j, u);
         tmem_wait_ld();
         if (dec == 0.f) {  // drops M whatever it holds
 #pragma unroll
@@ -604,21 +628,20 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
         }
       };
       for (int c = 0; c < count; ++c, ++i) {
-        if (!upd_wait(i)) break;
-        tc_fence_after();
+        if (c > 0 && !take_u(i)) break;
         if (OUT || c > 0) {
           float cs = 1.f;  // what M's copy carries
           if (OUT && kScaled) {
             // |U| is at most 128 times the largest |k~| (below 2^15 in U's units) times the
             // largest value: the bound is loose by the square root of what it counts, far
             // within what fp16's 30 octaves leave
-            if (c > 0) bound = bound * dec + 4194304.f * dn * fmisc[20 + ((i - 1) & 1)];
+            if (c > 0) bound = bound * dec + 4194304.f * dn * fmisc[24 + ((i - 1) & 1)];
             const int ex = min(max((int)(__float_as_uint(bound) >> 23) - 127, -100), 120);
             cs = exp2f((float)(14 - ex));  // the bound to [2^14, 2^15)
-            if (quarter == 0 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14));
+            if (warp == 4 && lane == 0) fmisc[6 + (i & 1)] = exp2f((float)(ex - 14));
           }
 #pragma unroll 1
-          for (int j = 0; j < DV; j += 32) {
+          for (int j = col0; j < col1; j += 32) {
             uint32_t x[32];
             state_of(j, x, c > 0);
             if (c > 0) tmem_st32(tq + PL::cM + j, x);
@@ -636,10 +659,9 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           dn = exp2f((float)-misc[4 + (i & 1)]);
         }
         tc_fence_before();
-        arrive(m_ready);
+        arrive(m_ready(i));
       }
-      if (!ok || !upd_wait(i)) break;
-      tc_fence_after();
+      if (!ok || !take_u(i)) break;
       // into the array if the head ends here, else this CTA's contribution
       const bool ends = w.chunk + count == w.chunks;
       float* dst = nullptr;
@@ -647,12 +669,12 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       else if (ends && a.s_out != nullptr && misc[2 + (part & 1)] != part + 1 && a.repair[unit] == 0)
         dst = a.s_out + unit * DK * DV;
 #pragma unroll 1
-      for (int j = 0; j < DV; j += 32) {
+      for (int j = col0; j < col1; j += 32) {
         uint32_t x[32];
         state_of(j, x, true);
         if constexpr (DK == 64) {
-          // rows 64-127 add theirs to rows 0-63 through the (idle) place of M's copy
-          float* const ex = reinterpret_cast<float*>(sb + PL::oSt);
+          // rows 64-127 add theirs to rows 0-63
+          float* const ex = reinterpret_cast<float*>(sb + PL::oEx) + half * 64 * 33;
           if (!owner) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) ex[(r - 64) * 33 + e] = __uint_as_float(x[e]);
@@ -667,10 +689,11 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           if (!await(met_m, meetings++ & 1)) break;
         }
         if (owner && dst != nullptr) {
-          float4* const p = reinterpret_cast<float4*>(dst + (long long)r * DV + j);
+          float4* const p = reinterpret_cast<float4*>(a.pass == 0 ? dst + j * DK + r * 4 : dst + (long long)r * DV + j);
+          const int step = a.pass == 0 ? DK : 1;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            p[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
+            p[e * step] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
                                __uint_as_float(x[4 * e + 3]));
         }
       }
@@ -679,11 +702,11 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       ++part;
       w.advance(a, count);
     }
-  } else if (warp < 8 + kKeyWarps) {
-    // ---- keys: thread = token (at eight warps: half of its elements) ----
+  } else if (warp < kKeys0 + kKeyWarps) {
+    // ---- keys: thread = token, at eight warps half of its elements ----
     const int quarter = warp & 3, r = quarter * 32 + lane;
     constexpr int kUnits = DK / 8 / (kKeyWarps / 4);  // a thread's 16-byte units
-    const int u0 = (warp - 8) / 4 * kUnits;
+    const int u0 = (warp - kKeys0) / 4 * kUnits;
     uint32_t meetings = 0;
     int part = 0;
     for (bool more = any; ok && more; more = w.more()) {
@@ -691,8 +714,8 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       const long long unit = (long long)w.b * a.H + w.h;
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
-        const uint32_t kb = base + PL::oK;
-        if (!await(k_full, i & 1)) break;
+        const uint32_t kb = base + PL::oK + buf(i) * PL::kK;
+        if (!await(k_full(i), phase(i))) break;
         // the largest key of the chunk sets its power of two; one that is not finite is noted
         uint32_t mx = 0;
         if (r < nv) {
@@ -714,11 +737,12 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
         int pre = 0;
         if (kScaled) {
           mx = __reduce_max_sync(0xffffffffu, mx);
-          if (lane == 0) misc[warp] = (int)mx;
+          if (lane == 0) misc[32 + 8 * (i & 1) + warp - kKeys0] = (int)mx;
           arrive(met);
           if (!await(met, meetings++ & 1)) break;
-          int bits = max(max(misc[8], misc[9]), max(misc[10], misc[11]));
-          if (kKeyWarps == 8) bits = max(bits, max(max(misc[12], misc[13]), max(misc[14], misc[15])));
+          int bits = 0;
+#pragma unroll
+          for (int e = 0; e < kKeyWarps; ++e) bits = max(bits, misc[32 + 8 * (i & 1) + e]);
           const float top = __half2float(__ushort_as_half((unsigned short)min(bits, 0x7bff)));
           const int ex = top == 0.f ? 0 : (int)(__float_as_uint(top) >> 23) - 127;
           // the largest to [2^14, 2^15): low parts then end at 2^-39 of it.  2^15 of it goes
@@ -727,7 +751,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           const int ek = min(14 - ex, 30);  // -1 .. 30
           pre = max(ek - 15, 0);
           up = exp2f((float)(ek - pre));
-          if (warp == 8 && lane == 0) {
+          if (warp == kKeys0 && lane == 0) {
             misc[4 + (i & 1)] = ek;
             mbar_arrive(ek_ready(i));
           }
@@ -740,7 +764,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
         const float pw = exp2f((float)pre);
         const uint32_t up2 = pack16<T>(pw, pw);
         arrive(tab_free(i));
-        if (!upd_wait(i)) break;  // the last product has read K~
+        if (OUT && !upd_wait(i)) break;  // the last product has read K~
 #pragma unroll 1
         for (int h = u0; h < u0 + kUnits; h += 4) {  // four 16-byte units in flight
           const uint32_t blk = (h >> 3) * 16384;
@@ -763,19 +787,19 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            sts128(base + PL::oHi + blk + swz128(r, (h & 7) + k), x[k]);
-            sts128(base + PL::oLo + blk + swz128(r, (h & 7) + k), lo[k]);
+            sts128(base + PL::oHi + buf(i) * PL::kK + blk + swz128(r, (h & 7) + k), x[k]);
+            sts128(base + PL::oLo + buf(i) * PL::kK + blk + swz128(r, (h & 7) + k), lo[k]);
           }
         }
         fence_proxy_async_smem();
-        arrive(k_read);
-        arrive(kv_ready);
+        if (OUT) arrive(k_read);
+        arrive(kv_ready(i));
       }
       if (!ok) break;
       ++part;
       w.advance(a, count);
     }
-  } else if (OUT && warp < 16) {
+  } else if (OUT && warp < kOut0) {
     // ---- scores: thread = token ----
     const int quarter = warp & 3, t = quarter * 32 + lane;
     const uint32_t tq = tm + ((uint32_t)(quarter * 32) << 16);
@@ -784,39 +808,34 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       for (int c = 0; c < count; ++c, ++i) {
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         const LinTables& tb = tabs[i & 1];
+        // fp16: a bound of the row's scores sets its power of two: Dk times the row's largest
+        // query times the chunk's largest key
+        float up = 1.f;
+        if (kScaled) {
+          if (!await(q_full, i & 1)) break;
+          uint32_t mx = 0;
+#pragma unroll 1
+          for (int h = 0; h < DK / 8; h += 4) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = lds128(base + PL::oQ + (h >> 3) * 16384 + swz128(t, (h & 7) + k));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+          }
+          arrive(q_read);
+          mx = min(max(mx & 0xffffu, mx >> 16), 0x7bffu);
+          const float top = __half2float(__ushort_as_half((unsigned short)mx));
+          if (!await(ek_ready(i), (i >> 1) & 1)) break;
+          // |q| below 2^(eq + 1), |k| below 2^(15 - ek), 2^7 products at most
+          const int eq = (int)(__float_as_uint(top) >> 23) - 127;
+          const int eu = min(14 - (eq + 1 + 15 - misc[4 + (i & 1)] + 7), 40);
+          up = exp2f((float)eu);
+          ups[(i & 1) * kLC + t] = up;
+          arrive(up_ready(i));
+        }
         if (!await(s_full, i & 1)) break;
         tc_fence_after();
         const uint32_t ts = tq + PL::cS;
-        // fp16: the row's largest score sets the row's power of two
-        float up = 1.f;
-        if (kScaled) {
-          float big = 0.f;
-#pragma unroll 1
-          for (int j = 0; j <= quarter; ++j) {
-            uint32_t x[32];
-            tmem_ld32(ts + 32 * j, x);
-            tmem_wait_ld();
-            if (j == quarter) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e > lane) x[e] = 0u;
-            }
-            big = fmaxf(big, abs_max32(x));
-          }
-          if (__any_sync(0xffffffffu, big == INFINITY)) {  // by its finite scores
-            big = 0.f;
-#pragma unroll 1
-            for (int j = 0; j <= quarter; ++j) big = fmaxf(big, finite_max32(ts + 32 * j, j == quarter ? lane : 31));
-          }
-          const uint32_t mx = __float_as_uint(big);
-          const int ex = min(max((int)(mx >> 23) - 127, -100), 120);
-          const int eu = min(14 - ex, 40);  // (a bound for the state's part in the same units)
-          up = exp2f((float)eu);
-        }
-        if (kScaled) {
-          ups[(i & 1) * kLC + t] = up;
-          arrive(up_ready);
-        }
         const float rf = tb.rf[t] * up, hi = tb.hi[t], lo = tb.lo[t];
         const bool mild = tb.mild[quarter] != 0;
 #pragma unroll 1
@@ -878,7 +897,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
       const int b = (int)(u / a.H), h = (int)(u % a.H);
       const int first = LinWalk::chunks_of(lin_tokens(a, b)) * kLC;
       constexpr int per = DV / 8;  // 16-byte units of a row
-      for (long long e = (long long)first * per + (warp - 16) * 32 + lane; e < (long long)a.T * per; e += 128)
+      for (long long e = (long long)first * per + (warp - kOut0) * 32 + lane; e < (long long)a.T * per; e += 128)
         reinterpret_cast<uint4*>(a.o)[(((long long)b * a.T + e / per) * a.H + h) * per + e % per] =
             make_uint4(0, 0, 0, 0);
     }
@@ -895,7 +914,7 @@ __global__ void __launch_bounds__(OUT ? 640 : 512, 1)
         arrive(tab_free(i));
         float up = 1.f;
         if (kScaled) {
-          if (!await(up_ready, i & 1)) break;
+          if (!await(up_ready(i), (i >> 1) & 1)) break;
           up = ups[(i & 1) * kLC + t];
         }
         if (!await(qm_done, i & 1)) break;
@@ -977,7 +996,7 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
   auto kernel = linear_tc_kernel<T, DK, DV, OUT>;
   // more than half an SM's: one CTA and one tensor-memory allocation per SM
   constexpr int half = 232448 / 2 + 1024;
-  constexpr int smem = LinPlan<DK, DV>::kTotal > half ? LinPlan<DK, DV>::kTotal : half;
+  constexpr int smem = LinPlan<DK, DV, OUT>::kTotal > half ? LinPlan<DK, DV, OUT>::kTotal : half;
   static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -987,7 +1006,7 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 640 : 512), smem, st, m, a);
+  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 768 : 512), smem, st, m, a);
 }
 
 }  // namespace
