@@ -42,11 +42,25 @@ struct AttnArgs {
   float* lse;               // or null
   float* part_o;            // [2 * CTAs][D / 4][row_tile][4]
   float* part_ml;           // [2 * CTAs][row_tile][2]: max (log2 domain), sum
-  unsigned* shared;         // [CTAs] arrivals at the unit whose first sharer a CTA is, or null: a join follows
+  unsigned* shared;         // arrivals at the unit whose first sharer a CTA is, a byte a CTA, or null: a join follows
   int* status;
   int ctas;                 // CTAs of the attention launch
   int slots, q_bufs;        // tensor-core kernel: ring slots, Q buffers
 };
+
+// Bytes of arrivals in the workspace's header, which alone is zero between calls of
+// different operations.
+constexpr int kAttnSharedAt = 64, kAttnSharedBytes = 192;
+
+// One more of the CTAs first .. last; how many came before.  The last one's sets the count
+// back to 0.
+__device__ __forceinline__ unsigned attn_arrive(unsigned* shared, int first, int last) {
+  const int at = 8 * (first & 3);
+  unsigned* const word = shared + (first >> 2);
+  const unsigned before = (atomicAdd(word, 1u << at) >> at) & 255u;
+  if (before == (unsigned)(last - first)) atomicSub(word, (before + 1) << at);
+  return before;
+}
 
 struct AttnSeq {
   int ctx, n;   // context positions, live window rows

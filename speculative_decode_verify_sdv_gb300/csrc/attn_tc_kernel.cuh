@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!meet()) break;
           const int first = g_first, last = g_last;
           if (quarter == 0 && lane == 0) {
-            const unsigned before = atomicInc(a.shared + first, (unsigned)(last - first));
+            const unsigned before = attn_arrive(a.shared, first, last);
             misc[3] = (misc[3] & ~1u) + 2u + (before == (unsigned)(last - first) ? 1u : 0u);
           }
           if (!meet()) break;
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int count = w.segment();
       int first, last;
       w.sharers(first, last);
-      if (first != last && --made < 0 && lane == 0) atomicInc(a.shared + first, (unsigned)(last - first));
+      if (first != last && --made < 0 && lane == 0) attn_arrive(a.shared, first, last);
       w.advance(a, count);
     }
   }

@@ -9,7 +9,7 @@
 
 namespace sdv {
 
-constexpr size_t kHeaderBytes = 256;  // a workspace's head: word 0 is the status
+constexpr size_t kHeaderBytes = 256;  // a workspace's head: word 0 is the status; zero between calls
 
 inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,6 +1,8 @@
 // Arguments of the linear-attention kernels.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -30,6 +32,12 @@ struct DecaySum {
 #endif
 };
 
+struct LinPart {
+  DecaySum decay;  // its log2 decay
+  int bad;         // a key or value is not finite
+  int pad;
+};
+
 struct LinArgs {
   const void *q, *k, *v;
   long long q_stride, k_stride, v_stride;
@@ -41,10 +49,11 @@ struct LinArgs {
   const float* s_in;
   float* s_out;
   void* o;
-  // chunked form: a CTA's local state and its log2 decay, heads whose values are not
-  // finite (recomputed by the recurrent kernel), status
-  float* part;             // [CTAs][Dv / 4][Dk][4]
-  DecaySum* part_decay;    // [CTAs]
+  // chunked form: what the first launch leaves of each CTA, heads with keys or values that
+  // are not finite (recomputed by the recurrent kernel), status
+  float* part;             // [CTAs][Dv / 4][Dk][4] local states
+  float* part_in;          // [CTAs][Dk][Dv] the given state of a head that starts in the CTA and goes on
+  LinPart* parts;          // [CTAs]
   int* repair;             // [B][H]
   int* status;
   int ctas;
@@ -72,10 +81,16 @@ __device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
   return a.n_tokens != nullptr ? min(max(__ldg(a.n_tokens + b), 0), a.T) : a.T;
 }
 
-// The log decay of token t, head h: at most 0 (NaN stays NaN).
+__device__ __forceinline__ float lin_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float lin_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The log decay of token t, head h, as it was given.
+__device__ __forceinline__ float lin_raw_decay(const LinArgs& a, int b, int t, int h) {
+  return __ldg(a.g + (a.g_token ? ((long long)b * a.T + t) * a.H + h : h));
+}
+__device__ __forceinline__ float lin_clamp_decay(float g) { return g > 0.f ? 0.f : g; }  // NaN stays NaN
 __device__ __forceinline__ float lin_decay(const LinArgs& a, int b, int t, int h) {
-  const float g = __ldg(a.g + (a.g_token ? ((long long)b * a.T + t) * a.H + h : h));
-  return g > 0.f ? 0.f : g;
+  return lin_clamp_decay(lin_raw_decay(a, b, t, h));
 }
 #endif
 

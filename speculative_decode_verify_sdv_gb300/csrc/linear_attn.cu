@@ -17,8 +17,6 @@ namespace sdv {
 
 namespace {
 
-__device__ __forceinline__ float lin_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float lin_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void lin_round(float x, __half& y) { y = __float2half_rn(x); }
 __device__ __forceinline__ void lin_round(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
 
@@ -31,7 +29,7 @@ __device__ __forceinline__ void lin_round(float x, __nv_bfloat16& y) { y = __flo
 constexpr int kRecWarps = 8;
 constexpr int kRecTokens = 8;  // tokens staged at once
 
-// With `repair` it recomputes the heads noted there and clears the notes.
+// With `repair` it recomputes the heads noted there.
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kRecWarps) linear_recurrent_kernel(const LinArgs a) {
   __shared__ float qs[kRecTokens][kRecWarps * R], ks[kRecTokens][kRecWarps * R];
@@ -40,11 +38,7 @@ __global__ void __launch_bounds__(32 * kRecWarps) linear_recurrent_kernel(const 
   __shared__ float4 red[kRecWarps][32];
   griddep_wait();
   if (a.repair != nullptr) {  // (one block a head: Dv is at most 128 here)
-    int* const note = a.repair + (long long)blockIdx.z * a.H + blockIdx.y;
-    const bool noted = *note != 0;
-    __syncthreads();
-    if (!noted) return;
-    if (threadIdx.x == 0) *note = 0;
+    if (a.repair[(long long)blockIdx.z * a.H + blockIdx.y] == 0) return;
   }
   const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.H / a.Hqk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -143,7 +137,7 @@ bool lin_shape(int B, int T, int H, int Dk, int Dv) {
 
 // The chunked form's workspace: notes of heads to repair, the CTAs' local states.
 size_t lin_notes(int B, int H) { return round_256((size_t)B * H * 4); }
-size_t lin_parts(int ctas, int Dk, int Dv) { return round_256((size_t)ctas * 8) + (size_t)ctas * Dk * Dv * 4; }
+size_t lin_parts(int ctas, int Dk, int Dv) { return (size_t)ctas * (sizeof(LinPart) + 2 * (size_t)Dk * Dv * 4); }
 
 // The window form for kLinWindowFrom to 32 tokens, the chunked form for more, both for
 // the head sizes that they have; one token, and other head sizes, are the recurrent form's.
@@ -223,8 +217,9 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
     char* const w8 = static_cast<char*>(ws);
     a.status = reinterpret_cast<int*>(w8);
     a.repair = reinterpret_cast<int*>(w8 + kHeaderBytes);
-    a.part_decay = reinterpret_cast<DecaySum*>(w8 + kHeaderBytes + lin_notes(B, H));
-    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_decay) + round_256((size_t)a.ctas * 8));
+    a.part = reinterpret_cast<float*>(w8 + kHeaderBytes + lin_notes(B, H));
+    a.part_in = a.part + (size_t)a.ctas * Dk * Dv;
+    a.parts = reinterpret_cast<LinPart*>(a.part_in + (size_t)a.ctas * Dk * Dv);
     const cudaError_t e = launch_linear_tc(dtype, a, st);
     if (e != cudaSuccess) return status_of(e);
   }

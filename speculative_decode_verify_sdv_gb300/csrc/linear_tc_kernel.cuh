@@ -23,7 +23,7 @@
 // computes each part's own contribution (keys and values alone), and in the second
 // one each CTA sums those before it, decayed, on its way in.
 //
-// Warp roles: 0 TMA; 1 MMA; 2 decay tables; 3 the values' check; then the
+// Warp roles: 0 TMA; 1 MMA; 2 the decays; 3 the values' check; then the
 // state's (key rows of M: U, decay, 16-bit copy for Q M; four, or eight with outputs,
 // where the copy is waited for), the keys' (K~'s two parts; eight, or four with outputs),
 // four for scores to P and four for outputs.  All of it runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
@@ -89,17 +89,10 @@ __device__ __forceinline__ uint32_t mul16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
-// Decay tables of a chunk.
+// The decays of a chunk, G_t in log2 units.
 struct LinTables {
-  float hi[kLC], lo[kLC];  // G_t (log2 units)
-  float eg[kLC];           // e^{G_t}
-  float w[kLC];            // e^{G_C - G_s}
-  float rf[kLC];           // e^{G_t - G_r}, r the last token before t's block of 32 (G_r = 0 in the first)
-  float cf[3][kLC];        // e^{G_r - G_s} for the blocks 1, 2, 3 (s <= r)
-  float cd[kLC];           // e^{G_r - G_s} inside s's own block, where `mild`
-  float dec;               // e^{G_C}
-  int mild[4];             // blocks that decay by less than 2^-60: e^{G_t - G_s} = rf_t cd_s there too
-  float pad[3];
+  float hi[kLC], lo[kLC];
+  __device__ __forceinline__ DecaySum at(int t) const { return DecaySum{hi[t], lo[t]}; }
 };
 
 template <int DK, int DV, bool OUT>
@@ -107,12 +100,14 @@ struct LinPlan {
   // The first launch, without queries, state copy and outputs, has room for two buffers
   // of keys, whose place K~'s high part then takes, of its low part and of values.
   static constexpr int kBufs = OUT ? 1 : 2;
+  static constexpr int kThreads = OUT ? 768 : 512;
   static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2;
   static constexpr int oK = 0, oHi = OUT ? oK + kK : oK, oLo = oK + 2 * kK, oV = oLo + kBufs * kK, oQ = oV + kBufs * kV;
   static constexpr int oSt = oQ + (OUT ? kK : 0), oOut = oSt + (OUT ? 128 * DV * 2 : 0);
   static constexpr int oEx = oOut + (OUT ? 4 * 4096 : 0);  // Dk = 64: the state's low rows on their way to the high ones
   static constexpr int oTab = oEx + (DK == 64 ? (OUT ? 2 : 1) * 64 * 33 * 4 : 0);
-  static constexpr int oBars = oTab + 2 * (int)sizeof(LinTables);
+  static constexpr int oFac = oTab + 2 * (int)sizeof(LinTables);  // the scores' warps' factors [4][128]
+  static constexpr int oBars = oFac + (OUT ? 4 * kLC * 4 : 0);
   static constexpr int kNumBars = 36;
   static constexpr int oMisc = oBars + kNumBars * 8;
   static constexpr int oUp = oMisc + 256;         // the rows' powers of two [2][128]
@@ -191,7 +186,7 @@ struct LinWalk {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(OUT ? 768 : 512, 1)
+__global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using PL = LinPlan<DK, DV, OUT>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -404,24 +399,30 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
     tc_commit_elect(drain);  // every MMA has ended before tensor memory is freed
     mbar_wait_bounded(drain, 0, kLinDrainNs);
   } else if (warp == 2) {
-    // ---- decay tables: four tokens a lane, sums in pairs of floats ----
+    // ---- decays: four tokens a lane, sums in pairs of floats ----
     DecaySum run;  // log2 decay of the part so far
-    float next[4];
-    auto load = [&](int t0) {  // natural log decays of the chunk at t0, ahead of their use
+    // natural log decays, asked for two chunks ahead of their use: a chunk takes less than
+    // memory under this load does
+    float next[2][4];
+    auto load = [&](int c, float (&x)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = t0 + 4 * lane + e;
-        next[e] = t < w.n ? lin_decay(a, w.b, t, w.h) : 0.f;
+        const int t = (w.chunk + c) * kLC + 4 * lane + e;
+        x[e] = t < w.n ? lin_raw_decay(a, w.b, t, w.h) : 0.f;
       }
     };
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
-      load(w.chunk * kLC);
+      load(0, next[0]);
+      load(1, next[1]);
       for (int c = 0; c < count; ++c, ++i) {
         DecaySum g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = DecaySum::log2_of(next[e]);
-        if (c + 1 < count) load((w.chunk + c + 1) * kLC);
+        for (int e = 0; e < 4; ++e) {
+          g[e] = DecaySum::log2_of(lin_clamp_decay(next[0][e]));
+          next[0][e] = next[1][e];
+        }
+        if (c + 2 < count) load(c + 2, next[1]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) g[e].add(g[e - 1]);
         DecaySum incl = g[3];
@@ -434,59 +435,15 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
         if (lane == 0) before = DecaySum();
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e].add(before);
-        const DecaySum all{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-        DecaySum ref[3];
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          ref[e] = DecaySum{__shfl_sync(0xffffffffu, incl.hi, 8 * e + 7), __shfl_sync(0xffffffffu, incl.lo, 8 * e + 7)};
         if (i >= 2 && !await(tab_free(i), ((i - 2) >> 1) & 1)) break;
         LinTables& tb = tabs[i & 1];
-        const int blk = lane >> 3;
-        float hi[4], lo[4], eg[4], wt[4], rf[4], cf[3][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[e] = g[e].hi;
-          lo[e] = g[e].lo;
-          eg[e] = exp2_approx(g[e].hi + g[e].lo);
-          wt[e] = exp2_approx(all.minus(g[e]));
-          if (OUT) {
-#pragma unroll
-            for (int q = 0; q < 3; ++q) cf[q][e] = blk <= q ? exp2_approx(ref[q].minus(g[e])) : 0.f;
-          }
-        }
-        auto put = [&](float* at, const float (&x)[4]) {
-          *reinterpret_cast<float4*>(at + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
-        };
-        put(tb.hi, hi);
-        put(tb.lo, lo);
-        put(tb.eg, eg);
-        put(tb.w, wt);
-        if (OUT) {
-#pragma unroll
-          for (int q = 0; q < 3; ++q) put(tb.cf[q], cf[q]);
-        }
-        if (OUT) {
-          // within the block: its last token's sum against r's
-          const DecaySum r = blk == 0 ? DecaySum() : blk == 1 ? ref[0] : blk == 2 ? ref[1] : ref[2];
-          const DecaySum end{__shfl_sync(0xffffffffu, incl.hi, lane | 7), __shfl_sync(0xffffffffu, incl.lo, lane | 7)};
-          const bool mild = end.minus(r) > -60.f;
-          float cd[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            cd[e] = mild ? exp2_approx(r.minus(g[e])) : 0.f;
-            rf[e] = exp2_approx(g[e].minus(r));
-          }
-          put(tb.cd, cd);
-          put(tb.rf, rf);
-          if ((lane & 7) == 0) tb.mild[blk] = mild;
-        }
-        if (lane == 0) tb.dec = exp2_approx(all.hi + all.lo);
-        run.add(all);
+        reinterpret_cast<float4*>(tb.hi)[lane] = make_float4(g[0].hi, g[1].hi, g[2].hi, g[3].hi);
+        reinterpret_cast<float4*>(tb.lo)[lane] = make_float4(g[0].lo, g[1].lo, g[2].lo, g[3].lo);
+        if (a.pass == 0) run.add(DecaySum{__shfl_sync(0xffffffffu, g[3].hi, 31), __shfl_sync(0xffffffffu, g[3].lo, 31)});
         arrive(tab_full(i));
       }
       if (!ok) break;
-      if (a.pass == 0 && lane == 0) a.part_decay[blockIdx.x] = run;
-      run = DecaySum();
+      if (a.pass == 0 && lane == 0) a.parts[blockIdx.x].decay = run;
       w.advance(a, count);
     }
   } else if (warp == 3) {
@@ -518,10 +475,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
         }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
         if (lane == 0) {
-          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
-            misc[2 + (part & 1)] = part + 1;
-            a.repair[(long long)w.b * a.H + w.h] = 1;
-          }
+          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) misc[2 + (part & 1)] = part + 1;
           if (kScaled) fmisc[24 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
         }
         arrive(v_seen(i));
@@ -546,6 +500,15 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
       // the state before the part: what was given, then the parts before this one, in order
       float bound = 0.f;  // of M's finite entries: what they start at, then what a chunk can add
       const int first = a.pass == 1 && w.chunk > 0 ? w.first_cta() : (int)blockIdx.x;
+      // Another CTA writes a shared head's final state, perhaps over the given one: the
+      // second launch takes the first one's copy of that.
+      const bool ends = w.chunk + count == w.chunks, whole = w.chunk == 0 && ends;
+      if (a.pass == 0 && w.chunk == 0 && a.s_in != nullptr) {
+        const float4* const from4 = reinterpret_cast<const float4*>(a.s_in + unit * DK * DV);
+        float4* const to4 = reinterpret_cast<float4*>(a.part_in + (long long)blockIdx.x * DK * DV);
+#pragma unroll 4
+        for (int e = threadIdx.x - 128; e < DK * DV / 4; e += 32 * kStateWarps) to4[e] = from4[e];
+      }
 #pragma unroll 1
       for (int j = col0; j < col1; j += 32) {
         float x[32];
@@ -556,11 +519,12 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
           for (int c = first - 1; c < (int)blockIdx.x; ++c) {
             if (c < first && a.s_in == nullptr) continue;
             // a row of the given state; the parts' lie column by column, as this reads them
-            const float* const src = c < first ? a.s_in + (unit * DK + r) * DV + j
-                                               : a.part + (long long)c * DK * DV + (j * DK + r * 4);
+            const float* const src = c >= first ? a.part + (long long)c * DK * DV + (j * DK + r * 4)
+                                     : whole    ? a.s_in + (unit * DK + r) * DV + j
+                                                : a.part_in + ((long long)first * DK + r) * DV + j;
             const int step = c < first ? 4 : DK * 4;
             float dec = 0.f;
-            if (c >= first) dec = exp2f(a.part_decay[c].hi + a.part_decay[c].lo);
+            if (c >= first) dec = exp2f(a.parts[c].decay.hi + a.parts[c].decay.lo);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 y = *reinterpret_cast<const float4*>(src + e / 4 * step);
@@ -652,7 +616,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
         }
         // this chunk's factors, before the product may go on (the next but one's come after it)
         if (!await(tab_full(i), (i >> 1) & 1)) break;
-        dec = tabs[i & 1].dec;
+        dec = exp2_approx(tabs[i & 1].hi[kLC - 1] + tabs[i & 1].lo[kLC - 1]);
         arrive(tab_free(i));
         if (kScaled) {
           if (!await(ek_ready(i), (i >> 1) & 1)) break;
@@ -663,11 +627,16 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
       }
       if (!ok || !take_u(i)) break;
       // into the array if the head ends here, else this CTA's contribution
-      const bool ends = w.chunk + count == w.chunks;
       float* dst = nullptr;
-      if (a.pass == 0) dst = a.part + (long long)blockIdx.x * DK * DV;
-      else if (ends && a.s_out != nullptr && misc[2 + (part & 1)] != part + 1 && a.repair[unit] == 0)
-        dst = a.s_out + unit * DK * DV;
+      int bad = misc[2 + (part & 1)] == part + 1;
+      if (a.pass == 0) {
+        dst = a.part + (long long)blockIdx.x * DK * DV;
+        if (threadIdx.x == 128) a.parts[blockIdx.x].bad = bad;
+      } else if (ends) {
+        for (int c = first; c < (int)blockIdx.x; ++c) bad |= a.parts[c].bad;
+        if (threadIdx.x == 128) a.repair[unit] = bad;
+        if (!bad) dst = a.s_out != nullptr ? a.s_out + unit * DK * DV : nullptr;
+      }
 #pragma unroll 1
       for (int j = col0; j < col1; j += 32) {
         uint32_t x[32];
@@ -711,7 +680,6 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
     int part = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
-      const long long unit = (long long)w.b * a.H + w.h;
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
         const uint32_t kb = base + PL::oK + buf(i) * PL::kK;
@@ -728,10 +696,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
             for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
           }
           mx = max(mx & 0xffffu, mx >> 16);
-          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) {
-            misc[2 + (part & 1)] = part + 1;
-            a.repair[unit] = 1;
-          }
+          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) misc[2 + (part & 1)] = part + 1;
         }
         float up = 1.f;
         int pre = 0;
@@ -757,7 +722,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
           }
         }
         if (!await(tab_full(i), (i >> 1) & 1)) break;
-        const float f = r < nv ? tabs[i & 1].w[r] * up : 0.f;
+        const float f = r < nv ? exp2_approx(tabs[i & 1].at(kLC - 1).minus(tabs[i & 1].at(r))) * up : 0.f;  // e^{G_C - G_s}
         const uint32_t fh = pack16<T>(f, f);
         const float fr = f - unpack16<T>(fh).x;
         const uint32_t fl = pack16<T>(fr, fr);
@@ -808,6 +773,16 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
       for (int c = 0; c < count; ++c, ++i) {
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         const LinTables& tb = tabs[i & 1];
+        // e^{G_t - G_s} = e^{G_t - G_r} e^{G_r - G_s}, r the last token before the warp's
+        // block of 32 (G_r = 0 in the first): exact enough for s <= r, and inside the block
+        // where that decays by less than 2^-60
+        const DecaySum gt = tb.at(t), gr = quarter > 0 ? tb.at(quarter * 32 - 1) : DecaySum();
+        const bool mild = tb.at(quarter * 32 + 31).minus(gr) > -60.f;
+        float* const fac = reinterpret_cast<float*>(sb + PL::oFac) + quarter * kLC;
+        __syncwarp();  // the last chunk's have been read
+        for (int j = 0; j <= quarter; ++j)
+          if (j < quarter || mild) fac[32 * j + lane] = exp2_approx(gr.minus(tb.at(32 * j + lane)));
+        __syncwarp();
         // fp16: a bound of the row's scores sets its power of two: Dk times the row's largest
         // query times the chunk's largest key
         float up = 1.f;
@@ -836,8 +811,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
         if (!await(s_full, i & 1)) break;
         tc_fence_after();
         const uint32_t ts = tq + PL::cS;
-        const float rf = tb.rf[t] * up, hi = tb.hi[t], lo = tb.lo[t];
-        const bool mild = tb.mild[quarter] != 0;
+        const float rf = exp2_approx(gt.minus(gr)) * up;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
           uint32_t y[16];
@@ -846,7 +820,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
             tmem_ld32(ts + 32 * j, x);
             tmem_wait_ld();
             if (j < quarter || mild) {
-              const float4* const cf = reinterpret_cast<const float4*>((j < quarter ? tb.cf[quarter - 1] : tb.cd) + 32 * j);
+              const float4* const cf = reinterpret_cast<const float4*>(fac + 32 * j);
               const f32x2 r2 = pair2(rf, rf);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -866,8 +840,8 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float4 hs = h4[e], ls = l4[e];
-                const float d0 = (hi - hs.x) + (lo - ls.x), d1 = (hi - hs.y) + (lo - ls.y);
-                const float d2 = (hi - hs.z) + (lo - ls.z), d3 = (hi - hs.w) + (lo - ls.w);
+                const float d0 = (gt.hi - hs.x) + (gt.lo - ls.x), d1 = (gt.hi - hs.y) + (gt.lo - ls.y);
+                const float d2 = (gt.hi - hs.z) + (gt.lo - ls.z), d3 = (gt.hi - hs.w) + (gt.lo - ls.w);
                 const float p0 = 4 * e <= lane ? __uint_as_float(x[4 * e]) * (up * exp2_approx(d0)) : 0.f;
                 const float p1 = 4 * e + 1 <= lane ? __uint_as_float(x[4 * e + 1]) * (up * exp2_approx(d1)) : 0.f;
                 const float p2 = 4 * e + 2 <= lane ? __uint_as_float(x[4 * e + 2]) * (up * exp2_approx(d2)) : 0.f;
@@ -910,7 +884,7 @@ __global__ void __launch_bounds__(OUT ? 768 : 512, 1)
         // the state's part of the output, in the units of P V: by e^{G_t}, M's copy's power
         // of two and the row's
         if (!await(tab_full(i), (i >> 1) & 1)) break;
-        const float eg = tabs[i & 1].eg[t];
+        const float eg = exp2_approx(tabs[i & 1].hi[t] + tabs[i & 1].lo[t]);
         arrive(tab_free(i));
         float up = 1.f;
         if (kScaled) {
@@ -1006,7 +980,7 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3(a.ctas), dim3(OUT ? 768 : 512), smem, st, m, a);
+  return launch_pdl(kernel, dim3(a.ctas), dim3(LinPlan<DK, DV, OUT>::kThreads), smem, st, m, a);
 }
 
 }  // namespace

@@ -265,18 +265,27 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
     for (int hf = 0; hf < 2; ++hf) {
       const int t = 16 * mt + nc + 8 * hf;
       if (t >= a.T) continue;
-      if (infinite) {  // one by one: a weight of zero must not meet them
+      if (infinite) {
+        // One by one: a weight of zero must not meet them, and what is not finite goes
+        // through the state, as the sum over the key rows of q (k v), not as (q k) v.
         for (int s = 0; s <= t && s < n; ++s) {
+          if (exp2_approx(sg[t].minus(sg[s])) == 0.f) continue;
           const float p = sp[t][s];
-          if (p == 0.f) continue;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint2 x = *reinterpret_cast<const uint2*>(&sv[s][32 * grp + 4 * (kr + e)]);
             const float2 y0 = unpack16<T>(x.x), y1 = unpack16<T>(x.y);
-            o[mt][0][2 * hf + e] = fmaf(p, y0.x, o[mt][0][2 * hf + e]);
-            o[mt][1][2 * hf + e] = fmaf(p, y0.y, o[mt][1][2 * hf + e]);
-            o[mt][2][2 * hf + e] = fmaf(p, y1.x, o[mt][2][2 * hf + e]);
-            o[mt][3][2 * hf + e] = fmaf(p, y1.y, o[mt][3][2 * hf + e]);
+            const float y[4] = {y0.x, y0.y, y1.x, y1.y};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float add = p * y[j];
+              if (!(fabsf(y[j]) < INFINITY)) {
+                add = 0.f;
+#pragma unroll 1
+                for (int r = 0; r < DK; ++r) add = fmaf(lin_float(sq[t][r]), lin_float(sk[s][r]) * y[j], add);
+              }
+              o[mt][j][2 * hf + e] += add;
+            }
           }
         }
       }

@@ -357,10 +357,9 @@ void set_window_rows(AttnArgs& a) {
   a.row_tile = a.tile_wrows * a.G;
 }
 
-// Behind the header: arrival counts, (max, sum) partials, output partials.
-size_t count_bytes(int ctas) { return sdv::round_256((size_t)ctas * 4); }
+// Behind the header: (max, sum) partials, output partials.
 size_t part_bytes(int ctas, int row_tile, int D) {
-  return count_bytes(ctas) + sdv::round_256((size_t)2 * ctas * row_tile * 8) + sdv::round_256((size_t)2 * ctas * row_tile * D * 4);
+  return sdv::round_256((size_t)2 * ctas * row_tile * 8) + sdv::round_256((size_t)2 * ctas * row_tile * D * 4);
 }
 
 constexpr int kSimplePerSm = 2;
@@ -462,13 +461,13 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
   a.lead = tc ? 2 : 1;
   a.ctas = tc ? sms : kSimplePerSm * sms;
-  char* const counts = static_cast<char*>(ws) + sdv::kHeaderBytes;
   // Shared units are joined by their last CTA where a partial is at most 4 KB (single
   // tokens): the GPU's time a call hardly changes (613 positions, 8 heads: 9.8 and
   // 10.0 us) and the host issues one launch less (8.1 against 6.6 us).  Larger ones go
   // to the join's many CTAs.
-  if (tc && a.row_tile * a.D <= 1024) a.shared = reinterpret_cast<unsigned*>(counts);
-  a.part_ml = reinterpret_cast<float*>(counts + count_bytes(a.ctas));
+  if (tc && a.row_tile * a.D <= 1024 && a.ctas <= sdv::kAttnSharedBytes)
+    a.shared = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kAttnSharedAt);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
   a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
                                       sdv::round_256((size_t)2 * a.ctas * a.row_tile * 8));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
