@@ -128,17 +128,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 // A bounded wait by a whole warp, in few instructions: the roles of one kernel share
-// the SM's instruction cache.  On expiry the status word is set.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
-  bool done = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-  if (!done) {
-    const uint64_t t0 = global_timer_ns();
+// the SM's instruction cache, so what follows a first look in vain is one function for
+// all of them.  On expiry the status word is set.
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, int* status) {
+  const uint64_t t0 = global_timer_ns();
+  do {
 #pragma unroll 1
-    do done = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-    while (!done && global_timer_ns() - t0 < kWaitLimitNs);
-    if (!done && (threadIdx.x & 31) == 0) atomicOr(status, 1 /* kDevErrTimeout */);
-  }
-  return done;
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  } while (__all_sync(0xffffffffu, global_timer_ns() - t0 < kWaitLimitNs));
+  if ((threadIdx.x & 31) == 0) atomicOr(status, 1 /* kDevErrTimeout */);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status);
 }
 
 // L2 policy of data that other CTAs read too.
