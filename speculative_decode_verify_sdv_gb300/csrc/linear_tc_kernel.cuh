@@ -23,15 +23,16 @@
 // computes each part's own contribution (keys and values alone), and in the second
 // one each CTA sums those before it, decayed, on its way in.
 //
-// Warp roles: 0 TMA; 1 MMA; 2 the decays; 3 the values' check; then the
+// Warp roles: 0 TMA; 1 MMA; 2 the decays; 3 the values' end and their largest; then the
 // state's (key rows of M: U, decay, 16-bit copy for Q M; four, or eight with outputs,
-// where the copy is waited for), the keys' (K~'s two parts; eight, or four with outputs),
+// where the copy is waited for), the keys' (K~'s two parts, then the decay of Q M;
+// eight, or four with outputs),
 // four for scores to P and four for outputs.  All of it runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
 // times as slow).
 //
-// A zero weight must not meet an infinite value (0 * inf): a head with keys or values
-// that are not finite is noted, its state left unwritten, and the recurrent kernel,
-// launched behind, recomputes noted heads by the definition.
+// A zero weight must not meet an infinite value (0 * inf): keys or values that are not
+// finite make U so, its head is noted, its state left unwritten, and the recurrent
+// kernel, launched behind, recomputes noted heads by the definition.
 #pragma once
 
 #include <cuda.h>
@@ -97,12 +98,12 @@ struct LinTables {
 
 template <int DK, int DV, bool OUT>
 struct LinPlan {
-  // The first launch, without queries, state copy and outputs, has room for two buffers
-  // of keys, whose place K~'s high part then takes, of its low part and of values.
+  // Two buffers of keys, whose place K~'s high part then takes; the first launch, without
+  // queries, state copy and outputs, has room for two of its low part and of values too.
   static constexpr int kBufs = OUT ? 1 : 2;
   static constexpr int kThreads = OUT ? 768 : 512;
   static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2;
-  static constexpr int oK = 0, oHi = OUT ? oK + kK : oK, oLo = oK + 2 * kK, oV = oLo + kBufs * kK, oQ = oV + kBufs * kV;
+  static constexpr int oK = 0, oLo = oK + 2 * kK, oV = oLo + kBufs * kK, oQ = oV + kBufs * kV;
   static constexpr int oSt = oQ + (OUT ? kK : 0), oOut = oSt + (OUT ? 128 * DV * 2 : 0);
   static constexpr int oEx = oOut + (OUT ? 4 * 4096 : 0);  // Dk = 64: the state's low rows on their way to the high ones
   static constexpr int oTab = oEx + (DK == 64 ? (OUT ? 2 : 1) * 64 * 33 * 4 : 0);
@@ -170,7 +171,7 @@ struct LinWalk {
   __device__ __forceinline__ bool more() const { return at < end; }
   // chunks of the part that starts here
   __device__ __forceinline__ int count() const { return min(end - at, chunks - chunk); }
-  __device__ __forceinline__ void advance(const LinArgs& a, int c) {
+  __device__ __noinline__ void advance(const LinArgs& a, int c) {
     at += c;
     chunk += c;
     if (chunk < chunks) return;
@@ -190,7 +191,8 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using PL = LinPlan<DK, DV, OUT>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr bool kScaled = !kBf16;  // powers of two beside fp16 operands
+  constexpr bool kScaled = !kBf16;       // powers of two beside fp16 operands
+  constexpr bool kBound = OUT && kScaled;  // the largest value of a chunk bounds what it adds to M
   constexpr int kStateWarps = OUT ? 8 : 4, kKeyWarps = OUT ? 4 : 8;
   constexpr int kKeys0 = 4 + kStateWarps, kScores0 = kKeys0 + 4, kOut0 = kScores0 + 4;  // the roles' first warps
   extern __shared__ uint8_t smem_raw[];
@@ -202,12 +204,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   const uint32_t q_full = bar(4), s_full = bar(6), qm_done = bar(7),
                  pv_done = bar(9), p_ready = bar(12), o_free = bar(13),
-                 met = bar(14), met_m = bar(15), drain = bar(16), q_read = bar(23), k_read = bar(28);
-  // keys and values per buffer, otherwise a barrier's phase is the chunk
+                 met = bar(14), met_m = bar(15), drain = bar(16), q_read = bar(23);
+  // lo parts and values per buffer; a barrier of two takes turns, another one's phase is the chunk
   auto buf = [&](int i) { return PL::kBufs == 2 ? i & 1 : 0; };
   auto u_col = [&](int i) { return PL::kBufs == 2 && (i & 1) ? PL::cO : PL::cU; };
   auto phase = [&](int i) { return (uint32_t)(PL::kBufs == 2 ? i >> 1 : i) & 1u; };
-  auto k_full = [&](int i) { return bar(24 + buf(i)); };
+  auto k_buf = [&](int i) { return base + PL::oK + (i & 1) * PL::kK; };
+  auto k_full = [&](int i) { return bar(24 + (i & 1)); };
   auto v_full = [&](int i) { return bar(26 + buf(i)); };
   auto v_free = [&](int i) { return bar(30 + buf(i)); };
   auto upd_done = [&](int i) { return i & 1 ? bar(8) : bar(32); };
@@ -237,12 +240,11 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     mbar_init(met_m, kStateWarps);
     mbar_init(q_read, 4);
     mbar_init(drain, 1);
-    mbar_init(k_read, kKeyWarps);
     mbar_init(v_seen(0), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(24 + i), 1);
       mbar_init(bar(26 + i), 1);
-      mbar_init(bar(30 + i), 2 + kStateWarps);
+      mbar_init(bar(30 + i), kBound ? 2 + kStateWarps : kScaled ? 1 + kStateWarps : 1);
       mbar_init(m_ready(i), kStateWarps);
       mbar_init(kv_ready(i), kKeyWarps + 1);
     }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     mbar_init(up_ready(0), 4);
     mbar_init(up_ready(1), 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(18 + i), kStateWarps + kKeyWarps + (OUT ? 8 : 0));
+      mbar_init(bar(18 + i), kStateWarps + kKeyWarps + (OUT ? 4 : 0));
       mbar_init(bar(20 + i), 1);
     }
     fence_barrier_init();
@@ -304,14 +306,12 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       const int z0 = w.b * a.T + w.chunk * kLC;
       for (int c = 0; c < count; ++c, ++i) {
         const int z = z0 + c * kLC;
-        // the keys before in this buffer: read by their warps and by Q K^T, or, where K~
-        // took their place, by the product, which also ends the use of the values
-        if (OUT && i > 0 && (!await(k_read, (i - 1) & 1) || !await(s_full, (i - 1) & 1))) break;
-        if (!OUT && i >= 2 && !await(v_free(i), phase(i - 2))) break;
+        // the product with K~ that took the place of the keys before in this buffer
+        if (OUT ? !upd_wait(i - 1) : i >= 2 && !await(v_free(i), phase(i - 2))) break;
         if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
         __syncwarp();
         if (lane < DK / 64)
-          tma_load_3d(base + PL::oK + buf(i) * PL::kK + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
+          tma_load_3d(k_buf(i) + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
         ++asked_k;
         if (OUT) {
           if (i > 0 && (!await(qm_done, (i - 1) & 1) || (kScaled && !await(q_read, (i - 1) & 1)))) break;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       w.advance(a, count);
     }
     if (!ok) {  // copies whose consumers gave up have to land before the CTA ends
-      for (int e = max(asked_k - PL::kBufs, 0); e < asked_k; ++e) mbar_wait_bounded(k_full(e), phase(e), kLinDrainNs);
+      for (int e = max(asked_k - 2, 0); e < asked_k; ++e) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
       for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
       if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
     }
@@ -342,7 +342,6 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     constexpr uint32_t id_kb = idesc_16_f32(kBf16, 128, DV, false, true);  // Q M and P V
     constexpr uint32_t id_up = idesc_16_f32(kBf16, 128, DV, true, true);
     const uint64_t qd = smem_desc_sw128(base + PL::oQ, 16, 1024);
-    const uint64_t kd = smem_desc_sw128(base + PL::oK, 16, 1024);
     const uint64_t md = smem_desc_sw128(base + PL::oSt, 16384, 1024);
     // the chunks of all parts follow each other alike; a uniform count keeps the operands
     // in uniform registers
@@ -351,8 +350,9 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       const uint64_t vd = smem_desc_sw128(base + PL::oV + buf(i) * PL::kV, 16384, 1024);
       if (OUT) {
         // scores; P of the chunk before has been read
-        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), phase(i))) break;
+        if (!pv_wait(i) || !await(q_full, i & 1) || !await(k_full(i), (i >> 1) & 1)) break;
         tc_fence_after();
+        const uint64_t kd = smem_desc_sw128(k_buf(i), 16, 1024);
 #pragma unroll 1
         for (int j = 0; j < DK / 64; ++j)
           tc_mma4_ss<2, 2>(tm + PL::cS, qd + j * 1024, kd + j * 1024, id_qk, j > 0);
@@ -374,13 +374,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       // K~^T V: the low parts first; at Dk = 64 both at once (rows 0-63 from the high,
       // 64-127 from the low part)
       if constexpr (DK == 128) {
-        const uint64_t hd = smem_desc_sw128(base + PL::oHi + buf(i) * PL::kK, 16384, 1024);
+        const uint64_t hd = smem_desc_sw128(k_buf(i), 16384, 1024);
         const uint64_t ld = smem_desc_sw128(base + PL::oLo + buf(i) * PL::kK, 16384, 1024);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j)
           tc_mma4_ss<128, 128>(tm + u_col(i), (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
       } else {
-        const uint64_t bd = smem_desc_sw128(base + PL::oHi + buf(i) * PL::kK, PL::oLo - PL::oHi, 1024);
+        const uint64_t bd = smem_desc_sw128(k_buf(i), base + PL::oLo + buf(i) * PL::kK - k_buf(i), 1024);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j)
           tc_mma4_ss<128, 128>(tm + u_col(i), bd + j * 512, vd + j * 512, id_up, j > 0);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     DecaySum run;  // log2 decay of the part so far
     // natural log decays, asked for two chunks ahead of their use: a chunk takes less than
     // memory under this load does
-    float next[2][4];
+    float next[2][4] = {};
     auto load = [&](int c, float (&x)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -413,9 +413,8 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     };
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
-      load(0, next[0]);
-      load(1, next[1]);
-      for (int c = 0; c < count; ++c, ++i) {
+#pragma unroll 1
+      for (int c = -2; c < count; ++c) {
         DecaySum g[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -423,10 +422,11 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
           next[0][e] = next[1][e];
         }
         if (c + 2 < count) load(c + 2, next[1]);
+        if (c < 0) continue;
 #pragma unroll
         for (int e = 1; e < 4; ++e) g[e].add(g[e - 1]);
         DecaySum incl = g[3];
-#pragma unroll
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
           const DecaySum o{__shfl_up_sync(0xffffffffu, incl.hi, off), __shfl_up_sync(0xffffffffu, incl.lo, off)};
           if (lane >= off) incl.add(o);
@@ -441,14 +441,14 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         reinterpret_cast<float4*>(tb.lo)[lane] = make_float4(g[0].lo, g[1].lo, g[2].lo, g[3].lo);
         if (a.pass == 0) run.add(DecaySum{__shfl_sync(0xffffffffu, g[3].hi, 31), __shfl_sync(0xffffffffu, g[3].lo, 31)});
         arrive(tab_full(i));
+        ++i;
       }
       if (!ok) break;
       if (a.pass == 0 && lane == 0) a.parts[blockIdx.x].decay = run;
       w.advance(a, count);
     }
   } else if (warp == 3) {
-    // ---- the values: zeros behind the end, a note where one is not finite, the largest ----
-    int part = 0;
+    // ---- the values: zeros behind the end, the largest ----
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
             for (int h = 0; h < DV / 64; ++h) sts128(vb + h * 16384 + swz128(e >> 3, e & 7), make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
         }
-        arrive(kv_ready(i));  // the check reads beside the products
+        arrive(kv_ready(i));  // the search reads beside the products
+        if (!kBound) continue;
         uint32_t mx = 0;
 #pragma unroll 1
         for (int e = 0; e < DV / 16; ++e) {  // rows 32 (e % 4) + lane, 64 columns
@@ -474,15 +475,11 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
           for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
         }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-        if (lane == 0) {
-          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) misc[2 + (part & 1)] = part + 1;
-          if (kScaled) fmisc[24 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
-        }
+        if (lane == 0) fmisc[24 + (i & 1)] = __half2float(__ushort_as_half((unsigned short)min(mx, 0x7bffu)));
         arrive(v_seen(i));
         if (lane == 0) mbar_arrive(v_free(i));
       }
       if (!ok) break;
-      ++part;
       w.advance(a, count);
     }
   } else if (warp < kKeys0) {
@@ -552,13 +549,19 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         for (int e = 0; e < kStateWarps; ++e) top = max(top, misc[16 + e]);
         bound = __int_as_float(top);
       }
-      auto take_u = [&](int chunks) {  // the last chunk's U is there, and its values checked
-        if (!upd_wait(chunks) || !await(v_seen(chunks - 1), ((chunks - 1) >> 1) & 1)) return false;
-        if (lane == 0) mbar_arrive(v_free(chunks - 1));
+      auto take_u = [&](int chunks) {  // the last chunk's U is there, and its largest value
+        if (!upd_wait(chunks)) return false;
+        if (kBound) {
+          if (!await(v_seen(chunks - 1), ((chunks - 1) >> 1) & 1)) return false;
+          if (lane == 0) mbar_arrive(v_free(chunks - 1));
+        }
         tc_fence_after();
         return true;
       };
       float dec = 0.f, dn = 1.f;  // of the last chunk: M = dec M + dn U
+      // 0 times U, summed: NaN once a key or value of the part is not finite, which makes
+      // a row or column of U so (0 times it is NaN)
+      f32x2 odd = pair2(0.f, 0.f);
       auto state_of = [&](int j, uint32_t (&x)[32], bool take) {  // 32 columns of M behind the last chunk
         tmem_ld32(tq + PL::cM + j, x);
         if (!take) {
@@ -575,8 +578,9 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         const f32x2 dec2 = pair2(dec, dec), dn2 = pair2(dn, dn);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 y = unpair2(fma2(pair2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), dn2,
-                                        mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), dec2)));
+          const f32x2 u2 = pair2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+          odd = fma2(u2, pair2(0.f, 0.f), odd);
+          const float2 y = unpair2(fma2(u2, dn2, mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), dec2)));
           x[e] = __float_as_uint(y.x);
           x[e + 1] = __float_as_uint(y.y);
         }
@@ -621,12 +625,29 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         if (kScaled) {
           if (!await(ek_ready(i), (i >> 1) & 1)) break;
           dn = exp2f((float)-misc[4 + (i & 1)]);
+          // without outputs the product does not wait for this: the next keys here do
+          if (!OUT) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_free(i));
+          }
         }
         tc_fence_before();
         arrive(m_ready(i));
       }
       if (!ok || !take_u(i)) break;
       // into the array if the head ends here, else this CTA's contribution
+#pragma unroll 1
+      for (int j = col0; j < col1; j += 32) {  // the last U
+        uint32_t u[32];
+        tmem_ld32(tq + u_col(i - 1) + j, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          odd = fma2(pair2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), pair2(0.f, 0.f), odd);
+      }
+      if (unpair2(odd).x != 0.f || unpair2(odd).y != 0.f) misc[2 + (part & 1)] = part + 1;
+      arrive(met_m);
+      if (!await(met_m, meetings++ & 1)) break;
       float* dst = nullptr;
       int bad = misc[2 + (part & 1)] == part + 1;
       if (a.pass == 0) {
@@ -677,30 +698,28 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     constexpr int kUnits = DK / 8 / (kKeyWarps / 4);  // a thread's 16-byte units
     const int u0 = (warp - kKeys0) / 4 * kUnits;
     uint32_t meetings = 0;
-    int part = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
         const int nv = w.n - (w.chunk + c) * kLC;  // tokens of the chunk
-        const uint32_t kb = base + PL::oK + buf(i) * PL::kK;
-        if (!await(k_full(i), phase(i))) break;
-        // the largest key of the chunk sets its power of two; one that is not finite is noted
-        uint32_t mx = 0;
-        if (r < nv) {
-#pragma unroll 1
-          for (int h = u0; h < u0 + kUnits; h += 4) {
-            uint4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = lds128(kb + (h >> 3) * 16384 + swz128(r, (h & 7) + k));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
-          }
-          mx = max(mx & 0xffffu, mx >> 16);
-          if (mx >= (kBf16 ? 0x7f80u : 0x7c00u)) misc[2 + (part & 1)] = part + 1;
-        }
+        const uint32_t kb = k_buf(i);
+        if (!await(k_full(i), (i >> 1) & 1)) break;
         float up = 1.f;
         int pre = 0;
         if (kScaled) {
+          // the largest key of the chunk sets its power of two
+          uint32_t mx = 0;
+          if (r < nv) {
+#pragma unroll 1
+            for (int h = u0; h < u0 + kUnits; h += 4) {
+              uint4 x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = lds128(kb + (h >> 3) * 16384 + swz128(r, (h & 7) + k));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, abs_max2(x[k]));
+            }
+            mx = max(mx & 0xffffu, mx >> 16);
+          }
           mx = __reduce_max_sync(0xffffffffu, mx);
           if (lane == 0) misc[32 + 8 * (i & 1) + warp - kKeys0] = (int)mx;
           arrive(met);
@@ -724,12 +743,14 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         if (!await(tab_full(i), (i >> 1) & 1)) break;
         const float f = r < nv ? exp2_approx(tabs[i & 1].at(kLC - 1).minus(tabs[i & 1].at(r))) * up : 0.f;  // e^{G_C - G_s}
         const uint32_t fh = pack16<T>(f, f);
+        const float eg = OUT ? exp2_approx(tabs[i & 1].hi[r] + tabs[i & 1].lo[r]) : 0.f;  // e^{G_t}
         const float fr = f - unpack16<T>(fh).x;
         const uint32_t fl = pack16<T>(fr, fr);
         const float pw = exp2f((float)pre);
         const uint32_t up2 = pack16<T>(pw, pw);
         arrive(tab_free(i));
-        if (OUT && !upd_wait(i)) break;  // the last product has read K~
+        // the last product has read K~'s low part, Q K^T the keys
+        if (OUT && (!upd_wait(i) || !await(s_full, i & 1))) break;
 #pragma unroll 1
         for (int h = u0; h < u0 + kUnits; h += 4) {  // four 16-byte units in flight
           const uint32_t blk = (h >> 3) * 16384;
@@ -752,16 +773,50 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            sts128(base + PL::oHi + buf(i) * PL::kK + blk + swz128(r, (h & 7) + k), x[k]);
+            sts128(kb + blk + swz128(r, (h & 7) + k), x[k]);
             sts128(base + PL::oLo + buf(i) * PL::kK + blk + swz128(r, (h & 7) + k), lo[k]);
           }
         }
         fence_proxy_async_smem();
-        if (OUT) arrive(k_read);
         arrive(kv_ready(i));
+        if (OUT) {
+          // the state's part of the output, in the units of P V: by e^{G_t}, M's copy's power
+          // of two and the row's
+          float rise = 1.f;
+          if (kScaled) {
+            if (!await(up_ready(i), (i >> 1) & 1)) break;
+            rise = ups[(i & 1) * kLC + r];
+          }
+          if (!await(qm_done, i & 1)) break;
+          tc_fence_after();
+          const float by = eg * (kScaled ? fmisc[6 + (i & 1)] : 1.f) * rise;
+          const f32x2 by2 = pair2(by, by);
+          const bool drop = eg == 0.f;  // whatever the state holds
+          const uint32_t to = tm + PL::cO + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+          for (int j = 0; j < DV; j += 32) {
+            uint32_t x[32];
+            tmem_ld32(to + j, x);
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, drop)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (drop) x[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = unpair2(mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), by2));
+              x[e] = __float_as_uint(y.x);
+              x[e + 1] = __float_as_uint(y.y);
+            }
+            tmem_st32(to + j, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(p_ready);
+        }
       }
       if (!ok) break;
-      ++part;
       w.advance(a, count);
     }
   } else if (OUT && warp < kOut0) {
@@ -867,13 +922,17 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   } else if (OUT) {
     // ---- outputs: thread = token, then rows as 128-byte lines ----
     // first the zeros behind the sequences' ends, whole chunks (heads dealt to the CTAs)
-    for (long long u = blockIdx.x; u < (long long)a.B * a.H; u += gridDim.x) {
-      const int b = (int)(u / a.H), h = (int)(u % a.H);
-      const int first = LinWalk::chunks_of(lin_tokens(a, b)) * kLC;
-      constexpr int per = DV / 8;  // 16-byte units of a row
-      for (long long e = (long long)first * per + (warp - kOut0) * 32 + lane; e < (long long)a.T * per; e += 128)
-        reinterpret_cast<uint4*>(a.o)[(((long long)b * a.T + e / per) * a.H + h) * per + e % per] =
-            make_uint4(0, 0, 0, 0);
+    if (a.n_tokens != nullptr) {
+#pragma unroll 1
+      for (int u = blockIdx.x; u < a.B * a.H; u += gridDim.x) {
+        const int b = u / a.H, h = u - b * a.H;
+        constexpr int per = DV / 8;  // 16-byte units of a row
+        const int e = (warp - kOut0) * 32 + lane;
+        int t = LinWalk::chunks_of(lin_tokens(a, b)) * kLC + e / per;
+        uint4* p = reinterpret_cast<uint4*>(a.o) + (((long long)b * a.T + t) * a.H + h) * per + e % per;
+#pragma unroll 1
+        for (; t < a.T; t += 128 / per, p += 128 / per * a.H * per) *p = make_uint4(0, 0, 0, 0);
+      }
     }
     const int quarter = warp & 3, t = quarter * 32 + lane;
     const uint32_t tq = tm + PL::cO + ((uint32_t)(quarter * 32) << 16);
@@ -881,52 +940,15 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       for (int c = 0; c < count; ++c, ++i) {
-        // the state's part of the output, in the units of P V: by e^{G_t}, M's copy's power
-        // of two and the row's
-        if (!await(tab_full(i), (i >> 1) & 1)) break;
-        const float eg = exp2_approx(tabs[i & 1].hi[t] + tabs[i & 1].lo[t]);
-        arrive(tab_free(i));
-        float up = 1.f;
-        if (kScaled) {
-          if (!await(up_ready(i), (i >> 1) & 1)) break;
-          up = ups[(i & 1) * kLC + t];
-        }
-        if (!await(qm_done, i & 1)) break;
-        tc_fence_after();
-        {
-          const float f = eg * (kScaled ? fmisc[6 + (i & 1)] : 1.f) * up;
-          const f32x2 f2 = pair2(f, f);
-          const bool drop = eg == 0.f;  // whatever the state holds
-#pragma unroll 1
-          for (int j = 0; j < DV; j += 32) {
-            uint32_t x[32];
-            tmem_ld32(tq + j, x);
-            tmem_wait_ld();
-            if (__any_sync(0xffffffffu, drop)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (drop) x[e] = 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = unpair2(mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2));
-              x[e] = __float_as_uint(y.x);
-              x[e + 1] = __float_as_uint(y.y);
-            }
-            tmem_st32(tq + j, x);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(p_ready);
         if (!pv_wait(i + 1)) break;
         tc_fence_after();
-        const float f = a.scale / up;  // (a power of two)
+        // (a power of two; the scores' warps have left it long ago)
+        const float f = kScaled ? a.scale / ups[(i & 1) * kLC + t] : a.scale;
         const int row = (w.chunk + c) * kLC + quarter * 32 + (lane >> 3);
         T* const dst = static_cast<T*>(a.o) + (((long long)w.b * a.T + row) * a.H + w.h) * DV + (lane & 7) * 8;
-#pragma unroll 1
-        for (int j = 0; j < DV; j += 64) {  // 64 columns at a time through shared memory
-          uint32_t y[32];
+        // 64 columns at a time through shared memory; all of them leave tensor memory first
+        uint32_t y[32];
+        auto take = [&](int j) {
 #pragma unroll
           for (int hf = 0; hf < 64; hf += 32) {
             uint32_t x[32];
@@ -936,13 +958,18 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
             for (int e = 0; e < 32; e += 2)
               y[(hf + e) / 2] = pack16<T>(mul2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair2(f, f)));
           }
-          if (j + 64 == DV) {  // the last read of this chunk's outputs
-            tc_fence_before();
-            arrive(o_free);
-          }
+        };
+        take(0);
+#pragma unroll 1
+        for (int j = 0; j < DV; j += 64) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             sts128(stage + swz128(lane, e), make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+          if (j + 64 < DV) take(j + 64);
+          if (j == 0) {
+            tc_fence_before();
+            arrive(o_free);
+          }
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
