@@ -421,7 +421,7 @@ SDV_API size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, 
  * 1, fp32 [H] (the same for every token) where it is 0; 0 or below, -inf drops the
  * state before the token; values above 0 are taken as 0.
  * n_tokens_or_null: device int32 [B] (NULL: T each; clamped to [0, T]): tokens
- * t >= n_tokens[b] neither enter the state nor are they read, and their o is 0.
+ * t >= n_tokens[b] have no effect, whatever they hold, and their o is 0.
  * state_in_or_null: fp32 [B][H][Dk][Dv] before the first token (NULL: zeros);
  * state_out_or_null: the state after the last one (NULL: not written).  The two may
  * be the same array.  o_or_null: [B][T][H][Dv] (NULL: not computed; q is then not
