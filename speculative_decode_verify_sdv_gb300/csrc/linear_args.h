@@ -84,13 +84,10 @@ __device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
 __device__ __forceinline__ float lin_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float lin_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// The log decay of token t, head h, as it was given.
-__device__ __forceinline__ float lin_raw_decay(const LinArgs& a, int b, int t, int h) {
-  return __ldg(a.g + (a.g_token ? ((long long)b * a.T + t) * a.H + h : h));
-}
-__device__ __forceinline__ float lin_clamp_decay(float g) { return g > 0.f ? 0.f : g; }  // NaN stays NaN
+// The log decay of token t, head h: at most 0 (NaN stays NaN).
+__device__ __forceinline__ float lin_clamp_decay(float g) { return g > 0.f ? 0.f : g; }
 __device__ __forceinline__ float lin_decay(const LinArgs& a, int b, int t, int h) {
-  return lin_clamp_decay(lin_raw_decay(a, b, t, h));
+  return lin_clamp_decay(__ldg(a.g + (a.g_token ? ((long long)b * a.T + t) * a.H + h : h)));
 }
 #endif
 

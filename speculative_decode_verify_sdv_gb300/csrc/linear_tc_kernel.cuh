@@ -108,7 +108,8 @@ struct LinPlan {
   static constexpr int oEx = oOut + (OUT ? 4 * 4096 : 0);  // Dk = 64: the state's low rows on their way to the high ones
   static constexpr int oTab = oEx + (DK == 64 ? (OUT ? 2 : 1) * 64 * 33 * 4 : 0);
   static constexpr int oFac = oTab + 2 * (int)sizeof(LinTables);  // the scores' warps' factors [4][128]
-  static constexpr int oBars = oFac + (OUT ? 4 * kLC * 4 : 0);
+  static constexpr int oRing = oFac + (OUT ? 4 * kLC * 4 : 0);  // four chunks' decays
+  static constexpr int oBars = oRing + 4 * kLC * 4;
   static constexpr int kNumBars = 36;
   static constexpr int oMisc = oBars + kNumBars * 8;
   static constexpr int oUp = oMisc + 256;         // the rows' powers of two [2][128]
@@ -266,7 +267,10 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = misc[0];
-  griddep_wait();
+  // The second launch needs nothing of the first but the parts, and that one has waited for
+  // what came before both.
+  const bool second = a.pass == 1 && a.T > kLC;
+  if (!second) griddep_wait();
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
@@ -401,28 +405,32 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   } else if (warp == 2) {
     // ---- decays: four tokens a lane, sums in pairs of floats ----
     DecaySum run;  // log2 decay of the part so far
-    // natural log decays, asked for two chunks ahead of their use: a chunk takes less than
-    // memory under this load does
-    float next[2][4] = {};
-    auto load = [&](int c, float (&x)[4]) {
+    // natural log decays, asked for three chunks ahead of their use (a chunk takes less than
+    // memory under this load does) into a ring of shared memory; a lane reads its own
+    const uint32_t ring = base + PL::oRing + 16 * lane;
+    auto ask = [&](int c, int count) {
+      if (c < count) {
+        const int t = (w.chunk + c) * kLC + 4 * lane;
+        const float* const from = a.g + (a.g_token ? ((long long)w.b * a.T + t) * a.H + w.h : w.h);
+        const int step = a.g_token ? a.H : 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = (w.chunk + c) * kLC + 4 * lane + e;
-        x[e] = t < w.n ? lin_raw_decay(a, w.b, t, w.h) : 0.f;
+        for (int e = 0; e < 4; ++e)
+          cp_async4(ring + (c & 3) * (kLC * 4) + 4 * e, t + e < w.n ? from + e * step : a.g, t + e < w.n);
       }
+      cp_async_commit();
     };
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
 #pragma unroll 1
-      for (int c = -2; c < count; ++c) {
+      for (int c = -3; c < count; ++c) {
+        ask(c + 3, count);
+        if (c < 0) continue;
+        cp_async_wait<3>();
+        const uint4 x = lds128(ring + (c & 3) * (kLC * 4));
+        const uint32_t given[4] = {x.x, x.y, x.z, x.w};
         DecaySum g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[e] = DecaySum::log2_of(lin_clamp_decay(next[0][e]));
-          next[0][e] = next[1][e];
-        }
-        if (c + 2 < count) load(c + 2, next[1]);
-        if (c < 0) continue;
+        for (int e = 0; e < 4; ++e) g[e] = DecaySum::log2_of(lin_clamp_decay(__uint_as_float(given[e])));
 #pragma unroll
         for (int e = 1; e < 4; ++e) g[e].add(g[e - 1]);
         DecaySum incl = g[3];
@@ -491,6 +499,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     const bool owner = r < DK;  // rows with a place in the state's array
     uint32_t meetings = 0;
     int part = 0;
+    if (second) griddep_wait();
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;

@@ -144,6 +144,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, in
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status);
 }
 
+// Four bytes into shared memory behind the thread's back, zeros where `real` is false.
+__device__ __forceinline__ void cp_async4(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(real ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // L2 policy of data that other CTAs read too.
 __device__ __forceinline__ uint64_t l2_policy_normal() {
   uint64_t p;
