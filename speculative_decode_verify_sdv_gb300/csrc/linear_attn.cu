@@ -139,10 +139,17 @@ bool lin_shape(int B, int T, int H, int Dk, int Dv) {
 size_t lin_notes(int B, int H) { return round_256((size_t)B * H * 4); }
 size_t lin_parts(int ctas, int Dk, int Dv) { return (size_t)ctas * (sizeof(LinPart) + 2 * (size_t)Dk * Dv * 4); }
 
-// The window form for kLinWindowFrom to 32 tokens, the chunked form for more, both for
-// the head sizes that they have; one token, and other head sizes, are the recurrent form's.
-constexpr int kLinWindowFrom = 2;
-bool lin_window(int T, int Dk, int Dv) { return linear_tc_takes(Dk, Dv) && T >= kLinWindowFrom && T <= kLinWindow; }
+// Which form (head sizes of 64 and 128; others are the recurrent form's, as one token is).
+// Microseconds, recurrent against window form, 512 heads of 128 x 128 and 32 of them, for
+// outputs and state: 31.4 to 33.4 and 12.9 to 15.0 at 6 tokens, 33.4 to 33.4 and 15.0 to
+// 15.0 at 7, 55.9 to 41.6 and 25.2 to 17.1 at 17; outputs alone: 17.0 to 21.2 and 8.9 to
+// 10.9 at 2 tokens, 21.3 to 20.5 and 10.9 to 10.9 at 4; the state alone: 21.1 to 21.2 and
+// 8.9 to 8.9 at 2, 23.2 to 21.1 and 10.9 to 8.9 at 4.  Window against chunked form: 48.8 to
+// 59.0 and 18.1 to 23.2 at 32, the window form's most.
+int lin_window_from(bool outputs, bool state) { return outputs && state ? 7 : outputs ? 4 : 2; }
+bool lin_window(int T, int Dk, int Dv, bool outputs, bool state) {
+  return linear_tc_takes(Dk, Dv) && T >= lin_window_from(outputs, state) && T <= kLinWindow;
+}
 bool lin_chunked(int B, int T, int H, int Dk, int Dv) {
   // the tensor maps' coordinates and the split's arithmetic are 32-bit
   const long long chunks = (long long)B * H * ((T + kLinChunk - 1) / kLinChunk);
@@ -210,7 +217,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
   a.s_out = state_out_or_null;
   a.o = o_or_null;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (lin_window(T, Dk, Dv)) return status_of(launch_linear_window(dtype, a, st));
+  if (lin_window(T, Dk, Dv, a.o != nullptr, a.s_out != nullptr)) return status_of(launch_linear_window(dtype, a, st));
   if (lin_chunked(B, T, H, Dk, Dv)) {
     a.ctas = sm_count();
     if (a.ctas <= 0) return SDV_ERR_CUDA;

@@ -37,7 +37,8 @@ struct AppendArgs {
 };
 
 // Row (b, t) of one tensor per warp: a copy of heads * vec 16-byte units, units
-// of one head contiguous on both sides.
+// of one head contiguous on both sides.  The copy bounds it: 148 MB read and written for
+// eight prompts of up to 4096 rows in 26.1 us, 5.7 TB/s; one row is the call itself, 8.6 us.
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   griddep_wait();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
@@ -68,7 +69,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
 // maximum and sum of two rows, each thread the outputs of up to two columns of
 // all rows.  It is the form for head sizes and page sizes outside the tensor-core
 // kernel's; a position a row does not see has weight zero and is skipped, so
-// nothing its values hold reaches the row.
+// nothing its values hold reaches the row.  Its arithmetic bounds it: 8 sequences of 4000
+// positions, 32 heads over 8 of 96: 474 us for one row each (0.2 TB/s of cache), 3.3 ms
+// for 17; the tensor-core kernel at heads of 128 takes 38 and 52.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = kAttnSimpleRows, P = kAttnSimpleTile;
@@ -220,7 +223,8 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
 // A thread per row and four columns (a unit's rows side by side, as the partials
 // lie) and quarter of the partials, eight loads in flight each: the partials sit in
 // L2, so latency is what there is to hide.  The order of the sums is fixed by the
-// split.
+// split.  48 units of 96 rows x 128 columns, four partials each: 15 us with the partials
+// in memory; fewer blocks that loop over their items took as long.
 constexpr int kJoinItems = 64, kJoinParts = 4;
 
 template <typename T>
