@@ -6,9 +6,10 @@
 // tiles and `lead` more, the time that its queries, its last tile's cleaning and its
 // outputs take in tiles' time, laid before its first tile: short contexts in a batch
 // would otherwise all fall to a few CTAs.  Ragged contexts are then balanced to one
-// tile whatever their lengths, and one long context spreads over the whole GPU.  A unit inside one CTA's range is finished there; the others
-// leave (unnormalised output, max, sum) partials that the join launch adds in CTA
-// order.  The lengths live on the device, so every warp that needs the split
+// tile whatever their lengths, and one long context spreads over the whole GPU.  A unit
+// inside one CTA's range is finished there; the others leave (unnormalised output, max,
+// sum) partials that are added in CTA order, by a launch of its own or, where they are
+// small, by the last of the CTAs.  The lengths live on the device, so every warp that needs the split
 // computes it from them (a warp-wide scan over the sequences), and the split is a
 // function of lengths and shapes alone: results do not vary from run to run.
 #pragma once

@@ -21,7 +21,7 @@
 //   warp 7      walks the units ahead of the others: stages a segment's Q (two
 //               buffers of the row tile's rows) and what it is, so that short
 //               contexts follow each other without a load in between.
-// With at most 32 rows (single tokens, short windows) the rows stand four times in
+// Few rows (single tokens, short windows) stand four times in
 // the MMA's 128, and each softmax warp takes a quarter of a tile's positions for all
 // of them, the other positions' weights being zero in its copy: the softmax of a tile
 // then takes a quarter of the time, and the four (m, l, O) are merged at the end.
@@ -38,6 +38,14 @@
 // before P V: what the last page holds behind the end becomes zeros, and a window
 // row's infinities and NaN are zeroed and noted, then added at the end to the rows
 // that do see them -- 0 * inf would otherwise reach the others.
+//
+// Measured, a call: one token over 500,000 positions of 8 heads of 128: 290 us, 7.1 TB/s
+// of cache; 48 sequences of up to 16,000: 92 us, 6.0 TB/s.  What shorter calls add is the
+// start (4 us until the first tile is there: the walk, cold instructions, the first read)
+// and the end.  17 rows of 8 heads a cache head of 256 over 32,768 positions: 31.7 us,
+// 2.1 TB/s: 136 rows are two tiles, and a tile of 64 positions is 2100 cycles, of which
+// the MMAs' issue takes 1700 (S reads Q and K from shared memory, 6 KB for 64 cycles of
+// products).  One token over 613 positions: 10.9 us, all of it start and end.
 #pragma once
 
 #include <cuda.h>
@@ -62,7 +70,8 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnSmem = 232448;                // all of an SM's: one CTA, one tensor-memory allocation
 constexpr uint64_t kAttnDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
 constexpr int kMaxSlots = 8;
-constexpr int kSpreadRows = 32;                  // rows that stand four times in the MMA tile
+constexpr int kSpreadRows = 32;                  // rows that can stand four times in the MMA tile
+constexpr int kSpreadMost = 2048;                // and do up to this many elements of an output
 // The merge buffer: 4 copies of up to 32 rows, at least 32 columns and 4 of padding.
 constexpr int kMergeBytes = 4 * kSpreadRows * (32 + 4) * 4;
 
@@ -789,7 +798,11 @@ cudaError_t attn_tc_launch(const AttnMaps& m, AttnArgs a, cudaStream_t st) {
 // The instance for one 16-bit type.
 template <typename T>
 cudaError_t attn_tc_dispatch(const AttnMaps& m, const AttnArgs& a, cudaStream_t st) {
-  const bool spread = a.row_tile <= kSpreadRows;
+  // Spread rows end with a merge of four outputs of rows x D.  Spread against not (us; 48
+  // sequences of 4000 positions unless stated): 4 rows x 128: 138 to 143, 300 of 100: 68 to
+  // 93, one of 613: 15.0 to 17.1; 8 x 256: 83 to 87; 16 x 256: 90 to 92; 32 x 128: 167 to
+  // 170, but 300 of 100: 117 to 93; 32 x 256, 8 of 8000: 49 to 45, one of 30,000: 38 to 34.
+  const bool spread = a.row_tile <= kSpreadRows && a.row_tile * a.D <= kSpreadMost;
   switch (a.D) {
     case 64: return spread ? attn_tc_launch<T, 64, true>(m, a, st) : attn_tc_launch<T, 64, false>(m, a, st);
     case 128: return spread ? attn_tc_launch<T, 128, true>(m, a, st) : attn_tc_launch<T, 128, false>(m, a, st);

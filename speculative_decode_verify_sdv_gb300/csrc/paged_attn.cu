@@ -463,6 +463,8 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   if (tc) set_window_rows(a);
   else set_rows(a, sdv::kAttnSimpleRows);
   a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
+  // (0, 1 and 2: six tree windows 43.0, 35.5 and 33.4 us, 48 ragged contexts 120.8, 104.4
+  // and 104.4)
   a.lead = tc ? 2 : 1;
   a.ctas = tc ? sms : kSimplePerSm * sms;
   // Shared units are joined by their last CTA where a partial is at most 4 KB (single

@@ -120,7 +120,14 @@ def test_one_workspace_for_every_operation(sdv):
     (BF16, 1, 3, 128, 1, 128, 16, [900], [3]),            # exactly as many
     (F16, 1, 32, 5, 1, 128, 64, [640], [32]),             # 160 rows: a tile of 32 words cut
     (BF16, 2, 32, 65, 1, 64, 16, [129, 0], [32, 31]),
-    (F16, 1, 4, 8, 2, 128, 512, [1000], [4])])
+    (F16, 1, 4, 8, 2, 128, 512, [1000], [4]),
+    # few rows, on both sides of 2048 elements of an output and of 32 rows
+    (F16, 3, 2, 8, 2, 256, 64, [0, 63, 700], [2, 1, 2]),
+    (BF16, 3, 3, 6, 2, 256, 32, [1, 64, 500], [3, 0, 3]),
+    (F16, 2, 4, 8, 1, 128, 16, [126, 2000], [4, 4]),
+    (BF16, 2, 17, 2, 2, 128, 16, [127, 400], [17, 9]),
+    (F16, 2, 8, 8, 2, 64, 16, [300, 0], [8, 8]),
+    (BF16, 2, 11, 3, 1, 64, 16, [300, 5], [11, 8])])
 def test_rows_past_a_tile(sdv, dt, B, S, hq, hkv, d, page, ctx, n):
     q, kp, vp, table = att.make(dt, B, S, hq, hkv, d, page, ctx, n, 55)
     mask = att.words(np.random.default_rng(5), B, S)
@@ -128,3 +135,22 @@ def test_rows_past_a_tile(sdv, dt, B, S, hq, hkv, d, page, ctx, n):
     assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
     ref = mixing.attention(f64(q), f64(kp), f64(vp), table.tolist(), ctx, n, mask, d ** -0.5)
     att.check(dt, ref, out, lse, d)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("d,S,page,ctx", [(256, 13, 64, 33), (128, 20, 16, 120), (64, 16, 32, 126)])
+def test_infinite_values_in_windows_of_few_rows(sdv, dt, d, S, page, ctx):
+    hq, hkv, j = 4, 2, 2
+    q, kp, vp, table = att.make(dt, 1, S, hq, hkv, d, page, [ctx], [S], 56)
+    where = (table[0, (ctx + j) // page], slice(None), (ctx + j) % page)
+    clean = vp.clone()
+    v = vp[where].clone()
+    v[..., 0], v[..., d - 1] = float("inf"), float("-inf")
+    vp[where] = v
+    out, lse, _ = att.call(sdv, q, kp, vp, table, [ctx], [S], None, d ** -0.5)
+    ref = mixing.attention(f64(q), f64(kp), f64(clean), table.tolist(), [ctx], [S], None, d ** -0.5)
+    att.check(dt, {k: x[:, :j] for k, x in ref.items()}, out[:, :j], lse[:, :j], d)
+    o = f64(out)[:, j:]
+    assert np.all(np.isposinf(o[..., 0])) and np.all(np.isneginf(o[..., -1]))
+    inner = {k: (x[:, j:, :, 1:-1] if x.ndim == 4 else x[:, j:]) for k, x in ref.items()}
+    att.check(dt, inner, out[:, j:, :, 1:-1], lse[:, j:], d)
