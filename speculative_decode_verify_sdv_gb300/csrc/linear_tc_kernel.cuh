@@ -25,9 +25,9 @@
 //
 // Warp roles: 0 TMA; 1 MMA; 2 the decays; 3 the values' end and their largest; then the
 // state's (key rows of M: U, decay, 16-bit copy for Q M; four, or eight with outputs,
-// where the copy is waited for), the keys' (K~'s two parts, then the decay of Q M;
-// eight, or four with outputs),
-// four for scores to P and four for outputs.  All of it runs in rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
+// where the copy is waited for), the keys' (K~'s two parts, then the decay of Q M; eight,
+// or four with outputs), four for scores to P and four for outputs.  All of it runs in
+// rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
 // times as slow).
 //
 // A zero weight must not meet an infinite value (0 * inf): keys or values that are not
@@ -37,8 +37,8 @@
 // Measured: 8192 tokens, 32 heads of 128 x 128 (16 of queries and keys), fp16: 133 us a
 // call, 1.6 TB/s of what has to move; of it the first launch 49 us, the second 93, 4 for
 // the recurrent kernel that finds nothing to do (each alone, nothing in L2).  Six
-// prompts of up to 3001 tokens, 24 heads of 64 x 128, bf16: 94 us, 2.5 TB/s (31, 72, 4).  The
-// memory and the tensor cores (12 to 19 %) wait for a chain of roles: a chunk of the
+// prompts of up to 3001 tokens, 24 heads of 64 x 128, bf16: 94 us, 2.5 TB/s (31, 72, 4).
+// The memory and the tensor cores (12 to 19 %) wait for a chain of roles: a chunk of the
 // second launch is 7 to 8 thousand cycles from U through the state's copy (3 thousand),
 // Q M, its decay and P V to the output, at 38 % of the issue slots; 680 KB of shared
 // memory traffic a chunk keep that at 5 thousand.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   volatile int* const misc = reinterpret_cast<int*>(sb + PL::oMisc);
   // misc: 0 tmem base; 2, 3 a part whose values are not all finite; 4, 5 exponent of K~;
   // 6, 7 M's copy's power of two undone; 16-23 the warps' maxima of the state; 24, 25 the
-  // chunk's largest value; 32-47 the warps' maxima of keys
+  // chunk's largest value; 32-47 the warps' maxima of the keys
   volatile float* const fmisc = reinterpret_cast<volatile float*>(misc);
   volatile float* const ups = reinterpret_cast<volatile float*>(sb + PL::oUp);
 
