@@ -393,7 +393,8 @@ SDV_API sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const 
  * A row that sees nothing, and every row i >= n_rows[b], gives out = 0 and
  * lse = -inf.  A position that a row does not see has no effect on it, whatever
  * its keys and values hold (infinities and NaN among them), nor has anything
- * behind a sequence's last row.
+ * behind a sequence's last row.  An infinity or NaN among the values of a position
+ * that a row does see reaches the row, however small its weight.
  *   q: [B][S] rows of [Hq][dim]; query head h reads cache head h / (Hq / heads).
  *   mask_or_null: device uint32 [B][S].  A draft tree (sdv_tree_accept) is the
  *   mask of each node's ancestors and itself, a pad node's word is 0.

@@ -172,25 +172,72 @@ struct AttnWalk {
   }
 };
 
+// What is not finite among the values of some positions: the sum of infinities and NaN is
+// told by which of them there are.
+constexpr uint32_t kOddPlus = 1, kOddMinus = 2, kOddNan = 4;
+__device__ __forceinline__ float odd_value(uint32_t odd) {
+  if ((odd & kOddNan) || (odd & (kOddPlus | kOddMinus)) == (kOddPlus | kOddMinus)) return __int_as_float(0x7fc00000);
+  return odd & kOddPlus ? INFINITY : odd & kOddMinus ? -INFINITY : 0.f;
+}
+
+// x times a softmax factor.  ODD: an infinity or NaN stays what it is, as the factor is
+// above 0 if not in 32 bits.
+template <bool ODD>
+__device__ __forceinline__ float weighted(float x, float f) {
+  return !ODD || fabsf(x) < INFINITY ? x * f : x;
+}
+
 // Softmax sums of four columns, partial by partial (m: reference maximum in the log2
 // domain, l and o relative to it; a partial that saw nothing is (-inf, 0)).
 struct AttnSum {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  template <bool ODD>
   __device__ __forceinline__ void add(float m2, float l2, const float4& x) {
     if (m2 == -INFINITY && l2 == 0.f) return;
     const float mn = fmaxf(m, m2), f = exp2f(m - mn), f2 = exp2f(m2 - mn);
     m = mn;
     l = l * f + l2 * f2;
-    o.x = o.x * f + x.x * f2;
-    o.y = o.y * f + x.y * f2;
-    o.z = o.z * f + x.z * f2;
-    o.w = o.w * f + x.w * f2;
+    o.x = weighted<ODD>(o.x, f) + weighted<ODD>(x.x, f2);
+    o.y = weighted<ODD>(o.y, f) + weighted<ODD>(x.y, f2);
+    o.z = weighted<ODD>(o.z, f) + weighted<ODD>(x.z, f2);
+    o.w = weighted<ODD>(o.w, f) + weighted<ODD>(x.w, f2);
+  }
+  __device__ __forceinline__ bool finite() const {
+    return fabsf(o.x) < INFINITY && fabsf(o.y) < INFINITY && fabsf(o.z) < INFINITY && fabsf(o.w) < INFINITY;
   }
   __device__ __forceinline__ float lse() const {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 };
+
+// The partials of CTAs from .. to of a unit that CTA `first` begins, in their order, eight
+// loads in flight; ml and po at the row (and columns) in slot 0, whose steps follow.
+template <bool ODD>
+__device__ __forceinline__ AttnSum attn_sum_parts(const float2* ml, const float4* po, int ml_step, size_t po_step,
+                                                  int first, int from, int to) {
+  AttnSum sum;
+  for (int c = from; c <= to; c += 8) {
+    float2 s[8];
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s[k] = make_float2(-INFINITY, 0.f);
+      if (c + k <= to) {
+        const size_t slot = 2 * (size_t)(c + k) + (c + k == first);
+        s[k] = __ldcg(ml + slot * ml_step);
+        x[k] = __ldcg(po + slot * po_step);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum.add<ODD>(s[k].x, s[k].y, x[k]);
+  }
+  return sum;
+}
+static __device__ __noinline__ AttnSum attn_sum_odd_parts(const float2* ml, const float4* po, int ml_step,
+                                                          size_t po_step, int first, int from, int to) {
+  return attn_sum_parts<true>(ml, po, ml_step, po_step, first, from, to);
+}
 
 // Visibility word of window row i (bit j: window position j), 0 for a dead row.
 __device__ __forceinline__ uint32_t attn_word(const AttnArgs& a, int b, int i, int n) {

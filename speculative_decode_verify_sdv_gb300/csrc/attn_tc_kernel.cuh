@@ -37,7 +37,10 @@
 // fills zeros.  In tiles that reach past the context V is cleaned in shared memory
 // before P V: what the last page holds behind the end becomes zeros, and a window
 // row's infinities and NaN are zeroed and noted, then added at the end to the rows
-// that do see them -- 0 * inf would otherwise reach the others.
+// that do see them -- 0 * inf would otherwise reach the others.  Every row sees the
+// context, but in 16 bits with weights that may be 0 (spread rows: are 0 in three copies
+// of four), so there too 0 * inf makes NaN what is an infinity: an output that is not
+// finite makes the warp look at the segment's values themselves.
 //
 // Measured, a call: one token over 500,000 positions of 8 heads of 128: 290 us, 7.1 TB/s
 // of cache; 48 sequences of up to 16,000: 92 us, 6.0 TB/s.  What shorter calls add is the
@@ -94,7 +97,7 @@ struct AttnPlan {
   static constexpr int kSlot = TK * D * 2;
   static constexpr int kNumBars = 2 * kMaxSlots + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;  // the last for alignment
   static constexpr int kMerge = SPREAD ? kMergeBytes + 4 * kSpreadRows * 8 + kSpreadRows * 4 : 0;
-  static constexpr int kSmall = 2 * D * 4 + kNumBars * 8 + 2 * (int)sizeof(AttnSegment) + 16 + kMerge;
+  static constexpr int kSmall = 2 * D * 4 + kNumBars * 8 + 2 * (int)sizeof(AttnSegment) + 32 + kMerge;
   static constexpr int kS = 0;       // tensor-memory columns: two score tiles (P inside),
   static constexpr int kO = 2 * TK;  // then the output
   static_assert(kO + D <= 512, "tensor memory");
@@ -123,6 +126,48 @@ __device__ __noinline__ float poison_of(const AttnArgs& a, const int32_t* trow, 
     sum += (float)static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d];
   }
   return sum;
+}
+
+// The infinities and NaN of positions from .. to - 1 of the context, by the whole warp in
+// 16-byte loads: lane l gets columns 8 (l % (D / 8)) .. + 7, four bits each.
+template <typename T, int D>
+__device__ __noinline__ uint32_t odd_columns(const AttnArgs& a, const int32_t* trow, int h, int from, int to) {
+  constexpr int C = D / 8;
+  const int lane = threadIdx.x & 31;
+  uint32_t odd = 0;
+#pragma unroll 4
+  for (int p = from + lane / C; p < to; p += 32 / C) {
+    const int id = __ldg(trow + p / a.page);
+    if (id < 0 || id >= a.n_pages) continue;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.v) +
+                          (((long long)id * a.Hkv + h) * a.page + p % a.page) * C + lane % C);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      if (!(nonfinite16<T>(xs[z >> 1]) >> (z & 1) & 1)) continue;
+      const float y = z & 1 ? unpack16<T>(xs[z >> 1]).y : unpack16<T>(xs[z >> 1]).x;
+      odd |= (y != y ? kOddNan : y > 0.f ? kOddPlus : kOddMinus) << (4 * z);
+    }
+  }
+#pragma unroll
+  for (int off = C; off < 32; off <<= 1) odd |= __shfl_xor_sync(0xffffffffu, odd, off);
+  return odd;
+}
+// Whether one of N floats is not finite: 0 times it is NaN then, and so is the sum.
+template <int N>
+__device__ __forceinline__ bool any_odd(const uint32_t* x) {
+  f32x2 sum[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = pair2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < N; e += 2)
+    sum[e / 2 & 3] = fma2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair2(0.f, 0.f), sum[e / 2 & 3]);
+  const float2 a = unpair2(sum[0]), b = unpair2(sum[1]), c = unpair2(sum[2]), d = unpair2(sum[3]);
+  return ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y)) != 0.f;
+}
+// Of column d, from the lane that has it.
+__device__ __forceinline__ uint32_t odd_of(uint32_t odd, int d) {
+  return __shfl_sync(0xffffffffu, odd, d >> 3) >> (4 * (d & 7)) & 7u;
 }
 
 // Visibility of 32 positions from p on: context positions, the window's by `word`.
@@ -164,9 +209,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t pv_done = bars + 8u * (kB + 8), drain = pv_done + 8, rows_met = pv_done + 16;
   uint32_t* const poison = reinterpret_cast<uint32_t*>(sp);  // [2][D]
   AttnSegment* const segs = reinterpret_cast<AttnSegment*>(sp + 2 * D * 4 + PL::kNumBars * 8);
-  // tmem base, poison seen [2], shared units: arrivals made and whether this was the last
+  // tmem base, poison seen [2], shared units: arrivals made and whether this was the last;
+  // spread rows: 1 + the last segment with an output that is not finite
   volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);
-  float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 4));
+  float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 8));
   float2* const mstat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + kMergeBytes);  // [4][32]
   uint32_t* const mword = reinterpret_cast<uint32_t*>(mstat + 4 * kSpreadRows);
   const int nq = SPREAD ? 4 : (a.row_tile + 31) / 32;  // softmax warps with rows
@@ -195,7 +241,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_desc(&maps.v);
   }
   for (int e = threadIdx.x; e < 2 * D; e += kAttnThreads) poison[e] = 0;
-  if (threadIdx.x < 3) misc[1 + threadIdx.x] = 0;
+  if (threadIdx.x < 4) misc[1 + threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -572,6 +618,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!pv_wait(i)) break;  // every warp has delivered its last P: it is past the last segment's merge
       tc_fence_after();
       const bool poisoned = misc[1 + (sg & 1)] != 0;  // noted before the P that this P V waited for
+      const int ctx0 = min(tile0 * TK, ctx), ctx1 = min((tile0 + count) * TK, ctx);  // the segment's part of the context
+      uint32_t odd = 0;  // what is not finite there, once looked at
+      bool looked = false;
       if constexpr (SPREAD) {
         // Merge the four copies: M = max m_q, out = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q,
         // in rounds of the columns that the merge buffer holds.
@@ -587,6 +636,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_ld32(tq + PL::kO + j0 + j, o);
             if (j + 32 < now) tmem_ld32(tq + PL::kO + j0 + j + 32, o + 32);
             tmem_wait_ld();
+            if (live && l > 0.f && (any_odd<32>(o) || (j + 32 < now && any_odd<32>(o + 32)))) misc[4] = sg + 1;
             if (lane < nr) {
               float4* const dst = reinterpret_cast<float4*>(merge + (quarter * a.row_tile + lane) * pad + j);
 #pragma unroll
@@ -596,8 +646,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
           if (!meet()) break;
-          for (int e = quarter * 32 + lane; e < nr * (now / 4); e += 128) {
-            const int rr = e / (now / 4), j = e % (now / 4) * 4;
+          if (misc[4] == sg + 1 && !looked) {
+            odd = odd_columns<T, D>(a, trow, h, ctx0, ctx1);
+            looked = true;
+          }
+          for (int e0 = quarter * 32; e0 < nr * (now / 4); e0 += 128) {
+            const int e = e0 + lane, j = e % (now / 4) * 4;
+            uint32_t odd4 = 0;  // of the thread's columns, which are in one lane's word
+            if (looked) odd4 = __shfl_sync(0xffffffffu, odd, (j0 + j) >> 3) >> (4 * (j & 7));
+            if (e >= nr * (now / 4)) continue;
+            const int rr = e / (now / 4);
             float mq[4], lq = 0.f, mo = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -618,6 +676,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               x.z = fmaf(f, y.z, x.z);
               x.w = fmaf(f, y.w, x.w);
             }
+            if (odd4 & 7u) x.x = odd_value(odd4);
+            if (odd4 >> 4 & 7u) x.y = odd_value(odd4 >> 4);
+            if (odd4 >> 8 & 7u) x.z = odd_value(odd4 >> 8);
+            if (odd4 >> 12 & 7u) x.w = odd_value(odd4 >> 12);
             if (poisoned) {
               const int d = j0 + j;
               const uint32_t see = mword[rr];
@@ -662,22 +724,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + rr;
               const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)j * a.row_tile + rr;
               const size_t step = (size_t)(D / 4) * a.row_tile;
-              AttnSum sum;
-              for (int k0 = first; k0 <= last; k0 += 8) {
-                float2 sx[8];
-                float4 ox[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  sx[k] = make_float2(-INFINITY, 0.f);
-                  if (k0 + k <= last) {
-                    const size_t from = 2 * (size_t)(k0 + k) + (k0 + k == first);
-                    sx[k] = __ldcg(ml + from * a.row_tile);
-                    ox[k] = __ldcg(po + from * step);
-                  }
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum.add(sx[k].x, sx[k].y, ox[k]);
-              }
+              AttnSum sum = attn_sum_parts<false>(ml, po, a.row_tile, step, first, first, last);
+              if (!sum.finite()) sum = attn_sum_odd_parts(ml, po, a.row_tile, step, first, first, last);
               const int rw = r0 + rr, rs = small_div(rw, inv_g);
               const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
               const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
@@ -710,9 +758,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
         for (int j = 0; j < D; j += OC) {
           uint32_t o[OC];
+#pragma unroll 1
+          for (bool again = false;; again = true) {
 #pragma unroll
-          for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
-          tmem_wait_ld();
+            for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
+            tmem_wait_ld();
+            if (again || !__any_sync(0xffffffffu, live && l > 0.f && any_odd<OC>(o))) break;
+            if (!looked) odd = odd_columns<T, D>(a, trow, h, ctx0, ctx1);
+            looked = true;
+#pragma unroll 1
+            for (int d = j; d < j + OC; ++d) {
+              const uint32_t kind = odd_of(odd, d);
+              if (kind == 0) continue;
+              const uint32_t bits = poisoned ? pois[d] & word : 0u;
+              const float x = odd_value(kind) + (bits ? poison_of<T>(a, trow, h, ctx, bits, d) : 0.f);
+              __syncwarp();
+              tmem_st1(tq + PL::kO + d, __float_as_uint(x));
+            }
+            tmem_wait_st();
+          }
           if (r >= nr) continue;
           if (final) {
             uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);

@@ -64,12 +64,29 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
 
 // ---- CUDA-core attention --------------------------------------------------------------
 
+// The sum of what is not finite in column d of the values that a row sees among positions
+// from .. to - 1 (`word`: its window positions).
+template <typename T>
+__device__ __noinline__ float attn_odd_sum(const AttnArgs& a, int b, int h, int ctx, int from, int to, uint32_t word,
+                                           int d) {
+  float sum = 0.f;
+  for (int p = from; p < to; ++p) {
+    if (p >= ctx && !(word >> (p - ctx) & 1u)) continue;
+    const int id = __ldg(a.table + (size_t)b * a.max_pages + p / a.page);
+    if (id < 0 || id >= a.n_pages) continue;
+    const float x = to_float(static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d]);
+    if (!(fabsf(x) < INFINITY)) sum += x;
+  }
+  return sum;
+}
+
 // One CTA walks its range of tiles (attn_sched.cuh) with 8 query rows per tile.
 // Positions come 32 at a time through shared memory; a warp holds the running
 // maximum and sum of two rows, each thread the outputs of up to two columns of
 // all rows.  It is the form for head sizes and page sizes outside the tensor-core
-// kernel's; a position a row does not see has weight zero and is skipped, so
-// nothing its values hold reaches the row.  Its arithmetic bounds it: 8 sequences of 4000
+// kernel's; a position a row does not see has weight -0 and is skipped, so nothing its
+// values hold reaches the row.  A weight of +0 times an infinity makes the sum NaN, and
+// an output that is not finite is then told from the values themselves.  Its arithmetic bounds it: 8 sequences of 4000
 // positions, 32 heads over 8 of 96: 474 us for one row each (0.2 TB/s of cache), 3.3 ms
 // for 17; the tensor-core kernel at heads of 128 takes 38 and 52.
 template <typename T>
@@ -150,7 +167,7 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const float mn = fmaxf(m[i], mx);
         const float ref = mn == -INFINITY ? 0.f : mn;
-        const float e = see ? exp2f(s - ref) : 0.f;
+        const float e = see ? exp2f(s - ref) : -0.f;
         const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - ref);
         float sum = e;
 #pragma unroll
@@ -173,7 +190,7 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float e = ps[r * P + j];
-            if (e != 0.f) o[c][r] = fmaf(e, x, o[c][r]);
+            if (__float_as_uint(e) != 0x80000000u) o[c][r] = fmaf(e, x, o[c][r]);
           }
         }
       }
@@ -190,6 +207,14 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
     for (int r = 0; r < R; ++r) {
       if (r >= nr) break;
       const int row = r0 + r;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = tid + 128 * c;
+        if (d < D && !(fabsf(o[c][r]) < INFINITY) && al[r] > 0.f) {
+          const float odd = attn_odd_sum<T>(a, w.b, h, w.seq.ctx, w.tile * P, min((w.tile + count) * P, total), words[r], d);
+          if (!(fabsf(odd) < INFINITY)) o[c][r] = odd;
+        }
+      }
       if (starts && ends) {
         const long long orow = ((long long)w.b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
         const float inv = al[r] > 0.f ? 1.f / al[r] : (al[r] == 0.f ? 0.f : al[r]);
@@ -263,28 +288,15 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
     const float4* const po = reinterpret_cast<const float4*>(a.part_o) + (size_t)d4 * a.row_tile + r;
     const size_t step = (size_t)(a.D / 4) * a.row_tile;
     const int per = (c1 - c0 + kJoinParts) / kJoinParts, from = c0 + part * per, to = min(from + per - 1, c1);
-    for (int c = from; c <= to; c += 8) {
-      float2 s[8];
-      float4 x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s[k] = make_float2(-INFINITY, 0.f);
-        if (c + k <= to) {
-          const size_t slot = 2 * (size_t)(c + k) + (c + k == c0);
-          s[k] = __ldcg(ml + slot * a.row_tile);
-          x[k] = __ldcg(po + slot * step);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum.add(s[k].x, s[k].y, x[k]);
-    }
+    sum = attn_sum_parts<false>(ml, po, a.row_tile, step, c0, from, to);
+    if (!sum.finite()) sum = attn_sum_odd_parts(ml, po, a.row_tile, step, c0, from, to);
   }
   so[part][item] = sum.o;
   sml[part][item] = make_float2(sum.m, sum.l);
   __syncthreads();
   if (part != 0 || !mine) return;
 #pragma unroll
-  for (int j = 1; j < kJoinParts; ++j) sum.add(sml[j][item].x, sml[j][item].y, so[j][item]);
+  for (int j = 1; j < kJoinParts; ++j) sum.add<true>(sml[j][item].x, sml[j][item].y, so[j][item]);
   const int row = r0 + r;
   const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
   const bool none = sum.l == 0.f;
