@@ -28,8 +28,10 @@
 //
 // The reference maximum moves only when it grows by more than 2^8 (the sum and
 // output stay exact relative to it), so O in tensor memory is rescaled rarely.
-// P carries a factor 2^6: with it the weights down to 2^-20 of the row's largest
-// stay in fp16's normal range, and 2^14 is the most it can reach.  Rounding P to
+// fp16's P carries a factor 2^6: with it the weights down to 2^-20 of the row's largest
+// stay in the normal range, and 2^14 is the most it can reach.  bf16's, with the range of
+// fp32, carries 2^-8 and never passes 1: values up to 2^128 are then added up without
+// overflow where a plain sum of weights up to 1 is.  Rounding P to
 // the 16-bit type is the one rounding inside the sum (the sum l takes P before
 // it); it is what a matrix instruction on 16-bit values needs.
 //
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int TK = PL::TK;
   constexpr int CW = SPREAD ? TK / 4 : TK;  // score columns of a softmax warp
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr float kLift = kBf16 ? -8.f : 6.f;  // P's power of two
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const sb = smem_raw + (base - raw);
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        const float ref = m == -INFINITY ? -6.f : m - 6.f;
+        const float ref = m == -INFINITY ? -kLift : m - kLift;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < CW; j += 2) {
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!ok) break;
       const bool starts = tile0 == 0, final = starts && ends;
       const size_t slot = 2 * (size_t)blockIdx.x + (starts ? 1 : 0);
-      const float mm = m == -INFINITY ? -INFINITY : m - 6.f;
+      const float mm = m == -INFINITY ? -INFINITY : m - kLift;
       if (!pv_wait(i)) break;  // every warp has delivered its last P: it is past the last segment's merge
       tc_fence_after();
       const bool poisoned = misc[1 + (sg & 1)] != 0;  // noted before the P that this P V waited for

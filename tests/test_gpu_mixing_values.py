@@ -108,3 +108,15 @@ def test_odd_values_of_the_context_and_of_the_window(sdv, dt, d, page, S, hq, hk
     ref = mixing.attention(f64(q), f64(kp), f64(clean), table.tolist(), [ctx], [S], None, d ** -0.5)
     check_odd(dt, ref, out, lse, d, {0: INF, 1: -INF}, slice(0, j))
     check_odd(dt, ref, out, lse, d, {0: NAN, 1: -INF, 2: INF}, slice(j, None))
+
+
+@pytest.mark.parametrize("d,page,S,hq,hkv,ctx", [(128, 16, 1, 8, 2, 613), (64, 16, 5, 8, 2, 300), (256, 64, 17, 16, 2, 777),
+                                                 (128, 64, 1, 8, 1, 9000), (40, 16, 3, 4, 2, 500)])
+@pytest.mark.parametrize("std", [0.0, 1.7])
+def test_values_close_to_the_largest_of_the_type(sdv, d, page, S, hq, hkv, ctx, std):
+    # a mean of values is no larger than they are: 2^120 in bf16 stays finite
+    q, kp, vp, table = att.make(BF16, 1, S, hq, hkv, d, page, [ctx], [S], 92, std=std)
+    vp = (vp.float() * 2.0 ** 116).to(BF16)
+    out, lse, _ = att.call(sdv, q, kp, vp, table, [ctx], [S], None, d ** -0.5)
+    ref = mixing.attention(f64(q), f64(kp), f64(vp), table.tolist(), [ctx], [S], None, d ** -0.5)
+    att.check(BF16, ref, out, lse, d)
