@@ -410,7 +410,10 @@ SDV_API sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64
                           const uint32_t* mask_or_null, float scale, void* out, float* lse_or_null,
                           void* ws, size_t ws_bytes, sdv_stream_t stream);
 
-/* Workspace bytes of sdv_paged_attn on the current device; 0 for invalid arguments. */
+/*
+ * Workspace bytes of sdv_paged_attn on the current device, for windows of up to S
+ * rows; 0 for invalid arguments.
+ */
 SDV_API size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim);
 
 /*

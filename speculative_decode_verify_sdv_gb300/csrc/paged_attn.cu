@@ -380,6 +380,24 @@ size_t part_bytes(int ctas, int row_tile, int D) {
 
 constexpr int kSimplePerSm = 2;
 
+// What a call of S rows needs; 0 for invalid arguments.
+size_t attn_need(int B, int S, int Hq, int heads, int dim) {
+  if (B < 1 || S < 1 || S > kMaxWindow || heads < 1 || Hq < 1 || Hq % heads != 0 || dim < 8 || dim % 8 != 0 ||
+      dim > kMaxDim || heads > kMaxHeads || Hq > kMaxHeads)
+    return 0;
+  const int sms = sdv::sm_count();
+  AttnArgs a{};
+  a.S = S;
+  a.G = Hq / heads;
+  a.rows = S * a.G;
+  // the larger of the two kernels' needs: which one runs depends on the page size too
+  set_rows(a, sdv::kAttnSimpleRows);
+  const size_t simple = part_bytes(kSimplePerSm * (sms > 0 ? sms : 256), a.row_tile, dim);
+  set_window_rows(a);
+  const size_t tc = part_bytes(sms > 0 ? sms : 256, a.row_tile, dim);
+  return sdv::kHeaderBytes + (simple > tc ? simple : tc);
+}
+
 }  // namespace
 
 extern "C" {
@@ -416,20 +434,13 @@ sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const void* v,
 }
 
 size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim) {
-  if (B < 1 || S < 1 || S > kMaxWindow || heads < 1 || Hq < 1 || Hq % heads != 0 || dim < 8 || dim % 8 != 0 ||
-      dim > kMaxDim || heads > kMaxHeads || Hq > kMaxHeads)
-    return 0;
-  const int sms = sdv::sm_count();
-  AttnArgs a{};
-  a.S = S;
-  a.G = Hq / heads;
-  a.rows = S * a.G;
-  // the larger of the two kernels' needs: which one runs depends on the page size too
-  set_rows(a, sdv::kAttnSimpleRows);
-  const size_t simple = part_bytes(kSimplePerSm * (sms > 0 ? sms : 256), a.row_tile, dim);
-  set_window_rows(a);
-  const size_t tc = part_bytes(sms > 0 ? sms : 256, a.row_tile, dim);
-  return sdv::kHeaderBytes + (simple > tc ? simple : tc);
+  size_t most = attn_need(B, S, Hq, heads, dim);
+  // shorter windows too: a row tile has fewer rows where a second one begins
+  for (int s = 1; most != 0 && s < S; ++s) {
+    const size_t need = attn_need(B, s, Hq, heads, dim);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
@@ -444,7 +455,7 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
     return SDV_ERR_INVALID_ARG;
   if (S > kMaxWindow || cache->dim > kMaxDim || Hq > kMaxHeads || (long long)B * Hq * S > kMaxUnits)
     return SDV_ERR_UNSUPPORTED;
-  const size_t need = sdv_paged_attn_workspace_bytes(B, S, Hq, cache->heads, cache->dim);
+  const size_t need = attn_need(B, S, Hq, cache->heads, cache->dim);
   if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
   AttnArgs a{};
   a.q = q;

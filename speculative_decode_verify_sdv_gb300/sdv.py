@@ -487,7 +487,7 @@ def quantize(w: torch.Tensor, bits: int) -> QWeight:
 
 
 def paged_attn_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
-    """A zero-filled workspace for sdv_paged_attn calls of this shape (q [B, S, Hq, dim])."""
+    """A zero-filled workspace for sdv_paged_attn calls of up to S rows of this shape (q [B, S, Hq, dim])."""
     B, S, hq, dim = q.shape
     nbytes = max(sdv_paged_attn_workspace_bytes(B, S, hq, k_pages.shape[1], dim), 256)
     return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
