@@ -444,7 +444,10 @@ SDV_API sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const v
                            const float* state_in_or_null, float* state_out_or_null, void* o_or_null,
                            void* ws, size_t ws_bytes, sdv_stream_t stream);
 
-/* Workspace bytes of sdv_linear_attn on the current device; 0 for invalid arguments. */
+/*
+ * Workspace bytes of sdv_linear_attn on the current device, for up to B sequences of
+ * up to T tokens; 0 for invalid arguments.
+ */
 SDV_API size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv);
 
 /*

@@ -172,7 +172,8 @@ extern "C" {
 
 size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv) {
   if (!sdv::lin_shape(B, T, H, Dk, Dv) || !sdv::lin_limits(B, H, Dk, Dv)) return 0;
-  if (!sdv::lin_chunked(B, T, H, Dk, Dv)) return sdv::kHeaderBytes;
+  // (also where a prompt is too long for the chunked form: shorter ones fit its workspace)
+  if (!sdv::linear_tc_takes(Dk, Dv) || T <= sdv::kLinWindow) return sdv::kHeaderBytes;
   const int sms = sdv::sm_count();
   return sdv::kHeaderBytes + sdv::lin_notes(B, H) + sdv::lin_parts(sms > 0 ? sms : 256, Dk, Dv);
 }
@@ -195,7 +196,8 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
       !std::isfinite(scale))
     return SDV_ERR_INVALID_ARG;
   if (!lin_limits(B, H, Dk, Dv)) return SDV_ERR_UNSUPPORTED;
-  const size_t need = sdv_linear_attn_workspace_bytes(B, T, H, Dk, Dv);
+  const bool chunked = lin_chunked(B, T, H, Dk, Dv);
+  const size_t need = chunked ? sdv_linear_attn_workspace_bytes(B, T, H, Dk, Dv) : kHeaderBytes;
   if (ws == nullptr || !is_aligned16(ws) || ws_bytes < need) return SDV_ERR_WORKSPACE;
   LinArgs a{};
   a.q = q_or_null;
@@ -219,7 +221,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
   a.o = o_or_null;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (lin_window(T, Dk, Dv, a.o != nullptr, a.s_out != nullptr)) return status_of(launch_linear_window(dtype, a, st));
-  if (lin_chunked(B, T, H, Dk, Dv)) {
+  if (chunked) {
     a.ctas = sm_count();
     if (a.ctas <= 0) return SDV_ERR_CUDA;
     char* const w8 = static_cast<char*>(ws);

@@ -494,7 +494,8 @@ def paged_attn_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Te
 
 
 def linear_attn_workspace(k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
-    """A zero-filled workspace for sdv_linear_attn calls of this shape (k [B, T, Hqk, Dk], v [B, T, H, Dv])."""
+    """A zero-filled workspace for sdv_linear_attn calls of this shape and of fewer tokens or sequences
+    (k [B, T, Hqk, Dk], v [B, T, H, Dv])."""
     B, T = k.shape[:2]
     nbytes = max(sdv_linear_attn_workspace_bytes(B, T, v.shape[2], k.shape[3], v.shape[3]), 256)
     return torch.zeros(nbytes, dtype=torch.uint8, device=k.device)

@@ -3,6 +3,7 @@ shorter one of the same heads, so a program allocates once for its largest."""
 import pytest
 import torch
 
+from tests import test_gpu_linear_attn as lin
 from tests import test_gpu_paged_attn as att
 
 
@@ -35,3 +36,25 @@ def test_one_workspace_serves_shorter_windows(sdv, hq, hkv, dim, page, most, sho
         want, _, _ = att.call(sdv, part, kp, vp, table, ctx, [S], None, 0.1)
         got, _, _ = att.call(sdv, part, kp, vp, table, ctx, [S], None, 0.1, ws=ws)
         assert torch.equal(got, want) and sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+
+
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 2, 128, 128), (40, 7, 64, 64), (300, 4096, 64, 128), (2, 3, 96, 128)])
+def test_linear_prompts_fit_the_longest_ones_workspace(sdv, B, H, dk, dv):
+    lengths = [1, 6, 31, 32, 33, 128, 129, 3000, 100000, 2 ** 22, 2 ** 25, 2 ** 30, 2 ** 31 - 1]
+    sizes = [sdv.sdv_linear_attn_workspace_bytes(B, T, H, dk, dv) for T in lengths]
+    assert sizes == sorted(sizes) and sizes[0] >= 256
+    more = [sdv.sdv_linear_attn_workspace_bytes(b, 5000, H, dk, dv) for b in (1, 2, 100, 5000, 65535)]
+    assert more == sorted(more)
+
+
+@pytest.mark.gpu
+def test_one_workspace_serves_shorter_prompts(sdv):
+    big = lin.make(torch.bfloat16, 3, 900, 4, 2, 128, 64, 2)
+    ws = sdv.linear_attn_workspace(big[1], big[2])
+    for B, T in ((3, 130), (1, 900), (2, 33), (3, 8), (1, 1)):
+        q, k, v, g, s = lin.make(torch.bfloat16, B, T, 4, 2, 128, 64, 3)
+        want, want_s = lin.call(sdv, q, k, v, g, None, s)
+        o, state = torch.empty_like(want), torch.empty_like(want_s)
+        sdv.sdv_linear_attn(q, k, v, g, 0.3, None, s, state, o, ws)
+        assert torch.equal(o, want) and torch.equal(state, want_s)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
