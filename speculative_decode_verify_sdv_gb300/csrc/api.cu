@@ -496,6 +496,7 @@ bool moe_args_ok(const sdv_qweight* gate, const sdv_qweight* up, const sdv_qweig
 
 namespace sdv {
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+DebugFault debug_fault() { return DebugFault{g_debug_wait_ns.load(), g_debug_withhold.load()}; }
 }  // namespace sdv
 
 extern "C" {

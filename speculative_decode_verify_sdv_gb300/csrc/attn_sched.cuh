@@ -47,6 +47,7 @@ struct AttnArgs {
   int* status;
   int ctas;                 // CTAs of the attention launch
   int slots, q_bufs;        // tensor-core kernel: ring slots, Q buffers
+  DebugFault fault;         // its timeout path's test hook: a tile whose keys are never asked for
 };
 
 // Bytes of arrivals in the workspace's header, which alone is zero between calls of

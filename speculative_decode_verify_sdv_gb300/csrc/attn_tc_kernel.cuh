@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* const poison = reinterpret_cast<uint32_t*>(sp);  // [2][D]
   AttnSegment* const segs = reinterpret_cast<AttnSegment*>(sp + 2 * D * 4 + PL::kNumBars * 8);
   // tmem base, poison seen [2], shared units: arrivals made and whether this was the last;
-  // spread rows: 1 + the last segment with an output that is not finite
+  // spread rows: 1 + the last segment with an output that is not finite; at the end: tiles
+  // asked for, keys and values
   volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);
   float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 8));
   float2* const mstat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + kMergeBytes);  // [4][32]
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok) ok = mbar_wait_warp(bar, parity, a.status);
+    if (ok) ok = mbar_wait_warp(bar, parity, a.status, a.fault.wait_ns);
     return ok;
   };
   // P V products complete in tile order.  Each role that needs them waits for every
@@ -268,6 +269,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // segment s is in Q buffer and note s % q_bufs
   auto seg_buf = [&](int s) { return q_bufs == 2 ? s & 1 : 0; };
   auto seg_parity = [&](int s) { return (q_bufs == 2 ? s >> 1 : s) & 1; };
+  int asked = 0;  // a producer's tiles, warp 7's segments: copies that may be in flight
+  bool closed = false;  // warp 7: the note behind the last segment is out
 
   if (warp == 0 || warp == 6) {
     // ---- producers: the warp's tile i takes ring place 2i (keys) or 2i + 1 (values) ----
@@ -306,10 +309,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           ids[k] = t + 4 < end ? page_of(t + 4) : -1;
           const int y = id >= 0 && id < a.n_pages ? (id * a.Hkv + h) * a.page + (p & (a.page - 1)) : beyond;
           if (use > 0 && !await(empty(slot), (use - 1) & 1)) break;
-          if (lane == 0) mbar_arrive_expect_tx(full(slot), PL::kSlot);
-          __syncwarp();
-          if (mine)
-            tma_load_2d(dst + slot * PL::kSlot, values ? &maps.v : &maps.k, cb * 64, y, full(slot), policy);
+          if (values || ++asked != a.fault.withhold) {
+            if (lane == 0) mbar_arrive_expect_tx(full(slot), PL::kSlot);
+            __syncwarp();
+            if (mine)
+              tma_load_2d(dst + slot * PL::kSlot, values ? &maps.v : &maps.k, cb * 64, y, full(slot), policy);
+          }
+          asked += values;
           slot += 2;
           if (slot >= NS) {
             slot -= NS;
@@ -321,26 +327,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       w.advance(a, count);
       more = w.more();
     }
-    // After a timeout the copies whose consumers gave up have to land before the CTA
-    // ends (otherwise their consumers have seen them): the places of the last pass
-    // before the next one.
-    if (!ok)
-      for (int back = 2; back <= 2 * NS; back += 2) {
-        int s = slot - back, u = use;
-        while (s < 0) {
-          s += NS;
-          --u;
-        }
-        if (u < 0) break;
-        mbar_wait_bounded(full(s), u & 1, kAttnDrainNs);
-      }
+    if (lane == 0) misc[5 + values] = asked;
   } else if (warp == 7) {
     // ---- segments: Q by TMA, and what the others need to know ----
     AttnWalk start;
     const int page_log = 31 - __clz(a.page);
     const uint64_t policy = l2_policy_normal();
     constexpr int kCopies = SPREAD ? 4 : 1;
-    uint32_t staged = 0;  // segments whose Q was asked for
     bool more = start.start(a, blockIdx.x, lane);
     AttnWalk w = start;
     for (int sg = 0;; ++sg) {
@@ -352,6 +345,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           g.count = 0;
           mbar_arrive(q_full(buf));
         }
+        closed = true;
         break;
       }
       const int count = w.segment();
@@ -387,11 +381,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane < kCopies * PL::kBlocks)  // rows past n_rows or S: whatever lies there, for rows that give 0
         tma_load_3d(base + buf * q_step + (lane / kCopies) * q_block + lane % kCopies * 4096, &maps.q,
                     lane / kCopies * 64, h * a.G, w.b * a.S + rt * a.tile_wrows, q_full(buf), policy);
-      ++staged;
+      ++asked;
       w.advance(a, count);
       more = w.more();
     }
-    if (!ok && staged > 0) mbar_wait_bounded(q_full(seg_buf(staged - 1)), seg_parity(staged - 1), kAttnDrainNs);
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
     constexpr uint32_t id_pv = idesc_16_f32(kBf16, 128, D, false, true);
@@ -817,10 +810,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc_fence_before();
     }
   }
+  __syncwarp();
+  tmem_wait_st();  // (of a role that gave up behind its stores)
   tc_fence_before();
-  if (__syncthreads_or(!ok) && a.shared != nullptr && warp == 0) {
-    // After a timeout: the arrivals that were not made, so that the counts are back at 0
-    // when every CTA has ended.
+  const bool dead = __syncthreads_or(!ok);
+  // After a timeout, whichever role met it, copies may be in flight that nobody has waited
+  // for: they have to land before the CTA ends.
+  if (dead && (warp == 0 || warp == 6)) {
+    const int other = misc[warp == 0 ? 6 : 5];
+    for (int i = max(asked - NS, 0); i < asked; ++i) {
+      const int place = 2 * i + (warp == 6), next = place + NS;  // a place is taken again once its copy was read
+      if (next / 2 < (next % 2 == place % 2 ? asked : other)) continue;
+      if (warp == 0 && i + 1 == a.fault.withhold) continue;
+      mbar_wait_bounded(full(place % NS), (place / NS) & 1, kAttnDrainNs);
+    }
+  }
+  if (dead && warp == 7) {
+    for (int s = max(asked - q_bufs + closed, 0); s < asked; ++s)
+      mbar_wait_bounded(q_full(seg_buf(s)), seg_parity(s), kAttnDrainNs);
+  }
+  if (dead && a.shared != nullptr && warp == 0) {
+    // the arrivals that were not made, so that the counts are back at 0 when every CTA has ended
     AttnWalk w;
     int made = misc[3] >> 1;
     for (bool more = w.start(a, blockIdx.x, lane); more; more = w.more()) {

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
-    if (ok) ok = mbar_wait_warp(b, parity, a.status);
+    if (ok) ok = mbar_wait_warp(b, parity, a.status, 0);
     return ok;
   };
   auto arrive = [&](uint32_t b) {

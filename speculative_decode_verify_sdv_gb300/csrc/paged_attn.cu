@@ -480,6 +480,7 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   a.out = out;
   a.lse = lse_or_null;
   a.status = static_cast<int*>(ws);
+  a.fault = sdv::debug_fault();
   const int sms = sdv::sm_count();
   if (sms <= 0) return SDV_ERR_CUDA;
   const bool tc = sdv::attn_tc_takes(a.D, a.G, a.page, (long long)a.n_pages * a.Hkv * a.page);

@@ -129,19 +129,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // A bounded wait by a whole warp, in few instructions: the roles of one kernel share
 // the SM's instruction cache, so what follows a first look in vain is one function for
-// all of them.  On expiry the status word is set.
-static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, int* status) {
+// all of them.  On expiry the status word is set.  limit_ns 0: the built-in limit.
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, int* status, uint64_t limit_ns) {
+  if (limit_ns == 0) limit_ns = kWaitLimitNs;
   const uint64_t t0 = global_timer_ns();
   do {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  } while (__all_sync(0xffffffffu, global_timer_ns() - t0 < kWaitLimitNs));
+  } while (__all_sync(0xffffffffu, global_timer_ns() - t0 < limit_ns));
   if ((threadIdx.x & 31) == 0) atomicOr(status, 1 /* kDevErrTimeout */);
   return false;
 }
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status);
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status, limit_ns);
 }
 
 // Four bytes into shared memory behind the thread's back, zeros where `real` is false.
