@@ -504,7 +504,8 @@ SDV_API int32_t sdv_set_gemm_path(int32_t path);
  * Test hook of the timeout path (process-wide; every later launch of the
  * tcgen05 path uses it until it is reset with (-1, 0)).  withhold_stage >= 0:
  * in every CTA the weight copy of that stage of the CTA's stage sequence (the
- * tensor-core attention: the keys' copy of that one of its tiles) is
+ * tensor-core attention: the keys' copy of that one of its tiles; the chunked
+ * linear attention: of that one of its chunks) is
  * never issued, so the roles waiting for it give up after the wait limit
  * -- a wait on a barrier that nothing completes, with no copy in flight behind
  * it; the kernel then drains what it issued, writes undefined outputs and sets

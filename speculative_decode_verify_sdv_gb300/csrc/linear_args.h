@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "sdv_kernels.h"
+
 namespace sdv {
 
 // A sum of log2 decays as a pair of floats (48 bits).
@@ -58,6 +60,7 @@ struct LinArgs {
   int* status;
   int ctas;
   int pass;                // 0: local states, 1: outputs and final states
+  DebugFault fault;        // the timeout path's test hook: a chunk whose keys are never asked for
 };
 
 struct LinMaps {

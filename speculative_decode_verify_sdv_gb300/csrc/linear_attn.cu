@@ -226,6 +226,7 @@ sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const void* k, 
     if (a.ctas <= 0) return SDV_ERR_CUDA;
     char* const w8 = static_cast<char*>(ws);
     a.status = reinterpret_cast<int*>(w8);
+    a.fault = debug_fault();
     a.repair = reinterpret_cast<int*>(w8 + kHeaderBytes);
     a.part = reinterpret_cast<float*>(w8 + kHeaderBytes + lin_notes(B, H));
     a.part_in = a.part + (size_t)a.ctas * Dk * Dv;

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
-    if (ok) ok = mbar_wait_warp(b, parity, a.status, 0);
+    if (ok) ok = mbar_wait_warp(b, parity, a.status, a.fault.wait_ns);
     return ok;
   };
   auto arrive = [&](uint32_t b) {
@@ -307,13 +307,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   const bool any = from.start(a, blockIdx.x, lane);
   LinWalk w = from;
   int i = 0;  // the CTA's chunk number
+  int asked_k = 0, asked_q = 0, asked_v = 0;  // of the TMA warp
 
   if (warp == 0) {
     // ---- TMA ----
     const uint64_t normal = l2_policy_normal();
     const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
     const int shared = a.H / a.Hqk;
-    int asked_k = 0, asked_q = 0, asked_v = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count(), hk = w.h / shared;
       const int z0 = w.b * a.T + w.chunk * kLC;
@@ -321,11 +321,12 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         const int z = z0 + c * kLC;
         // the product with K~ that took the place of the keys before in this buffer
         if (OUT ? !upd_wait(i - 1) : i >= 2 && !await(v_free(i), phase(i - 2))) break;
-        if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
-        __syncwarp();
-        if (lane < DK / 64)
-          tma_load_3d(k_buf(i) + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
-        ++asked_k;
+        if (++asked_k != a.fault.withhold) {
+          if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
+          __syncwarp();
+          if (lane < DK / 64)
+            tma_load_3d(k_buf(i) + lane * 16384, &maps.k, lane * 64, hk, z, k_full(i), normal);
+        }
         if (OUT) {
           if (i > 0 && (!await(qm_done, (i - 1) & 1) || (kScaled && !await(q_read, (i - 1) & 1)))) break;
           if (lane == 0) mbar_arrive_expect_tx(q_full, PL::kK);
@@ -343,11 +344,6 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       }
       if (!ok) break;
       w.advance(a, count);
-    }
-    if (!ok) {  // copies whose consumers gave up have to land before the CTA ends
-      for (int e = max(asked_k - 2, 0); e < asked_k; ++e) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
-      for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
-      if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
     }
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
@@ -464,6 +460,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       if (a.pass == 0 && lane == 0) a.parts[blockIdx.x].decay = run;
       w.advance(a, count);
     }
+    cp_async_wait<0>();
   } else if (warp == 3) {
     // ---- the values: zeros behind the end, the largest ----
     for (bool more = any; ok && more; more = w.more()) {
@@ -1002,8 +999,17 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       w.advance(a, count);
     }
   }
+  __syncwarp();
+  tmem_wait_st();  // (of a role that gave up behind its stores)
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok) && warp == 0) {
+    // After a timeout, whichever role met it, copies may be in flight that nobody has waited
+    // for: they have to land before the CTA ends.
+    for (int e = max(asked_k - 2, 0); e < asked_k; ++e)
+      if (e + 1 != a.fault.withhold) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
+    for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
+    if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tm, 512);

@@ -10,6 +10,7 @@ its shared units among them), and the next call on that workspace is the one bef
 import pytest
 import torch
 
+from tests import test_gpu_linear_attn as lin
 from tests import test_gpu_paged_attn as att
 from tests.test_gpu_paged_attn import BF16, F16
 from tests.test_gpu_timeout import fault
@@ -49,3 +50,33 @@ def test_attention_timeout_reported_then_next_call_correct(sdv, dt, B, S, hq, hk
     for _ in range(2):
         got, _, _ = att.call(sdv, q, kp, vp, table, ctx, n, None, d ** -0.5, ws=ws)
         assert torch.equal(got, want) and sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+
+
+@pytest.mark.parametrize("stage", [0, 1, 3])
+@pytest.mark.parametrize("dt,B,T,H,hqk,dk,dv,parts", [
+    (F16, 1, 5000, 8, 4, 128, 128, "both"),             # heads that many CTAs share: both launches
+    (BF16, 2, 3000, 30, 10, 64, 128, "both"),
+    (F16, 3, 100, 60, 60, 64, 64, "both"),              # one chunk a head: the second launch alone
+    (BF16, 2, 4000, 24, 24, 128, 64, "state"),
+    (F16, 2, 4000, 24, 24, 128, 128, "outputs")])
+def test_linear_timeout_reported_then_next_call_correct(sdv, dt, B, T, H, hqk, dk, dv, parts, stage):
+    q, k, v, g, s = lin.make(dt, B, T, H, hqk, dk, dv, 71, rate=0.01)
+    want, want_s = lin.call(sdv, q, k, v, g, None, s)
+    ws = sdv.linear_attn_workspace(k, v)
+
+    def call():
+        o = torch.full_like(want, float("nan")) if parts != "state" else None
+        state = torch.full_like(want_s, float("nan")) if parts != "outputs" else None
+        sdv.sdv_linear_attn(q, k, v, g, 0.3, None, s, state, o, ws)
+        return o, state, sdv.sdv_last_device_status(ws)
+
+    with fault(sdv, stage):
+        status = call()[2]
+    if stage == 0 or B * H * (-(-T // 128)) > 152 * (stage + 1):
+        assert status == sdv.SDV_ERR_TIMEOUT
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK and not ws[:256].any()
+    for _ in range(2):
+        o, state, status = call()
+        assert status == sdv.SDV_OK
+        assert o is None or torch.equal(o, want)
+        assert state is None or torch.equal(state, want_s)
