@@ -72,7 +72,7 @@ namespace sdv {
 namespace {
 
 constexpr int kAttnThreads = 256;
-constexpr int kAttnSmem = 232448;                // all of an SM's: one CTA, one tensor-memory allocation
+constexpr int kAttnSmem = 232448 - kWaitLimitBytes;  // all of an SM's: one CTA, one tensor-memory allocation
 constexpr uint64_t kAttnDrainNs = 100000000ull;  // 0.1 s: in-flight work at teardown
 constexpr int kMaxSlots = 8;
 constexpr int kSpreadRows = 32;                  // rows that can stand four times in the MMA tile
@@ -213,8 +213,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* const poison = reinterpret_cast<uint32_t*>(sp);  // [2][D]
   AttnSegment* const segs = reinterpret_cast<AttnSegment*>(sp + 2 * D * 4 + PL::kNumBars * 8);
   // tmem base, poison seen [2], shared units: arrivals made and whether this was the last;
-  // spread rows: 1 + the last segment with an output that is not finite; at the end: tiles
-  // asked for, keys and values
+  // spread rows: 1 + the last segment with an output that is not finite
   volatile uint32_t* const misc = reinterpret_cast<uint32_t*>(segs + 2);
   float* const merge = const_cast<float*>(reinterpret_cast<volatile float*>(misc + 8));
   float2* const mstat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + kMergeBytes);  // [4][32]
@@ -226,6 +225,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
+    set_wait_limit(a.fault);
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok) ok = mbar_wait_warp(bar, parity, a.status, a.fault.wait_ns);
+    if (ok) ok = mbar_wait_warp(bar, parity, a.status);
     return ok;
   };
   // P V products complete in tile order.  Each role that needs them waits for every
@@ -269,8 +269,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // segment s is in Q buffer and note s % q_bufs
   auto seg_buf = [&](int s) { return q_bufs == 2 ? s & 1 : 0; };
   auto seg_parity = [&](int s) { return (q_bufs == 2 ? s >> 1 : s) & 1; };
-  int asked = 0;  // a producer's tiles, warp 7's segments: copies that may be in flight
-  bool closed = false;  // warp 7: the note behind the last segment is out
 
   if (warp == 0 || warp == 6) {
     // ---- producers: the warp's tile i takes ring place 2i (keys) or 2i + 1 (values) ----
@@ -283,6 +281,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int cb = lane % PL::kBlocks, chunk = lane / PL::kBlocks;
     const bool mine = chunk < chunks;
     const uint32_t dst = ring + cb * (TK * 128) + chunk * box * 128;
+    int asked = 0;  // tiles
     int slot = values ? 1 : 0, use = 0;  // ring place: slot, and how often the ring has been passed
     bool more = first.start(a, blockIdx.x, lane);
     AttnWalk w = first;
@@ -327,13 +326,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       w.advance(a, count);
       more = w.more();
     }
-    if (lane == 0) misc[5 + values] = asked;
+    // The copies into places that are not taken again have to land before the CTA ends,
+    // whoever else gives up waiting for them, and when: those in the ring's last NS places, or,
+    // if it is this warp that gave up, any of its last (one whose place the other producer
+    // has taken since had landed; the wait for it runs out).
+    for (int i = max(asked - NS, 0); i < asked; ++i) {
+      const int place = 2 * i + values;
+      if ((ok && place < 2 * asked - NS) || (!values && i + 1 == a.fault.withhold)) continue;
+      mbar_wait_bounded(full(place % NS), (place / NS) & 1, kAttnDrainNs);
+    }
   } else if (warp == 7) {
     // ---- segments: Q by TMA, and what the others need to know ----
     AttnWalk start;
     const int page_log = 31 - __clz(a.page);
     const uint64_t policy = l2_policy_normal();
     constexpr int kCopies = SPREAD ? 4 : 1;
+    int asked = 0;        // segments
+    bool closed = false;  // the note behind the last one is out, in the buffer of one that has been read
     bool more = start.start(a, blockIdx.x, lane);
     AttnWalk w = start;
     for (int sg = 0;; ++sg) {
@@ -385,6 +394,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       w.advance(a, count);
       more = w.more();
     }
+    for (int s = max(asked - q_bufs + closed, 0); s < asked; ++s)  // as the producers do
+      mbar_wait_bounded(q_full(seg_buf(s)), seg_parity(s), kAttnDrainNs);
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
     constexpr uint32_t id_pv = idesc_16_f32(kBf16, 128, D, false, true);
@@ -753,12 +764,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         constexpr int OC = D < 128 ? D : 128;  // columns at once
 #pragma unroll 1
         for (int j = 0; j < D; j += OC) {
-          uint32_t o[OC];
+          // written first, so that the look at them hides behind the stores; again if they were odd
 #pragma unroll 1
           for (bool again = false;; again = true) {
+            uint32_t o[OC];
 #pragma unroll
             for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
             tmem_wait_ld();
+            if (r < nr && final) {
+              uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);
+#pragma unroll
+              for (int e = 0; e < OC; e += 8) {
+                uint32_t y[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  y[z] = none ? 0u : pack16<T>(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+                dst[e / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else if (r < nr) {
+              float4* const dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + j / 4) * a.row_tile + r;
+#pragma unroll
+              for (int e = 0; e < OC; e += 4)
+                dst[(e / 4) * a.row_tile] = live ? make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                               __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             if (again || !__any_sync(0xffffffffu, live && l > 0.f && any_odd<OC>(o))) break;
             if (!looked) odd = odd_columns<T, D>(a, trow, h, ctx0, ctx1);
             looked = true;
@@ -772,25 +802,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tmem_st1(tq + PL::kO + d, __float_as_uint(x));
             }
             tmem_wait_st();
-          }
-          if (r >= nr) continue;
-          if (final) {
-            uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);
-#pragma unroll
-            for (int e = 0; e < OC; e += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                y[z] = none ? 0u : pack16<T>(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
-              dst[e / 8] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          } else {
-            float4* const dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + j / 4) * a.row_tile + r;
-#pragma unroll
-            for (int e = 0; e < OC; e += 4)
-              dst[(e / 4) * a.row_tile] = live ? make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                             __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]))
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
         if (r < nr) {
@@ -813,24 +824,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncwarp();
   tmem_wait_st();  // (of a role that gave up behind its stores)
   tc_fence_before();
-  const bool dead = __syncthreads_or(!ok);
-  // After a timeout, whichever role met it, copies may be in flight that nobody has waited
-  // for: they have to land before the CTA ends.
-  if (dead && (warp == 0 || warp == 6)) {
-    const int other = misc[warp == 0 ? 6 : 5];
-    for (int i = max(asked - NS, 0); i < asked; ++i) {
-      const int place = 2 * i + (warp == 6), next = place + NS;  // a place is taken again once its copy was read
-      if (next / 2 < (next % 2 == place % 2 ? asked : other)) continue;
-      if (warp == 0 && i + 1 == a.fault.withhold) continue;
-      mbar_wait_bounded(full(place % NS), (place / NS) & 1, kAttnDrainNs);
-    }
-  }
-  if (dead && warp == 7) {
-    for (int s = max(asked - q_bufs + closed, 0); s < asked; ++s)
-      mbar_wait_bounded(q_full(seg_buf(s)), seg_parity(s), kAttnDrainNs);
-  }
-  if (dead && a.shared != nullptr && warp == 0) {
-    // the arrivals that were not made, so that the counts are back at 0 when every CTA has ended
+  if (__syncthreads_or(!ok) && a.shared != nullptr && warp == 0) {
+    // After a timeout: the arrivals that were not made, so that the counts are back at 0
+    // when every CTA has ended.
     AttnWalk w;
     int made = misc[3] >> 1;
     for (bool more = w.start(a, blockIdx.x, lane); more; more = w.more()) {

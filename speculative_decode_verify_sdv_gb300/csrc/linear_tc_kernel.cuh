@@ -124,7 +124,7 @@ struct LinPlan {
   static constexpr int oUp = oMisc + 256;         // the rows' powers of two [2][128]
   static constexpr int kTotal = oUp + 2 * kLC * 4 + 1024;  // the base is aligned to 1024
   static constexpr int cS = 0, cO = 128, cU = 256, cM = 384;  // tensor-memory columns
-  static_assert(kTotal <= 232448, "shared memory");
+  static_assert(kTotal <= 232448 - kWaitLimitBytes, "shared memory");
 };
 
 // A CTA's way through its range of chunks; all lanes of a warp keep the same.  The host
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
+    set_wait_limit(a.fault);
     for (int i = 0; i < 10; ++i)
       if (i != 1) mbar_init(bar(i), 1);
     mbar_init(upd_done(0), 1);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
-    if (ok) ok = mbar_wait_warp(b, parity, a.status, a.fault.wait_ns);
+    if (ok) ok = mbar_wait_warp(b, parity, a.status);
     return ok;
   };
   auto arrive = [&](uint32_t b) {
@@ -307,13 +308,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   const bool any = from.start(a, blockIdx.x, lane);
   LinWalk w = from;
   int i = 0;  // the CTA's chunk number
-  int asked_k = 0, asked_q = 0, asked_v = 0;  // of the TMA warp
 
   if (warp == 0) {
     // ---- TMA ----
     const uint64_t normal = l2_policy_normal();
     const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
     const int shared = a.H / a.Hqk;
+    int asked_k = 0, asked_q = 0, asked_v = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count(), hk = w.h / shared;
       const int z0 = w.b * a.T + w.chunk * kLC;
@@ -345,6 +346,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       if (!ok) break;
       w.advance(a, count);
     }
+    // The last copies have to land before the CTA ends, whoever else gives up waiting for
+    // them, and when.  (The same behind the block's barrier, for dead CTAs alone, made a
+    // prompt 3 % slower.)
+    for (int e = max(asked_k - 2, 0); e < asked_k; ++e)
+      if (e + 1 != a.fault.withhold) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
+    for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
+    if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
   } else if (warp == 1) {
     // ---- MMA: every lane keeps the same state, one elected lane issues ----
     constexpr uint32_t id_qk = idesc_16_f32(kBf16, 128, kLC, false, false);
@@ -1002,14 +1010,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   __syncwarp();
   tmem_wait_st();  // (of a role that gave up behind its stores)
   tc_fence_before();
-  if (__syncthreads_or(!ok) && warp == 0) {
-    // After a timeout, whichever role met it, copies may be in flight that nobody has waited
-    // for: they have to land before the CTA ends.
-    for (int e = max(asked_k - 2, 0); e < asked_k; ++e)
-      if (e + 1 != a.fault.withhold) mbar_wait_bounded(k_full(e), (e >> 1) & 1, kLinDrainNs);
-    for (int e = max(asked_v - PL::kBufs, 0); e < asked_v; ++e) mbar_wait_bounded(v_full(e), phase(e), kLinDrainNs);
-    if (asked_q > 0) mbar_wait_bounded(q_full, (asked_q - 1) & 1, kLinDrainNs);
-  }
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tm, 512);

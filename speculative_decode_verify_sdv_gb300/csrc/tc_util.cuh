@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "sdv_device.cuh"
+#include "sdv_kernels.h"
 
 namespace sdv {
 
@@ -129,20 +130,29 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // A bounded wait by a whole warp, in few instructions: the roles of one kernel share
 // the SM's instruction cache, so what follows a first look in vain is one function for
-// all of them.  On expiry the status word is set.  limit_ns 0: the built-in limit.
-static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, int* status, uint64_t limit_ns) {
-  if (limit_ns == 0) limit_ns = kWaitLimitNs;
+// all of them.  On expiry the status word is set.  The limit stands in shared memory,
+// where one thread has put it before the block's first barrier: as an argument it cost a
+// prompt of linear attention 2 % and a window's attention 3 %.
+constexpr int kWaitLimitBytes = 16;  // of static shared memory
+__device__ __forceinline__ volatile uint64_t& wait_limit_ns() {
+  __shared__ alignas(kWaitLimitBytes) volatile uint64_t limit;
+  return limit;
+}
+__device__ __forceinline__ void set_wait_limit(const DebugFault& f) {
+  wait_limit_ns() = f.wait_ns != 0 ? f.wait_ns : kWaitLimitNs;
+}
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, int* status) {
   const uint64_t t0 = global_timer_ns();
   do {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  } while (__all_sync(0xffffffffu, global_timer_ns() - t0 < limit_ns));
+  } while (__all_sync(0xffffffffu, global_timer_ns() - t0 < wait_limit_ns()));
   if ((threadIdx.x & 31) == 0) atomicOr(status, 1 /* kDevErrTimeout */);
   return false;
 }
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status, limit_ns);
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_on(bar, parity, status);
 }
 
 // Four bytes into shared memory behind the thread's back, zeros where `real` is false.
