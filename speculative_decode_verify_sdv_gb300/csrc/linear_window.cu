@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
   __shared__ float sp[kWin][kWin + 1];        // decayed scores
   __shared__ DecaySum sg[kWin];
   __shared__ float smax[kWarps];
-  __shared__ float ssum[(kParts - 1) * kWin * DV];  // the other parts' sums
+  __shared__ alignas(16) float ssum[(kParts - 1) * kWin * DV];  // the other parts' sums
   griddep_wait();
   const int h = blockIdx.x, b = blockIdx.y, hk = h / (a.H / a.Hqk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
