@@ -98,3 +98,48 @@ def linear(q, k, v, g, scale, n, state):
                     o[b, t, h] = scale * (q[b, t, h // r] @ m[b, h])
                     oa[b, t, h] = abs(scale) * (np.abs(q[b, t, h // r]) @ ma[b, h])
     return {"o": o, "state": m, "o_abs": oa, "state_abs": ma}
+
+
+def linear_squares(q, k, v, g, scale, n, state, chunk):
+    """Per output the sum of squares of what may be rounded to 16 bits on its way: the
+    decayed scores' terms inside the token's chunk, the terms of the state at the chunk's
+    start, and the output.  Arguments as for ``linear`` (g above -inf); also returns o."""
+    B, T, H, dv = v.shape
+    r = H // k.shape[2]
+    out, squares = np.zeros((B, T, H, dv)), np.zeros((B, T, H, dv))
+    for b in range(B):
+        for h in range(H):
+            m = state[b, h].astype(np.float64)
+            for t in range(0, n[b], chunk):
+                at = slice(t, min(t + chunk, n[b]))
+                qc, kc, vc = q[b, at, h // r], k[b, at, h // r], v[b, at, h]
+                run = np.cumsum(np.minimum(g[b, at, h], 0.0))
+                p = np.tril(qc @ kc.T * np.exp(np.minimum(run[:, None] - run[None, :], 0.0)))
+                dec = np.exp(run)[:, None]
+                o = scale * (p @ vc + dec * (qc @ m))
+                out[b, at, h] = o
+                squares[b, at, h] = scale ** 2 * ((p * p) @ (vc * vc) + dec ** 2 * ((qc * qc) @ (m * m))) + o * o
+                m = np.exp(run[-1]) * m + (kc * np.exp(run[-1] - run)[:, None]).T @ vc
+    return out, squares
+
+
+def attention_squares(q, k_pages, v_pages, table, ctx, n, mask, scale):
+    """Per output of ``attention`` the sum of squares of its weights' terms and of itself."""
+    B, S, hq, d = q.shape
+    hkv = k_pages.shape[1]
+    g = hq // hkv
+    squares = np.zeros((B, S, hq, d))
+    for b in range(B):
+        for h in range(hkv):
+            k = rows_of_cache(k_pages, table[b], h, ctx[b] + n[b])
+            v = rows_of_cache(v_pages, table[b], h, ctx[b] + n[b])
+            for i in range(n[b]):
+                at = list(range(ctx[b])) + [ctx[b] + j for j in seen(i, n[b], None if mask is None else mask[b][i])]
+                if not at:
+                    continue
+                for e in range(g):
+                    s = k[at] @ q[b, i, h * g + e] * scale
+                    w = np.exp(s - s.max())
+                    w = w / w.sum()
+                    squares[b, i, h * g + e] = (w * w) @ (v[at] * v[at]) + (w @ v[at]) ** 2
+    return squares
