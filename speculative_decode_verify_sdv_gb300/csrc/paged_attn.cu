@@ -491,11 +491,14 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   // and 104.4)
   a.lead = tc ? 2 : 1;
   a.ctas = tc ? sms : kSimplePerSm * sms;
-  // Shared units are joined by their last CTA where a partial is at most 4 KB (single
-  // tokens): the GPU's time a call hardly changes (613 positions, 8 heads: 9.8 and
-  // 10.0 us) and the host issues one launch less (8.1 against 6.6 us).  Larger ones go
-  // to the join's many CTAs.
-  if (tc && a.row_tile * a.D <= 1024 && a.ctas <= sdv::kAttnSharedBytes)
+  // Shared units are joined by their last CTA where a partial is at most 2 KB (single
+  // tokens), larger ones by a launch of many CTAs.  GPU us a call, launch against last CTA,
+  // fp16, 8 cache heads: one sequence of 613, 5000 and 30,000 positions, then 48 of 40 to
+  // 15,550.  4 rows x 128 (512 elements): 10.9 to 10.7, 15.2 to 16.5, 29.5 to 31.3, 236 to
+  // 233, and the host issues one launch less (8.1 against 6.6 us).  8 x 128 (1024): 11.6 to
+  // 12.9, 15.9 to 22.1, 30.0 to 36.9, 240 to 235; 4 x 256: 12.6 to 14.8, 19.3 to 23.3, 47.0
+  // to 52.0, 454 to 448.  16 x 128 (2048): 12.5 to 16.0, 17.0 to 28.9, 30.9 to 44.2, 247 to 239.
+  if (tc && a.row_tile * a.D <= 512 && a.ctas <= sdv::kAttnSharedBytes)
     a.shared = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kAttnSharedAt);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
   a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
