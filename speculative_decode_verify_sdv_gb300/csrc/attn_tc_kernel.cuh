@@ -848,7 +848,10 @@ cudaError_t attn_tc_launch(const AttnMaps& m, AttnArgs a, cudaStream_t st) {
   using PL = AttnPlan<D, SPREAD>;
   auto kernel = attn_tc_kernel<T, D, SPREAD>;
   // two Q buffers where they cost the ring nothing (spread rows: two sets of up to 16
-  // in the buffer of 128), or leave it five slots (two and a half tiles)
+  // in the buffer of 128), or leave it five slots (two and a half tiles).  One buffer against
+  // two, bf16, 4 cache heads, 64 sequences of 700 positions and one of 30,000: 128 rows x 128,
+  // five slots left: 101.9 to 100.0 us and 25.3 to 25.6; 96 rows: 83.2 to 81.1 and 24.3 to
+  // 24.5; 64 rows x 256, four slots left: 115 to 114 and 33.0 to 32.7, within the noise.
   a.q_bufs = SPREAD ? (a.row_tile <= 16 ? 2 : 1) : PL::slots(a.row_tile, 2) >= 5 ? 2 : 1;
   a.slots = PL::slots(a.row_tile, a.q_bufs);
   // more than half an SM's: one CTA and one tensor-memory allocation per SM

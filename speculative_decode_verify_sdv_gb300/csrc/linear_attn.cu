@@ -26,7 +26,9 @@ __device__ __forceinline__ void lin_round(float x, __nv_bfloat16& y) { y = __flo
 // access per warp and a thread has R 16-byte loads in flight.  Reading and writing
 // the state bounds it for one token (4096 heads of 128 x 128: 540 MB in 95.9 us,
 // 5.6 TB/s; 32 heads: 9.9 us, the call itself); the outputs' sum over the key rows
-// crosses the warps through shared memory.
+// crosses the warps through shared memory.  At 64 value columns half of each warp has no
+// column: 4096 heads of 128 x 64 take 69 us, 3.9 TB/s, where 64 x 128 takes 50, 5.4 TB/s;
+// with 256 key rows 4.7 TB/s.
 constexpr int kRecWarps = 8;
 constexpr int kRecTokens = 8;  // tokens staged at once
 
@@ -141,15 +143,31 @@ size_t lin_notes(int B, int H) { return round_256((size_t)B * H * 4); }
 size_t lin_parts(int ctas, int Dk, int Dv) { return (size_t)ctas * (sizeof(LinPart) + 2 * (size_t)Dk * Dv * 4); }
 
 // Which form (head sizes of 64 and 128; others are the recurrent form's, as one token is).
-// Microseconds, recurrent against window form, 512 heads of 128 x 128 and 32 of them, for
-// outputs and state: 31.4 to 33.4 and 12.9 to 15.0 at 6 tokens, 33.4 to 33.4 and 15.0 to
-// 15.0 at 7, 55.9 to 41.6 and 25.2 to 17.1 at 17; outputs alone: 17.0 to 21.2 and 8.9 to
-// 10.9 at 2 tokens, 21.3 to 20.5 and 10.9 to 10.9 at 4; the state alone: 21.1 to 21.2 and
-// 8.9 to 8.9 at 2, 23.2 to 21.1 and 10.9 to 8.9 at 4.  Window against chunked form: 48.8 to
-// 59.0 and 18.1 to 23.2 at 32, the window form's most.
-int lin_window_from(bool outputs, bool state) { return outputs && state ? 7 : outputs ? 4 : 2; }
+// The recurrent form's time grows with the tokens, the window form's with the state: the
+// tokens from which the latter is the faster one depend on what a call computes and on the
+// state's proportions.  GPU us, recurrent against window form, 512 heads and 4096 of them,
+// fp16 (bf16 is within 5 %):
+//   128 x 128  both     6: 25.6 to 29.1, 169 to 190   8: 29.9 to 29.9, 197 to 194
+//              outputs  3: 14.5 to 15.2,  94 to 87    4: 15.8 to 15.3, 103 to 88
+//              state    2: 15.7 to 15.8, 100 to 94    4: 18.9 to 16.5, 122 to 98
+//   128 x 64   both     4: 16.6 to 18.1, 108 to 100   5: 19.8 to 18.3, 129 to 101
+//              outputs  2:  9.8 to 9.5,   61 to 47
+//              state    2: 11.0 to 10.1,  69 to 50
+//   64 x 64    both     6: 11.1 to 12.1,  66 to 61    8: 12.8 to 12.5,  78 to 62
+//              outputs  3:  6.8 to 7.1,   38 to 32    4:  7.5 to 7.1,   43 to 32
+//              state    2:  6.2 to 6.1,   34 to 28
+//   64 x 128   both    10: 17.9 to 21.5, 106 to 132  13: 21.3 to 22.3, 126 to 136
+//              outputs  6: 10.9 to 12.3,  65 to 67    8: 12.7 to 12.2,  76 to 67
+//              state    2:  8.8 to 9.8,   50 to 51    4:  9.9 to 10.0,  58 to 53
+// Window against chunked form at 32 tokens, the window form's most (128 x 128, 512 heads and
+// 32): 48.8 to 59.0 and 18.1 to 23.2.
+int lin_window_from(int Dk, int Dv, bool outputs, bool state) {
+  if (outputs && state) return Dv < Dk ? 5 : Dv == Dk ? 7 : 12;
+  if (outputs) return Dv < Dk ? 2 : Dv == Dk ? 4 : 7;
+  return Dv <= Dk ? 2 : 3;
+}
 bool lin_window(int T, int Dk, int Dv, bool outputs, bool state) {
-  return linear_tc_takes(Dk, Dv) && T >= lin_window_from(outputs, state) && T <= kLinWindow;
+  return linear_tc_takes(Dk, Dv) && T >= lin_window_from(Dk, Dv, outputs, state) && T <= kLinWindow;
 }
 bool lin_chunked(int B, int T, int H, int Dk, int Dv) {
   // the tensor maps' coordinates and the split's arithmetic are 32-bit
