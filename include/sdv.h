@@ -433,6 +433,10 @@ SDV_API size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, 
  * One entry point serves a prompt (state_in NULL or zeros), a single token
  * (T == 1), the verify of a window (state_out NULL: the state stays as it is) and
  * its commit (o NULL, n_tokens = the accepted rows, on the device).
+ * Infinities and NaN among keys, values and states go where the formula takes them, up
+ * to a token whose decay is 0; a row whose query is not finite gives values that are not.
+ * What the decays of several tokens have taken below 2^-126 may count as dropped,
+ * infinities among it.
  * Dk, Dv: multiples of 8, 8 to 256.  H a multiple of Hqk.  Outputs and states do
  * not overlap the inputs otherwise.  The workspace is
  * sdv_linear_attn_workspace_bytes(...) bytes.

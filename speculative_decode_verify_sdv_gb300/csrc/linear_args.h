@@ -68,7 +68,8 @@ struct LinMaps {
 };
 
 constexpr int kLinChunk = 128;   // tokens of a chunk
-constexpr int kLinRuns = 16;     // CTAs that share one head at most
+constexpr int kLinRuns = 16;     // CTAs are 16 times the heads of all sequences at most (a long
+                                 // sequence among short ones may have more of them than that)
 
 constexpr int kLinWindow = 32;   // tokens of the window form at most
 
