@@ -10,8 +10,9 @@
 // U with rounded fp32 operations: added up inside the tensor cores over a long prompt it
 // was 5 times less exact.
 //
-// Precision.  M is a sum over all tokens, so its terms are kept to 22 (fp16) or 16
-// (bf16) bits: K~ goes into the product as high and low part.  P and the copy of M
+// Precision.  M is a sum over all tokens, so its terms are kept to 22 (fp16) or 24
+// (bf16) bits: K~ goes into the product as high and low part, of bf16 as three parts
+// (two left the state 3e-6 off where sums of fp32 are 4e-7).  P and the copy of M
 // that Q multiplies are rounded to the 16-bit type once, as the values of a matrix
 // instruction have to be.  fp16 has neither the range of scores nor of states nor of
 // decayed keys, so each carries a power of two: P one per row, M's copy one per chunk,
@@ -25,7 +26,7 @@
 //
 // Warp roles: 0 TMA; 1 MMA; 2 the decays; 3 the values' end and their largest; then the
 // state's (key rows of M: U, decay, 16-bit copy for Q M; four, or eight with outputs,
-// where the copy is waited for), the keys' (K~'s two parts, then the decay of Q M; eight,
+// where the copy is waited for), the keys' (K~'s parts, then the decay of Q M; eight,
 // or four with outputs), four for scores to P and four for outputs.  All of it runs in
 // rolled loops: sixteen warps of unrolled code were bound by the instruction cache (three
 // times as slow).
@@ -71,26 +72,32 @@ __device__ __forceinline__ uint32_t abs_max2(const uint4& x) {  // of 16-bit mag
   return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 }
 
-// A pair times f = fh + fl (each in both halves) as the 16-bit type's nearest (in place)
+// A pair of fp16 times f = fh + fl (each in both halves) as the type's nearest (in place)
 // and the rest: k fh rounds to h, the rest k fh - h is a value of the type and exact
-// (twice the type's bits less those of h), and k fl goes on top.
-template <typename T>
-__device__ __forceinline__ void split16(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo);
-template <>
-__device__ __forceinline__ void split16<__half>(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo) {
+// (twice the type's bits less those of h), and k fl goes on top: 22 bits.
+__device__ __forceinline__ void split16(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo) {
   asm("{\n\t.reg .b32 h, n, r;\n\t"
       "mul.rn.f16x2 h, %0, %2;\n\tneg.f16x2 n, h;\n\t"
       "fma.rn.f16x2 r, %0, %2, n;\n\tfma.rn.f16x2 %1, %0, %3, r;\n\tmov.b32 %0, h;\n\t}"
       : "+r"(x), "=&r"(lo)
       : "r"(fh), "r"(fl));
 }
-template <>
-__device__ __forceinline__ void split16<__nv_bfloat16>(uint32_t& x, uint32_t fh, uint32_t fl, uint32_t& lo) {
-  asm("{\n\t.reg .b32 h, n, r;\n\t"
-      "mul.rn.bf16x2 h, %0, %2;\n\tneg.bf16x2 n, h;\n\t"
-      "fma.rn.bf16x2 r, %0, %2, n;\n\tfma.rn.bf16x2 %1, %0, %3, r;\n\tmov.b32 %0, h;\n\t}"
-      : "+r"(x), "=&r"(lo)
-      : "r"(fh), "r"(fl));
+
+// A pair of bf16 times f in fp32 as three pairs of bf16, the first in place: each takes the
+// leading 8 bits of what is left, so the three are the product to its last bit, without a
+// conversion.
+__device__ __forceinline__ uint32_t upper_halves(f32x2 x) {
+  return __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+}
+__device__ __forceinline__ f32x2 without_upper(f32x2 x) {
+  return fma2(x & 0xffff0000ffff0000ull, pair2(-1.f, -1.f), x);
+}
+__device__ __forceinline__ void split3(uint32_t& x, f32x2 f, uint32_t& lo, uint32_t& third) {
+  const float2 k = unpack16<__nv_bfloat16>(x);
+  const f32x2 p = mul2(pair2(k.x, k.y), f), r = without_upper(p);
+  x = upper_halves(p);
+  lo = upper_halves(r);
+  third = upper_halves(without_upper(r));
 }
 
 __device__ __forceinline__ uint32_t mul16x2(uint32_t x, uint32_t y) {
@@ -105,14 +112,19 @@ struct LinTables {
   __device__ __forceinline__ DecaySum at(int t) const { return DecaySum{hi[t], lo[t]}; }
 };
 
-template <int DK, int DV, bool OUT>
+template <int DK, int DV, bool OUT, bool THIRD>
 struct LinPlan {
-  // Two buffers of keys, whose place K~'s high part then takes; the first launch, without
-  // queries, state copy and outputs, has room for two of its low part and of values too.
-  static constexpr int kBufs = OUT ? 1 : 2;
+  // Two buffers of keys, whose place K~'s high part then takes (one where its third part
+  // leaves room for no more); the first launch, without queries, state copy and outputs, has
+  // room for two of values too, and of the lower parts but where those are three of 128 wide.
+  static constexpr int kBufs = OUT ? 1 : 2;  // values
+  static constexpr int kLoBufs = OUT || (THIRD && DK == 128) ? 1 : 2;
+  static constexpr int kKeyBufs = OUT && THIRD && DK == 128 && DV == 128 ? 1 : 2;
   static constexpr int kThreads = OUT ? 768 : 512;
   static constexpr int kK = kLC * DK * 2, kV = kLC * DV * 2;
-  static constexpr int oK = 0, oLo = oK + 2 * kK, oV = oLo + kBufs * kK, oQ = oV + kBufs * kV;
+  static constexpr int oK = 0, oLo = oK + kKeyBufs * kK, o3 = oLo + kLoBufs * kK;
+  static constexpr int oZero = o3 + (THIRD ? kLoBufs * kK : 0);  // Dk = 64: the third part's lower half
+  static constexpr int oV = oZero + (THIRD && DK == 64 ? kK : 0), oQ = oV + kBufs * kV;
   static constexpr int oSt = oQ + (OUT ? kK : 0), oOut = oSt + (OUT ? 128 * DV * 2 : 0);
   static constexpr int oEx = oOut + (OUT ? 4 * 4096 : 0);  // Dk = 64: the state's low rows on their way to the high ones
   static constexpr int oTab = oEx + (DK == 64 ? (OUT ? 2 : 1) * 64 * 33 * 4 : 0);
@@ -197,10 +209,14 @@ struct LinWalk {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
+using LinPlanOf = LinPlan<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
+
+template <typename T, int DK, int DV, bool OUT>
+__global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
-  using PL = LinPlan<DK, DV, OUT>;
+  using PL = LinPlanOf<T, DK, DV, OUT>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kThird = kBf16;         // three parts of 8 bits make K~ as exact as fp32
   constexpr bool kScaled = !kBf16;       // powers of two beside fp16 operands
   constexpr bool kBound = OUT && kScaled;  // the largest value of a chunk bounds what it adds to M
   constexpr int kStateWarps = OUT ? 8 : 4, kKeyWarps = OUT ? 4 : 8;
@@ -215,11 +231,13 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
   const uint32_t q_full = bar(4), s_full = bar(6), qm_done = bar(7),
                  pv_done = bar(9), p_ready = bar(12), o_free = bar(13),
                  met = bar(14), met_m = bar(15), drain = bar(16), q_read = bar(23);
-  // lo parts and values per buffer; a barrier of two takes turns, another one's phase is the chunk
+  // values and lower parts per buffer; a barrier of two takes turns, another one's phase is the chunk
   auto buf = [&](int i) { return PL::kBufs == 2 ? i & 1 : 0; };
-  auto u_col = [&](int i) { return PL::kBufs == 2 && (i & 1) ? PL::cO : PL::cU; };
+  auto lo_at = [&](int i) { return base + PL::oLo + (PL::kLoBufs == 2 ? i & 1 : 0) * PL::kK; };
+  auto third_at = [&](int i) { return base + PL::o3 + (PL::kLoBufs == 2 ? i & 1 : 0) * PL::kK; };
+  auto u_col = [&](int i) { return !OUT && (i & 1) ? PL::cO : PL::cU; };
   auto phase = [&](int i) { return (uint32_t)(PL::kBufs == 2 ? i >> 1 : i) & 1u; };
-  auto k_buf = [&](int i) { return base + PL::oK + (i & 1) * PL::kK; };
+  auto k_buf = [&](int i) { return base + PL::oK + (PL::kKeyBufs == 2 ? i & 1 : 0) * PL::kK; };
   auto k_full = [&](int i) { return bar(24 + (i & 1)); };
   auto v_full = [&](int i) { return bar(26 + buf(i)); };
   auto v_free = [&](int i) { return bar(30 + buf(i)); };
@@ -273,6 +291,10 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
     if (OUT) tma_prefetch_desc(&maps.q);
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) misc[2 + threadIdx.x - 32] = 0;
+  if (kThird && DK == 64) {
+    for (int e = threadIdx.x; e < PL::kK / 16; e += PL::kThreads) sts128(base + PL::oZero + 16 * e, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       for (int c = 0; c < count; ++c, ++i) {
         const int z = z0 + c * kLC;
         // the product with K~ that took the place of the keys before in this buffer
-        if (OUT ? !upd_wait(i - 1) : i >= 2 && !await(v_free(i), phase(i - 2))) break;
+        if (OUT ? !upd_wait(i + 1 - PL::kKeyBufs) : i >= 2 && !await(v_free(i), phase(i - 2))) break;
         if (++asked_k != a.fault.withhold) {
           if (lane == 0) mbar_arrive_expect_tx(k_full(i), PL::kK);
           __syncwarp();
@@ -388,19 +410,23 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
       }
       if (!await(kv_ready(i), (i >> 1) & 1)) break;
       tc_fence_after();
-      // K~^T V: the low parts first; at Dk = 64 both at once (rows 0-63 from the high,
-      // 64-127 from the low part)
+      // K~^T V: the lowest parts first; at Dk = 64 high and low at once (rows 0-63 from the
+      // high, 64-127 from the low part), and before them the third part over zeros
+      const uint32_t lo = lo_at(i), third = third_at(i);
       if constexpr (DK == 128) {
-        const uint64_t hd = smem_desc_sw128(k_buf(i), 16384, 1024);
-        const uint64_t ld = smem_desc_sw128(base + PL::oLo + buf(i) * PL::kK, 16384, 1024);
+        const uint64_t hd = smem_desc_sw128(k_buf(i), 16384, 1024), ld = smem_desc_sw128(lo, 16384, 1024);
+        const uint64_t td = smem_desc_sw128(third, 16384, 1024);
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j)
-          tc_mma4_ss<128, 128>(tm + u_col(i), (j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up, j > 0);
+        for (int j = kThird ? -2 : 0; j < 4; ++j)
+          tc_mma4_ss<128, 128>(tm + u_col(i), (j < 0 ? td : j < 2 ? ld : hd) + (j & 1) * 512, vd + (j & 1) * 512, id_up,
+                               j > (kThird ? -2 : 0));
       } else {
-        const uint64_t bd = smem_desc_sw128(k_buf(i), base + PL::oLo + buf(i) * PL::kK - k_buf(i), 1024);
+        const uint64_t bd = smem_desc_sw128(k_buf(i), lo - k_buf(i), 1024);
+        const uint64_t td = smem_desc_sw128(third, base + PL::oZero - third, 1024);
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j)
-          tc_mma4_ss<128, 128>(tm + u_col(i), bd + j * 512, vd + j * 512, id_up, j > 0);
+        for (int j = kThird ? -2 : 0; j < 2; ++j)
+          tc_mma4_ss<128, 128>(tm + u_col(i), (j < 0 ? td : bd) + (j & 1) * 512, vd + (j & 1) * 512, id_up,
+                               j > (kThird ? -2 : 0));
       }
       tc_commit_elect(upd_done(i));
       if (!OUT) tc_commit_elect(v_free(i));
@@ -772,8 +798,8 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
         const float pw = exp2f((float)pre);
         const uint32_t up2 = pack16<T>(pw, pw);
         arrive(tab_free(i));
-        // the last product has read K~'s low part, Q K^T the keys
-        if (OUT && (!upd_wait(i) || !await(s_full, i & 1))) break;
+        // the last product has read K~'s lower parts, Q K^T the keys
+        if ((PL::kLoBufs == 1 && !upd_wait(i)) || (OUT && !await(s_full, i & 1))) break;
 #pragma unroll 1
         for (int h = u0; h < u0 + kUnits; h += 4) {  // four 16-byte units in flight
           const uint32_t blk = (h >> 3) * 16384;
@@ -789,15 +815,25 @@ __global__ void __launch_bounds__(LinPlan<DK, DV, OUT>::kThreads, 1)
               x[k].z = mul16x2(x[k].z, up2);
               x[k].w = mul16x2(x[k].w, up2);
             }
-            split16<T>(x[k].x, fh, fl, lo[k].x);
-            split16<T>(x[k].y, fh, fl, lo[k].y);
-            split16<T>(x[k].z, fh, fl, lo[k].z);
-            split16<T>(x[k].w, fh, fl, lo[k].w);
+            if constexpr (kThird) {
+              const f32x2 f2 = pair2(f, f);
+              uint4 third;
+              split3(x[k].x, f2, lo[k].x, third.x);
+              split3(x[k].y, f2, lo[k].y, third.y);
+              split3(x[k].z, f2, lo[k].z, third.z);
+              split3(x[k].w, f2, lo[k].w, third.w);
+              sts128(third_at(i) + blk + swz128(r, (h & 7) + k), third);
+              continue;
+            }
+            split16(x[k].x, fh, fl, lo[k].x);
+            split16(x[k].y, fh, fl, lo[k].y);
+            split16(x[k].z, fh, fl, lo[k].z);
+            split16(x[k].w, fh, fl, lo[k].w);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             sts128(kb + blk + swz128(r, (h & 7) + k), x[k]);
-            sts128(base + PL::oLo + buf(i) * PL::kK + blk + swz128(r, (h & 7) + k), lo[k]);
+            sts128(lo_at(i) + blk + swz128(r, (h & 7) + k), lo[k]);
           }
         }
         fence_proxy_async_smem();
@@ -1022,7 +1058,8 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
   auto kernel = linear_tc_kernel<T, DK, DV, OUT>;
   // more than half an SM's: one CTA and one tensor-memory allocation per SM
   constexpr int half = 232448 / 2 + 1024;
-  constexpr int smem = LinPlan<DK, DV, OUT>::kTotal > half ? LinPlan<DK, DV, OUT>::kTotal : half;
+  using PL = LinPlanOf<T, DK, DV, OUT>;
+  constexpr int smem = PL::kTotal > half ? PL::kTotal : half;
   static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1032,7 +1069,7 @@ cudaError_t linear_tc_launch(const LinMaps& m, const LinArgs& a, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3(a.ctas), dim3(LinPlan<DK, DV, OUT>::kThreads), smem, st, m, a);
+  return launch_pdl(kernel, dim3(a.ctas), dim3(PL::kThreads), smem, st, m, a);
 }
 
 }  // namespace
