@@ -334,7 +334,9 @@ SDV_API sdv_status sdv_moe_route(const float* router_logits, int32_t S, int32_t 
  * the products above ("Spec-decode on GDN hybrids (Qwen3.5/3.6 family) -- static-S
  * verify design", sections "Verify graph = STATIC S=K+1 + chunked GDN scan" and
  * "Hybrid state discipline": rejected drafts must leave no trace in a layer's
- * state).  Both 16-bit types are served; q, k, v and the outputs of one call share
+ * state).  The recurrent layers of those hybrids have a write strength and a delta term
+ * besides the decay, which this state does not: it is decayed and added to, no more.
+ * Both 16-bit types are served; q, k, v and the outputs of one call share
  * one type.  Sums, softmax statistics and states are fp32.
  *
  * Rows of q, k and v are given with a token stride in elements (a multiple of 8,

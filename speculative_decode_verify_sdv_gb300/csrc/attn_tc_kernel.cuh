@@ -44,10 +44,10 @@
 // of four), so there too 0 * inf makes NaN what is an infinity: an output that is not
 // finite makes the warp look at the segment's values themselves.
 //
-// Measured, a call: one token over 500,000 positions of 8 heads of 128: 290 us, 7.1 TB/s
-// of cache; 48 sequences of up to 16,000: 92 us, 6.0 TB/s.  What shorter calls add is the
+// Measured, a call: one token over 500,000 positions of 8 heads of 128: 291 us, 7.0 TB/s
+// of cache; 48 sequences of up to 16,000: 93 us, 5.9 TB/s.  What shorter calls add is the
 // start (4 us until the first tile is there: the walk, cold instructions, the first read)
-// and the end.  17 rows of 8 heads a cache head of 256 over 32,768 positions: 31.7 us,
+// and the end.  17 rows of 8 heads a cache head of 256 over 32,768 positions: 32.1 us,
 // 2.1 TB/s: 136 rows are two tiles, and a tile of 64 positions is 2100 cycles, of which
 // the MMAs' issue takes 1700 (S reads Q and K from shared memory, 6 KB for 64 cycles of
 // products).  One token over 613 positions: 10.9 us, all of it start and end.

@@ -35,14 +35,18 @@
 // finite make U so, its head is noted, its state left unwritten, and the recurrent
 // kernel, launched behind, recomputes noted heads by the definition.
 //
-// Measured: 8192 tokens, 32 heads of 128 x 128 (16 of queries and keys), fp16: 133 us a
-// call, 1.6 TB/s of what has to move; of it the first launch 49 us, the second 93, 4 for
+// Measured: 8192 tokens, 32 heads of 128 x 128 (16 of queries and keys), fp16: 132 us a
+// call, 1.6 TB/s of what has to move; of it the first launch 48 us, the second 90, 4 for
 // the recurrent kernel that finds nothing to do (each alone, nothing in L2).  Six
-// prompts of up to 3001 tokens, 24 heads of 64 x 128, bf16: 94 us, 2.5 TB/s (31, 72, 4).
+// prompts of up to 3001 tokens, 24 heads of 64 x 128, bf16: 102 us, 2.3 TB/s (32, 76, 4).
+// bf16's third part is 7 % of that (95 without it), 19 % at 128 x 128 (140 against 118 for
+// 8192 tokens): the keys' warps write half as much again, and the room for it is the second
+// buffer of keys.
 // The memory and the tensor cores (12 to 19 %) wait for a chain of roles: a chunk of the
 // second launch is 7 to 8 thousand cycles from U through the state's copy (3 thousand),
 // Q M, its decay and P V to the output, at 38 % of the issue slots; 680 KB of shared
-// memory traffic a chunk keep that at 5 thousand.
+// memory traffic a chunk keep that at 5 thousand.  768 threads leave 80 registers each: the
+// instances with outputs spill, 28 to 64 bytes a thread.
 #pragma once
 
 #include <cuda.h>

@@ -12,9 +12,11 @@
 // several per SM so that one's loads hide the other's arithmetic.  The state's update is
 // fp32 multiply-adds in registers.
 //
-// 17 tokens, 512 heads of 128 x 128, fp16: outputs 21 us (1.8 TB/s: two
-// CTAs an SM do not hide the products and the sum over the key rows behind the read), the state 19 us (3.6 TB/s
-// read and written, 32 multiply-adds for each of its elements), a round of both 33 us.
+// 17 tokens, 512 heads of 128 x 128, fp16, calls in a row on states that are not in L2:
+// outputs 18.9 us (1.8 TB/s: two CTAs an SM do not hide the products and the sum over the key
+// rows behind the read), the state 23.9 us at 17 tokens and 18.1 at 9 (3.7 TB/s read and
+// written: 1024 CTAs, three on an SM, are 2.2 waves of load, update and store; a token more
+// is 0.3 to 0.7 us), a round of both 33 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -306,10 +308,9 @@ __global__ void __launch_bounds__(DV * 2, 512 / (DV * 2)) linear_window_kernel(c
 
 // ---- the state behind the window --------------------------------------------------------
 
-// A CTA per head and 64 value columns; thread = 4 columns x DK / 16 rows of the state:
-// few enough registers for four CTAs and more per SM (one CTA of twice the rows per head
-// was 1.7 waves of two: 21.8 us for 512 heads).  Keys and values come from shared memory
-// in fp32.
+// A CTA per head and 64 value columns; thread = 4 columns x DK / 16 rows of the state: 77
+// registers at 128 key rows, three CTAs per SM (one CTA of twice the rows per head was 1.7
+// waves of two: 21.8 us for 512 heads).  Keys and values come from shared memory in fp32.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kWinThreads) linear_commit_kernel(const LinArgs a) {
   constexpr int kCols = 16, kRowSets = kWinThreads / kCols, kRows = DK / kRowSets;

@@ -86,9 +86,9 @@ __device__ __noinline__ float attn_odd_sum(const AttnArgs& a, int b, int h, int 
 // all rows.  It is the form for head sizes and page sizes outside the tensor-core
 // kernel's; a position a row does not see has weight -0 and is skipped, so nothing its
 // values hold reaches the row.  A weight of +0 times an infinity makes the sum NaN, and
-// an output that is not finite is then told from the values themselves.  Its arithmetic bounds it: 8 sequences of 4000
-// positions, 32 heads over 8 of 96: 474 us for one row each (0.2 TB/s of cache), 3.3 ms
-// for 17; the tensor-core kernel at heads of 128 takes 38 and 52.
+// an output that is not finite is then told from the values themselves.  Its arithmetic
+// bounds it: 8 sequences of 4000 positions, 32 heads over 8 of 96: 374 us for one row each
+// (0.3 TB/s of cache), 2.7 ms for 17; the tensor-core kernel at heads of 128 takes 30 and 43.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = kAttnSimpleRows, P = kAttnSimpleTile;
