@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "mixing.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
 #include "sdv_kernels.h"

@@ -17,7 +17,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "sdv_kernels.h"
+#include "mixing.h"
 #include "split_math.cuh"
 
 namespace sdv {

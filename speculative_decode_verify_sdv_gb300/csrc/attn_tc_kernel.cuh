@@ -64,7 +64,7 @@
 
 #include "attn_sched.cuh"
 #include "attn_tc.h"
-#include "sdv_kernels.h"
+#include "mixing.h"
 #include "tc_util.cuh"
 
 namespace sdv {

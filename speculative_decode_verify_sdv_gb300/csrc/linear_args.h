@@ -7,7 +7,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
-#include "sdv_kernels.h"
+#include "mixing.h"
 
 namespace sdv {
 

@@ -9,9 +9,9 @@
 
 #include "host_util.h"
 #include "linear_args.h"
+#include "mixing.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
-#include "sdv_kernels.h"
 
 namespace sdv {
 

@@ -59,7 +59,7 @@
 #include <type_traits>
 
 #include "linear_args.h"
-#include "sdv_kernels.h"
+#include "mixing.h"
 #include "tc_util.cuh"
 
 namespace sdv {

@@ -25,8 +25,8 @@
 #include <type_traits>
 
 #include "linear_args.h"
+#include "mixing.h"
 #include "sdv.h"
-#include "sdv_kernels.h"
 #include "tc_util.cuh"
 
 namespace sdv {

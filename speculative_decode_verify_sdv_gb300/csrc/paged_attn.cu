@@ -12,9 +12,9 @@
 #include "attn_sched.cuh"
 #include "attn_tc.h"
 #include "host_util.h"
+#include "mixing.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
-#include "sdv_kernels.h"
 
 namespace sdv {
 

@@ -38,15 +38,6 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 // Device status word bits (first word of every workspace).
 constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrTmemBase = 2;  // tensor-memory allocation not at column 0
-constexpr int kDevErrIndex = 4;     // a table entry or a length on the device out of range
-
-// The timeout-path test hook (sdv_debug_fault): the limit of every bounded wait (0: the
-// built-in one) and 1 + the stage whose copy is never issued (0: none).
-struct DebugFault {
-  unsigned long long wait_ns;
-  int withhold;
-};
-DebugFault debug_fault();
 
 constexpr int kModeY = 0;     // write fp32 Y [S][N]
 constexpr int kModeHead = 1;  // verify head: argmax partials + last-CTA reduce + accept

@@ -6,8 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "mixing.h"
 #include "sdv_device.cuh"
-#include "sdv_kernels.h"
 
 namespace sdv {
 
