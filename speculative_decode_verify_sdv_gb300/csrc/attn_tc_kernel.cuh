@@ -30,8 +30,8 @@
 // output stay exact relative to it), so O in tensor memory is rescaled rarely.
 // fp16's P carries a factor 2^6: with it the weights down to 2^-20 of the row's largest
 // stay in the normal range, and 2^14 is the most it can reach.  bf16's, with the range of
-// fp32, carries 2^-8 and never passes 1: values up to 2^128 are then added up without
-// overflow where a plain sum of weights up to 1 is.  Rounding P to
+// fp32, carries 2^-8 and never passes 1, so that values of any size overflow no sooner than
+// in a plain sum with weights up to 1.  Rounding P to
 // the 16-bit type is the one rounding inside the sum (the sum l takes P before
 // it); it is what a matrix instruction on 16-bit values needs.
 //

@@ -131,8 +131,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // A bounded wait by a whole warp, in few instructions: the roles of one kernel share
 // the SM's instruction cache, so what follows a first look in vain is one function for
 // all of them.  On expiry the status word is set.  The limit stands in shared memory,
-// where one thread has put it before the block's first barrier: as an argument it cost a
-// prompt of linear attention 2 % and a window's attention 3 %.
+// where one thread has put it before the block's first barrier, so that the many places of
+// a wait carry no argument for it.
 constexpr int kWaitLimitBytes = 16;  // of static shared memory
 __device__ __forceinline__ volatile uint64_t& wait_limit_ns() {
   __shared__ alignas(kWaitLimitBytes) volatile uint64_t limit;
