@@ -345,7 +345,7 @@ SDV_API sdv_status sdv_moe_route(const float* router_logits, int32_t S, int32_t 
  * slices of a fused projection's output can be passed as they are.  Base pointers
  * are 16-byte aligned.  Outputs are contiguous.
  */
-typedef enum { SDV_F16 = 16, SDV_BF16 = 17 } sdv_dtype;
+typedef enum { SDV_F16 = 16, SDV_BF16 = 17, SDV_F32 = 32 } sdv_dtype; /* F32: inputs only, where said */
 
 /*
  * A paged cache: position p of sequence b lives in slot p % page_size of page
@@ -455,6 +455,186 @@ SDV_API sdv_status sdv_linear_attn(int32_t dtype, const void* q_or_null, const v
  * up to T tokens; 0 for invalid arguments.
  */
 SDV_API size_t sdv_linear_attn_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t Dk, int32_t Dv);
+
+/* ---- around a batched round: pages, positions, a shared prefix, drafted tokens -------
+ *
+ * What a program that serves many requests at once does between its products and its
+ * attention, on the device: the pages' bookkeeping, the keys' and queries' norms and
+ * positions, one read of what all requests have in common, and the accept under a
+ * drafter's and the target's probabilities.  No step of a round needs the host, so a
+ * round can be captured into a CUDA graph.
+ */
+
+/*
+ * The pages of a cache and who holds them.  free_pages[0 .. n_free - 1] is a stack of
+ * the pages that nobody holds; sequence b holds table[b][0 .. held[b] - 1].  All of it is
+ * device memory that the calls update.  Pages that sequences share (a prefix's) are not
+ * in a table here: give them a table of their own.
+ */
+typedef struct {
+  int32_t n_pages;     /* >= 1: places of free_pages */
+  int32_t page_size;   /* positions per page, >= 1 */
+  int32_t max_pages;   /* entries of a table row, >= 1 */
+  int32_t* free_pages; /* device int32 [n_pages] */
+  int32_t* n_free;     /* device int32 [1] */
+  int32_t* table;      /* device int32 [B][max_pages] */
+  int32_t* held;       /* device int32 [B] */
+} sdv_pagepool;
+
+/*
+ * Pages for the rows that the sequences are about to append, and those rows' places.
+ * Sequence b has ctx[b] positions and n_rows[b] new ones (NULL: T each; clamped to [0, T]):
+ *   want = ceil((ctx[b] + n_rows[b]) / page_size) pages, at most max_pages.
+ * Sequences that hold more give the rest back first: the k-th page given back, in the order
+ * of sequences and entries, goes to free_pages[top - 1 - k], top = n_free + all given back,
+ * and its entry becomes -1.  Then the sequences that hold less take theirs, in order: the k-th
+ * page taken is free_pages[top - 1 - k].  From the first sequence on that cannot have all it
+ * needs, none takes any (those that need none are not affected).  n_free and held are updated.
+ * A retired sequence is ctx = 0 with no rows; giving back what a call has taken restores the
+ * list.
+ *   granted_or_null:   device int32 [B], the rows of n_rows[b] that have a place in the
+ *     pages held: the n_rows of sdv_kv_append, sdv_paged_attn (may be n_rows itself);
+ *   positions_or_null: device int32 [B][T], ctx[b] + t for t < granted[b], else -1;
+ *   slots_or_null:     device int32 [B][T], page * page_size + place in it, else -1.
+ * A sequence whose new rows do not fit, a value of n_rows or ctx or held out of range (each
+ * clamped), a page id outside [0, n_pages) (its rows' slots are -1) and a list that would
+ * overflow (what does not fit is dropped): sdv_last_device_status(ws) reports
+ * SDV_ERR_INVALID_ARG for all but the shortage of pages, which granted tells.
+ * B <= 65535, n_pages * page_size and max_pages * page_size below 2^31.  Arrays other than
+ * granted and n_rows do not overlap.  One or two launches, deterministic.
+ */
+SDV_API sdv_status sdv_page_assign(const sdv_pagepool* pool, int32_t B, int32_t T, const int32_t* ctx,
+                           const int32_t* n_rows_or_null, int32_t* granted_or_null, int32_t* positions_or_null,
+                           int32_t* slots_or_null, void* ws, size_t ws_bytes, sdv_stream_t stream);
+
+/* Workspace bytes of sdv_page_assign for up to B sequences; 0 for invalid arguments. */
+SDV_API size_t sdv_page_assign_workspace_bytes(int32_t B);
+
+/*
+ * The rotation by position of the first rot_dim elements of a head.  Pair i at position p
+ * turns by the angle 2 pi frac(p * steps[i] / 2^64): steps are the turns per position in
+ * units of 2^-64 (sdv_rope_steps makes them), so that the angle of a far position is as
+ * exact as that of a near one.
+ */
+typedef enum { SDV_ROPE_HALF = 0, SDV_ROPE_PAIRS = 1 } sdv_rope_layout;
+typedef struct {
+  int32_t layout;        /* pair i: elements i and i + rot_dim / 2 (HALF), 2 i and 2 i + 1 (PAIRS) */
+  int32_t rot_dim;       /* even, 2 to dim */
+  float amplitude;       /* factor on rotated elements; 1 without a scaling that asks for one */
+  const uint64_t* steps; /* device [rot_dim / 2] */
+} sdv_rope;
+
+/*
+ * Frequencies for contexts longer than the trained ones (host arithmetic in 64 bits).
+ *   PLAIN:  f_i = theta^(-2 i / rot_dim) radians per position;
+ *   LINEAR: f_i / factor (position interpolation, Chen et al. 2023);
+ *   BASE:   theta * factor^(rot_dim / (rot_dim - 2)) in theta's place (rot_dim >= 4);
+ *   RAMP:   pairs that turn `high` times or more in `trained` positions stay, those that
+ *           turn `low` times or fewer are divided by factor, a linear ramp over the pair's
+ *           index, its ends rounded outwards, between; amplitude 0.1 ln(factor) + 1
+ *           (Peng et al. 2023);
+ *   BANDS:  the same ends, the ramp linear in the number of turns; amplitude 1.
+ */
+typedef enum {
+  SDV_ROPE_PLAIN = 0, SDV_ROPE_LINEAR = 1, SDV_ROPE_BASE = 2, SDV_ROPE_RAMP = 3, SDV_ROPE_BANDS = 4
+} sdv_rope_kind;
+typedef struct {
+  int32_t kind;      /* sdv_rope_kind */
+  int32_t trained;   /* RAMP, BANDS: positions the frequencies were trained for, >= 1 */
+  double factor;     /* >= 1 */
+  double low, high;  /* RAMP, BANDS: turns, 0 < low < high */
+} sdv_rope_scaling;
+
+/*
+ * steps: HOST uint64 [rot_dim / 2]; amplitude_or_null: HOST float [1].  theta > 1.
+ * scaling_or_null: NULL is PLAIN.  Nothing touches the GPU.
+ */
+SDV_API sdv_status sdv_rope_steps(int32_t rot_dim, double theta, const sdv_rope_scaling* scaling_or_null,
+                          uint64_t* steps, float* amplitude_or_null);
+
+/*
+ * The way of a projection's rows into the attention: norm of each query and key head,
+ * rotation by the row's position, queries to q_out, keys and values into the cache.
+ *   norm:     y = x / sqrt(mean over dim of x^2 + eps) * weight[e]; none where the weight is
+ *             NULL (weights fp32 [dim], 16-byte aligned, one for all heads);
+ *   rotation: for a pair (a, b) at angle phi (sdv_rope):
+ *             (A (a cos phi - b sin phi), A (b cos phi + a sin phi)), A the amplitude;
+ *             none where rope is NULL;
+ *   values are stored as they are.  All arithmetic in fp32, one rounding at the end.
+ * q: [B][T] rows of [Hq][dim]; k, v: [B][T] rows of [cache->heads][dim], at strides as for
+ * sdv_kv_append, of in_dtype: the cache's type or SDV_F32 (sdv_qlinear's output).  q and
+ * q_out may be NULL together (Hq is then ignored), k and v too (the cache's arrays are then
+ * not used); cache->table and max_pages are not used.
+ * positions: device int32 [B][T]; below 0 the row is left out: its q_out stays as it was and
+ * nothing is stored.  slots_or_null: device int32 [B][T] (with k and v only), the row's place
+ * page * page_size + offset; below 0 the row's k and v are not stored.  A slot past the cache
+ * is not stored either, and reported by the workspace's status (ws_or_null: 256 bytes or more).
+ * No two rows of a call share a slot.  Both as sdv_page_assign writes them; a tree's
+ * positions are the context's length plus the node's depth.
+ * q_out: [B][T][Hq][dim] of the cache's type; it may be q itself where q is of that type
+ * and its stride Hq * dim.  One launch.
+ */
+SDV_API sdv_status sdv_qk_norm_rope(const sdv_kvcache* cache, int32_t in_dtype, const void* q_or_null,
+                            const void* k_or_null, const void* v_or_null, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int32_t B, int32_t T, int32_t Hq, const float* q_weight_or_null,
+                            const float* k_weight_or_null, float eps, const sdv_rope* rope_or_null,
+                            const int32_t* positions, const int32_t* slots_or_null, void* q_out_or_null,
+                            void* ws_or_null, sdv_stream_t stream);
+
+/*
+ * sdv_paged_attn for sequences that share their first prefix_len positions: those lie in
+ * the pages prefix_table[0 ..] of the same cache, are seen by every live row, and are
+ * read once for the whole batch; ctx, n_rows, mask and the cache's table are of what follows,
+ * each sequence's own, as for sdv_paged_attn.
+ *   prefix_table: device int32 [prefix_pages]; prefix_len: device int32 [1], clamped to
+ *   [0, prefix_pages * page_size] (a clamp is reported as for a bad table entry).
+ * The result is that of sdv_paged_attn on the joined positions: lse over both, a row
+ * i >= n_rows[b] gives 0 and -inf.  Arguments otherwise as there; the workspace is
+ * sdv_prefix_attn_workspace_bytes(...) bytes.  Several prefixes: a call each, on their
+ * sequences.  Deterministic.
+ */
+SDV_API sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table, int32_t prefix_pages,
+                           const int32_t* prefix_len, const void* q, int64_t q_stride, int32_t B, int32_t S,
+                           int32_t Hq, const int32_t* ctx, const int32_t* n_rows_or_null,
+                           const uint32_t* mask_or_null, float scale, void* out, float* lse_or_null, void* ws,
+                           size_t ws_bytes, sdv_stream_t stream);
+
+/* Workspace bytes of sdv_prefix_attn on the current device; 0 for invalid arguments. */
+SDV_API size_t sdv_prefix_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim);
+
+/*
+ * Speculative sampling of a batch (Leviathan, Kalman & Matias, ICML 2023) from given logits,
+ * drafter's probabilities and random numbers.  Sequence b's window has n = n_drafts[b]
+ * drafts (NULL: S - 1 each; clamped to [0, S - 1]); logits row i is the target's after draft
+ * i - 1 (row 0: after the anchor):
+ *   p_i = softmax(logits[b][i] / temperature[b]);
+ *   accepted[b] = the first i < n with NOT (uniforms[b][i] * q_i(d_i) < p_i(d_i)), else n;
+ *   next_token[b] = a draw, at a rejection from max(p_i - q_i, 0) (from p_i where that is 0
+ *     everywhere), else from p_n: the lowest v at which the running sum of the weights
+ *     exceeds uniforms[b][S - 1] times their total.
+ * q_i = draft_probs[b][i], or 1 at the draft and 0 elsewhere where draft_probs is NULL (a
+ * drafter that proposes deterministically, as sdv_ngram_propose).  A temperature of 0,
+ * below or NaN is greedy: p_i is 1 at the lowest index of the maximum.
+ *   logits: rows of V elements of `dtype` (SDV_F32, SDV_F16 or SDV_BF16) at row_stride >= V
+ *     elements, [B][S], aligned to their element; -inf takes a token out (top-k and top-p
+ *     filters), NaN counts as -inf, +inf as the largest number;
+ *   drafts_or_null: device int32 [B][S - 1] (NULL where S == 1); a draft outside [0, V) is
+ *     not accepted; draft_probs_or_null: device fp32 [B][S - 1][V], below 0 and NaN count as 0;
+ *   uniforms: device fp32 [B][S] in [0, 1).
+ * A sequence whose drawn row has no token left gives next_token -1.  Weights below 2^-125 of
+ * the row's largest count as 0.  Rows past n_drafts[b] are not read.
+ * 1 <= S <= 32, V and B <= 2^24.  The workspace is sdv_verify_drafts_workspace_bytes(...) bytes.
+ * Deterministic.  The tests' sums are fp32, the draw's weights and sums exact to some 2^-36:
+ * a test or a draw nearer to its border than that may differ from a 64-bit evaluation.
+ */
+SDV_API sdv_status sdv_verify_drafts(int32_t dtype, const void* logits, int64_t row_stride, int32_t B, int32_t S,
+                             int32_t V, const float* temperature, const int32_t* drafts_or_null,
+                             const int32_t* n_drafts_or_null, const float* draft_probs_or_null,
+                             const float* uniforms, int32_t* accepted, int32_t* next_token, void* ws,
+                             size_t ws_bytes, sdv_stream_t stream);
+
+/* Workspace bytes of sdv_verify_drafts, for up to B sequences; 0 for invalid arguments. */
+SDV_API size_t sdv_verify_drafts_workspace_bytes(int32_t B, int32_t S, int32_t V);
 
 /*
  * Workspace bytes an operation needs on the current device.

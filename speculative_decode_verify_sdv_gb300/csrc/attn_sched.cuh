@@ -19,6 +19,7 @@
 
 #include "mixing.h"
 #include "split_math.cuh"
+#include "tc_util.cuh"
 
 namespace sdv {
 
@@ -40,6 +41,7 @@ struct AttnArgs {
   int tile;                 // cache positions per tile
   int lead;                 // weight of a unit beyond its tiles
   void* out;
+  float* out32;             // or null: outputs in fp32 here instead
   float* lse;               // or null
   float* part_o;            // [2 * CTAs][D / 4][row_tile][4]
   float* part_ml;           // [2 * CTAs][row_tile][2]: max (log2 domain), sum
@@ -84,9 +86,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return attn_seq(a, __ldg(a.ctx + b), a.n_rows != nullptr ? __ldg(a.n_rows + b) : a.S);
 }
 
-__device__ __forceinline__ int attn_live_ctas(const AttnArgs& a, long long total) {
-  return total < a.ctas ? (int)total : a.ctas;
-}
+__device__ __forceinline__ int attn_live_ctas(int ctas, long long total) { return total < ctas ? (int)total : ctas; }
 // Start of CTA c's range, and the CTA whose range holds place w.
 __device__ __forceinline__ long long attn_first(long long total, int live, int c) { return muldiv(total, c, live); }
 __device__ __forceinline__ int attn_owner(long long total, int live, long long w) {
@@ -110,7 +110,7 @@ struct AttnWalk {
     for (int s = lane + 32; s < a.B; s += 32) total += ((long long)attn_seq(a, s).tiles + a.lead) * units;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    live = attn_live_ctas(a, total);
+    live = attn_live_ctas(a.ctas, total);
     if (cta >= live) return false;
     at = attn_first(total, live, cta);
     end = attn_first(total, live, cta + 1);
@@ -246,6 +246,15 @@ __device__ __forceinline__ uint32_t attn_word(const AttnArgs& a, int b, int i, i
   const uint32_t live = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   if (a.mask != nullptr) return __ldg(a.mask + (size_t)b * a.S + i) & live;
   return (2u << i) - 1u;  // i = 31: 2 << 31 is 0, minus 1 is all ones
+}
+
+// Four columns of an output: as the 16-bit type, or fp32 where another launch goes on with them.
+template <typename T>
+__device__ __forceinline__ void attn_store4(const AttnArgs& a, long long at, float x, float y, float z, float w) {
+  if (a.out32 != nullptr)
+    *reinterpret_cast<float4*>(a.out32 + at) = make_float4(x, y, z, w);
+  else
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at) = make_uint2(pack16<T>(x, y), pack16<T>(z, w));
 }
 
 cudaError_t launch_attn_simple(int dtype, const AttnArgs& a, cudaStream_t st);

@@ -698,10 +698,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int rw = r0 + rr, rs = small_div(rw, inv_g);
             const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
             if (final) {
-              const float inv = lq == 0.f ? 0.f : 1.f / lq;
-              const uint2 y = lq == 0.f ? make_uint2(0u, 0u)
-                                        : make_uint2(pack16<T>(x.x * inv, x.y * inv), pack16<T>(x.z * inv, x.w * inv));
-              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + j0 + j) = y;
+              const float inv = 1.f / lq;
+              if (lq == 0.f) attn_store4<T>(a, orow * D + j0 + j, 0.f, 0.f, 0.f, 0.f);
+              else attn_store4<T>(a, orow * D + j0 + j, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
               if (j0 + j == 0 && a.lse != nullptr)
                 a.lse[orow] = lq == 0.f ? -INFINITY : (mo + log2f(lq)) * 0.6931471805599453f;
             } else {
@@ -735,11 +734,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (!sum.finite()) sum = attn_sum_odd_parts(ml, po, a.row_tile, step, first, first, last);
               const int rw = r0 + rr, rs = small_div(rw, inv_g);
               const long long orow = ((long long)b * a.S + rs) * a.Hq + h * a.G + (rw - rs * a.G);
-              const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
-              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + j * 4) =
-                  sum.l == 0.f ? make_uint2(0u, 0u)
-                               : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv),
-                                            pack16<T>(sum.o.z * inv, sum.o.w * inv));
+              const float inv = 1.f / sum.l;
+              if (sum.l == 0.f) attn_store4<T>(a, orow * D + j * 4, 0.f, 0.f, 0.f, 0.f);
+              else attn_store4<T>(a, orow * D + j * 4, sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
               if (j == 0 && a.lse != nullptr) a.lse[orow] = sum.lse();
             }
           }
@@ -771,7 +768,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int e = 0; e < OC; e += 32) tmem_ld32(tq + PL::kO + j + e, o + e);
             tmem_wait_ld();
-            if (r < nr && final) {
+            if (r < nr && final && a.out32 != nullptr) {
+              float4* const dst = reinterpret_cast<float4*>(a.out32 + orow * D + j);
+#pragma unroll
+              for (int e = 0; e < OC; e += 4)
+                dst[e / 4] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                  : make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            } else if (r < nr && final) {
               uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + j);
 #pragma unroll
               for (int e = 0; e < OC; e += 8) {

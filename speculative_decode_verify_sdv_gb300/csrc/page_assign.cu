@@ -1,0 +1,291 @@
+// Page tables and slot maps of a paged cache from the requests' lengths (sdv_page_assign).
+//
+// want_b = ceil((ctx_b + n_b) / page) pages against held_b.  With R pages given back in all and
+// `count` on the list, top = count + R: the k-th page given back, in the order of the table,
+// goes to place top - 1 - k, and the k-th one taken comes from there; who cannot have all its
+// pages, and everyone behind, takes none.  Giving the same pages back restores the list.
+//
+// Two exclusive sums over the requests, of what is given back and of what is needed, and a
+// copy of page ids.  A round of 48 windows moves some 50 ids and writes 6 KB: latency bounds it,
+// the loads of the lengths, of the list and of the table's entries one after another.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "host_util.h"
+#include "mixing.h"
+#include "sdv.h"
+#include "sdv_device.cuh"
+
+namespace sdv {
+
+namespace {
+
+struct PageArgs {
+  int32_t *free_pages, *n_free, *table, *held;
+  const int32_t *ctx, *n_rows;
+  int32_t *granted, *positions, *slots;  // each may be null
+  int32_t *plan_held, *plan_rows;        // [B] each: pages held and rows granted after the call
+  int B, T, n_pages, page, max_pages;
+  int* status;
+};
+
+constexpr int kPageThreads = 1024;
+
+struct PageNeed {
+  int ctx, n, held, want;
+  bool bad;
+  __device__ __forceinline__ int back() const { return max(held - want, 0); }
+  __device__ __forceinline__ int need() const { return max(want - held, 0); }
+};
+
+__device__ __forceinline__ PageNeed page_need(const PageArgs& a, int b) {
+  PageNeed p{0, 0, 0, 0, false};
+  if (b >= a.B) return p;
+  const int c = __ldcg(a.ctx + b), n = a.n_rows != nullptr ? __ldcg(a.n_rows + b) : a.T, h = __ldcg(a.held + b);
+  p.ctx = max(c, 0);
+  p.n = min(max(n, 0), a.T);
+  p.held = min(max(h, 0), a.max_pages);
+  const long long want = ((long long)p.ctx + p.n + a.page - 1) / a.page;
+  p.want = want > a.max_pages ? a.max_pages : (int)want;
+  p.bad = p.ctx != c || p.n != n || p.held != h || want > a.max_pages;
+  return p;
+}
+
+// Sum over the block's threads in front of this one; `all`: over all of them.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  __syncthreads();  // the last call's sums have been read
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  const long long mine = warp_sums[lane];
+  long long s = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += o;
+  }
+  all = __shfl_sync(0xffffffffu, s, 31);
+  return incl - x + __shfl_sync(0xffffffffu, s - mine, warp);
+}
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster meet; what they wrote before is seen behind it.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Position and slot of row t of sequence b; false where the table's entry is not a page.
+__device__ __forceinline__ bool place_row(const PageArgs& a, int b, int t, int ctx, int rows) {
+  int pos = -1, slot = -1;
+  bool ok = true;
+  if (t < rows) {
+    pos = ctx + t;
+    if (a.slots != nullptr) {
+      const int id = __ldcg(a.table + (size_t)b * a.max_pages + pos / a.page);
+      ok = id >= 0 && id < a.n_pages;
+      if (ok) slot = id * a.page + pos % a.page;
+    }
+  }
+  const size_t e = (size_t)b * a.T + t;
+  if (a.positions != nullptr) a.positions[e] = pos;
+  if (a.slots != nullptr) a.slots[e] = slot;
+  return ok;
+}
+
+// One cluster: every CTA computes the sums, the warps of all share the copies.
+__global__ void __launch_bounds__(kPageThreads, 1) page_assign_kernel(const PageArgs a, int place) {
+  __shared__ long long warp_sums[32], s_off[kPageThreads];
+  __shared__ int s_from[kPageThreads], s_count[kPageThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = cluster_rank(), warps = cluster_size() * (kPageThreads / 32), me = rank * (kPageThreads / 32) + (tid >> 5);
+  griddep_wait();
+  const int listed = __ldcg(a.n_free), count = min(max(listed, 0), a.n_pages);
+  bool bad = listed != count;
+  PageNeed first = page_need(a, tid);  // of the first 1024 sequences, kept
+  long long sum = 0, back_all, all;
+  for (int b0 = 0; b0 < a.B; b0 += kPageThreads) {
+    const PageNeed p = b0 == 0 ? first : page_need(a, b0 + tid);
+    bad |= p.bad;
+    sum += p.back();
+  }
+  block_scan(sum, warp_sums, back_all);
+  const long long top = count + back_all;
+  bad |= top > a.n_pages;
+  if (back_all > 0) {
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPageThreads) {
+      const PageNeed p = b0 == 0 ? first : page_need(a, b0 + tid);
+      const long long off = block_scan(p.back(), warp_sums, all) + before;
+      s_off[tid] = off;
+      s_from[tid] = p.want;
+      s_count[tid] = p.back();
+      __syncthreads();
+      for (int i = me; i < min(kPageThreads, a.B - b0); i += warps) {
+        int32_t* const row = a.table + (size_t)(b0 + i) * a.max_pages + s_from[i];
+#pragma unroll 4
+        for (int j = lane; j < s_count[i]; j += 32) {
+          const int id = __ldcg(row + j);
+          const long long at = top - 1 - (s_off[i] + j);
+          bad |= id < 0 || id >= a.n_pages;
+          row[j] = -1;
+          if (at < a.n_pages) a.free_pages[at] = id;
+        }
+      }
+      before += all;
+    }
+    cluster_meet();
+  }
+  long long before = 0, taken = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPageThreads) {
+    const PageNeed p = b0 == 0 ? first : page_need(a, b0 + tid);
+    const long long off = block_scan(p.need(), warp_sums, all) + before;
+    const bool served = off + p.need() <= top;
+    const int fresh = served ? p.need() : 0, held = served ? p.want : min(p.held, p.want);
+    taken += fresh;
+    if (rank == 0 && b0 + tid < a.B) {
+      a.plan_held[b0 + tid] = held;
+      a.plan_rows[b0 + tid] = (int)min((long long)p.n, max((long long)held * a.page - p.ctx, 0ll));
+    }
+    s_off[tid] = off;
+    s_from[tid] = p.held;
+    s_count[tid] = fresh;
+    __syncthreads();
+    if (all > 0) {
+      for (int i = me; i < min(kPageThreads, a.B - b0); i += warps) {
+        int32_t* const row = a.table + (size_t)(b0 + i) * a.max_pages + s_from[i];
+#pragma unroll 4
+        for (int j = lane; j < s_count[i]; j += 32) {
+          const long long at = top - 1 - (s_off[i] + j);
+          const int id = at < a.n_pages ? __ldcg(a.free_pages + at) : -1;
+          bad |= id < 0 || id >= a.n_pages;
+          row[j] = id;
+        }
+      }
+    }
+    before += all;
+  }
+  block_scan(taken, warp_sums, all);
+  cluster_meet();  // every CTA has read the lengths, every copy and the plan are there
+  if (rank == 0) {
+    for (int b = tid; b < a.B; b += kPageThreads) {
+      a.held[b] = __ldcg(a.plan_held + b);
+      if (a.granted != nullptr) a.granted[b] = __ldcg(a.plan_rows + b);
+    }
+    if (tid == 0) *a.n_free = (int)min(top - all, (long long)a.n_pages);
+  }
+  if (place) {
+    for (int b = me; b < a.B; b += warps) {
+      const int ctx = max(__ldcg(a.ctx + b), 0), rows = __ldcg(a.plan_rows + b);
+      for (int t = lane; t < a.T; t += 32) bad |= !place_row(a, b, t, ctx, rows);
+    }
+  }
+  if (bad && a.status != nullptr) atomicOr(a.status, kDevErrIndex);
+}
+
+constexpr int kPlaceThreads = 256, kPlaceRows = 4;
+
+__global__ void __launch_bounds__(kPlaceThreads) page_place_kernel(const PageArgs a) {
+  griddep_wait();
+  const int b = blockIdx.y, t0 = blockIdx.x * kPlaceThreads * kPlaceRows + threadIdx.x;
+  const int ctx = max(__ldcg(a.ctx + b), 0), rows = __ldcg(a.plan_rows + b);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPlaceRows; ++i) {
+    const int t = t0 + i * kPlaceThreads;
+    if (t < a.T) bad |= !place_row(a, b, t, ctx, rows);
+  }
+  if (bad) atomicOr(a.status, kDevErrIndex);
+}
+
+constexpr int kMaxPageSeqs = 65535;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+}  // namespace sdv
+
+extern "C" {
+
+size_t sdv_page_assign_workspace_bytes(int32_t B) {
+  if (B < 1 || B > sdv::kMaxPageSeqs) return 0;
+  return sdv::kHeaderBytes + 2 * sdv::round_256((size_t)B * 4);
+}
+
+sdv_status sdv_page_assign(const sdv_pagepool* pool, int32_t B, int32_t T, const int32_t* ctx,
+                           const int32_t* n_rows_or_null, int32_t* granted_or_null, int32_t* positions_or_null,
+                           int32_t* slots_or_null, void* ws, size_t ws_bytes, sdv_stream_t stream) {
+  if (pool == nullptr || pool->free_pages == nullptr || pool->n_free == nullptr || pool->table == nullptr ||
+      pool->held == nullptr || ctx == nullptr || B < 1 || T < 1)
+    return SDV_ERR_INVALID_ARG;
+  if (pool->n_pages < 1 || pool->page_size < 1 || pool->max_pages < 1) return SDV_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)pool->free_pages, (const void*)pool->n_free, (const void*)pool->table,
+                        (const void*)pool->held, (const void*)ctx, (const void*)n_rows_or_null,
+                        (const void*)granted_or_null, (const void*)positions_or_null, (const void*)slots_or_null})
+    if (!sdv::aligned4(p)) return SDV_ERR_INVALID_ARG;
+  // positions and slots are 32-bit numbers
+  if (B > sdv::kMaxPageSeqs || (long long)pool->n_pages * pool->page_size > INT32_MAX ||
+      (long long)pool->max_pages * pool->page_size > INT32_MAX)
+    return SDV_ERR_UNSUPPORTED;
+  if (ws == nullptr || !sdv::is_aligned16(ws) || ws_bytes < sdv_page_assign_workspace_bytes(B)) return SDV_ERR_WORKSPACE;
+  sdv::PageArgs a{};
+  a.free_pages = pool->free_pages;
+  a.n_free = pool->n_free;
+  a.table = pool->table;
+  a.held = pool->held;
+  a.ctx = ctx;
+  a.n_rows = n_rows_or_null;
+  a.granted = granted_or_null;
+  a.positions = positions_or_null;
+  a.slots = slots_or_null;
+  a.plan_held = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
+  a.plan_rows = a.plan_held + sdv::round_256((size_t)B * 4) / 4;
+  a.B = B;
+  a.T = T;
+  a.n_pages = pool->n_pages;
+  a.page = pool->page_size;
+  a.max_pages = pool->max_pages;
+  a.status = static_cast<int*>(ws);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool maps = positions_or_null != nullptr || slots_or_null != nullptr;
+  const bool place = maps && T <= 256 && (long long)B * T <= 4096;
+  const int cluster = B >= 256 ? 8 : 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(sdv::kPageThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = sdv::counted(cudaLaunchKernelEx(&cfg, sdv::page_assign_kernel, a, place ? 1 : 0));
+  if (e == cudaSuccess && maps && !place) {
+    const int per = sdv::kPlaceThreads * sdv::kPlaceRows;
+    e = sdv::launch_pdl(sdv::page_place_kernel, dim3((unsigned)(((long long)T + per - 1) / per), B),
+                        dim3(sdv::kPlaceThreads), 0, st, a);
+  }
+  return sdv::status_of(e);
+}
+
+}  // extern "C"

@@ -13,6 +13,7 @@
 #include "attn_tc.h"
 #include "host_util.h"
 #include "mixing.h"
+#include "paged_attn.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
 
@@ -221,7 +222,10 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int d = tid + 128 * c;
-          if (d < D) from_float(al[r] == 0.f ? 0.f : o[c][r] * inv, static_cast<T*>(a.out)[orow * D + d]);
+          if (d >= D) continue;
+          const float y = al[r] == 0.f ? 0.f : o[c][r] * inv;
+          if (a.out32 != nullptr) a.out32[orow * D + d] = y;
+          else from_float(y, static_cast<T*>(a.out)[orow * D + d]);
         }
         if (tid == 0 && a.lse != nullptr)
           a.lse[orow] = al[r] == 0.f ? -INFINITY : (ps[r] + log2f(al[r])) * 0.6931471805599453f;
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
   }
   const AttnSeq seq = attn_seq(a, b);
   const long long total = all * units, first = before * units + (long long)unit * (seq.tiles + a.lead) + a.lead;
-  const int live = attn_live_ctas(a, total);
+  const int live = attn_live_ctas(a.ctas, total);
   const int c0 = attn_owner(total, live, first), c1 = attn_owner(total, live, first + seq.tiles - 1);
   griddep_wait();
   if (c0 == c1) return;
@@ -301,12 +305,8 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
   const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
   const bool none = sum.l == 0.f;
   const float inv = none ? 0.f : 1.f / sum.l;
-  alignas(8) T y[4];
-  from_float(none ? 0.f : sum.o.x * inv, y[0]);
-  from_float(none ? 0.f : sum.o.y * inv, y[1]);
-  from_float(none ? 0.f : sum.o.z * inv, y[2]);
-  from_float(none ? 0.f : sum.o.w * inv, y[3]);
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * a.D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
+  attn_store4<T>(a, orow * a.D + d4 * 4, none ? 0.f : sum.o.x * inv, none ? 0.f : sum.o.y * inv,
+                 none ? 0.f : sum.o.z * inv, none ? 0.f : sum.o.w * inv);
   if (d4 == 0 && a.lse != nullptr) a.lse[orow] = sum.lse();
 }
 
@@ -400,6 +400,90 @@ size_t attn_need(int B, int S, int Hq, int heads, int dim) {
 
 }  // namespace
 
+namespace sdv {
+
+size_t attn_bytes(int B, int S, int Hq, int heads, int dim) {
+  size_t most = attn_need(B, S, Hq, heads, dim);
+  // shorter windows too: a row tile has fewer rows where a second one begins
+  for (int s = 1; most != 0 && s < S; ++s) {
+    const size_t need = attn_need(B, s, Hq, heads, dim);
+    if (need > most) most = need;
+  }
+  return most;
+}
+
+sdv_status attn_check(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
+                      const int32_t* ctx, const int32_t* n_rows, const uint32_t* mask, float scale, const void* out,
+                      const float* lse) {
+  if (!valid_cache(cache) || ctx == nullptr || out == nullptr || B < 1 || S < 1 || Hq < 1)
+    return SDV_ERR_INVALID_ARG;
+  if (Hq % cache->heads != 0 || !valid_rows(q, q_stride, Hq, cache->dim)) return SDV_ERR_INVALID_ARG;
+  if (!aligned4(ctx) || !aligned4(n_rows) || !aligned4(mask) || !aligned4(lse) || !is_aligned16(out) ||
+      !std::isfinite(scale))
+    return SDV_ERR_INVALID_ARG;
+  if (S > kMaxWindow || cache->dim > kMaxDim || Hq > kMaxHeads || (long long)B * Hq * S > kMaxUnits)
+    return SDV_ERR_UNSUPPORTED;
+  return SDV_OK;
+}
+
+AttnArgs attn_args(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
+                   const int32_t* ctx, const int32_t* n_rows, const uint32_t* mask, float scale) {
+  AttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.table = cache->table;
+  a.ctx = ctx;
+  a.n_rows = n_rows;
+  a.mask = mask;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.B = B;
+  a.S = S;
+  a.Hq = Hq;
+  a.Hkv = cache->heads;
+  a.G = Hq / cache->heads;
+  a.D = cache->dim;
+  a.n_pages = cache->n_pages;
+  a.page = cache->page_size;
+  a.max_pages = cache->max_pages;
+  a.rows = S * a.G;
+  return a;
+}
+
+sdv_status attn_run(const sdv_kvcache* cache, AttnArgs a, void* ws, cudaStream_t st) {
+  a.status = static_cast<int*>(ws);
+  a.fault = debug_fault();
+  const int sms = sm_count();
+  if (sms <= 0) return SDV_ERR_CUDA;
+  const bool tc = attn_tc_takes(a.D, a.G, a.page, (long long)a.n_pages * a.Hkv * a.page);
+  if (tc) set_window_rows(a);
+  else set_rows(a, kAttnSimpleRows);
+  a.tile = tc ? attn_tc_tile(a.D) : kAttnSimpleTile;
+  // (0, 1 and 2: six tree windows 43.0, 35.5 and 33.4 us, 48 ragged contexts 120.8, 104.4
+  // and 104.4)
+  a.lead = tc ? 2 : 1;
+  a.ctas = tc ? sms : kSimplePerSm * sms;
+  // Shared units are joined by their last CTA where a partial is at most 2 KB (single
+  // tokens), larger ones by a launch of many CTAs.  GPU us a call, launch against last CTA,
+  // fp16, 8 cache heads: one sequence of 613, 5000 and 30,000 positions, then 48 of 40 to
+  // 15,550.  4 rows x 128 (512 elements): 10.9 to 10.7, 15.2 to 16.5, 29.5 to 31.3, 236 to
+  // 233, and the host issues one launch less (8.1 against 6.6 us).  8 x 128 (1024): 11.6 to
+  // 12.9, 15.9 to 22.1, 30.0 to 36.9, 240 to 235; 4 x 256: 12.6 to 14.8, 19.3 to 23.3, 47.0
+  // to 52.0, 454 to 448.  16 x 128 (2048): 12.5 to 16.0, 17.0 to 28.9, 30.9 to 44.2, 247 to 239.
+  if (tc && a.row_tile * a.D <= 512 && a.ctas <= kAttnSharedBytes)
+    a.shared = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kAttnSharedAt);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
+  a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
+                                      round_256((size_t)2 * a.ctas * a.row_tile * 8));
+  cudaError_t e = tc ? launch_attn_tc(cache->dtype, a, st) : launch_attn_simple(cache->dtype, a, st);
+  // the join, unless the kernel joins or no unit can have more than one tile
+  if (e == cudaSuccess && a.shared == nullptr && (long long)a.max_pages * a.page > a.tile) e = launch_attn_join(cache->dtype, a, st);
+  return status_of(e);
+}
+
+}  // namespace sdv
+
 extern "C" {
 
 sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -434,80 +518,22 @@ sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const void* v,
 }
 
 size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim) {
-  size_t most = attn_need(B, S, Hq, heads, dim);
-  // shorter windows too: a row tile has fewer rows where a second one begins
-  for (int s = 1; most != 0 && s < S; ++s) {
-    const size_t need = attn_need(B, s, Hq, heads, dim);
-    if (need > most) most = need;
-  }
-  return most;
+  return sdv::attn_bytes(B, S, Hq, heads, dim);
 }
 
 sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
                           const int32_t* ctx, const int32_t* n_rows_or_null, const uint32_t* mask_or_null,
                           float scale, void* out, float* lse_or_null, void* ws, size_t ws_bytes,
                           sdv_stream_t stream) {
-  if (!valid_cache(cache) || ctx == nullptr || out == nullptr || B < 1 || S < 1 || Hq < 1)
-    return SDV_ERR_INVALID_ARG;
-  if (Hq % cache->heads != 0 || !valid_rows(q, q_stride, Hq, cache->dim)) return SDV_ERR_INVALID_ARG;
-  if (!aligned4(ctx) || !aligned4(n_rows_or_null) || !aligned4(mask_or_null) || !aligned4(lse_or_null) ||
-      !sdv::is_aligned16(out) || !std::isfinite(scale))
-    return SDV_ERR_INVALID_ARG;
-  if (S > kMaxWindow || cache->dim > kMaxDim || Hq > kMaxHeads || (long long)B * Hq * S > kMaxUnits)
-    return SDV_ERR_UNSUPPORTED;
+  const sdv_status ok = sdv::attn_check(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale, out,
+                                        lse_or_null);
+  if (ok != SDV_OK) return ok;
   const size_t need = attn_need(B, S, Hq, cache->heads, cache->dim);
   if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
-  AttnArgs a{};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.k = cache->k;
-  a.v = cache->v;
-  a.table = cache->table;
-  a.ctx = ctx;
-  a.n_rows = n_rows_or_null;
-  a.mask = mask_or_null;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.B = B;
-  a.S = S;
-  a.Hq = Hq;
-  a.Hkv = cache->heads;
-  a.G = Hq / cache->heads;
-  a.D = cache->dim;
-  a.n_pages = cache->n_pages;
-  a.page = cache->page_size;
-  a.max_pages = cache->max_pages;
-  a.rows = S * a.G;
+  AttnArgs a = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
   a.out = out;
   a.lse = lse_or_null;
-  a.status = static_cast<int*>(ws);
-  a.fault = sdv::debug_fault();
-  const int sms = sdv::sm_count();
-  if (sms <= 0) return SDV_ERR_CUDA;
-  const bool tc = sdv::attn_tc_takes(a.D, a.G, a.page, (long long)a.n_pages * a.Hkv * a.page);
-  if (tc) set_window_rows(a);
-  else set_rows(a, sdv::kAttnSimpleRows);
-  a.tile = tc ? sdv::attn_tc_tile(a.D) : sdv::kAttnSimpleTile;
-  // (0, 1 and 2: six tree windows 43.0, 35.5 and 33.4 us, 48 ragged contexts 120.8, 104.4
-  // and 104.4)
-  a.lead = tc ? 2 : 1;
-  a.ctas = tc ? sms : kSimplePerSm * sms;
-  // Shared units are joined by their last CTA where a partial is at most 2 KB (single
-  // tokens), larger ones by a launch of many CTAs.  GPU us a call, launch against last CTA,
-  // fp16, 8 cache heads: one sequence of 613, 5000 and 30,000 positions, then 48 of 40 to
-  // 15,550.  4 rows x 128 (512 elements): 10.9 to 10.7, 15.2 to 16.5, 29.5 to 31.3, 236 to
-  // 233, and the host issues one launch less (8.1 against 6.6 us).  8 x 128 (1024): 11.6 to
-  // 12.9, 15.9 to 22.1, 30.0 to 36.9, 240 to 235; 4 x 256: 12.6 to 14.8, 19.3 to 23.3, 47.0
-  // to 52.0, 454 to 448.  16 x 128 (2048): 12.5 to 16.0, 17.0 to 28.9, 30.9 to 44.2, 247 to 239.
-  if (tc && a.row_tile * a.D <= 512 && a.ctas <= sdv::kAttnSharedBytes)
-    a.shared = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kAttnSharedAt);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
-  a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
-                                      sdv::round_256((size_t)2 * a.ctas * a.row_tile * 8));
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = tc ? sdv::launch_attn_tc(cache->dtype, a, st) : sdv::launch_attn_simple(cache->dtype, a, st);
-  // the join, unless the kernel joins or no unit can have more than one tile
-  if (e == cudaSuccess && a.shared == nullptr && (long long)a.max_pages * a.page > a.tile) e = sdv::launch_attn_join(cache->dtype, a, st);
-  return sdv::status_of(e);
+  return sdv::attn_run(cache, a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,390 @@
+// Attention of a batch over a prefix that its sequences share, computed once for all, and each
+// sequence's own cache (sdv_prefix_attn): the prefix on the CUDA cores for shapes that the
+// tensor-core kernel does not take, the join, and the entry point.
+//
+// Per query row, with the prefix's positions in parts j and the row's own positions:
+//   M = max m_j;  out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j;  lse = M + log sum.
+// The query rows of all sequences stand side by side as the rows of one product with the
+// prefix, which is so read once, not once a sequence; the own caches go through the paged
+// attention, which leaves fp32 outputs here; the join adds the two.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_tc.h"
+#include "host_util.h"
+#include "mixing.h"
+#include "paged_attn.h"
+#include "prefix_attn.cuh"
+#include "sdv.h"
+#include "sdv_device.cuh"
+
+namespace sdv {
+
+namespace {
+
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// ---- the prefix on the CUDA cores -------------------------------------------------------
+
+// What is not finite in column d of the values from position `from` to `to` - 1.
+template <typename T>
+__device__ __noinline__ uint32_t prefix_odd(const PrefixArgs& a, int h, int from, int to, int d) {
+  uint32_t odd = 0;
+  for (int p = from; p < to; ++p) {
+    const int id = __ldg(a.table + p / a.page);
+    if (id < 0 || id >= a.n_pages) continue;
+    const float x = to_float(static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d]);
+    if (!(fabsf(x) < INFINITY)) odd |= x != x ? kOddNan : x > 0.f ? kOddPlus : kOddMinus;
+  }
+  return odd;
+}
+
+// One CTA walks its range of tiles with 8 query rows per tile, as the paged attention's does:
+// 32 positions at a time through shared memory, two rows' maximum and sum in a warp, up to two
+// columns of all rows' outputs in a thread.  Weights carry a factor 2^-kPrefixDrop, so that the sums
+// of 2^24 values near the largest number stay numbers.
+template <typename T>
+__global__ void __launch_bounds__(128) prefix_simple_kernel(const __grid_constant__ PrefixArgs a) {
+  constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile;
+  extern __shared__ float sm[];
+  const int D = a.D, ld = D + 1;
+  float* const qs = sm;                    // [R][D]
+  float* const ks = qs + R * D;            // [P][D + 1]
+  float* const vs = ks + P * ld;           // [P][D]
+  float* const ps = vs + P * D;            // [R][P] weights
+  float* const al = ps + R * P;            // [R] factor of the old sum and output
+  __shared__ bool gone[P];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  bool bad;
+  const int length = prefix_length(a, bad);
+  if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, kDevErrIndex);
+  PrefixWalk w;
+  if (!w.start(a, length, blockIdx.x)) return;
+  while (w.more()) {
+    const int count = w.segment();
+    const int h = w.unit / a.row_tiles, r0 = (w.unit % a.row_tiles) * a.row_tile;
+    const int nr = min(a.row_tile, a.tokens * a.G - r0);
+    __syncthreads();
+    for (int e = tid; e < R * D; e += 128) {
+      const int r = e / D, row = r0 + r;
+      float x = 0.f;
+      if (r < nr)
+        x = to_float(static_cast<const T*>(a.q)[(long long)(row / a.G) * a.q_stride + (h * a.G + row % a.G) * D + e % D]);
+      qs[e] = x;
+    }
+    float o[2][R], m[2], l[2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[0][r] = o[1][r] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    for (int t = w.tile; t < w.tile + count; ++t) {
+      const int p0 = t * P;
+      __syncthreads();
+      for (int j = warp; j < P; j += 4) {  // a position per warp
+        const int p = p0 + j;
+        int id = -1;
+        if (p < length) {
+          id = __ldg(a.table + p / a.page);
+          if (id < 0 || id >= a.n_pages) {
+            if (lane == 0) atomicOr(a.status, kDevErrIndex);
+            id = -1;
+          }
+        }
+        const long long at = (((long long)id * a.Hkv + h) * a.page + p % a.page) * D;
+        for (int d = lane; d < D; d += 32) {
+          ks[j * ld + d] = id < 0 ? 0.f : to_float(static_cast<const T*>(a.k)[at + d]);
+          vs[j * D + d] = id < 0 ? 0.f : to_float(static_cast<const T*>(a.v)[at + d]);
+        }
+        if (lane == 0) gone[j] = id < 0;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // warp's rows 2 warp + i, lane = position
+        const int r = 2 * warp + i;
+        const bool see = !gone[lane] && r < nr;
+        float s = -INFINITY;
+        if (see) {
+          s = 0.f;
+#pragma unroll 4
+          for (int d = 0; d < D; ++d) s = fmaf(qs[r * D + d], ks[lane * ld + d], s);
+          s *= a.scale_log2;
+        }
+        float mx = s;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m[i], mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float e = see ? exp2f(s - ref - kPrefixDrop) : -0.f;
+        const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - ref);
+        float sum = e;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+        ps[r * P + lane] = e;
+        if (lane == 0) al[r] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = tid + 128 * c;
+        if (d >= D) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) o[c][r] *= al[r];
+#pragma unroll 2
+        for (int j = 0; j < P; ++j) {
+          const float x = vs[j * D + d];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float e = ps[r * P + j];
+            if (__float_as_uint(e) != 0x80000000u) o[c][r] = fmaf(e, x, o[c][r]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (lane < 2) {  // the rows' statistics for the columns' threads
+      ps[2 * warp + lane] = (lane == 0 ? m[0] : m[1]) + kPrefixDrop;
+      al[2 * warp + lane] = lane == 0 ? l[0] : l[1];
+    }
+    __syncthreads();
+    const size_t place = (size_t)w.unit * a.sharers + w.place(blockIdx.x);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= nr) break;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = tid + 128 * c;
+        if (d >= D) continue;
+        if (!(fabsf(o[c][r]) < INFINITY) && al[r] > 0.f) {  // a weight of 0 times an infinity, or a value's own
+          const uint32_t odd = prefix_odd<T>(a, h, w.tile * P, min((w.tile + count) * P, length), d);
+          if (odd) o[c][r] = odd_value(odd);
+        }
+        a.part_o[((place * (D / 4) + d / 4) * a.row_tile + r) * 4 + d % 4] = o[c][r];
+      }
+      if (tid == 0)
+        *reinterpret_cast<float2*>(a.part_ml + (place * a.row_tile + r) * 2) = make_float2(ps[r], al[r]);
+    }
+    w.advance(count);
+  }
+}
+
+int simple_smem(int D) {
+  constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile;
+  return (R * D + P * (D + 1) + P * D + R * P + R) * 4;
+}
+
+cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st) {
+  auto kernel = dtype == SDV_F16 ? prefix_simple_kernel<__half> : prefix_simple_kernel<__nv_bfloat16>;
+  const int smem = simple_smem(a.D);
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(a.ctas), dim3(128), smem, st, a);
+}
+
+// ---- join -------------------------------------------------------------------------------
+
+constexpr int kMergeRows = 32, kMergeWarps = 8;
+
+// 32 rows of a row tile per block.  The partials lie row beside row, the outputs column beside
+// column: the rows' sums go through shared memory between the two.
+template <typename T>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_join_kernel(const PrefixArgs a, const AttnArgs own,
+                                                                        float* lse_or_null) {
+  extern __shared__ float sm[];
+  const int D = a.D, ld = D + 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* const so = sm;                                  // [32][D + 4]
+  float2* const sml = reinterpret_cast<float2*>(sm + kMergeRows * ld);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, r0 = blockIdx.y * kMergeRows;
+  const int per_head = (a.row_tiles + a.unit_tiles - 1) / a.unit_tiles;
+  const int unit = h * per_head + rt / a.unit_tiles, sub = rt % a.unit_tiles;
+  const int nr = min(a.row_tile, a.tokens * a.G - rt * a.row_tile);
+  bool bad;
+  PrefixWalk w;
+  w.tiles = prefix_tiles(a, prefix_length(a, bad));
+  w.total = (long long)w.tiles * a.units;
+  w.live = attn_live_ctas(a.ctas, w.total);
+  int parts = 0;
+  if (w.tiles > 0)
+    parts = attn_owner(w.total, w.live, (long long)unit * w.tiles + w.tiles - 1) -
+            attn_owner(w.total, w.live, (long long)unit * w.tiles) + 1;
+  {
+    const int r = r0 + lane;
+    const bool mine = r < nr;
+    for (int d4 = warp; d4 < D / 4; d4 += kMergeWarps) {
+      AttnSum sum;
+      for (int k0 = 0; mine && k0 < parts; k0 += 4) {
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          if (k0 + k >= parts) continue;
+          const size_t place = ((size_t)unit * a.sharers + k0 + k) * a.unit_tiles + sub;
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place * a.row_tile + r);
+          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (place * (D / 4) + d4) * a.row_tile + r);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.add<true>(ml[k].x, ml[k].y, x[k]);
+      }
+      *reinterpret_cast<float4*>(so + lane * ld + d4 * 4) = sum.o;
+      if (d4 == 0) sml[lane] = make_float2(sum.m, sum.l);
+    }
+  }
+  __syncthreads();
+  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
+    const int r = r0 + i;
+    if (r >= nr) break;
+    const int row = rt * a.row_tile + r, token = row / a.G;
+    const int b = token / own.S, s = token - b * own.S;
+    const bool live = s < attn_seq(own, b).n;
+    const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
+    const float lse = __ldcg(own.lse + orow);
+    for (int d4 = lane; d4 < D / 4; d4 += 32) {
+      AttnSum sum;
+      sum.m = sml[i].x;
+      sum.l = sml[i].y;
+      sum.o = *reinterpret_cast<const float4*>(so + i * ld + d4 * 4);
+      // the own positions' output is that of a sum of 1 at a maximum of their lse
+      if (lse != -INFINITY)
+        sum.add<true>(lse * 1.4426950408889634f, 1.f, __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4));
+      const bool none = !live || sum.l == 0.f;
+      const float inv = 1.f / sum.l;
+      const uint2 y = none ? make_uint2(0u, 0u)
+                           : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv), pack16<T>(sum.o.z * inv, sum.o.w * inv));
+      reinterpret_cast<uint2*>(static_cast<T*>(own.out) + orow * D)[d4] = y;
+      if (d4 == 0 && lse_or_null != nullptr) lse_or_null[orow] = none ? -INFINITY : sum.lse();
+    }
+  }
+}
+
+// `own`: the paged attention's arguments, out32 and lse where it has left its outputs, `out` the
+// call's own; lse_or_null: the call's.
+cudaError_t launch_prefix_join(int dtype, const PrefixArgs& a, const AttnArgs& own, float* lse_or_null,
+                               cudaStream_t st) {
+  auto kernel = dtype == SDV_F16 ? prefix_join_kernel<__half> : prefix_join_kernel<__nv_bfloat16>;
+  return launch_pdl(kernel, dim3(a.Hkv * a.row_tiles, (a.row_tile + kMergeRows - 1) / kMergeRows), dim3(32 * kMergeWarps),
+                    (size_t)kMergeRows * (a.D + 4) * 4 + kMergeRows * 8, st, a, own, lse_or_null);
+}
+
+constexpr int kSimplePerSm = 2;
+
+// Row tiles and units of a call; `tc`: of the tensor-core kernel.
+void set_units(PrefixArgs& a, bool tc, int sms) {
+  (void)tc;
+  a.row_tile = kPrefixSimpleRows;
+  a.row_tiles = (a.tokens * a.G + a.row_tile - 1) / a.row_tile;
+  a.unit_tiles = 1;
+  a.tile = kPrefixSimpleTile;
+  a.ctas = kSimplePerSm * sms;
+  a.units = a.Hkv * ((a.row_tiles + a.unit_tiles - 1) / a.unit_tiles);
+  // a unit's tiles take at most ceil(ctas / units) CTAs' ranges, and begin and end inside one
+  a.sharers = (a.ctas + a.units - 1) / a.units + 1;
+}
+
+struct PrefixBytes {
+  size_t part_ml, part_o, out32, lse, total;  // offsets
+};
+
+PrefixBytes prefix_layout(const PrefixArgs& a, size_t own, int B, int S, int Hq) {
+  const size_t rows = (size_t)a.units * a.sharers * a.unit_tiles * a.row_tile, outs = (size_t)B * S * Hq;
+  PrefixBytes p;
+  p.part_ml = round_256(own);
+  p.part_o = p.part_ml + round_256(rows * 8);
+  p.out32 = p.part_o + round_256(rows * a.D * 4);
+  p.lse = p.out32 + round_256(outs * a.D * 4);
+  p.total = p.lse + round_256(outs * 4);
+  return p;
+}
+
+PrefixArgs prefix_shape(int B, int S, int Hq, int heads, int dim, bool tc, int sms) {
+  PrefixArgs a{};
+  a.tokens = B * S;
+  a.Hq = Hq;
+  a.Hkv = heads;
+  a.G = Hq / heads;
+  a.D = dim;
+  set_units(a, tc, sms);
+  return a;
+}
+
+size_t prefix_need(int B, int S, int Hq, int heads, int dim) {
+  const size_t own = attn_bytes(B, S, Hq, heads, dim);
+  if (own == 0 || (long long)B * S * Hq > (1ll << 30)) return 0;
+  const int sms = sm_count() > 0 ? sm_count() : 256;
+  size_t most = 0;
+  for (int tc = 0; tc < 2; ++tc) {
+    const size_t n = prefix_layout(prefix_shape(B, S, Hq, heads, dim, tc, sms), own, B, S, Hq).total;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+}  // namespace
+
+}  // namespace sdv
+
+extern "C" {
+
+size_t sdv_prefix_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim) {
+  return sdv::prefix_need(B, S, Hq, heads, dim);
+}
+
+sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table, int32_t prefix_pages,
+                           const int32_t* prefix_len, const void* q, int64_t q_stride, int32_t B, int32_t S,
+                           int32_t Hq, const int32_t* ctx, const int32_t* n_rows_or_null,
+                           const uint32_t* mask_or_null, float scale, void* out, float* lse_or_null, void* ws,
+                           size_t ws_bytes, sdv_stream_t stream) {
+  const sdv_status ok = sdv::attn_check(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale, out,
+                                        lse_or_null);
+  if (ok != SDV_OK) return ok;
+  if (prefix_table == nullptr || prefix_len == nullptr || prefix_pages < 1 ||
+      ((reinterpret_cast<uintptr_t>(prefix_table) | reinterpret_cast<uintptr_t>(prefix_len)) & 3u) != 0)
+    return SDV_ERR_INVALID_ARG;
+  const size_t need = sdv::prefix_need(B, S, Hq, cache->heads, cache->dim);
+  if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
+  const int sms = sdv::sm_count();
+  if (sms <= 0) return SDV_ERR_CUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool tc = false;
+  sdv::PrefixArgs a = sdv::prefix_shape(B, S, Hq, cache->heads, cache->dim, tc, sms);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.table = prefix_table;
+  a.length = prefix_len;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.n_pages = cache->n_pages;
+  a.page = cache->page_size;
+  a.max_pages = prefix_pages;
+  a.status = static_cast<int*>(ws);
+  a.fault = sdv::debug_fault();
+  const sdv::PrefixBytes at = sdv::prefix_layout(a, sdv::attn_bytes(B, S, Hq, cache->heads, cache->dim), B, S, Hq);
+  char* const base = static_cast<char*>(ws);
+  a.part_ml = reinterpret_cast<float*>(base + at.part_ml);
+  a.part_o = reinterpret_cast<float*>(base + at.part_o);
+  sdv::AttnArgs own = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
+  own.out32 = reinterpret_cast<float*>(base + at.out32);
+  own.lse = reinterpret_cast<float*>(base + at.lse);
+  const cudaError_t e = sdv::launch_prefix_simple(cache->dtype, a, st);
+  if (e != cudaSuccess) return sdv::status_of(e);
+  const sdv_status run = sdv::attn_run(cache, own, ws, st);
+  if (run != SDV_OK) return run;
+  own.out = out;
+  own.tile = 1;  // (of no meaning to the join)
+  return sdv::status_of(sdv::launch_prefix_join(cache->dtype, a, own, lse_or_null, st));
+}
+
+}  // extern "C"

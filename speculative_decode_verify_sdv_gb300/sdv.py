@@ -17,7 +17,9 @@ LIB_PATH = os.path.join(_HERE, "libsdv.so")
 
 SDV_OK, SDV_ERR_INVALID_ARG, SDV_ERR_UNSUPPORTED, SDV_ERR_CUDA, SDV_ERR_TIMEOUT, SDV_ERR_WORKSPACE = range(6)
 SDV_Q8, SDV_Q4, SDV_F4 = 8, 4, 2
-SDV_F16, SDV_BF16 = 16, 17
+SDV_F16, SDV_BF16, SDV_F32 = 16, 17, 32
+SDV_ROPE_HALF, SDV_ROPE_PAIRS = 0, 1
+SDV_ROPE_PLAIN, SDV_ROPE_LINEAR, SDV_ROPE_BASE, SDV_ROPE_RAMP, SDV_ROPE_BANDS = range(5)
 SDV_OP_QLINEAR, SDV_OP_QLINEAR_SWIGLU, SDV_OP_VERIFY_HEAD, SDV_OP_MOE, SDV_OP_VERIFY_SAMPLE = 1, 2, 3, 4, 5
 
 EXPORTED = (
@@ -27,7 +29,9 @@ EXPORTED = (
     "sdv_moe_route", "sdv_verify_sample", "sdv_tree_accept", "sdv_debug_fault",
     "sdv_ngram_create", "sdv_ngram_destroy", "sdv_ngram_append", "sdv_ngram_propose",
     "sdv_kv_append", "sdv_paged_attn", "sdv_paged_attn_workspace_bytes", "sdv_linear_attn",
-    "sdv_linear_attn_workspace_bytes",
+    "sdv_linear_attn_workspace_bytes", "sdv_page_assign", "sdv_page_assign_workspace_bytes", "sdv_rope_steps",
+    "sdv_qk_norm_rope", "sdv_prefix_attn", "sdv_prefix_attn_workspace_bytes", "sdv_verify_drafts",
+    "sdv_verify_drafts_workspace_bytes",
 )
 
 
@@ -46,6 +50,22 @@ class sdv_kvcache(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("dim", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
+class sdv_pagepool(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("held", ctypes.c_void_p)]
+
+
+class sdv_rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("steps", ctypes.c_void_p)]
+
+
+class sdv_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("trained", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
 _lib = None
@@ -95,6 +115,16 @@ def load() -> ctypes.CDLL:
         "sdv_linear_attn": ([i32, vp, vp, vp, i64, i64, i64, vp, i32, f32, i32, i32, i32, i32, i32, i32, vp, vp, vp,
                              vp, vp, sz, vp], i32),
         "sdv_linear_attn_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "sdv_page_assign": ([ctypes.POINTER(sdv_pagepool), i32, i32, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "sdv_page_assign_workspace_bytes": ([i32], sz),
+        "sdv_rope_steps": ([i32, ctypes.c_double, ctypes.POINTER(sdv_rope_scaling), ctypes.POINTER(ctypes.c_uint64),
+                            ctypes.POINTER(f32)], i32),
+        "sdv_qk_norm_rope": ([kvc, i32, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, vp, f32,
+                              ctypes.POINTER(sdv_rope), vp, vp, vp, vp, vp], i32),
+        "sdv_prefix_attn": ([kvc, vp, i32, vp, vp, i64, i32, i32, i32, vp, vp, vp, f32, vp, vp, vp, sz, vp], i32),
+        "sdv_prefix_attn_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "sdv_verify_drafts": ([i32, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "sdv_verify_drafts_workspace_bytes": ([i32, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -442,6 +472,161 @@ def sdv_linear_attn(q, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor
         _check("sdv_linear_attn", st)
 
 
+# ---- around a batched round: pages, positions, a shared prefix, drafted tokens ----
+
+def sdv_page_assign_workspace_bytes(B: int) -> int:
+    return int(load().sdv_page_assign_workspace_bytes(B))
+
+
+def sdv_prefix_attn_workspace_bytes(B: int, S: int, Hq: int, heads: int, dim: int) -> int:
+    return int(load().sdv_prefix_attn_workspace_bytes(B, S, Hq, heads, dim))
+
+
+def sdv_verify_drafts_workspace_bytes(B: int, S: int, V: int) -> int:
+    return int(load().sdv_verify_drafts_workspace_bytes(B, S, V))
+
+
+def sdv_page_assign(free_pages: torch.Tensor, n_free: torch.Tensor, table: torch.Tensor, held: torch.Tensor,
+                    page_size: int, ctx: torch.Tensor, n_rows, granted, positions, slots, ws: torch.Tensor,
+                    stream=None, T=None) -> None:
+    """Pages of table [B, max_pages] for n_rows [B] rows behind ctx [B], from and to the stack
+    free_pages [n_pages] of n_free [1]; granted [B], positions and slots [B, T] or None (T: the
+    most rows of a sequence where both are None, 1 if left out).  All int32."""
+    i32 = torch.int32
+    if table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("free_pages is [n_pages], table is [B, max_pages]")
+    B = table.shape[0]
+    for t in (positions, slots):
+        if t is not None:
+            if t.dim() != 2:
+                raise ValueError("positions and slots are [B, T]")
+            T = t.shape[1] if T is None else T
+    T = 1 if T is None else T
+    pool = sdv_pagepool(free_pages.shape[0], page_size, table.shape[1], _addr(free_pages, i32, "free_pages"),
+                        _addr(n_free, i32, "n_free", (1,)), _addr(table, i32, "table"), _addr(held, i32, "held", (B,)))
+    st = load().sdv_page_assign(
+        ctypes.byref(pool), B, T, _addr(ctx, i32, "ctx", (B,)), _addr(n_rows, i32, "n_rows", (B,)),
+        _addr(granted, i32, "granted", (B,)), _addr(positions, i32, "positions", (B, T)),
+        _addr(slots, i32, "slots", (B, T)), _addr(ws, ws.dtype, "ws"), ws.nbytes, _raw_stream(stream, table.device))
+    if st:
+        _check("sdv_page_assign", st)
+
+
+def sdv_rope_steps(rot_dim: int, theta: float, kind: int = SDV_ROPE_PLAIN, factor: float = 1.0, trained: int = 1,
+                   low: float = 1.0, high: float = 2.0) -> tuple[list[int], float]:
+    """(steps, amplitude): turns per position of each pair in units of 2^-64 (host arithmetic)."""
+    steps = (ctypes.c_uint64 * max(rot_dim // 2, 1))()
+    amplitude = ctypes.c_float(0.0)
+    scaling = sdv_rope_scaling(kind, trained, factor, low, high)
+    _check("sdv_rope_steps", load().sdv_rope_steps(rot_dim, theta, ctypes.byref(scaling), steps,
+                                                   ctypes.byref(amplitude)))
+    return list(steps), float(amplitude.value)
+
+
+class Rope:
+    """A rotation's plan: layout, rot_dim, amplitude and the steps on the GPU."""
+
+    def __init__(self, layout: int, rot_dim: int, amplitude: float, steps: torch.Tensor):
+        self.layout, self.rot_dim, self.amplitude, self.steps = layout, rot_dim, amplitude, steps
+
+    def c(self) -> sdv_rope:
+        return sdv_rope(self.layout, self.rot_dim, self.amplitude,
+                        _addr(self.steps, torch.int64, "steps", (self.rot_dim // 2,)))
+
+
+def sdv_qk_norm_rope(q, k, v, k_pages: torch.Tensor, v_pages: torch.Tensor, q_weight, k_weight, eps: float, rope,
+                     positions: torch.Tensor, slots, q_out, ws, stream=None) -> None:
+    """Norms (weights fp32 [dim] or None) and rotation (a Rope or None) of q [B, T, Hq, dim] and
+    k [B, T, heads, dim]; q goes to q_out, k and v into the cache at slots.  q with q_out, or k with
+    v and slots, may be None; positions and slots int32 [B, T]; ws: for the device status, or None."""
+    dt, i32, f32 = k_pages.dtype, torch.int32, torch.float32
+    if dt not in _DTYPES:
+        raise TypeError(f"a cache is float16 or bfloat16, got {dt}")
+    if k_pages.dim() != 4 or positions.dim() != 2:
+        raise ValueError("k_pages and v_pages are [n_pages, heads, page_size, dim], positions is [B, T]")
+    n, heads, page, dim = k_pages.shape
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k and v must be given")
+    ty = first.dtype
+    if ty != dt and ty != f32:
+        raise TypeError(f"rows are {dt} as the cache or float32, got {ty}")
+    B, T = positions.shape
+    c = sdv_kvcache(_DTYPES[dt], n, heads, page, dim, 1, _addr(k_pages, dt, "k_pages"),
+                    _addr(v_pages, dt, "v_pages", k_pages.shape), None)
+    hq = 0 if q is None else q.shape[2] if q.dim() == 4 else -1
+    qa, qs = (None, 0) if q is None else _rows(q, ty, "q", B, T, hq, dim)
+    ka, ks = (None, 0) if k is None else _rows(k, ty, "k", B, T, heads, dim)
+    va, vs = (None, 0) if v is None else _rows(v, ty, "v", B, T, heads, dim)
+    if ws is not None and ws.nbytes < 256:
+        raise ValueError("ws must hold at least 256 bytes")
+    r = None if rope is None else rope.c()
+    st = load().sdv_qk_norm_rope(
+        ctypes.byref(c), SDV_F32 if ty == f32 else _DTYPES[dt], qa, ka, va, qs, ks, vs, B, T, hq,
+        _addr(q_weight, f32, "q_weight", (dim,)), _addr(k_weight, f32, "k_weight", (dim,)), eps,
+        None if r is None else ctypes.byref(r), _addr(positions, i32, "positions"), _addr(slots, i32, "slots", (B, T)),
+        _addr(q_out, dt, "q_out", (B, T, hq, dim)), None if ws is None else _addr(ws, ws.dtype, "ws"),
+        _raw_stream(stream, first.device))
+    if st:
+        _check("sdv_qk_norm_rope", st)
+
+
+def sdv_prefix_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                    prefix_len: torch.Tensor, table: torch.Tensor, ctx: torch.Tensor, n_rows, mask, scale: float,
+                    out: torch.Tensor, lse, ws: torch.Tensor, stream=None) -> None:
+    """sdv_paged_attn behind a prefix of prefix_len [1] positions in the pages prefix_table
+    [prefix_pages], shared by all sequences; the other arguments are of what follows it."""
+    c = _kvcache(k_pages, v_pages, table)
+    B, S, hq = q.shape[:3]
+    i32 = torch.int32
+    dt = k_pages.dtype
+    qa, qs = _rows(q, dt, "q", B, S, hq, c.dim)
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table is [prefix_pages]")
+    st = load().sdv_prefix_attn(
+        ctypes.byref(c), _addr(prefix_table, i32, "prefix_table"), prefix_table.shape[0],
+        _addr(prefix_len, i32, "prefix_len", (1,)), qa, qs, B, S, hq, _addr(ctx, i32, "ctx", (B,)),
+        _addr(n_rows, i32, "n_rows", (B,)), _addr(mask, i32, "mask", (B, S)), scale, _addr(out, dt, "out", q.shape),
+        _addr(lse, torch.float32, "lse", (B, S, hq)), _addr(ws, ws.dtype, "ws"), ws.nbytes,
+        _raw_stream(stream, q.device))
+    if st:
+        _check("sdv_prefix_attn", st)
+
+
+def sdv_verify_drafts(logits: torch.Tensor, temperature: torch.Tensor, drafts, n_drafts, draft_probs,
+                      uniforms: torch.Tensor, accepted: torch.Tensor, next_token: torch.Tensor, ws: torch.Tensor,
+                      stream=None) -> None:
+    """Drafts [B, S - 1] against the target's logits [B, S, V] (fp32 or 16-bit; rows evenly strided)
+    at temperature [B], by uniforms [B, S]; draft_probs fp32 [B, S - 1, V] or None (a deterministic
+    drafter), n_drafts [B] or None; accepted and next_token int32 [B]."""
+    dtype = SDV_F32 if logits.dtype == torch.float32 else _DTYPES.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits are float32, float16 or bfloat16, got {logits.dtype}")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dim() != 3:
+        raise ValueError("logits are [B, S, V]")
+    B, S, V = logits.shape
+    sb, st, sv = logits.stride()
+    if S == 1:
+        st = sb if B > 1 else V
+    if (sv != 1 and V > 1) or (B > 1 and sb != S * st):
+        raise ValueError("logits: a row must be contiguous and the rows evenly strided")
+    i32, f32 = torch.int32, torch.float32
+    if S == 1:  # no drafts: whatever is given for them is empty
+        drafts = draft_probs = None
+    st = load().sdv_verify_drafts(
+        dtype, logits.data_ptr(), st, B, S, V, _addr(temperature, f32, "temperature", (B,)),
+        _addr(drafts, i32, "drafts", (B, S - 1)), _addr(n_drafts, i32, "n_drafts", (B,)),
+        _addr(draft_probs, f32, "draft_probs", (B, S - 1, V)), _addr(uniforms, f32, "uniforms", (B, S)),
+        _addr(accepted, i32, "accepted", (B,)), _addr(next_token, i32, "next_token", (B,)), _addr(ws, ws.dtype, "ws"),
+        ws.nbytes, _raw_stream(stream, logits.device))
+    if st:
+        _check("sdv_verify_drafts", st)
+
+
 # ---- host n-gram drafter (host pointers; no GPU involved) -------------------------
 
 def sdv_ngram_create(m: int) -> int:
@@ -499,3 +684,42 @@ def linear_attn_workspace(k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
     B, T = k.shape[:2]
     nbytes = max(sdv_linear_attn_workspace_bytes(B, T, v.shape[2], k.shape[3], v.shape[3]), 256)
     return torch.zeros(nbytes, dtype=torch.uint8, device=k.device)
+
+
+def page_assign_workspace(ctx: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for sdv_page_assign calls of up to this many sequences (ctx [B])."""
+    nbytes = max(sdv_page_assign_workspace_bytes(ctx.shape[0]), 256)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=ctx.device)
+
+
+def prefix_attn_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for sdv_prefix_attn calls of this shape and of smaller batches and windows
+    (q [B, S, Hq, dim])."""
+    B, S, hq, dim = q.shape
+    nbytes = max(sdv_prefix_attn_workspace_bytes(B, S, hq, k_pages.shape[1], dim), 256)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+
+
+def verify_drafts_workspace(logits: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for sdv_verify_drafts calls of this shape and of smaller batches (logits
+    [B, S, V])."""
+    nbytes = max(sdv_verify_drafts_workspace_bytes(*logits.shape), 256)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=logits.device)
+
+
+_LAYOUTS = {"half": SDV_ROPE_HALF, "pairs": SDV_ROPE_PAIRS}
+_SCALINGS = {None: SDV_ROPE_PLAIN, "linear": SDV_ROPE_LINEAR, "base": SDV_ROPE_BASE, "ramp": SDV_ROPE_RAMP,
+             "bands": SDV_ROPE_BANDS}
+
+
+def rope_plan(rot_dim: int, theta: float, layout: str, scaling=None, factor: float = 1.0, trained: int = 1,
+              low: float = 1.0, high: float = 2.0, device="cuda") -> Rope:
+    """A rotation of the first rot_dim elements of a head, layout "half" or "pairs"; scaling None, "linear",
+    "base", "ramp" or "bands" (see sdv_rope_scaling in the header)."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be None or one of {sorted(k for k in _SCALINGS if k)}, got {scaling!r}")
+    steps, amplitude = sdv_rope_steps(rot_dim, theta, _SCALINGS[scaling], factor, trained, low, high)
+    signed = [x - 2 ** 64 if x >= 2 ** 63 else x for x in steps]
+    return Rope(_LAYOUTS[layout], rot_dim, amplitude, torch.tensor(signed, dtype=torch.int64, device=device))

@@ -1,0 +1,247 @@
+"""sdv_prefix_attn on the GPU against the 64-bit oracle: attention over a shared prefix and each
+sequence's own positions is attention over both.
+
+Tolerances as for sdv_paged_attn (tests/test_gpu_paged_attn.py): from the operation alone, with
+one merge more of the same kind.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rounds
+from tests.test_gpu_paged_attn import as_i32, check, f64, words
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sdv():
+    from speculative_decode_verify_sdv_gb300 import build, sdv as _sdv
+    build.build()
+    _sdv.load()
+    return _sdv
+
+
+def make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, seed, std=1.7):
+    """A cache of randomly placed pages with NaN in every slot that nothing uses."""
+    gen = torch.Generator().manual_seed(seed)
+    need = [-(-(c + r) // page) for c, r in zip(ctx, n)]
+    front = -(-prefix // page)
+    pages, width = sum(need) + front + 3, max(max(need), 1)
+    ids = torch.randperm(pages, generator=gen).tolist()
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    ptable = torch.tensor(ids[:front] + [-1], dtype=torch.int32)
+    kp = torch.full((pages, hkv, page, d), float("nan"), dtype=dt)
+    vp = kp.clone()
+    at = front
+
+    def fill(page_id, used):
+        for x in (kp, vp):
+            x[page_id, :, :used] = torch.randn((hkv, used, d), generator=gen).to(dt)
+
+    for j in range(front):
+        fill(ids[j], min(page, prefix - j * page))
+    for b in range(B):
+        for j in range(need[b]):
+            table[b, j] = ids[at]
+            fill(ids[at], min(page, ctx[b] + n[b] - j * page))
+            at += 1
+    q = (torch.randn((B, S, hq, d), generator=gen) * std).to(dt)
+    return q, kp, vp, ptable, table
+
+
+def dev(x):
+    return None if x is None else torch.as_tensor(x, dtype=torch.int32).cuda()
+
+
+def call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, mask, scale, want_lse=True, ws=None, stream=None):
+    q, kp, vp, ptable, table = (x if x.is_cuda else x.cuda() for x in (q, kp, vp, ptable, table))
+    out = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:3], float("nan"), dtype=torch.float32, device="cuda") if want_lse else None
+    ws = sdv.prefix_attn_workspace(q, kp, table) if ws is None else ws
+    sdv.sdv_prefix_attn(q, kp, vp, ptable, dev([prefix]), table, dev(ctx), dev(n), dev(mask), scale, out, lse, ws,
+                        stream)
+    return out, lse, ws
+
+
+def reference(q, kp, vp, ptable, prefix, table, ctx, n, mask, scale):
+    return rounds.prefix_attention(f64(q), f64(kp), f64(vp), ptable.tolist(), prefix, table.tolist(), ctx, n, mask,
+                                   scale)
+
+
+SHAPES = [
+    # dtype, B, S, Hq, Hkv, D, page, prefix, ctx, n, mask
+    (F16, 1, 1, 1, 1, 128, 16, 1, [0], [1], False),
+    (F16, 2, 1, 8, 2, 128, 16, 129, [0, 5], [1, 1], False),
+    (BF16, 3, 1, 8, 2, 128, 16, 1000, [17, 0, 300], [1, 1, 1], False),
+    (BF16, 5, 1, 4, 4, 64, 64, 127, [0, 63, 64, 255, 511], [1] * 5, False),
+    (F16, 3, 1, 6, 1, 256, 32, 64, [62, 63, 700], [1] * 3, False),
+    (F16, 4, 9, 16, 2, 256, 64, 801, [7, 0, 90, 33], [9, 6, 3, 9], True),
+    (BF16, 40, 5, 8, 2, 128, 32, 640, [3 * i for i in range(40)], [5] * 40, False),   # 800 rows of a kv head
+    (F16, 33, 1, 28, 4, 128, 8, 300, [i for i in range(33)], [1] * 33, False),        # a group of 7
+    (BF16, 20, 32, 4, 1, 64, 16, 333, [i * 7 for i in range(20)], [32 - i for i in range(20)], True),
+    (F16, 70, 1, 64, 1, 128, 128, 500, [0] * 70, [1] * 70, False),                    # rows of 64 heads
+    (F16, 2, 2, 128, 1, 128, 16, 200, [0, 9], [2, 1], False),                         # a token a row tile
+    (BF16, 6, 4, 24, 8, 64, 16, 15, [0] * 6, [4, 0, 1, 2, 3, 4], True),
+    (BF16, 2, 3, 8, 2, 128, 16, 0, [40, 0], [3, 3], False),                           # no prefix
+    (F16, 1, 1, 8, 1, 128, 64, 5003, [3], [1], False),
+    (BF16, 9, 2, 8, 8, 256, 16, 1500, [1] * 9, [2] * 9, False),
+    # head and page sizes outside the tensor-core kernel's, a group of more than 128
+    (F16, 2, 3, 4, 2, 40, 16, 100, [33, 200], [3, 2], True),
+    (BF16, 2, 1, 4, 1, 8, 5, 33, [0, 77], [1, 1], False),
+    (F16, 3, 5, 4, 2, 128, 1, 70, [30, 3, 0], [5, 5, 5], False),
+    (BF16, 4, 6, 4, 1, 96, 48, 400, [40, 0, 1, 2], [6] * 4, True),
+    (F16, 2, 2, 2, 2, 248, 20, 61, [39, 41], [2, 2], True),
+    (F16, 1, 2, 130, 1, 64, 16, 70, [5], [2], False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_matches_the_oracle(sdv, case):
+    dt, B, S, hq, hkv, d, page, prefix, ctx, n, masked = SHAPES[case]
+    q, kp, vp, ptable, table = make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, 300 + case)
+    mask = words(np.random.default_rng(case), B, S) if masked else None
+    im = None if mask is None else as_i32(mask)
+    scale = d ** -0.5
+    out, lse, ws = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, im, scale)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    ref = reference(q, kp, vp, ptable, prefix, table, ctx, n, mask, scale)
+    check(dt, ref, out, lse, d)
+    # the same call again, and without lse: the same bits
+    out2, _, _ = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, im, scale, want_lse=False, ws=ws)
+    assert torch.equal(out2, out)
+
+
+@pytest.mark.parametrize("d,page", [(128, 16), (256, 16), (64, 128), (96, 16)])
+def test_every_length_around_a_tile(sdv, d, page):
+    B, S, hq, hkv = 3, 2, 4, 1
+    for prefix in (1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257):
+        ctx, n = [0, 1, 30], [2, 1, 2]
+        q, kp, vp, ptable, table = make(F16, B, S, hq, hkv, d, page, prefix, ctx, n, prefix)
+        out, lse, _ = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, None, 0.2)
+        check(F16, reference(q, kp, vp, ptable, prefix, table, ctx, n, None, 0.2), out, lse, d)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
+def test_scales(sdv, scale):
+    ctx, n = [20, 3], [2, 2]
+    q, kp, vp, ptable, table = make(BF16, 2, 2, 8, 2, 128, 16, 300, ctx, n, 7, std=1.0)
+    out, lse, _ = call(sdv, q, kp, vp, ptable, 300, table, ctx, n, None, scale)
+    check(BF16, reference(q, kp, vp, ptable, 300, table, ctx, n, None, scale), out, lse, 128)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 96])
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_infinities_and_nan_of_seen_values_arrive(sdv, dt, d):
+    """Every live row sees the whole prefix: what is not finite there reaches all of them, in
+    its column, however small its weight; the rows of dead windows stay 0."""
+    ctx, n = [20, 3, 0], [2, 1, 0]
+    q, kp, vp, ptable, table = make(dt, 3, 2, 8, 2, d, 16, 400, ctx, n, 8, std=20.0)
+    at = lambda p: (int(ptable[p // 16]), p % 16)  # noqa: E731
+    for p, h, c, x in ((3, 0, 1, float("inf")), (390, 0, 5, float("nan")), (140, 1, 7, float("-inf")),
+                       (5, 1, 9, float("inf")), (391, 1, 9, float("-inf"))):
+        page, slot = at(p)
+        vp[page, h, slot, c] = x
+    out, lse, _ = call(sdv, q, kp, vp, ptable, 400, table, ctx, n, None, d ** -0.5)
+    out = out.float().cpu()
+    for b, i in ((0, 0), (0, 1), (1, 0)):
+        for h in range(8):
+            row = out[b, i, h]
+            odd = {1: float("inf"), 5: float("nan")} if h < 4 else {7: float("-inf"), 9: float("nan")}
+            for c in range(d):
+                if c not in odd:
+                    assert torch.isfinite(row[c])
+                elif odd[c] != odd[c]:
+                    assert torch.isnan(row[c])
+                else:
+                    assert row[c] == odd[c]
+    assert not out[1, 1].any() and not out[2].any()
+
+
+def test_large_values_do_not_overflow(sdv):
+    """bf16 values near the type's largest, weights spread over many positions."""
+    ctx, n = [20, 3], [1, 1]
+    q, kp, vp, ptable, table = make(BF16, 2, 1, 8, 2, 128, 16, 700, ctx, n, 9, std=0.1)
+    vp = torch.where(torch.isnan(vp), vp, torch.full_like(vp, 2.0 ** 127))
+    out, _, _ = call(sdv, q, kp, vp, ptable, 700, table, ctx, n, None, 0.1)
+    assert torch.all((out.float() / 2.0 ** 127 - 1.0).abs() <= 2.0 ** -6)
+
+
+def test_absent_pages_and_lengths_out_of_range(sdv):
+    """Positions behind an entry that is not a page are absent, and reported, lengths clamped."""
+    ctx, n = [20, 3], [2, 2]
+    for d in (128, 96):
+        q, kp, vp, ptable, table = make(F16, 2, 2, 8, 2, d, 16, 320, ctx, n, 10)
+        bad = ptable.clone()
+        bad[5], bad[19] = -1, kp.shape[0]
+        out, lse, ws = call(sdv, q, kp, vp, bad, 320, table, ctx, n, None, 0.1)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+        keep = torch.cat([ptable[:5], ptable[6:19]])
+        ref = reference(q, kp, vp, keep, 288, table, ctx, n, None, 0.1)
+        check(F16, ref, out, lse, d)
+        # the table names 21 pages, the last of which is none: 336 positions at most
+        out, lse, ws = call(sdv, q, kp, vp, ptable, 5000, table, ctx, n, None, 0.1)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+        check(F16, reference(q, kp, vp, ptable, 320, table, ctx, n, None, 0.1), out, lse, d)
+        out, lse, ws = call(sdv, q, kp, vp, ptable, -3, table, ctx, n, None, 0.1)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+        check(F16, reference(q, kp, vp, ptable, 0, table, ctx, n, None, 0.1), out, lse, d)
+
+
+def test_queries_of_a_fused_projection_and_nan_of_dead_rows(sdv):
+    ctx, n = [20, 3, 0], [2, 1, 0]
+    q, kp, vp, ptable, table = make(F16, 3, 2, 8, 2, 128, 16, 400, ctx, n, 11)
+    want, wl, _ = call(sdv, q, kp, vp, ptable, 400, table, ctx, n, None, 0.1)
+    wide = torch.full((3, 2, 14, 128), float("nan"), dtype=F16, device="cuda")
+    wide[:, :, 3:11] = q.cuda()
+    wide[1, 1], wide[2] = float("nan"), float("inf")
+    out, lse, _ = call(sdv, wide[:, :, 3:11], kp, vp, ptable, 400, table, ctx, n, None, 0.1)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_one_workspace_captured_and_shared(sdv):
+    """Two captured calls of other shapes on one workspace, replayed in turn; the same bits."""
+    calls = []
+    for dt, B, S, d, prefix, seed in ((F16, 3, 2, 128, 500, 1), (BF16, 30, 3, 64, 1000, 2), (F16, 2, 2, 96, 90, 3)):
+        ctx, n = [5 * i for i in range(B)], [S] * B
+        made = make(dt, B, S, 8, 2, d, 16, prefix, ctx, n, seed)
+        made = [x.cuda() for x in made]
+        calls.append((made, prefix, ctx, n, call(sdv, *made[:4], prefix, made[4], ctx, n, None, 0.1)[0]))
+    size = max(sdv.prefix_attn_workspace(c[0][0], c[0][1], c[0][4]).numel() for c in calls)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for made, prefix, ctx, n, want in calls:
+        q, kp, vp, ptable, table = made
+        out = torch.zeros_like(q)
+        fixed = (dev([prefix]), table, dev(ctx), dev(n), None, 0.1, out, None, ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sdv.sdv_prefix_attn(q, kp, vp, ptable, *fixed)
+        graphs.append((graph, out, want, fixed))
+    for _ in range(3):
+        for graph, out, want, _ in graphs:
+            out.zero_()
+            graph.replay()
+        for _, out, want, _ in graphs:
+            assert torch.equal(out, want)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+
+
+def test_the_binding_refuses_layouts_and_shapes(sdv):
+    q, kp, vp, ptable, table = (x.cuda() for x in make(F16, 2, 2, 8, 2, 64, 16, 100, [0, 3], [2, 2], 12))
+    i, out = dev([0, 3]), torch.zeros_like(q)
+    ws = sdv.prefix_attn_workspace(q, kp, table)
+    ok = dict(q=q, k_pages=kp, v_pages=vp, prefix_table=ptable, prefix_len=dev([100]), table=table, ctx=i, n_rows=None,
+              mask=None, scale=0.1, out=out, lse=None, ws=ws)
+    sdv.sdv_prefix_attn(**ok)
+    for kw in (dict(prefix_table=ptable[None]), dict(prefix_len=i), dict(table=table[:1]), dict(ctx=i[:1]),
+               dict(prefix_table=ptable[::2]), dict(out=out[..., :32])):
+        with pytest.raises(ValueError):
+            sdv.sdv_prefix_attn(**{**ok, **kw})
+    for kw in (dict(prefix_len=dev([100]).long()), dict(prefix_table=ptable.float()), dict(q=q.bfloat16())):
+        with pytest.raises(TypeError):
+            sdv.sdv_prefix_attn(**{**ok, **kw})
+    with pytest.raises(sdv.SdvError) as e:
+        sdv.sdv_prefix_attn(**{**ok, "ws": ws[:ws.numel() // 2]})
+    assert e.value.status == sdv.SDV_ERR_WORKSPACE
