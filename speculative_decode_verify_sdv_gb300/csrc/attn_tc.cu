@@ -23,9 +23,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// The cache as rows of dim elements: boxes of 64 elements x one page's rows of a
-// tile, 128-byte swizzle.
-bool page_map(const void* pages, bool bf16, uint64_t rows, int dim, int box_rows, CUtensorMap* map) {
+}  // namespace
+
+bool attn_page_map(const void* pages, bool bf16, uint64_t rows, int dim, int box_rows, CUtensorMap* map) {
   auto enc = encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)dim, rows};
@@ -38,22 +38,19 @@ bool page_map(const void* pages, bool bf16, uint64_t rows, int dim, int box_rows
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The query rows as [B * S][Hq][dim]: boxes of 64 elements x a group's heads x a row
-// tile's window rows, which land as the MMA's rows in order.
-bool query_map(const AttnArgs& a, bool bf16, CUtensorMap* map) {
+bool attn_query_map(const void* q, bool bf16, long long tokens, int heads, int group, int dim, long long stride,
+                    int box_tokens, CUtensorMap* map) {
   auto enc = encoder();
   if (enc == nullptr) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.S};
-  cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)a.tile_wrows};
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 cudaError_t attn_tc_bf16(const AttnMaps& m, const AttnArgs& a, cudaStream_t st);
 
@@ -67,7 +64,8 @@ cudaError_t launch_attn_tc(int dtype, const AttnArgs& a, cudaStream_t st) {
   const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * a.page;
   const int box = a.page < a.tile ? a.page : a.tile;
   const bool bf = dtype == SDV_BF16;
-  if (!page_map(a.k, bf, rows, a.D, box, &m.k) || !page_map(a.v, bf, rows, a.D, box, &m.v) || !query_map(a, bf, &m.q))
+  if (!attn_page_map(a.k, bf, rows, a.D, box, &m.k) || !attn_page_map(a.v, bf, rows, a.D, box, &m.v) ||
+      !attn_query_map(a.q, bf, (long long)a.B * a.S, a.Hq, a.G, a.D, a.q_stride, a.tile_wrows, &m.q))
     return cudaErrorUnknown;
   return bf ? attn_tc_bf16(m, a, st) : attn_tc_dispatch<__half>(m, a, st);
 }

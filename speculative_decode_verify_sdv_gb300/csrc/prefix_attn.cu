@@ -20,6 +20,7 @@
 #include "mixing.h"
 #include "paged_attn.h"
 #include "prefix_attn.cuh"
+#include "prefix_tc.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
 
@@ -282,12 +283,23 @@ constexpr int kSimplePerSm = 2;
 
 // Row tiles and units of a call; `tc`: of the tensor-core kernel.
 void set_units(PrefixArgs& a, bool tc, int sms) {
-  (void)tc;
-  a.row_tile = kPrefixSimpleRows;
-  a.row_tiles = (a.tokens * a.G + a.row_tile - 1) / a.row_tile;
-  a.unit_tiles = 1;
-  a.tile = kPrefixSimpleTile;
-  a.ctas = kSimplePerSm * sms;
+  if (tc) {
+    // whole tokens, at most 128 rows, tiles of equal size
+    const int most = a.G < kPrefixTcRows ? kPrefixTcRows / a.G : 1;
+    a.row_tiles = (a.tokens + most - 1) / most;
+    a.tile_tokens = (a.tokens + a.row_tiles - 1) / a.row_tiles;
+    a.row_tiles = (a.tokens + a.tile_tokens - 1) / a.tile_tokens;
+    a.row_tile = a.tile_tokens * a.G;
+    a.unit_tiles = prefix_tc_streams(a.D, a.row_tiles);
+    a.tile = kPrefixTcTile;
+    a.ctas = sms;
+  } else {
+    a.row_tile = kPrefixSimpleRows;
+    a.row_tiles = (a.tokens * a.G + a.row_tile - 1) / a.row_tile;
+    a.unit_tiles = 1;
+    a.tile = kPrefixSimpleTile;
+    a.ctas = kSimplePerSm * sms;
+  }
   a.units = a.Hkv * ((a.row_tiles + a.unit_tiles - 1) / a.unit_tiles);
   // a unit's tiles take at most ceil(ctas / units) CTAs' ranges, and begin and end inside one
   a.sharers = (a.ctas + a.units - 1) / a.units + 1;
@@ -357,7 +369,8 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   const int sms = sdv::sm_count();
   if (sms <= 0) return SDV_ERR_CUDA;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool tc = false;
+  const bool tc = sdv::attn_tc_takes(cache->dim, Hq / cache->heads, cache->page_size,
+                                     (long long)cache->n_pages * cache->heads * cache->page_size);
   sdv::PrefixArgs a = sdv::prefix_shape(B, S, Hq, cache->heads, cache->dim, tc, sms);
   a.q = q;
   a.q_stride = q_stride;
@@ -378,7 +391,8 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   sdv::AttnArgs own = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
   own.out32 = reinterpret_cast<float*>(base + at.out32);
   own.lse = reinterpret_cast<float*>(base + at.lse);
-  const cudaError_t e = sdv::launch_prefix_simple(cache->dtype, a, st);
+  const cudaError_t e =
+      tc ? sdv::launch_prefix_tc(cache->dtype, a, st) : sdv::launch_prefix_simple(cache->dtype, a, st);
   if (e != cudaSuccess) return sdv::status_of(e);
   const sdv_status run = sdv::attn_run(cache, own, ws, st);
   if (run != SDV_OK) return run;

@@ -191,11 +191,6 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftA
 struct Pair {  // two numbers, each the sum of two floats
   f32x2 hi, lo;
 };
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
 __device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return add2(a, neg2(b)); }
 __device__ __forceinline__ f32x2 both(float x) { return pair2(x, x); }
