@@ -257,31 +257,47 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const __grid_constant_
 constexpr int kJoinItems = 64, kJoinParts = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const AttnArgs a, bool by_cta) {
   __shared__ float4 so[kJoinParts][kJoinItems];
   __shared__ float2 sml[kJoinParts][kJoinItems];
   const int lane = threadIdx.x & 31;
   // The split first, before the attention launch has ended: lengths are inputs, and
   // whatever wrote them had ended before that launch let this one start.
-  const int units = a.Hkv * a.row_tiles;
-  const int b = blockIdx.x / units, unit = blockIdx.x % units;
-  long long before = 0, all = 0;
-  for (int s = lane; s < a.B; s += 32) {
-    const int t = attn_seq(a, s).tiles + a.lead;
-    all += t;
-    if (s < b) before += t;
-  }
+  int unit, c0, c1;
+  AttnWalk w;
+  if (by_cta) {
+    // the unit that the first tile of a CTA's range lies inside, by its second sharer
+    const int c = blockIdx.x + 1;
+    const bool some = w.start(a, c, lane);
+    griddep_wait();
+    if (!some || w.tile == 0) return;
+    w.sharers(c0, c1);
+    if (c0 != c - 1) return;
+    unit = w.unit;
+  } else {
+    const int units = a.Hkv * a.row_tiles;
+    w.b = blockIdx.x / units;
+    unit = blockIdx.x % units;
+    long long before = 0, all = 0;
+    for (int s = lane; s < a.B; s += 32) {
+      const int t = attn_seq(a, s).tiles + a.lead;
+      all += t;
+      if (s < w.b) before += t;
+    }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
+    for (int off = 16; off > 0; off >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, off);
+      before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    const AttnSeq seq = attn_seq(a, w.b);
+    const long long total = all * units, first = before * units + (long long)unit * (seq.tiles + a.lead) + a.lead;
+    const int live = attn_live_ctas(a.ctas, total);
+    c0 = attn_owner(total, live, first);
+    c1 = attn_owner(total, live, first + seq.tiles - 1);
+    griddep_wait();
+    if (c0 == c1) return;
   }
-  const AttnSeq seq = attn_seq(a, b);
-  const long long total = all * units, first = before * units + (long long)unit * (seq.tiles + a.lead) + a.lead;
-  const int live = attn_live_ctas(a.ctas, total);
-  const int c0 = attn_owner(total, live, first), c1 = attn_owner(total, live, first + seq.tiles - 1);
-  griddep_wait();
-  if (c0 == c1) return;
+  const int b = w.b;
   const int h = unit / a.row_tiles, r0 = (unit % a.row_tiles) * a.row_tile;
   const int item = threadIdx.x % kJoinItems, part = threadIdx.x / kJoinItems;
   const int e = blockIdx.y * kJoinItems + item, r = e % a.row_tile, d4 = e / a.row_tile;
@@ -328,8 +344,13 @@ cudaError_t launch_attn_simple(int dtype, const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_join(int dtype, const AttnArgs& a, cudaStream_t st) {
   auto kernel = dtype == SDV_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
-  return launch_pdl(kernel, dim3(a.B * a.Hkv * a.row_tiles, (a.row_tile * (a.D / 4) + kJoinItems - 1) / kJoinItems),
-                    dim3(kJoinItems * kJoinParts), 0, st, a);
+  // blocks for the units, or for the CTAs' ranges, in each of which one shared unit at most begins
+  // to be another CTA's: whichever are fewer (2048 units of 20 rows: 92 us by unit, mostly blocks
+  // with nothing to do)
+  const int units = a.B * a.Hkv * a.row_tiles;
+  const bool by_cta = a.ctas <= units;
+  return launch_pdl(kernel, dim3(by_cta ? a.ctas - 1 : units, (a.row_tile * (a.D / 4) + kJoinItems - 1) / kJoinItems),
+                    dim3(kJoinItems * kJoinParts), 0, st, a, by_cta);
 }
 
 }  // namespace sdv

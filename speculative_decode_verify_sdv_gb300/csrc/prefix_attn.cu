@@ -194,80 +194,79 @@ cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st
 
 // ---- join -------------------------------------------------------------------------------
 
-constexpr int kMergeRows = 32, kMergeWarps = 8;
+constexpr int kMergeRows = 32, kMergeCols = 32;
 
-// 32 rows of a row tile per block.  The partials lie row beside row, the outputs column beside
-// column: the rows' sums go through shared memory between the two.
+// 32 rows of a row tile and 32 columns per block, a thread per row and four columns with eight
+// partials in flight.  The partials lie row beside row, the outputs column beside column: the
+// sums go through shared memory between the two.
 template <typename T>
-__global__ void __launch_bounds__(32 * kMergeWarps) prefix_join_kernel(const PrefixArgs a, const AttnArgs own,
-                                                                        float* lse_or_null) {
-  extern __shared__ float sm[];
-  const int D = a.D, ld = D + 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* const so = sm;                                  // [32][D + 4]
-  float2* const sml = reinterpret_cast<float2*>(sm + kMergeRows * ld);
-  griddep_wait();
-  griddep_launch_dependents();
+__global__ void __launch_bounds__(kMergeRows* kMergeCols / 4) prefix_join_kernel(const PrefixArgs a, const AttnArgs own,
+                                                                                 float* lse_or_null) {
+  constexpr int LD = kMergeCols + 4;
+  __shared__ float4 so[kMergeRows * LD / 4];
+  __shared__ float2 sml[kMergeRows];
+  const int D = a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, r0 = blockIdx.y * kMergeRows;
   const int per_head = (a.row_tiles + a.unit_tiles - 1) / a.unit_tiles;
   const int unit = h * per_head + rt / a.unit_tiles, sub = rt % a.unit_tiles;
-  const int nr = min(a.row_tile, a.tokens * a.G - rt * a.row_tile);
+  const int nr = min(a.row_tile, a.tokens * a.G - rt * a.row_tile), c0 = blockIdx.z * kMergeCols;
+  // (the split first, before the launches in front have ended: the length is an input)
   bool bad;
-  PrefixWalk w;
-  w.tiles = prefix_tiles(a, prefix_length(a, bad));
-  w.total = (long long)w.tiles * a.units;
-  w.live = attn_live_ctas(a.ctas, w.total);
+  const int tiles = prefix_tiles(a, prefix_length(a, bad));
+  const long long total = (long long)tiles * a.units;
+  const int live = attn_live_ctas(a.ctas, total);
   int parts = 0;
-  if (w.tiles > 0)
-    parts = attn_owner(w.total, w.live, (long long)unit * w.tiles + w.tiles - 1) -
-            attn_owner(w.total, w.live, (long long)unit * w.tiles) + 1;
+  if (tiles > 0)
+    parts = attn_owner(total, live, (long long)unit * tiles + tiles - 1) - attn_owner(total, live, (long long)unit * tiles) + 1;
+  griddep_wait();
+  griddep_launch_dependents();
   {
-    const int r = r0 + lane;
-    const bool mine = r < nr;
-    for (int d4 = warp; d4 < D / 4; d4 += kMergeWarps) {
-      AttnSum sum;
-      for (int k0 = 0; mine && k0 < parts; k0 += 4) {
-        float2 ml[4];
-        float4 x[4];
+    const int r = r0 + lane, d4 = c0 / 4 + warp;
+    AttnSum sum;
+    if (r < nr && d4 < D / 4) {
+      const size_t first = (size_t)unit * a.sharers * a.unit_tiles + sub;
+      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * a.row_tile + r;
+      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * (D / 4) + d4) * a.row_tile + r;
+      const size_t step = (size_t)a.unit_tiles * a.row_tile;
+      for (int k0 = 0; k0 < parts; k0 += 8) {
+        float2 s[8];
+        float4 x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
+        for (int k = 0; k < 8; ++k) {
+          s[k] = make_float2(-INFINITY, 0.f);
           if (k0 + k >= parts) continue;
-          const size_t place = ((size_t)unit * a.sharers + k0 + k) * a.unit_tiles + sub;
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place * a.row_tile + r);
-          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (place * (D / 4) + d4) * a.row_tile + r);
+          s[k] = __ldcg(ml + (k0 + k) * step);
+          x[k] = __ldcg(po + (k0 + k) * step * (D / 4));
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum.add<true>(ml[k].x, ml[k].y, x[k]);
+        for (int k = 0; k < 8; ++k) sum.add<true>(s[k].x, s[k].y, x[k]);
       }
-      *reinterpret_cast<float4*>(so + lane * ld + d4 * 4) = sum.o;
-      if (d4 == 0) sml[lane] = make_float2(sum.m, sum.l);
     }
+    so[lane * (LD / 4) + warp] = sum.o;
+    if (warp == 0) sml[lane] = make_float2(sum.m, sum.l);
   }
   __syncthreads();
-  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
-    const int r = r0 + i;
-    if (r >= nr) break;
-    const int row = rt * a.row_tile + r, token = row / a.G;
-    const int b = token / own.S, s = token - b * own.S;
-    const bool live = s < attn_seq(own, b).n;
-    const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
-    const float lse = __ldcg(own.lse + orow);
-    for (int d4 = lane; d4 < D / 4; d4 += 32) {
-      AttnSum sum;
-      sum.m = sml[i].x;
-      sum.l = sml[i].y;
-      sum.o = *reinterpret_cast<const float4*>(so + i * ld + d4 * 4);
-      // the own positions' output is that of a sum of 1 at a maximum of their lse
-      if (lse != -INFINITY)
-        sum.add<true>(lse * 1.4426950408889634f, 1.f, __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4));
-      const bool none = !live || sum.l == 0.f;
-      const float inv = 1.f / sum.l;
-      const uint2 y = none ? make_uint2(0u, 0u)
-                           : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv), pack16<T>(sum.o.z * inv, sum.o.w * inv));
-      reinterpret_cast<uint2*>(static_cast<T*>(own.out) + orow * D)[d4] = y;
-      if (d4 == 0 && lse_or_null != nullptr) lse_or_null[orow] = none ? -INFINITY : sum.lse();
-    }
-  }
+  // eight threads a row
+  const int i = threadIdx.x / (kMergeCols / 4), j4 = threadIdx.x % (kMergeCols / 4), d4 = c0 / 4 + j4, r = r0 + i;
+  if (r >= nr || d4 >= D / 4) return;
+  const int row = rt * a.row_tile + r, token = row / a.G;
+  const int b = token / own.S, s = token - b * own.S;
+  const bool alive = s < attn_seq(own, b).n;
+  const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
+  const float lse = __ldcg(own.lse + orow);
+  const float4 x = __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4);
+  AttnSum sum;
+  sum.m = sml[i].x;
+  sum.l = sml[i].y;
+  sum.o = so[i * (LD / 4) + j4];
+  // the own positions' output is that of a sum of 1 at a maximum of their lse
+  if (lse != -INFINITY) sum.add<true>(lse * 1.4426950408889634f, 1.f, x);
+  const bool none = !alive || sum.l == 0.f;
+  const float inv = 1.f / sum.l;
+  const uint2 y = none ? make_uint2(0u, 0u)
+                       : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv), pack16<T>(sum.o.z * inv, sum.o.w * inv));
+  reinterpret_cast<uint2*>(static_cast<T*>(own.out) + orow * D)[d4] = y;
+  if (d4 == 0 && lse_or_null != nullptr) lse_or_null[orow] = none ? -INFINITY : sum.lse();
 }
 
 // `own`: the paged attention's arguments, out32 and lse where it has left its outputs, `out` the
@@ -275,8 +274,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_join_kernel(const Pre
 cudaError_t launch_prefix_join(int dtype, const PrefixArgs& a, const AttnArgs& own, float* lse_or_null,
                                cudaStream_t st) {
   auto kernel = dtype == SDV_F16 ? prefix_join_kernel<__half> : prefix_join_kernel<__nv_bfloat16>;
-  return launch_pdl(kernel, dim3(a.Hkv * a.row_tiles, (a.row_tile + kMergeRows - 1) / kMergeRows), dim3(32 * kMergeWarps),
-                    (size_t)kMergeRows * (a.D + 4) * 4 + kMergeRows * 8, st, a, own, lse_or_null);
+  return launch_pdl(kernel, dim3(a.Hkv * a.row_tiles, (a.row_tile + kMergeRows - 1) / kMergeRows,
+                                 (a.D + kMergeCols - 1) / kMergeCols),
+                    dim3(kMergeRows * kMergeCols / 4), 0, st, a, own, lse_or_null);
 }
 
 constexpr int kSimplePerSm = 2;

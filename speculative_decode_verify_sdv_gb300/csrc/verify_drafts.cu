@@ -8,14 +8,15 @@
 // Two launches.  The first reads every row once: per chunk of 2048 logits the maximum m and
 // sum 2^((x - m) c), c = log2(e) / T (or, greedy, the place of the maximum).  Reading the logits
 // bounds it.  The second has a cluster per sequence: it joins the rows' sums, runs the tests and
-// draws from the one row left.
+// draws from the one row left.  Without drafts the second does it all.
 //
 // A draw compares running sums of up to 10^5 weights with a random number, so an error of e of
 // the total gives another token with a chance of 10^5 e: 32-bit weights, whose errors of 2^-24
 // add up to 10^-9 of the total or more, would miss one draw in some thousands.  The row's weights
-// are therefore computed to 2^-36 of each as pairs of floats (2^x by a table of 2^(k/32) and a
+// are therefore pairs of floats, exact to some 2^-30 of each (2^x by a table of 2^(k/32) and a
 // short polynomial: Tang, "Table-driven implementation of the exponential function", ACM TOMS
-// 1989) and their sums carry the rounding of every addition along (Knuth's two-sum).
+// 1989), and their sums carry the rounding of every addition along (Knuth's two-sum).  No sum is
+// of 64-bit numbers: this GPU adds those at a fiftieth of the rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,9 +36,11 @@ namespace sdv {
 
 namespace {
 
-constexpr int kChunk = 2048;       // logits of a warp's unit of work
+constexpr int kStatChunk = 2048;   // logits of a warp's unit of work in the first launch
+constexpr int kDrawChunk = 1024;   // and in the second: two for each thread of a CTA
 constexpr int kStatThreads = 128;
-constexpr int kDrawThreads = 256;
+constexpr int kDrawThreads = 512;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxDrafts = 31;
 
 struct DraftArgs {
@@ -47,9 +50,9 @@ struct DraftArgs {
   const int32_t *drafts, *n_drafts;
   const float *probs, *uniforms;
   int32_t *accepted, *next;
-  int B, S, V, chunks;
-  float2* stats;              // [B * S][chunks]: maximum, sum (greedy: the bits of its place)
-  double *sums, *rests;       // [B][chunks]: the drawn row's weights, and what the drafter's leave of them
+  int B, S, V, chunks, draws;  // chunks of a row in the two launches
+  float2* stats;              // [B * S][chunks] (no drafts: [B][draws]): maximum, sum (greedy: the bits of its place)
+  float2 *sums, *rests;       // [B][draws]: the drawn row's weights, and what the drafter's leave of them
 };
 
 __device__ const float kPowHi[32] = {
@@ -75,11 +78,11 @@ __device__ __forceinline__ float logit(const T* p) {
 }
 
 // Row r's logits in groups of 16 bytes from an aligned address on, the first `shift` elements of
-// which lie before the row; a chunk is kChunk elements of groups, 32 groups (one a lane) a step.
-template <typename T>
+// which lie before the row; a chunk is CHUNK elements of groups, 32 groups (one a lane) a step.
+template <typename T, int CHUNK>
 struct Row {
   static constexpr int kPer = 16 / sizeof(T);            // elements of a group
-  static constexpr int kSteps = kChunk / kPer / 32;      // groups of a lane in a chunk
+  static constexpr int kSteps = CHUNK / kPer / 32;       // groups of a lane in a chunk
   const T* p;
   int V, shift;
   __device__ __forceinline__ Row(const DraftArgs& a, long long row)
@@ -87,7 +90,7 @@ struct Row {
     shift = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
   }
   __device__ __forceinline__ int first(int chunk, int step, int lane) const {  // element of a group's start
-    return (chunk * (kChunk / kPer) + step * 32 + lane) * kPer - shift;
+    return (chunk * (CHUNK / kPer) + step * 32 + lane) * kPer - shift;
   }
   __device__ __forceinline__ bool whole(int v) const { return v >= 0 && v + kPer <= V; }
   __device__ __forceinline__ uint4 load(int v) const { return __ldg(reinterpret_cast<const uint4*>(p + v)); }
@@ -95,6 +98,8 @@ struct Row {
   __device__ __forceinline__ float at(int v) const {
     return v >= 0 && v < V ? counted_logit((float)__ldg(p + v)) : -INFINITY;
   }
+  // A chunk's elements as they count, of this lane; their maximum over the warp.
+  __device__ __forceinline__ float chunk(int n, int lane, float (&x)[kSteps][kPer]) const;
 };
 
 __device__ __forceinline__ void group_floats(const uint4& x, float (&f)[4], float) {
@@ -111,67 +116,84 @@ __device__ __forceinline__ void group_floats(const uint4& x, float (&f)[8], T) {
   }
 }
 
-// 1 / T in the log2 domain as a pair; greedy where T is 0, below, NaN, or so small that it overflows.
+template <typename T, int CHUNK>
+__device__ __forceinline__ float Row<T, CHUNK>::chunk(int n, int lane, float (&x)[kSteps][kPer]) const {
+  uint4 raw[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int v = first(n, s, lane);
+    if (whole(v)) raw[s] = load(v);
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int v = first(n, s, lane);
+    if (whole(v)) {
+      group_floats(raw[s], x[s], T());
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[s][e] = counted_logit(x[s][e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[s][e] = at(v + e);
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[s][e]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+
+// The lowest place of a chunk's maximum.
+template <typename R>
+__device__ __forceinline__ int place_of(const R& r, int n, int lane, const float (&x)[R::kSteps][R::kPer], float m) {
+  int best = INT_MAX;
+#pragma unroll
+  for (int s = 0; s < R::kSteps; ++s)
+#pragma unroll
+    for (int e = 0; e < R::kPer; ++e) {
+      const int v = r.first(n, s, lane) + e;
+      if (x[s][e] == m && v >= 0 && v < r.V) best = min(best, v);
+    }
+  return __reduce_min_sync(0xffffffffu, best);
+}
+
+// log2(e) / T as a pair; greedy where T is 0, below, NaN, or so small that it overflows.
 struct Warmth {
   float hi, lo;
   bool greedy;
   __device__ __forceinline__ explicit Warmth(float t) {
-    const double c = 1.4426950408889634 / (double)t;
-    hi = fmaxf((float)c, 1e-44f);  // an infinite T: all equal, and 0 times -inf nowhere
-    lo = (float)(c - (double)hi);
+    constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f;  // log2(e)
+    hi = kHi / t;
+    lo = (fmaf(-hi, t, kHi) + kLo) / t;
     greedy = !(t > 0.f) || !(hi < INFINITY);
+    if (!(hi >= 1e-37f)) {  // where the rest is no number any more; an infinite T: all equal, and 0 times -inf nowhere
+      hi = fmaxf(hi, 1e-44f);
+      lo = 0.f;
+    }
   }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftArgs a) {
-  using R = Row<T>;
+  using R = Row<T, kStatChunk>;
   constexpr int W = kStatThreads / 32;
   const int lane = threadIdx.x & 31, blocks = (a.chunks + W - 1) / W;
-  const long long row = blockIdx.x / blocks;
-  const int chunk = (int)(blockIdx.x - row * blocks) * W + (threadIdx.x >> 5);
-  const int b = (int)(row / a.S), i = (int)(row - (long long)b * a.S);
+  const int row = blockIdx.x / blocks;
+  const int chunk = (blockIdx.x - row * blocks) * W + (threadIdx.x >> 5);
+  const int b = row / a.S, i = row - b * a.S;
   griddep_wait();
   griddep_launch_dependents();
   const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
   if (chunk >= a.chunks || i > n) return;
   const R r(a, row);
-  const Warmth c(__ldg(a.temperature + b));
-  uint4 raw[R::kSteps];
-#pragma unroll
-  for (int s = 0; s < R::kSteps; ++s) {
-    const int v = r.first(chunk, s, lane);
-    if (r.whole(v)) raw[s] = r.load(v);
-  }
-  float m = -INFINITY;
+  const float t = __ldg(a.temperature + b);
   float x[R::kSteps][R::kPer];
-#pragma unroll
-  for (int s = 0; s < R::kSteps; ++s) {
-    const int v = r.first(chunk, s, lane);
-    if (r.whole(v)) {
-      group_floats(raw[s], x[s], T());
-#pragma unroll
-      for (int e = 0; e < R::kPer; ++e) x[s][e] = counted_logit(x[s][e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < R::kPer; ++e) x[s][e] = r.at(v + e);
-    }
-#pragma unroll
-    for (int e = 0; e < R::kPer; ++e) m = fmaxf(m, x[s][e]);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float m = r.chunk(chunk, lane, x);
+  const Warmth c(t);
   float2 out = make_float2(m, 0.f);
   if (c.greedy) {
-    int best = INT_MAX;
-#pragma unroll
-    for (int s = 0; s < R::kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < R::kPer; ++e) {
-        const int v = r.first(chunk, s, lane) + e;
-        if (x[s][e] == m && v >= 0 && v < a.V) best = min(best, v);
-      }
-    out.y = __int_as_float(__reduce_min_sync(0xffffffffu, best));
+    out.y = __int_as_float(place_of(r, chunk, lane, x, m));
   } else if (m != -INFINITY) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -183,7 +205,7 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftA
     for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     out.y = all;
   }
-  if (lane == 0) a.stats[row * a.chunks + chunk] = out;
+  if (lane == 0) a.stats[(long long)row * a.chunks + chunk] = out;
 }
 
 // ---- precise weights -------------------------------------------------------------------
@@ -201,112 +223,126 @@ __device__ __forceinline__ f32x2 two_sum(f32x2 a, f32x2 b, f32x2& err) {
   return s;
 }
 
-// 2^((x - M) c) for the two x of a pair, to some 2^-36 of each; 0 where it is below 2^-125 and
-// where x is -inf.  For all lanes of a warp: lane k holds 2^(k/32).
+// One number as the sum of two floats, the second far below the first.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  const float err = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+  return Two{s, __fadd_rn(err, __fadd_rn(a.lo, b.lo))};
+}
+__device__ __forceinline__ Two shfl_up(Two a, int off) {
+  return Two{__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
+}
+__device__ __forceinline__ Two shfl_at(Two a, int lane) {
+  return Two{__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+__device__ __forceinline__ bool exceeds(Two a, Two b) {
+  return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) > 0.f;
+}
+__device__ __forceinline__ Two warp_sum(Two x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    x = add_two(x, Two{__shfl_xor_sync(0xffffffffu, x.hi, off), __shfl_xor_sync(0xffffffffu, x.lo, off)});
+  return x;
+}
+// The sum up to and with this lane's.
+__device__ __forceinline__ Two warp_scan(Two x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const Two o = shfl_up(x, off);
+    if (lane >= off) x = add_two(o, x);
+  }
+  return x;
+}
+
+// 2^(x c - K) for the two x of a pair, K the exponent of the row's largest weight: exact to some
+// 2^-30 of each; 0 where it is below 2^-124 and where x is -inf.  For all lanes of a warp: lane k
+// holds 2^(k/32).  x c is taken apart as it is, K being a whole number; where it is so large that
+// its last bits are no fraction any more, the row's maximum is taken off x first.
 struct Weigher {
   float M, c_hi, c_lo, pow_hi, pow_lo, least;
+  uint32_t bias;
+  bool off;
   __device__ __forceinline__ Weigher(float m, const Warmth& c, int lane)
-      : M(m), c_hi(c.hi), c_lo(c.lo), pow_hi(kPowHi[lane]), pow_lo(kPowLo[lane]), least(m - 125.f / c.hi) {}
+      : M(m), c_hi(c.hi), c_lo(c.lo), pow_hi(kPowHi[lane]), pow_lo(kPowLo[lane]) {
+    least = fmaxf(m - 124.f / c.hi, -FLT_MAX);
+    off = fabsf(m) * c.hi >= 16384.f;
+    const int K = off ? 0 : (int)ceilf(m * c.hi);
+    bias = ((uint32_t)(127 - K) << 23) - ((0x4b400000u >> 5) << 23);
+  }
   __device__ __forceinline__ Pair operator()(float x0, float x1) const {
-    const bool in0 = x0 >= least && x0 > -INFINITY, in1 = x1 >= least && x1 > -INFINITY;
-    const f32x2 x = pair2(in0 ? x0 : M, in1 ? x1 : M);
-    f32x2 d_lo;
-    const f32x2 d = two_sum(x, both(-M), d_lo), ch = both(c_hi);
-    const f32x2 t = mul2(d, ch);
-    const f32x2 t_lo = fma2(d, ch, neg2(t));
-    const f32x2 tl = add2(t_lo, fma2(d, both(c_lo), mul2(d_lo, ch)));
+    const bool in0 = x0 >= least, in1 = x1 >= least;
+    f32x2 x = pair2(in0 ? x0 : M, in1 ? x1 : M), x_lo = 0;
+    if (off) x = two_sum(x, both(-M), x_lo);
+    const f32x2 ch = both(c_hi), t = mul2(x, ch);
+    f32x2 tl = fma2(x, both(c_lo), fma2(x, ch, neg2(t)));
+    if (off) tl = fma2(x_lo, ch, tl);
     // t = k / 32 + r, |r| <= 1 / 64: k in the low bits of a number of 1.5 2^23
-    const f32x2 magic = both(12582912.f);
-    const f32x2 kk = fma2(t, both(32.f), magic);
+    const f32x2 magic = both(12582912.f), kk = fma2(t, both(32.f), magic);
     const f32x2 r = fma2(sub2(kk, magic), both(-0.03125f), t);
     const float2 kf = unpair2(kk);
-    const int k0 = __float_as_int(kf.x) - 0x4b400000, k1 = __float_as_int(kf.y) - 0x4b400000;
-    const f32x2 th = pair2(__shfl_sync(0xffffffffu, pow_hi, k0 & 31), __shfl_sync(0xffffffffu, pow_hi, k1 & 31));
-    const f32x2 tlo = pair2(__shfl_sync(0xffffffffu, pow_lo, k0 & 31), __shfl_sync(0xffffffffu, pow_lo, k1 & 31));
-    // 2^r = 1 + s + g: s = fl(r ln 2), g the rest
-    const f32x2 ln_hi = both(0x1.62e430p-1f), ln_lo = both(-0x1.05c610p-29f);
-    const f32x2 quad = fma2(r, fma2(r, both(0.009618129f), both(0.05550411f)), both(0.24022651f));
-    const f32x2 s = mul2(r, ln_hi);
-    f32x2 g = fma2(r, ln_hi, neg2(s));
-    g = fma2(r, ln_lo, g);
-    g = fma2(tl, ln_hi, g);
-    g = fma2(mul2(r, r), quad, g);
-    const f32x2 p = mul2(th, s);
-    Pair w;
-    w.hi = add2(th, p);
-    f32x2 l = add2(sub2(th, w.hi), p);  // exact: th is the larger
-    l = add2(l, fma2(th, s, neg2(p)));
-    l = fma2(th, g, l);
-    w.lo = add2(l, fma2(tlo, s, tlo));
-    const int n0 = k0 >> 5, n1 = k1 >> 5;
-    const f32x2 scale = pair2(in0 ? __int_as_float((n0 + 127) << 23) : 0.f, in1 ? __int_as_float((n1 + 127) << 23) : 0.f);
-    w.hi = mul2(w.hi, scale);
-    w.lo = mul2(w.lo, scale);
-    return w;
+    const uint32_t k0 = __float_as_uint(kf.x), k1 = __float_as_uint(kf.y);
+    const f32x2 th = pair2(__shfl_sync(0xffffffffu, pow_hi, k0), __shfl_sync(0xffffffffu, pow_hi, k1));
+    const f32x2 tlo = pair2(__shfl_sync(0xffffffffu, pow_lo, k0), __shfl_sync(0xffffffffu, pow_lo, k1));
+    // 2^r = 1 + s, |s| < 0.011
+    f32x2 p = fma2(r, both(0.009618129f), both(0.05550411f));
+    p = fma2(r, p, both(0.24022651f));
+    p = fma2(r, p, both(0x1.62e430p-1f));
+    f32x2 s = fma2(tl, both(0x1.62e430p-1f), mul2(r, both(-0x1.05c610p-29f)));
+    s = fma2(r, p, s);
+    const f32x2 scale = pair2(in0 ? __uint_as_float(((k0 >> 5) << 23) + bias) : 0.f,
+                              in1 ? __uint_as_float(((k1 >> 5) << 23) + bias) : 0.f);
+    return Pair{mul2(th, scale), mul2(fma2(th, s, tlo), scale)};
   }
 };
 
-// What max(w - q Z, 0) leaves, Z = z_hi + z_lo.
-__device__ __forceinline__ Pair rest_of(const Pair& w, float q0, float q1, float z_hi, float z_lo) {
+// What max(w - q Z, 0) leaves, Z = z.hi + z.lo.
+__device__ __forceinline__ Pair rest_of(const Pair& w, float q0, float q1, Two z) {
   const f32x2 q = pair2(q0 > 0.f ? q0 : 0.f, q1 > 0.f ? q1 : 0.f);
-  const f32x2 a = mul2(q, both(z_hi));
-  const f32x2 al = fma2(q, both(z_lo), fma2(q, both(z_hi), neg2(a)));
+  const f32x2 a = mul2(q, both(z.hi));
+  const f32x2 al = fma2(q, both(z.lo), fma2(q, both(z.hi), neg2(a)));
   f32x2 err;
   const f32x2 d = two_sum(w.hi, neg2(a), err);
   const f32x2 l = add2(err, sub2(w.lo, al));
   const float2 sum = unpair2(add2(d, l)), dh = unpair2(d), dl = unpair2(l);
-  Pair r;
-  r.hi = pair2(sum.x > 0.f ? dh.x : 0.f, sum.y > 0.f ? dh.y : 0.f);
-  r.lo = pair2(sum.x > 0.f ? dl.x : 0.f, sum.y > 0.f ? dl.y : 0.f);
-  return r;
-}
-
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  return x;
+  return Pair{pair2(sum.x > 0.f ? dh.x : 0.f, sum.y > 0.f ? dh.y : 0.f),
+              pair2(sum.x > 0.f ? dl.x : 0.f, sum.y > 0.f ? dl.y : 0.f)};
 }
 
 // A chunk's weights added up: of the row, without token `gone`, or (q given) what q leaves.
-template <typename T>
-__device__ __forceinline__ double chunk_sum(const Row<T>& r, const Weigher& weigh, int chunk, int lane, int gone,
-                                            const float* q, float z_hi, float z_lo) {
-  using R = Row<T>;
-  Pair sum{both(0.f), both(0.f)};
-  constexpr int kAhead = 4;
-#pragma unroll 1
-  for (int s0 = 0; s0 < R::kSteps; s0 += kAhead) {
-    float x[kAhead][R::kPer], qs[kAhead][R::kPer];
+template <typename R>
+__device__ __forceinline__ Two chunk_sum(const R& r, const Weigher& weigh, int n, int lane,
+                                         float (&x)[R::kSteps][R::kPer], int gone, const float* q, Two z) {
+  Pair sum{0, 0};
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      const int v = r.first(chunk, s0 + s, lane);
-      if (r.whole(v)) {
-        group_floats(r.load(v), x[s], T());
+  for (int s = 0; s < R::kSteps; ++s) {
+    const int v = r.first(n, s, lane);
+    float qs[R::kPer];
+    if (q != nullptr) {
+      if (r.whole(v) && (reinterpret_cast<uintptr_t>(q + v) & 15u) == 0) {
 #pragma unroll
-        for (int e = 0; e < R::kPer; ++e) x[s][e] = counted_logit(x[s][e]);
+        for (int e = 0; e < R::kPer; e += 4)
+          *reinterpret_cast<float4*>(qs + e) = __ldg(reinterpret_cast<const float4*>(q + v + e));
       } else {
 #pragma unroll
-        for (int e = 0; e < R::kPer; ++e) x[s][e] = r.at(v + e);
-      }
-#pragma unroll
-      for (int e = 0; e < R::kPer; ++e) {
-        if (v + e == gone) x[s][e] = -INFINITY;
-        qs[s][e] = q != nullptr && v + e >= 0 && v + e < r.V ? __ldg(q + v + e) : 0.f;
+        for (int e = 0; e < R::kPer; ++e) qs[e] = v + e >= 0 && v + e < r.V ? __ldg(q + v + e) : 0.f;
       }
     }
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s)
-#pragma unroll
-      for (int e = 0; e < R::kPer; e += 2) {
-        Pair w = weigh(x[s][e], x[s][e + 1]);
-        if (q != nullptr) w = rest_of(w, qs[s][e], qs[s][e + 1], z_hi, z_lo);
-        f32x2 err;
-        sum.hi = two_sum(sum.hi, w.hi, err);
-        sum.lo = add2(sum.lo, add2(err, w.lo));
-      }
+    for (int e = 0; e < R::kPer; e += 2) {
+      if (v + e == gone) x[s][e] = -INFINITY;
+      if (v + e + 1 == gone) x[s][e + 1] = -INFINITY;
+      Pair w = weigh(x[s][e], x[s][e + 1]);
+      if (q != nullptr) w = rest_of(w, qs[e], qs[e + 1], z);
+      f32x2 err;
+      sum.hi = two_sum(sum.hi, w.hi, err);
+      sum.lo = add2(sum.lo, add2(err, w.lo));
+    }
   }
   const float2 h = unpair2(sum.hi), l = unpair2(sum.lo);
-  return warp_sum(((double)h.x + (double)h.y) + ((double)l.x + (double)l.y));
+  return warp_sum(add_two(Two{h.x, l.x}, Two{h.y, l.y}));
 }
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -323,62 +359,85 @@ __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// The total of a list of sums, and (u >= 0) the first one at which the running total exceeds
-// u of it, with the running total in front: by one warp, in a fixed order.
-__device__ __forceinline__ double list_total(const double* sums, int n, int lane) {
-  double t = 0.0;
-  for (int i = lane; i < n; i += 32) t += __ldcg(sums + i);
-  return warp_sum(t);
-}
+// A list of sums by one warp, a lane a stretch of it in order.
+struct Listed {
+  int from, to;
+  Two upto;  // all up to the end of this lane's
+  __device__ __forceinline__ Listed(const float2* list, int n, int lane) {
+    const int per = (n + 31) / 32;
+    from = min(lane * per, n);
+    to = min(from + per, n);
+    Two mine{0.f, 0.f};
+    for (int i = from; i < to; ++i) {
+      const float2 x = __ldcg(list + i);
+      mine = add_two(mine, Two{x.x, x.y});
+    }
+    upto = warp_scan(mine, lane);
+  }
+  __device__ __forceinline__ Two total() const { return shfl_at(upto, 31); }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const DraftArgs a) {
+  using R = Row<T, kDrawChunk>;
   constexpr int W = kDrawThreads / 32;
+  static_assert(kDrawChunk == 2 * kDrawThreads, "a pair of elements for each thread");
   __shared__ float s_max[kMaxDrafts + 1];
   __shared__ int s_best[kMaxDrafts + 1];
   __shared__ bool s_ok[kMaxDrafts + 1];
-  __shared__ double s_total, s_before, s_part[W];
+  __shared__ Two s_total, s_before, s_want, s_part[W];
   __shared__ int s_chunk, s_token, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int size = cluster_size(), rank = cluster_rank(), b = blockIdx.x / size;
   griddep_wait();
+  const float t = __ldg(a.temperature + b);
   const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
-  const Warmth c(__ldg(a.temperature + b));
+  const Warmth c(t);
+  float x[R::kSteps][R::kPer];
+  if (a.S == 1) {  // no launch in front has looked at the row
+    const R r(a, b);
+    for (int k = rank * W + warp; k < a.draws; k += size * W) {
+      const float m = r.chunk(k, lane, x);
+      const int best = c.greedy ? place_of(r, k, lane, x, m) : 0;
+      if (lane == 0) a.stats[(long long)b * a.draws + k] = make_float2(m, __int_as_float(best));
+    }
+    cluster_meet();
+  }
   // every row's statistics, and its draft's test
+  const int listed = a.S == 1 ? a.draws : a.chunks;
   for (int i = warp; i <= n; i += W) {
     const long long row = (long long)b * a.S + i;
-    const float2* const st = a.stats + row * a.chunks;
-    float m = -INFINITY;
-    int best = INT_MAX;
-    for (int k = lane; k < a.chunks; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    double z = 0.0;
-    if (m != -INFINITY) {
-      for (int k = lane; k < a.chunks; k += 32) {
-        const float2 s = __ldcg(st + k);
-        if (c.greedy) best = s.x == m ? min(best, __float_as_int(s.y)) : best;
-        else z += (double)(s.y * exp2f((s.x - m) * c.hi));
-      }
-    }
-    best = __reduce_min_sync(0xffffffffu, best);
-    z = warp_sum(z);
+    const float2* const st = a.stats + row * listed;
     const int d = i < n ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;
     const bool real = d >= 0 && d < a.V;
-    const float x = real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
-    double p = 0.0;  // of the draft, times z
+    float m = -INFINITY;
+    for (int k = lane; k < listed; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
+    const float xd = real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
+    float q = a.probs != nullptr && real ? __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d) : 1.f;
+    q = q > 0.f ? q : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float z = 0.f, p = 0.f;
+    int best = INT_MAX;
     if (c.greedy) {
-      z = 1.0;
-      p = real && d == best ? 1.0 : 0.0;
-    } else if (m != -INFINITY) {
-      const float2 h = unpair2(Weigher(m, c, lane)(x, x).hi);
-      p = (double)h.x;
+      for (int k = lane; k < listed; k += 32) {
+        const float2 s = __ldcg(st + k);
+        if (s.x == m) best = min(best, __float_as_int(s.y));
+      }
+      best = __reduce_min_sync(0xffffffffu, best);
+      z = 1.f;
+      p = real && d == best ? 1.f : 0.f;
+    } else if (i < n && m != -INFINITY) {
+      for (int k = lane; k < listed; k += 32) {
+        const float2 s = __ldcg(st + k);
+        z += s.y * exp2f((s.x - m) * c.hi);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+      p = exp2f((xd - m) * c.hi);
     }
     if (lane == 0) {
-      float q = 1.f;
-      if (a.probs != nullptr && real) q = __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d);
-      q = q > 0.f ? q : 0.f;
-      s_ok[i] = i < n && real && (double)__ldg(a.uniforms + (long long)b * a.S + i) * (double)q * z < p;
+      s_ok[i] = i < n && real && __ldg(a.uniforms + (long long)b * a.S + i) * q * z < p;
       s_max[i] = m;
       s_best[i] = best;
     }
@@ -394,138 +453,123 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const DraftAr
     if (rank == 0 && tid == 0) a.next[b] = m == -INFINITY ? -1 : s_best[j];
     return;
   }
-  const Row<T> r(a, (long long)b * a.S + j);
+  const R r(a, (long long)b * a.S + j);
   const Weigher weigh(m, c, lane);
   const bool rest = missed && a.probs != nullptr;
   const int gone = missed && a.probs == nullptr ? __ldg(a.drafts + (long long)b * (a.S - 1) + j) : INT_MIN;
   const float* const q = rest ? a.probs + ((long long)b * (a.S - 1) + j) * a.V : nullptr;
-  double* const sums = a.sums + (long long)b * a.chunks;
-  double* const rests = a.rests + (long long)b * a.chunks;
-  for (int k = rank * W + warp; k < a.chunks; k += size * W) {
-    const double s = chunk_sum(r, weigh, k, lane, gone, nullptr, 0.f, 0.f);
-    if (lane == 0) sums[k] = s;
+  float2* const sums = a.sums + (long long)b * a.draws;
+  float2* const rests = a.rests + (long long)b * a.draws;
+  for (int k = rank * W + warp; k < a.draws; k += size * W) {
+    r.chunk(k, lane, x);
+    const Two s = chunk_sum(r, weigh, k, lane, x, gone, nullptr, Two{0.f, 0.f});
+    if (lane == 0) sums[k] = make_float2(s.hi, s.lo);
   }
   cluster_meet();
-  if (warp == 0) {
-    const double t = list_total(sums, a.chunks, lane);
-    if (lane == 0) s_total = t;
-  }
-  __syncthreads();
-  double total = s_total;
-  const double* list = sums;
-  const float* q_list = nullptr;
-  const float z_hi = (float)total, z_lo = (float)(total - (double)z_hi);
+  const float2* list = sums;
+  Two z{0.f, 0.f};
+  bool left = false;  // whether the drafter's probabilities leave anything
   if (rest) {
-    for (int k = rank * W + warp; k < a.chunks; k += size * W) {
-      const double s = chunk_sum(r, weigh, k, lane, INT_MIN, q, z_hi, z_lo);
-      if (lane == 0) rests[k] = s;
-    }
-    cluster_meet();
-    if (rank != 0) return;
-    __syncthreads();  // s_total has been read
     if (warp == 0) {
-      const double t = list_total(rests, a.chunks, lane);
-      if (lane == 0) s_total = t;
+      const Two all = Listed(sums, a.draws, lane).total();
+      if (lane == 0) s_total = all;
     }
     __syncthreads();
-    if (s_total > 0.0) {
-      total = s_total;
-      list = rests;
-      q_list = q;
+    z = s_total;
+    for (int k = rank * W + warp; k < a.draws; k += size * W) {
+      r.chunk(k, lane, x);
+      const Two s = chunk_sum(r, weigh, k, lane, x, INT_MIN, q, z);
+      if (lane == 0) rests[k] = make_float2(s.hi, s.lo);
     }
+    cluster_meet();
   }
   if (rank != 0) return;
-  const int without = total > 0.0 ? gone : INT_MIN;
-  if (!(total > 0.0)) {
-    // nothing is left without the draft: from the row itself, of which only the draft's weight counts
-    if (tid == 0) a.next[b] = gone;
-    return;
-  }
   // the chunk that the draw falls into
-  const double want = (double)__ldg(a.uniforms + (long long)b * a.S + a.S - 1) * total;
   if (warp == 0) {
-    double before = 0.0, in_front = 0.0;
-    int at = -1, last = -1;
-    double last_front = 0.0;
-    for (int k0 = 0; k0 < a.chunks && at < 0; k0 += 32) {
-      const double s = k0 + lane < a.chunks ? __ldcg(list + k0 + lane) : 0.0;
-      double incl = s;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, s > 0.0 && before + incl > want);
-      const unsigned some = __ballot_sync(0xffffffffu, s > 0.0);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        at = k0 + l;
-        in_front = before + __shfl_sync(0xffffffffu, incl - s, l);
-      } else if (some) {
-        const int l = 31 - __clz(some);
-        last = k0 + l;
-        last_front = before + __shfl_sync(0xffffffffu, incl - s, l);
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+    Listed l(rest ? rests : sums, a.draws, lane);
+    list = rest ? rests : sums;
+    left = rest;
+    if (rest && !(l.total().hi > 0.f)) {  // nothing: from the row itself
+      l = Listed(sums, a.draws, lane);
+      list = sums;
+      left = false;
     }
-    if (lane == 0) {
-      s_chunk = at >= 0 ? at : last;
-      s_before = at >= 0 ? in_front : last_front;
+    const Two all = l.total();
+    const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1), p = __fmul_rn(u, all.hi);
+    const Two want{p, fmaf(u, all.lo, fmaf(u, all.hi, -p))};
+    const unsigned hit = __ballot_sync(0xffffffffu, exceeds(l.upto, want));
+    // its lane, and the running sum in front; a random number of 1 and above, or none: the last one's
+    const int at = hit ? __ffs(hit) - 1 : 31;
+    const Two front = at > 0 ? shfl_at(l.upto, at - 1) : Two{0.f, 0.f};
+    if (lane == at) {
+      int chunk = -1, i = hit ? l.from : 0;
+      Two run = hit ? front : Two{0.f, 0.f}, before = run, bound = want;
+      for (; i < a.draws; ++i) {
+        const float2 s = __ldcg(list + i);
+        const Two next = add_two(run, Two{s.x, s.y});
+        if (s.x > 0.f) {
+          chunk = i;
+          before = run;
+          if (exceeds(next, want)) break;
+        }
+        run = next;
+      }
+      if (chunk < 0) {  // only roundings of the running sum were behind: the last weight there is
+        for (i = l.from - 1; i >= 0 && chunk < 0; --i)
+          if (__ldcg(list + i).x > 0.f) chunk = i;
+        bound = Two{INFINITY, 0.f};
+      }
+      s_chunk = all.hi > 0.f ? chunk : -1;
+      s_before = before;
+      s_want = bound;
+      s_total = Two{left ? 1.f : 0.f, 0.f};
       s_token = INT_MAX;
       s_last = -1;
     }
   }
   __syncthreads();
-  // and the token in it: a thread has eight elements, in order
-  constexpr int E = kChunk / kDrawThreads;
-  const int v0 = r.first(s_chunk, 0, 0) + tid * E;
-  double w[E], mine = 0.0;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    float x[2], qs[2];
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int v = v0 + e + z;
-      x[z] = v == without ? -INFINITY : r.at(v);
-      qs[z] = q_list != nullptr && v >= 0 && v < a.V ? __ldg(q_list + v) : 0.f;
-    }
-    Pair p = weigh(x[0], x[1]);
-    if (q_list != nullptr) p = rest_of(p, qs[0], qs[1], z_hi, z_lo);
-    const float2 h = unpair2(p.hi), l = unpair2(p.lo);
-    w[e] = (double)h.x + (double)l.x;
-    w[e + 1] = (double)h.y + (double)l.y;
-    mine += w[e];
-    mine += w[e + 1];
+  if (s_chunk < 0) {  // all weight was the draft's that was not kept
+    if (tid == 0) a.next[b] = gone;
+    return;
   }
-  double incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const double o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
+  // and the token in it: two elements a thread, in order
+  const int v0 = r.first(s_chunk, 0, 0) + 2 * tid;
+  Pair w = weigh(v0 == gone ? -INFINITY : r.at(v0), v0 + 1 == gone ? -INFINITY : r.at(v0 + 1));
+  if (s_total.hi > 0.f)
+    w = rest_of(w, v0 >= 0 && v0 < a.V ? __ldg(q + v0) : 0.f, v0 + 1 >= 0 && v0 + 1 < a.V ? __ldg(q + v0 + 1) : 0.f, z);
+  const float2 h = unpair2(w.hi), l = unpair2(w.lo);
+  const Two w0{h.x, l.x}, w1{h.y, l.y}, mine = add_two(w0, w1), incl = warp_scan(mine, lane);
   if (lane == 31) s_part[warp] = incl;
   __syncthreads();
-  double run = s_before + (incl - mine);
-  for (int k = 0; k < warp; ++k) run += s_part[k];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    run += w[e];
-    if (w[e] > 0.0) {
-      if (run > want) atomicMin(&s_token, v0 + e);
-      atomicMax(&s_last, v0 + e);
-    }
+  Two run = s_before;
+  for (int k = 0; k < warp; ++k) run = add_two(run, s_part[k]);
+  const Two up = shfl_up(incl, 1);
+  if (lane > 0) run = add_two(run, up);
+  const Two want = s_want;
+  run = add_two(run, w0);
+  if (w0.hi > 0.f) {
+    if (exceeds(run, want)) atomicMin(&s_token, v0);
+    atomicMax(&s_last, v0);
+  }
+  run = add_two(run, w1);
+  if (w1.hi > 0.f) {
+    if (exceeds(run, want)) atomicMin(&s_token, v0 + 1);
+    atomicMax(&s_last, v0 + 1);
   }
   __syncthreads();
   if (tid == 0) a.next[b] = s_token != INT_MAX ? s_token : s_last;
 }
 
-int draft_chunks(int V) { return (int)(((long long)V + 7 + kChunk - 1) / kChunk); }
+int chunks_of(int V, int chunk) { return (int)(((long long)V + 7 + chunk - 1) / chunk); }
+
+size_t drafts_stats(int B, int S, int V) {
+  return round_256((size_t)B * (S == 1 ? chunks_of(V, kDrawChunk) : (size_t)S * chunks_of(V, kStatChunk)) * 8);
+}
 
 size_t drafts_need(int B, int S, int V) {
   if (B < 1 || S < 1 || S > kMaxDrafts + 1 || V < 1 || V > (1 << 24) || B > (1 << 24)) return 0;
-  const size_t chunks = draft_chunks(V);
-  if ((unsigned long long)B * S * ((chunks + 3) / 4) > INT_MAX) return 0;
-  return kHeaderBytes + round_256((size_t)B * S * chunks * 8) + 2 * round_256((size_t)B * chunks * 8);
+  if ((unsigned long long)B * S * ((chunks_of(V, kStatChunk) + 3) / 4) > INT_MAX) return 0;
+  return kHeaderBytes + drafts_stats(B, S, V) + 2 * round_256((size_t)B * chunks_of(V, kDrawChunk) * 8);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -533,10 +577,13 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 template <typename T>
 cudaError_t drafts_launch(const DraftArgs& a, cudaStream_t st) {
   constexpr int W = kStatThreads / 32;
-  const unsigned grid = (unsigned)((long long)a.B * a.S * ((a.chunks + W - 1) / W));
-  cudaError_t e = launch_pdl(verify_stats_kernel<T>, dim3(grid), dim3(kStatThreads), 0, st, a);
-  if (e != cudaSuccess) return e;
-  const int cluster = 8;
+  if (a.S > 1) {
+    const unsigned grid = (unsigned)((long long)a.B * a.S * ((a.chunks + W - 1) / W));
+    const cudaError_t e = launch_pdl(verify_stats_kernel<T>, dim3(grid), dim3(kStatThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  int cluster = 1;  // CTAs of a sequence: a chunk for every warp, eight at most
+  while (cluster < kMaxCluster && cluster * (kDrawThreads / 32) < a.draws) cluster *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -591,11 +638,12 @@ sdv_status sdv_verify_drafts(int32_t dtype, const void* logits, int64_t row_stri
   a.B = B;
   a.S = S;
   a.V = V;
-  a.chunks = sdv::draft_chunks(V);
+  a.chunks = sdv::chunks_of(V, sdv::kStatChunk);
+  a.draws = sdv::chunks_of(V, sdv::kDrawChunk);
   char* const at = static_cast<char*>(ws) + sdv::kHeaderBytes;
   a.stats = reinterpret_cast<float2*>(at);
-  a.sums = reinterpret_cast<double*>(at + sdv::round_256((size_t)B * S * a.chunks * 8));
-  a.rests = a.sums + sdv::round_256((size_t)B * a.chunks * 8) / 8;
+  a.sums = reinterpret_cast<float2*>(at + sdv::drafts_stats(B, S, V));
+  a.rests = a.sums + sdv::round_256((size_t)B * a.draws * 8) / 8;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return sdv::status_of(dtype == SDV_F32   ? sdv::drafts_launch<float>(a, st)
                         : dtype == SDV_F16 ? sdv::drafts_launch<__half>(a, st)
