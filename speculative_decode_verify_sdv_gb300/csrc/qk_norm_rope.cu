@@ -9,7 +9,9 @@
 // would have lost 2^-24 of hundreds of turns.
 //
 // A warp per token and part of its heads; a head takes dim / 8 lanes of eight elements each.
-// cos and sin of a lane's eight elements are computed once a token and serve all heads.
+// The token's angles are computed once, one or more a lane, and go round through shared memory;
+// cos and sin times the norm's weights then serve all query heads, and once more all key heads.
+// Reading the rows and writing them bounds it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,6 +67,18 @@ struct Chunk {  // eight elements as they lie
       f[2 * i + 1] = y.y;
     }
   }
+  __device__ __forceinline__ void clear() { x = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void from_lane(int lane) {
+    x.x = __shfl_sync(0xffffffffu, x.x, lane);
+    x.y = __shfl_sync(0xffffffffu, x.y, lane);
+    x.z = __shfl_sync(0xffffffffu, x.z, lane);
+    x.w = __shfl_sync(0xffffffffu, x.w, lane);
+  }
+  template <typename TO>
+  __device__ __forceinline__ uint4 packed() const {
+    static_assert(std::is_same<T, TO>::value, "rows of the cache's type");
+    return x;
+  }
 };
 template <>
 struct Chunk<float> {
@@ -76,6 +90,16 @@ struct Chunk<float> {
   __device__ __forceinline__ void floats(float* f) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void from_lane(int lane) {
+    float* const f[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) *f[e] = __shfl_sync(0xffffffffu, *f[e], lane);
+  }
+  template <typename TO>
+  __device__ __forceinline__ uint4 packed() const {
+    return make_uint4(pack16<TO>(a.x, a.y), pack16<TO>(a.z, a.w), pack16<TO>(b.x, b.y), pack16<TO>(b.z, b.w));
+  }
 };
 
 // Signed turns of position p at a step of 2^-64 turns, doubled: half turns in [-1, 1).
@@ -83,20 +107,65 @@ __device__ __forceinline__ float half_turns(int p, unsigned long long step) {
   return (float)(int)((step * (unsigned long long)p) >> 32) * 0x1p-31f;
 }
 
+// A head's eight elements of this lane, those of the partners in the same order.
+template <typename TI, typename T, int FORM>
+struct RopeLane {
+  int lane, c, e0, half, rot;
+  bool mine, turned;
+  float* mem;  // the head's elements, for partners that are not a lane's chunk
+
+  __device__ __forceinline__ void partners(const Chunk<TI>& raw, const float (&x)[8], float (&other)[8]) const {
+    if constexpr (FORM == kRopePairs) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = e0 + e < rot ? x[e ^ 1] : 0.f;
+    } else if constexpr (FORM == kRopeHalf) {
+      const int from = (lane - c + (e0 < half ? c + half / 8 : c - half / 8)) & 31;
+      Chunk<TI> o = raw;
+      o.from_lane(from);
+      o.floats(other);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = turned ? other[e] : 0.f;
+    } else if constexpr (FORM == kRopeHalfOdd) {
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mem[e0 + e] = x[e];
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int el = e0 + e;
+        other[e] = el < half ? mem[el + half] : el < rot ? mem[el - half] : 0.f;
+      }
+    }
+  }
+};
+
 template <typename TI, typename T, int FORM>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int W = kRopeThreads / 32;
   __shared__ float exchange[FORM == kRopeHalfOdd ? kRopeThreads * 8 : 1];
+  __shared__ float2 turns[FORM == kRopeNone ? 1 : W][FORM == kRopeNone ? 1 : 128 + 4];  // A cos, A sin of a pair
   const int lane = threadIdx.x & 31;
-  const int L = a.lanes, c = lane & (L - 1), sub = lane / L, heads_at_once = 32 / L;
-  const int e0 = c * 8, half = a.rot / 2;
-  const bool mine = e0 < a.dim;
-  const long long warp = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
+  const int L = a.lanes, sub = lane / L, at_once = 32 / L;
+  RopeLane<TI, T, FORM> me;
+  me.lane = lane;
+  me.c = lane & (L - 1);
+  me.e0 = me.c * 8;
+  me.rot = a.rot;
+  me.half = a.rot / 2;
+  me.mine = me.e0 < a.dim;
+  me.turned = me.mine && me.e0 < a.rot;
+  me.mem = exchange + (FORM == kRopeHalfOdd ? (threadIdx.x - me.c) * 8 : 0);
+  const int e0 = me.e0;
+  const bool mine = me.mine;
+  float2* const angle = turns[FORM == kRopeNone ? 0 : threadIdx.x >> 5];
+  const long long warp = (long long)blockIdx.x * W + (threadIdx.x >> 5);
+  const long long warps = (long long)gridDim.x * W;
+  const float inv_dim = 1.f / (float)a.dim;
   griddep_wait();
   griddep_launch_dependents();
   const int q_heads = a.q_heads, kv = a.kv_heads, all = q_heads + 2 * kv;
   for (long long item = warp; item < a.tokens * a.parts; item += warps) {
-    const long long t = item / a.parts;
+    const long long t = a.parts == 1 ? item : item / a.parts;
     const int h0 = (int)(item - t * a.parts) * a.per_part, h1 = min(h0 + a.per_part, all);
     const int pos = __ldg(a.positions + t);
     if (pos < 0) continue;  // uniform in the warp: not a row
@@ -110,107 +179,94 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
     }
     const int id = slot < 0 ? 0 : slot / a.page;
     const long long row = ((long long)id * kv * a.page + (slot - id * a.page)) * a.dim;  // head 0 of the slot
-    // the rotation of this lane's elements
-    float cs[8], sn[8];
-    bool turned = false;
     if constexpr (FORM != kRopeNone) {
-      turned = mine && e0 < a.rot;
+      if (h0 < q_heads + kv) {
+        __syncwarp();  // the last token's have been read
+        for (int i = lane; i < me.half; i += 32) {
+          float s, co;
+          sincospif(half_turns(pos, __ldg(a.steps + i)), &s, &co);
+          angle[i] = make_float2(co * a.amplitude, s * a.amplitude);
+        }
+        __syncwarp();
+      }
+    }
+    // query heads, then key heads
+#pragma unroll 1
+    for (int keys = 0; keys < 2; ++keys) {
+      const int first = keys ? q_heads : 0, end = keys ? q_heads + kv : q_heads;
+      const int from = max(h0, first), to = min(h1, end);
+      if (from >= to || (keys && slot < 0)) continue;
+      const float* const w = keys ? a.k_weight : a.q_weight;
+      // the factors of this lane's elements and of their partners
+      float own[8], far[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int el = e0 + e;
-        const bool in = el < a.rot;
-        const int i = FORM == kRopePairs ? el / 2 : el < half ? el : el - half;
-        if (FORM == kRopePairs && (e & 1)) {
-          cs[e] = cs[e - 1];
-          sn[e] = -sn[e - 1];
-          continue;
+        const bool in = FORM != kRopeNone && el < a.rot;
+        const int i = FORM == kRopePairs ? el >> 1 : el < me.half ? el : el - me.half;
+        const int partner = FORM == kRopePairs ? el ^ 1 : el < me.half ? el + me.half : el - me.half;
+        float2 cs = make_float2(1.f, 0.f);
+        if (in) cs = angle[i];
+        // y = x cos + partner sin: the first of a pair takes - sin, the second + sin
+        const bool second = FORM == kRopePairs ? e & 1 : el >= me.half;
+        own[e] = cs.x;
+        far[e] = second ? cs.y : -cs.y;
+        if (w != nullptr && mine) {
+          own[e] *= __ldg(w + el);
+          if (in) far[e] *= __ldg(w + partner);
         }
-        float s = 0.f, co = 1.f;
-        if (in) {
-          sincospif(half_turns(pos, __ldg(a.steps + i)), &s, &co);
-          s *= a.amplitude;
-          co *= a.amplitude;
+      }
+      const TI* const src = (keys ? static_cast<const TI*>(a.k) + t * a.k_stride : static_cast<const TI*>(a.q) + t * a.q_stride) + e0;
+      T* const dst = (keys ? static_cast<T*>(a.ck) + row : static_cast<T*>(a.q_out) + t * q_heads * a.dim) + e0;
+      const long long step = keys ? (long long)a.page * a.dim : a.dim;
+#pragma unroll 1
+      for (int hb = from; hb < to; hb += at_once * kRopeAhead) {
+        Chunk<TI> raw[kRopeAhead];
+#pragma unroll
+        for (int u = 0; u < kRopeAhead; ++u) {
+          const int h = hb + u * at_once + sub;
+          if (mine && h < to) raw[u].load(src + (h - first) * a.dim);
+          else raw[u].clear();
         }
-        // y = x cos + partner sn: the first of a pair takes - sin, the second + sin
-        cs[e] = co;
-        sn[e] = FORM == kRopePairs || el < half ? -s : s;
+#pragma unroll
+        for (int u = 0; u < kRopeAhead; ++u) {
+          const int h = hb + u * at_once + sub;
+          if (hb + u * at_once >= to) break;  // of every lane
+          float x[8], y[8];
+          raw[u].floats(x);
+          float r = 1.f;
+          if (w != nullptr) {
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+            for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            r = rsqrtf(fmaf(sum, inv_dim, a.eps));
+          }
+          if constexpr (FORM == kRopeNone) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e] * own[e] * r;
+          } else {
+            float other[8];
+            me.partners(raw[u], x, other);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(other[e], far[e], x[e] * own[e]) * r;
+          }
+          if (mine && h < to)
+            *reinterpret_cast<uint4*>(dst + (h - first) * step) = make_uint4(
+                pack16<T>(y[0], y[1]), pack16<T>(y[2], y[3]), pack16<T>(y[4], y[5]), pack16<T>(y[6], y[7]));
+        }
       }
     }
-    for (int hb = h0; hb < h1; hb += heads_at_once * kRopeAhead) {
-      Chunk<TI> raw[kRopeAhead];
-#pragma unroll
-      for (int u = 0; u < kRopeAhead; ++u) {
-        const int h = hb + u * heads_at_once + sub;
-        if (!mine || h >= h1) continue;
-        const TI* const src = h < q_heads ? static_cast<const TI*>(a.q) + t * a.q_stride + (long long)h * a.dim
-                              : h < q_heads + kv
-                                  ? static_cast<const TI*>(a.k) + t * a.k_stride + (long long)(h - q_heads) * a.dim
-                                  : static_cast<const TI*>(a.v) + t * a.v_stride + (long long)(h - q_heads - kv) * a.dim;
-        raw[u].load(src + e0);
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeAhead; ++u) {
-        const int h = hb + u * heads_at_once + sub;
-        if (hb + u * heads_at_once >= h1) break;  // of every lane
-        const bool live = mine && h < h1, value = h >= q_heads + kv;
-        float x[8];
-        if (live) {
-          raw[u].floats(x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        }
-        const float* const w = h < q_heads ? a.q_weight : a.k_weight;
-        // (the sum's shuffles are for all lanes)
-        if (a.q_weight != nullptr || a.k_weight != nullptr) {
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-          for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          if (w != nullptr && live && !value) {
-            const float r = 1.f / sqrtf(sum / (float)a.dim + a.eps);
-            const float4 wa = __ldg(reinterpret_cast<const float4*>(w + e0)), wb = __ldg(reinterpret_cast<const float4*>(w + e0) + 1);
-            const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * r * ws[e];
-          }
-        }
-        if constexpr (FORM != kRopeNone) {
-          float other[8];
-          if constexpr (FORM == kRopePairs) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) other[e] = x[e ^ 1];
-          } else if constexpr (FORM == kRopeHalf) {
-            const int from = lane - c + (e0 < half ? c + half / 8 : c - half / 8);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(0xffffffffu, x[e], from & 31);
-          } else {
-            float* const mem = exchange + (threadIdx.x - c) * 8;  // the head's elements
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mem[e0 + e] = x[e];
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int el = e0 + e;
-              other[e] = el < half ? mem[el + half] : el < a.rot ? mem[el - half] : 0.f;
-            }
-          }
-          if (turned && !value) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e0 + e < a.rot) x[e] = fmaf(other[e], sn[e], x[e] * cs[e]);
-          }
-        }
-        if (!live) continue;
-        T* dst;
-        if (h < q_heads) dst = static_cast<T*>(a.q_out) + (t * q_heads + h) * a.dim;
-        else if (slot < 0) continue;
-        else if (!value) dst = static_cast<T*>(a.ck) + row + (long long)(h - q_heads) * a.page * a.dim;
-        else dst = static_cast<T*>(a.cv) + row + (long long)(h - q_heads - kv) * a.page * a.dim;
-        *reinterpret_cast<uint4*>(dst + e0) = make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]),
-                                                         pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
-      }
+    // values as they are
+    const int from = max(h0, q_heads + kv);
+    if (from >= h1 || slot < 0 || !mine) continue;
+    const TI* const src = static_cast<const TI*>(a.v) + t * a.v_stride + e0;
+    T* const dst = static_cast<T*>(a.cv) + row + e0;
+#pragma unroll 4
+    for (int h = from + sub; h < h1; h += at_once) {
+      Chunk<TI> raw;
+      raw.load(src + (h - q_heads - kv) * a.dim);
+      *reinterpret_cast<uint4*>(dst + (long long)(h - q_heads - kv) * a.page * a.dim) = raw.template packed<T>();
     }
   }
 }

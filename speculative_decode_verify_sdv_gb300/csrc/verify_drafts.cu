@@ -5,14 +5,15 @@
 //   one that is not, the next token is drawn from max(p_i - q_i, 0), else from p_n:
 //   the lowest v whose running weight exceeds u_S-1 of the total.
 //
-// Two launches.  The first reads every row once: per chunk of 2048 logits the maximum m and
-// sum 2^((x - m) c), c = log2(e) / T (or, greedy, the place of the maximum).  Reading the logits
-// bounds it.  The second has a cluster per sequence: it joins the rows' sums, runs the tests and
-// draws from the one row left.  Without drafts the second does it all.
+// Two launches.  The first reads every row once: per chunk of 1024 logits the maximum m and
+// sum 2^(x c - K), c = log2(e) / T, K = ceil(m c) (or, greedy, the place of the maximum).  The
+// second joins the rows' sums, runs the tests and draws: from a row of the target by the chunks'
+// sums and one more look at one chunk; from what a drafter's probabilities leave of a row by a
+// pass over it with a cluster of CTAs per sequence.
 //
 // A draw compares running sums of up to 10^5 weights with a random number, so an error of e of
 // the total gives another token with a chance of 10^5 e: 32-bit weights, whose errors of 2^-24
-// add up to 10^-9 of the total or more, would miss one draw in some thousands.  The row's weights
+// add up to 10^-9 of the total or more, would miss one draw in some thousands.  The weights
 // are therefore pairs of floats, exact to some 2^-30 of each (2^x by a table of 2^(k/32) and a
 // short polynomial: Tang, "Table-driven implementation of the exponential function", ACM TOMS
 // 1989), and their sums carry the rounding of every addition along (Knuth's two-sum).  No sum is
@@ -36,11 +37,13 @@ namespace sdv {
 
 namespace {
 
-constexpr int kStatChunk = 2048;   // logits of a warp's unit of work in the first launch
-constexpr int kDrawChunk = 1024;   // and in the second: two for each thread of a CTA
+constexpr int kStatChunk = 1024;   // logits of a warp's unit of work in the first launch
+constexpr int kDrawChunk = 512;    // and of its pass in the second
 constexpr int kStatThreads = 128;
-constexpr int kDrawThreads = 512;
+constexpr int kDrawThreads = 256;
+constexpr int kDrawWarps = kDrawThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kShares = kMaxCluster * kDrawWarps;  // warps of a sequence, at most
 constexpr int kMaxDrafts = 31;
 
 struct DraftArgs {
@@ -51,8 +54,8 @@ struct DraftArgs {
   const float *probs, *uniforms;
   int32_t *accepted, *next;
   int B, S, V, chunks, draws;  // chunks of a row in the two launches
-  float2* stats;              // [B * S][chunks] (no drafts: [B][draws]): maximum, sum (greedy: the bits of its place)
-  float2 *sums, *rests;       // [B][draws]: the drawn row's weights, and what the drafter's leave of them
+  int share;                   // chunks of a warp in the second
+  float4* stats;              // [B * S][chunks]: maximum, sum in two floats (greedy: the bits of its place)
 };
 
 __device__ const float kPowHi[32] = {
@@ -77,6 +80,20 @@ __device__ __forceinline__ float logit(const T* p) {
   return counted_logit((float)*p);
 }
 
+__device__ __forceinline__ void group_floats(const uint4& x, float (&f)[4], float) {
+  f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+}
+template <typename T>
+__device__ __forceinline__ void group_floats(const uint4& x, float (&f)[8], T) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = unpack16<T>(w[i]);
+    f[2 * i] = y.x;
+    f[2 * i + 1] = y.y;
+  }
+}
+
 // Row r's logits in groups of 16 bytes from an aligned address on, the first `shift` elements of
 // which lie before the row; a chunk is CHUNK elements of groups, 32 groups (one a lane) a step.
 template <typename T, int CHUNK>
@@ -98,65 +115,54 @@ struct Row {
   __device__ __forceinline__ float at(int v) const {
     return v >= 0 && v < V ? counted_logit((float)__ldg(p + v)) : -INFINITY;
   }
-  // A chunk's elements as they count, of this lane; their maximum over the warp.
-  __device__ __forceinline__ float chunk(int n, int lane, float (&x)[kSteps][kPer]) const;
-};
-
-__device__ __forceinline__ void group_floats(const uint4& x, float (&f)[4], float) {
-  f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
-}
-template <typename T>
-__device__ __forceinline__ void group_floats(const uint4& x, float (&f)[8], T) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  __device__ __forceinline__ void load_chunk(int n, int lane, uint4 (&raw)[kSteps]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 y = unpack16<T>(w[i]);
-    f[2 * i] = y.x;
-    f[2 * i + 1] = y.y;
+    for (int s = 0; s < kSteps; ++s) {
+      const int v = first(n, s, lane);
+      if (whole(v)) raw[s] = load(v);
+    }
   }
-}
-
-template <typename T, int CHUNK>
-__device__ __forceinline__ float Row<T, CHUNK>::chunk(int n, int lane, float (&x)[kSteps][kPer]) const {
-  uint4 raw[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int v = first(n, s, lane);
-    if (whole(v)) raw[s] = load(v);
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
+  // Elements of a loaded chunk's step as they count.
+  __device__ __forceinline__ void step(int n, int s, int lane, const uint4& raw, float (&x)[kPer]) const {
     const int v = first(n, s, lane);
     if (whole(v)) {
-      group_floats(raw[s], x[s], T());
+      group_floats(raw, x, T());
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[s][e] = counted_logit(x[s][e]);
+      for (int e = 0; e < kPer; ++e) x[e] = counted_logit(x[e]);
     } else {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[s][e] = at(v + e);
+      for (int e = 0; e < kPer; ++e) x[e] = at(v + e);
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[s][e]);
   }
+  __device__ __forceinline__ float largest(int n, int lane, const uint4 (&raw)[kSteps]) const {
+    float m = -INFINITY;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  return m;
-}
-
-// The lowest place of a chunk's maximum.
-template <typename R>
-__device__ __forceinline__ int place_of(const R& r, int n, int lane, const float (&x)[R::kSteps][R::kPer], float m) {
-  int best = INT_MAX;
+    for (int s = 0; s < kSteps; ++s) {
+      float x[kPer];
+      step(n, s, lane, raw[s], x);
 #pragma unroll
-  for (int s = 0; s < R::kSteps; ++s)
-#pragma unroll
-    for (int e = 0; e < R::kPer; ++e) {
-      const int v = r.first(n, s, lane) + e;
-      if (x[s][e] == m && v >= 0 && v < r.V) best = min(best, v);
+      for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[e]);
     }
-  return __reduce_min_sync(0xffffffffu, best);
-}
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    return m;
+  }
+  // The lowest place of a chunk's maximum.
+  __device__ __forceinline__ int place_of(int n, int lane, const uint4 (&raw)[kSteps], float m) const {
+    int best = INT_MAX;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float x[kPer];
+      step(n, s, lane, raw[s], x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int v = first(n, s, lane) + e;
+        if (x[e] == m && v >= 0 && v < V) best = min(best, v);
+      }
+    }
+    return __reduce_min_sync(0xffffffffu, best);
+  }
+};
 
 // log2(e) / T as a pair; greedy where T is 0, below, NaN, or so small that it overflows.
 struct Warmth {
@@ -173,40 +179,6 @@ struct Warmth {
     }
   }
 };
-
-template <typename T>
-__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftArgs a) {
-  using R = Row<T, kStatChunk>;
-  constexpr int W = kStatThreads / 32;
-  const int lane = threadIdx.x & 31, blocks = (a.chunks + W - 1) / W;
-  const int row = blockIdx.x / blocks;
-  const int chunk = (blockIdx.x - row * blocks) * W + (threadIdx.x >> 5);
-  const int b = row / a.S, i = row - b * a.S;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
-  if (chunk >= a.chunks || i > n) return;
-  const R r(a, row);
-  const float t = __ldg(a.temperature + b);
-  float x[R::kSteps][R::kPer];
-  const float m = r.chunk(chunk, lane, x);
-  const Warmth c(t);
-  float2 out = make_float2(m, 0.f);
-  if (c.greedy) {
-    out.y = __int_as_float(place_of(r, chunk, lane, x, m));
-  } else if (m != -INFINITY) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < R::kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < R::kPer; ++e) sum[e & 3] += exp2_approx((x[s][e] - m) * c.hi);
-    float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    out.y = all;
-  }
-  if (lane == 0) a.stats[(long long)row * a.chunks + chunk] = out;
-}
 
 // ---- precise weights -------------------------------------------------------------------
 
@@ -257,28 +229,43 @@ __device__ __forceinline__ Two warp_scan(Two x, int lane) {
   return x;
 }
 
-// 2^(x c - K) for the two x of a pair, K the exponent of the row's largest weight: exact to some
-// 2^-30 of each; 0 where it is below 2^-124 and where x is -inf.  For all lanes of a warp: lane k
-// holds 2^(k/32).  x c is taken apart as it is, K being a whole number; where it is so large that
-// its last bits are no fraction any more, the row's maximum is taken off x first.
+// 2^(x c - K) for the two x of a pair, K = ceil(m c) for the largest x: exact to some 2^-30 of
+// each; 0 where it is below 2^-124 and where x is -inf.  For all lanes of a warp: lane k holds
+// 2^(k/32).  x c is taken apart as it is, K being a whole number; where it is so large that its
+// last bits are no fraction any more, K is taken off first (exact: the two are close).  Past 2^24,
+// where neighbouring logits are a power of two and more apart, K is m c itself.
 struct Weigher {
-  float M, c_hi, c_lo, pow_hi, pow_lo, least;
+  float M, c_hi, c_lo, pow_hi, pow_lo, least, K, K_lo;
   uint32_t bias;
-  bool off;
+  bool off, far;
   __device__ __forceinline__ Weigher(float m, const Warmth& c, int lane)
       : M(m), c_hi(c.hi), c_lo(c.lo), pow_hi(kPowHi[lane]), pow_lo(kPowLo[lane]) {
     least = fmaxf(m - 124.f / c.hi, -FLT_MAX);
-    off = fabsf(m) * c.hi >= 16384.f;
-    const int K = off ? 0 : (int)ceilf(m * c.hi);
-    bias = ((uint32_t)(127 - K) << 23) - ((0x4b400000u >> 5) << 23);
+    K = ceilf(m * c.hi);
+    K_lo = 0.f;
+    if (!(fabsf(K) < INFINITY)) {  // so far from 0 that nothing but the largest has a weight
+      c_hi = c_lo = K = 0.f;
+      least = m;
+    }
+    off = fabsf(K) >= 65536.f;
+    far = fabsf(K) >= 16777216.f;
+    if (far) K_lo = fmaf(m, c_lo, fmaf(m, c_hi, -K));
+    bias = ((uint32_t)(127 - (off ? 0 : (int)K)) << 23) - ((0x4b400000u >> 5) << 23);
+  }
+  // The weight of a sum that is relative to the K of its own largest x, mk.
+  __device__ __forceinline__ float of_chunk(float mk) const {
+    if (!(mk >= least)) return 0.f;
+    if (far) {
+      const float d = mk - M, t = d * c_hi, tl = fmaf(d, c_lo, fmaf(d, c_hi, -t));
+      return exp2f(t) * fmaf(tl, 0.6931472f, 1.f);
+    }
+    return __uint_as_float((uint32_t)(127 + (int)(ceilf(mk * c_hi) - K)) << 23);
   }
   __device__ __forceinline__ Pair operator()(float x0, float x1) const {
     const bool in0 = x0 >= least, in1 = x1 >= least;
-    f32x2 x = pair2(in0 ? x0 : M, in1 ? x1 : M), x_lo = 0;
-    if (off) x = two_sum(x, both(-M), x_lo);
-    const f32x2 ch = both(c_hi), t = mul2(x, ch);
-    f32x2 tl = fma2(x, both(c_lo), fma2(x, ch, neg2(t)));
-    if (off) tl = fma2(x_lo, ch, tl);
+    const f32x2 x = pair2(in0 ? x0 : M, in1 ? x1 : M), ch = both(c_hi);
+    f32x2 t = mul2(x, ch), tl = fma2(x, both(c_lo), fma2(x, ch, neg2(t)));
+    if (off) t = two_sum(sub2(t, both(K)), sub2(tl, both(K_lo)), tl);
     // t = k / 32 + r, |r| <= 1 / 64: k in the low bits of a number of 1.5 2^23
     const f32x2 magic = both(12582912.f), kk = fma2(t, both(32.f), magic);
     const f32x2 r = fma2(sub2(kk, magic), both(-0.03125f), t);
@@ -298,6 +285,54 @@ struct Weigher {
   }
 };
 
+__device__ __forceinline__ void add_pair(Pair& sum, const Pair& w) {
+  f32x2 err;
+  sum.hi = two_sum(sum.hi, w.hi, err);
+  sum.lo = add2(sum.lo, add2(err, w.lo));
+}
+__device__ __forceinline__ Two lanes_sum(const Pair& sum) {
+  const float2 h = unpair2(sum.hi), l = unpair2(sum.lo);
+  return warp_sum(add_two(Two{h.x, l.x}, Two{h.y, l.y}));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftArgs a) {
+  using R = Row<T, kStatChunk>;
+  constexpr int W = kStatThreads / 32;
+  const int lane = threadIdx.x & 31, blocks = (a.chunks + W - 1) / W;
+  const int row = blockIdx.x / blocks;
+  const int chunk = (blockIdx.x - row * blocks) * W + (threadIdx.x >> 5);
+  const int b = row / a.S, i = row - b * a.S;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
+  if (chunk >= a.chunks || i > n) return;
+  const R r(a, row);
+  const float t = __ldg(a.temperature + b);
+  uint4 raw[R::kSteps];
+  r.load_chunk(chunk, lane, raw);
+  const float m = r.largest(chunk, lane, raw);
+  const Warmth c(t);
+  float4 out = make_float4(m, 0.f, 0.f, 0.f);
+  if (c.greedy) {
+    out.y = __int_as_float(r.place_of(chunk, lane, raw, m));
+  } else if (m != -INFINITY) {
+    const Weigher weigh(m, c, lane);
+    Pair sum{0, 0};
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      float x[R::kPer];
+      r.step(chunk, s, lane, raw[s], x);
+#pragma unroll
+      for (int e = 0; e < R::kPer; e += 2) add_pair(sum, weigh(x[e], x[e + 1]));
+    }
+    const Two all = lanes_sum(sum);
+    out.y = all.hi;
+    out.z = all.lo;
+  }
+  if (lane == 0) a.stats[(long long)row * a.chunks + chunk] = out;
+}
+
 // What max(w - q Z, 0) leaves, Z = z.hi + z.lo.
 __device__ __forceinline__ Pair rest_of(const Pair& w, float q0, float q1, Two z) {
   const f32x2 q = pair2(q0 > 0.f ? q0 : 0.f, q1 > 0.f ? q1 : 0.f);
@@ -311,38 +346,30 @@ __device__ __forceinline__ Pair rest_of(const Pair& w, float q0, float q1, Two z
               pair2(sum.x > 0.f ? dl.x : 0.f, sum.y > 0.f ? dl.y : 0.f)};
 }
 
-// A chunk's weights added up: of the row, without token `gone`, or (q given) what q leaves.
+// To a lane's sum what q leaves of the weights of its part of a chunk.
 template <typename R>
-__device__ __forceinline__ Two chunk_sum(const R& r, const Weigher& weigh, int n, int lane,
-                                         float (&x)[R::kSteps][R::kPer], int gone, const float* q, Two z) {
-  Pair sum{0, 0};
+__device__ __forceinline__ void add_rest(Pair& sum, const R& r, const Weigher& weigh, int n, int lane, const float* q,
+                                         Two z) {
+  uint4 raw[R::kSteps];
+  r.load_chunk(n, lane, raw);
 #pragma unroll
   for (int s = 0; s < R::kSteps; ++s) {
     const int v = r.first(n, s, lane);
-    float qs[R::kPer];
-    if (q != nullptr) {
-      if (r.whole(v) && (reinterpret_cast<uintptr_t>(q + v) & 15u) == 0) {
+    float x[R::kPer], qs[R::kPer];
+    if (r.whole(v) && (reinterpret_cast<uintptr_t>(q + v) & 15u) == 0) {
 #pragma unroll
-        for (int e = 0; e < R::kPer; e += 4)
-          *reinterpret_cast<float4*>(qs + e) = __ldg(reinterpret_cast<const float4*>(q + v + e));
-      } else {
-#pragma unroll
-        for (int e = 0; e < R::kPer; ++e) qs[e] = v + e >= 0 && v + e < r.V ? __ldg(q + v + e) : 0.f;
+      for (int e = 0; e < R::kPer; e += 4) {
+        const float4 y = __ldg(reinterpret_cast<const float4*>(q + v + e));
+        qs[e] = y.x, qs[e + 1] = y.y, qs[e + 2] = y.z, qs[e + 3] = y.w;
       }
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < R::kPer; e += 2) {
-      if (v + e == gone) x[s][e] = -INFINITY;
-      if (v + e + 1 == gone) x[s][e + 1] = -INFINITY;
-      Pair w = weigh(x[s][e], x[s][e + 1]);
-      if (q != nullptr) w = rest_of(w, qs[e], qs[e + 1], z);
-      f32x2 err;
-      sum.hi = two_sum(sum.hi, w.hi, err);
-      sum.lo = add2(sum.lo, add2(err, w.lo));
+      for (int e = 0; e < R::kPer; ++e) qs[e] = v + e >= 0 && v + e < r.V ? __ldg(q + v + e) : 0.f;
     }
+    r.step(n, s, lane, raw[s], x);
+#pragma unroll
+    for (int e = 0; e < R::kPer; e += 2) add_pair(sum, rest_of(weigh(x[e], x[e + 1]), qs[e], qs[e + 1], z));
   }
-  const float2 h = unpair2(sum.hi), l = unpair2(sum.lo);
-  return warp_sum(add_two(Two{h.x, l.x}, Two{h.y, l.y}));
 }
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -355,91 +382,134 @@ __device__ __forceinline__ unsigned cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
-// A list of sums by one warp, a lane a stretch of it in order.
+// Writes y to place `at` of the same list in every CTA of the cluster, a lane each.
+__device__ __forceinline__ void tell(float2* list, int at, float2 y, int lane, int size) {
+  if (lane >= size) return;
+  uint32_t to;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(list + at)), "r"(lane));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(y.x), "f"(y.y) : "memory");
+}
+
+// A list of sums, by one warp, a lane a stretch of it in order; `entry(i)` gives one.
+template <typename F>
 struct Listed {
-  int from, to;
+  F entry;
+  int n, lane, from, to;
   Two upto;  // all up to the end of this lane's
-  __device__ __forceinline__ Listed(const float2* list, int n, int lane) {
+  __device__ __forceinline__ Listed(int count, int l, F f) : entry(f), n(count), lane(l) {
     const int per = (n + 31) / 32;
     from = min(lane * per, n);
     to = min(from + per, n);
     Two mine{0.f, 0.f};
-    for (int i = from; i < to; ++i) {
-      const float2 x = __ldcg(list + i);
-      mine = add_two(mine, Two{x.x, x.y});
-    }
+#pragma unroll 4
+    for (int i = from; i < to; ++i) mine = add_two(mine, entry(i));
     upto = warp_scan(mine, lane);
   }
   __device__ __forceinline__ Two total() const { return shfl_at(upto, 31); }
+  // The entry in which the running sum first exceeds `want`, and the sum in front of it; the last
+  // entry with any weight and no bound where none does.
+  __device__ __forceinline__ int find(Two& want, Two& before) const {
+    const Two up = shfl_up(upto, 1);
+    Two run = lane > 0 ? up : Two{0.f, 0.f};
+    int hit = INT_MAX, last = -1;
+    before = run;
+#pragma unroll 4
+    for (int i = from; i < to; ++i) {
+      const Two x = entry(i), next = add_two(run, x);
+      if (x.hi > 0.f) {
+        last = i;
+        if (hit == INT_MAX && exceeds(next, want)) {
+          hit = i;
+          before = run;
+        }
+      }
+      run = next;
+    }
+    const int at = __reduce_min_sync(0xffffffffu, hit);
+    if (at != INT_MAX) {
+      before = shfl_at(before, __ffs(__ballot_sync(0xffffffffu, hit == at)) - 1);
+      return at;
+    }
+    want = Two{INFINITY, 0.f};
+    return __reduce_max_sync(0xffffffffu, last);
+  }
 };
+template <typename F>
+__device__ __forceinline__ Listed<F> listed(int n, int lane, F f) {
+  return Listed<F>(n, lane, f);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const DraftArgs a) {
+__global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const DraftArgs a) {
   using R = Row<T, kDrawChunk>;
-  constexpr int W = kDrawThreads / 32;
-  static_assert(kDrawChunk == 2 * kDrawThreads, "a pair of elements for each thread");
+  constexpr int W = kDrawWarps;
+  __shared__ float2 s_rests[kShares];
   __shared__ float s_max[kMaxDrafts + 1];
-  __shared__ int s_best[kMaxDrafts + 1];
+  __shared__ Two s_total[kMaxDrafts + 1], s_part[W], s_want, s_before;
+  __shared__ int s_best[kMaxDrafts + 1], s_token, s_last, s_at;
   __shared__ bool s_ok[kMaxDrafts + 1];
-  __shared__ Two s_total, s_before, s_want, s_part[W];
-  __shared__ int s_chunk, s_token, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int size = cluster_size(), rank = cluster_rank(), b = blockIdx.x / size;
+  if (tid == 0) {
+    s_token = INT_MAX;
+    s_last = -1;
+  }
+  cluster_arrive();
   griddep_wait();
+  cluster_wait();  // every CTA has begun: its shared memory can be written
   const float t = __ldg(a.temperature + b);
   const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
   const Warmth c(t);
-  float x[R::kSteps][R::kPer];
-  if (a.S == 1) {  // no launch in front has looked at the row
-    const R r(a, b);
-    for (int k = rank * W + warp; k < a.draws; k += size * W) {
-      const float m = r.chunk(k, lane, x);
-      const int best = c.greedy ? place_of(r, k, lane, x, m) : 0;
-      if (lane == 0) a.stats[(long long)b * a.draws + k] = make_float2(m, __int_as_float(best));
-    }
-    cluster_meet();
-  }
-  // every row's statistics, and its draft's test
-  const int listed = a.S == 1 ? a.draws : a.chunks;
+  // every row's sum, and its draft's test
   for (int i = warp; i <= n; i += W) {
     const long long row = (long long)b * a.S + i;
-    const float2* const st = a.stats + row * listed;
+    const float4* const st = a.stats + row * a.chunks;
     const int d = i < n ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;
     const bool real = d >= 0 && d < a.V;
     float m = -INFINITY;
-    for (int k = lane; k < listed; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
+#pragma unroll 4
+    for (int k = lane; k < a.chunks; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
+    const float u = __ldg(a.uniforms + (long long)b * a.S + i);
     const float xd = real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
     float q = a.probs != nullptr && real ? __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d) : 1.f;
     q = q > 0.f ? q : 0.f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float z = 0.f, p = 0.f;
+    Two z{0.f, 0.f};
+    float p = 0.f;
     int best = INT_MAX;
     if (c.greedy) {
-      for (int k = lane; k < listed; k += 32) {
-        const float2 s = __ldcg(st + k);
+      for (int k = lane; k < a.chunks; k += 32) {
+        const float4 s = __ldcg(st + k);
         if (s.x == m) best = min(best, __float_as_int(s.y));
       }
       best = __reduce_min_sync(0xffffffffu, best);
-      z = 1.f;
+      z.hi = 1.f;
       p = real && d == best ? 1.f : 0.f;
-    } else if (i < n && m != -INFINITY) {
-      for (int k = lane; k < listed; k += 32) {
-        const float2 s = __ldcg(st + k);
-        z += s.y * exp2f((s.x - m) * c.hi);
+    } else if (m != -INFINITY) {
+      const Weigher weigh(m, c, lane);
+#pragma unroll 4
+      for (int k = lane; k < a.chunks; k += 32) {
+        const float4 s = __ldcg(st + k);
+        const float f = weigh.of_chunk(s.x);
+        z = add_two(z, Two{s.y * f, s.z * f});
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-      p = exp2f((xd - m) * c.hi);
+      z = warp_sum(z);
+      const Pair w = weigh(xd, xd);
+      p = unpair2(add2(w.hi, w.lo)).x;
     }
     if (lane == 0) {
-      s_ok[i] = i < n && real && __ldg(a.uniforms + (long long)b * a.S + i) * q * z < p;
+      s_ok[i] = i < n && real && u * q * z.hi < p;
       s_max[i] = m;
       s_best[i] = best;
+      s_total[i] = z;
     }
   }
   __syncthreads();
@@ -456,105 +526,122 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const DraftAr
   const R r(a, (long long)b * a.S + j);
   const Weigher weigh(m, c, lane);
   const bool rest = missed && a.probs != nullptr;
-  const int gone = missed && a.probs == nullptr ? __ldg(a.drafts + (long long)b * (a.S - 1) + j) : INT_MIN;
+  const int d = missed ? __ldg(a.drafts + (long long)b * (a.S - 1) + j) : -1;
+  const int gone = !rest && d >= 0 && d < a.V ? d : INT_MIN;  // the token that is not drawn
   const float* const q = rest ? a.probs + ((long long)b * (a.S - 1) + j) * a.V : nullptr;
-  float2* const sums = a.sums + (long long)b * a.draws;
-  float2* const rests = a.rests + (long long)b * a.draws;
-  for (int k = rank * W + warp; k < a.draws; k += size * W) {
-    r.chunk(k, lane, x);
-    const Two s = chunk_sum(r, weigh, k, lane, x, gone, nullptr, Two{0.f, 0.f});
-    if (lane == 0) sums[k] = make_float2(s.hi, s.lo);
-  }
-  cluster_meet();
-  const float2* list = sums;
-  Two z{0.f, 0.f};
-  bool left = false;  // whether the drafter's probabilities leave anything
+  const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1);
+  const Two z = s_total[j];
+  auto bound = [&](Two all) {
+    const float p = __fmul_rn(u, all.hi);
+    return Two{p, fmaf(u, all.lo, fmaf(u, all.hi, -p))};
+  };
+  bool left = false;    // whether the drafter's probabilities leave anything
+  int at, from, each;   // the entry of the list that the draw falls into; its first element, elements per thread
+  Two want, run;
   if (rest) {
+    const int share = rank * W + warp, k1 = min((share + 1) * a.share, a.draws);
+    Pair sum{0, 0};
+    for (int k = share * a.share; k < k1; ++k) add_rest(sum, r, weigh, k, lane, q, z);
+    const Two s = lanes_sum(sum);
+    tell(s_rests, share, make_float2(s.hi, s.lo), lane, size);
+    cluster_meet();
+    const auto list = listed(size * W, lane, [&](int i) { return Two{s_rests[i].x, s_rests[i].y}; });
+    const Two all = list.total();
+    left = all.hi > 0.f;
+    if (left) {
+      want = bound(all);
+      at = list.find(want, run);
+      if (at / W != rank) return;
+      from = at * a.share * kDrawChunk - r.shift;
+      each = kDrawChunk / kDrawThreads * a.share;
+    }
+  }
+  auto pair_at = [&](int v) {
+    Pair w = weigh(v == gone ? -INFINITY : r.at(v), v + 1 == gone ? -INFINITY : r.at(v + 1));
+    if (left)
+      w = rest_of(w, v >= 0 && v < a.V ? __ldg(q + v) : 0.f, v + 1 >= 0 && v + 1 < a.V ? __ldg(q + v + 1) : 0.f, z);
+    return w;
+  };
+  // The sum of a thread's stretch of elements, in order, and of all threads' in front of it.
+  auto stretch = [&](Two& before) {
+    Two mine{0.f, 0.f};
+    for (int e = 0; e < each; e += 2) {
+      const Pair w = pair_at(from + each * tid + e);
+      const float2 h = unpair2(w.hi), l = unpair2(w.lo);
+      mine = add_two(mine, add_two(Two{h.x, l.x}, Two{h.y, l.y}));
+    }
+    const Two incl = warp_scan(mine, lane);
+    if (lane == 31) s_part[warp] = incl;
+    __syncthreads();
+    Two all{0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if (k == warp) before = all;
+      all = add_two(all, s_part[k]);
+    }
+    const Two up = shfl_up(incl, 1);
+    if (lane > 0) before = add_two(before, up);
+    return all;
+  };
+  if (!left) {  // from the row itself, by the first launch's sums
+    if (rank != 0) return;
+    const int gone_chunk = gone >= 0 ? (gone + r.shift) / kStatChunk : -1;
+    each = kStatChunk / kDrawThreads;
+    Two without{0.f, 0.f}, front;
+    if (gone_chunk >= 0) {  // that chunk's sum without the token
+      from = gone_chunk * kStatChunk - r.shift;
+      without = stretch(front);
+    }
     if (warp == 0) {
-      const Two all = Listed(sums, a.draws, lane).total();
-      if (lane == 0) s_total = all;
+      const float4* const st = a.stats + ((long long)b * a.S + j) * a.chunks;
+      const auto list = listed(a.chunks, lane, [&](int i) {
+        if (i == gone_chunk) return without;
+        const float4 s = __ldcg(st + i);
+        const float f = weigh.of_chunk(s.x);
+        return Two{s.y * f, s.z * f};
+      });
+      want = bound(list.total());
+      at = list.find(want, run);
+      if (lane == 0) {
+        s_at = at;
+        s_want = want;
+        s_before = run;
+      }
     }
     __syncthreads();
-    z = s_total;
-    for (int k = rank * W + warp; k < a.draws; k += size * W) {
-      r.chunk(k, lane, x);
-      const Two s = chunk_sum(r, weigh, k, lane, x, INT_MIN, q, z);
-      if (lane == 0) rests[k] = make_float2(s.hi, s.lo);
+    at = s_at;
+    want = s_want;
+    run = s_before;
+    if (at < 0) {  // all weight was the draft's that was not kept
+      if (tid == 0) a.next[b] = gone;
+      return;
     }
-    cluster_meet();
+    from = at * kStatChunk - r.shift;
   }
-  if (rank != 0) return;
-  // the chunk that the draw falls into
-  if (warp == 0) {
-    Listed l(rest ? rests : sums, a.draws, lane);
-    list = rest ? rests : sums;
-    left = rest;
-    if (rest && !(l.total().hi > 0.f)) {  // nothing: from the row itself
-      l = Listed(sums, a.draws, lane);
-      list = sums;
-      left = false;
+  Two front;
+  stretch(front);
+  run = add_two(run, front);
+  int token = INT_MAX, last = -1;
+  for (int e = 0; e < each; e += 2) {
+    const int v = from + each * tid + e;
+    const Pair w = pair_at(v);
+    const float2 h = unpair2(w.hi), l = unpair2(w.lo);
+    run = add_two(run, Two{h.x, l.x});
+    if (h.x > 0.f) {
+      last = v;
+      if (exceeds(run, want)) token = min(token, v);
     }
-    const Two all = l.total();
-    const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1), p = __fmul_rn(u, all.hi);
-    const Two want{p, fmaf(u, all.lo, fmaf(u, all.hi, -p))};
-    const unsigned hit = __ballot_sync(0xffffffffu, exceeds(l.upto, want));
-    // its lane, and the running sum in front; a random number of 1 and above, or none: the last one's
-    const int at = hit ? __ffs(hit) - 1 : 31;
-    const Two front = at > 0 ? shfl_at(l.upto, at - 1) : Two{0.f, 0.f};
-    if (lane == at) {
-      int chunk = -1, i = hit ? l.from : 0;
-      Two run = hit ? front : Two{0.f, 0.f}, before = run, bound = want;
-      for (; i < a.draws; ++i) {
-        const float2 s = __ldcg(list + i);
-        const Two next = add_two(run, Two{s.x, s.y});
-        if (s.x > 0.f) {
-          chunk = i;
-          before = run;
-          if (exceeds(next, want)) break;
-        }
-        run = next;
-      }
-      if (chunk < 0) {  // only roundings of the running sum were behind: the last weight there is
-        for (i = l.from - 1; i >= 0 && chunk < 0; --i)
-          if (__ldcg(list + i).x > 0.f) chunk = i;
-        bound = Two{INFINITY, 0.f};
-      }
-      s_chunk = all.hi > 0.f ? chunk : -1;
-      s_before = before;
-      s_want = bound;
-      s_total = Two{left ? 1.f : 0.f, 0.f};
-      s_token = INT_MAX;
-      s_last = -1;
+    run = add_two(run, Two{h.y, l.y});
+    if (h.y > 0.f) {
+      last = v + 1;
+      if (exceeds(run, want)) token = min(token, v + 1);
     }
   }
-  __syncthreads();
-  if (s_chunk < 0) {  // all weight was the draft's that was not kept
-    if (tid == 0) a.next[b] = gone;
-    return;
-  }
-  // and the token in it: two elements a thread, in order
-  const int v0 = r.first(s_chunk, 0, 0) + 2 * tid;
-  Pair w = weigh(v0 == gone ? -INFINITY : r.at(v0), v0 + 1 == gone ? -INFINITY : r.at(v0 + 1));
-  if (s_total.hi > 0.f)
-    w = rest_of(w, v0 >= 0 && v0 < a.V ? __ldg(q + v0) : 0.f, v0 + 1 >= 0 && v0 + 1 < a.V ? __ldg(q + v0 + 1) : 0.f, z);
-  const float2 h = unpair2(w.hi), l = unpair2(w.lo);
-  const Two w0{h.x, l.x}, w1{h.y, l.y}, mine = add_two(w0, w1), incl = warp_scan(mine, lane);
-  if (lane == 31) s_part[warp] = incl;
-  __syncthreads();
-  Two run = s_before;
-  for (int k = 0; k < warp; ++k) run = add_two(run, s_part[k]);
-  const Two up = shfl_up(incl, 1);
-  if (lane > 0) run = add_two(run, up);
-  const Two want = s_want;
-  run = add_two(run, w0);
-  if (w0.hi > 0.f) {
-    if (exceeds(run, want)) atomicMin(&s_token, v0);
-    atomicMax(&s_last, v0);
-  }
-  run = add_two(run, w1);
-  if (w1.hi > 0.f) {
-    if (exceeds(run, want)) atomicMin(&s_token, v0 + 1);
-    atomicMax(&s_last, v0 + 1);
+  token = __reduce_min_sync(0xffffffffu, token);
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0) {
+    if (token != INT_MAX) atomicMin(&s_token, token);
+    if (last >= 0) atomicMax(&s_last, last);
   }
   __syncthreads();
   if (tid == 0) a.next[b] = s_token != INT_MAX ? s_token : s_last;
@@ -562,28 +649,27 @@ __global__ void __launch_bounds__(kDrawThreads) verify_draw_kernel(const DraftAr
 
 int chunks_of(int V, int chunk) { return (int)(((long long)V + 7 + chunk - 1) / chunk); }
 
-size_t drafts_stats(int B, int S, int V) {
-  return round_256((size_t)B * (S == 1 ? chunks_of(V, kDrawChunk) : (size_t)S * chunks_of(V, kStatChunk)) * 8);
-}
-
 size_t drafts_need(int B, int S, int V) {
   if (B < 1 || S < 1 || S > kMaxDrafts + 1 || V < 1 || V > (1 << 24) || B > (1 << 24)) return 0;
   if ((unsigned long long)B * S * ((chunks_of(V, kStatChunk) + 3) / 4) > INT_MAX) return 0;
-  return kHeaderBytes + drafts_stats(B, S, V) + 2 * round_256((size_t)B * chunks_of(V, kDrawChunk) * 8);
+  return kHeaderBytes + round_256((size_t)B * S * chunks_of(V, kStatChunk) * 16);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <typename T>
-cudaError_t drafts_launch(const DraftArgs& a, cudaStream_t st) {
+cudaError_t drafts_launch(DraftArgs a, int sms, cudaStream_t st) {
   constexpr int W = kStatThreads / 32;
-  if (a.S > 1) {
-    const unsigned grid = (unsigned)((long long)a.B * a.S * ((a.chunks + W - 1) / W));
-    const cudaError_t e = launch_pdl(verify_stats_kernel<T>, dim3(grid), dim3(kStatThreads), 0, st, a);
-    if (e != cudaSuccess) return e;
-  }
-  int cluster = 1;  // CTAs of a sequence: a chunk for every warp, eight at most
-  while (cluster < kMaxCluster && cluster * (kDrawThreads / 32) < a.draws) cluster *= 2;
+  const unsigned grid = (unsigned)((long long)a.B * a.S * ((a.chunks + W - 1) / W));
+  const cudaError_t e = launch_pdl(verify_stats_kernel<T>, dim3(grid), dim3(kStatThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  // CTAs of a sequence: one, or where there are drafter's probabilities to look at eight at most,
+  // a chunk for every warp, and not more than run at once
+  int cluster = 1;
+  while (a.probs != nullptr && cluster < kMaxCluster && cluster * kDrawWarps < a.draws &&
+         2ll * cluster * a.B <= 3ll * sms)
+    cluster *= 2;
+  a.share = (a.draws + cluster * kDrawWarps - 1) / (cluster * kDrawWarps);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -640,14 +726,13 @@ sdv_status sdv_verify_drafts(int32_t dtype, const void* logits, int64_t row_stri
   a.V = V;
   a.chunks = sdv::chunks_of(V, sdv::kStatChunk);
   a.draws = sdv::chunks_of(V, sdv::kDrawChunk);
-  char* const at = static_cast<char*>(ws) + sdv::kHeaderBytes;
-  a.stats = reinterpret_cast<float2*>(at);
-  a.sums = reinterpret_cast<float2*>(at + sdv::drafts_stats(B, S, V));
-  a.rests = a.sums + sdv::round_256((size_t)B * a.draws * 8) / 8;
+  a.stats = reinterpret_cast<float4*>(static_cast<char*>(ws) + sdv::kHeaderBytes);
+  const int sms = sdv::sm_count();
+  if (sms <= 0) return SDV_ERR_CUDA;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return sdv::status_of(dtype == SDV_F32   ? sdv::drafts_launch<float>(a, st)
-                        : dtype == SDV_F16 ? sdv::drafts_launch<__half>(a, st)
-                                           : sdv::drafts_launch<__nv_bfloat16>(a, st));
+  return sdv::status_of(dtype == SDV_F32   ? sdv::drafts_launch<float>(a, sms, st)
+                        : dtype == SDV_F16 ? sdv::drafts_launch<__half>(a, sms, st)
+                                           : sdv::drafts_launch<__nv_bfloat16>(a, sms, st));
 }
 
 }  // extern "C"

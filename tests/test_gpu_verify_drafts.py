@@ -131,7 +131,7 @@ def test_filtered_rows(sdv):
     check(args, accepted, token)
 
 
-@pytest.mark.parametrize("t", [0.0, -1.0, float("nan"), 1e-42, float("inf"), 1e30, 1e-4])
+@pytest.mark.parametrize("t", [0.0, -1.0, float("nan"), 1e-42, float("inf"), 1e30, 1e-4, 1e-6, 1e-37, 3e-38])
 def test_temperatures(sdv, t):
     args = make(F32, 4, 3, 3001, True, 7)
     args[1].fill_(t)
@@ -245,5 +245,5 @@ def test_the_binding_refuses(sdv):
         with pytest.raises(TypeError):
             sdv.sdv_verify_drafts(*args[:k], bad, *args[k + 1:], i, i.clone(), ws)
     with pytest.raises(sdv.SdvError) as e:
-        sdv.sdv_verify_drafts(*args, i, i.clone(), ws[:512])
+        sdv.sdv_verify_drafts(*args, i, i.clone(), ws[:256])
     assert e.value.status == sdv.SDV_ERR_WORKSPACE
