@@ -58,13 +58,12 @@ template <typename T>
 struct Chunk {  // eight elements as they lie
   uint4 x;
   __device__ __forceinline__ void load(const T* p) { x = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void floats(float* f) const {
+  __device__ __forceinline__ void pairs(f32x2 (&f)[4]) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 y = unpack16<T>(w[i]);
-      f[2 * i] = y.x;
-      f[2 * i + 1] = y.y;
+      f[i] = pair2(y.x, y.y);
     }
   }
   __device__ __forceinline__ void clear() { x = make_uint4(0, 0, 0, 0); }
@@ -87,8 +86,8 @@ struct Chunk<float> {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void floats(float* f) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  __device__ __forceinline__ void pairs(f32x2 (&f)[4]) const {
+    f[0] = pair2(a.x, a.y), f[1] = pair2(a.z, a.w), f[2] = pair2(b.x, b.y), f[3] = pair2(b.z, b.w);
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void from_lane(int lane) {
@@ -114,27 +113,32 @@ struct RopeLane {
   bool mine, turned;
   float* mem;  // the head's elements, for partners that are not a lane's chunk
 
-  __device__ __forceinline__ void partners(const Chunk<TI>& raw, const float (&x)[8], float (&other)[8]) const {
+  __device__ __forceinline__ void partners(const Chunk<TI>& raw, const f32x2 (&x)[4], f32x2 (&other)[4]) const {
     if constexpr (FORM == kRopePairs) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) other[e] = e0 + e < rot ? x[e ^ 1] : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = unpair2(x[e]);
+        other[e] = e0 + 2 * e < rot ? pair2(v.y, v.x) : 0;
+      }
     } else if constexpr (FORM == kRopeHalf) {
       const int from = (lane - c + (e0 < half ? c + half / 8 : c - half / 8)) & 31;
       Chunk<TI> o = raw;
       o.from_lane(from);
-      o.floats(other);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) other[e] = turned ? other[e] : 0.f;
+      if (!turned) o.clear();
+      o.pairs(other);
     } else if constexpr (FORM == kRopeHalfOdd) {
       __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mem[e0 + e] = x[e];
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<f32x2*>(mem + e0 + 2 * e) = x[e];
       __syncwarp();
+      float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int el = e0 + e;
-        other[e] = el < half ? mem[el + half] : el < rot ? mem[el - half] : 0.f;
+        y[e] = el < half ? mem[el + half] : el < rot ? mem[el - half] : 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) other[e] = pair2(y[2 * e], y[2 * e + 1]);
     }
   }
 };
@@ -142,7 +146,7 @@ struct RopeLane {
 template <typename TI, typename T, int FORM>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int W = kRopeThreads / 32;
-  __shared__ float exchange[FORM == kRopeHalfOdd ? kRopeThreads * 8 : 1];
+  __shared__ alignas(16) float exchange[FORM == kRopeHalfOdd ? kRopeThreads * 8 : 1];
   __shared__ float2 turns[FORM == kRopeNone ? 1 : W][FORM == kRopeNone ? 1 : 128 + 4];  // A cos, A sin of a pair
   const int lane = threadIdx.x & 31;
   const int L = a.lanes, sub = lane / L, at_once = 32 / L;
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
       if (from >= to || (keys && slot < 0)) continue;
       const float* const w = keys ? a.k_weight : a.q_weight;
       // the factors of this lane's elements and of their partners
-      float own[8], far[8];
+      float fo[8], ff[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int el = e0 + e;
@@ -209,12 +213,18 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         if (in) cs = angle[i];
         // y = x cos + partner sin: the first of a pair takes - sin, the second + sin
         const bool second = FORM == kRopePairs ? e & 1 : el >= me.half;
-        own[e] = cs.x;
-        far[e] = second ? cs.y : -cs.y;
+        fo[e] = cs.x;
+        ff[e] = second ? cs.y : -cs.y;
         if (w != nullptr && mine) {
-          own[e] *= __ldg(w + el);
-          if (in) far[e] *= __ldg(w + partner);
+          fo[e] *= __ldg(w + el);
+          if (in) ff[e] *= __ldg(w + partner);
         }
+      }
+      f32x2 own[4], far[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        own[e] = pair2(fo[2 * e], fo[2 * e + 1]);
+        far[e] = pair2(ff[2 * e], ff[2 * e + 1]);
       }
       const TI* const src = (keys ? static_cast<const TI*>(a.k) + t * a.k_stride : static_cast<const TI*>(a.q) + t * a.q_stride) + e0;
       T* const dst = (keys ? static_cast<T*>(a.ck) + row : static_cast<T*>(a.q_out) + t * q_heads * a.dim) + e0;
@@ -232,28 +242,30 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         for (int u = 0; u < kRopeAhead; ++u) {
           const int h = hb + u * at_once + sub;
           if (hb + u * at_once >= to) break;  // of every lane
-          float x[8], y[8];
-          raw[u].floats(x);
+          f32x2 x[4];
+          raw[u].pairs(x);
           float r = 1.f;
           if (w != nullptr) {
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+            const f32x2 s2 = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
+            float sum = unpair2(s2).x + unpair2(s2).y;
             for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             r = rsqrtf(fmaf(sum, inv_dim, a.eps));
           }
-          if constexpr (FORM == kRopeNone) {
+          const f32x2 r2 = pair2(r, r);
+          f32x2 y[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * own[e] * r;
-          } else {
-            float other[8];
+          for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], own[e]);
+          if constexpr (FORM != kRopeNone) {
+            f32x2 other[4];
             me.partners(raw[u], x, other);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(other[e], far[e], x[e] * own[e]) * r;
+            for (int e = 0; e < 4; ++e) y[e] = fma2(other[e], far[e], y[e]);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], r2);
           if (mine && h < to)
-            *reinterpret_cast<uint4*>(dst + (h - first) * step) = make_uint4(
-                pack16<T>(y[0], y[1]), pack16<T>(y[2], y[3]), pack16<T>(y[4], y[5]), pack16<T>(y[6], y[7]));
+            *reinterpret_cast<uint4*>(dst + (h - first) * step) =
+                make_uint4(pack16<T>(y[0]), pack16<T>(y[1]), pack16<T>(y[2]), pack16<T>(y[3]));
         }
       }
     }

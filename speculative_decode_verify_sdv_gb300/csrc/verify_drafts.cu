@@ -26,6 +26,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "host_util.h"
 #include "mixing.h"
@@ -122,13 +123,11 @@ struct Row {
       if (whole(v)) raw[s] = load(v);
     }
   }
-  // Elements of a loaded chunk's step as they count.
+  // Elements of a loaded chunk's step as they lie; outside the row -inf.
   __device__ __forceinline__ void step(int n, int s, int lane, const uint4& raw, float (&x)[kPer]) const {
     const int v = first(n, s, lane);
     if (whole(v)) {
       group_floats(raw, x, T());
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) x[e] = counted_logit(x[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) x[e] = at(v + e);
@@ -141,11 +140,11 @@ struct Row {
       float x[kPer];
       step(n, s, lane, raw[s], x);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[e]);
+      for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[e]);  // (of a number and NaN the number)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    return m;
+    return fminf(m, FLT_MAX);
   }
   // The lowest place of a chunk's maximum.
   __device__ __forceinline__ int place_of(int n, int lane, const uint4 (&raw)[kSteps], float m) const {
@@ -157,7 +156,7 @@ struct Row {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         const int v = first(n, s, lane) + e;
-        if (x[e] == m && v >= 0 && v < V) best = min(best, v);
+        if (counted_logit(x[e]) == m && v >= 0 && v < V) best = min(best, v);
       }
     }
     return __reduce_min_sync(0xffffffffu, best);
@@ -185,9 +184,8 @@ struct Warmth {
 struct Pair {  // two numbers, each the sum of two floats
   f32x2 hi, lo;
 };
-__device__ __forceinline__ f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
-__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return add2(a, neg2(b)); }
 __device__ __forceinline__ f32x2 both(float x) { return pair2(x, x); }
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, both(-1.f), a); }  // (one instruction)
 // s = fl(a + b) and what the rounding took.
 __device__ __forceinline__ f32x2 two_sum(f32x2 a, f32x2 b, f32x2& err) {
   const f32x2 s = add2(a, b), t = sub2(s, a);
@@ -243,14 +241,16 @@ struct Weigher {
     least = fmaxf(m - 124.f / c.hi, -FLT_MAX);
     K = ceilf(m * c.hi);
     K_lo = 0.f;
-    if (!(fabsf(K) < INFINITY)) {  // so far from 0 that nothing but the largest has a weight
-      c_hi = c_lo = K = 0.f;
-      least = m;
+    if (!(fabsf(K) < 0x1p100f)) {  // nothing but the largest has a weight, nor has it at this c
+      c_hi = 0x1p40f / fabsf(m);
+      c_lo = 0.f;
+      K = ceilf(m * c_hi);
+      least = fmaxf(m - 124.f / c_hi, -FLT_MAX);
     }
     off = fabsf(K) >= 65536.f;
     far = fabsf(K) >= 16777216.f;
     if (far) K_lo = fmaf(m, c_lo, fmaf(m, c_hi, -K));
-    bias = ((uint32_t)(127 - (off ? 0 : (int)K)) << 23) - ((0x4b400000u >> 5) << 23);
+    bias = ((uint32_t)(127 - (off ? 0 : (int)K)) << 23) - (0x4b400000u << 18);
   }
   // The weight of a sum that is relative to the K of its own largest x, mk.
   __device__ __forceinline__ float of_chunk(float mk) const {
@@ -261,28 +261,41 @@ struct Weigher {
     }
     return __uint_as_float((uint32_t)(127 + (int)(ceilf(mk * c_hi) - K)) << 23);
   }
-  __device__ __forceinline__ Pair operator()(float x0, float x1) const {
-    const bool in0 = x0 >= least, in1 = x1 >= least;
-    const f32x2 x = pair2(in0 ? x0 : M, in1 ? x1 : M), ch = both(c_hi);
-    f32x2 t = mul2(x, ch), tl = fma2(x, both(c_lo), fma2(x, ch, neg2(t)));
-    if (off) t = two_sum(sub2(t, both(K)), sub2(tl, both(K_lo)), tl);
-    // t = k / 32 + r, |r| <= 1 / 64: k in the low bits of a number of 1.5 2^23
-    const f32x2 magic = both(12582912.f), kk = fma2(t, both(32.f), magic);
-    const f32x2 r = fma2(sub2(kk, magic), both(-0.03125f), t);
+  // EXACT: a weight that does not count is 0; else that of the least x that does, some 2^-124, which
+  // a sum does not notice (EXACT it is where no number is that far below).
+  template <bool EXACT = true>
+  __device__ __forceinline__ Pair weights(float x0, float x1) const {
+    // (NaN and -inf become the least)
+    const f32x2 x = pair2(fminf(fmaxf(x0, least), M), fminf(fmaxf(x1, least), M));
+    f32x2 t = mul2(x, both(-c_hi));  // - x c
+    f32x2 tl = fma2(x, both(c_lo), fma2(x, both(c_hi), t));
+    if (off) {
+      f32x2 err;
+      t = two_sum(add2(t, both(K)), sub2(both(K_lo), tl), err);
+      tl = sub2(both(0.f), err);
+    }
+    // x c = k / 32 - r, |r| <= 1 / 64: k in the low bits of a number of 1.5 2^23
+    const f32x2 magic = both(12582912.f), kk = fma2(t, both(-32.f), magic);
+    const f32x2 r = fma2(sub2(kk, magic), both(0.03125f), t);
     const float2 kf = unpair2(kk);
     const uint32_t k0 = __float_as_uint(kf.x), k1 = __float_as_uint(kf.y);
     const f32x2 th = pair2(__shfl_sync(0xffffffffu, pow_hi, k0), __shfl_sync(0xffffffffu, pow_hi, k1));
     const f32x2 tlo = pair2(__shfl_sync(0xffffffffu, pow_lo, k0), __shfl_sync(0xffffffffu, pow_lo, k1));
-    // 2^r = 1 + s, |s| < 0.011
-    f32x2 p = fma2(r, both(0.009618129f), both(0.05550411f));
+    // 2^-r = 1 + s, |s| < 0.011
+    f32x2 p = fma2(r, both(0.009618129f), both(-0.05550411f));
     p = fma2(r, p, both(0.24022651f));
-    p = fma2(r, p, both(0x1.62e430p-1f));
-    f32x2 s = fma2(tl, both(0x1.62e430p-1f), mul2(r, both(-0x1.05c610p-29f)));
+    p = fma2(r, p, both(-0x1.62e430p-1f));
+    f32x2 s = fma2(tl, both(0x1.62e430p-1f), mul2(r, both(0x1.05c610p-29f)));
     s = fma2(r, p, s);
-    const f32x2 scale = pair2(in0 ? __uint_as_float(((k0 >> 5) << 23) + bias) : 0.f,
-                              in1 ? __uint_as_float(((k1 >> 5) << 23) + bias) : 0.f);
+    float s0 = __uint_as_float(((k0 & ~31u) << 18) + bias), s1 = __uint_as_float(((k1 & ~31u) << 18) + bias);
+    if (EXACT) {
+      s0 = x0 >= least ? s0 : 0.f;
+      s1 = x1 >= least ? s1 : 0.f;
+    }
+    const f32x2 scale = pair2(s0, s1);
     return Pair{mul2(th, scale), mul2(fma2(th, s, tlo), scale)};
   }
+  __device__ __forceinline__ Pair operator()(float x0, float x1) const { return weights(x0, x1); }
 };
 
 __device__ __forceinline__ void add_pair(Pair& sum, const Pair& w) {
@@ -319,13 +332,18 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftA
   } else if (m != -INFINITY) {
     const Weigher weigh(m, c, lane);
     Pair sum{0, 0};
+    auto add = [&](auto exact) {
 #pragma unroll
-    for (int s = 0; s < R::kSteps; ++s) {
-      float x[R::kPer];
-      r.step(chunk, s, lane, raw[s], x);
+      for (int s = 0; s < R::kSteps; ++s) {
+        float x[R::kPer];
+        r.step(chunk, s, lane, raw[s], x);
 #pragma unroll
-      for (int e = 0; e < R::kPer; e += 2) add_pair(sum, weigh(x[e], x[e + 1]));
-    }
+        for (int e = 0; e < R::kPer; e += 2)
+          add_pair(sum, weigh.template weights<decltype(exact)::value>(x[e], x[e + 1]));
+      }
+    };
+    if (weigh.least > -FLT_MAX && !weigh.far) add(std::false_type());
+    else add(std::true_type());
     const Two all = lanes_sum(sum);
     out.y = all.hi;
     out.z = all.lo;
@@ -336,10 +354,10 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftA
 // What max(w - q Z, 0) leaves, Z = z.hi + z.lo.
 __device__ __forceinline__ Pair rest_of(const Pair& w, float q0, float q1, Two z) {
   const f32x2 q = pair2(q0 > 0.f ? q0 : 0.f, q1 > 0.f ? q1 : 0.f);
-  const f32x2 a = mul2(q, both(z.hi));
-  const f32x2 al = fma2(q, both(z.lo), fma2(q, both(z.hi), neg2(a)));
+  const f32x2 a = mul2(q, both(-z.hi));  // - q Z
+  const f32x2 al = fma2(q, both(z.lo), fma2(q, both(z.hi), a));
   f32x2 err;
-  const f32x2 d = two_sum(w.hi, neg2(a), err);
+  const f32x2 d = two_sum(w.hi, a, err);
   const f32x2 l = add2(err, sub2(w.lo, al));
   const float2 sum = unpair2(add2(d, l)), dh = unpair2(d), dl = unpair2(l);
   return Pair{pair2(sum.x > 0.f ? dh.x : 0.f, sum.y > 0.f ? dh.y : 0.f),
