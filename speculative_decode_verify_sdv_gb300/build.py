@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "dq_gemm.cu", "tc_gemm.cu", "gemv.cu", "small_kernels.cu", 
            "ngram_drafter.cu", "paged_attn.cu", "attn_tc.cu", "attn_tc_bf16.cu",
            "linear_attn.cu", "linear_tc.cu", "linear_tc_bf16.cu",
            "linear_window.cu", "page_assign.cu", "qk_norm_rope.cu", "prefix_attn.cu", "prefix_tc.cu",
-           "prefix_tc_bf16.cu", "verify_drafts.cu"]
+           "prefix_tc_bf16.cu", "prefix_own.cu", "verify_drafts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

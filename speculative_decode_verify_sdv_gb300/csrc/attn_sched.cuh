@@ -248,6 +248,15 @@ __device__ __forceinline__ uint32_t attn_word(const AttnArgs& a, int b, int i, i
   return (2u << i) - 1u;  // i = 31: 2 << 31 is 0, minus 1 is all ones
 }
 
+// Visibility of 32 positions from p on: context positions, the window's by `word`.
+__device__ __forceinline__ uint32_t attn_visible(int p, int ctx, uint32_t word) {
+  const int nc = min(max(ctx - p, 0), 32);
+  uint32_t bits = nc >= 32 ? 0xffffffffu : (1u << nc) - 1u;
+  if (p < ctx) bits |= nc >= 32 ? 0u : word << nc;
+  else bits |= p - ctx < 32 ? word >> (p - ctx) : 0u;
+  return bits;
+}
+
 // Four columns of an output: as the 16-bit type, or fp32 where another launch goes on with them.
 template <typename T>
 __device__ __forceinline__ void attn_store4(const AttnArgs& a, long long at, float x, float y, float z, float w) {

@@ -172,15 +172,6 @@ __device__ __forceinline__ uint32_t odd_of(uint32_t odd, int d) {
   return __shfl_sync(0xffffffffu, odd, d >> 3) >> (4 * (d & 7)) & 7u;
 }
 
-// Visibility of 32 positions from p on: context positions, the window's by `word`.
-__device__ __forceinline__ uint32_t attn_visible(int p, int ctx, uint32_t word) {
-  const int nc = min(max(ctx - p, 0), 32);
-  uint32_t bits = nc >= 32 ? 0xffffffffu : (1u << nc) - 1u;
-  if (p < ctx) bits |= nc >= 32 ? 0u : word << nc;
-  else bits |= p - ctx < 32 ? word >> (p - ctx) : 0u;
-  return bits;
-}
-
 // x / g for 0 <= x < 2^16 and 1 <= g <= 128, from 1 / g: x + 1/2 is at least 1/(2 g)
 // of a quotient away from the next, more than the error of two roundings.
 __device__ __forceinline__ int small_div(int x, float inv_g) { return (int)(((float)x + 0.5f) * inv_g); }

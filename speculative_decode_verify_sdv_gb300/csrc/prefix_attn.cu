@@ -5,8 +5,9 @@
 // Per query row, with the prefix's positions in parts j and the row's own positions:
 //   M = max m_j;  out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j;  lse = M + log sum.
 // The query rows of all sequences stand side by side as the rows of one product with the
-// prefix, which is so read once, not once a sequence; the own caches go through the paged
-// attention, which leaves fp32 outputs here; the join adds the two.
+// prefix, which is so read once, not once a sequence; the own caches go through a kernel of their
+// own (prefix_own.cu), or, where they may be long, through the paged attention, which deals any
+// lengths evenly and leaves fp32 outputs here; the join adds them all.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -14,12 +15,14 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_tc.h"
 #include "host_util.h"
 #include "mixing.h"
 #include "paged_attn.h"
 #include "prefix_attn.cuh"
+#include "prefix_own.cuh"
 #include "prefix_tc.h"
 #include "sdv.h"
 #include "sdv_device.cuh"
@@ -196,21 +199,29 @@ cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st
 
 constexpr int kMergeRows = 32, kMergeCols = 32;
 
+struct JoinArgs {
+  PrefixArgs prefix;
+  OwnArgs own;           // parts > 0: its partials; else attn.out32 and attn.lse hold outputs
+  void* out;
+  float* lse;            // or null
+};
+
 // 32 rows of a row tile and 32 columns per block, a thread per row and four columns with eight
-// partials in flight.  The partials lie row beside row, the outputs column beside column: the
-// sums go through shared memory between the two.
+// partials in flight.  The prefix's partials lie row beside row, the outputs column beside column:
+// the sums go through shared memory between the two.
 template <typename T>
-__global__ void __launch_bounds__(kMergeRows* kMergeCols / 4) prefix_join_kernel(const PrefixArgs a, const AttnArgs own,
-                                                                                 float* lse_or_null) {
+__global__ void __launch_bounds__(kMergeRows* kMergeCols / 4) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
   constexpr int LD = kMergeCols + 4;
   __shared__ float4 so[kMergeRows * LD / 4];
   __shared__ float2 sml[kMergeRows];
+  const PrefixArgs& a = j.prefix;
+  const AttnArgs& own = j.own.attn;
   const int D = a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, r0 = blockIdx.y * kMergeRows;
   const int per_head = (a.row_tiles + a.unit_tiles - 1) / a.unit_tiles;
   const int unit = h * per_head + rt / a.unit_tiles, sub = rt % a.unit_tiles;
   const int nr = min(a.row_tile, a.tokens * a.G - rt * a.row_tile), c0 = blockIdx.z * kMergeCols;
-  // (the split first, before the launches in front have ended: the length is an input)
+  // (the split first, before the launches in front have ended: the lengths are inputs)
   bool bad;
   const int tiles = prefix_tiles(a, prefix_length(a, bad));
   const long long total = (long long)tiles * a.units;
@@ -218,65 +229,80 @@ __global__ void __launch_bounds__(kMergeRows* kMergeCols / 4) prefix_join_kernel
   int parts = 0;
   if (tiles > 0)
     parts = attn_owner(total, live, (long long)unit * tiles + tiles - 1) - attn_owner(total, live, (long long)unit * tiles) + 1;
+  // eight threads a row for the outputs
+  const int i = threadIdx.x / (kMergeCols / 4), j4 = threadIdx.x % (kMergeCols / 4), d4 = c0 / 4 + j4, r = r0 + i;
+  const int row = rt * a.row_tile + min(r, nr - 1), token = row / a.G;
+  const int b = token / own.S, s = token - b * own.S;
+  const AttnSeq seq = attn_seq(own, b);
+  const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
   griddep_wait();
   griddep_launch_dependents();
   {
-    const int r = r0 + lane, d4 = c0 / 4 + warp;
+    const int rr = r0 + lane, dd = c0 / 4 + warp;
     AttnSum sum;
-    if (r < nr && d4 < D / 4) {
+    if (rr < nr && dd < D / 4) {
       const size_t first = (size_t)unit * a.sharers * a.unit_tiles + sub;
-      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * a.row_tile + r;
-      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * (D / 4) + d4) * a.row_tile + r;
+      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * a.row_tile + rr;
+      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * (D / 4) + dd) * a.row_tile + rr;
       const size_t step = (size_t)a.unit_tiles * a.row_tile;
-      for (int k0 = 0; k0 < parts; k0 += 8) {
-        float2 s[8];
-        float4 x[8];
+      auto gather = [&](auto odd) {
+        sum = AttnSum();
+        for (int k0 = 0; k0 < parts; k0 += 4) {
+          float2 ms[4];
+          float4 x[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s[k] = make_float2(-INFINITY, 0.f);
-          if (k0 + k >= parts) continue;
-          s[k] = __ldcg(ml + (k0 + k) * step);
-          x[k] = __ldcg(po + (k0 + k) * step * (D / 4));
+          for (int k = 0; k < 4; ++k) {
+            if (k0 + k >= parts) break;
+            ms[k] = __ldcg(ml + (k0 + k) * step);
+            x[k] = __ldcg(po + (k0 + k) * step * (D / 4));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k0 + k >= parts) break;
+            sum.add<decltype(odd)::value>(ms[k].x, ms[k].y, x[k]);
+          }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum.add<true>(s[k].x, s[k].y, x[k]);
-      }
+      };
+      gather(std::false_type());
+      if (!sum.finite()) gather(std::true_type());
     }
     so[lane * (LD / 4) + warp] = sum.o;
     if (warp == 0) sml[lane] = make_float2(sum.m, sum.l);
   }
   __syncthreads();
-  // eight threads a row
-  const int i = threadIdx.x / (kMergeCols / 4), j4 = threadIdx.x % (kMergeCols / 4), d4 = c0 / 4 + j4, r = r0 + i;
   if (r >= nr || d4 >= D / 4) return;
-  const int row = rt * a.row_tile + r, token = row / a.G;
-  const int b = token / own.S, s = token - b * own.S;
-  const bool alive = s < attn_seq(own, b).n;
-  const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
-  const float lse = __ldcg(own.lse + orow);
-  const float4 x = __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4);
   AttnSum sum;
   sum.m = sml[i].x;
   sum.l = sml[i].y;
   sum.o = so[i * (LD / 4) + j4];
-  // the own positions' output is that of a sum of 1 at a maximum of their lse
-  if (lse != -INFINITY) sum.add<true>(lse * 1.4426950408889634f, 1.f, x);
-  const bool none = !alive || sum.l == 0.f;
+  if (j.own.parts > 0) {
+    const int count = own_live_parts(seq.tiles, j.own.parts);
+    const long long step = (long long)a.tokens * a.Hq;
+#pragma unroll 2
+    for (int k = 0; k < count; ++k) {
+      const float2 ml = __ldcg(j.own.part_ml + k * step + orow);
+      sum.add<true>(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(j.own.part_o + (k * step + orow) * D) + d4));
+    }
+  } else {
+    // the own positions' output is that of a sum of 1 at a maximum of their lse
+    const float lse = __ldcg(own.lse + orow);
+    if (lse != -INFINITY)
+      sum.add<true>(lse * 1.4426950408889634f, 1.f, __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4));
+  }
+  const bool none = s >= seq.n || sum.l == 0.f;
   const float inv = 1.f / sum.l;
   const uint2 y = none ? make_uint2(0u, 0u)
                        : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv), pack16<T>(sum.o.z * inv, sum.o.w * inv));
-  reinterpret_cast<uint2*>(static_cast<T*>(own.out) + orow * D)[d4] = y;
-  if (d4 == 0 && lse_or_null != nullptr) lse_or_null[orow] = none ? -INFINITY : sum.lse();
+  reinterpret_cast<uint2*>(static_cast<T*>(j.out) + orow * D)[d4] = y;
+  if (d4 == 0 && j.lse != nullptr) j.lse[orow] = none ? -INFINITY : sum.lse();
 }
 
-// `own`: the paged attention's arguments, out32 and lse where it has left its outputs, `out` the
-// call's own; lse_or_null: the call's.
-cudaError_t launch_prefix_join(int dtype, const PrefixArgs& a, const AttnArgs& own, float* lse_or_null,
-                               cudaStream_t st) {
+cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, cudaStream_t st) {
+  const PrefixArgs& a = j.prefix;
   auto kernel = dtype == SDV_F16 ? prefix_join_kernel<__half> : prefix_join_kernel<__nv_bfloat16>;
   return launch_pdl(kernel, dim3(a.Hkv * a.row_tiles, (a.row_tile + kMergeRows - 1) / kMergeRows,
                                  (a.D + kMergeCols - 1) / kMergeCols),
-                    dim3(kMergeRows * kMergeCols / 4), 0, st, a, own, lse_or_null);
+                    dim3(kMergeRows * kMergeCols / 4), 0, st, j);
 }
 
 constexpr int kSimplePerSm = 2;
@@ -286,11 +312,11 @@ void set_units(PrefixArgs& a, bool tc, int sms) {
   if (tc) {
     // whole tokens, at most 128 rows, tiles of equal size
     const int most = a.G < kPrefixTcRows ? kPrefixTcRows / a.G : 1;
-    a.row_tiles = (a.tokens + most - 1) / most;
-    a.tile_tokens = (a.tokens + a.row_tiles - 1) / a.row_tiles;
+    a.tiles_most = (a.tokens + most - 1) / most;
+    a.tile_tokens = (a.tokens + a.tiles_most - 1) / a.tiles_most;
     a.row_tiles = (a.tokens + a.tile_tokens - 1) / a.tile_tokens;
     a.row_tile = a.tile_tokens * a.G;
-    a.unit_tiles = prefix_tc_streams(a.D, a.row_tiles);
+    a.unit_tiles = prefix_tc_streams(a.D, a.tiles_most);
     a.tile = kPrefixTcTile;
     a.ctas = sms;
   } else {
@@ -305,18 +331,36 @@ void set_units(PrefixArgs& a, bool tc, int sms) {
   a.sharers = (a.ctas + a.units - 1) / a.units + 1;
 }
 
+// Parts of a sequence's own positions: enough CTAs for two rounds of them.
+void set_parts(OwnArgs& o, int sms) {
+  o.row_tiles = own_row_tiles(o.attn.D, o.attn.rows);
+  o.row_groups = (o.attn.rows + 16 * o.row_tiles - 1) / (16 * o.row_tiles);
+  const long long units = (long long)o.attn.B * o.attn.Hkv * o.row_groups;
+  const long long parts = (16ll * sms + units - 1) / units;
+  o.parts = parts < kOwnMaxParts ? (int)parts : kOwnMaxParts;
+}
+
 struct PrefixBytes {
-  size_t part_ml, part_o, out32, lse, total;  // offsets
+  size_t part_ml, part_o, own_ml, own_o, total;  // offsets; own_ml, own_o: or the outputs' lse and fp32 values
 };
 
-PrefixBytes prefix_layout(const PrefixArgs& a, size_t own, int B, int S, int Hq) {
-  const size_t rows = (size_t)a.units * a.sharers * a.unit_tiles * a.row_tile, outs = (size_t)B * S * Hq;
+PrefixBytes prefix_layout(const PrefixArgs& a, size_t own, int B, int S, int sms) {
+  // units * sharers partials of unit_tiles * row_tile rows each, in terms that grow with the call
+  const int most = a.tile_tokens == 0 ? a.row_tile : kPrefixTcRows;
+  const size_t tiles_most = a.tile_tokens == 0 ? a.row_tiles : a.tiles_most;
+  const size_t units_most = a.Hkv * ((tiles_most + a.unit_tiles - 1) / a.unit_tiles);
+  const size_t rows = (a.ctas + 2 * units_most) * a.unit_tiles * most, outs = (size_t)B * S * a.Hq;
+  // a CTA has 16 * row_tiles rows at most, 256 / dim (at least one) row tiles at most
+  const int tiles = a.D >= 256 ? 1 : a.D >= 128 ? 2 : 4;
+  const size_t groups = ((size_t)S * a.G + 16 * tiles - 1) / (16 * tiles) * a.Hkv * B;
+  const size_t parts = (16 * (size_t)sms + 4 * groups) * 16 * tiles;
+  const size_t own_rows = parts > outs ? parts : outs;
   PrefixBytes p;
   p.part_ml = round_256(own);
   p.part_o = p.part_ml + round_256(rows * 8);
-  p.out32 = p.part_o + round_256(rows * a.D * 4);
-  p.lse = p.out32 + round_256(outs * a.D * 4);
-  p.total = p.lse + round_256(outs * 4);
+  p.own_ml = p.part_o + round_256(rows * a.D * 4);
+  p.own_o = p.own_ml + round_256(own_rows * 8);
+  p.total = p.own_o + round_256(own_rows * a.D * 4);
   return p;
 }
 
@@ -337,7 +381,7 @@ size_t prefix_need(int B, int S, int Hq, int heads, int dim) {
   const int sms = sm_count() > 0 ? sm_count() : 256;
   size_t most = 0;
   for (int tc = 0; tc < 2; ++tc) {
-    const size_t n = prefix_layout(prefix_shape(B, S, Hq, heads, dim, tc, sms), own, B, S, Hq).total;
+    const size_t n = prefix_layout(prefix_shape(B, S, Hq, heads, dim, tc, sms), own, B, S, sms).total;
     if (n > most) most = n;
   }
   return most;
@@ -384,21 +428,37 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   a.max_pages = prefix_pages;
   a.status = static_cast<int*>(ws);
   a.fault = sdv::debug_fault();
-  const sdv::PrefixBytes at = sdv::prefix_layout(a, sdv::attn_bytes(B, S, Hq, cache->heads, cache->dim), B, S, Hq);
+  const sdv::PrefixBytes at = sdv::prefix_layout(a, sdv::attn_bytes(B, S, Hq, cache->heads, cache->dim), B, S, sms);
   char* const base = static_cast<char*>(ws);
   a.part_ml = reinterpret_cast<float*>(base + at.part_ml);
   a.part_o = reinterpret_cast<float*>(base + at.part_o);
-  sdv::AttnArgs own = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
-  own.out32 = reinterpret_cast<float*>(base + at.out32);
-  own.lse = reinterpret_cast<float*>(base + at.lse);
   const cudaError_t e =
       tc ? sdv::launch_prefix_tc(cache->dtype, a, st) : sdv::launch_prefix_simple(cache->dtype, a, st);
   if (e != cudaSuccess) return sdv::status_of(e);
-  const sdv_status run = sdv::attn_run(cache, own, ws, st);
-  if (run != SDV_OK) return run;
-  own.out = out;
-  own.tile = 1;  // (of no meaning to the join)
-  return sdv::status_of(sdv::launch_prefix_join(cache->dtype, a, own, lse_or_null, st));
+  sdv::JoinArgs j{};
+  j.prefix = a;
+  j.out = out;
+  j.lse = lse_or_null;
+  sdv::OwnArgs& own = j.own;
+  own.attn = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
+  own.status = a.status;
+  sdv::set_parts(own, sms);
+  own.attn.fault = sdv::debug_fault();
+  if (tc && sdv::own_takes((long long)cache->max_pages * cache->page_size, own.parts)) {
+    own.attn.tile = sdv::kOwnTile;
+    own.part_ml = reinterpret_cast<float2*>(base + at.own_ml);
+    own.part_o = reinterpret_cast<float*>(base + at.own_o);
+    const cudaError_t e2 = sdv::launch_prefix_own(cache->dtype, own, st);
+    if (e2 != cudaSuccess) return sdv::status_of(e2);
+  } else {
+    own.parts = 0;
+    own.attn.out32 = reinterpret_cast<float*>(base + at.own_o);
+    own.attn.lse = reinterpret_cast<float*>(base + at.own_ml);
+    const sdv_status run = sdv::attn_run(cache, own.attn, ws, st);
+    if (run != SDV_OK) return run;
+    own.attn.tile = 1;  // (of no meaning to the join)
+  }
+  return sdv::status_of(sdv::launch_prefix_join(cache->dtype, j, st));
 }
 
 }  // extern "C"

@@ -27,7 +27,7 @@ struct PrefixArgs {
   int Hq, Hkv, G, D;
   int n_pages, page, max_pages;
   int tile_tokens, row_tile;  // tokens and query rows (tokens * G) of a row tile, at most 128
-  int row_tiles;              // of a kv head
+  int row_tiles, tiles_most;  // of a kv head; and what they would be if tiles held all rows they can
   int unit_tiles, units;      // row tiles of a unit (the last unit of a head may have fewer), units in all
   int tile;                   // positions per tile
   int sharers;                // places for partials of a unit

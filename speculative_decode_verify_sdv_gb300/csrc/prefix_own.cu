@@ -1,0 +1,418 @@
+// Attention of a batch's window rows to each sequence's own positions, behind a shared prefix.
+//
+// Per query row r of a kv head and own position p, as everywhere here:
+//   s = q_r . k_p;  m = running max of scale s;  P = 2^((scale s - m) log2 e)
+//   l += sum P;  O = O 2^(m_old - m) + P V
+// What follows a shared prefix is short and there is a lot of it: reading it bounds the kernel,
+// and a unit is over before a deep pipeline has filled.  So a warp, a CTA by itself, takes a part
+// of one sequence's positions for one kv head in slices of 32, which come by TMA: the next slice's
+// keys while this one's softmax and second product run, its values during the next first product.
+// What is start and end for one warp is not for the seven and more others of its SM.
+//
+// The products are m16n8k16 MMAs whose operands are read as they lie, 16 bytes a lane.  A dot
+// product does not ask for the order of its terms: a lane's 16 bytes of a key row are the reduction
+// indices of two MMAs, the queries being taken in the same order.  Nor does an output ask for
+// the order of its columns: a lane's 16 bytes of four value rows are one column each of eight
+// MMAs, after the halves of two rows have been put side by side.
+//
+// Window positions that a row does not see have weight 0, their values what is not finite taken
+// out; what is not finite among seen ones is told from the values at the end (as in the paged
+// attention's kernels).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_tc.h"
+#include "prefix_attn.cuh"
+#include "prefix_own.cuh"
+#include "sdv.h"
+#include "sdv_device.cuh"
+#include "tc_util.cuh"
+
+namespace sdv {
+
+namespace {
+
+constexpr int kOwnMost = 2048;  // positions that a part may come to
+constexpr uint64_t kOwnDrainNs = 100000000ull;  // 0.1 s: copies under way at the end
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// What is not finite in column d of the values that a row sees among positions from .. to - 1.
+template <typename T>
+__device__ __noinline__ uint32_t own_odd(const AttnArgs& a, int b, int h, int ctx, int from, int to, uint32_t word,
+                                         int d) {
+  uint32_t odd = 0;
+  for (int p = from; p < to; ++p) {
+    if (p >= ctx && !(word >> (p - ctx) & 1u)) continue;
+    const int id = __ldg(a.table + (size_t)b * a.max_pages + p / a.page);
+    if (id < 0 || id >= a.n_pages) continue;
+    const float x = (float)static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d];
+    if (!(fabsf(x) < INFINITY)) odd |= x != x ? kOddNan : x > 0.f ? kOddPlus : kOddMinus;
+  }
+  return odd;
+}
+
+constexpr int kSlice = 32;  // positions
+
+template <int D, int MT>
+struct OwnPlan {
+  static constexpr int R = 16 * MT;
+  static constexpr int kHalf = kSlice * D * 2;    // a slice's keys, its values
+  static constexpr int LQ = D * 2 + 64;           // bytes between query rows: eight lanes' 16-byte reads meet no bank twice
+  static constexpr int kSmem = 1024 + 2 * kHalf + R * LQ + 16;
+};
+
+struct OwnMaps {
+  CUtensorMap k, v;
+};
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(const __grid_constant__ OwnMaps maps,
+                                                                              const __grid_constant__ OwnArgs o) {
+  using PL = OwnPlan<D, MT>;
+  constexpr int R = PL::R, DB = D / 64, KB = D / 32, LQ = PL::LQ, NT = kSlice / 8, BLOCK = kSlice * 128;
+  constexpr float kLift = std::is_same<T, __nv_bfloat16>::value ? -kPrefixDrop : 6.f;  // P's power of two
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const sb = smem_raw + (base - raw);
+  uint8_t* const mem = sb + 2 * PL::kHalf;  // queries
+  const uint32_t bars = base + 2 * PL::kHalf + R * LQ;
+  const AttnArgs& a = o.attn;
+  const int lane = threadIdx.x, g = lane >> 2, c = lane & 3;
+  const int rg = blockIdx.x % o.row_groups, bh = blockIdx.x / o.row_groups, h = bh % a.Hkv, b = bh / a.Hkv;
+  // The launch in front has let this one start, so what came before it has ended; nothing is read
+  // that it writes.  It is waited for at the end, for the launch behind.
+  griddep_launch_dependents();
+  const AttnSeq seq = attn_seq(a, b);
+  const int ctx = seq.ctx, n = seq.n, total = ctx + n, per = own_per_part(seq.tiles, o.parts);
+  const int from = (int)blockIdx.y * per * kOwnTile, to = min(from + per * kOwnTile, total);
+  if (blockIdx.y > 0 && from >= total) return;
+  if (lane == 0) {
+    set_wait_limit(a.fault);
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
+    fence_barrier_init();
+    if (seq.bad) atomicOr(o.status, kDevErrIndex);
+  }
+  __syncwarp();
+  const int r0 = rg * R, rows = a.rows;
+  const int32_t* const table = a.table + (size_t)b * a.max_pages;
+  // ---- the copies: slice i is positions from + 32 i .. + 31 ----
+  const int page_log = 31 - __clz(a.page), box = min(a.page, kSlice), boxes = kSlice / box;
+  const int slices = (to - from + kSlice - 1) / kSlice;
+  const int beyond = a.n_pages * a.Hkv * a.page;  // a row past the tensor map's end: zeros
+  const uint64_t policy = l2_policy_evict_first();
+  // a lane's copy: a block of 64 elements, a page's part of the slice
+  const int cb = lane % DB, bx = lane / DB;
+  const bool mine = bx < boxes;
+  const uint32_t dst = base + cb * BLOCK + bx * box * 128;
+  auto page_of = [&](int i) {  // of the lane's copy in slice i; -1 past the end
+    const int p = from + kSlice * i + bx * box;
+    return mine && i < slices && p < to ? __ldg(table + (p >> page_log)) : -1;
+  };
+  auto row_of = [&](int i, int id) {
+    const int p = from + kSlice * i + bx * box;
+    return id >= 0 && id < a.n_pages ? (id * a.Hkv + h) * a.page + (p & (a.page - 1)) : beyond;
+  };
+  auto issue = [&](int values, int row) {
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8u * values, PL::kHalf);
+    __syncwarp();
+    if (mine) tma_load_2d(dst + values * PL::kHalf, values ? &maps.v : &maps.k, cb * 64, row, bars + 8u * values, policy);
+  };
+  int row_now = beyond, row_next = beyond, id_after = page_of(1);
+  if (slices > 0) {
+    row_now = row_of(0, page_of(0));
+    issue(0, row_now);
+    issue(1, row_now);
+  }
+  for (int e = lane; e < R * (D / 8); e += 32) {
+    const int r = e / (D / 8), ch = e % (D / 8), row = r0 + r;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (row < rows && row / a.G < n)
+      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + ((long long)b * a.S + row / a.G) * a.q_stride +
+                                               (h * a.G + row % a.G) * D) + ch);
+    *reinterpret_cast<uint4*>(mem + r * LQ + ch * 16) = x;
+  }
+  uint32_t words[MT][2];  // visibility of rows g and g + 8
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = r0 + t * 16 + half * 8 + g;
+      words[t][half] = row < rows ? attn_word(a, b, row / a.G, n) : 0u;
+    }
+  auto live = [&](int t, int half) {
+    const int row = r0 + t * 16 + half * 8 + g;
+    return row < rows && row / a.G < n;
+  };
+  // Pages of the part that cannot be followed make every slice look for them.
+  bool some_absent = false;
+  if (from < to)
+    for (int e = (from >> page_log) + lane; e <= (to - 1) >> page_log; e += 32) {
+      const int id = __ldg(table + e);
+      some_absent |= id < 0 || id >= a.n_pages;
+    }
+  some_absent = __any_sync(0xffffffffu, some_absent);
+  if (some_absent && lane == 0) atomicOr(o.status, kDevErrIndex);
+  __syncwarp();
+  float out[MT][8 * DB][4];
+  float m[MT][2], l[MT][2];
+  bool odd_values = false, ok = true;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+#pragma unroll
+    for (int j = 0; j < 8 * DB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[t][j][e] = 0.f;
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+  }
+  // operands' places: key row g, value row 2 c, under the 128-byte swizzle
+  const uint8_t* const ks = sb + g * 128;
+  const uint8_t* const vs = sb + PL::kHalf + c * 256;
+  const int k_chunk[2] = {(c ^ g) << 4, ((4 + c) ^ g) << 4};
+  const int v_chunk[2] = {(g ^ (2 * c)) << 4, (g ^ (2 * c + 1)) << 4};
+  const uint8_t* const qs = mem + g * LQ + c * 16;
+  int i = 0;
+  for (; i < slices; ++i) {
+    const int p0 = from + kSlice * i;
+    const bool more = i + 1 < slices;
+    row_next = row_of(i + 1, id_after);
+    id_after = page_of(i + 2);
+    ok = mbar_wait_warp(bars, i & 1, o.status);
+    if (!ok) break;
+    const bool edge = p0 + kSlice > ctx || some_absent;
+    float s[MT][NT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][j][e] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      uint4 kx[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        kx[j] = *reinterpret_cast<const uint4*>(ks + (kb >> 1) * BLOCK + j * 1024 + k_chunk[kb & 1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(qs + t * 16 * LQ + kb * 64);
+        const uint4 hi = *reinterpret_cast<const uint4*>(qs + (t * 16 + 8) * LQ + kb * 64);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816<T>(s[t][j], lo.x, hi.x, lo.y, hi.y, kx[j].x, kx[j].y);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816<T>(s[t][j], lo.z, hi.z, lo.w, hi.w, kx[j].z, kx[j].w);
+      }
+    }
+    __syncwarp();  // every lane has read the keys
+    if (more) issue(0, row_next);
+    uint32_t there = 0xffffffffu;  // positions that are there
+    if (edge) {
+      there = to - p0 >= 32 ? 0xffffffffu : (1u << (to - p0)) - 1u;
+      if (some_absent) {
+        int e = -1;
+        if (p0 + lane < to) e = __ldg(table + ((p0 + lane) >> page_log));
+        there &= __ballot_sync(0xffffffffu, e >= 0 && e < a.n_pages);
+      }
+    }
+    uint32_t p16[MT][2][NT];  // packed pairs
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[2 * NT];
+#pragma unroll
+        for (int e = 0; e < 2 * NT; ++e) x[e] = s[t][e >> 1][half * 2 + (e & 1)] * a.scale_log2;
+        if (edge) {
+          const uint32_t see = live(t, half) ? there & attn_visible(p0, ctx, words[t][half]) : 0u;
+#pragma unroll
+          for (int e = 0; e < 2 * NT; ++e)
+            if (!(see >> ((e >> 1) * 8 + c * 2 + (e & 1)) & 1u)) x[e] = -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int e = 1; e < 2 * NT; ++e) mx = fmaxf(mx, x[e]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool grow = mx > m[t][half] + 8.f;  // also from -inf to any number
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow && m[t][half] != -INFINITY ? exp2_approx(m[t][half] - mx) : 1.f;
+          if (grow) m[t][half] = mx;
+          l[t][half] *= f;
+#pragma unroll
+          for (int j = 0; j < 8 * DB; ++j) {
+            out[t][j][half * 2] *= f;
+            out[t][j][half * 2 + 1] *= f;
+          }
+        }
+        const float ref = m[t][half] == -INFINITY ? -kLift : m[t][half] - kLift;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2 * NT; e += 2) {
+          const float y0 = exp2_approx(x[e] - ref), y1 = exp2_approx(x[e + 1] - ref);
+          sum += y0 + y1;
+          p16[t][half][e >> 1] = pack16<T>(y0, y1);
+        }
+        l[t][half] += sum;
+      }
+    }
+    ok = mbar_wait_warp(bars + 8, i & 1, o.status);
+    if (!ok) break;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {
+        uint4 vx[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int row = k * 16 + (z & 1) + (z >> 1) * 8;  // + 2 c
+          vx[z] = *reinterpret_cast<const uint4*>(vs + d * BLOCK + row * 128 + v_chunk[z & 1]);
+          if (edge && p0 + row + 2 * c >= ctx) {  // what is not finite must not meet a weight of 0
+            uint32_t* const w = reinterpret_cast<uint32_t*>(&vx[z]);
+            if (!(there >> (row + 2 * c) & 1u)) vx[z] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t bad = nonfinite16<T>(w[y]);
+              if (bad) {
+                odd_values = true;
+                w[y] &= (bad & 1u ? 0xffff0000u : 0xffffffffu) & (bad & 2u ? 0x0000ffffu : 0xffffffffu);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+          uint32_t v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) v[z] = reinterpret_cast<const uint32_t*>(&vx[z])[e >> 1];
+          const uint32_t b0 = __byte_perm(v[0], v[1], sel), b1 = __byte_perm(v[2], v[3], sel);
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            mma16816<T>(out[t][d * 8 + e], p16[t][0][2 * k], p16[t][1][2 * k], p16[t][0][2 * k + 1],
+                        p16[t][1][2 * k + 1], b0, b1);
+        }
+      }
+    __syncwarp();  // every lane has read the values
+    if (more) issue(1, row_next);
+  }
+  if (!ok) {  // the copies under way have to land before the CTA ends: this slice's, and the next keys
+    mbar_wait_bounded(bars, i & 1, kOwnDrainNs);
+    mbar_wait_bounded(bars + 8, i & 1, kOwnDrainNs);
+    if (i + 1 < slices) mbar_wait_bounded(bars, (i + 1) & 1, kOwnDrainNs);
+  }
+  odd_values = __any_sync(0xffffffffu, odd_values);
+  const size_t part = (size_t)blockIdx.y * a.B * a.S * a.Hq;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float sum = l[t][half];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int row = r0 + t * 16 + half * 8 + g;
+      if (row >= rows) continue;
+      const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
+      float4* const dst4 = reinterpret_cast<float4*>(o.part_o + (part + orow) * D);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {  // a lane's 16 columns of a row lie side by side
+          const int col = half * 2 + (e >> 3), j = d * 8 + (e & 7);
+          float y[4] = {out[t][j][col], out[t][j + 1][col], out[t][j + 2][col], out[t][j + 3][col]};
+          if (odd_values || !(fabsf(y[0]) + fabsf(y[1]) + fabsf(y[2]) + fabsf(y[3]) < INFINITY)) {
+#pragma unroll 1
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t odd =
+                  live(t, half) ? own_odd<T>(a, b, h, ctx, from, to, words[t][half], d * 64 + c * 16 + e + z) : 0u;
+              if (odd) {
+                const float v = odd_value(odd);
+                y[0] = z == 0 ? v : y[0];
+                y[1] = z == 1 ? v : y[1];
+                y[2] = z == 2 ? v : y[2];
+                y[3] = z == 3 ? v : y[3];
+              }
+            }
+          }
+          // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
+          dst4[(d * 64 + c * 16 + e) / 4] =
+              sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[0], y[1], y[2], y[3]);
+        }
+      if (c == 0) o.part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
+    }
+  griddep_wait();
+}
+
+template <typename T, int D, int MT>
+cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
+  auto kernel = prefix_own_kernel<T, D, MT>;
+  constexpr int smem = OwnPlan<D, MT>::kSmem;
+  static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3(a.attn.B * a.attn.Hkv * a.row_groups, a.parts), dim3(32), smem, st, m, a);
+}
+
+template <typename T>
+cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
+  switch (a.attn.D * 8 + a.row_tiles) {
+    case 64 * 8 + 1: return own_launch<T, 64, 1>(m, a, st);
+    case 64 * 8 + 2: return own_launch<T, 64, 2>(m, a, st);
+    case 64 * 8 + 4: return own_launch<T, 64, 4>(m, a, st);
+    case 128 * 8 + 1: return own_launch<T, 128, 1>(m, a, st);
+    case 128 * 8 + 2: return own_launch<T, 128, 2>(m, a, st);
+    case 256 * 8 + 1: return own_launch<T, 256, 1>(m, a, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+bool own_takes(long long positions, int parts) { return positions <= (long long)kOwnMost * parts; }
+
+// A row tile's outputs take dim / 2 registers of a thread.
+int own_row_tiles(int dim, int rows) {
+  const int most = 256 / dim, need = (rows + 15) / 16;
+  return need >= 4 && most >= 4 ? 4 : need >= 2 && most >= 2 ? 2 : 1;
+}
+
+cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st) {
+  OwnMaps m;
+  const AttnArgs& t = a.attn;
+  const uint64_t rows = (uint64_t)t.n_pages * t.Hkv * t.page;
+  const int box = t.page < kSlice ? t.page : kSlice;
+  const bool bf = dtype == SDV_BF16;
+  if (!attn_page_map(t.k, bf, rows, t.D, box, &m.k) || !attn_page_map(t.v, bf, rows, t.D, box, &m.v))
+    return cudaErrorUnknown;
+  return bf ? own_dispatch<__nv_bfloat16>(m, a, st) : own_dispatch<__half>(m, a, st);
+}
+
+}  // namespace sdv

@@ -1,0 +1,36 @@
+// Attention of a batch's rows to each sequence's own positions, behind a shared prefix: the
+// interface of its kernel to the entry point and the join.
+#pragma once
+
+#include "attn_sched.cuh"
+
+namespace sdv {
+
+constexpr int kOwnTile = 64;        // positions that a part is a whole number of
+constexpr int kOwnMaxParts = 16;
+
+// A sequence's own positions in parts of whole tiles, a CTA each.
+struct OwnArgs {
+  AttnArgs attn;      // tile = kOwnTile; out, lse and workspace fields of no meaning
+  int row_tiles;      // m16 row tiles of a CTA
+  int row_groups;     // CTAs for all rows of a kv head
+  int parts;          // of a sequence, at most
+  float* part_o;      // [parts][B * S][Hq][D], relative to the part's maximum
+  float2* part_ml;    // [parts][B * S][Hq]: maximum (log2 domain), sum
+  int* status;
+};
+
+// Tiles of each part of a sequence but the last, and how many parts have any.
+__device__ __forceinline__ int own_per_part(int tiles, int parts) { return (tiles + parts - 1) / parts; }
+__device__ __forceinline__ int own_live_parts(int tiles, int parts) {
+  const int per = own_per_part(tiles, parts);
+  return (tiles + per - 1) / per;
+}
+
+// Whether so many positions of a sequence are few enough for its parts (the shapes are those of the
+// tensor-core kernels, attn_tc_takes).
+bool own_takes(long long positions, int parts);
+int own_row_tiles(int dim, int rows);
+cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st);
+
+}  // namespace sdv

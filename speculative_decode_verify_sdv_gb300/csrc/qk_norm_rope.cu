@@ -49,6 +49,13 @@ struct RopeArgs {
   int* status;
 };
 
+// 1 / sqrt(x), to 2^-22.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 enum RopeForm { kRopeNone, kRopePairs, kRopeHalf, kRopeHalfOdd };
 
 constexpr int kRopeThreads = 128;
@@ -144,7 +151,7 @@ struct RopeLane {
 };
 
 template <typename TI, typename T, int FORM>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int W = kRopeThreads / 32;
   __shared__ alignas(16) float exchange[FORM == kRopeHalfOdd ? kRopeThreads * 8 : 1];
   __shared__ float2 turns[FORM == kRopeNone ? 1 : W][FORM == kRopeNone ? 1 : 128 + 4];  // A cos, A sin of a pair
@@ -226,47 +233,56 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         own[e] = pair2(fo[2 * e], fo[2 * e + 1]);
         far[e] = pair2(ff[2 * e], ff[2 * e + 1]);
       }
-      const TI* const src = (keys ? static_cast<const TI*>(a.k) + t * a.k_stride : static_cast<const TI*>(a.q) + t * a.q_stride) + e0;
-      T* const dst = (keys ? static_cast<T*>(a.ck) + row : static_cast<T*>(a.q_out) + t * q_heads * a.dim) + e0;
-      const long long step = keys ? (long long)a.page * a.dim : a.dim;
-#pragma unroll 1
-      for (int hb = from; hb < to; hb += at_once * kRopeAhead) {
+      const TI* src = (keys ? static_cast<const TI*>(a.k) + t * a.k_stride : static_cast<const TI*>(a.q) + t * a.q_stride) + e0;
+      T* dst = (keys ? static_cast<T*>(a.ck) + row : static_cast<T*>(a.q_out) + t * q_heads * a.dim) + e0;
+      const int in_step = at_once * a.dim;                                           // elements between a lane's heads
+      const long long out_step = (long long)at_once * (keys ? (long long)a.page * a.dim : a.dim);
+      src += (from - first + sub) * a.dim;
+      dst += (from - first + sub) * (keys ? (long long)a.page * a.dim : a.dim);
+      auto work = [&](const Chunk<TI>& raw, bool live) {
+        f32x2 x[4], y[4];
+        raw.pairs(x);
+        float r = 1.f;
+        if (w != nullptr) {
+          const f32x2 s2 = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
+          float sum = unpair2(s2).x + unpair2(s2).y;
+          for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          r = rsqrt_approx(fmaf(sum, inv_dim, a.eps));
+        }
+        const f32x2 r2 = pair2(r, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], own[e]);
+        if constexpr (FORM != kRopeNone) {
+          f32x2 other[4];
+          me.partners(raw, x, other);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = fma2(other[e], far[e], y[e]);
+        }
+        if (live)
+          *reinterpret_cast<uint4*>(dst) = make_uint4(pack16<T>(mul2(y[0], r2)), pack16<T>(mul2(y[1], r2)),
+                                                      pack16<T>(mul2(y[2], r2)), pack16<T>(mul2(y[3], r2)));
+        dst += out_step;
+      };
+      int hb = from;
+      for (; hb + at_once * kRopeAhead <= to; hb += at_once * kRopeAhead) {
         Chunk<TI> raw[kRopeAhead];
 #pragma unroll
         for (int u = 0; u < kRopeAhead; ++u) {
-          const int h = hb + u * at_once + sub;
-          if (mine && h < to) raw[u].load(src + (h - first) * a.dim);
+          if (mine) raw[u].load(src + u * in_step);
           else raw[u].clear();
         }
+        src += kRopeAhead * in_step;
 #pragma unroll
-        for (int u = 0; u < kRopeAhead; ++u) {
-          const int h = hb + u * at_once + sub;
-          if (hb + u * at_once >= to) break;  // of every lane
-          f32x2 x[4];
-          raw[u].pairs(x);
-          float r = 1.f;
-          if (w != nullptr) {
-            const f32x2 s2 = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
-            float sum = unpair2(s2).x + unpair2(s2).y;
-            for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            r = rsqrtf(fmaf(sum, inv_dim, a.eps));
-          }
-          const f32x2 r2 = pair2(r, r);
-          f32x2 y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], own[e]);
-          if constexpr (FORM != kRopeNone) {
-            f32x2 other[4];
-            me.partners(raw[u], x, other);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fma2(other[e], far[e], y[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], r2);
-          if (mine && h < to)
-            *reinterpret_cast<uint4*>(dst + (h - first) * step) =
-                make_uint4(pack16<T>(y[0]), pack16<T>(y[1]), pack16<T>(y[2]), pack16<T>(y[3]));
-        }
+        for (int u = 0; u < kRopeAhead; ++u) work(raw[u], mine);
+      }
+#pragma unroll 1
+      for (; hb < to; hb += at_once) {
+        Chunk<TI> raw;
+        const bool live = mine && hb + sub < to;
+        if (live) raw.load(src);
+        else raw.clear();
+        src += in_step;
+        work(raw, live);
       }
     }
     // values as they are
