@@ -7,7 +7,10 @@
 //
 // Two exclusive sums over the requests, of what is given back and of what is needed, and a
 // copy of page ids.  A round of 48 windows moves some 50 ids and writes 6 KB: latency bounds it,
-// the loads of the lengths, of the list and of the table's entries one after another.
+// the lengths' loads and then those of the list and of the table's entries.  So for up to 512
+// requests one CTA makes both sums in one scan, and takes the new pages' ids for the slots from the
+// list itself, not from the table that it writes.  More requests, or many rows: a cluster shares the
+// copies, and a launch of its own writes positions and slots.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -110,7 +113,7 @@ __device__ __forceinline__ bool place_row(const PageArgs& a, int b, int t, int c
 }
 
 // One cluster: every CTA computes the sums, the warps of all share the copies.
-__global__ void __launch_bounds__(kPageThreads, 1) page_assign_kernel(const PageArgs a, int place) {
+__global__ void __launch_bounds__(kPageThreads, 1) page_assign_kernel(const PageArgs a) {
   __shared__ long long warp_sums[32], s_off[kPageThreads];
   __shared__ int s_from[kPageThreads], s_count[kPageThreads];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -190,13 +193,118 @@ __global__ void __launch_bounds__(kPageThreads, 1) page_assign_kernel(const Page
     }
     if (tid == 0) *a.n_free = (int)min(top - all, (long long)a.n_pages);
   }
-  if (place) {
-    for (int b = me; b < a.B; b += warps) {
-      const int ctx = max(__ldcg(a.ctx + b), 0), rows = __ldcg(a.plan_rows + b);
-      for (int t = lane; t < a.T; t += 32) bad |= !place_row(a, b, t, ctx, rows);
+  if (bad) atomicOr(a.status, kDevErrIndex);
+}
+
+// ---- one CTA ----------------------------------------------------------------------------
+
+constexpr int kSmallThreads = 512, kSmallSeqs = 255;
+constexpr long long kSmallRows = 16384;
+
+struct TwoSums {
+  long long back, need;
+};
+__device__ __forceinline__ TwoSums up_by(TwoSums x, int off) {
+  return TwoSums{__shfl_up_sync(0xffffffffu, x.back, off), __shfl_up_sync(0xffffffffu, x.need, off)};
+}
+
+// The last of n sorted numbers that is not above k, the first of them being 0: whose k-th page it is.
+__device__ __forceinline__ int owner_of(const long long* sums, int n, long long k) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) page_assign_small_kernel(const PageArgs a) {
+  constexpr int W = kSmallThreads / 32;
+  __shared__ TwoSums s_warp[W];
+  __shared__ long long s_back[kSmallThreads], s_need[kSmallThreads], s_taken;
+  __shared__ int s_ctx[kSmallThreads], s_held[kSmallThreads], s_want[kSmallThreads], s_rows[kSmallThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  const int listed = __ldcg(a.n_free), count = min(max(listed, 0), a.n_pages);
+  const PageNeed p = page_need(a, tid);
+  bool bad = listed != count || p.bad;
+  const TwoSums mine{p.back(), p.need()};
+  TwoSums incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const TwoSums o = up_by(incl, off);
+    if (lane >= off) incl = TwoSums{incl.back + o.back, incl.need + o.need};
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  if (tid == 0) s_taken = 0;
+  __syncthreads();
+  TwoSums all{0, 0}, front{0, 0};
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w == warp) front = all;
+    all = TwoSums{all.back + s_warp[w].back, all.need + s_warp[w].need};
+  }
+  const long long back_off = front.back + incl.back - mine.back, need_off = front.need + incl.need - mine.need;
+  const long long top = count + all.back;
+  bad |= top > a.n_pages;
+  const bool served = need_off + mine.need <= top;
+  const int held = served ? p.want : min(p.held, p.want);
+  const int rows = (int)min((long long)p.n, max((long long)held * a.page - p.ctx, 0ll));
+  s_back[tid] = back_off;
+  s_need[tid] = need_off;
+  s_ctx[tid] = p.ctx;
+  s_held[tid] = p.held;
+  s_want[tid] = p.want;
+  s_rows[tid] = rows;
+  if (all.need > top && served) atomicMax(reinterpret_cast<unsigned long long*>(&s_taken), (unsigned long long)(need_off + mine.need));
+  __syncthreads();
+  const long long taken = all.need > top ? s_taken : all.need;
+#pragma unroll 4
+  for (long long k = tid; k < all.back; k += kSmallThreads) {
+    const int b = owner_of(s_back, a.B, k);
+    int32_t* const entry = a.table + (size_t)b * a.max_pages + s_want[b] + (k - s_back[b]);
+    const int id = __ldcg(entry);
+    const long long at = top - 1 - k;
+    bad |= id < 0 || id >= a.n_pages;
+    *entry = -1;
+    if (at < a.n_pages) a.free_pages[at] = id;
+  }
+  if (all.back > 0) __syncthreads();
+  auto listed_id = [&](long long k) {  // the k-th page taken
+    const long long at = top - 1 - k;
+    const int id = at < a.n_pages ? a.free_pages[at] : -1;
+    bad |= id < 0 || id >= a.n_pages;
+    return id;
+  };
+#pragma unroll 4
+  for (long long k = tid; k < taken; k += kSmallThreads) {
+    const int b = owner_of(s_need, a.B, k);
+    a.table[(size_t)b * a.max_pages + s_held[b] + (k - s_need[b])] = listed_id(k);
+  }
+  if (tid < a.B) {
+    a.held[tid] = held;
+    if (a.granted != nullptr) a.granted[tid] = rows;
+  }
+  if (tid == 0) *a.n_free = (int)min(top - taken, (long long)a.n_pages);
+  if (a.positions != nullptr || a.slots != nullptr) {
+    const int total = a.B * a.T;
+#pragma unroll 2
+    for (int e = tid; e < total; e += kSmallThreads) {
+      const int b = e / a.T, t = e - b * a.T;
+      int pos = -1, slot = -1;
+      if (t < s_rows[b]) {
+        pos = s_ctx[b] + t;
+        const int j = pos / a.page;
+        const int id = j < s_held[b] ? a.table[(size_t)b * a.max_pages + j] : listed_id(s_need[b] + j - s_held[b]);
+        if (id >= 0 && id < a.n_pages) slot = id * a.page + pos - j * a.page;
+        else bad = true;
+      }
+      if (a.positions != nullptr) a.positions[e] = pos;
+      if (a.slots != nullptr) a.slots[e] = slot;
     }
   }
-  if (bad && a.status != nullptr) atomicOr(a.status, kDevErrIndex);
+  if (bad) atomicOr(a.status, kDevErrIndex);
 }
 
 constexpr int kPlaceThreads = 256, kPlaceRows = 4;
@@ -265,8 +373,9 @@ sdv_status sdv_page_assign(const sdv_pagepool* pool, int32_t B, int32_t T, const
   a.status = static_cast<int*>(ws);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool maps = positions_or_null != nullptr || slots_or_null != nullptr;
-  const bool place = maps && T <= 256 && (long long)B * T <= 4096;
-  const int cluster = B >= 256 ? 8 : 1;
+  if (B <= sdv::kSmallSeqs && (!maps || (long long)B * T <= sdv::kSmallRows))
+    return sdv::status_of(sdv::launch_pdl(sdv::page_assign_small_kernel, dim3(1), dim3(sdv::kSmallThreads), 0, st, a));
+  const int cluster = 8;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -279,8 +388,8 @@ sdv_status sdv_page_assign(const sdv_pagepool* pool, int32_t B, int32_t T, const
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = sdv::counted(cudaLaunchKernelEx(&cfg, sdv::page_assign_kernel, a, place ? 1 : 0));
-  if (e == cudaSuccess && maps && !place) {
+  cudaError_t e = sdv::counted(cudaLaunchKernelEx(&cfg, sdv::page_assign_kernel, a));
+  if (e == cudaSuccess && maps) {
     const int per = sdv::kPlaceThreads * sdv::kPlaceRows;
     e = sdv::launch_pdl(sdv::page_place_kernel, dim3((unsigned)(((long long)T + per - 1) / per), B),
                         dim3(sdv::kPlaceThreads), 0, st, a);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(128) prefix_simple_kernel(const __grid_constan
           const uint32_t odd = prefix_odd<T>(a, h, w.tile * P, min((w.tile + count) * P, length), d);
           if (odd) o[c][r] = odd_value(odd);
         }
-        a.part_o[((place * (D / 4) + d / 4) * a.row_tile + r) * 4 + d % 4] = o[c][r];
+        a.part_o[(place * a.row_tile + r) * D + d] = o[c][r];
       }
       if (tid == 0)
         *reinterpret_cast<float2*>(a.part_ml + (place * a.row_tile + r) * 2) = make_float2(ps[r], al[r]);
@@ -197,8 +197,6 @@ cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st
 
 // ---- join -------------------------------------------------------------------------------
 
-constexpr int kMergeRows = 32, kMergeCols = 32;
-
 struct JoinArgs {
   PrefixArgs prefix;
   OwnArgs own;           // parts > 0: its partials; else attn.out32 and attn.lse hold outputs
@@ -206,103 +204,128 @@ struct JoinArgs {
   float* lse;            // or null
 };
 
-// 32 rows of a row tile and 32 columns per block, a thread per row and four columns with eight
-// partials in flight.  The prefix's partials lie row beside row, the outputs column beside column:
-// the sums go through shared memory between the two.
-template <typename T>
-__global__ void __launch_bounds__(kMergeRows* kMergeCols / 4) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
-  constexpr int LD = kMergeCols + 4;
-  __shared__ float4 so[kMergeRows * LD / 4];
-  __shared__ float2 sml[kMergeRows];
+// A row's softmax sums over some columns, partial by partial.
+template <int N>
+struct RowSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o[N];
+  template <bool ODD>
+  __device__ __forceinline__ void add(float2 ml, const float4 (&x)[N]) {
+    if (ml.x == -INFINITY && ml.y == 0.f) return;
+    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), f2 = exp2f(ml.x - mn);
+    m = mn;
+    l = l * f + ml.y * f2;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      o[k].x = weighted<ODD>(o[k].x, f) + weighted<ODD>(x[k].x, f2);
+      o[k].y = weighted<ODD>(o[k].y, f) + weighted<ODD>(x[k].y, f2);
+      o[k].z = weighted<ODD>(o[k].z, f) + weighted<ODD>(x[k].z, f2);
+      o[k].w = weighted<ODD>(o[k].w, f) + weighted<ODD>(x[k].w, f2);
+    }
+  }
+};
+
+constexpr int kJoinThreads = 128, kRowThreads = 8;
+
+// Eight threads a row, each with every eighth four columns (N of them) of all its partials, `AHEAD`
+// partials in flight.
+template <typename T, int N, int AHEAD>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
   const PrefixArgs& a = j.prefix;
   const AttnArgs& own = j.own.attn;
-  const int D = a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, r0 = blockIdx.y * kMergeRows;
+  const int D = a.D, j4 = threadIdx.x % kRowThreads;
+  const long long orow = (long long)blockIdx.x * (kJoinThreads / kRowThreads) + threadIdx.x / kRowThreads;
+  // (the split first, before the launches in front have ended: the lengths are inputs)
+  const bool is = orow < (long long)a.tokens * a.Hq;
+  const int token = is ? (int)(orow / a.Hq) : 0, head = is ? (int)(orow - (long long)token * a.Hq) : 0;
+  const int h = head / a.G, row = token * a.G + head - h * a.G, rt = row / a.row_tile, r = row - rt * a.row_tile;
   const int per_head = (a.row_tiles + a.unit_tiles - 1) / a.unit_tiles;
   const int unit = h * per_head + rt / a.unit_tiles, sub = rt % a.unit_tiles;
-  const int nr = min(a.row_tile, a.tokens * a.G - rt * a.row_tile), c0 = blockIdx.z * kMergeCols;
-  // (the split first, before the launches in front have ended: the lengths are inputs)
-  bool bad;
-  const int tiles = prefix_tiles(a, prefix_length(a, bad));
-  const long long total = (long long)tiles * a.units;
-  const int live = attn_live_ctas(a.ctas, total);
-  int parts = 0;
-  if (tiles > 0)
-    parts = attn_owner(total, live, (long long)unit * tiles + tiles - 1) - attn_owner(total, live, (long long)unit * tiles) + 1;
-  // eight threads a row for the outputs
-  const int i = threadIdx.x / (kMergeCols / 4), j4 = threadIdx.x % (kMergeCols / 4), d4 = c0 / 4 + j4, r = r0 + i;
-  const int row = rt * a.row_tile + min(r, nr - 1), token = row / a.G;
   const int b = token / own.S, s = token - b * own.S;
   const AttnSeq seq = attn_seq(own, b);
-  const long long orow = (long long)token * a.Hq + h * a.G + (row - token * a.G);
+  bool bad;
+  const int tiles = prefix_tiles(a, prefix_length(a, bad));
+  const long long total = (long long)tiles * a.units, first = (long long)unit * tiles;
+  const int live = attn_live_ctas(a.ctas, total);
+  const int parts = tiles > 0 ? attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1 : 0;
+  const int own_parts = j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
   griddep_wait();
   griddep_launch_dependents();
-  {
-    const int rr = r0 + lane, dd = c0 / 4 + warp;
-    AttnSum sum;
-    if (rr < nr && dd < D / 4) {
-      const size_t first = (size_t)unit * a.sharers * a.unit_tiles + sub;
-      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * a.row_tile + rr;
-      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * (D / 4) + dd) * a.row_tile + rr;
-      const size_t step = (size_t)a.unit_tiles * a.row_tile;
-      auto gather = [&](auto odd) {
-        sum = AttnSum();
-        for (int k0 = 0; k0 < parts; k0 += 4) {
-          float2 ms[4];
-          float4 x[4];
+  if (!is) return;
+  RowSum<N> sum;
+  auto gather = [&](auto odd, const float2* ml, const float4* po, long long ml_step, long long po_step, int count) {
+    for (int k0 = 0; k0 < count; k0 += AHEAD) {
+      float2 ms[AHEAD];
+      float4 x[AHEAD][N];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k0 + k >= parts) break;
-            ms[k] = __ldcg(ml + (k0 + k) * step);
-            x[k] = __ldcg(po + (k0 + k) * step * (D / 4));
-          }
+      for (int k = 0; k < AHEAD; ++k) {
+        if (k0 + k >= count) break;
+        ms[k] = __ldcg(ml + (k0 + k) * ml_step);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k0 + k >= parts) break;
-            sum.add<decltype(odd)::value>(ms[k].x, ms[k].y, x[k]);
-          }
-        }
-      };
-      gather(std::false_type());
-      if (!sum.finite()) gather(std::true_type());
+        for (int n = 0; n < N; ++n)
+          x[k][n] = j4 + n * kRowThreads < D / 4 ? __ldcg(po + (k0 + k) * po_step + j4 + n * kRowThreads)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (k0 + k >= count) break;
+        sum.template add<decltype(odd)::value>(ms[k], x[k]);
+      }
     }
-    so[lane * (LD / 4) + warp] = sum.o;
-    if (warp == 0) sml[lane] = make_float2(sum.m, sum.l);
-  }
-  __syncthreads();
-  if (r >= nr || d4 >= D / 4) return;
-  AttnSum sum;
-  sum.m = sml[i].x;
-  sum.l = sml[i].y;
-  sum.o = so[i * (LD / 4) + j4];
-  if (j.own.parts > 0) {
-    const int count = own_live_parts(seq.tiles, j.own.parts);
-    const long long step = (long long)a.tokens * a.Hq;
-#pragma unroll 2
-    for (int k = 0; k < count; ++k) {
-      const float2 ml = __ldcg(j.own.part_ml + k * step + orow);
-      sum.add<true>(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(j.own.part_o + (k * step + orow) * D) + d4));
+  };
+  auto all = [&](auto odd) {
+    sum.m = -INFINITY;
+    sum.l = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) sum.o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long at = ((long long)unit * a.sharers * a.unit_tiles + sub) * a.row_tile + r;
+    const long long step = (long long)a.unit_tiles * a.row_tile, step2 = (long long)a.tokens * a.Hq;
+    gather(odd, reinterpret_cast<const float2*>(a.part_ml) + at, reinterpret_cast<const float4*>(a.part_o) + at * (D / 4),
+           step, step * (D / 4), parts);
+    if (j.own.parts > 0) {
+      gather(odd, j.own.part_ml + orow, reinterpret_cast<const float4*>(j.own.part_o) + orow * (D / 4), step2,
+             step2 * (D / 4), own_parts);
+    } else {
+      // the own positions' output is that of a sum of 1 at a maximum of their lse
+      const float lse = __ldcg(own.lse + orow);
+      float4 x[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        x[n] = j4 + n * kRowThreads < D / 4
+                   ? __ldcg(reinterpret_cast<const float4*>(own.out32) + orow * (D / 4) + j4 + n * kRowThreads)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lse != -INFINITY) sum.template add<decltype(odd)::value>(make_float2(lse * 1.4426950408889634f, 1.f), x);
     }
-  } else {
-    // the own positions' output is that of a sum of 1 at a maximum of their lse
-    const float lse = __ldcg(own.lse + orow);
-    if (lse != -INFINITY)
-      sum.add<true>(lse * 1.4426950408889634f, 1.f, __ldcg(reinterpret_cast<const float4*>(own.out32 + orow * D) + d4));
-  }
+  };
+  all(std::false_type());
+  bool finite = true;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    finite &= fabsf(sum.o[n].x) + fabsf(sum.o[n].y) + fabsf(sum.o[n].z) + fabsf(sum.o[n].w) < INFINITY;
+  if (!finite) all(std::true_type());
   const bool none = s >= seq.n || sum.l == 0.f;
   const float inv = 1.f / sum.l;
-  const uint2 y = none ? make_uint2(0u, 0u)
-                       : make_uint2(pack16<T>(sum.o.x * inv, sum.o.y * inv), pack16<T>(sum.o.z * inv, sum.o.w * inv));
-  reinterpret_cast<uint2*>(static_cast<T*>(j.out) + orow * D)[d4] = y;
-  if (d4 == 0 && j.lse != nullptr) j.lse[orow] = none ? -INFINITY : sum.lse();
+  uint2* const dst = reinterpret_cast<uint2*>(static_cast<T*>(j.out) + orow * D);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (j4 + n * kRowThreads < D / 4)
+      dst[j4 + n * kRowThreads] =
+          none ? make_uint2(0u, 0u)
+               : make_uint2(pack16<T>(sum.o[n].x * inv, sum.o[n].y * inv), pack16<T>(sum.o[n].z * inv, sum.o[n].w * inv));
+  if (j4 == 0 && j.lse != nullptr)
+    j.lse[orow] = none ? -INFINITY : (sum.m + log2f(sum.l)) * 0.6931471805599453f;
+}
+
+template <typename T>
+void (*join_kernel(int D))(JoinArgs) {
+  return D <= 64 ? prefix_join_kernel<T, 2, 4> : D <= 128 ? prefix_join_kernel<T, 4, 4> : prefix_join_kernel<T, 8, 2>;
 }
 
 cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, cudaStream_t st) {
   const PrefixArgs& a = j.prefix;
-  auto kernel = dtype == SDV_F16 ? prefix_join_kernel<__half> : prefix_join_kernel<__nv_bfloat16>;
-  return launch_pdl(kernel, dim3(a.Hkv * a.row_tiles, (a.row_tile + kMergeRows - 1) / kMergeRows,
-                                 (a.D + kMergeCols - 1) / kMergeCols),
-                    dim3(kMergeRows * kMergeCols / 4), 0, st, j);
+  const long long rows = (long long)a.tokens * a.Hq, per = kJoinThreads / kRowThreads;
+  return launch_pdl(dtype == SDV_F16 ? join_kernel<__half>(a.D) : join_kernel<__nv_bfloat16>(a.D),
+                    dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, st, j);
 }
 
 constexpr int kSimplePerSm = 2;

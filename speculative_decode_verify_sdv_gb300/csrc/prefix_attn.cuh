@@ -32,7 +32,7 @@ struct PrefixArgs {
   int tile;                   // positions per tile
   int sharers;                // places for partials of a unit
   int ctas;
-  float* part_o;              // [units][sharers][unit_tiles][D / 4][row_tile][4]
+  float* part_o;              // [units][sharers][unit_tiles][row_tile][D]
   float* part_ml;             // [units][sharers][unit_tiles][row_tile][2]: maximum (log2 domain), sum
   int* status;
   DebugFault fault;

@@ -55,7 +55,7 @@ struct PrefixPlan {
   static constexpr int kBlocks = kWide / 64;
   static constexpr int kSlot = TK * kWide * 2;
   static constexpr int kQ = 128 * D * 2;              // one row tile's queries
-  static constexpr int kNumBars = 2 * kPrefixMaxSlots + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;
+  static constexpr int kNumBars = 2 * kPrefixMaxSlots + 2 + 4 + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int kSmall = kNumBars * 8 + 32;
   static constexpr int kFit = (kPrefixSmem - 1024 - kSmall - STREAMS * kQ) / kSlot;
   static constexpr int NS = kFit < kPrefixMaxSlots ? kFit : kPrefixMaxSlots;
@@ -65,6 +65,30 @@ struct PrefixPlan {
   static_assert(kO + STREAMS * D <= 512, "tensor memory");
   static_assert(NS >= 2 * kHalves + 1 && kSmem * 2 > kPrefixSmem, "a tile ahead; one CTA per SM");
 };
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Lane q of four has y[0 .. 3] of its row; afterwards y[q] of rows 0 .. 3.
+__device__ __forceinline__ void quad_transpose(float (&y)[4][4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const float give = up ? y[i][z] : y[i | bit][z], got = __shfl_xor_sync(0xffffffffu, give, bit);
+        if (up) y[i][z] = got;
+        else y[i | bit][z] = got;
+      }
+    }
+  }
+}
 
 template <typename T, int D>
 __device__ __noinline__ uint32_t prefix_odd_columns(const PrefixArgs& a, int h, int from, int to) {
@@ -108,10 +132,10 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
   auto empty = [&](int s) { return bars + 8u * (kPrefixMaxSlots + s); };
   constexpr int kB = 2 * kPrefixMaxSlots;
   auto s_full = [&](int i) { return bars + 8u * (kB + i); };       // a set of scores is there
-  auto p_ready = [&](int i) { return bars + 8u * (kB + 2 + i); };  // its weights are
-  auto pv_done = [&](int q) { return bars + 8u * (kB + 4 + q); };  // a row tile's P V has ended
-  auto o_free = [&](int q) { return bars + 8u * (kB + 6 + q); };   // its outputs have been read
-  const uint32_t q_full = bars + 8u * (kB + 8), q_free = q_full + 8, drain = q_full + 16;
+  auto p_ready = [&](int i, int half) { return bars + 8u * (kB + 2 + 2 * i + half); };  // the weights of its 64 positions are
+  auto pv_done = [&](int q) { return bars + 8u * (kB + 6 + q); };  // a row tile's P V has ended
+  auto o_free = [&](int q) { return bars + 8u * (kB + 8 + q); };   // its outputs have been read
+  const uint32_t q_full = bars + 8u * (kB + 10), q_free = q_full + 8, drain = q_full + 16;
   const int nq = (a.row_tile + 31) / 32;  // softmax warps of a row tile with rows
 
   if (warp == 1) {
@@ -126,7 +150,8 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(p_ready(i), nq);
+      mbar_init(p_ready(i, 0), nq);
+      mbar_init(p_ready(i, 1), nq);
       mbar_init(pv_done(i), 1);
       mbar_init(o_free(i), nq);
     }
@@ -282,17 +307,22 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
       }
       tc_commit_elect(s_full(set));
     };
-    auto pv = [&](int q, int set, int place, bool add) {
+    // O += P V in two steps of 64 positions, each as soon as its weights are there
+    auto pv = [&](int q, int set, int place, bool add, uint32_t parity) {
 #pragma unroll
-      for (int half = 0; half < KH; ++half) {
-        const uint64_t vd = smem_desc_sw128(ring + (place + half) % NS * PL::kSlot, TK * 128, 1024);
+      for (int j = 0; j < TK / 64; ++j) {
+        if (!await(p_ready(set, j), parity)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < TK / 64; ++j)
+        for (int half = 0; half < KH; ++half) {
+          const uint64_t vd = smem_desc_sw128(ring + (place + half) % NS * PL::kSlot, TK * 128, 1024);
           tc_mma4_ts(tm + PL::kO + q * D + half * 128, tm + set * TK + j * 32, vd + j * (4 * 2048 >> 4), id_pv,
                      add || j > 0);
+        }
       }
       tc_commit_elect(pv_done(q));
       ++sent[q];
+      return true;
     };
     auto release = [&](int place) {
 #pragma unroll
@@ -322,9 +352,7 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
           if (!wait_tile(v)) break;
           for (int q = 0; q < streams; ++q) {
             if (t == 0 && begun[q] > 0 && !await(o_free(q), (begun[q] - 1) & 1)) break;
-            if (!await(p_ready(q), sent[q] & 1)) break;
-            tc_fence_after();
-            pv(q, q, v, t > 0);
+            if (!pv(q, q, v, t > 0, sent[q] & 1)) break;
             if (q == streams - 1) release(v);
             if (t + 1 < count) {
               if (q == 0 && !wait_tile(k)) break;
@@ -356,9 +384,7 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
           const int v = first + place_v(t, count);
           if (!wait_tile(v)) break;
           if (t == 0 && begun[0] > 0 && !await(o_free(0), (begun[0] - 1) & 1)) break;
-          if (!await(p_ready(i & 1), (i >> 1) & 1) || !pv_wait(0, i)) break;
-          tc_fence_after();
-          pv(0, i & 1, v, t > 0);
+          if (!pv_wait(0, i) || !pv(0, i & 1, v, t > 0, (i >> 1) & 1)) break;
           release(v);
         }
       }
@@ -406,36 +432,41 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
 #pragma unroll
         for (int j = 0; j < TK; j += 32) tmem_ld32(ts + j, sr + j);
         tmem_wait_ld();
+        uint32_t absent = 0;  // pages of the tile that cannot be followed, a bit each
+        if (some_absent) {
+          const int p = p0 + lane * box;
+          bool gone = false;
+          if (lane * box < TK && p < length) {
+            const int id = __ldg(a.table + (p >> page_log));
+            gone = id < 0 || id >= a.n_pages;
+          }
+          absent = __ballot_sync(0xffffffffu, gone);
+        }
+        auto mask32 = [&](uint32_t* x, int j) {  // of 32 columns from j on
+          const int n = min(max(length - p0 - j, 0), 32);
+          uint32_t bits = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+          if (absent != 0) {
+            for (int e = 0; e < 32; e += 8)
+              if (absent >> ((j + e) / box) & 1) bits &= ~(0xffu << e);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits >> e & 1)) x[e] = 0xff800000u;
+        };
         if (edge) {
-          uint32_t absent = 0;  // pages of the tile that cannot be followed, a bit each
-          if (some_absent) {
-            const int p = p0 + lane * box;
-            bool gone = false;
-            if (lane * box < TK && p < length) {
-              const int id = __ldg(a.table + (p >> page_log));
-              gone = id < 0 || id >= a.n_pages;
-            }
-            absent = __ballot_sync(0xffffffffu, gone);
-          }
 #pragma unroll
-          for (int j = 0; j < TK; j += 32) {
-            const int n = min(max(length - p0 - j, 0), 32);
-            uint32_t bits = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-            if (absent != 0) {
-              for (int e = 0; e < 32; e += 8)
-                if (absent >> ((j + e) / box) & 1) bits &= ~(0xffu << e);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(bits >> e & 1)) sr[j + e] = 0xff800000u;
-          }
+          for (int j = 0; j < TK; j += 32) mask32(sr + j, j);
         }
         float mx[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(sr[j]);
 #pragma unroll
-        for (int j = 4; j < TK; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        for (int j = 4; j < TK - 4; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(sr[j + e]), __uint_as_float(sr[j + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sr[TK - 4 + e]));
+        const float mt = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
         const bool grow = mt > m + 8.f;  // also from -inf to any number
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow && m != -INFINITY ? exp2_approx(m - mt) : 1.f;
@@ -458,20 +489,6 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
         const float ref = m == -INFINITY ? -kLift : m - kLift;
         const f32x2 c2 = pair2(c, c), ref2 = pair2(-ref, -ref);
         f32x2 l2[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
-#pragma unroll
-        for (int j = 0; j < TK; j += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = unpair2(fma2(pair2(__uint_as_float(sr[j + e]), __uint_as_float(sr[j + e + 1])), c2, ref2));
-            const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
-            l2[e / 2 & 1] = add2(l2[e / 2 & 1], pair2(e0, e1));
-            p[e / 2] = pack16<T>(e0, e1);
-          }
-          tmem_st16(ts + j / 2, p);
-        }
-        const float2 la = unpair2(l2[0]), lb = unpair2(l2[1]);
-        l += (la.x + la.y) + (lb.x + lb.y);
         if (p0 + TK > length && q == 0) {
           // what the last page holds behind the end must not meet its zero weights
           const int from = length - p0, to = min(TK, (int)(((uint32_t)length + a.page - 1) / a.page * a.page - p0));
@@ -486,11 +503,39 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
             fence_proxy_async_smem();
           }
         }
-        if (!pv_wait(i)) break;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready(set));
+        if (!ok) break;
+        // The weights, in two halves: the products with the first run under the second, whose scores
+        // are read again rather than kept in registers.  (2^x of a part of them by a polynomial, beside
+        // the special function unit, made every tile longer: 245 to 260 us for 20,480 tiles of two row
+        // tiles, and so did two threads a row, 281; 239 as it is.)
+        uint32_t again[2][32];
+#pragma unroll
+        for (int j = 0; ok && j < TK / 32; ++j) {
+          uint32_t* const x = j < 2 ? sr + 32 * j : again[j & 1];
+          if (j >= 2) {
+            tmem_wait_ld();
+            if (edge) mask32(x, 32 * j);
+          }
+          if (j == 1 || j == 2) tmem_ld32(ts + 32 * (j + 1), again[(j + 1) & 1]);
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 z = unpair2(fma2(pair2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, ref2));
+            const f32x2 y = pair2(exp2_approx(z.x), exp2_approx(z.y));
+            l2[e & 1] = add2(l2[e & 1], y);
+            p[e] = pack16<T>(y);
+          }
+          tmem_st16(ts + j * 16, p);
+          if (j == 0 || j == 2) continue;
+          if (j == 3 && !pv_wait(i)) break;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready(set, j / 2));
+        }
+        if (!ok) break;
+        const float2 la = unpair2(l2[0]), lb = unpair2(l2[1]);
+        l += (la.x + la.y) + (lb.x + lb.y);
       }
       if (!ok) break;
       if (!pv_wait(i)) break;
@@ -519,12 +564,17 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
             if (kind && l > 0.f) o[e] = __float_as_uint(odd_value(kind));
           }
         }
-        if (live) {
-          float4* const dst = reinterpret_cast<float4*>(a.part_o) + (at * (D / 4) + j / 4) * a.row_tile + r;
+        // four lanes pass 16-byte pieces round so that they write 64 bytes of one row side by side
+        float* const dst = a.part_o + (at * a.row_tile + (r & ~3)) * D + j + (lane & 3) * 4;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            dst[(e / 4) * a.row_tile] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                    __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        for (int e = 0; e < 32; e += 16) {
+          float y[4][4];
+#pragma unroll
+          for (int z = 0; z < 16; ++z) y[z >> 2][z & 3] = __uint_as_float(o[e + z]);
+          quad_transpose(y, lane);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if ((r & ~3) + z < nr) *reinterpret_cast<float4*>(dst + z * D + e) = make_float4(y[z][0], y[z][1], y[z][2], y[z][3]);
         }
       }
       tc_fence_before();

@@ -346,15 +346,15 @@ def _addr(t, dtype, name, shape=None):
     """Device address of a contiguous CUDA tensor (None for None)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _rows(t, dtype, name, B, T, heads, dim):
@@ -528,10 +528,11 @@ class Rope:
 
     def __init__(self, layout: int, rot_dim: int, amplitude: float, steps: torch.Tensor):
         self.layout, self.rot_dim, self.amplitude, self.steps = layout, rot_dim, amplitude, steps
+        self._struct = sdv_rope(layout, rot_dim, amplitude, None)
 
     def c(self) -> sdv_rope:
-        return sdv_rope(self.layout, self.rot_dim, self.amplitude,
-                        _addr(self.steps, torch.int64, "steps", (self.rot_dim // 2,)))
+        self._struct.steps = _addr(self.steps, torch.int64, "steps", (self.rot_dim // 2,))
+        return self._struct
 
 
 def sdv_qk_norm_rope(q, k, v, k_pages: torch.Tensor, v_pages: torch.Tensor, q_weight, k_weight, eps: float, rope,
