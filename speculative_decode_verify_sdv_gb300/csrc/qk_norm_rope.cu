@@ -150,13 +150,19 @@ struct RopeLane {
   }
 };
 
-template <typename TI, typename T, int FORM>
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// LANES: of a head (0: any number, read from the arguments).
+template <typename TI, typename T, int FORM, int LANES>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int W = kRopeThreads / 32;
   __shared__ alignas(16) float exchange[FORM == kRopeHalfOdd ? kRopeThreads * 8 : 1];
-  __shared__ float2 turns[FORM == kRopeNone ? 1 : W][FORM == kRopeNone ? 1 : 128 + 4];  // A cos, A sin of a pair
+  __shared__ alignas(16) float2 turns[FORM == kRopeNone ? 1 : W][FORM == kRopeNone ? 1 : 128 + 4];  // A cos, A sin of a pair
   const int lane = threadIdx.x & 31;
-  const int L = a.lanes, sub = lane / L, at_once = 32 / L;
+  const int L = LANES != 0 ? LANES : a.lanes, sub = lane / L, at_once = 32 / L;
   RopeLane<TI, T, FORM> me;
   me.lane = lane;
   me.c = lane & (L - 1);
@@ -190,6 +196,16 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
     }
     const int id = slot < 0 ? 0 : slot / a.page;
     const long long row = ((long long)id * kv * a.page + (slot - id * a.page)) * a.dim;  // head 0 of the slot
+    // the first query heads' loads go out before the angles are computed
+    Chunk<TI> raw[kRopeAhead];
+    const bool early = h0 < q_heads && h0 + at_once * kRopeAhead <= min(h1, q_heads);
+    if (early) {
+#pragma unroll
+      for (int u = 0; u < kRopeAhead; ++u) {
+        if (mine) raw[u].load(static_cast<const TI*>(a.q) + t * a.q_stride + (h0 + u * at_once + sub) * a.dim + e0);
+        else raw[u].clear();
+      }
+    }
     if constexpr (FORM != kRopeNone) {
       if (h0 < q_heads + kv) {
         __syncwarp();  // the last token's have been read
@@ -208,23 +224,47 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
       const int from = max(h0, first), to = min(h1, end);
       if (from >= to || (keys && slot < 0)) continue;
       const float* const w = keys ? a.k_weight : a.q_weight;
-      // the factors of this lane's elements and of their partners
-      float fo[8], ff[8];
+      // the factors of this lane's elements and of their partners: y = x cos + partner sin, where the
+      // first of a pair takes - sin and the second + sin
+      float fo[8], ff[8], wo[8], wf[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int el = e0 + e;
-        const bool in = FORM != kRopeNone && el < a.rot;
-        const int i = FORM == kRopePairs ? el >> 1 : el < me.half ? el : el - me.half;
-        const int partner = FORM == kRopePairs ? el ^ 1 : el < me.half ? el + me.half : el - me.half;
-        float2 cs = make_float2(1.f, 0.f);
-        if (in) cs = angle[i];
-        // y = x cos + partner sin: the first of a pair takes - sin, the second + sin
-        const bool second = FORM == kRopePairs ? e & 1 : el >= me.half;
-        fo[e] = cs.x;
-        ff[e] = second ? cs.y : -cs.y;
-        if (w != nullptr && mine) {
-          fo[e] *= __ldg(w + el);
-          if (in) ff[e] *= __ldg(w + partner);
+      for (int e = 0; e < 8; ++e) wo[e] = wf[e] = 1.f;
+      if (w != nullptr && mine) {
+        load8(w + e0, wo);
+        if (FORM == kRopeHalf && me.turned) load8(w + (e0 < me.half ? e0 + me.half : e0 - me.half), wf);
+      }
+      if constexpr (FORM == kRopeHalf) {
+        float cs[16];
+        const float2* const at = angle + (me.turned ? (e0 < me.half ? e0 : e0 - me.half) : 0);
+        load8(reinterpret_cast<const float*>(at), cs);
+        load8(reinterpret_cast<const float*>(at) + 8, cs + 8);
+        const float sign = e0 < me.half ? -1.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          fo[e] = me.turned ? cs[2 * e] * wo[e] : wo[e];
+          ff[e] = me.turned ? sign * cs[2 * e + 1] * wf[e] : 0.f;
+        }
+      } else if constexpr (FORM == kRopePairs) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const bool in = e0 + e < a.rot;
+          const float2 cs = in ? angle[(e0 + e) / 2] : make_float2(1.f, 0.f);
+          fo[e] = cs.x * wo[e];
+          fo[e + 1] = cs.x * wo[e + 1];
+          ff[e] = -cs.y * wo[e + 1];
+          ff[e + 1] = cs.y * wo[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int el = e0 + e;
+          fo[e] = wo[e];
+          ff[e] = 0.f;
+          if (FORM == kRopeNone || el >= a.rot) continue;
+          const bool second = el >= me.half;
+          const float2 cs = angle[second ? el - me.half : el];
+          fo[e] *= cs.x;
+          ff[e] = (second ? cs.y : -cs.y) * (w != nullptr && mine ? __ldg(w + (second ? el - me.half : el + me.half)) : 1.f);
         }
       }
       f32x2 own[4], far[4];
@@ -246,7 +286,9 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
         if (w != nullptr) {
           const f32x2 s2 = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
           float sum = unpair2(s2).x + unpair2(s2).y;
-          for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            if (off < L) sum += __shfl_xor_sync(0xffffffffu, sum, off);
           r = rsqrt_approx(fmaf(sum, inv_dim, a.eps));
         }
         const f32x2 r2 = pair2(r, r);
@@ -265,11 +307,12 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
       };
       int hb = from;
       for (; hb + at_once * kRopeAhead <= to; hb += at_once * kRopeAhead) {
-        Chunk<TI> raw[kRopeAhead];
+        if (keys || hb > from) {
 #pragma unroll
-        for (int u = 0; u < kRopeAhead; ++u) {
-          if (mine) raw[u].load(src + u * in_step);
-          else raw[u].clear();
+          for (int u = 0; u < kRopeAhead; ++u) {
+            if (mine) raw[u].load(src + u * in_step);
+            else raw[u].clear();
+          }
         }
         src += kRopeAhead * in_step;
 #pragma unroll
@@ -277,12 +320,12 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
       }
 #pragma unroll 1
       for (; hb < to; hb += at_once) {
-        Chunk<TI> raw;
+        Chunk<TI> one;
         const bool live = mine && hb + sub < to;
-        if (live) raw.load(src);
-        else raw.clear();
+        if (live) one.load(src);
+        else one.clear();
         src += in_step;
-        work(raw, live);
+        work(one, live);
       }
     }
     // values as they are
@@ -299,13 +342,20 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 5 : 4) qk_norm
   }
 }
 
+template <typename TI, typename T, int FORM>
+cudaError_t rope_form(const RopeArgs& a, int blocks, cudaStream_t st) {
+  auto kernel = a.lanes == 16 ? qk_norm_rope_kernel<TI, T, FORM, 16> : qk_norm_rope_kernel<TI, T, FORM, 0>;
+  return launch_pdl(kernel, dim3(blocks), dim3(kRopeThreads), 0, st, a);
+}
+
 template <typename TI, typename T>
 cudaError_t rope_launch(int form, const RopeArgs& a, int blocks, cudaStream_t st) {
-  auto kernel = form == kRopeNone    ? qk_norm_rope_kernel<TI, T, kRopeNone>
-                : form == kRopePairs ? qk_norm_rope_kernel<TI, T, kRopePairs>
-                : form == kRopeHalf  ? qk_norm_rope_kernel<TI, T, kRopeHalf>
-                                     : qk_norm_rope_kernel<TI, T, kRopeHalfOdd>;
-  return launch_pdl(kernel, dim3(blocks), dim3(kRopeThreads), 0, st, a);
+  switch (form) {
+    case kRopeNone: return rope_form<TI, T, kRopeNone>(a, blocks, st);
+    case kRopePairs: return rope_form<TI, T, kRopePairs>(a, blocks, st);
+    case kRopeHalf: return rope_form<TI, T, kRopeHalf>(a, blocks, st);
+    default: return rope_form<TI, T, kRopeHalfOdd>(a, blocks, st);
+  }
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -433,7 +483,8 @@ sdv_status sdv_qk_norm_rope(const sdv_kvcache* cache, int32_t in_dtype, const vo
   a.per_part = (a.per_part + least - 1) / least * least;
   a.parts = (heads + a.per_part - 1) / a.per_part;
   const long long per_block = sdv::kRopeThreads / 32, want = (a.tokens * a.parts + per_block - 1) / per_block;
-  const int blocks = (int)(want < 12ll * sms ? want : 12ll * sms);
+  const long long room_blocks = (in_dtype == SDV_F32 ? 4ll : 5ll) * sms;
+  const int blocks = (int)(want < room_blocks ? want : room_blocks);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SDV_BF16;
   cudaError_t e;

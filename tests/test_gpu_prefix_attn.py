@@ -245,3 +245,62 @@ def test_the_binding_refuses_layouts_and_shapes(sdv):
     with pytest.raises(sdv.SdvError) as e:
         sdv.sdv_prefix_attn(**{**ok, "ws": ws[:ws.numel() // 2]})
     assert e.value.status == sdv.SDV_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("case", [2, 4, 5, 6, 8])
+def test_tables_for_long_sequences(sdv, case):
+    """A table row that could hold more positions than one warp should walk sends the own positions through
+    the paged attention, which deals any lengths evenly: the same result to the tolerances."""
+    dt, B, S, hq, hkv, d, page, prefix, ctx, n, masked = SHAPES[case]
+    q, kp, vp, ptable, table = make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, 300 + case)
+    wide = torch.full((B, 40000 // page), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    mask = words(np.random.default_rng(case), B, S) if masked else None
+    im = None if mask is None else as_i32(mask)
+    out, lse, ws = call(sdv, q, kp, vp, ptable, prefix, wide, ctx, n, im, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    check(dt, reference(q, kp, vp, ptable, prefix, table, ctx, n, mask, d ** -0.5), out, lse, d)
+
+
+@pytest.mark.parametrize("d,page", [(64, 8), (128, 16), (128, 32), (256, 128)])
+def test_own_lengths_around_a_slice(sdv, d, page):
+    """Own positions of every length around the slices, parts and pages of their kernel."""
+    ctx = [0, 1, 7, 30, 31, 32, 33, 62, 63, 64, 65, 95, 127, 128, 190, 511]
+    n = [1 + i % 3 for i in range(len(ctx))]
+    q, kp, vp, ptable, table = make(BF16, len(ctx), 3, 8, 2, d, page, 40, ctx, n, d + page)
+    out, lse, ws = call(sdv, q, kp, vp, ptable, 40, table, ctx, n, None, 0.1)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    check(BF16, reference(q, kp, vp, ptable, 40, table, ctx, n, None, 0.1), out, lse, d)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_own_positions_that_are_not_finite_or_absent(sdv, d):
+    """A window row's infinities and NaN reach the rows that see it and no others, the context's reach all
+    rows of their sequence; a page of a sequence's own that is none is absent, and reported."""
+    ctx, n = [20, 40, 0], [3, 3, 2]
+    q, kp, vp, ptable, table = make(F16, 3, 3, 8, 2, d, 16, 100, ctx, n, 30)
+    at = lambda b, p: (int(table[b, p // 16]), p % 16)  # noqa: E731
+    page, slot = at(0, 21)  # window row 1 of sequence 0
+    vp[page, 0, slot, 3], vp[page, 0, slot, 9] = float("inf"), float("nan")
+    page, slot = at(1, 5)   # a context position of sequence 1
+    vp[page, 1, slot, 4] = float("-inf")
+    out, _, ws = call(sdv, q, kp, vp, ptable, 100, table, ctx, n, None, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    out = out.float().cpu()
+    odd = ~torch.isfinite(out)
+    want = torch.zeros_like(odd)
+    want[0, 1:, :4, 3] = want[0, 1:, :4, 9] = True
+    want[1, :, 4:, 4] = True
+    assert torch.equal(odd, want)
+    assert torch.isposinf(out[0, 1:, :4, 3]).all() and torch.isneginf(out[1, :, 4:, 4]).all()
+    bad = table.clone()
+    bad[1, 1] = kp.shape[0] + 5
+    vp = torch.where(torch.isinf(vp), torch.zeros_like(vp), vp)
+    vp[at(0, 21)[0], 0, at(0, 21)[1], 9] = 0.0
+    out, lse, ws = call(sdv, q, kp, vp, ptable, 100, bad, ctx, n, None, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+    # positions 16 .. 31 of sequence 1 are gone: pages 0 and 2 as its first two
+    short = table.clone()
+    short[1, 1] = table[1, 2]
+    ref = reference(q, kp, vp, ptable, 100, short, [20, 24, 0], n, None, d ** -0.5)
+    check(F16, ref, out, lse, d)
