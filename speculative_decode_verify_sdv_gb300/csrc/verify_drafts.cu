@@ -26,7 +26,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "host_util.h"
 #include "mixing.h"
@@ -75,6 +74,12 @@ __device__ const float kPowLo[32] = {  // 2^(k/32) - kPowHi[k]
 
 // A logit as it counts: NaN as one that is never drawn, +inf as the largest number.
 __device__ __forceinline__ float counted_logit(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 template <typename T>
 __device__ __forceinline__ float logit(const T* p) {
@@ -140,7 +145,7 @@ struct Row {
       float x[kPer];
       step(n, s, lane, raw[s], x);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) m = fmaxf(m, x[e]);  // (of a number and NaN the number)
+      for (int e = 0; e < kPer; e += 2) m = max3(m, x[e], x[e + 1]);  // (of a number and NaN the number)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -261,12 +266,13 @@ struct Weigher {
     }
     return __uint_as_float((uint32_t)(127 + (int)(ceilf(mk * c_hi) - K)) << 23);
   }
-  // EXACT: a weight that does not count is 0; else that of the least x that does, some 2^-124, which
-  // a sum does not notice (EXACT it is where no number is that far below).
-  template <bool EXACT = true>
-  __device__ __forceinline__ Pair weights(float x0, float x1) const {
-    // (NaN and -inf become the least)
-    const f32x2 x = pair2(fminf(fmaxf(x0, least), M), fminf(fmaxf(x1, least), M));
+  // What 2^(x c - K) of two finite x is made of: (th + tlo) (1 + s) times a power of two.
+  struct Made {
+    f32x2 th, tlo, s;
+    float scale0, scale1;
+  };
+  __device__ __forceinline__ Made made(float x0, float x1) const {
+    const f32x2 x = pair2(x0, x1);
     f32x2 t = mul2(x, both(-c_hi));  // - x c
     f32x2 tl = fma2(x, both(c_lo), fma2(x, both(c_hi), t));
     if (off) {
@@ -279,23 +285,37 @@ struct Weigher {
     const f32x2 r = fma2(sub2(kk, magic), both(0.03125f), t);
     const float2 kf = unpair2(kk);
     const uint32_t k0 = __float_as_uint(kf.x), k1 = __float_as_uint(kf.y);
-    const f32x2 th = pair2(__shfl_sync(0xffffffffu, pow_hi, k0), __shfl_sync(0xffffffffu, pow_hi, k1));
-    const f32x2 tlo = pair2(__shfl_sync(0xffffffffu, pow_lo, k0), __shfl_sync(0xffffffffu, pow_lo, k1));
+    Made w;
+    w.th = pair2(__shfl_sync(0xffffffffu, pow_hi, k0), __shfl_sync(0xffffffffu, pow_hi, k1));
+    w.tlo = pair2(__shfl_sync(0xffffffffu, pow_lo, k0), __shfl_sync(0xffffffffu, pow_lo, k1));
     // 2^-r = 1 + s, |s| < 0.011
     f32x2 p = fma2(r, both(0.009618129f), both(-0.05550411f));
     p = fma2(r, p, both(0.24022651f));
     p = fma2(r, p, both(-0x1.62e430p-1f));
-    f32x2 s = fma2(tl, both(0x1.62e430p-1f), mul2(r, both(0x1.05c610p-29f)));
-    s = fma2(r, p, s);
-    float s0 = __uint_as_float(((k0 & ~31u) << 18) + bias), s1 = __uint_as_float(((k1 & ~31u) << 18) + bias);
-    if (EXACT) {
-      s0 = x0 >= least ? s0 : 0.f;
-      s1 = x1 >= least ? s1 : 0.f;
-    }
-    const f32x2 scale = pair2(s0, s1);
-    return Pair{mul2(th, scale), mul2(fma2(th, s, tlo), scale)};
+    w.s = fma2(r, p, fma2(tl, both(0x1.62e430p-1f), mul2(r, both(0x1.05c610p-29f))));
+    w.scale0 = __uint_as_float(((k0 & ~31u) << 18) + bias);
+    w.scale1 = __uint_as_float(((k1 & ~31u) << 18) + bias);
+    return w;
   }
-  __device__ __forceinline__ Pair operator()(float x0, float x1) const { return weights(x0, x1); }
+  // Two weights; 0 for an x that does not count.
+  __device__ __forceinline__ Pair operator()(float x0, float x1) const {
+    // (NaN and -inf become the least)
+    const Made w = made(fminf(fmaxf(x0, least), M), fminf(fmaxf(x1, least), M));
+    const f32x2 scale = pair2(x0 >= least ? w.scale0 : 0.f, x1 >= least ? w.scale1 : 0.f);
+    return Pair{mul2(w.th, scale), mul2(fma2(w.th, w.s, w.tlo), scale)};
+  }
+  // Whether `add` may be used: an x that does not count then adds some 2^-124, which a sum whose
+  // largest weight is 1/2 or more does not notice.
+  __device__ __forceinline__ bool plain() const { return least > -FLT_MAX && !far && M < FLT_MAX; }
+  // Two weights of up to 1 to a sum of up to 64 of them: to sum.hi (its negative) what of them is a
+  // multiple of 2^-17, exactly, and to sum.lo the rest.
+  __device__ __forceinline__ void add(Pair& sum, float x0, float x1) const {
+    const Made w = made(fmaxf(x0, least), fmaxf(x1, least));
+    const f32x2 scale = pair2(w.scale0, w.scale1), grid = both(96.f);  // 1.5 2^6: the last place is 2^-17
+    const f32x2 down = sub2(grid, fma2(w.th, scale, grid));
+    sum.hi = add2(sum.hi, down);
+    sum.lo = add2(sum.lo, fma2(fma2(w.th, w.s, w.tlo), scale, fma2(w.th, scale, down)));
+  }
 };
 
 __device__ __forceinline__ void add_pair(Pair& sum, const Pair& w) {
@@ -332,18 +352,25 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const DraftA
   } else if (m != -INFINITY) {
     const Weigher weigh(m, c, lane);
     Pair sum{0, 0};
-    auto add = [&](auto exact) {
+    if (weigh.plain()) {
 #pragma unroll
       for (int s = 0; s < R::kSteps; ++s) {
         float x[R::kPer];
         r.step(chunk, s, lane, raw[s], x);
 #pragma unroll
-        for (int e = 0; e < R::kPer; e += 2)
-          add_pair(sum, weigh.template weights<decltype(exact)::value>(x[e], x[e + 1]));
+        for (int e = 0; e < R::kPer; e += 2) weigh.add(sum, x[e], x[e + 1]);
       }
-    };
-    if (weigh.least > -FLT_MAX && !weigh.far) add(std::false_type());
-    else add(std::true_type());
+      sum.hi = sub2(both(0.f), sum.hi);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < R::kSteps; ++s) {
+        float x[R::kPer];
+#pragma unroll
+        for (int e = 0; e < R::kPer; ++e) x[e] = r.at(r.first(chunk, s, lane) + e);
+#pragma unroll
+        for (int e = 0; e < R::kPer; e += 2) add_pair(sum, weigh(x[e], x[e + 1]));
+      }
+    }
     const Two all = lanes_sum(sum);
     out.y = all.hi;
     out.z = all.lo;
@@ -415,19 +442,25 @@ __device__ __forceinline__ void tell(float2* list, int at, float2 y, int lane, i
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(y.x), "f"(y.y) : "memory");
 }
 
-// A list of sums, by one warp, a lane a stretch of it in order; `entry(i)` gives one.
+// A list of sums, by one warp, a lane a stretch of it in order; `entry(i)` gives one.  The first
+// kHeld of each lane are read once.
 template <typename F>
 struct Listed {
+  static constexpr int kHeld = 5;
   F entry;
   int n, lane, from, to;
-  Two upto;  // all up to the end of this lane's
+  Two held[kHeld], upto;  // and all up to the end of this lane's
   __device__ __forceinline__ Listed(int count, int l, F f) : entry(f), n(count), lane(l) {
     const int per = (n + 31) / 32;
     from = min(lane * per, n);
     to = min(from + per, n);
-    Two mine{0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = from + i < to ? entry(from + i) : Two{0.f, 0.f};
+    Two mine = held[0];
+#pragma unroll
+    for (int i = 1; i < kHeld; ++i) mine = add_two(mine, held[i]);
 #pragma unroll 4
-    for (int i = from; i < to; ++i) mine = add_two(mine, entry(i));
+    for (int i = from + kHeld; i < to; ++i) mine = add_two(mine, entry(i));
     upto = warp_scan(mine, lane);
   }
   __device__ __forceinline__ Two total() const { return shfl_at(upto, 31); }
@@ -438,9 +471,8 @@ struct Listed {
     Two run = lane > 0 ? up : Two{0.f, 0.f};
     int hit = INT_MAX, last = -1;
     before = run;
-#pragma unroll 4
-    for (int i = from; i < to; ++i) {
-      const Two x = entry(i), next = add_two(run, x);
+    auto look = [&](int i, Two x) {
+      const Two next = add_two(run, x);
       if (x.hi > 0.f) {
         last = i;
         if (hit == INT_MAX && exceeds(next, want)) {
@@ -449,7 +481,11 @@ struct Listed {
         }
       }
       run = next;
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) look(from + i, held[i]);
+#pragma unroll 4
+    for (int i = from + kHeld; i < to; ++i) look(i, entry(i));
     const int at = __reduce_min_sync(0xffffffffu, hit);
     if (at != INT_MAX) {
       before = shfl_at(before, __ffs(__ballot_sync(0xffffffffu, hit == at)) - 1);
@@ -480,51 +516,82 @@ __global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const Draf
     s_last = -1;
   }
   cluster_arrive();
-  griddep_wait();
-  cluster_wait();  // every CTA has begun: its shared memory can be written
+  // The launch in front has let this one start, so what came before it has ended: its inputs can
+  // be read before it ends itself.
   const float t = __ldg(a.temperature + b);
   const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
+  const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1);
+  struct Test {
+    bool real;
+    float x, q, u;  // the draft's logit and probability, its random number
+  };
+  auto test_of = [&](int i) {
+    const long long row = (long long)b * a.S + i;
+    const int d = i < n ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;
+    Test v;
+    v.real = d >= 0 && d < a.V;
+    v.u = __ldg(a.uniforms + row);
+    v.x = v.real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
+    v.q = a.probs != nullptr && v.real ? __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d) : 1.f;
+    v.q = v.q > 0.f ? v.q : 0.f;
+    return v;
+  };
+  Test test{};
+  if (warp <= n) test = test_of(warp);
   const Warmth c(t);
+  griddep_wait();
+  cluster_wait();  // every CTA has begun: its shared memory can be written
   // every row's sum, and its draft's test
   for (int i = warp; i <= n; i += W) {
     const long long row = (long long)b * a.S + i;
     const float4* const st = a.stats + row * a.chunks;
-    const int d = i < n ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;
-    const bool real = d >= 0 && d < a.V;
+    constexpr int kHeld = 5;  // entries of a lane that are read once
+    float4 e[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      e[k] = lane + 32 * k < a.chunks ? __ldcg(st + lane + 32 * k) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    if (i != warp) test = test_of(i);
     float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) m = fmaxf(m, e[k].x);
 #pragma unroll 4
-    for (int k = lane; k < a.chunks; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
-    const float u = __ldg(a.uniforms + (long long)b * a.S + i);
-    const float xd = real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
-    float q = a.probs != nullptr && real ? __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d) : 1.f;
-    q = q > 0.f ? q : 0.f;
+    for (int k = lane + 32 * kHeld; k < a.chunks; k += 32) m = fmaxf(m, __ldcg(&st[k].x));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     Two z{0.f, 0.f};
     float p = 0.f;
     int best = INT_MAX;
     if (c.greedy) {
-      for (int k = lane; k < a.chunks; k += 32) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (e[k].x == m && lane + 32 * k < a.chunks) best = min(best, __float_as_int(e[k].y));
+      for (int k = lane + 32 * kHeld; k < a.chunks; k += 32) {
         const float4 s = __ldcg(st + k);
         if (s.x == m) best = min(best, __float_as_int(s.y));
       }
       best = __reduce_min_sync(0xffffffffu, best);
       z.hi = 1.f;
-      p = real && d == best ? 1.f : 0.f;
+      if (m == -INFINITY) best = INT_MAX;
+      p = test.real && test.x == m && m != -INFINITY && __ldg(a.drafts + (long long)b * (a.S - 1) + i) == best ? 1.f : 0.f;
     } else if (m != -INFINITY) {
       const Weigher weigh(m, c, lane);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const float f = weigh.of_chunk(e[k].x);
+        z = add_two(z, Two{e[k].y * f, e[k].z * f});
+      }
 #pragma unroll 4
-      for (int k = lane; k < a.chunks; k += 32) {
+      for (int k = lane + 32 * kHeld; k < a.chunks; k += 32) {
         const float4 s = __ldcg(st + k);
         const float f = weigh.of_chunk(s.x);
         z = add_two(z, Two{s.y * f, s.z * f});
       }
       z = warp_sum(z);
-      const Pair w = weigh(xd, xd);
+      const Pair w = weigh(test.x, test.x);
       p = unpair2(add2(w.hi, w.lo)).x;
     }
     if (lane == 0) {
-      s_ok[i] = i < n && real && u * q * z.hi < p;
+      s_ok[i] = i < n && test.real && test.u * test.q * z.hi < p;
       s_max[i] = m;
       s_best[i] = best;
       s_total[i] = z;
@@ -547,7 +614,6 @@ __global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const Draf
   const int d = missed ? __ldg(a.drafts + (long long)b * (a.S - 1) + j) : -1;
   const int gone = !rest && d >= 0 && d < a.V ? d : INT_MIN;  // the token that is not drawn
   const float* const q = rest ? a.probs + ((long long)b * (a.S - 1) + j) * a.V : nullptr;
-  const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1);
   const Two z = s_total[j];
   auto bound = [&](Two all) {
     const float p = __fmul_rn(u, all.hi);
