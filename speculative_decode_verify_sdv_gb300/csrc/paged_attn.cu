@@ -401,12 +401,11 @@ size_t part_bytes(int ctas, int row_tile, int D) {
 
 constexpr int kSimplePerSm = 2;
 
-// What a call of S rows needs; 0 for invalid arguments.
-size_t attn_need(int B, int S, int Hq, int heads, int dim) {
+// What a call of S rows needs on a GPU of `sms` SMs; 0 for invalid arguments.
+size_t attn_need(int B, int S, int Hq, int heads, int dim, int sms) {
   if (B < 1 || S < 1 || S > kMaxWindow || heads < 1 || Hq < 1 || Hq % heads != 0 || dim < 8 || dim % 8 != 0 ||
       dim > kMaxDim || heads > kMaxHeads || Hq > kMaxHeads)
     return 0;
-  const int sms = sdv::sm_count();
   AttnArgs a{};
   a.S = S;
   a.G = Hq / heads;
@@ -423,11 +422,11 @@ size_t attn_need(int B, int S, int Hq, int heads, int dim) {
 
 namespace sdv {
 
-size_t attn_bytes(int B, int S, int Hq, int heads, int dim) {
-  size_t most = attn_need(B, S, Hq, heads, dim);
+size_t attn_bytes(int B, int S, int Hq, int heads, int dim, int sms) {
+  size_t most = attn_need(B, S, Hq, heads, dim, sms);
   // shorter windows too: a row tile has fewer rows where a second one begins
   for (int s = 1; most != 0 && s < S; ++s) {
-    const size_t need = attn_need(B, s, Hq, heads, dim);
+    const size_t need = attn_need(B, s, Hq, heads, dim, sms);
     if (need > most) most = need;
   }
   return most;
@@ -539,7 +538,7 @@ sdv_status sdv_kv_append(const sdv_kvcache* cache, const void* k, const void* v,
 }
 
 size_t sdv_paged_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim) {
-  return sdv::attn_bytes(B, S, Hq, heads, dim);
+  return sdv::attn_bytes(B, S, Hq, heads, dim, sdv::sm_count());
 }
 
 sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,
@@ -549,7 +548,7 @@ sdv_status sdv_paged_attn(const sdv_kvcache* cache, const void* q, int64_t q_str
   const sdv_status ok = sdv::attn_check(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale, out,
                                         lse_or_null);
   if (ok != SDV_OK) return ok;
-  const size_t need = attn_need(B, S, Hq, cache->heads, cache->dim);
+  const size_t need = attn_need(B, S, Hq, cache->heads, cache->dim, sdv::sm_count());
   if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
   AttnArgs a = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
   a.out = out;

@@ -13,8 +13,8 @@ sdv_status attn_check(const sdv_kvcache* cache, const void* q, int64_t q_stride,
                       const int32_t* ctx, const int32_t* n_rows, const uint32_t* mask, float scale, const void* out,
                       const float* lse);
 
-// Workspace bytes of calls of up to S rows; 0 for invalid arguments.
-size_t attn_bytes(int B, int S, int Hq, int heads, int dim);
+// Workspace bytes of calls of up to S rows on a GPU of `sms` SMs (0: not known); 0 for invalid arguments.
+size_t attn_bytes(int B, int S, int Hq, int heads, int dim, int sms);
 
 // A checked call's arguments, without outputs and workspace.
 AttnArgs attn_args(const sdv_kvcache* cache, const void* q, int64_t q_stride, int32_t B, int32_t S, int32_t Hq,

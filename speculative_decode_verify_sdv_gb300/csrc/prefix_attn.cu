@@ -247,8 +247,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const int tiles = prefix_tiles(a, prefix_length(a, bad));
   const long long total = (long long)tiles * a.units, first = (long long)unit * tiles;
   const int live = attn_live_ctas(a.ctas, total);
-  const int parts = tiles > 0 ? attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1 : 0;
-  const int own_parts = j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
+  const bool row_is = s < seq.n;
+  const int parts = row_is && tiles > 0 ? attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1 : 0;
+  const int own_parts = row_is && j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
   griddep_wait();
   griddep_launch_dependents();
   if (!is) return;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     if (j.own.parts > 0) {
       gather(odd, j.own.part_ml + orow, reinterpret_cast<const float4*>(j.own.part_o) + orow * (D / 4), step2,
              step2 * (D / 4), own_parts);
-    } else {
+    } else if (row_is) {
       // the own positions' output is that of a sum of 1 at a maximum of their lse
       const float lse = __ldcg(own.lse + orow);
       float4 x[N];
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   for (int n = 0; n < N; ++n)
     finite &= fabsf(sum.o[n].x) + fabsf(sum.o[n].y) + fabsf(sum.o[n].z) + fabsf(sum.o[n].w) < INFINITY;
   if (!finite) all(std::true_type());
-  const bool none = s >= seq.n || sum.l == 0.f;
+  const bool none = !row_is || sum.l == 0.f;
   const float inv = 1.f / sum.l;
   uint2* const dst = reinterpret_cast<uint2*>(static_cast<T*>(j.out) + orow * D);
 #pragma unroll
@@ -398,10 +399,10 @@ PrefixArgs prefix_shape(int B, int S, int Hq, int heads, int dim, bool tc, int s
   return a;
 }
 
-size_t prefix_need(int B, int S, int Hq, int heads, int dim) {
-  const size_t own = attn_bytes(B, S, Hq, heads, dim);
+// `own`: attn_bytes of the call.
+size_t prefix_need(size_t own, int B, int S, int Hq, int heads, int dim, int sms) {
   if (own == 0 || (long long)B * S * Hq > (1ll << 30)) return 0;
-  const int sms = sm_count() > 0 ? sm_count() : 256;
+  if (sms <= 0) sms = 256;
   size_t most = 0;
   for (int tc = 0; tc < 2; ++tc) {
     const size_t n = prefix_layout(prefix_shape(B, S, Hq, heads, dim, tc, sms), own, B, S, sms).total;
@@ -417,7 +418,8 @@ size_t prefix_need(int B, int S, int Hq, int heads, int dim) {
 extern "C" {
 
 size_t sdv_prefix_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq, int32_t heads, int32_t dim) {
-  return sdv::prefix_need(B, S, Hq, heads, dim);
+  const int sms = sdv::sm_count();
+  return sdv::prefix_need(sdv::attn_bytes(B, S, Hq, heads, dim, sms), B, S, Hq, heads, dim, sms);
 }
 
 sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table, int32_t prefix_pages,
@@ -431,9 +433,10 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   if (prefix_table == nullptr || prefix_len == nullptr || prefix_pages < 1 ||
       ((reinterpret_cast<uintptr_t>(prefix_table) | reinterpret_cast<uintptr_t>(prefix_len)) & 3u) != 0)
     return SDV_ERR_INVALID_ARG;
-  const size_t need = sdv::prefix_need(B, S, Hq, cache->heads, cache->dim);
-  if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
   const int sms = sdv::sm_count();
+  const size_t own_bytes = sdv::attn_bytes(B, S, Hq, cache->heads, cache->dim, sms);
+  const size_t need = sdv::prefix_need(own_bytes, B, S, Hq, cache->heads, cache->dim, sms);
+  if (ws == nullptr || !sdv::is_aligned16(ws) || need == 0 || ws_bytes < need) return SDV_ERR_WORKSPACE;
   if (sms <= 0) return SDV_ERR_CUDA;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool tc = sdv::attn_tc_takes(cache->dim, Hq / cache->heads, cache->page_size,
@@ -451,7 +454,7 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   a.max_pages = prefix_pages;
   a.status = static_cast<int*>(ws);
   a.fault = sdv::debug_fault();
-  const sdv::PrefixBytes at = sdv::prefix_layout(a, sdv::attn_bytes(B, S, Hq, cache->heads, cache->dim), B, S, sms);
+  const sdv::PrefixBytes at = sdv::prefix_layout(a, own_bytes, B, S, sms);
   char* const base = static_cast<char*>(ws);
   a.part_ml = reinterpret_cast<float*>(base + at.part_ml);
   a.part_o = reinterpret_cast<float*>(base + at.part_o);

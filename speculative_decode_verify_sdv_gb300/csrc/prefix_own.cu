@@ -75,6 +75,47 @@ __device__ __noinline__ uint32_t own_odd(const AttnArgs& a, int b, int h, int ct
 
 constexpr int kSlice = 32;  // positions
 
+// Values of a slice from row `first` on: 0 in rows that are not there, and for what is not finite;
+// whether there was any of that.  (A loop of its own: what a warp does once a slice or once a part
+// is kept out of the straight code around it, whose instructions come late enough as it is.)
+template <typename T, int D>
+__device__ __forceinline__ bool own_clean(uint8_t* values, int first, uint32_t there, int lane) {
+  bool odd = false;
+#pragma unroll 1
+  for (int e = first * (D / 8) + lane; e < kSlice * (D / 8); e += 32) {
+    const int row = e / (D / 8), ch = e % (D / 8);
+    uint4* const at = reinterpret_cast<uint4*>(values + (ch >> 3) * (kSlice * 128) + row * 128 + (((ch ^ row) & 7) << 4));
+    if (!(there >> row & 1u)) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *at;
+    uint32_t* const w = reinterpret_cast<uint32_t*>(&x);
+    bool any = false;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const uint32_t bad = nonfinite16<T>(w[y]);
+      any |= bad != 0;
+      w[y] &= (bad & 1u ? 0xffff0000u : 0xffffffffu) & (bad & 2u ? 0x0000ffffu : 0xffffffffu);
+    }
+    if (any) *at = x;
+    odd |= any;
+  }
+  return odd;
+}
+
+// A lane's outputs of a row, 16 columns of every 64 from `first` on, once more where they are not
+// finite (`all`: where they are, too): what the row's values say.
+template <typename T>
+__device__ __noinline__ void own_mend(const AttnArgs& a, int b, int h, int ctx, int from, int to, uint32_t word,
+                                      float* row, int first, bool all) {
+  for (int d = first; d < a.D; d = (d & 15) == 15 ? d + 49 : d + 1) {
+    if (!all && fabsf(row[d]) < INFINITY) continue;
+    const uint32_t odd = own_odd<T>(a, b, h, ctx, from, to, word, d);
+    if (odd) row[d] = odd_value(odd);
+  }
+}
+
 template <int D, int MT>
 struct OwnPlan {
   static constexpr int R = 16 * MT;
@@ -120,7 +161,7 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
   const int32_t* const table = a.table + (size_t)b * a.max_pages;
   // ---- the copies: slice i is positions from + 32 i .. + 31 ----
   const int page_log = 31 - __clz(a.page), box = min(a.page, kSlice), boxes = kSlice / box;
-  const int slices = (to - from + kSlice - 1) / kSlice;
+  const int slices = r0 < n * a.G ? (to - from + kSlice - 1) / kSlice : 0;  // none for rows behind the window's end
   const int beyond = a.n_pages * a.Hkv * a.page;  // a row past the tensor map's end: zeros
   const uint64_t policy = l2_policy_evict_first();
   // a lane's copy: a block of 64 elements, a page's part of the slice
@@ -283,6 +324,11 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
     }
     ok = mbar_wait_warp(bars + 8, i & 1, o.status);
     if (!ok) break;
+    if (edge && p0 + kSlice > ctx) {  // what is not finite must not meet a weight of 0
+      odd_values |= own_clean<T, D>(sb + PL::kHalf, max(ctx - p0, 0), there, lane);
+      fence_proxy_async_smem();  // before the next values' copy
+      __syncwarp();
+    }
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -292,18 +338,6 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
         for (int z = 0; z < 4; ++z) {
           const int row = k * 16 + (z & 1) + (z >> 1) * 8;  // + 2 c
           vx[z] = *reinterpret_cast<const uint4*>(vs + d * BLOCK + row * 128 + v_chunk[z & 1]);
-          if (edge && p0 + row + 2 * c >= ctx) {  // what is not finite must not meet a weight of 0
-            uint32_t* const w = reinterpret_cast<uint32_t*>(&vx[z]);
-            if (!(there >> (row + 2 * c) & 1u)) vx[z] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t bad = nonfinite16<T>(w[y]);
-              if (bad) {
-                odd_values = true;
-                w[y] &= (bad & 1u ? 0xffff0000u : 0xffffffffu) & (bad & 2u ? 0x0000ffffu : 0xffffffffu);
-              }
-            }
-          }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -336,33 +370,24 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int row = r0 + t * 16 + half * 8 + g;
-      if (row >= rows) continue;
+      if (!live(t, half)) continue;  // (nor does the join read these)
       const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
-      float4* const dst4 = reinterpret_cast<float4*>(o.part_o + (part + orow) * D);
+      float* const dst = o.part_o + (part + orow) * D;
+      // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
+      const bool none = sum == 0.f;
+      bool finite = true;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {  // a lane's 16 columns of a row lie side by side
           const int col = half * 2 + (e >> 3), j = d * 8 + (e & 7);
-          float y[4] = {out[t][j][col], out[t][j + 1][col], out[t][j + 2][col], out[t][j + 3][col]};
-          if (odd_values || !(fabsf(y[0]) + fabsf(y[1]) + fabsf(y[2]) + fabsf(y[3]) < INFINITY)) {
-#pragma unroll 1
-            for (int z = 0; z < 4; ++z) {
-              const uint32_t odd =
-                  live(t, half) ? own_odd<T>(a, b, h, ctx, from, to, words[t][half], d * 64 + c * 16 + e + z) : 0u;
-              if (odd) {
-                const float v = odd_value(odd);
-                y[0] = z == 0 ? v : y[0];
-                y[1] = z == 1 ? v : y[1];
-                y[2] = z == 2 ? v : y[2];
-                y[3] = z == 3 ? v : y[3];
-              }
-            }
-          }
-          // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
-          dst4[(d * 64 + c * 16 + e) / 4] =
-              sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[0], y[1], y[2], y[3]);
+          const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : make_float4(out[t][j][col], out[t][j + 1][col], out[t][j + 2][col], out[t][j + 3][col]);
+          finite &= fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY;
+          *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) = y;
         }
+      if ((odd_values && !none) || !finite)
+        own_mend<T>(a, b, h, ctx, from, to, words[t][half], dst, c * 16, odd_values);
       if (c == 0) o.part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
     }
   griddep_wait();
