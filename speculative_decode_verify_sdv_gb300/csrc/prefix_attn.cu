@@ -225,11 +225,15 @@ struct RowSum {
   }
 };
 
-constexpr int kJoinThreads = 128, kRowThreads = 8;
+constexpr int kJoinThreads = 128;
+// CTAs per SM up to which a row has more threads with more partials in flight each: six partials of
+// 3456 rows of 256 columns 12.4 us by 8 threads a row, 10.7 by 32; three to four partials of 40,960 rows
+// of 128 columns 21 us by 8 threads, 35 by 16.
+constexpr int kJoinFewCtas = 8;
 
-// Eight threads a row, each with every eighth four columns (N of them) of all its partials, `AHEAD`
-// partials in flight.
-template <typename T, int N, int AHEAD>
+// kRowThreads threads a row, each with every kRowThreads-th four columns (N of them) of all its
+// partials, `AHEAD` partials in flight.
+template <typename T, int kRowThreads, int N, int AHEAD>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
   const PrefixArgs& a = j.prefix;
   const AttnArgs& own = j.own.attn;
@@ -244,11 +248,15 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const int b = token / own.S, s = token - b * own.S;
   const AttnSeq seq = attn_seq(own, b);
   bool bad;
-  const int tiles = prefix_tiles(a, prefix_length(a, bad));
+  const int length = prefix_length(a, bad), tiles = prefix_tiles(a, length);
   const long long total = (long long)tiles * a.units, first = (long long)unit * tiles;
   const int live = attn_live_ctas(a.ctas, total);
   const bool row_is = s < seq.n;
-  const int parts = row_is && tiles > 0 ? attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1 : 0;
+  const bool in_parts = j.own.prefix_parts > 0;
+  int parts = 0;
+  if (row_is && tiles > 0)
+    parts = in_parts ? own_live_parts((length + kOwnTile - 1) / kOwnTile, j.own.prefix_parts)
+                     : attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1;
   const int own_parts = row_is && j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
   griddep_wait();
   griddep_launch_dependents();
@@ -279,8 +287,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     sum.l = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n) sum.o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const long long at = ((long long)unit * a.sharers * a.unit_tiles + sub) * a.row_tile + r;
-    const long long step = (long long)a.unit_tiles * a.row_tile, step2 = (long long)a.tokens * a.Hq;
+    const long long step2 = (long long)a.tokens * a.Hq, step = in_parts ? step2 : (long long)a.unit_tiles * a.row_tile;
+    const long long at = in_parts ? orow : ((long long)unit * a.sharers * a.unit_tiles + sub) * a.row_tile + r;
     gather(odd, reinterpret_cast<const float2*>(a.part_ml) + at, reinterpret_cast<const float4*>(a.part_o) + at * (D / 4),
            step, step * (D / 4), parts);
     if (j.own.parts > 0) {
@@ -317,19 +325,39 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     j.lse[orow] = none ? -INFINITY : (sum.m + log2f(sum.l)) * 0.6931471805599453f;
 }
 
-template <typename T>
-void (*join_kernel(int D))(JoinArgs) {
-  return D <= 64 ? prefix_join_kernel<T, 2, 4> : D <= 128 ? prefix_join_kernel<T, 4, 4> : prefix_join_kernel<T, 8, 2>;
+template <typename T, int kRowThreads, int N, int AHEAD>
+cudaError_t join_launch(const JoinArgs& j, cudaStream_t st) {
+  const long long rows = (long long)j.prefix.tokens * j.prefix.Hq, per = kJoinThreads / kRowThreads;
+  return launch_pdl(prefix_join_kernel<T, kRowThreads, N, AHEAD>, dim3((unsigned)((rows + per - 1) / per)),
+                    dim3(kJoinThreads), 0, st, j);
 }
 
-cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, cudaStream_t st) {
-  const PrefixArgs& a = j.prefix;
-  const long long rows = (long long)a.tokens * a.Hq, per = kJoinThreads / kRowThreads;
-  return launch_pdl(dtype == SDV_F16 ? join_kernel<__half>(a.D) : join_kernel<__nv_bfloat16>(a.D),
-                    dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, st, j);
+template <typename T>
+cudaError_t join_dispatch(const JoinArgs& j, int sms, cudaStream_t st) {
+  const int D = j.prefix.D;
+  const bool few = (long long)j.prefix.tokens * j.prefix.Hq * (D <= 64 ? 8 : D <= 128 ? 16 : 32) <=
+                   (long long)kJoinFewCtas * kJoinThreads * sms;
+  if (D <= 64) return few ? join_launch<T, 8, 2, 8>(j, st) : join_launch<T, 8, 2, 4>(j, st);
+  if (D <= 128) return few ? join_launch<T, 16, 2, 8>(j, st) : join_launch<T, 8, 4, 4>(j, st);
+  return few ? join_launch<T, 32, 2, 8>(j, st) : join_launch<T, 8, 8, 2>(j, st);
+}
+
+cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, int sms, cudaStream_t st) {
+  return dtype == SDV_F16 ? join_dispatch<__half>(j, sms, st) : join_dispatch<__nv_bfloat16>(j, sms, st);
 }
 
 constexpr int kSimplePerSm = 2;
+// Up to 16 rows a kv head, heads of up to 128 and up to 8192 positions: the prefix goes into the
+// launch of the own positions, in at most 32 parts a head (the join reads them all: 75 parts of 4800
+// positions 21.3 us, 25 of them 18.0).  Against the tensor-core kernel in front of that launch,
+// four rows of 32 heads over 8 of 128, 100 positions of their own: 300 positions 10.7 against
+// 11.7 us, 2400 15.4 against 20.5, 8000 22.1 against 23.7; one row 9.2 against 12.2, 13.3 against
+// 20.4, 20.2 against 23.0.  32 rows a head (two row tiles a warp) lose, 18.3 against 14.8 at 1201
+// positions, and so do heads of 256, 25.6 against 22.1 at 4800.  Its partials are at most
+// 2 sms * 16 rows, a quarter of what the workspace has room for.
+constexpr int kPrefixFewRows = 16;
+constexpr int kPrefixFewParts = 32;
+constexpr int kPrefixFewTiles = 4;  // of kOwnTile positions in a part of it
 
 // Row tiles and units of a call; `tc`: of the tensor-core kernel.
 void set_units(PrefixArgs& a, bool tc, int sms) {
@@ -355,13 +383,22 @@ void set_units(PrefixArgs& a, bool tc, int sms) {
   a.sharers = (a.ctas + a.units - 1) / a.units + 1;
 }
 
-// Parts of a sequence's own positions: enough CTAs for two rounds of them.
+// Parts of a sequence's own positions: enough CTAs for two rounds of them, and no more than tiles.
+// The prefix too where there are few rows and a part of it is short.
 void set_parts(OwnArgs& o, int sms) {
-  o.row_tiles = own_row_tiles(o.attn.D, o.attn.rows);
-  o.row_groups = (o.attn.rows + 16 * o.row_tiles - 1) / (16 * o.row_tiles);
-  const long long units = (long long)o.attn.B * o.attn.Hkv * o.row_groups;
-  const long long parts = (16ll * sms + units - 1) / units;
-  o.parts = parts < kOwnMaxParts ? (int)parts : kOwnMaxParts;
+  const AttnArgs& a = o.attn;
+  const long long tiles = ((long long)a.max_pages * a.page + kOwnTile - 1) / kOwnTile;
+  const long long prefix_tiles = ((long long)o.prefix_pages * a.page + kOwnTile - 1) / kOwnTile;
+  const int room = 2 * sms / a.Hkv, most = room < kPrefixFewParts ? room : kPrefixFewParts;
+  const long long prefix_parts = prefix_tiles < most ? prefix_tiles : most;
+  const bool few = a.D <= 128 && (long long)a.B * a.rows <= kPrefixFewRows && prefix_tiles <= kPrefixFewTiles * prefix_parts;
+  o.prefix_parts = few ? (int)prefix_parts : 0;
+  o.row_tiles = own_row_tiles(a.D, a.rows);
+  o.row_groups = (a.rows + 16 * o.row_tiles - 1) / (16 * o.row_tiles);
+  const long long units = (long long)a.B * a.Hkv * o.row_groups;
+  long long parts = (16ll * sms + units - 1) / units;
+  if (parts > kOwnMaxParts) parts = kOwnMaxParts;
+  o.parts = parts < tiles ? (int)parts : (int)tiles;
 }
 
 struct PrefixBytes {
@@ -458,19 +495,29 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   char* const base = static_cast<char*>(ws);
   a.part_ml = reinterpret_cast<float*>(base + at.part_ml);
   a.part_o = reinterpret_cast<float*>(base + at.part_o);
-  const cudaError_t e =
-      tc ? sdv::launch_prefix_tc(cache->dtype, a, st) : sdv::launch_prefix_simple(cache->dtype, a, st);
-  if (e != cudaSuccess) return sdv::status_of(e);
   sdv::JoinArgs j{};
-  j.prefix = a;
   j.out = out;
   j.lse = lse_or_null;
   sdv::OwnArgs& own = j.own;
   own.attn = sdv::attn_args(cache, q, q_stride, B, S, Hq, ctx, n_rows_or_null, mask_or_null, scale);
   own.status = a.status;
+  own.prefix_table = prefix_table;
+  own.prefix_length = prefix_len;
+  own.prefix_pages = prefix_pages;
   sdv::set_parts(own, sms);
   own.attn.fault = sdv::debug_fault();
-  if (tc && sdv::own_takes((long long)cache->max_pages * cache->page_size, own.parts)) {
+  const bool parts = tc && sdv::own_takes((long long)cache->max_pages * cache->page_size, own.parts);
+  if (!parts) own.prefix_parts = 0;
+  if (own.prefix_parts > 0) {
+    own.prefix_o = a.part_o;
+    own.prefix_ml = reinterpret_cast<float2*>(a.part_ml);
+  } else {
+    const cudaError_t e =
+        tc ? sdv::launch_prefix_tc(cache->dtype, a, st) : sdv::launch_prefix_simple(cache->dtype, a, st);
+    if (e != cudaSuccess) return sdv::status_of(e);
+  }
+  j.prefix = a;
+  if (parts) {
     own.attn.tile = sdv::kOwnTile;
     own.part_ml = reinterpret_cast<float2*>(base + at.own_ml);
     own.part_o = reinterpret_cast<float*>(base + at.own_o);
@@ -484,7 +531,7 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
     if (run != SDV_OK) return run;
     own.attn.tile = 1;  // (of no meaning to the join)
   }
-  return sdv::status_of(sdv::launch_prefix_join(cache->dtype, j, st));
+  return sdv::status_of(sdv::launch_prefix_join(cache->dtype, j, sms, st));
 }
 
 }  // extern "C"

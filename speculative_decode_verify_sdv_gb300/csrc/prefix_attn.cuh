@@ -39,12 +39,15 @@ struct PrefixArgs {
 };
 
 // The prefix's length as it counts, and its tiles.
-__device__ __forceinline__ int prefix_length(const PrefixArgs& a, bool& bad) {
-  const int n = __ldg(a.length);
-  const long long cap = (long long)a.max_pages * a.page;
+__device__ __forceinline__ int prefix_length(const int32_t* length, int max_pages, int page, bool& bad) {
+  const int n = __ldg(length);
+  const long long cap = (long long)max_pages * page;
   const int most = cap > 0x7fffff00ll ? 0x7fffff00 : (int)cap, m = min(max(n, 0), most);
   bad = m != n;
   return m;
+}
+__device__ __forceinline__ int prefix_length(const PrefixArgs& a, bool& bad) {
+  return prefix_length(a.length, a.max_pages, a.page, bad);
 }
 __device__ __forceinline__ int prefix_tiles(const PrefixArgs& a, int length) {
   return (int)(((unsigned)length + a.tile - 1) / (unsigned)a.tile);

@@ -60,12 +60,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // What is not finite in column d of the values that a row sees among positions from .. to - 1.
 template <typename T>
-__device__ __noinline__ uint32_t own_odd(const AttnArgs& a, int b, int h, int ctx, int from, int to, uint32_t word,
-                                         int d) {
+__device__ __noinline__ uint32_t own_odd(const AttnArgs& a, const int32_t* table, int h, int ctx, int from, int to,
+                                         uint32_t word, int d) {
   uint32_t odd = 0;
   for (int p = from; p < to; ++p) {
     if (p >= ctx && !(word >> (p - ctx) & 1u)) continue;
-    const int id = __ldg(a.table + (size_t)b * a.max_pages + p / a.page);
+    const int id = __ldg(table + p / a.page);
     if (id < 0 || id >= a.n_pages) continue;
     const float x = (float)static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d];
     if (!(fabsf(x) < INFINITY)) odd |= x != x ? kOddNan : x > 0.f ? kOddPlus : kOddMinus;
@@ -107,11 +107,11 @@ __device__ __forceinline__ bool own_clean(uint8_t* values, int first, uint32_t t
 // A lane's outputs of a row, 16 columns of every 64 from `first` on, once more where they are not
 // finite (`all`: where they are, too): what the row's values say.
 template <typename T>
-__device__ __noinline__ void own_mend(const AttnArgs& a, int b, int h, int ctx, int from, int to, uint32_t word,
-                                      float* row, int first, bool all) {
+__device__ __noinline__ void own_mend(const AttnArgs& a, const int32_t* table, int h, int ctx, int from, int to,
+                                      uint32_t word, float* row, int first, bool all) {
   for (int d = first; d < a.D; d = (d & 15) == 15 ? d + 49 : d + 1) {
     if (!all && fabsf(row[d]) < INFINITY) continue;
-    const uint32_t odd = own_odd<T>(a, b, h, ctx, from, to, word, d);
+    const uint32_t odd = own_odd<T>(a, table, h, ctx, from, to, word, d);
     if (odd) row[d] = odd_value(odd);
   }
 }
@@ -141,14 +141,29 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
   const uint32_t bars = base + 2 * PL::kHalf + R * LQ;
   const AttnArgs& a = o.attn;
   const int lane = threadIdx.x, g = lane >> 2, c = lane & 3;
-  const int rg = blockIdx.x % o.row_groups, bh = blockIdx.x / o.row_groups, h = bh % a.Hkv, b = bh / a.Hkv;
-  // The launch in front has let this one start, so what came before it has ended; nothing is read
-  // that it writes.  It is waited for at the end, for the launch behind.
+  // the prefix's parts first; of a sequence all first parts, then all second ones
+  const int prefix_ctas = a.Hkv * o.prefix_parts, cta = (int)blockIdx.x - prefix_ctas;
+  const bool shared = cta < 0;
+  const int units = shared ? a.Hkv : a.B * a.Hkv * o.row_groups, at = shared ? (int)blockIdx.x : cta;
+  const int y = at / units, unit = at - y * units;
+  const int rg = shared ? 0 : unit % o.row_groups, bh = shared ? unit : unit / o.row_groups, h = bh % a.Hkv,
+            b = bh / a.Hkv;  // (the rows of all sequences are those of "sequence" 0, were it that long)
+  // Behind another launch of this call: that one has let this one start, so what came before it has
+  // ended; nothing is read that it writes.  It is waited for at the end, for the launch behind.
+  if (o.prefix_parts > 0) griddep_wait();
   griddep_launch_dependents();
-  const AttnSeq seq = attn_seq(a, b);
-  const int ctx = seq.ctx, n = seq.n, total = ctx + n, per = own_per_part(seq.tiles, o.parts);
-  const int from = (int)blockIdx.y * per * kOwnTile, to = min(from + per * kOwnTile, total);
-  if (blockIdx.y > 0 && from >= total) return;
+  AttnSeq seq;
+  if (shared) {
+    seq.ctx = prefix_length(o.prefix_length, o.prefix_pages, a.page, seq.bad);
+    seq.n = a.B * a.S;
+    seq.tiles = (seq.ctx + kOwnTile - 1) / kOwnTile;
+  } else {
+    seq = attn_seq(a, b);
+  }
+  const int ctx = seq.ctx, n = seq.n, total = shared ? ctx : ctx + n;
+  const int per = own_per_part(seq.tiles, shared ? o.prefix_parts : o.parts);
+  const int from = y * per * kOwnTile, to = min(from + per * kOwnTile, total);
+  if (y > 0 && from >= total) return;
   if (lane == 0) {
     set_wait_limit(a.fault);
     mbar_init(bars, 1);
@@ -157,8 +172,8 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
     if (seq.bad) atomicOr(o.status, kDevErrIndex);
   }
   __syncwarp();
-  const int r0 = rg * R, rows = a.rows;
-  const int32_t* const table = a.table + (size_t)b * a.max_pages;
+  const int r0 = rg * R, rows = shared ? n * a.G : a.rows;
+  const int32_t* const table = shared ? o.prefix_table : a.table + (size_t)b * a.max_pages;
   // ---- the copies: slice i is positions from + 32 i .. + 31 ----
   const int page_log = 31 - __clz(a.page), box = min(a.page, kSlice), boxes = kSlice / box;
   const int slices = r0 < n * a.G ? (to - from + kSlice - 1) / kSlice : 0;  // none for rows behind the window's end
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int row = r0 + t * 16 + half * 8 + g;
-      words[t][half] = row < rows ? attn_word(a, b, row / a.G, n) : 0u;
+      words[t][half] = row < rows && !shared ? attn_word(a, b, row / a.G, n) : 0u;
     }
   auto live = [&](int t, int half) {
     const int row = r0 + t * 16 + half * 8 + g;
@@ -361,7 +376,9 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
     if (next_keys && i + 2 != a.fault.withhold) mbar_wait_bounded(bars, (i + 1) & 1, kOwnDrainNs);
   }
   odd_values = __any_sync(0xffffffffu, odd_values);
-  const size_t part = (size_t)blockIdx.y * a.B * a.S * a.Hq;
+  const size_t part = (size_t)y * a.B * a.S * a.Hq;
+  float* const part_o = shared ? o.prefix_o : o.part_o;
+  float2* const part_ml = shared ? o.prefix_ml : o.part_ml;
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
       const int row = r0 + t * 16 + half * 8 + g;
       if (!live(t, half)) continue;  // (nor does the join read these)
       const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
-      float* const dst = o.part_o + (part + orow) * D;
+      float* const dst = part_o + (part + orow) * D;
       // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
       const bool none = sum == 0.f;
       bool finite = true;
@@ -387,10 +404,10 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
           *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) = y;
         }
       if ((odd_values && !none) || !finite)
-        own_mend<T>(a, b, h, ctx, from, to, words[t][half], dst, c * 16, odd_values);
-      if (c == 0) o.part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
+        own_mend<T>(a, table, h, ctx, from, to, words[t][half], dst, c * 16, odd_values);
+      if (c == 0) part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
     }
-  griddep_wait();
+  if (o.prefix_parts == 0) griddep_wait();
 }
 
 template <typename T, int D, int MT>
@@ -406,7 +423,8 @@ cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3(a.attn.B * a.attn.Hkv * a.row_groups, a.parts), dim3(32), smem, st, m, a);
+  const unsigned ctas = (unsigned)a.attn.Hkv * a.prefix_parts + (unsigned)a.attn.B * a.attn.Hkv * a.row_groups * a.parts;
+  return launch_pdl(kernel, dim3(ctas), dim3(32), smem, st, m, a);
 }
 
 template <typename T>

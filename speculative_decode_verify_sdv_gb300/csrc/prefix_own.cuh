@@ -9,7 +9,7 @@ namespace sdv {
 constexpr int kOwnTile = 64;        // positions that a part is a whole number of
 constexpr int kOwnMaxParts = 16;
 
-// A sequence's own positions in parts of whole tiles, a CTA each.
+// A sequence's own positions in parts of whole tiles, a CTA each (and the prefix's).
 struct OwnArgs {
   AttnArgs attn;      // tile = kOwnTile; out, lse and workspace fields of no meaning
   int row_tiles;      // m16 row tiles of a CTA
@@ -18,6 +18,12 @@ struct OwnArgs {
   float* part_o;      // [parts][B * S][Hq][D], relative to the part's maximum
   float2* part_ml;    // [parts][B * S][Hq]: maximum (log2 domain), sum
   int* status;
+  // The prefix in parts too, for few rows: all rows of a kv head in one CTA.
+  int prefix_parts;   // 0: it is the tensor-core kernel's
+  const int32_t *prefix_table, *prefix_length;
+  int prefix_pages;
+  float* prefix_o;    // [prefix_parts][B * S][Hq][D], [2]: as above
+  float2* prefix_ml;
 };
 
 // Tiles of each part of a sequence but the last, and how many parts have any.
