@@ -304,3 +304,70 @@ def test_own_positions_that_are_not_finite_or_absent(sdv, d):
     short[1, 1] = table[1, 2]
     ref = reference(q, kp, vp, ptable, 100, short, [20, 24, 0], n, None, d ** -0.5)
     check(F16, ref, out, lse, d)
+
+
+def forms(ptable, page):
+    """The prefix's table as it is, and with room for more positions than few rows take in parts: what is
+    asked for is the same, the kernel is another."""
+    wide = torch.full((9000 // page + 1,), -1, dtype=torch.int32)
+    wide[:len(ptable)] = ptable
+    return ptable, wide
+
+
+@pytest.mark.parametrize("dt,d,page", [(F16, 128, 16), (BF16, 64, 64), (BF16, 128, 8), (F16, 64, 32)])
+@pytest.mark.parametrize("prefix", [1, 31, 32, 33, 63, 64, 65, 129, 2047, 2049, 4100, 8192])
+def test_a_prefix_before_few_rows(sdv, dt, d, page, prefix):
+    ctx, n = [0, 70], [2, 1]
+    q, kp, vp, ptable, table = make(dt, 2, 2, 8, 2, d, page, prefix, ctx, n, prefix + d)
+    ref = reference(q, kp, vp, ptable, prefix, table, ctx, n, None, d ** -0.5)
+    for pt in forms(ptable[:-1], page):
+        out, lse, ws = call(sdv, q, kp, vp, pt, prefix, table, ctx, n, None, d ** -0.5)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+        check(dt, ref, out, lse, d)
+
+
+@pytest.mark.parametrize("dt,d", [(F16, 128), (BF16, 64)])
+def test_odd_values_and_absent_pages_before_few_rows(sdv, dt, d):
+    ctx, n = [20, 3], [2, 1]
+    q, kp, vp, ptable, table = make(dt, 2, 2, 8, 2, d, 16, 400, ctx, n, 8, std=20.0)
+    for pt in forms(ptable[:-1], 16):
+        bad = pt.clone()
+        bad[5], bad[19] = -1, kp.shape[0]
+        out, lse, ws = call(sdv, q, kp, vp, bad, 400, table, ctx, n, None, d ** -0.5)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+        keep = torch.cat([ptable[:5], ptable[6:19], ptable[20:25]])
+        check(dt, reference(q, kp, vp, keep, 368, table, ctx, n, None, d ** -0.5), out, lse, d)
+    at = lambda p: (int(ptable[p // 16]), p % 16)  # noqa: E731
+    want = {}
+    for p, h, c, x in ((3, 0, 1, float("inf")), (390, 0, d - 1, float("nan")), (140, 1, 7, float("-inf")),
+                       (5, 1, 9, float("inf")), (391, 1, 9, float("-inf"))):
+        page, slot = at(p)
+        vp[page, h, slot, c] = x
+        want[h, c] = float("nan") if (h, c) in want else x
+    for pt in forms(ptable[:-1], 16):
+        out, _, ws = call(sdv, q, kp, vp, pt, 400, table, ctx, n, None, d ** -0.5)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+        out = out.float().cpu()
+        for b, i in ((0, 0), (0, 1), (1, 0)):
+            for h in range(8):
+                for c in range(d):
+                    x, y = float(out[b, i, h, c]), want.get((h // 4, c), 0.0)
+                    assert np.isfinite(x) if y == 0.0 else (np.isnan(x) if np.isnan(y) else x == y)
+        assert not out[1, 1].any()
+
+
+def test_a_prefix_before_few_rows_behind_the_launch_that_writes_it(sdv):
+    """A call reads what the launch in front of it in the stream writes: queries, cache and lengths."""
+    ctx, n = [20, 3], [2, 2]
+    q, kp, vp, ptable, table = (x.cuda() for x in make(F16, 2, 2, 8, 2, 128, 16, 1000, ctx, n, 31))
+    want, _, ws = call(sdv, q, kp, vp, ptable, 1000, table, ctx, n, None, 0.1)
+    out, c, m, ln = torch.zeros_like(q), dev(ctx), dev(n), dev([1000])
+    q2, k2, v2, l2 = torch.zeros_like(q), torch.zeros_like(kp), torch.zeros_like(vp), torch.zeros_like(ln)
+    for _ in range(50):
+        out.zero_()
+        for x in (q2, k2, v2, l2):
+            x.zero_()
+        for x, y in ((v2, vp), (k2, kp), (q2, q), (l2, ln)):
+            x.copy_(y)
+        sdv.sdv_prefix_attn(q2, k2, v2, ptable, l2, table, c, m, None, 0.1, out, None, ws)
+        assert torch.equal(out, want)
