@@ -355,6 +355,7 @@ constexpr int kSimplePerSm = 2;
 // 20.4, 20.2 against 23.0.  32 rows a head (two row tiles a warp) lose, 18.3 against 14.8 at 1201
 // positions, and so do heads of 256, 25.6 against 22.1 at 4800.  Its partials are at most
 // 2 sms * 16 rows, a quarter of what the workspace has room for.
+constexpr int kOwnPerSm = 16;  // CTAs for the own positions, if all their parts have some
 constexpr int kPrefixFewRows = 16;
 constexpr int kPrefixFewParts = 32;
 constexpr int kPrefixFewTiles = 4;  // of kOwnTile positions in a part of it
@@ -396,7 +397,7 @@ void set_parts(OwnArgs& o, int sms) {
   o.row_tiles = own_row_tiles(a.D, a.rows);
   o.row_groups = (a.rows + 16 * o.row_tiles - 1) / (16 * o.row_tiles);
   const long long units = (long long)a.B * a.Hkv * o.row_groups;
-  long long parts = (16ll * sms + units - 1) / units;
+  long long parts = ((long long)kOwnPerSm * sms + units - 1) / units;
   if (parts > kOwnMaxParts) parts = kOwnMaxParts;
   o.parts = parts < tiles ? (int)parts : (int)tiles;
 }
@@ -414,7 +415,7 @@ PrefixBytes prefix_layout(const PrefixArgs& a, size_t own, int B, int S, int sms
   // a CTA has 16 * row_tiles rows at most, 256 / dim (at least one) row tiles at most
   const int tiles = a.D >= 256 ? 1 : a.D >= 128 ? 2 : 4;
   const size_t groups = ((size_t)S * a.G + 16 * tiles - 1) / (16 * tiles) * a.Hkv * B;
-  const size_t parts = (16 * (size_t)sms + 4 * groups) * 16 * tiles;
+  const size_t parts = (kOwnPerSm * (size_t)sms + 4 * groups) * 16 * tiles;
   const size_t own_rows = parts > outs ? parts : outs;
   PrefixBytes p;
   p.part_ml = round_256(own);
