@@ -655,8 +655,9 @@ SDV_API sdv_status sdv_workspace_init(void* ws, size_t ws_bytes, sdv_stream_t st
  * leaves in `ws`: SDV_OK, or SDV_ERR_TIMEOUT if a bounded device-side wait gave
  * up (the outputs of that call are then undefined; later calls on the same
  * workspace are unaffected), or SDV_ERR_INVALID_ARG if a device-side table entry
- * or length was out of range (sdv_kv_append, sdv_paged_attn).  Any other flag (the tensor-memory allocation was
- * not where the kernel expects it) reads as SDV_ERR_CUDA.  The status word
+ * or length was out of range (sdv_kv_append, sdv_paged_attn, sdv_page_assign,
+ * sdv_qk_norm_rope, sdv_prefix_attn).  Any other flag (the tensor-memory allocation
+ * was not where the kernel expects it) reads as SDV_ERR_CUDA.  The status word
  * collects the flags of every call since the last read.
  * (The boundary's "bounded-wait / debug-assert flags" read: "Stream C --
  * Speculative decoding: feasibility verdict + implementation plan", section
@@ -691,8 +692,8 @@ SDV_API int32_t sdv_set_gemm_path(int32_t path);
  * Test hook of the timeout path (process-wide; every later launch of the
  * tcgen05 path uses it until it is reset with (-1, 0)).  withhold_stage >= 0:
  * in every CTA the weight copy of that stage of the CTA's stage sequence (the
- * tensor-core attention: the keys' copy of that one of its tiles; the chunked
- * linear attention: of that one of its chunks) is
+ * tensor-core attention, behind a shared prefix too: the keys' copy of that one
+ * of its tiles or slices; the chunked linear attention: of that one of its chunks) is
  * never issued, so the roles waiting for it give up after the wait limit
  * -- a wait on a barrier that nothing completes, with no copy in flight behind
  * it; the kernel then drains what it issued, writes undefined outputs and sets

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
           finite &= fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY;
           *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) = y;
         }
-      if ((odd_values && !none) || !finite)
+      if (sum > 0.f && (odd_values || !finite))  // (NaN scores, a padding row's for one, leave NaN)
         own_mend<T>(a, table, h, ctx, from, to, words[t][half], dst, c * 16, odd_values);
       if (c == 0) part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
     }

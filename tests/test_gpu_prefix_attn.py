@@ -371,3 +371,16 @@ def test_a_prefix_before_few_rows_behind_the_launch_that_writes_it(sdv):
             x.copy_(y)
         sdv.sdv_prefix_attn(q2, k2, v2, ptable, l2, table, c, m, None, 0.1, out, None, ws)
         assert torch.equal(out, want)
+
+
+def test_what_padding_rows_hold_before_few_rows(sdv):
+    """Rows behind a window's end hold anything: the live rows' bits are the same, the others 0."""
+    ctx, n = [20, 3], [2, 1]
+    q, kp, vp, ptable, table = make(F16, 2, 2, 8, 2, 128, 16, 400, ctx, n, 32)
+    want, wl, _ = call(sdv, q, kp, vp, ptable, 400, table, ctx, n, None, 0.1)
+    for x in (float("nan"), float("inf"), 60000.0):
+        other = q.clone()
+        other[1, 1] = x
+        out, lse, ws = call(sdv, other, kp, vp, ptable, 400, table, ctx, n, None, 0.1)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+        assert torch.equal(out, want) and torch.equal(lse, wl) and not out[1, 1].any()
