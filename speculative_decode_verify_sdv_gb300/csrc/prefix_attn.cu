@@ -347,6 +347,9 @@ cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, int sms, cudaStream
 }
 
 constexpr int kSimplePerSm = 2;
+// CTAs per SM for the own positions, were all tables full: some end at once.  (16, 24, 32, 48: 64
+// sequences of up to 2001 positions 72.1, 71.3, 71.0, 73.1 us a call, 256 of up to 1001 364, 366, 374, 389.)
+constexpr int kOwnPerSm = 16;
 // Up to 16 rows a kv head, heads of up to 128 and up to 8192 positions: the prefix goes into the
 // launch of the own positions, in at most 32 parts a head (the join reads them all: 75 parts of 4800
 // positions 21.3 us, 25 of them 18.0).  Against the tensor-core kernel in front of that launch,
@@ -355,7 +358,6 @@ constexpr int kSimplePerSm = 2;
 // 20.4, 20.2 against 23.0.  32 rows a head (two row tiles a warp) lose, 18.3 against 14.8 at 1201
 // positions, and so do heads of 256, 25.6 against 22.1 at 4800.  Its partials are at most
 // 2 sms * 16 rows, a quarter of what the workspace has room for.
-constexpr int kOwnPerSm = 16;  // CTAs for the own positions, if all their parts have some
 constexpr int kPrefixFewRows = 16;
 constexpr int kPrefixFewParts = 32;
 constexpr int kPrefixFewTiles = 4;  // of kOwnTile positions in a part of it
@@ -507,7 +509,7 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   own.prefix_pages = prefix_pages;
   sdv::set_parts(own, sms);
   own.attn.fault = sdv::debug_fault();
-  const bool parts = tc && sdv::own_takes((long long)cache->max_pages * cache->page_size, own.parts);
+  const bool parts = tc && sdv::own_takes(own);
   if (!parts) own.prefix_parts = 0;
   if (own.prefix_parts > 0) {
     own.prefix_o = a.part_o;

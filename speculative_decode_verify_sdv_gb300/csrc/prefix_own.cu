@@ -7,7 +7,10 @@
 // and a unit is over before a deep pipeline has filled.  So a warp, a CTA by itself, takes a part
 // of one sequence's positions for one kv head in slices of 32, which come by TMA: the next slice's
 // keys while this one's softmax and second product run, its values during the next first product.
-// What is start and end for one warp is not for the seven and more others of its SM.
+// What is start and end for one warp is not for the seven and more others of its SM.  256 sequences of
+// 100 to 1001 positions, five rows, 8 heads of 128 (417 MB): 112 us, 3.7 TB/s; 64 of up to 2001,
+// one row (134 MB): 35 us, 3.8 TB/s.  Two warps a scheduler wait for copies, products and instructions
+// in turn; four warps a CTA and loads without TMA were slower, more and shorter parts no faster.
 //
 // The products are m16n8k16 MMAs whose operands are read as they lie, 16 bytes a lane.  A dot
 // product does not ask for the order of its terms: a lane's 16 bytes of a key row are the reduction
@@ -38,7 +41,17 @@ namespace sdv {
 
 namespace {
 
-constexpr int kOwnMost = 2048;  // positions that a part may come to
+// The paged attention deals any lengths evenly and takes some 10 us more in launches; here a part is
+// a chain of slices, 1.2 us each for one row tile of 128 columns where little else runs.  Full tables of
+// 32 heads over 8 of 128, prefix of 1000, warps against paged attention: one sequence of one row,
+// 4000 positions 20 against 28 us, 8000 30 against 31, 16,000 49 against 37; of five rows 1000
+// 24 against 26, 2000 28 against 27, 8000 55 against 31.  With more sequences both are bound by
+// reading: eight of one row, 16,000 92 against 101, of five 104 against 111.  Several row groups read
+// everything several times: nine rows of 16 heads over 2 of 256, one sequence 2000 27 against 29,
+// 8000 54 against 34; sixteen 500 45 against 45, 1000 71 against 47 -- but where most of 24 such tables
+// stay empty (rows and positions half and a sixth of what they could be) 60 against 76.
+constexpr int kOwnChain = 300;  // positions of a part, one row tile of 128 columns, up to 16 units
+constexpr int kOwnMost = 2048;  // and at most, of a single long sequence
 constexpr uint64_t kOwnDrainNs = 100000000ull;  // 0.1 s: copies under way at the end
 
 template <typename T>
@@ -442,7 +455,12 @@ cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool own_takes(long long positions, int parts) { return positions <= (long long)kOwnMost * parts; }
+bool own_takes(const OwnArgs& o) {
+  const AttnArgs& a = o.attn;
+  const long long positions = (long long)a.max_pages * a.page, units = (long long)a.B * a.Hkv;
+  const long long most = (long long)kOwnChain * (o.row_groups == 1 && units > 16 ? units : 16) / 16;
+  return positions <= (long long)kOwnMost * o.parts && positions * o.row_tiles * a.D <= most * 128 * o.parts;
+}
 
 // A row tile's outputs take dim / 2 registers of a thread.
 int own_row_tiles(int dim, int rows) {

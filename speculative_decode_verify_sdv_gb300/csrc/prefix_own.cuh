@@ -33,9 +33,9 @@ __device__ __forceinline__ int own_live_parts(int tiles, int parts) {
   return (tiles + per - 1) / per;
 }
 
-// Whether so many positions of a sequence are few enough for its parts (the shapes are those of the
-// tensor-core kernels, attn_tc_takes).
-bool own_takes(long long positions, int parts);
+// Whether the positions that a table may hold are few enough for the parts (the shapes are those of
+// the tensor-core kernels, attn_tc_takes).
+bool own_takes(const OwnArgs& o);
 int own_row_tiles(int dim, int rows);
 cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st);
 
