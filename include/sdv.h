@@ -624,8 +624,8 @@ SDV_API size_t sdv_prefix_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq,
  * A sequence whose drawn row has no token left gives next_token -1.  Weights below 2^-125 of
  * the row's largest count as 0.  Rows past n_drafts[b] are not read.
  * 1 <= S <= 32, V and B <= 2^24.  The workspace is sdv_verify_drafts_workspace_bytes(...) bytes.
- * Deterministic.  A test's probability is exact to some 2^-18, the draw's weights to some 2^-30
- * of each and their sums to 2^-40: a test or a draw nearer to its border than that may differ
+ * Deterministic.  A test's probability is exact to some 2^-18, the draw's weights and the sums
+ * of 1024 of them to some 2^-30: a test or a draw nearer to its border than that may differ
  * from a 64-bit evaluation.
  */
 SDV_API sdv_status sdv_verify_drafts(int32_t dtype, const void* logits, int64_t row_stride, int32_t B, int32_t S,

@@ -16,8 +16,10 @@
 // add up to 10^-9 of the total or more, would miss one draw in some thousands.  The weights
 // are therefore pairs of floats, exact to some 2^-30 of each (2^x by a table of 2^(k/32) and a
 // short polynomial: Tang, "Table-driven implementation of the exponential function", ACM TOMS
-// 1989), and their sums carry the rounding of every addition along (Knuth's two-sum).  No sum is
-// of 64-bit numbers: this GPU adds those at a fiftieth of the rate.
+// 1989), and their sums carry the rounding of every addition along (Knuth's two-sum); the first
+// launch takes each weight apart at 2^-17 instead, adds the upper parts exactly and the rest, a
+// hundredth at most, in 32 bits: a chunk's sum to 2^-32 (in the mean of random logits; 2^-29 the
+// worst of 1800).  No sum is of 64-bit numbers: this GPU adds those at a fiftieth of the rate.
 //
 // 25 instructions a logit bound the first launch, not its read: 32 windows, 226 rows of 151,936
 // fp32 logits in all (137 MB), 47 us, 60 % of the issue slots; 200 rows of 50,257 in bf16 16 us.  A warp

@@ -1,6 +1,6 @@
 """sdv_verify_drafts on the GPU against the 64-bit oracle: every value equal, but where the oracle's
 own margin is below what the documentation allows (fp32 sums of a test: 2^-18 of a probability; the
-draw: 2^-34 of all weights)."""
+draw: held to 2^-34 of all weights here, a sixteenth of it)."""
 import numpy as np
 import pytest
 import torch
