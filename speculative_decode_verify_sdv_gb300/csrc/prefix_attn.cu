@@ -347,9 +347,11 @@ cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, int sms, cudaStream
 }
 
 constexpr int kSimplePerSm = 2;
-// CTAs per SM for the own positions, were all tables full: some end at once.  (16, 24, 32, 48: 64
-// sequences of up to 2001 positions 72.1, 71.3, 71.0, 73.1 us a call, 256 of up to 1001 364, 366, 374, 389.)
-constexpr int kOwnPerSm = 16;
+// CTAs for the own positions, were all tables full (some end at once): per SM 16 of one warp (16, 24, 32,
+// 48: 64 sequences of up to 2001 positions 72.1, 71.3, 71.0, 73.1 us a call), 8 of more (8, 12, 16: 256
+// windows of five rows, up to 1001 positions, 361.8, 360.6, 361.7).
+int own_ctas(int warps, int sms) { return (warps > 1 ? 8 : 16) * sms; }
+
 // Up to 16 rows a kv head, heads of up to 128 and up to 8192 positions: the prefix goes into the
 // launch of the own positions, in at most 32 parts a head (the join reads them all: 75 parts of 4800
 // positions 21.3 us, 25 of them 18.0).  Against the tensor-core kernel in front of that launch,
@@ -396,10 +398,10 @@ void set_parts(OwnArgs& o, int sms) {
   const long long prefix_parts = prefix_tiles < most ? prefix_tiles : most;
   const bool few = a.D <= 128 && (long long)a.B * a.rows <= kPrefixFewRows && prefix_tiles <= kPrefixFewTiles * prefix_parts;
   o.prefix_parts = few ? (int)prefix_parts : 0;
-  o.row_tiles = own_row_tiles(a.D, a.rows);
-  o.row_groups = (a.rows + 16 * o.row_tiles - 1) / (16 * o.row_tiles);
+  o.warps = a.rows <= 16 || a.D > 128 ? 1 : a.rows <= 32 ? 2 : 4;
+  o.row_groups = (a.rows + 16 * o.warps - 1) / (16 * o.warps);
   const long long units = (long long)a.B * a.Hkv * o.row_groups;
-  long long parts = ((long long)kOwnPerSm * sms + units - 1) / units;
+  long long parts = ((long long)own_ctas(o.warps, sms) + units - 1) / units;
   if (parts > kOwnMaxParts) parts = kOwnMaxParts;
   o.parts = parts < tiles ? (int)parts : (int)tiles;
 }
@@ -414,10 +416,10 @@ PrefixBytes prefix_layout(const PrefixArgs& a, size_t own, int B, int S, int sms
   const size_t tiles_most = a.tile_tokens == 0 ? a.row_tiles : a.tiles_most;
   const size_t units_most = a.Hkv * ((tiles_most + a.unit_tiles - 1) / a.unit_tiles);
   const size_t rows = (a.ctas + 2 * units_most) * a.unit_tiles * most, outs = (size_t)B * S * a.Hq;
-  // a CTA has 16 * row_tiles rows at most, 256 / dim (at least one) row tiles at most
-  const int tiles = a.D >= 256 ? 1 : a.D >= 128 ? 2 : 4;
-  const size_t groups = ((size_t)S * a.G + 16 * tiles - 1) / (16 * tiles) * a.Hkv * B;
-  const size_t parts = (kOwnPerSm * (size_t)sms + 4 * groups) * 16 * tiles;
+  // parts * units * 16 warps rows, parts at most own_ctas / units + 1, in terms that grow with the call
+  const int wide = a.D > 128 ? 1 : 4;
+  const size_t groups = ((size_t)S * a.G + 16 * wide - 1) / (16 * wide) * a.Hkv * B;
+  const size_t parts = (own_ctas(wide, sms) + groups) * 16 * wide;
   const size_t own_rows = parts > outs ? parts : outs;
   PrefixBytes p;
   p.part_ml = round_256(own);

@@ -4,13 +4,18 @@
 //   s = q_r . k_p;  m = running max of scale s;  P = 2^((scale s - m) log2 e)
 //   l += sum P;  O = O 2^(m_old - m) + P V
 // What follows a shared prefix is short and there is a lot of it: reading it bounds the kernel,
-// and a unit is over before a deep pipeline has filled.  So a warp, a CTA by itself, takes a part
-// of one sequence's positions for one kv head in slices of 32, which come by TMA: the next slice's
-// keys while this one's softmax and second product run, its values during the next first product.
-// What is start and end for one warp is not for the seven and more others of its SM.  256 sequences of
-// 100 to 1001 positions, five rows, 8 heads of 128 (417 MB): 112 us, 3.7 TB/s; 64 of up to 2001,
-// one row (134 MB): 35 us, 3.8 TB/s.  Two warps a scheduler wait for copies, products and instructions
-// in turn; four warps a CTA and loads without TMA were slower, more and shorter parts no faster.
+// and a unit is over before a deep pipeline has filled.  So a CTA of few warps, 16 rows each, takes a
+// part of one sequence's positions for one kv head in slices of 32, which come by TMA: the next
+// slice's keys while this one's softmax and second product run, its values during the next first
+// product.  What is start and end for one CTA is not for the others of its SM.
+//
+// 256 sequences of 100 to 1001 positions, five rows, 8 heads of 128 (417 MB): 108 us, 3.9 TB/s; 64 of
+// up to 2001, one row (134 MB): 34 us, 3.9 TB/s.  Three warps a scheduler, as many as their outputs leave
+// registers for, wait for products, copies and one another.  Up to 64 rows have a warp for 16: with two
+// row tiles in one warp and groups of 32 rows 256 windows of five rows took 364 us a call for 358,
+// one of nine rows 21.7 for 15.5, 64 of them 58.5 for 53.1 (100 positions of their own).  Heads of
+// 256, whose outputs fill a warp's registers, have a CTA for 16 rows: 24 tree windows 59.6 us, by four
+// warps 61.5.  Loads without TMA were slower, more and shorter parts and two slices ahead no faster.
 //
 // The products are m16n8k16 MMAs whose operands are read as they lie, 16 bytes a lane.  A dot
 // product does not ask for the order of its terms: a lane's 16 bytes of a key row are the reduction
@@ -41,17 +46,21 @@ namespace sdv {
 
 namespace {
 
-// The paged attention deals any lengths evenly and takes some 10 us more in launches; here a part is
-// a chain of slices, 1.2 us each for one row tile of 128 columns where little else runs.  Full tables of
-// 32 heads over 8 of 128, prefix of 1000, warps against paged attention: one sequence of one row,
-// 4000 positions 20 against 28 us, 8000 30 against 31, 16,000 49 against 37; of five rows 1000
-// 24 against 26, 2000 28 against 27, 8000 55 against 31.  With more sequences both are bound by
-// reading: eight of one row, 16,000 92 against 101, of five 104 against 111.  Several row groups read
-// everything several times: nine rows of 16 heads over 2 of 256, one sequence 2000 27 against 29,
-// 8000 54 against 34; sixteen 500 45 against 45, 1000 71 against 47 -- but where most of 24 such tables
-// stay empty (rows and positions half and a sixth of what they could be) 60 against 76.
-constexpr int kOwnChain = 300;  // positions of a part, one row tile of 128 columns, up to 16 units
-constexpr int kOwnMost = 2048;  // and at most, of a single long sequence
+// Positions of a table up to which this kernel is taken.  The paged attention deals any lengths evenly
+// and takes some 10 us more in launches; here a part is a chain of slices, 1.2 us each for 128
+// columns, and several row groups read everything several times.  Full tables of 32 heads over 8 of
+// 128 behind a prefix of 1000, this kernel against the paged attention, us a call: one sequence of
+// one row, 4000 positions 20 against 28, 8000 30 against 31, 16,000 49 against 37, eight of them
+// 16,000 92 against 101; five rows (two warps), one sequence 2000 23 against 27, 4000 31 against 29,
+// sixteen 2000 52 against 56, 4000 80 against 75; 16 rows (four warps), one 1000 22 against 26, 2000
+// 26 against 27, 64 of them 500 122 against 139, 1000 160 against 151.  Nine rows of 16 heads over 2 of
+// 256 (five row groups), one sequence 2000 27 against 29, sixteen 500 45 against 45, 1000 71
+// against 47 -- but where most of 24 such tables stay empty (rows and positions half and a sixth of
+// what they could be) 60 against 76.
+constexpr int kOwnMostOne = 4800;   // one warp, 128 columns, up to 16 cache heads of sequences; more by their number
+constexpr int kOwnMostTwo = 3000;   // two warps
+constexpr int kOwnMostFour = 1000;  // four, or several row groups
+constexpr int kOwnMost = 2048;      // of a part, of a single long sequence
 constexpr uint64_t kOwnDrainNs = 100000000ull;  // 0.1 s: copies under way at the end
 
 template <typename T>
@@ -91,11 +100,11 @@ constexpr int kSlice = 32;  // positions
 // Values of a slice from row `first` on: 0 in rows that are not there, and for what is not finite;
 // whether there was any of that.  (A loop of its own: what a warp does once a slice or once a part
 // is kept out of the straight code around it, whose instructions come late enough as it is.)
-template <typename T, int D>
-__device__ __forceinline__ bool own_clean(uint8_t* values, int first, uint32_t there, int lane) {
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ bool own_clean(uint8_t* values, int first, uint32_t there) {
   bool odd = false;
 #pragma unroll 1
-  for (int e = first * (D / 8) + lane; e < kSlice * (D / 8); e += 32) {
+  for (int e = first * (D / 8) + threadIdx.x; e < kSlice * (D / 8); e += 32 * WARPS) {
     const int row = e / (D / 8), ch = e % (D / 8);
     uint4* const at = reinterpret_cast<uint4*>(values + (ch >> 3) * (kSlice * 128) + row * 128 + (((ch ^ row) & 7) << 4));
     if (!(there >> row & 1u)) {
@@ -129,9 +138,9 @@ __device__ __noinline__ void own_mend(const AttnArgs& a, const int32_t* table, i
   }
 }
 
-template <int D, int MT>
+template <int D, int WARPS>
 struct OwnPlan {
-  static constexpr int R = 16 * MT;
+  static constexpr int R = 16 * WARPS;
   static constexpr int kHalf = kSlice * D * 2;    // a slice's keys, its values
   static constexpr int LQ = D * 2 + 64;           // bytes between query rows: eight lanes' 16-byte reads meet no bank twice
   static constexpr int kSmem = 1024 + 2 * kHalf + R * LQ + 16;
@@ -141,19 +150,32 @@ struct OwnMaps {
   CUtensorMap k, v;
 };
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(const __grid_constant__ OwnMaps maps,
-                                                                              const __grid_constant__ OwnArgs o) {
-  using PL = OwnPlan<D, MT>;
+// The CTA's warps, and whether the condition holds in all (one) of them.
+template <int WARPS>
+__device__ __forceinline__ bool all_of(bool x) {
+  if constexpr (WARPS > 1) return __syncthreads_and(x);
+  __syncwarp();
+  return x;
+}
+template <int WARPS>
+__device__ __forceinline__ bool one_of(bool x) {
+  if constexpr (WARPS > 1) return __syncthreads_or(x);
+  return __any_sync(0xffffffffu, x);
+}
+
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
+    prefix_own_kernel(const __grid_constant__ OwnMaps maps, const __grid_constant__ OwnArgs o) {
+  using PL = OwnPlan<D, WARPS>;
   constexpr int R = PL::R, DB = D / 64, KB = D / 32, LQ = PL::LQ, NT = kSlice / 8, BLOCK = kSlice * 128;
   constexpr float kLift = std::is_same<T, __nv_bfloat16>::value ? -kPrefixDrop : 6.f;  // P's power of two
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const sb = smem_raw + (base - raw);
-  uint8_t* const mem = sb + 2 * PL::kHalf;  // queries
-  const uint32_t bars = base + 2 * PL::kHalf + R * LQ;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* const mem = sb + 2 * PL::kHalf + warp * 16 * LQ;  // the warp's queries
+  const uint32_t bars = base + 2 * PL::kHalf + R * LQ;  // of the keys' place, then the values'
   const AttnArgs& a = o.attn;
-  const int lane = threadIdx.x, g = lane >> 2, c = lane & 3;
   // the prefix's parts first; of a sequence all first parts, then all second ones
   const int prefix_ctas = a.Hkv * o.prefix_parts, cta = (int)blockIdx.x - prefix_ctas;
   const bool shared = cta < 0;
@@ -177,24 +199,25 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
   const int per = own_per_part(seq.tiles, shared ? o.prefix_parts : o.parts);
   const int from = y * per * kOwnTile, to = min(from + per * kOwnTile, total);
   if (y > 0 && from >= total) return;
-  if (lane == 0) {
+  if (threadIdx.x == 0) {
     set_wait_limit(a.fault);
     mbar_init(bars, 1);
     mbar_init(bars + 8, 1);
     fence_barrier_init();
     if (seq.bad) atomicOr(o.status, kDevErrIndex);
   }
-  __syncwarp();
-  const int r0 = rg * R, rows = shared ? n * a.G : a.rows;
+  all_of<WARPS>(true);
+  const int r0 = rg * R + warp * 16, rows = shared ? n * a.G : a.rows;
   const int32_t* const table = shared ? o.prefix_table : a.table + (size_t)b * a.max_pages;
   // ---- the copies: slice i is positions from + 32 i .. + 31 ----
   const int page_log = 31 - __clz(a.page), box = min(a.page, kSlice), boxes = kSlice / box;
-  const int slices = r0 < n * a.G ? (to - from + kSlice - 1) / kSlice : 0;  // none for rows behind the window's end
+  const int slices = rg * R < n * a.G ? (to - from + kSlice - 1) / kSlice : 0;  // none for rows behind the window's end
+  const bool busy = WARPS == 1 || r0 < min(n * a.G, rows);  // whether the warp has a row (of a CTA with some)
   const int beyond = a.n_pages * a.Hkv * a.page;  // a row past the tensor map's end: zeros
   const uint64_t policy = l2_policy_evict_first();
   // a lane's copy: a block of 64 elements, a page's part of the slice
   const int cb = lane % DB, bx = lane / DB;
-  const bool mine = bx < boxes;
+  const bool mine = warp == 0 && bx < boxes;
   const uint32_t dst = base + cb * BLOCK + bx * box * 128;
   auto page_of = [&](int i) {  // of the lane's copy in slice i; -1 past the end
     const int p = from + kSlice * i + bx * box;
@@ -210,13 +233,13 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
     __syncwarp();
     if (mine) tma_load_2d(dst + values * PL::kHalf, values ? &maps.v : &maps.k, cb * 64, row, bars + 8u * values, policy);
   };
-  int row_now = beyond, row_next = beyond, id_after = page_of(1);
-  if (slices > 0) {
-    row_now = row_of(0, page_of(0));
-    issue(0, 0, row_now);
-    issue(0, 1, row_now);
+  int row_next = beyond, id_after = page_of(1);
+  if (slices > 0 && warp == 0) {
+    const int row = row_of(0, page_of(0));
+    issue(0, 0, row);
+    issue(0, 1, row);
   }
-  for (int e = lane; e < R * (D / 8); e += 32) {
+  for (int e = lane; e < 16 * (D / 8); e += 32) {
     const int r = e / (D / 8), ch = e % (D / 8), row = r0 + r;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (row < rows && row / a.G < n)
@@ -224,16 +247,14 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
                                                (h * a.G + row % a.G) * D) + ch);
     *reinterpret_cast<uint4*>(mem + r * LQ + ch * 16) = x;
   }
-  uint32_t words[MT][2];  // visibility of rows g and g + 8
+  uint32_t words[2];  // visibility of rows g and g + 8
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = r0 + t * 16 + half * 8 + g;
-      words[t][half] = row < rows && !shared ? attn_word(a, b, row / a.G, n) : 0u;
-    }
-  auto live = [&](int t, int half) {
-    const int row = r0 + t * 16 + half * 8 + g;
+  for (int half = 0; half < 2; ++half) {
+    const int row = r0 + half * 8 + g;
+    words[half] = row < rows && !shared ? attn_word(a, b, row / a.G, n) : 0u;
+  }
+  auto live = [&](int half) {
+    const int row = r0 + half * 8 + g;
     return row < rows && row / a.G < n;
   };
   // Pages of the part that cannot be followed make every slice look for them.
@@ -244,20 +265,15 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
       some_absent |= id < 0 || id >= a.n_pages;
     }
   some_absent = __any_sync(0xffffffffu, some_absent);
-  if (some_absent && lane == 0) atomicOr(o.status, kDevErrIndex);
+  if (some_absent && threadIdx.x == 0) atomicOr(o.status, kDevErrIndex);
   __syncwarp();
-  float out[MT][8 * DB][4];
-  float m[MT][2], l[MT][2];
+  float out[8 * DB][4];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   bool odd_values = false, ok = true, next_keys = false;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
+  for (int j = 0; j < 8 * DB; ++j)
 #pragma unroll
-    for (int j = 0; j < 8 * DB; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[t][j][e] = 0.f;
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e) out[j][e] = 0.f;
   // operands' places: key row g, value row 2 c, under the 128-byte swizzle
   const uint8_t* const ks = sb + g * 128;
   const uint8_t* const vs = sb + PL::kHalf + c * 256;
@@ -272,33 +288,30 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
     id_after = page_of(i + 2);
     next_keys = false;
     ok = mbar_wait_warp(bars, i & 1, o.status);
-    if (!ok) break;
     const bool edge = p0 + kSlice > ctx || some_absent;
-    float s[MT][NT][4];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][j][e] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      uint4 kx[NT];
+    float s[NT][4];
+    if (busy) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        kx[j] = *reinterpret_cast<const uint4*>(ks + (kb >> 1) * BLOCK + j * 1024 + k_chunk[kb & 1]);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(qs + t * 16 * LQ + kb * 64);
-        const uint4 hi = *reinterpret_cast<const uint4*>(qs + (t * 16 + 8) * LQ + kb * 64);
+        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma16816<T>(s[t][j], lo.x, hi.x, lo.y, hi.y, kx[j].x, kx[j].y);
+      for (int kb = 0; kb < KB; ++kb) {
+        uint4 kx[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma16816<T>(s[t][j], lo.z, hi.z, lo.w, hi.w, kx[j].z, kx[j].w);
+        for (int j = 0; j < NT; ++j)
+          kx[j] = *reinterpret_cast<const uint4*>(ks + (kb >> 1) * BLOCK + j * 1024 + k_chunk[kb & 1]);
+        const uint4 lo = *reinterpret_cast<const uint4*>(qs + kb * 64);
+        const uint4 hi = *reinterpret_cast<const uint4*>(qs + 8 * LQ + kb * 64);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816<T>(s[j], lo.x, hi.x, lo.y, hi.y, kx[j].x, kx[j].y);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816<T>(s[j], lo.z, hi.z, lo.w, hi.w, kx[j].z, kx[j].w);
       }
     }
-    __syncwarp();  // every lane has read the keys
-    if (more) issue(i + 1, 0, row_next);
+    ok = all_of<WARPS>(ok);  // every lane has read the keys
+    if (!ok) break;
+    if (more && warp == 0) issue(i + 1, 0, row_next);
     next_keys = more;
     uint32_t there = 0xffffffffu;  // positions that are there
     if (edge) {
@@ -309,16 +322,15 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
         there &= __ballot_sync(0xffffffffu, e >= 0 && e < a.n_pages);
       }
     }
-    uint32_t p16[MT][2][NT];  // packed pairs
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    uint32_t p16[2][NT];  // packed pairs
+    if (busy) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float x[2 * NT];
 #pragma unroll
-        for (int e = 0; e < 2 * NT; ++e) x[e] = s[t][e >> 1][half * 2 + (e & 1)] * a.scale_log2;
+        for (int e = 0; e < 2 * NT; ++e) x[e] = s[e >> 1][half * 2 + (e & 1)] * a.scale_log2;
         if (edge) {
-          const uint32_t see = live(t, half) ? there & attn_visible(p0, ctx, words[t][half]) : 0u;
+          const uint32_t see = live(half) ? there & attn_visible(p0, ctx, words[half]) : 0u;
 #pragma unroll
           for (int e = 0; e < 2 * NT; ++e)
             if (!(see >> ((e >> 1) * 8 + c * 2 + (e & 1)) & 1u)) x[e] = -INFINITY;
@@ -328,79 +340,76 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
         for (int e = 1; e < 2 * NT; ++e) mx = fmaxf(mx, x[e]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const bool grow = mx > m[t][half] + 8.f;  // also from -inf to any number
+        const bool grow = mx > m[half] + 8.f;  // also from -inf to any number
         if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow && m[t][half] != -INFINITY ? exp2_approx(m[t][half] - mx) : 1.f;
-          if (grow) m[t][half] = mx;
-          l[t][half] *= f;
+          const float f = grow && m[half] != -INFINITY ? exp2_approx(m[half] - mx) : 1.f;
+          if (grow) m[half] = mx;
+          l[half] *= f;
 #pragma unroll
           for (int j = 0; j < 8 * DB; ++j) {
-            out[t][j][half * 2] *= f;
-            out[t][j][half * 2 + 1] *= f;
+            out[j][half * 2] *= f;
+            out[j][half * 2 + 1] *= f;
           }
         }
-        const float ref = m[t][half] == -INFINITY ? -kLift : m[t][half] - kLift;
+        const float ref = m[half] == -INFINITY ? -kLift : m[half] - kLift;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 2 * NT; e += 2) {
           const float y0 = exp2_approx(x[e] - ref), y1 = exp2_approx(x[e + 1] - ref);
           sum += y0 + y1;
-          p16[t][half][e >> 1] = pack16<T>(y0, y1);
+          p16[half][e >> 1] = pack16<T>(y0, y1);
         }
-        l[t][half] += sum;
+        l[half] += sum;
       }
     }
     ok = mbar_wait_warp(bars + 8, i & 1, o.status);
-    if (!ok) break;
     if (edge && p0 + kSlice > ctx) {  // what is not finite must not meet a weight of 0
-      odd_values |= own_clean<T, D>(sb + PL::kHalf, max(ctx - p0, 0), there, lane);
+      odd_values |= own_clean<T, D, WARPS>(sb + PL::kHalf, max(ctx - p0, 0), there);
       fence_proxy_async_smem();  // before the next values' copy
-      __syncwarp();
+      all_of<WARPS>(true);
     }
+    if (busy) {
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {
-        uint4 vx[4];
+        for (int k = 0; k < NT / 2; ++k) {
+          uint4 vx[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int row = k * 16 + (z & 1) + (z >> 1) * 8;  // + 2 c
-          vx[z] = *reinterpret_cast<const uint4*>(vs + d * BLOCK + row * 128 + v_chunk[z & 1]);
+          for (int z = 0; z < 4; ++z) {
+            const int row = k * 16 + (z & 1) + (z >> 1) * 8;  // + 2 c
+            vx[z] = *reinterpret_cast<const uint4*>(vs + d * BLOCK + row * 128 + v_chunk[z & 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+            uint32_t v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] = reinterpret_cast<const uint32_t*>(&vx[z])[e >> 1];
+            const uint32_t b0 = __byte_perm(v[0], v[1], sel), b1 = __byte_perm(v[2], v[3], sel);
+            mma16816<T>(out[d * 8 + e], p16[0][2 * k], p16[1][2 * k], p16[0][2 * k + 1], p16[1][2 * k + 1], b0, b1);
+          }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
-          uint32_t v[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) v[z] = reinterpret_cast<const uint32_t*>(&vx[z])[e >> 1];
-          const uint32_t b0 = __byte_perm(v[0], v[1], sel), b1 = __byte_perm(v[2], v[3], sel);
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            mma16816<T>(out[t][d * 8 + e], p16[t][0][2 * k], p16[t][1][2 * k], p16[t][0][2 * k + 1],
-                        p16[t][1][2 * k + 1], b0, b1);
-        }
-      }
-    __syncwarp();  // every lane has read the values
-    if (more) issue(i + 1, 1, row_next);
+    }
+    ok = all_of<WARPS>(ok);  // every lane has read the values
+    if (!ok) break;
+    if (more && warp == 0) issue(i + 1, 1, row_next);
   }
   if (!ok) {  // the copies under way have to land before the CTA ends: this slice's, and the next keys
     if (i + 1 != a.fault.withhold) mbar_wait_bounded(bars, i & 1, kOwnDrainNs);
     mbar_wait_bounded(bars + 8, i & 1, kOwnDrainNs);
     if (next_keys && i + 2 != a.fault.withhold) mbar_wait_bounded(bars, (i + 1) & 1, kOwnDrainNs);
   }
-  odd_values = __any_sync(0xffffffffu, odd_values);
+  odd_values = one_of<WARPS>(odd_values);
   const size_t part = (size_t)y * a.B * a.S * a.Hq;
   float* const part_o = shared ? o.prefix_o : o.part_o;
   float2* const part_ml = shared ? o.prefix_ml : o.part_ml;
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
     for (int half = 0; half < 2; ++half) {
-      float sum = l[t][half];
+      float sum = l[half];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int row = r0 + t * 16 + half * 8 + g;
-      if (!live(t, half)) continue;  // (nor does the join read these)
+      const int row = r0 + half * 8 + g;
+      if (!live(half)) continue;  // (nor does the join read these)
       const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
       float* const dst = part_o + (part + orow) * D;
       // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
@@ -412,21 +421,21 @@ __global__ void __launch_bounds__(32, MT * D > 128 ? 8 : 12) prefix_own_kernel(c
         for (int e = 0; e < 16; e += 4) {  // a lane's 16 columns of a row lie side by side
           const int col = half * 2 + (e >> 3), j = d * 8 + (e & 7);
           const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : make_float4(out[t][j][col], out[t][j + 1][col], out[t][j + 2][col], out[t][j + 3][col]);
+                                : make_float4(out[j][col], out[j + 1][col], out[j + 2][col], out[j + 3][col]);
           finite &= fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY;
           *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) = y;
         }
       if (sum > 0.f && (odd_values || !finite))  // (NaN scores, a padding row's for one, leave NaN)
-        own_mend<T>(a, table, h, ctx, from, to, words[t][half], dst, c * 16, odd_values);
-      if (c == 0) part_ml[part + orow] = make_float2(m[t][half] == -INFINITY ? -INFINITY : m[t][half] - kLift, sum);
+        own_mend<T>(a, table, h, ctx, from, to, words[half], dst, c * 16, odd_values);
+      if (c == 0) part_ml[part + orow] = make_float2(m[half] == -INFINITY ? -INFINITY : m[half] - kLift, sum);
     }
   if (o.prefix_parts == 0) griddep_wait();
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int WARPS>
 cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
-  auto kernel = prefix_own_kernel<T, D, MT>;
-  constexpr int smem = OwnPlan<D, MT>::kSmem;
+  auto kernel = prefix_own_kernel<T, D, WARPS>;
+  constexpr int smem = OwnPlan<D, WARPS>::kSmem;
   static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -437,20 +446,18 @@ cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   const unsigned ctas = (unsigned)a.attn.Hkv * a.prefix_parts + (unsigned)a.attn.B * a.attn.Hkv * a.row_groups * a.parts;
-  return launch_pdl(kernel, dim3(ctas), dim3(32), smem, st, m, a);
+  return launch_pdl(kernel, dim3(ctas), dim3(32 * WARPS), smem, st, m, a);
 }
 
+template <typename T, int D>
+cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
+  return a.warps == 1 ? own_launch<T, D, 1>(m, a, st) : a.warps == 2 ? own_launch<T, D, 2>(m, a, st) : own_launch<T, D, 4>(m, a, st);
+}
 template <typename T>
 cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
-  switch (a.attn.D * 8 + a.row_tiles) {
-    case 64 * 8 + 1: return own_launch<T, 64, 1>(m, a, st);
-    case 64 * 8 + 2: return own_launch<T, 64, 2>(m, a, st);
-    case 64 * 8 + 4: return own_launch<T, 64, 4>(m, a, st);
-    case 128 * 8 + 1: return own_launch<T, 128, 1>(m, a, st);
-    case 128 * 8 + 2: return own_launch<T, 128, 2>(m, a, st);
-    case 256 * 8 + 1: return own_launch<T, 256, 1>(m, a, st);
-    default: return cudaErrorInvalidValue;
-  }
+  return a.attn.D == 64    ? own_dispatch<T, 64>(m, a, st)
+         : a.attn.D == 128 ? own_dispatch<T, 128>(m, a, st)
+                           : own_dispatch<T, 256>(m, a, st);
 }
 
 }  // namespace
@@ -458,14 +465,10 @@ cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
 bool own_takes(const OwnArgs& o) {
   const AttnArgs& a = o.attn;
   const long long positions = (long long)a.max_pages * a.page, units = (long long)a.B * a.Hkv;
-  const long long most = (long long)kOwnChain * (o.row_groups == 1 && units > 16 ? units : 16) / 16;
-  return positions <= (long long)kOwnMost * o.parts && positions * o.row_tiles * a.D <= most * 128 * o.parts;
-}
-
-// A row tile's outputs take dim / 2 registers of a thread.
-int own_row_tiles(int dim, int rows) {
-  const int most = 256 / dim, need = (rows + 15) / 16;
-  return need >= 4 && most >= 4 ? 4 : need >= 2 && most >= 2 ? 2 : 1;
+  const long long most = o.warps == 4 || o.row_groups > 1 ? kOwnMostFour
+                         : o.warps == 2                   ? kOwnMostTwo
+                                                          : kOwnMostOne * 128 / a.D * (units > 16 ? units : 16) / 16;
+  return positions <= most && positions <= (long long)kOwnMost * o.parts;
 }
 
 cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st) {

@@ -9,10 +9,10 @@ namespace sdv {
 constexpr int kOwnTile = 64;        // positions that a part is a whole number of
 constexpr int kOwnMaxParts = 16;
 
-// A sequence's own positions in parts of whole tiles, a CTA each (and the prefix's).
+// A sequence's own positions in parts of whole tiles, a CTA each for up to 64 rows (and the prefix's).
 struct OwnArgs {
   AttnArgs attn;      // tile = kOwnTile; out, lse and workspace fields of no meaning
-  int row_tiles;      // m16 row tiles of a CTA
+  int warps;          // of a CTA, 1, 2 or 4: 16 rows of a kv head each
   int row_groups;     // CTAs for all rows of a kv head
   int parts;          // of a sequence, at most
   float* part_o;      // [parts][B * S][Hq][D], relative to the part's maximum
@@ -36,7 +36,6 @@ __device__ __forceinline__ int own_live_parts(int tiles, int parts) {
 // Whether the positions that a table may hold are few enough for the parts (the shapes are those of
 // the tensor-core kernels, attn_tc_takes).
 bool own_takes(const OwnArgs& o);
-int own_row_tiles(int dim, int rows);
 cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st);
 
 }  // namespace sdv

@@ -384,3 +384,48 @@ def test_what_padding_rows_hold_before_few_rows(sdv):
         out, lse, ws = call(sdv, other, kp, vp, ptable, 400, table, ctx, n, None, 0.1)
         assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
         assert torch.equal(out, want) and torch.equal(lse, wl) and not out[1, 1].any()
+
+
+@pytest.mark.parametrize("S,d,page", [(5, 128, 16), (8, 64, 8), (9, 128, 32), (16, 64, 16), (16, 128, 128), (20, 64, 32)])
+def test_own_lengths_of_wide_windows(sdv, S, d, page):
+    """Windows of 20 to 80 rows a kv head, several warps to a sequence: lengths around the slices, parts and
+    pages, windows with rows left out, some of whole warps."""
+    ctx = [0, 1, 12, 27, 31, 32, 60, 64, 95, 128, 300]
+    n = [S - (3 * i) % (S + 1) for i in range(len(ctx))]
+    mask = words(np.random.default_rng(S), len(ctx), S)
+    q, kp, vp, ptable, table = make(F16, len(ctx), S, 8, 2, d, page, 40, ctx, n, d + page + S)
+    out, lse, ws = call(sdv, q, kp, vp, ptable, 40, table, ctx, n, as_i32(mask), 0.1)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    check(F16, reference(q, kp, vp, ptable, 40, table, ctx, n, mask, 0.1), out, lse, d)
+
+
+@pytest.mark.parametrize("S,d", [(6, 128), (6, 64), (12, 128), (16, 64)])
+def test_odd_values_and_absent_pages_of_wide_windows(sdv, S, d):
+    """As for narrow windows above: what is not finite reaches the rows that see it, whichever warp they are in."""
+    ctx, n = [20, 40, 0], [S, S, S - 1]
+    q, kp, vp, ptable, table = make(F16, 3, S, 8, 2, d, 16, 100, ctx, n, 33)
+    at = lambda b, p: (int(table[b, p // 16]), p % 16)  # noqa: E731
+    i = S - 2
+    page, slot = at(0, 20 + i)  # a window row that only the last two rows see
+    vp[page, 0, slot, 3], vp[page, 0, slot, 9] = float("inf"), float("nan")
+    page, slot = at(1, 5)       # a context position of sequence 1
+    vp[page, 1, slot, 4] = float("-inf")
+    out, _, ws = call(sdv, q, kp, vp, ptable, 100, table, ctx, n, None, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    out = out.float().cpu()
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[0, i:, :4, 3] = want[0, i:, :4, 9] = True
+    want[1, :, 4:, 4] = True
+    assert torch.equal(~torch.isfinite(out), want)
+    assert torch.isposinf(out[0, i:, :4, 3]).all() and torch.isneginf(out[1, :, 4:, 4]).all()
+    bad = table.clone()
+    bad[1, 1] = kp.shape[0] + 5
+    vp = torch.where(torch.isinf(vp), torch.zeros_like(vp), vp)
+    page, slot = at(0, 20 + i)
+    vp[page, 0, slot, 9] = 0.0
+    out, lse, ws = call(sdv, q, kp, vp, ptable, 100, bad, ctx, n, None, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_ERR_INVALID_ARG
+    short = table.clone()  # positions 16 .. 31 of sequence 1 are gone: pages 0 and 2 as its first two
+    short[1, 1:-1] = table[1, 2:]
+    ref = reference(q, kp, vp, ptable, 100, short, [20, 24, 0], n, None, d ** -0.5)
+    check(F16, ref, out, lse, d)

@@ -26,7 +26,9 @@ def sdv():
     (F16, 4, 1, 32, 8, 128, 16, 1201, 90),        # one row tile, few tiles
     (BF16, 64, 1, 32, 8, 128, 16, 9000, 300),     # two row tiles a unit
     (F16, 24, 9, 16, 2, 256, 64, 3000, 200),      # wide heads
-    (BF16, 33, 4, 8, 2, 64, 32, 700, 40)])        # an odd number of row tiles
+    (BF16, 33, 4, 8, 2, 64, 32, 700, 40),         # an odd number of row tiles
+    (F16, 6, 5, 32, 8, 128, 16, 500, 200),        # two warps for a sequence's own positions
+    (BF16, 4, 16, 16, 4, 64, 16, 500, 300)])      # four
 def test_timeout_reported_then_next_call_correct(sdv, dt, B, S, hq, hkv, d, page, prefix, ctx, stage):
     ctx, n = [ctx] * B, [S] * B
     made = [x.cuda() for x in att.make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, 70)]
