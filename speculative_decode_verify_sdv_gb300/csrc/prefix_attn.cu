@@ -197,13 +197,6 @@ cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st
 
 // ---- join -------------------------------------------------------------------------------
 
-struct JoinArgs {
-  PrefixArgs prefix;
-  OwnArgs own;           // parts > 0: its partials; else attn.out32 and attn.lse hold outputs
-  void* out;
-  float* lse;            // or null
-};
-
 // A row's softmax sums over some columns, partial by partial.
 template <int N>
 struct RowSum {
@@ -347,6 +340,12 @@ cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, int sms, cudaStream
 }
 
 constexpr int kSimplePerSm = 2;
+// Partials of a row that the own positions' kernel adds up itself, where it has all of a sequence's
+// positions in one part: no launch and no partials of its own for the join.  256 windows of five rows,
+// 32 heads over 8 of 128, up to 500 positions 121 us a call against 129, up to 1001 behind 16,384
+// 355 against 360; 199 of 20 rows, one position 36 against 41; 450 of one row, up to 60 41 against 40;
+// 256 of 16 rows, heads of 64, 50 against 52.  Heads of 256 have no registers for it (72 against 59).
+constexpr int kLastSharers = 4;
 // CTAs for the own positions, were all tables full (some end at once): per SM 16 of one warp (16, 24, 32,
 // 48: 64 sequences of up to 2001 positions 72.1, 71.3, 71.0, 73.1 us a call), 8 of more (8, 12, 16: 256
 // windows of five rows, up to 1001 positions, 361.8, 360.6, 361.7).
@@ -526,8 +525,9 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
     own.attn.tile = sdv::kOwnTile;
     own.part_ml = reinterpret_cast<float2*>(base + at.own_ml);
     own.part_o = reinterpret_cast<float*>(base + at.own_o);
-    const cudaError_t e2 = sdv::launch_prefix_own(cache->dtype, own, st);
-    if (e2 != cudaSuccess) return sdv::status_of(e2);
+    const bool last = own.prefix_parts == 0 && own.parts == 1 && a.D <= 128 && a.sharers <= sdv::kLastSharers;
+    const cudaError_t e2 = sdv::launch_prefix_own(cache->dtype, j, last, st);
+    if (e2 != cudaSuccess || last) return sdv::status_of(e2);
   } else {
     own.parts = 0;
     own.attn.out32 = reinterpret_cast<float*>(base + at.own_o);

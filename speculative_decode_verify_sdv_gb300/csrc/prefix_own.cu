@@ -163,9 +163,9 @@ __device__ __forceinline__ bool one_of(bool x) {
   return __any_sync(0xffffffffu, x);
 }
 
-template <typename T, int D, int WARPS>
+template <typename T, int D, int WARPS, bool LAST>
 __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
-    prefix_own_kernel(const __grid_constant__ OwnMaps maps, const __grid_constant__ OwnArgs o) {
+    prefix_own_kernel(const __grid_constant__ OwnMaps maps, const __grid_constant__ JoinArgs join) {
   using PL = OwnPlan<D, WARPS>;
   constexpr int R = PL::R, DB = D / 64, KB = D / 32, LQ = PL::LQ, NT = kSlice / 8, BLOCK = kSlice * 128;
   constexpr float kLift = std::is_same<T, __nv_bfloat16>::value ? -kPrefixDrop : 6.f;  // P's power of two
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   uint8_t* const mem = sb + 2 * PL::kHalf + warp * 16 * LQ;  // the warp's queries
   const uint32_t bars = base + 2 * PL::kHalf + R * LQ;  // of the keys' place, then the values'
+  const OwnArgs& o = join.own;
   const AttnArgs& a = o.attn;
   // the prefix's parts first; of a sequence all first parts, then all second ones
   const int prefix_ctas = a.Hkv * o.prefix_parts, cta = (int)blockIdx.x - prefix_ctas;
@@ -403,38 +404,108 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const size_t part = (size_t)y * a.B * a.S * a.Hq;
   float* const part_o = shared ? o.prefix_o : o.part_o;
   float2* const part_ml = shared ? o.prefix_ml : o.part_ml;
+  // with the join: where the prefix's partials of a row lie, after the launch in front has written them
+  const PrefixArgs& pre = join.prefix;
+  long long pre_total = 0;
+  int pre_tiles = 0, pre_live = 0;
+  if constexpr (LAST) {
+    bool bad;  // (reported by that launch)
+    pre_tiles = prefix_tiles(pre, prefix_length(pre, bad));
+    pre_total = (long long)pre_tiles * pre.units;
+    pre_live = attn_live_ctas(pre.ctas, pre_total);
+    griddep_wait();
+  }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float sum = l[half];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int row = r0 + half * 8 + g;
-      if (!live(half)) continue;  // (nor does the join read these)
-      const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
-      float* const dst = part_o + (part + orow) * D;
-      // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
-      const bool none = sum == 0.f;
-      bool finite = true;
+  for (int half = 0; half < 2; ++half) {
+    float sum = l[half];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const int row = r0 + half * 8 + g;
+    if (LAST ? row >= rows : !live(half)) continue;  // (nor does the join read these)
+    const long long orow = ((long long)b * a.S + row / a.G) * a.Hq + h * a.G + row % a.G;
+    float* const dst = part_o + (part + orow) * D;
+    // (a row that saw nothing has weights 0 only: its O is 0, or NaN by 0 * inf)
+    const bool none = sum == 0.f;
+    float top = m[half] == -INFINITY || none ? -INFINITY : m[half] - kLift;
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < 8 * DB; ++e)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if (none) out[e][half * 2 + z] = 0.f;
+        finite &= fabsf(out[e][half * 2 + z]) < INFINITY;
+      }
+    const bool odd = sum > 0.f && (odd_values || !finite);  // (NaN scores, a padding row's for one, leave NaN)
+    if (!LAST || (odd && live(half))) {
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {  // a lane's 16 columns of a row lie side by side
           const int col = half * 2 + (e >> 3), j = d * 8 + (e & 7);
-          const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : make_float4(out[j][col], out[j + 1][col], out[j + 2][col], out[j + 3][col]);
-          finite &= fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY;
-          *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) = y;
+          *reinterpret_cast<float4*>(dst + d * 64 + c * 16 + e) =
+              make_float4(out[j][col], out[j + 1][col], out[j + 2][col], out[j + 3][col]);
         }
-      if (sum > 0.f && (odd_values || !finite))  // (NaN scores, a padding row's for one, leave NaN)
-        own_mend<T>(a, table, h, ctx, from, to, words[half], dst, c * 16, odd_values);
-      if (c == 0) part_ml[part + orow] = make_float2(m[half] == -INFINITY ? -INFINITY : m[half] - kLift, sum);
+      if (odd) own_mend<T>(a, table, h, ctx, from, to, words[half], dst, c * 16, odd_values);
     }
-  if (o.prefix_parts == 0) griddep_wait();
+    if constexpr (!LAST) {
+      if (c == 0) part_ml[part + orow] = make_float2(top, sum);
+    } else {
+      if (odd && live(half)) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) out[d * 8 + (e & 7)][half * 2 + (e >> 3)] = dst[d * 64 + c * 16 + e];
+      }
+      const int at = (b * a.S + row / a.G) * a.G + row % a.G;  // among all rows of the kv head
+      const int rt = at / pre.row_tile, r = at - rt * pre.row_tile;
+      const int unit = h * ((pre.row_tiles + pre.unit_tiles - 1) / pre.unit_tiles) + rt / pre.unit_tiles;
+      const long long first = (long long)unit * pre_tiles;
+      const int count = live(half) && pre_tiles > 0 ? attn_owner(pre_total, pre_live, first + pre_tiles - 1) -
+                                                          attn_owner(pre_total, pre_live, first) + 1
+                                                    : 0;
+      const long long step = (long long)pre.unit_tiles * pre.row_tile;
+      const long long place = ((long long)unit * pre.sharers * pre.unit_tiles + rt % pre.unit_tiles) * pre.row_tile + r;
+#pragma unroll 1
+      for (int k = 0; k < count; ++k) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(pre.part_ml) + place + k * step);
+        const float4* const po = reinterpret_cast<const float4*>(pre.part_o + (place + k * step) * D) + c * 4;
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float mn = fmaxf(top, ml.x), f = exp2f(top - mn), f2 = exp2f(ml.x - mn);
+        top = mn;
+        sum = sum * f + ml.y * f2;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 x = __ldcg(po + d * 16 + e / 4);
+            const int col = half * 2 + (e >> 3), j = d * 8 + (e & 7);
+            out[j][col] = weighted<true>(out[j][col], f) + weighted<true>(x.x, f2);
+            out[j + 1][col] = weighted<true>(out[j + 1][col], f) + weighted<true>(x.y, f2);
+            out[j + 2][col] = weighted<true>(out[j + 2][col], f) + weighted<true>(x.z, f2);
+            out[j + 3][col] = weighted<true>(out[j + 3][col], f) + weighted<true>(x.w, f2);
+          }
+      }
+      const bool empty = !live(half) || sum == 0.f;
+      const float inv = 1.f / sum;
+      uint4* const to16 = reinterpret_cast<uint4*>(static_cast<T*>(join.out) + orow * D) + c * 2;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int col = half * 2 + z;
+          auto two = [&](int e) { return empty ? 0u : pack16<T>(out[d * 8 + e][col] * inv, out[d * 8 + e + 1][col] * inv); };
+          to16[d * 8 + z] = make_uint4(two(0), two(2), two(4), two(6));
+        }
+      if (c == 0 && join.lse != nullptr)
+        join.lse[orow] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+  if (!LAST && o.prefix_parts == 0) griddep_wait();
 }
 
-template <typename T, int D, int WARPS>
-cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
-  auto kernel = prefix_own_kernel<T, D, WARPS>;
+template <typename T, int D, int WARPS, bool LAST>
+cudaError_t own_launch(const OwnMaps& m, const JoinArgs& j, cudaStream_t st) {
+  auto kernel = prefix_own_kernel<T, D, WARPS, LAST>;
   constexpr int smem = OwnPlan<D, WARPS>::kSmem;
   static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
   int dev = 0;
@@ -445,19 +516,29 @@ cudaError_t own_launch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
+  const OwnArgs& a = j.own;
   const unsigned ctas = (unsigned)a.attn.Hkv * a.prefix_parts + (unsigned)a.attn.B * a.attn.Hkv * a.row_groups * a.parts;
-  return launch_pdl(kernel, dim3(ctas), dim3(32 * WARPS), smem, st, m, a);
+  return launch_pdl(kernel, dim3(ctas), dim3(32 * WARPS), smem, st, m, j);
 }
 
-template <typename T, int D>
-cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
-  return a.warps == 1 ? own_launch<T, D, 1>(m, a, st) : a.warps == 2 ? own_launch<T, D, 2>(m, a, st) : own_launch<T, D, 4>(m, a, st);
+template <typename T, int D, int WARPS>
+cudaError_t own_dispatch(const OwnMaps& m, const JoinArgs& j, bool last, cudaStream_t st) {
+  if constexpr (D <= 128)
+    if (last) return own_launch<T, D, WARPS, true>(m, j, st);
+  return own_launch<T, D, WARPS, false>(m, j, st);
 }
 template <typename T>
-cudaError_t own_dispatch(const OwnMaps& m, const OwnArgs& a, cudaStream_t st) {
-  return a.attn.D == 64    ? own_dispatch<T, 64>(m, a, st)
-         : a.attn.D == 128 ? own_dispatch<T, 128>(m, a, st)
-                           : own_dispatch<T, 256>(m, a, st);
+cudaError_t own_dispatch(const OwnMaps& m, const JoinArgs& j, bool last, cudaStream_t st) {
+  switch (j.own.attn.D + j.own.warps) {  // (heads of 256 have one warp)
+    case 64 + 1: return own_dispatch<T, 64, 1>(m, j, last, st);
+    case 64 + 2: return own_dispatch<T, 64, 2>(m, j, last, st);
+    case 64 + 4: return own_dispatch<T, 64, 4>(m, j, last, st);
+    case 128 + 1: return own_dispatch<T, 128, 1>(m, j, last, st);
+    case 128 + 2: return own_dispatch<T, 128, 2>(m, j, last, st);
+    case 128 + 4: return own_dispatch<T, 128, 4>(m, j, last, st);
+    case 256 + 1: return own_dispatch<T, 256, 1>(m, j, last, st);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
@@ -471,15 +552,15 @@ bool own_takes(const OwnArgs& o) {
   return positions <= most && positions <= (long long)kOwnMost * o.parts;
 }
 
-cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st) {
+cudaError_t launch_prefix_own(int dtype, const JoinArgs& j, bool last, cudaStream_t st) {
   OwnMaps m;
-  const AttnArgs& t = a.attn;
+  const AttnArgs& t = j.own.attn;
   const uint64_t rows = (uint64_t)t.n_pages * t.Hkv * t.page;
   const int box = t.page < kSlice ? t.page : kSlice;
   const bool bf = dtype == SDV_BF16;
   if (!attn_page_map(t.k, bf, rows, t.D, box, &m.k) || !attn_page_map(t.v, bf, rows, t.D, box, &m.v))
     return cudaErrorUnknown;
-  return bf ? own_dispatch<__nv_bfloat16>(m, a, st) : own_dispatch<__half>(m, a, st);
+  return bf ? own_dispatch<__nv_bfloat16>(m, j, last, st) : own_dispatch<__half>(m, j, last, st);
 }
 
 }  // namespace sdv

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attn_sched.cuh"
+#include "prefix_attn.cuh"
 
 namespace sdv {
 
@@ -26,6 +27,13 @@ struct OwnArgs {
   float2* prefix_ml;
 };
 
+struct JoinArgs {
+  PrefixArgs prefix;
+  OwnArgs own;           // parts > 0: its partials; else attn.out32 and attn.lse hold outputs
+  void* out;
+  float* lse;            // or null
+};
+
 // Tiles of each part of a sequence but the last, and how many parts have any.
 __device__ __forceinline__ int own_per_part(int tiles, int parts) { return (tiles + parts - 1) / parts; }
 __device__ __forceinline__ int own_live_parts(int tiles, int parts) {
@@ -36,6 +44,8 @@ __device__ __forceinline__ int own_live_parts(int tiles, int parts) {
 // Whether the positions that a table may hold are few enough for the parts (the shapes are those of
 // the tensor-core kernels, attn_tc_takes).
 bool own_takes(const OwnArgs& o);
-cudaError_t launch_prefix_own(int dtype, const OwnArgs& a, cudaStream_t st);
+// last: the own positions, of a single part each, are joined with the prefix's partials here (heads
+// of up to 128).
+cudaError_t launch_prefix_own(int dtype, const JoinArgs& j, bool last, cudaStream_t st);
 
 }  // namespace sdv

@@ -429,3 +429,50 @@ def test_odd_values_and_absent_pages_of_wide_windows(sdv, S, d):
     short[1, 1:-1] = table[1, 2:]
     ref = reference(q, kp, vp, ptable, 100, short, [20, 24, 0], n, None, d ** -0.5)
     check(F16, ref, out, lse, d)
+
+
+MANY = [  # so many rows that the prefix's partials of a row are few, tables of one tile: joined on the spot
+    (F16, 450, 1, 32, 8, 128, 16, 200, False),
+    (BF16, 60, 8, 32, 8, 128, 32, 129, True),
+    (F16, 32, 16, 32, 8, 64, 8, 300, True),
+    (F16, 200, 2, 16, 8, 256, 16, 65, False),
+    (BF16, 230, 2, 32, 8, 64, 64, 0, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows_and_short_tables(sdv, case):
+    dt, B, S, hq, hkv, d, page, prefix, masked = MANY[case]
+    n = [S - (5 * i) % (S + 1) for i in range(B)]
+    ctx = [min((11 * i) % 64, 64 - n[i]) for i in range(B)]
+    q, kp, vp, ptable, table = make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, 50 + case)
+    mask = words(np.random.default_rng(case), B, S) if masked else None
+    im = None if mask is None else as_i32(mask)
+    out, lse, ws = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, im, d ** -0.5)
+    assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+    check(dt, reference(q, kp, vp, ptable, prefix, table, ctx, n, mask, d ** -0.5), out, lse, d)
+    out2, _, _ = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, im, d ** -0.5, want_lse=False, ws=ws)
+    assert torch.equal(out2, out)
+    # what is not finite: in the prefix (all live rows of its head), in a context, in a window row
+    want = torch.zeros(out.shape, dtype=torch.bool)
+    b = next(i for i in range(B) if ctx[i] > 3 and n[i] > 0)
+    group = hq // hkv
+    if prefix:
+        vp[int(ptable[0]), 1, 3 % min(page, prefix), 5] = float("inf")
+        for i in range(B):
+            want[i, :n[i], group:2 * group, 5] = True
+    vp[int(table[b, 2 // page]), 0, 2 % page, 7] = float("nan")
+    want[b, :n[b], :group, 7] = True
+    if not masked:
+        at = ctx[b] + n[b] - 1
+        vp[int(table[b, at // page]), 2, at % page, 9] = float("-inf")
+        want[b, n[b] - 1, 2 * group:3 * group, 9] = True
+    odd, _, _ = call(sdv, q, kp, vp, ptable, prefix, table, ctx, n, im, d ** -0.5, ws=ws)
+    odd = odd.float().cpu()
+    assert torch.equal(~torch.isfinite(odd), want)
+    assert torch.isnan(odd[b, :n[b], :group, 7]).all()
+    if prefix:
+        assert all(torch.isposinf(odd[i, :n[i], group:2 * group, 5]).all() for i in range(B))
+    if not masked:
+        assert torch.isneginf(odd[b, n[b] - 1, 2 * group:3 * group, 9]).all()
+    assert torch.equal(odd[~want], out.float().cpu()[~want])
