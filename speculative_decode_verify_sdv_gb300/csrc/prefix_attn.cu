@@ -7,7 +7,7 @@
 // The query rows of all sequences stand side by side as the rows of one product with the
 // prefix, which is so read once, not once a sequence; the own caches go through a kernel of their
 // own (prefix_own.cu), or, where they may be long, through the paged attention, which deals any
-// lengths evenly and leaves fp32 outputs here; the join adds them all.
+// lengths evenly and leaves fp32 outputs here; the join adds them all, or the own positions' kernel does.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
