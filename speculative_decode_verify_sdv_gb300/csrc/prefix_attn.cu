@@ -1,6 +1,6 @@
 // Attention of a batch over a prefix that its sequences share, computed once for all, and each
-// sequence's own cache (sdv_prefix_attn): the prefix on the CUDA cores for shapes that the
-// tensor-core kernel does not take, the join, and the entry point.
+// sequence's own cache (sdv_prefix_attn): the prefix for head and page sizes that the tcgen05
+// kernel does not take, the join, and the entry point.
 //
 // Per query row, with the prefix's positions in parts j and the row's own positions:
 //   M = max m_j;  out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j;  lse = M + log sum.
@@ -34,7 +34,7 @@ namespace {
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// ---- the prefix on the CUDA cores -------------------------------------------------------
+// ---- the prefix for any head and page size ----------------------------------------------
 
 // What is not finite in column d of the values from position `from` to `to` - 1.
 template <typename T>
@@ -49,22 +49,41 @@ __device__ __noinline__ uint32_t prefix_odd(const PrefixArgs& a, int h, int from
   return odd;
 }
 
-// One CTA walks its range of tiles with 8 query rows per tile, as the paged attention's does:
-// 32 positions at a time through shared memory, two rows' maximum and sum in a warp, up to two
-// columns of all rows' outputs in a thread.  Weights carry a factor 2^-kPrefixDrop, so that the sums
-// of 2^24 values near the largest number stay numbers.
+// Outputs of a row, two columns of every eight from `first` on, once more where they are not finite.
 template <typename T>
-__global__ void __launch_bounds__(128) prefix_simple_kernel(const __grid_constant__ PrefixArgs a) {
-  constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile;
-  extern __shared__ float sm[];
-  const int D = a.D, ld = D + 1;
-  float* const qs = sm;                    // [R][D]
-  float* const ks = qs + R * D;            // [P][D + 1]
-  float* const vs = ks + P * ld;           // [P][D]
-  float* const ps = vs + P * D;            // [R][P] weights
-  float* const al = ps + R * P;            // [R] factor of the old sum and output
-  __shared__ bool gone[P];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__device__ __noinline__ void prefix_mend(const PrefixArgs& a, int h, int from, int to, float* row, int first) {
+  for (int d = first; d < a.D; d += d & 1 ? 7 : 1) {
+    if (fabsf(row[d]) < INFINITY) continue;
+    const uint32_t odd = prefix_odd<T>(a, h, from, to, d);
+    if (odd) row[d] = odd_value(odd);
+  }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+
+// Any head size and any page size.  One CTA walks its range of tiles with 64 query rows, 16 a warp:
+// 32 positions at a time, the next ones on their way, by m16n8k16 MMAs out of rows that are padded so
+// that eight of them meet no bank twice.  NB: blocks of eight columns, at least as many as a head has.
+// 64 rows of 32 heads over 8 of 96, 8192 positions and 100 of their own 240 us a call (by the CUDA cores
+// 3218), eight rows 72 (315); copies a position a warp and two barriers for 32 positions bound it.
+template <typename T, int NB>
+__global__ void __launch_bounds__(128, 2) prefix_simple_kernel(const __grid_constant__ PrefixArgs a) {
+  constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile, NT = P / 8;
+  constexpr float kLift = std::is_same<T, __nv_bfloat16>::value ? -kPrefixDrop : 6.f;  // P's power of two
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int D = a.D, chunks = D / 8, steps = (D + 15) / 16, ld = steps * 16 + 8;  // elements between rows
+  T* const qs = reinterpret_cast<T*>(smem_raw);  // [R][ld]
+  T* const ks = qs + R * ld;                     // [2][P][ld]
+  T* const vs = ks + 2 * P * ld;                 // [2][P][ld]
+  __shared__ bool gone[2][P];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
   bool bad;
@@ -72,127 +91,170 @@ __global__ void __launch_bounds__(128) prefix_simple_kernel(const __grid_constan
   if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, kDevErrIndex);
   PrefixWalk w;
   if (!w.start(a, length, blockIdx.x)) return;
+  for (int e = tid; e < (R + 4 * P) * ld / 8; e += 128) reinterpret_cast<uint4*>(smem_raw)[e] = make_uint4(0, 0, 0, 0);
+  // The copies of a tile: a position a warp, 16 bytes a lane.
+  auto copy = [&](int h, int t, int buf) {
+#pragma unroll
+    for (int i = 0; i < P / 4; ++i) {
+      const int j = warp + 4 * i, p = t * P + j;
+      int id = -1;
+      if (p < length) {
+        id = __ldg(a.table + p / a.page);
+        if (id < 0 || id >= a.n_pages) {
+          if (lane == 0) atomicOr(a.status, kDevErrIndex);
+          id = -1;
+        }
+      }
+      if (lane == 0) gone[buf][j] = id < 0;
+      if (lane < chunks) {
+        const long long at = id < 0 ? 0 : (((long long)id * a.Hkv + h) * a.page + p % a.page) * D + lane * 8;
+        const int to = (buf * P + j) * ld + lane * 8;
+        cp_async16(smem_addr(ks + to), static_cast<const T*>(a.k) + at, id >= 0);
+        cp_async16(smem_addr(vs + to), static_cast<const T*>(a.v) + at, id >= 0);
+      }
+    }
+    cp_async_commit();
+  };
   while (w.more()) {
     const int count = w.segment();
     const int h = w.unit / a.row_tiles, r0 = (w.unit % a.row_tiles) * a.row_tile;
     const int nr = min(a.row_tile, a.tokens * a.G - r0);
     __syncthreads();
-    for (int e = tid; e < R * D; e += 128) {
-      const int r = e / D, row = r0 + r;
-      float x = 0.f;
+    for (int e = tid; e < R * chunks; e += 128) {
+      const int r = e / chunks, ch = e - r * chunks, row = r0 + r;
+      uint4 x = make_uint4(0, 0, 0, 0);
       if (r < nr)
-        x = to_float(static_cast<const T*>(a.q)[(long long)(row / a.G) * a.q_stride + (h * a.G + row % a.G) * D + e % D]);
-      qs[e] = x;
+        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(row / a.G) * a.q_stride +
+                                                 (h * a.G + row % a.G) * D) + ch);
+      *reinterpret_cast<uint4*>(qs + r * ld + ch * 8) = x;
     }
-    float o[2][R], m[2], l[2];
+    float out[NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r) o[0][r] = o[1][r] = 0.f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
-    for (int t = w.tile; t < w.tile + count; ++t) {
-      const int p0 = t * P;
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[n][e] = 0.f;
+    const bool busy = warp * 16 < nr;
+    copy(h, w.tile, 0);
+    for (int i = 0; i < count; ++i) {
+      const int buf = i & 1;
+      if (i + 1 < count) copy(h, w.tile + i + 1, buf ^ 1);
+      else cp_async_commit();
+      cp_async_wait<1>();
       __syncthreads();
-      for (int j = warp; j < P; j += 4) {  // a position per warp
-        const int p = p0 + j;
-        int id = -1;
-        if (p < length) {
-          id = __ldg(a.table + p / a.page);
-          if (id < 0 || id >= a.n_pages) {
-            if (lane == 0) atomicOr(a.status, kDevErrIndex);
-            id = -1;
-          }
-        }
-        const long long at = (((long long)id * a.Hkv + h) * a.page + p % a.page) * D;
-        for (int d = lane; d < D; d += 32) {
-          ks[j * ld + d] = id < 0 ? 0.f : to_float(static_cast<const T*>(a.k)[at + d]);
-          vs[j * D + d] = id < 0 ? 0.f : to_float(static_cast<const T*>(a.v)[at + d]);
-        }
-        if (lane == 0) gone[j] = id < 0;
-      }
-      __syncthreads();
+      if (busy) {
+        const T* const k0 = ks + (buf * P + g) * ld + 2 * c;
+        const T* const q0 = qs + (warp * 16 + g) * ld + 2 * c;
+        auto word = [](const T* p) { return *reinterpret_cast<const uint32_t*>(p); };
+        float s[NT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // warp's rows 2 warp + i, lane = position
-        const int r = 2 * warp + i;
-        const bool see = !gone[lane] && r < nr;
-        float s = -INFINITY;
-        if (see) {
-          s = 0.f;
-#pragma unroll 4
-          for (int d = 0; d < D; ++d) s = fmaf(qs[r * D + d], ks[lane * ld + d], s);
-          s *= a.scale_log2;
-        }
-        float mx = s;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(m[i], mx);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float e = see ? exp2f(s - ref - kPrefixDrop) : -0.f;
-        const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - ref);
-        float sum = e;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l[i] = l[i] * f + sum;
-        m[i] = mn;
-        ps[r * P + lane] = e;
-        if (lane == 0) al[r] = f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int d = tid + 128 * c;
-        if (d >= D) continue;
-#pragma unroll
-        for (int r = 0; r < R; ++r) o[c][r] *= al[r];
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll 2
-        for (int j = 0; j < P; ++j) {
-          const float x = vs[j * D + d];
+        for (int k = 0; k < steps; ++k) {
+          const T* const q = q0 + k * 16;
+          const uint32_t a0 = word(q), a1 = word(q + 8 * ld), a2 = word(q + 8), a3 = word(q + 8 * ld + 8);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float e = ps[r * P + j];
-            if (__float_as_uint(e) != 0x80000000u) o[c][r] = fmaf(e, x, o[c][r]);
+          for (int n = 0; n < NT; ++n) {
+            const T* const x = k0 + n * 8 * ld + k * 16;
+            mma16816<T>(s[n], a0, a1, a2, a3, word(x), word(x + 8));
+          }
+        }
+        const uint32_t there = ~__ballot_sync(0xffffffffu, gone[buf][lane]);
+        uint32_t p16[2][NT];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[2 * NT];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 2 * NT; ++e) {
+            const bool see = there >> ((e >> 1) * 8 + c * 2 + (e & 1)) & 1u;
+            x[e] = see ? s[e >> 1][half * 2 + (e & 1)] * a.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, x[e]);
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const bool grow = mx > m[half] + 8.f;  // also from -inf to any number
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow && m[half] != -INFINITY ? exp2f(m[half] - mx) : 1.f;
+            if (grow) m[half] = mx;
+            l[half] *= f;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              out[n][half * 2] *= f;
+              out[n][half * 2 + 1] *= f;
+            }
+          }
+          const float ref = m[half] == -INFINITY ? -kLift : m[half] - kLift;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2 * NT; e += 2) {
+            const float y0 = exp2f(x[e] - ref), y1 = exp2f(x[e + 1] - ref);
+            sum += y0 + y1;
+            p16[half][e >> 1] = pack16<T>(y0, y1);
+          }
+          l[half] += sum;
+        }
+        // lane's row of the four 8 x 8 blocks: 16 positions by 16 columns
+        const uint32_t v0 = smem_addr(vs + (buf * P + (lane & 15)) * ld + (lane >> 4) * 8);
+#pragma unroll
+        for (int n = 0; n < NB; n += 2) {
+          if (n >= chunks) break;
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, v0 + (k * 16 * ld + n * 8) * 2);
+            mma16816<T>(out[n], p16[0][2 * k], p16[1][2 * k], p16[0][2 * k + 1], p16[1][2 * k + 1], b[0], b[1]);
+            mma16816<T>(out[n + 1], p16[0][2 * k], p16[1][2 * k], p16[0][2 * k + 1], p16[1][2 * k + 1], b[2], b[3]);
           }
         }
       }
+      __syncthreads();  // everyone has read the tile
     }
-    __syncthreads();
-    if (lane < 2) {  // the rows' statistics for the columns' threads
-      ps[2 * warp + lane] = (lane == 0 ? m[0] : m[1]) + kPrefixDrop;
-      al[2 * warp + lane] = lane == 0 ? l[0] : l[1];
-    }
-    __syncthreads();
     const size_t place = (size_t)w.unit * a.sharers + w.place(blockIdx.x);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= nr) break;
+    for (int half = 0; half < 2; ++half) {
+      float sum = l[half];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int r = warp * 16 + half * 8 + g;
+      if (r >= nr) continue;
+      float* const row = a.part_o + (place * a.row_tile + r) * D;
+      bool finite = true;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int d = tid + 128 * c;
-        if (d >= D) continue;
-        if (!(fabsf(o[c][r]) < INFINITY) && al[r] > 0.f) {  // a weight of 0 times an infinity, or a value's own
-          const uint32_t odd = prefix_odd<T>(a, h, w.tile * P, min((w.tile + count) * P, length), d);
-          if (odd) o[c][r] = odd_value(odd);
-        }
-        a.part_o[(place * a.row_tile + r) * D + d] = o[c][r];
+      for (int n = 0; n < NB; ++n) {
+        if (n >= chunks) break;
+        const float2 y = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(out[n][half * 2], out[n][half * 2 + 1]);
+        finite &= fabsf(y.x) + fabsf(y.y) < INFINITY;
+        *reinterpret_cast<float2*>(row + n * 8 + 2 * c) = y;
       }
-      if (tid == 0)
-        *reinterpret_cast<float2*>(a.part_ml + (place * a.row_tile + r) * 2) = make_float2(ps[r], al[r]);
+      // (a weight of 0 times an infinity, or a value's own; NaN scores leave NaN)
+      if (!finite && sum > 0.f) prefix_mend<T>(a, h, w.tile * P, min((w.tile + count) * P, length), row, 2 * c);
+      if (c == 0)
+        *reinterpret_cast<float2*>(a.part_ml + (place * a.row_tile + r) * 2) =
+            make_float2(m[half] == -INFINITY ? -INFINITY : m[half] - kLift, sum);
     }
     w.advance(count);
   }
 }
 
-int simple_smem(int D) {
-  constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile;
-  return (R * D + P * (D + 1) + P * D + R * P + R) * 4;
-}
-
-cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st) {
-  auto kernel = dtype == SDV_F16 ? prefix_simple_kernel<__half> : prefix_simple_kernel<__nv_bfloat16>;
-  const int smem = simple_smem(a.D);
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int NB>
+cudaError_t simple_launch(const PrefixArgs& a, cudaStream_t st) {
+  auto kernel = prefix_simple_kernel<T, NB>;
+  const int smem = (kPrefixSimpleRows + 4 * kPrefixSimpleTile) * ((a.D + 15) / 16 * 16 + 8) * 2;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(a.ctas), dim3(128), smem, st, a);
+}
+template <typename T>
+cudaError_t simple_dispatch(const PrefixArgs& a, cudaStream_t st) {
+  return a.D <= 64    ? simple_launch<T, 8>(a, st)
+         : a.D <= 128 ? simple_launch<T, 16>(a, st)
+                      : simple_launch<T, 32>(a, st);
+}
+cudaError_t launch_prefix_simple(int dtype, const PrefixArgs& a, cudaStream_t st) {
+  return dtype == SDV_F16 ? simple_dispatch<__half>(a, st) : simple_dispatch<__nv_bfloat16>(a, st);
 }
 
 // ---- join -------------------------------------------------------------------------------

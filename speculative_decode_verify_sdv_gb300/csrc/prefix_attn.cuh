@@ -7,8 +7,12 @@
 // lives on the device; the split is a function of it and the shapes.
 #pragma once
 
-#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
 
 #include "attn_sched.cuh"
 #include "mixing.h"
@@ -82,8 +86,25 @@ struct PrefixWalk {
   __device__ __forceinline__ int place(int cta) const { return cta - attn_owner(total, live, (long long)unit * tiles); }
 };
 
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 constexpr float kPrefixDrop = 24.f;    // bits by which weights are lowered where the type has the range for it
-constexpr int kPrefixSimpleRows = 8;   // rows per tile of the CUDA-core kernel
+constexpr int kPrefixSimpleRows = 64;  // rows per tile of the kernel for any head and page size
 constexpr int kPrefixSimpleTile = 32;  // positions per tile of it
 
 }  // namespace sdv

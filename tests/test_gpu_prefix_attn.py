@@ -476,3 +476,15 @@ def test_many_rows_and_short_tables(sdv, case):
     if not masked:
         assert torch.isneginf(odd[b, n[b] - 1, 2 * group:3 * group, 9]).all()
     assert torch.equal(odd[~want], out.float().cpu()[~want])
+
+
+@pytest.mark.parametrize("dt,B,S,hq,hkv,d,page,prefix", [
+    (F16, 5, 3, 8, 2, 80, 16, 333), (BF16, 9, 4, 12, 3, 112, 24, 129), (F16, 40, 2, 8, 1, 72, 5, 95), (BF16, 3, 1, 4, 4, 8, 16, 31),
+    (F16, 30, 5, 6, 2, 192, 16, 200), (BF16, 70, 1, 16, 2, 136, 3, 64), (F16, 2, 32, 9, 1, 24, 1, 33), (BF16, 17, 2, 200, 2, 64, 16, 65)])
+def test_other_head_and_page_sizes(sdv, dt, B, S, hq, hkv, d, page, prefix):
+    ctx, n = [(7 * i) % 40 for i in range(B)], [S - i % (S + 1) for i in range(B)]
+    q, kp, vp, ptable, table = make(dt, B, S, hq, hkv, d, page, prefix, ctx, n, d)
+    for length in (prefix, max(prefix - page, 0)):
+        out, lse, ws = call(sdv, q, kp, vp, ptable, length, table, ctx, n, None, d ** -0.5)
+        assert sdv.sdv_last_device_status(ws) == sdv.SDV_OK
+        check(dt, reference(q, kp, vp, ptable, length, table, ctx, n, None, d ** -0.5), out, lse, d)
