@@ -77,9 +77,9 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(128, 2) prefix_simple_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int R = kPrefixSimpleRows, P = kPrefixSimpleTile, NT = P / 8;
   constexpr float kLift = std::is_same<T, __nv_bfloat16>::value ? -kPrefixDrop : 6.f;  // P's power of two
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ uint4 smem_wide[];
   const int D = a.D, chunks = D / 8, steps = (D + 15) / 16, ld = steps * 16 + 8;  // elements between rows
-  T* const qs = reinterpret_cast<T*>(smem_raw);  // [R][ld]
+  T* const qs = reinterpret_cast<T*>(smem_wide);  // [R][ld]
   T* const ks = qs + R * ld;                     // [2][P][ld]
   T* const vs = ks + 2 * P * ld;                 // [2][P][ld]
   __shared__ bool gone[2][P];
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(128, 2) prefix_simple_kernel(const __grid_cons
   if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, kDevErrIndex);
   PrefixWalk w;
   if (!w.start(a, length, blockIdx.x)) return;
-  for (int e = tid; e < (R + 4 * P) * ld / 8; e += 128) reinterpret_cast<uint4*>(smem_raw)[e] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < (R + 4 * P) * ld / 8; e += 128) smem_wide[e] = make_uint4(0, 0, 0, 0);
   // The copies of a tile: a position a warp, 16 bytes a lane.
   auto copy = [&](int h, int t, int buf) {
 #pragma unroll
