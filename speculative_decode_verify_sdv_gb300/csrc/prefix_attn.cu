@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const AttnArgs& own = j.own.attn;
   const int D = a.D, j4 = threadIdx.x % kRowThreads;
   const long long orow = (long long)blockIdx.x * (kJoinThreads / kRowThreads) + threadIdx.x / kRowThreads;
-  // (the split first, before the launches in front have ended: the lengths are inputs)
+  griddep_wait();
+  griddep_launch_dependents();
   const bool is = orow < (long long)a.tokens * a.Hq;
   const int token = is ? (int)(orow / a.Hq) : 0, head = is ? (int)(orow - (long long)token * a.Hq) : 0;
   const int h = head / a.G, row = token * a.G + head - h * a.G, rt = row / a.row_tile, r = row - rt * a.row_tile;
@@ -313,8 +314,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     parts = in_parts ? own_live_parts((length + kOwnTile - 1) / kOwnTile, j.own.prefix_parts)
                      : attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1;
   const int own_parts = row_is && j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
-  griddep_wait();
-  griddep_launch_dependents();
   if (!is) return;
   RowSum<N> sum;
   auto gather = [&](auto odd, const float2* ml, const float4* po, long long ml_step, long long po_step, int count) {

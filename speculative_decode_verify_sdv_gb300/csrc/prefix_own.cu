@@ -167,9 +167,15 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const int y = at / units, unit = at - y * units;
   const int rg = shared ? 0 : unit % o.row_groups, bh = shared ? unit : unit / o.row_groups, h = bh % a.Hkv,
             b = bh / a.Hkv;  // (the rows of all sequences are those of "sequence" 0, were it that long)
-  // Behind another launch of this call: that one has let this one start, so what came before it has
-  // ended; nothing is read that it writes.  It is waited for at the end, for the launch behind.
-  if (o.prefix_parts > 0) griddep_wait();
+  if (threadIdx.x == 0) {
+    set_wait_limit(a.fault);
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
+    fence_barrier_init();
+  }
+  // Queries, lengths, tables and pages may be what launches in front of this call have written, and what
+  // they wrote is only sure to be seen behind the wait: nothing is read before it.
+  griddep_wait();
   griddep_launch_dependents();
   AttnSeq seq;
   if (shared) {
@@ -183,13 +189,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const int per = own_per_part(seq.tiles, shared ? o.prefix_parts : o.parts);
   const int from = y * per * kOwnTile, to = min(from + per * kOwnTile, total);
   if (y > 0 && from >= total) return;
-  if (threadIdx.x == 0) {
-    set_wait_limit(a.fault);
-    mbar_init(bars, 1);
-    mbar_init(bars + 8, 1);
-    fence_barrier_init();
-    if (seq.bad) atomicOr(o.status, kDevErrIndex);
-  }
+  if (seq.bad && threadIdx.x == 0) atomicOr(o.status, kDevErrIndex);
   all_of<WARPS>(true);
   const int r0 = rg * R + warp * 16, rows = shared ? n * a.G : a.rows;
   const int32_t* const table = shared ? o.prefix_table : a.table + (size_t)b * a.max_pages;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const size_t part = (size_t)y * a.B * a.S * a.Hq;
   float* const part_o = shared ? o.prefix_o : o.part_o;
   float2* const part_ml = shared ? o.prefix_ml : o.part_ml;
-  // with the join: where the prefix's partials of a row lie, after the launch in front has written them
+  // with the join: where the prefix's partials of a row lie
   const PrefixArgs& pre = join.prefix;
   long long pre_total = 0;
   int pre_tiles = 0, pre_live = 0;
@@ -396,7 +396,6 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     pre_tiles = prefix_tiles(pre, prefix_length(pre, bad));
     pre_total = (long long)pre_tiles * pre.units;
     pre_live = attn_live_ctas(pre.ctas, pre_total);
-    griddep_wait();
   }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -483,7 +482,6 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
         join.lse[orow] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
-  if (!LAST && o.prefix_parts == 0) griddep_wait();
 }
 
 template <typename T, int D, int WARPS, bool LAST>
