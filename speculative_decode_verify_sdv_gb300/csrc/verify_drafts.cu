@@ -526,8 +526,9 @@ __global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const Draf
     s_last = -1;
   }
   cluster_arrive();
-  // The launch in front has let this one start, so what came before it has ended: its inputs can
-  // be read before it ends itself.
+  // Logits, drafts and counts may be what launches in front of this call have written: like the sums,
+  // they are only sure to be seen behind the wait.
+  griddep_wait();
   const float t = __ldg(a.temperature + b);
   const int n = a.n_drafts != nullptr ? min(max(__ldg(a.n_drafts + b), 0), a.S - 1) : a.S - 1;
   const float u = __ldg(a.uniforms + (long long)b * a.S + a.S - 1);
@@ -537,9 +538,9 @@ __global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const Draf
   };
   auto test_of = [&](int i) {
     const long long row = (long long)b * a.S + i;
-    const int d = i < n ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;
+    const int d = i < a.S - 1 ? __ldg(a.drafts + (long long)b * (a.S - 1) + i) : -1;  // (not behind the load of n)
     Test v;
-    v.real = d >= 0 && d < a.V;
+    v.real = i < n && d >= 0 && d < a.V;
     v.u = __ldg(a.uniforms + row);
     v.x = v.real ? logit(static_cast<const T*>(a.logits) + row * a.stride + d) : -INFINITY;
     v.q = a.probs != nullptr && v.real ? __ldg(a.probs + ((long long)b * (a.S - 1) + i) * a.V + d) : 1.f;
@@ -547,9 +548,8 @@ __global__ void __launch_bounds__(kDrawThreads, 3) verify_draw_kernel(const Draf
     return v;
   };
   Test test{};
-  if (warp <= n) test = test_of(warp);
+  if (warp < a.S) test = test_of(warp);
   const Warmth c(t);
-  griddep_wait();
   cluster_wait();  // every CTA has begun: its shared memory can be written
   // every row's sum, and its draft's test
   for (int i = warp; i <= n; i += W) {
