@@ -261,15 +261,13 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
   __shared__ float4 so[kJoinParts][kJoinItems];
   __shared__ float2 sml[kJoinParts][kJoinItems];
   const int lane = threadIdx.x & 31;
-  // The split first, before the attention launch has ended: lengths are inputs, and
-  // whatever wrote them had ended before that launch let this one start.
+  griddep_wait();
   int unit, c0, c1;
   AttnWalk w;
   if (by_cta) {
     // the unit that the first tile of a CTA's range lies inside, by its second sharer
     const int c = blockIdx.x + 1;
     const bool some = w.start(a, c, lane);
-    griddep_wait();
     if (!some || w.tile == 0) return;
     w.sharers(c0, c1);
     if (c0 != c - 1) return;
@@ -294,7 +292,6 @@ __global__ void __launch_bounds__(kJoinItems* kJoinParts) attn_join_kernel(const
     const int live = attn_live_ctas(a.ctas, total);
     c0 = attn_owner(total, live, first);
     c1 = attn_owner(total, live, first + seq.tiles - 1);
-    griddep_wait();
     if (c0 == c1) return;
   }
   const int b = w.b;
