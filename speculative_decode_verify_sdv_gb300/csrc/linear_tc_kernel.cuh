@@ -303,10 +303,7 @@ __global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = misc[0];
-  // The second launch needs nothing of the first but the parts, and that one has waited for
-  // what came before both.
-  const bool second = a.pass == 1 && a.T > kLC;
-  if (!second) griddep_wait();
+  griddep_wait();
   griddep_launch_dependents();
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
@@ -543,7 +540,6 @@ __global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
     const bool owner = r < DK;  // rows with a place in the state's array
     uint32_t meetings = 0;
     int part = 0;
-    if (second) griddep_wait();
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;

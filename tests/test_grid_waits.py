@@ -13,7 +13,8 @@ import pytest
 from speculative_decode_verify_sdv_gb300 import build
 
 FILES = ["page_assign.cu", "qk_norm_rope.cu", "prefix_attn.cu", "prefix_own.cu", "prefix_tc_kernel.cuh",
-         "verify_drafts.cu", "paged_attn.cu", "attn_tc_kernel.cuh"]
+         "verify_drafts.cu", "paged_attn.cu", "attn_tc_kernel.cuh",
+         "linear_attn.cu", "linear_tc_kernel.cuh", "linear_window.cu"]
 READS = (r"\b(?:__ldg|__ldcg|tma_load\w*|attn_seq|attn_word|lin_tokens|prefix_length|page_need|place_row|"
          r"griddep_launch_dependents)\s*\(|\.start\(|<const (?:u?int\d|float\d|uint)\w*\s*\*>\(a\.")
 
