@@ -8,9 +8,9 @@
 // Two exclusive sums over the requests, of what is given back and of what is needed, and a
 // copy of page ids.  A round of 48 windows moves some 50 ids and writes 6 KB: latency bounds it,
 // the lengths' loads and then those of the list and of the table's entries (3.5 us a call, 48
-// requests of 17 rows).  So for up to 255 requests and 2560 rows one CTA makes both sums in one
-// scan, and takes the new pages' ids for the slots from the list itself, not from the table that it
-// writes.  More requests, or more rows: a cluster shares the copies, and a launch of its own writes
+// requests of 17 rows).  So for up to 255 requests, 2560 rows to place and tables of 65,536 entries in all
+// one CTA makes both sums in one scan, and takes the new pages' ids for the slots from the list itself, not
+// from the table that it writes.  Beyond one of them a cluster shares the copies, and a launch of its own writes
 // positions and slots (512 prompts of up to 2001 rows, 31,843 pages taken and given back: 20.5 us the
 // two calls, 8 MB written).
 #include <cuda_runtime.h>
@@ -203,8 +203,15 @@ __global__ void __launch_bounds__(kPageThreads, 1) page_assign_kernel(const Page
 // One CTA against the cluster and its second launch, us a call (the giving back half of the calls):
 // 8 sequences of 256 rows 3.7 against 4.2, of 512 4.6 against 4.4; 32 of 64 4.2 against 4.6, of 128
 // 5.2 against 4.6; 255 of 9 4.9 against 5.3, of 17 6.0 against 5.3.
-constexpr int kSmallThreads = 512, kSmallSeqs = 255;
-constexpr long long kSmallRows = 2560;
+//
+// How many pages a call moves is only known on the device; the tables' entries bound it.  Moved pages,
+// us a call without places: 48 sequences, 48 pages 3.1 against 5.5, 12,288 14.7 against 7.8, 49,152 49.7 against
+// 17.1; 255, 255 pages 3.1 against 5.4, 4080 8.6 against 5.9, 65,280 72 against 8.7, 261,120 273 against 20.  At
+// the limit a call that moves every entry loses some 60 us, once in the life of its sequences, and every
+// round with few pages gains 2.  Of up to eight sequences the cluster copies each by one warp: of eight
+// 32,768 pages take 27.7 against 39.5.
+constexpr int kSmallThreads = 512, kSmallSeqs = 255, kSmallAnyTable = 8;
+constexpr long long kSmallRows = 2560, kSmallEntries = 65536;
 
 struct TwoSums {
   long long back, need;
@@ -378,7 +385,8 @@ sdv_status sdv_page_assign(const sdv_pagepool* pool, int32_t B, int32_t T, const
   a.status = static_cast<int*>(ws);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool maps = positions_or_null != nullptr || slots_or_null != nullptr;
-  if (B <= sdv::kSmallSeqs && (!maps || (long long)B * T <= sdv::kSmallRows))
+  if (B <= sdv::kSmallSeqs && (!maps || (long long)B * T <= sdv::kSmallRows) &&
+      (B <= sdv::kSmallAnyTable || (long long)B * pool->max_pages <= sdv::kSmallEntries))
     return sdv::status_of(sdv::launch_pdl(sdv::page_assign_small_kernel, dim3(1), dim3(sdv::kSmallThreads), 0, st, a));
   const int cluster = 8;
   cudaLaunchAttribute attr[2];

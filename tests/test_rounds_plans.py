@@ -1,0 +1,50 @@
+"""Which kernels the calls around a batched round launch, on both sides of each rule, checked on the
+CPU (the library's host code with the stand-in runtime of ``tests/launch_trace``)."""
+import os
+import shutil
+import sys
+
+import pytest
+
+sys.path.insert(0, os.path.join(os.path.dirname(__file__), "launch_trace"))
+import build_trace  # noqa: E402
+
+SOURCES = ["api.cu", "dq_gemm.cu", "tc_gemm.cu", "gemv.cu", "small_kernels.cu", "moe_kernels.cu", "noalloc.cu",
+           "page_assign.cu", "paged_attn.cu", "attn_tc.cu", "attn_tc_bf16.cu", "prefix_attn.cu", "prefix_tc.cu",
+           "prefix_tc_bf16.cu", "prefix_own.cu"]
+
+
+@pytest.fixture(scope="module")
+def plan(request):
+    if shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"):
+        pytest.skip("nvcc not available")
+    patch = pytest.MonkeyPatch()
+    patch.setattr(build_trace, "SOURCES", SOURCES)
+    patch.setattr(build_trace, "HOST", ["stub_runtime.cpp", "rounds_main.cpp"])
+    exe = build_trace.build(out_dir=build_trace.OUT + "_rounds")
+    patch.undo()
+
+    def run(command, sms=152):
+        _, call = build_trace.run(exe, [f"device {sms} 232448", command])
+        assert call["status"] == 0
+        return call["launches"]
+
+    return run
+
+
+def kinds(launches, *names):
+    """The launches by which of the names is theirs."""
+    return [next(n for n in names if n in launch["name"]) for launch in launches]
+
+
+SMALL, CLUSTER, PLACE = "page_assign_small", "page_assign_kernel", "page_place"
+
+
+@pytest.mark.parametrize("B,T,most,maps,want", [
+    (48, 17, 1003, 1, [SMALL]), (255, 1, 257, 1, [SMALL]), (255, 1, 258, 1, [CLUSTER, PLACE]),
+    (64, 17, 1024, 0, [SMALL]), (64, 17, 1025, 0, [CLUSTER]), (255, 1, 1000, 0, [CLUSTER]),
+    (8, 1, 100000, 0, [SMALL]), (8, 320, 100000, 1, [SMALL]), (9, 1, 100000, 0, [CLUSTER]),
+    (8, 321, 10, 1, [CLUSTER, PLACE]), (256, 1, 10, 0, [CLUSTER]), (1, 5000, 500, 0, [SMALL]),
+])
+def test_pages_by_sequences_rows_and_entries(plan, B, T, most, maps, want):
+    assert kinds(plan(f"pages {B} {T} {most} {maps}"), SMALL, CLUSTER, PLACE) == want
