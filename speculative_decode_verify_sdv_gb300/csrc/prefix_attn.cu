@@ -571,7 +571,7 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   own.prefix_pages = prefix_pages;
   sdv::set_parts(own, sms);
   own.attn.fault = sdv::debug_fault();
-  const bool parts = tc && sdv::own_takes(own);
+  const bool parts = tc && sdv::own_takes(own, sms);
   if (!parts) own.prefix_parts = 0;
   if (own.prefix_parts > 0) {
     own.prefix_o = a.part_o;

@@ -53,13 +53,25 @@ namespace {
 // one row, 4000 positions 20 against 28, 8000 30 against 31, 16,000 49 against 37, eight of them
 // 16,000 92 against 101; five rows (two warps), one sequence 2000 23 against 27, 4000 31 against 29,
 // sixteen 2000 52 against 56, 4000 80 against 75; 16 rows (four warps), one 1000 22 against 26, 2000
-// 26 against 27, 64 of them 500 122 against 139, 1000 160 against 151.  Nine rows of 16 heads over 2 of
-// 256 (five row groups), one sequence 2000 27 against 29, sixteen 500 45 against 45, 1000 71
-// against 47 -- but where most of 24 such tables stay empty (rows and positions half and a sixth of
-// what they could be) 60 against 76.
+// 26 against 27, 64 of them 500 122 against 139, 1000 160 against 151.
+// How full the tables are is known on the device alone: half empty ones (lengths spread evenly) speak for this
+// kernel, mostly empty ones more so.  960 positions, full, half and mostly empty, this kernel's time over
+// the paged attention's: 16 rows of 32 heads over 8 of 128, one sequence 1.06, 16 of them 0.97, 0.88, 0.66,
+// 64 1.07, 0.84, 0.67; 32 rows (two row groups), four 1.16, 0.97, 0.78, 64 1.14, 0.91, 0.64.
+//
+// Heads of more than 128 columns have one warp a CTA, and every group of 16 rows reads the sequence
+// again.  16 heads over 2 of 256, one group: one row, one sequence of 500 positions 0.94, 1000 1.00, 2000
+// 1.08, 16 of them 2000 0.88, 0.96, 1.06, 64 of 3000 0.96, 0.92, 0.91; 16 rows, four of 500 1.11, 1.05,
+// 0.97, 1000 1.15, 1.13, 1.01, 2000 1.22, 1.22, 1.16, 16 of 1000 1.02, 1.08, 1.03, 64 of 1000 1.05,
+// 0.94, 0.79, 200 of 2000 0.88, 0.80, 0.67.  Several groups, by the row groups of all sequences and heads: 40
+// (four sequences of nine rows) 500 positions 1.00, 0.99, 0.93, 1000 1.08, 1.02, 0.95; 144 500 1.01, 0.82,
+// 0.86, 960 1.26, 1.05, 0.89; 160 500 1.00, 0.96, 0.79, 960 1.46, 1.09, 0.88; 240 960 1.16, 1.09, 0.84; 288
+// 960 1.18, 1.01, 0.79; 432 960 0.96, 0.97, 0.72; 640 1000 1.12, 0.96, 0.73, 1500 1.24, 1.08, 0.80: in the
+// mean of the three the border lies by 700 positions at 160 groups, 900 at 240, 1300 at 640.
 constexpr int kOwnMostOne = 4800;   // one warp, 128 columns, up to 16 cache heads of sequences; more by their number
 constexpr int kOwnMostTwo = 3000;   // two warps
 constexpr int kOwnMostFour = 1000;  // four, or several row groups
+constexpr int kOwnMostWide = 500;   // more than 128 columns, up to 16 cache heads of sequences, or few row groups
 constexpr int kOwnMost = 2048;      // of a part, of a single long sequence
 constexpr uint64_t kOwnDrainNs = 100000000ull;  // 0.1 s: copies under way at the end
 
@@ -524,12 +536,16 @@ cudaError_t own_dispatch(const OwnMaps& m, const JoinArgs& j, bool last, cudaStr
 
 }  // namespace
 
-bool own_takes(const OwnArgs& o) {
+bool own_takes(const OwnArgs& o, int sms) {
   const AttnArgs& a = o.attn;
   const long long positions = (long long)a.max_pages * a.page, units = (long long)a.B * a.Hkv;
-  const long long most = o.warps == 4 || o.row_groups > 1 ? kOwnMostFour
-                         : o.warps == 2                   ? kOwnMostTwo
-                                                          : kOwnMostOne * 128 / a.D * (units > 16 ? units : 16) / 16;
+  const long long by_units = units > 16 ? units : 16;
+  const bool wide = a.D > 128, few = 2 * units * o.row_groups < 3 * sms;  // (groups an SM: 1.5)
+  const long long most = o.row_groups > 1 ? (wide && few ? kOwnMostWide : kOwnMostFour)
+                         : wide           ? kOwnMostWide * by_units / 16
+                         : o.warps == 4   ? kOwnMostFour
+                         : o.warps == 2   ? kOwnMostTwo
+                                          : kOwnMostOne * 128 / a.D * by_units / 16;
   return positions <= most && positions <= (long long)kOwnMost * o.parts;
 }
 

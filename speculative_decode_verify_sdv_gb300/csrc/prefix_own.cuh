@@ -43,7 +43,7 @@ __device__ __forceinline__ int own_live_parts(int tiles, int parts) {
 
 // Whether the positions that a table may hold are few enough for the parts (the shapes are those of
 // the tensor-core kernels, attn_tc_takes).
-bool own_takes(const OwnArgs& o);
+bool own_takes(const OwnArgs& o, int sms);
 // last: the own positions, of a single part each, are joined with the prefix's partials here (heads
 // of up to 128).
 cudaError_t launch_prefix_own(int dtype, const JoinArgs& j, bool last, cudaStream_t st);

@@ -48,3 +48,34 @@ SMALL, CLUSTER, PLACE = "page_assign_small", "page_assign_kernel", "page_place"
 ])
 def test_pages_by_sequences_rows_and_entries(plan, B, T, most, maps, want):
     assert kinds(plan(f"pages {B} {T} {most} {maps}"), SMALL, CLUSTER, PLACE) == want
+
+
+OWN, PAGED = "prefix_own", "attn_tc_kernel"
+
+
+def own_form(launches):
+    found = [n for launch in launches for n in (OWN, PAGED) if n in launch["name"]]
+    assert len(found) == 1
+    return found[0]
+
+
+@pytest.mark.parametrize("B,S,hq,hkv,d,most,want", [
+    # heads of 128: one warp, two, four, and several row groups
+    (1, 1, 32, 8, 128, 4800, OWN), (1, 1, 32, 8, 128, 4816, PAGED), (4, 1, 32, 8, 128, 9600, OWN),
+    (16, 5, 32, 8, 128, 3008, PAGED), (16, 5, 32, 8, 128, 2992, OWN), (16, 16, 32, 8, 128, 992, OWN),
+    (16, 16, 32, 8, 128, 1008, PAGED), (4, 32, 32, 8, 128, 992, OWN), (4, 32, 32, 8, 128, 1008, PAGED),
+    # heads of 256, one row group: by sequences and heads
+    (1, 1, 16, 2, 256, 496, OWN), (1, 1, 16, 2, 256, 512, PAGED), (4, 2, 16, 2, 256, 1008, PAGED),
+    (64, 2, 16, 2, 256, 2000, OWN),
+    # several row groups: as many as 1.5 an SM, and fewer
+    (16, 9, 16, 2, 256, 496, OWN), (16, 9, 16, 2, 256, 1000 // 16 * 16, PAGED), (4, 9, 16, 2, 256, 992, PAGED),
+    (64, 9, 16, 2, 256, 992, OWN), (64, 9, 16, 2, 256, 1008, PAGED),
+])
+def test_own_positions_by_rows_sequences_and_tables(plan, B, S, hq, hkv, d, most, want):
+    # (a prefix of more positions than few rows take in parts)
+    assert own_form(plan(f"prefix {B} {S} {hq} {hkv} {d} 16 1000 {most // 16}")) == want
+
+
+@pytest.mark.parametrize("B,sms,want", [(22, 152, PAGED), (23, 152, OWN), (23, 160, PAGED), (24, 160, OWN)])
+def test_row_groups_are_counted_by_the_device(plan, B, sms, want):
+    assert own_form(plan(f"prefix {B} 9 16 2 256 16 100 60", sms=sms)) == want
