@@ -573,6 +573,8 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   own.attn.fault = sdv::debug_fault();
   const bool parts = tc && sdv::own_takes(own, sms);
   if (!parts) own.prefix_parts = 0;
+  if (parts && own.prefix_parts == 0)
+    a.passed = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kPassedAt);
   if (own.prefix_parts > 0) {
     own.prefix_o = a.part_o;
     own.prefix_ml = reinterpret_cast<float2*>(a.part_ml);

@@ -82,12 +82,19 @@ __device__ __noinline__ uint32_t own_odd(const AttnArgs& a, const int32_t* table
   uint32_t odd = 0;
   for (int p = from; p < to; ++p) {
     if (p >= ctx && !(word >> (p - ctx) & 1u)) continue;
-    const int id = __ldg(table + p / a.page);
+    const int id = __ldcg(table + p / a.page);
     if (id < 0 || id >= a.n_pages) continue;
     const float x = (float)static_cast<const T*>(a.v)[(((long long)id * a.Hkv + h) * a.page + p % a.page) * a.D + d];
     if (!(fabsf(x) < INFINITY)) odd |= x != x ? kOddNan : x > 0.f ? kOddPlus : kOddMinus;
   }
   return odd;
+}
+
+// As attn_word, by a coherent load.
+__device__ __forceinline__ uint32_t own_word(const AttnArgs& a, int b, int i, int n) {
+  if (i >= n) return 0u;
+  const uint32_t live = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  return a.mask != nullptr ? __ldcg(a.mask + (size_t)b * a.S + i) & live : (2u << i) - 1u;
 }
 
 constexpr int kSlice = 32;  // positions
@@ -185,9 +192,16 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     mbar_init(bars + 8, 1);
     fence_barrier_init();
   }
-  // Queries, lengths, tables and pages may be what launches in front of this call have written, and what
-  // they wrote is only sure to be seen behind the wait: nothing is read before it.
-  griddep_wait();
+  // Queries, lengths, tables and pages may be what launches in front of this call have written: they are read
+  // behind the wait, or, beside the prefix's launch, behind the word that passes its wait on, by coherent
+  // loads; then that launch is waited for at the end, for its partials and for the launch behind.
+  bool beside = false;
+  if (join.prefix.passed != nullptr) {
+    beside = passed_on(join.prefix.passed);
+    if constexpr (WARPS > 1) beside = __syncthreads_and(beside);
+    else beside = __all_sync(0xffffffffu, beside);
+  }
+  if (!beside) griddep_wait();
   griddep_launch_dependents();
   AttnSeq seq;
   if (shared) {
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     seq.n = a.B * a.S;
     seq.tiles = (seq.ctx + kOwnTile - 1) / kOwnTile;
   } else {
-    seq = attn_seq(a, b);
+    seq = attn_seq(a, __ldcg(a.ctx + b), a.n_rows != nullptr ? __ldcg(a.n_rows + b) : a.S);
   }
   const int ctx = seq.ctx, n = seq.n, total = shared ? ctx : ctx + n;
   const int per = own_per_part(seq.tiles, shared ? o.prefix_parts : o.parts);
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   const uint32_t dst = base + cb * BLOCK + bx * box * 128;
   auto page_of = [&](int i) {  // of the lane's copy in slice i; -1 past the end
     const int p = from + kSlice * i + bx * box;
-    return mine && i < slices && p < to ? __ldg(table + (p >> page_log)) : -1;
+    return mine && i < slices && p < to ? __ldcg(table + (p >> page_log)) : -1;
   };
   auto row_of = [&](int i, int id) {
     const int p = from + kSlice * i + bx * box;
@@ -231,6 +245,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   };
   int row_next = beyond, id_after = page_of(1);
   if (slices > 0 && warp == 0) {
+    fence_proxy_async_global();
     const int row = row_of(0, page_of(0));
     issue(0, 0, row);
     issue(0, 1, row);
@@ -239,15 +254,15 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     const int r = e / (D / 8), ch = e % (D / 8), row = r0 + r;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (row < rows && row / a.G < n)
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + ((long long)b * a.S + row / a.G) * a.q_stride +
-                                               (h * a.G + row % a.G) * D) + ch);
+      x = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + ((long long)b * a.S + row / a.G) * a.q_stride +
+                                                (h * a.G + row % a.G) * D) + ch);
     *reinterpret_cast<uint4*>(mem + r * LQ + ch * 16) = x;
   }
   uint32_t words[2];  // visibility of rows g and g + 8
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int row = r0 + half * 8 + g;
-    words[half] = row < rows && !shared ? attn_word(a, b, row / a.G, n) : 0u;
+    words[half] = row < rows && !shared ? own_word(a, b, row / a.G, n) : 0u;
   }
   auto live = [&](int half) {
     const int row = r0 + half * 8 + g;
@@ -257,7 +272,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   bool some_absent = false;
   if (from < to)
     for (int e = (from >> page_log) + lane; e <= (to - 1) >> page_log; e += 32) {
-      const int id = __ldg(table + e);
+      const int id = __ldcg(table + e);
       some_absent |= id < 0 || id >= a.n_pages;
     }
   some_absent = __any_sync(0xffffffffu, some_absent);
@@ -314,7 +329,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
       there = to - p0 >= 32 ? 0xffffffffu : (1u << (to - p0)) - 1u;
       if (some_absent) {
         int e = -1;
-        if (p0 + lane < to) e = __ldg(table + ((p0 + lane) >> page_log));
+        if (p0 + lane < to) e = __ldcg(table + ((p0 + lane) >> page_log));
         there &= __ballot_sync(0xffffffffu, e >= 0 && e < a.n_pages);
       }
     }
@@ -404,6 +419,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   long long pre_total = 0;
   int pre_tiles = 0, pre_live = 0;
   if constexpr (LAST) {
+    if (beside) griddep_wait();
     bool bad;  // (reported by that launch)
     pre_tiles = prefix_tiles(pre, prefix_length(pre, bad));
     pre_total = (long long)pre_tiles * pre.units;
@@ -494,6 +510,9 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
         join.lse[orow] = empty ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
+  if (!LAST && beside) griddep_wait();
+  // whoever starts from here on finds the prefix's launch ended
+  if (join.prefix.passed != nullptr && cta == 0 && threadIdx.x == 0) *join.prefix.passed = 0;
 }
 
 template <typename T, int D, int WARPS, bool LAST>

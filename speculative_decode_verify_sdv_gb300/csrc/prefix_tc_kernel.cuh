@@ -173,7 +173,14 @@ __global__ void __launch_bounds__(128 + 128 * STREAMS, 1)
   tc_fence_after();
   const uint32_t tm = misc[0];
   griddep_wait();
-  griddep_launch_dependents();
+  // the launch behind may start when the word is there: the last block's idle warp sees to it
+  if (a.passed == nullptr || blockIdx.x + 1 < gridDim.x) {
+    griddep_launch_dependents();
+  } else if (warp == 3) {
+    if (lane == 0) pass_on(a.passed);
+    __syncwarp();
+    griddep_launch_dependents();
+  }
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
     if (ok) ok = mbar_wait_warp(bar, parity, a.status);

@@ -317,6 +317,7 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // The 16 MMAs of one 256-column stage under a single elect.sync (one lane
 // issues, the warp stays converged): MMA m multiplies A columns a + 8m by the

@@ -3,7 +3,9 @@ wait (CPU: reads the sources).
 
 What the launches in front have written is only promised to the grid that waits, behind its wait,
 whatever the launch in front has itself waited for: queries, lengths and pages of a call may have
-been written by the launch before the call's first.
+been written by the launch before the call's first.  A kernel that runs beside the one in front may
+read them where that one passes on what it has seen, by a word that it releases and this one
+acquires; then by coherent loads alone.
 """
 import os
 import re
@@ -42,8 +44,13 @@ def early_reads(body):
     """What a body reads (or starts) before it waits unconditionally; None where it never does."""
     for m in re.finditer(r"griddep_wait\(\);", body):
         front = body[:m.start()]
-        if front.rstrip()[-1:] in ("", ";", "}", "{") and front.count("{") == front.count("}"):
+        if front.count("{") != front.count("}"):
+            continue
+        if front.rstrip()[-1:] in ("", ";", "}", "{"):
             return re.findall(READS, front)
+        guard = re.search(r"if \(!(\w+)\)\s*$", front)
+        if guard and re.search(rf"\b{guard.group(1)} = passed_on\(", front):
+            return re.findall(READS, front) + re.findall(r"\b(?:__ldg|attn_word)\(", body[m.end():])
     return None
 
 
@@ -61,4 +68,7 @@ def test_a_late_or_conditional_wait_is_found():
     assert [(n, early_reads(b)) for n, b in kernels(text)] == [("k", ["__ldg("])]
     assert early_reads("if (x) griddep_wait(); y = 1;") is None
     assert early_reads("if (x) { griddep_wait(); }") is None
+    assert early_reads("x = passed_on(w); if (!x) griddep_wait(); y = __ldcg(p);") == []
+    assert early_reads("x = passed_on(w); if (!x) griddep_wait(); y = __ldg(p);") == ["__ldg("]
+    assert early_reads("x = 1; if (!x) griddep_wait(); y = __ldcg(p);") is None
     assert early_reads("if (x) { y = 1; } griddep_wait(); z = __ldg(p);") == []
