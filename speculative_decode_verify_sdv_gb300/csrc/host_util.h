@@ -10,6 +10,7 @@
 namespace sdv {
 
 constexpr size_t kHeaderBytes = 256;  // a workspace's head: word 0 is the status; zero between calls
+constexpr int kPassedAt = 32;           // there, the word by which a call's first launch passes its wait on
 
 inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

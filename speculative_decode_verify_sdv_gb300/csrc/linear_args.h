@@ -60,6 +60,7 @@ struct LinArgs {
   int* status;
   int ctas;
   int pass;                // 0: local states, 1: outputs and final states
+  unsigned* passed;        // of two launches: the word by which the first passes its wait on
   DebugFault fault;        // the timeout path's test hook: a chunk whose keys are never asked for
 };
 
@@ -82,7 +83,7 @@ cudaError_t linear_tc_bf16(const LinMaps& m, const LinArgs& a, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
-  return a.n_tokens != nullptr ? min(max(__ldg(a.n_tokens + b), 0), a.T) : a.T;
+  return a.n_tokens != nullptr ? min(max(a.n_tokens[b], 0), a.T) : a.T;
 }
 
 __device__ __forceinline__ float lin_float(__half x) { return __half2float(x); }

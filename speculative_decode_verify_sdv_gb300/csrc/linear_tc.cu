@@ -3,6 +3,7 @@
 
 #include <mutex>
 
+#include "host_util.h"
 #include "linear_tc_kernel.cuh"
 #include "sdv.h"
 
@@ -55,6 +56,7 @@ cudaError_t launch_linear_tc(int dtype, const LinArgs& args, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.T > kLinChunk) {  // a head of one chunk is never shared
     a.pass = 0;
+    a.passed = reinterpret_cast<unsigned*>(a.status) + kPassedAt / 4;
     e = bf ? linear_tc_bf16(m, a, st) : linear_tc_f16(m, a, st);
     if (e != cudaSuccess) return e;
   }

@@ -299,12 +299,22 @@ __global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
     for (int e = threadIdx.x; e < PL::kK / 16; e += PL::kThreads) sts128(base + PL::oZero + 16 * e, make_uint4(0, 0, 0, 0));
     fence_proxy_async_smem();
   }
+  // The second launch needs nothing of the first but the parts, which the state's warps wait for: it reads
+  // keys, values, queries and decays beside it, behind the word that passes the first one's wait on.
   tc_fence_before();
-  __syncthreads();
+  const bool beside = __syncthreads_and(a.passed != nullptr && a.pass == 1 && passed_on(a.passed));
   tc_fence_after();
   const uint32_t tm = misc[0];
-  griddep_wait();
-  griddep_launch_dependents();
+  if (!beside) griddep_wait();
+  if (a.passed != nullptr && a.pass == 0 && blockIdx.x + 1 == gridDim.x) {  // (one warp: the trigger is the first thread's)
+    if (warp == 3) {
+      if (lane == 0) pass_on(a.passed);
+      __syncwarp();
+      griddep_launch_dependents();
+    }
+  } else {
+    griddep_launch_dependents();
+  }
   bool ok = true;
   auto await = [&](uint32_t b, uint32_t parity) {
     if (ok) ok = mbar_wait_warp(b, parity, a.status);
@@ -335,6 +345,7 @@ __global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
   if (warp == 0) {
     // ---- TMA ----
     const uint64_t normal = l2_policy_normal();
+    fence_proxy_async_global();
     const uint64_t v_policy = OUT ? l2_policy_evict_first() : normal;  // the second launch reads values last
     const int shared = a.H / a.Hqk;
     int asked_k = 0, asked_q = 0, asked_v = 0;
@@ -540,6 +551,9 @@ __global__ void __launch_bounds__(LinPlanOf<T, DK, DV, OUT>::kThreads, 1)
     const bool owner = r < DK;  // rows with a place in the state's array
     uint32_t meetings = 0;
     int part = 0;
+    griddep_wait();
+    // whoever starts from here on finds the first launch ended
+    if (a.passed != nullptr && a.pass == 1 && blockIdx.x == 0 && warp == 4 && lane == 0) *a.passed = 0;
     for (bool more = any; ok && more; more = w.more()) {
       const int count = w.count();
       const long long unit = (long long)w.b * a.H + w.h;

@@ -43,22 +43,6 @@ struct PrefixArgs {
   DebugFault fault;
 };
 
-// What launches in front of a call wrote is visible to a grid behind its own wait.  A launch that is to run
-// beside the call's first one cannot wait, as it would wait for that one too.  So a thread of the first
-// launch, behind its wait, writes a word with release semantics; who has read it with acquire semantics
-// sees what that thread saw (by loads that are coherent, and by the asynchronous proxy behind a fence).
-// Nobody waits for the word: who does not find it waits for the launch instead.
-constexpr int kPassedAt = 32;  // in the workspace's header: 0 between calls
-__device__ __forceinline__ void pass_on(unsigned* word) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(1u) : "memory");
-  __threadfence();
-}
-__device__ __forceinline__ bool passed_on(const unsigned* word) {
-  unsigned x;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(word) : "memory");
-  return x != 0;
-}
-
 // The prefix's length as it counts, and its tiles.
 __device__ __forceinline__ int prefix_length(const int32_t* length, int max_pages, int page, bool& bad) {
   const int n = __ldg(length);

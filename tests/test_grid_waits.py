@@ -49,7 +49,7 @@ def early_reads(body):
         if front.rstrip()[-1:] in ("", ";", "}", "{"):
             return re.findall(READS, front)
         guard = re.search(r"if \(!(\w+)\)\s*$", front)
-        if guard and re.search(rf"\b{guard.group(1)} = passed_on\(", front):
+        if guard and re.search(rf"\b{guard.group(1)} = [^;]*\bpassed_on\(", front):
             return re.findall(READS, front) + re.findall(r"\b(?:__ldg|attn_word)\(", body[m.end():])
     return None
 
