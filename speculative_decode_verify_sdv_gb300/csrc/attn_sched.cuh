@@ -82,8 +82,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int c, int n) {
   s.tiles = max(1, (int)(((unsigned)s.ctx + s.n + a.tile - 1) / (unsigned)a.tile));
   return s;
 }
+// (By coherent loads: some kernels read lengths beside the launch in front of them.)
 __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
-  return attn_seq(a, __ldg(a.ctx + b), a.n_rows != nullptr ? __ldg(a.n_rows + b) : a.S);
+  return attn_seq(a, a.ctx[b], a.n_rows != nullptr ? a.n_rows[b] : a.S);
 }
 
 __device__ __forceinline__ int attn_live_ctas(int ctas, long long total) { return total < ctas ? (int)total : ctas; }
@@ -168,8 +169,8 @@ struct AttnWalk {
   }
   __device__ __forceinline__ void load_next(const AttnArgs& a) {
     const bool is = b + 1 < a.B;
-    next_ctx = is ? __ldg(a.ctx + b + 1) : 0;
-    next_n = is && a.n_rows != nullptr ? __ldg(a.n_rows + b + 1) : a.S;
+    next_ctx = is ? a.ctx[b + 1] : 0;
+    next_n = is && a.n_rows != nullptr ? a.n_rows[b + 1] : a.S;
   }
 };
 

@@ -294,8 +294,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const AttnArgs& own = j.own.attn;
   const int D = a.D, j4 = threadIdx.x % kRowThreads;
   const long long orow = (long long)blockIdx.x * (kJoinThreads / kRowThreads) + threadIdx.x / kRowThreads;
-  griddep_wait();
-  griddep_launch_dependents();
+  // The split first, while the launches in front end: its lengths are read behind the word that passes
+  // the first one's wait on.
+  const bool beside = a.passed != nullptr && passed_on(a.passed);
+  if (!beside) griddep_wait();
   const bool is = orow < (long long)a.tokens * a.Hq;
   const int token = is ? (int)(orow / a.Hq) : 0, head = is ? (int)(orow - (long long)token * a.Hq) : 0;
   const int h = head / a.G, row = token * a.G + head - h * a.G, rt = row / a.row_tile, r = row - rt * a.row_tile;
@@ -314,6 +316,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     parts = in_parts ? own_live_parts((length + kOwnTile - 1) / kOwnTile, j.own.prefix_parts)
                      : attn_owner(total, live, first + tiles - 1) - attn_owner(total, live, first) + 1;
   const int own_parts = row_is && j.own.parts > 0 ? own_live_parts(seq.tiles, j.own.parts) : 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.passed != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.passed = 0;  // (who starts now finds them ended)
   if (!is) return;
   RowSum<N> sum;
   auto gather = [&](auto odd, const float2* ml, const float4* po, long long ml_step, long long po_step, int count) {
@@ -573,8 +578,7 @@ sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table
   own.attn.fault = sdv::debug_fault();
   const bool parts = tc && sdv::own_takes(own, sms);
   if (!parts) own.prefix_parts = 0;
-  if (parts && own.prefix_parts == 0)
-    a.passed = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kPassedAt);
+  if (parts) a.passed = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + sdv::kPassedAt);
   if (own.prefix_parts > 0) {
     own.prefix_o = a.part_o;
     own.prefix_ml = reinterpret_cast<float2*>(a.part_ml);

@@ -45,7 +45,7 @@ struct PrefixArgs {
 
 // The prefix's length as it counts, and its tiles.
 __device__ __forceinline__ int prefix_length(const int32_t* length, int max_pages, int page, bool& bad) {
-  const int n = __ldg(length);
+  const int n = *length;
   const long long cap = (long long)max_pages * page;
   const int most = cap > 0x7fffff00ll ? 0x7fffff00 : (int)cap, m = min(max(n, 0), most);
   bad = m != n;

@@ -195,13 +195,18 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
   // Queries, lengths, tables and pages may be what launches in front of this call have written: they are read
   // behind the wait, or, beside the prefix's launch, behind the word that passes its wait on, by coherent
   // loads; then that launch is waited for at the end, for its partials and for the launch behind.
+  unsigned* const word = join.prefix.passed;
   bool beside = false;
-  if (join.prefix.passed != nullptr) {
-    beside = passed_on(join.prefix.passed);
+  if (o.prefix_parts == 0) {
+    beside = passed_on(word);
     if constexpr (WARPS > 1) beside = __syncthreads_and(beside);
     else beside = __all_sync(0xffffffffu, beside);
   }
   if (!beside) griddep_wait();
+  if (o.prefix_parts > 0 && blockIdx.x + 1 == gridDim.x) {  // the first launch: to the join
+    if (threadIdx.x == 0) pass_on(word);
+    all_of<WARPS>(true);
+  }
   griddep_launch_dependents();
   AttnSeq seq;
   if (shared) {
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     seq.n = a.B * a.S;
     seq.tiles = (seq.ctx + kOwnTile - 1) / kOwnTile;
   } else {
-    seq = attn_seq(a, __ldcg(a.ctx + b), a.n_rows != nullptr ? __ldcg(a.n_rows + b) : a.S);
+    seq = attn_seq(a, b);
   }
   const int ctx = seq.ctx, n = seq.n, total = shared ? ctx : ctx + n;
   const int per = own_per_part(seq.tiles, shared ? o.prefix_parts : o.parts);
@@ -511,8 +516,8 @@ __global__ void __launch_bounds__(32 * WARPS, (D > 128 ? 8 : 12) / WARPS)
     }
   }
   if (!LAST && beside) griddep_wait();
-  // whoever starts from here on finds the prefix's launch ended
-  if (join.prefix.passed != nullptr && cta == 0 && threadIdx.x == 0) *join.prefix.passed = 0;
+  // (whoever starts from here on finds the prefix's launch ended; where a join follows, it does this)
+  if (LAST && cta == 0 && threadIdx.x == 0) *word = 0;
 }
 
 template <typename T, int D, int WARPS, bool LAST>
