@@ -50,28 +50,27 @@ namespace {
 // and takes some 10 us more in launches; here a part is a chain of slices, 1.2 us each for 128
 // columns, and several row groups read everything several times.  Full tables of 32 heads over 8 of
 // 128 behind a prefix of 1000, this kernel against the paged attention, us a call: one sequence of
-// one row, 4000 positions 20 against 28, 8000 30 against 31, 16,000 49 against 37, eight of them
-// 16,000 92 against 101; five rows (two warps), one sequence 2000 23 against 27, 4000 31 against 29,
-// sixteen 2000 52 against 56, 4000 80 against 75; 16 rows (four warps), one 1000 22 against 26, 2000
-// 26 against 27, 64 of them 500 122 against 139, 1000 160 against 151.
+// one row, 4000 positions 20 against 30, 8000 30 against 32, 16,000 50 against 37, eight of them
+// 16,000 91 against 102; five rows (two warps), one sequence 2000 22 against 28, 4000 29 against 31,
+// sixteen 2000 53 against 57, 4000 81 against 77; 16 rows (four warps), one 1000 22 against 27, 2000
+// 27 against 28, 64 of them 500 124 against 142, 1000 161 against 155.
 // How full the tables are is known on the device alone: half empty ones (lengths spread evenly) speak for this
-// kernel, mostly empty ones more so.  960 positions, full, half and mostly empty, this kernel's time over
-// the paged attention's: 16 rows of 32 heads over 8 of 128, one sequence 1.06, 16 of them 0.97, 0.88, 0.66,
-// 64 1.07, 0.84, 0.67; 32 rows (two row groups), four 1.16, 0.97, 0.78, 64 1.14, 0.91, 0.64.
+// kernel, mostly empty ones more so.  1000 positions, full, half and mostly empty, this kernel's time over
+// the paged attention's: 16 rows of 32 heads over 8 of 128, one sequence 0.78, 16 of them 0.97, 0.81, 0.66,
+// 64 1.03, 0.85, 0.64; 32 rows (two row groups), four 1.18, 0.89, 0.72, 64 1.16, 0.92, 0.64.
 //
 // Heads of more than 128 columns have one warp a CTA, and every group of 16 rows reads the sequence
-// again.  16 heads over 2 of 256, one group: one row, one sequence of 500 positions 0.94, 1000 1.00, 2000
-// 1.08, 16 of them 2000 0.88, 0.96, 1.06, 64 of 3000 0.96, 0.92, 0.91; 16 rows, four of 500 1.11, 1.05,
-// 0.97, 1000 1.15, 1.13, 1.01, 2000 1.22, 1.22, 1.16, 16 of 1000 1.02, 1.08, 1.03, 64 of 1000 1.05,
-// 0.94, 0.79, 200 of 2000 0.88, 0.80, 0.67.  Several groups, by the row groups of all sequences and heads: 40
-// (four sequences of nine rows) 500 positions 1.00, 0.99, 0.93, 1000 1.08, 1.02, 0.95; 144 500 1.01, 0.82,
-// 0.86, 960 1.26, 1.05, 0.89; 160 500 1.00, 0.96, 0.79, 960 1.46, 1.09, 0.88; 240 960 1.16, 1.09, 0.84; 288
-// 960 1.18, 1.01, 0.79; 432 960 0.96, 0.97, 0.72; 640 1000 1.12, 0.96, 0.73, 1500 1.24, 1.08, 0.80: in the
-// mean of the three the border lies by 700 positions at 160 groups, 900 at 240, 1300 at 640.
+// again.  16 heads over 2 of 256, one group, 16 rows: one sequence of 3000 positions 0.91, 24 of them 0.89, 0.86,
+// 0.82, 64 0.97, 0.91, 0.88.  Several groups, by how many there are of all sequences and heads: 40 (four
+// sequences of nine rows) 1000 positions 1.05, 0.83, 0.69, 72 1.23, 0.99, 0.68; 96 1.20, 0.96, 0.84; 144 1.32,
+// 1.06, 0.86; 160 1.52, 1.12, 0.79; 240 1.17, 1.04, 0.78; 288 1.20, 0.97, 0.78; 640 1.11, 0.96, 0.71; 2000 1.00,
+// 0.82, 0.53.  Up to half as many as SMs all parts run at once, from some 1.5 an SM on their rounds
+// are full; between, where the mean of the three passes 1, tables of 500: 96 0.86, 0.83, 0.71, 144 0.99, 0.80,
+// 0.80, 160 1.00, 0.91, 0.74.
 constexpr int kOwnMostOne = 4800;   // one warp, 128 columns, up to 16 cache heads of sequences; more by their number
 constexpr int kOwnMostTwo = 3000;   // two warps
 constexpr int kOwnMostFour = 1000;  // four, or several row groups
-constexpr int kOwnMostWide = 500;   // more than 128 columns, up to 16 cache heads of sequences, or few row groups
+constexpr int kOwnMostWide = 500;   // several of more than 128 columns, half as many in all as SMs to 1.5 an SM
 constexpr int kOwnMost = 2048;      // of a part, of a single long sequence
 constexpr uint64_t kOwnDrainNs = 100000000ull;  // 0.1 s: copies under way at the end
 
@@ -563,13 +562,12 @@ cudaError_t own_dispatch(const OwnMaps& m, const JoinArgs& j, bool last, cudaStr
 bool own_takes(const OwnArgs& o, int sms) {
   const AttnArgs& a = o.attn;
   const long long positions = (long long)a.max_pages * a.page, units = (long long)a.B * a.Hkv;
-  const long long by_units = units > 16 ? units : 16;
-  const bool wide = a.D > 128, few = 2 * units * o.row_groups < 3 * sms;  // (groups an SM: 1.5)
-  const long long most = o.row_groups > 1 ? (wide && few ? kOwnMostWide : kOwnMostFour)
-                         : wide           ? kOwnMostWide * by_units / 16
+  const long long groups = units * o.row_groups;
+  const bool wide = a.D > 128 && 2 * groups > sms && 2 * groups < 3 * sms;
+  const long long most = o.row_groups > 1 ? (wide ? kOwnMostWide : kOwnMostFour)
                          : o.warps == 4   ? kOwnMostFour
                          : o.warps == 2   ? kOwnMostTwo
-                                          : kOwnMostOne * 128 / a.D * by_units / 16;
+                                          : kOwnMostOne * 128 / a.D * (units > 16 ? units : 16) / 16;
   return positions <= most && positions <= (long long)kOwnMost * o.parts;
 }
 

@@ -65,17 +65,17 @@ def own_form(launches):
     (16, 5, 32, 8, 128, 3008, PAGED), (16, 5, 32, 8, 128, 2992, OWN), (16, 16, 32, 8, 128, 992, OWN),
     (16, 16, 32, 8, 128, 1008, PAGED), (4, 32, 32, 8, 128, 992, OWN), (4, 32, 32, 8, 128, 1008, PAGED),
     # heads of 256, one row group: by sequences and heads
-    (1, 1, 16, 2, 256, 496, OWN), (1, 1, 16, 2, 256, 512, PAGED), (4, 2, 16, 2, 256, 1008, PAGED),
-    (64, 2, 16, 2, 256, 2000, OWN),
-    # several row groups: as many as 1.5 an SM, and fewer
-    (16, 9, 16, 2, 256, 496, OWN), (16, 9, 16, 2, 256, 1000 // 16 * 16, PAGED), (4, 9, 16, 2, 256, 992, PAGED),
-    (64, 9, 16, 2, 256, 992, OWN), (64, 9, 16, 2, 256, 1008, PAGED),
+    (1, 1, 16, 2, 256, 2400, OWN), (1, 1, 16, 2, 256, 2416, PAGED), (64, 2, 16, 2, 256, 19200, OWN),
+    # several row groups: up to half as many as SMs, up to 1.5 an SM, more
+    (4, 9, 16, 2, 256, 992, OWN), (4, 9, 16, 2, 256, 1008, PAGED), (16, 9, 16, 2, 256, 496, OWN),
+    (16, 9, 16, 2, 256, 512, PAGED), (64, 9, 16, 2, 256, 992, OWN), (64, 9, 16, 2, 256, 1008, PAGED),
 ])
 def test_own_positions_by_rows_sequences_and_tables(plan, B, S, hq, hkv, d, most, want):
     # (a prefix of more positions than few rows take in parts)
     assert own_form(plan(f"prefix {B} {S} {hq} {hkv} {d} 16 1000 {most // 16}")) == want
 
 
-@pytest.mark.parametrize("B,sms,want", [(22, 152, PAGED), (23, 152, OWN), (23, 160, PAGED), (24, 160, OWN)])
+@pytest.mark.parametrize("B,sms,want", [(7, 152, OWN), (8, 152, PAGED), (8, 160, OWN), (22, 152, PAGED), (23, 152, OWN),
+                                         (23, 160, PAGED), (24, 160, OWN)])
 def test_row_groups_are_counted_by_the_device(plan, B, sms, want):
     assert own_form(plan(f"prefix {B} 9 16 2 256 16 100 60", sms=sms)) == want
