@@ -317,7 +317,6 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // The 16 MMAs of one 256-column stage under a single elect.sync (one lane
 // issues, the warp stays converged): MMA m multiplies A columns a + 8m by the
@@ -427,21 +426,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// What launches in front of a call wrote is visible to a grid behind its own wait.  A launch that is to run
-// beside the call's first one cannot wait, as it would wait for that one too.  So a thread of the first
-// launch, behind its wait, writes a word with release semantics; who has read it with acquire semantics
-// sees what that thread saw (by loads that are coherent, and by the asynchronous proxy behind a fence).
-// Nobody waits for the word: who does not find it waits for the launch instead.
-__device__ __forceinline__ void pass_on(unsigned* word) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(1u) : "memory");
-  __threadfence();
-}
-__device__ __forceinline__ bool passed_on(const unsigned* word) {
-  unsigned x;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(word) : "memory");
-  return x != 0;
 }
 
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {

@@ -252,4 +252,21 @@ __device__ __forceinline__ uint32_t nonfinite16<__nv_bfloat16>(uint32_t x) {
   return ((x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 2u : 0u);
 }
 
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// What launches in front of a call wrote is visible to a grid behind its own wait.  A launch that is to run
+// beside the call's first one cannot wait, as it would wait for that one too.  So a thread of the first
+// launch, behind its wait, writes a word with release semantics; who has read it with acquire semantics
+// sees what that thread saw (by loads that are coherent, and by the asynchronous proxy behind a fence).
+// Nobody waits for the word: who does not find it waits for the launch instead.
+__device__ __forceinline__ void pass_on(unsigned* word) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(1u) : "memory");
+  __threadfence();
+}
+__device__ __forceinline__ bool passed_on(const unsigned* word) {
+  unsigned x;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(word) : "memory");
+  return x != 0;
+}
+
 }  // namespace sdv
