@@ -591,7 +591,10 @@ SDV_API sdv_status sdv_qk_norm_rope(const sdv_kvcache* cache, int32_t in_dtype, 
  * The result is that of sdv_paged_attn on the joined positions: lse over both, a row
  * i >= n_rows[b] gives 0 and -inf.  Arguments otherwise as there; the workspace is
  * sdv_prefix_attn_workspace_bytes(...) bytes.  Several prefixes: a call each, on their
- * sequences.  Deterministic.
+ * sequences.  Deterministic.  The lengths being on the device, kernels are chosen by what the
+ * tables could hold: tables that are as wide as the longest sequence (max_pages, prefix_pages)
+ * are up to 1.7 times as fast as tables for 32,768 positions, and give the same result within
+ * the operation's rounding, not the same bits.
  */
 SDV_API sdv_status sdv_prefix_attn(const sdv_kvcache* cache, const int32_t* prefix_table, int32_t prefix_pages,
                            const int32_t* prefix_len, const void* q, int64_t q_stride, int32_t B, int32_t S,
@@ -621,12 +624,13 @@ SDV_API size_t sdv_prefix_attn_workspace_bytes(int32_t B, int32_t S, int32_t Hq,
  *   drafts_or_null: device int32 [B][S - 1] (NULL where S == 1); a draft outside [0, V) is
  *     not accepted; draft_probs_or_null: device fp32 [B][S - 1][V], below 0 and NaN count as 0;
  *   uniforms: device fp32 [B][S] in [0, 1).
- * A sequence whose drawn row has no token left gives next_token -1.  Weights below 2^-125 of
+ * A sequence whose drawn row has no token left gives next_token -1.  Weights below 2^-124 of
  * the row's largest count as 0.  Rows past n_drafts[b] are not read.
  * 1 <= S <= 32, V and B <= 2^24.  The workspace is sdv_verify_drafts_workspace_bytes(...) bytes.
  * Deterministic.  A test's probability is exact to some 2^-18, the draw's weights and the sums
- * of 1024 of them to some 2^-30: a test or a draw nearer to its border than that may differ
- * from a 64-bit evaluation.
+ * of 1024 of them to some 2^-30 where |logit| / temperature stays below some 10^5 (beyond, a
+ * weight's error grows with it, to 2^-25 at 10^7): a test or a draw nearer to its border than
+ * that may differ from a 64-bit evaluation.
  */
 SDV_API sdv_status sdv_verify_drafts(int32_t dtype, const void* logits, int64_t row_stride, int32_t B, int32_t S,
                              int32_t V, const float* temperature, const int32_t* drafts_or_null,

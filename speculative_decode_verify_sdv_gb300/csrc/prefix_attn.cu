@@ -408,9 +408,9 @@ cudaError_t launch_prefix_join(int dtype, const JoinArgs& j, int sms, cudaStream
 constexpr int kSimplePerSm = 2;
 // Partials of a row that the own positions' kernel adds up itself, where it has all of a sequence's
 // positions in one part: no launch and no partials of its own for the join.  256 windows of five rows,
-// 32 heads over 8 of 128, up to 500 positions 121 us a call against 129, up to 1001 behind 16,384
-// 355 against 360; 199 of 20 rows, one position 36 against 41; 450 of one row, up to 60 41 against 40;
-// 256 of 16 rows, heads of 64, 50 against 52.  Heads of 256 have no registers for it (72 against 59).
+// 32 heads over 8 of 128, up to 500 positions 123 us a call against 132, up to 1001 behind 16,384
+// 352 against 362; 199 of 20 rows, one position 38 against 43; 450 of one row, up to 60 43 against 42;
+// 256 of 16 rows, heads of 64, 52 against 55.  Heads of 256 have no registers for it (72 against 59).
 constexpr int kLastSharers = 4;
 // CTAs for the own positions, were all tables full (some end at once): per SM 16 of one warp (16, 24, 32,
 // 48: 64 sequences of up to 2001 positions 72.1, 71.3, 71.0, 73.1 us a call), 8 of more (8, 12, 16: 256
@@ -420,9 +420,9 @@ int own_ctas(int warps, int sms) { return (warps > 1 ? 8 : 16) * sms; }
 // Up to 16 rows a kv head, heads of up to 128 and up to 8192 positions: the prefix goes into the
 // launch of the own positions, in at most 32 parts a head (the join reads them all: 75 parts of 4800
 // positions 21.3 us, 25 of them 18.0).  Against the tensor-core kernel in front of that launch,
-// four rows of 32 heads over 8 of 128, 100 positions of their own: 300 positions 10.7 against
-// 11.7 us, 2400 15.4 against 20.5, 8000 22.1 against 23.7; one row 9.2 against 12.2, 13.3 against
-// 20.4, 20.2 against 23.0.  32 rows a head (two row tiles a warp) lose, 18.3 against 14.8 at 1201
+// four rows of 32 heads over 8 of 128, 100 positions of their own: 300 positions 11.9 against
+// 13.3 us, 2400 16.0 against 21.8, 8000 23.1 against 25.0; one row 11.2 against 13.0, 14.4 against
+// 21.4, 21.1 against 24.3.  32 rows a head (two row tiles a warp) lose, 18.3 against 14.8 at 1201
 // positions, and so do heads of 256, 25.6 against 22.1 at 4800.  Its partials are at most
 // 2 sms * 16 rows, a quarter of what the workspace has room for.
 constexpr int kPrefixFewRows = 16;

@@ -9,8 +9,8 @@
 // slice's keys while this one's softmax and second product run, its values during the next first
 // product.  What is start and end for one CTA is not for the others of its SM.
 //
-// 256 sequences of 100 to 1001 positions, five rows, 8 heads of 128 (417 MB): 108 us, 3.9 TB/s, or 119 with the join; 64 of
-// up to 2001, one row (134 MB): 34 us, 3.9 TB/s.  Three warps a scheduler, as many as their outputs leave
+// 256 sequences of 100 to 1001 positions, five rows, 8 heads of 128 (417 MB): 123 us with the join; 64 of
+// up to 2001, one row (134 MB): 38 us, 3.5 TB/s, each alone.  Three warps a scheduler, as many as their outputs leave
 // registers for, wait for products, copies and one another.  Up to 64 rows have a warp for 16: with two
 // row tiles in one warp and groups of 32 rows 256 windows of five rows took 364 us a call for 358,
 // one of nine rows 21.7 for 15.5, 64 of them 58.5 for 53.1 (100 positions of their own).  Heads of

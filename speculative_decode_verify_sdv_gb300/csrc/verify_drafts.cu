@@ -14,20 +14,20 @@
 // A draw compares running sums of up to 10^5 weights with a random number, so an error of e of
 // the total gives another token with a chance of 10^5 e: 32-bit weights, whose errors of 2^-24
 // add up to 10^-9 of the total or more, would miss one draw in some thousands.  The weights
-// are therefore pairs of floats, exact to some 2^-30 of each (2^x by a table of 2^(k/32) and a
-// short polynomial: Tang, "Table-driven implementation of the exponential function", ACM TOMS
-// 1989), and their sums carry the rounding of every addition along (Knuth's two-sum); the first
-// launch takes each weight apart at 2^-17 instead, adds the upper parts exactly and the rest, a
-// hundredth at most, in 32 bits: a chunk's sum to 2^-32 (in the mean of random logits; 2^-29 the
-// worst of 1800).  No sum is of 64-bit numbers: this GPU adds those at a fiftieth of the rate.
+// are therefore pairs of floats, exact to some 2^-30 of each while logits over temperatures stay below
+// 10^5 (2^x by a table of 2^(k/32) and a short polynomial: Tang, "Table-driven implementation of the
+// exponential function", ACM TOMS 1989), and their sums carry the rounding of every addition along
+// (Knuth's two-sum); the first launch takes each weight apart at 2^-17 instead, adds the upper parts
+// exactly and the rest, a hundredth at most, in 32 bits: a chunk's sum to 2^-32 (in the mean of random
+// logits; 2^-29 the worst of 1800).  No sum is of 64-bit numbers: this GPU adds those at a fiftieth of the rate.
 //
 // 25 instructions a logit bound the first launch, not its read: 32 windows, 226 rows of 151,936
 // fp32 logits in all (137 MB), 47 us, 60 % of the issue slots; 200 rows of 50,257 in bf16 16 us.  A warp
 // takes one chunk and ends: looping with the next chunk's loads ahead took 88 registers for 80 and
 // 65 us for 48, and loading a chunk again for its sum 75 to 77 us a call for 71.  The second launch is a
 // chain of latencies: 10 us where a row of the target is drawn from, 28 where a cluster looks
-// through the drafter's probabilities (eight CTAs of a sequence).  Both together 71, 19 and, one window
-// of five rows, 10.4 us.
+// through the drafter's probabilities (eight CTAs of a sequence).  Both together 71, 20 and, one window
+// of five rows, 10.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -243,7 +243,7 @@ __device__ __forceinline__ Two warp_scan(Two x, int lane) {
 }
 
 // 2^(x c - K) for the two x of a pair, K = ceil(m c) for the largest x: exact to some 2^-30 of
-// each; 0 where it is below 2^-124 and where x is -inf.  For all lanes of a warp: lane k holds
+// each, or to 2^-48 |x c|, that of x c itself, where this is more; 0 where it is below 2^-124 and where x is -inf.  For all lanes of a warp: lane k holds
 // 2^(k/32).  x c is taken apart as it is, K being a whole number; where it is so large that its
 // last bits are no fraction any more, K is taken off first (exact: the two are close).  Past 2^24,
 // where neighbouring logits are a power of two and more apart, K is m c itself.
